@@ -78,7 +78,11 @@ typedef enum mla_dtype { MLA_DTYPE_F32 = 0, MLA_DTYPE_BF16 = 1 } mla_dtype;
 #define MLA_DEVICE_VALUE_RANGE (1 << 8)         /* a split piece's context (an average
                                                    of latent rows) left the fp16
                                                    range of the bf16 decode's
-                                                   partials; saturated               */
+                                                   partials; saturated; or a latent
+                                                   value to be held in 8 bits is
+                                                   beyond 57344; saturated          */
+#define MLA_DEVICE_BAD_BLOCK_START (1 << 9)     /* an 8-bit cache row whose kv_start is not
+                                                   a whole number of scale blocks   */
 /* Largest |half score| (unscaled q . k over one CTA's 288 features) that the
  * bf16 decode's fp16 score exchange carries within the bf16 tolerance. */
 #define MLA_FP16_SCORE_LIMIT 256.0f
@@ -500,6 +504,155 @@ int mla_prefill_attend(const void* q_nope, int64_t q_nope_row_stride, int64_t q_
                        int32_t s_q, int32_t heads, int32_t nope, int32_t rope_dim, int32_t v_dim, int64_t t_max,
                        float softmax_scale, void* out, int64_t out_row_stride, int out_dtype, float* lse_out,
                        int32_t* device_status, mla_stream_t stream);
+
+/*
+ * The 8-bit cache (no counterpart on the pages).  It holds the latent in half
+ * the bytes; the rope key stays in `dtype`.
+ *
+ * codes[b*codes_batch_stride + r*codes_row_stride + 0:rank] are e4m3 codes
+ * (OCP 8-bit float, 0x7F / 0xFF = NaN) of buffer row r, in units of
+ * 2^(e - 127), where the exponent byte e = scales[b*scales_batch_stride +
+ * r / scale_block] is shared by scale_block consecutive buffer rows
+ * (scale_block a power of two up to 64) and lies in [64, 134] (a byte outside
+ * is read as the nearer end).  Units are powers of two, so a held value is
+ * exact in bf16 and f32.  A batch row's window [kv_start[b], kv_start[b] +
+ * kv_len[b]) must start on a whole block, so that rows packed in one buffer
+ * share no exponent: a row with kv_start[b] not a multiple of scale_block sets
+ * MLA_DEVICE_BAD_BLOCK_START, one whose window does not lie in [0, t_max)
+ * sets MLA_DEVICE_INDEX_OUT_OF_RANGE, and either is skipped (attention: no
+ * visible key).  The selection, scores, outputs, workspace and errors of the
+ * entry points below are those of their bf16 / f32 counterparts.
+ *
+ * mla_append_compressed_q8: mla_append_compressed into an 8-bit cache.  The
+ * normalised f32 values of a block's tokens take the smallest unit in which
+ * the largest magnitude is at most 448; a block that already holds tokens of
+ * the window keeps its unit or takes a larger one, and its codes are then
+ * rounded again to the larger unit (exact but for what falls below e4m3's
+ * smallest step).  Codes round to nearest, ties to even.  A magnitude beyond
+ * 57344 (or infinite) saturates and sets MLA_DEVICE_VALUE_RANGE; NaN stays
+ * NaN and sets no unit.  kv_len_out may alias kv_len.  At most 65535 batch rows.
+ *
+ * mla_quantize_cache: the windows of a latent buffer [b, r, rank] (dtype f32 or
+ * bf16) into codes and exponents, rows outside the windows left as they
+ * were (a block's exponent is written when the window reaches into it).
+ * mla_dequantize_cache: the windows back into a latent buffer, exact.
+ */
+int mla_append_compressed_q8(const void* latent_raw, int64_t latent_raw_row_stride, int64_t latent_raw_token_stride,
+                             const void* rope_raw, int64_t rope_raw_row_stride, int64_t rope_raw_token_stride,
+                             int dtype, const void* norm_weight, float eps, float theta, const int32_t* row_offsets,
+                             uint8_t* codes, int64_t codes_row_stride, int64_t codes_batch_stride, uint8_t* scales,
+                             int64_t scales_batch_stride, int32_t scale_block, void* rope, int64_t rope_row_stride,
+                             int64_t rope_batch_stride, int rope_dtype, const int32_t* kv_start,
+                             const int32_t* kv_len, int32_t* kv_len_out, int32_t batch, int32_t s_new, int32_t rank,
+                             int32_t rope_dim, int64_t t_max, int32_t* device_status, mla_stream_t stream);
+int mla_quantize_cache(const void* latent, int64_t latent_row_stride, int64_t latent_batch_stride, int dtype,
+                       uint8_t* codes, int64_t codes_row_stride, int64_t codes_batch_stride, uint8_t* scales,
+                       int64_t scales_batch_stride, int32_t scale_block, const int32_t* kv_start,
+                       const int32_t* kv_len, int32_t batch, int32_t rank, int64_t t_max, int32_t* device_status,
+                       mla_stream_t stream);
+int mla_dequantize_cache(const uint8_t* codes, int64_t codes_row_stride, int64_t codes_batch_stride,
+                         const uint8_t* scales, int64_t scales_batch_stride, int32_t scale_block, void* latent,
+                         int64_t latent_row_stride, int64_t latent_batch_stride, int dtype, const int32_t* kv_start,
+                         const int32_t* kv_len, int32_t batch, int32_t rank, int64_t t_max, int32_t* device_status,
+                         mla_stream_t stream);
+
+/*
+ * mla_decode_attend over an 8-bit cache: the same attention over the held
+ * values (no further rounding of them: over bf16 queries the result is that of
+ * mla_decode_attend over the dequantised bf16 cache).  q and rope have
+ * `dtype`.  bf16 is served for the shapes of mla_decode_attend, with codes and
+ * rope 16-byte aligned, codes strides multiples of 16 and rope strides
+ * multiples of 8 elements; f32 for any shape.  The workspace is that of
+ * mla_decode_workspace_size for `dtype`.
+ */
+int mla_decode_attend_q8(const void* q, int64_t q_row_stride, int64_t q_head_stride, const uint8_t* codes,
+                         int64_t codes_row_stride, int64_t codes_batch_stride, const uint8_t* scales,
+                         int64_t scales_batch_stride, int32_t scale_block, const void* rope, int64_t rope_row_stride,
+                         int64_t rope_batch_stride, int dtype, const int32_t* kv_start, const int32_t* kv_len,
+                         int32_t batch, int32_t s_q, int32_t heads, int32_t rank, int32_t rope_dim, int64_t t_max,
+                         const int32_t* selected_positions, const int32_t* selected_counts, int32_t k_max,
+                         float softmax_scale, void* ctx_out, int64_t ctx_row_stride, int64_t ctx_head_stride,
+                         int out_dtype, float* lse_out, void* workspace, size_t workspace_bytes,
+                         int32_t* device_status, mla_stream_t stream);
+
+/*
+ * Accumulated attention weight of every cached key (no counterpart on the
+ * pages): what an eviction ranks the keys by.
+ *
+ * For window key t < kv_len[b] of batch row b, with W = weights[b *
+ * weights_batch_stride + kv_start[b] + t] (f32, one per buffer row),
+ *   W <- (t < kv_len[b] - n_new ? decay * W : 0)
+ *        + sum over tokens i < s_q that see t and heads h of exp(s[n, h, t] - lse[n, h]),
+ * n = b*s_q + i, s the scaled score of mla_decode_attend over the dense causal
+ * window and lse [n_q, heads] its lse_out.  The n_new newest keys start from
+ * zero (the tokens appended since the last call: buffer rows behind a window
+ * may hold weights of evicted keys).  decay in [0, 1]; 0 does not read W.
+ * Weights outside the windows are left as they were.  Sums are f32 in a fixed
+ * order (the same inputs give the same bits).
+ * q, latent and rope as in mla_decode_attend, codes / scales as in
+ * mla_decode_attend_q8.  bf16 is served for heads 64 or 128, rank 512, rope
+ * 64 (tensor cores; 16-byte aligned pointers and strides as in
+ * mla_decode_attend), f32 for any shape; at most 65535 batch rows.  A row
+ * whose window does not lie in [0, t_max) sets MLA_DEVICE_INDEX_OUT_OF_RANGE
+ * and is skipped.  Windows of the rows must not overlap in `weights`.
+ */
+int mla_key_weights(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* latent,
+                    int64_t latent_row_stride, int64_t latent_batch_stride, const void* rope, int64_t rope_row_stride,
+                    int64_t rope_batch_stride, int dtype, const int32_t* kv_start, const int32_t* kv_len,
+                    int32_t batch, int32_t s_q, int32_t heads, int32_t rank, int32_t rope_dim, int64_t t_max,
+                    const float* lse, float softmax_scale, float decay, int32_t n_new, float* weights,
+                    int64_t weights_batch_stride, int32_t* device_status, mla_stream_t stream);
+int mla_key_weights_q8(const void* q, int64_t q_row_stride, int64_t q_head_stride, const uint8_t* codes,
+                       int64_t codes_row_stride, int64_t codes_batch_stride, const uint8_t* scales,
+                       int64_t scales_batch_stride, int32_t scale_block, const void* rope, int64_t rope_row_stride,
+                       int64_t rope_batch_stride, int dtype, const int32_t* kv_start, const int32_t* kv_len,
+                       int32_t batch, int32_t s_q, int32_t heads, int32_t rank, int32_t rope_dim, int64_t t_max,
+                       const float* lse, float softmax_scale, float decay, int32_t n_new, float* weights,
+                       int64_t weights_batch_stride, int32_t* device_status, mla_stream_t stream);
+
+/*
+ * Eviction by accumulated weight (no counterpart on the pages).
+ *
+ * mla_evict_plan: a row with kv_len[b] > n_keep keeps n_keep tokens: its first
+ * n_sink, its last n_recent, and of the rest the n_keep - n_sink - n_recent
+ * with the largest weights[b*weights_batch_stride + kv_start[b] + t] (ties to
+ * the lower position; the order of mla_select_topk's keys: -0 below +0, NaN by
+ * its bits).  kept[b*kept_row_stride + 0..n_keep) receives their window
+ * positions in ascending order and counts[b] = n_keep.  A row within its
+ * budget gets counts[b] = -1 (everything stays) and its kept row is left as it
+ * was.  kv_len_out[b] (may be NULL, may alias kv_len) receives min(kv_len[b],
+ * n_keep).  A row whose window does not lie in [0, t_max) is treated as within
+ * its budget, keeps its length and sets MLA_DEVICE_INDEX_OUT_OF_RANGE.
+ * n_keep > 0, n_sink + n_recent <= n_keep, batch <= 65535.
+ *
+ * mla_cache_compact: moves each row's kept tokens to the front of its window, in
+ * place and in order: for j < counts[b], buffer row kv_start[b] + j of every
+ * listed array receives row kv_start[b] + kept[b*kept_row_stride + j]; rows
+ * behind are left as they were.  `arrays` is a HOST array of n_arrays (1..8)
+ * state arrays that do not overlap: element (b, r, byte) at data +
+ * b*batch_stride_bytes + r*token_stride_bytes + byte, row_bytes of it moved
+ * (latent, codes, rope keys, weights, per-token exponents; an exponent shared
+ * by several tokens cannot be moved with one of them, so an 8-bit cache is
+ * compacted with scale_block 1).  counts[b] = -1 moves nothing; another count
+ * outside [0, n_keep] sets MLA_DEVICE_BAD_SELECTION_COUNT and moves nothing.
+ * A position that is not above its predecessor, below j, or outside the
+ * buffer sets MLA_DEVICE_INDEX_OUT_OF_RANGE and is not moved.  Windows must not overlap.
+ * The kept tokens keep the rotation of their old positions: later appends and
+ * queries pass their own positions (row_offsets).
+ */
+typedef struct mla_state_array {
+  void* data;
+  int64_t token_stride_bytes;
+  int64_t batch_stride_bytes;
+  int32_t row_bytes;
+} mla_state_array;
+int mla_evict_plan(const float* weights, int64_t weights_batch_stride, const int32_t* kv_start, const int32_t* kv_len,
+                   int32_t batch, int64_t t_max, int32_t n_keep, int32_t n_sink, int32_t n_recent, int32_t* kept,
+                   int64_t kept_row_stride, int32_t* counts, int32_t* kv_len_out, int32_t* device_status,
+                   mla_stream_t stream);
+int mla_cache_compact(const mla_state_array* arrays, int32_t n_arrays, const int32_t* kv_start, const int32_t* kept,
+                      int64_t kept_row_stride, const int32_t* counts, int32_t n_keep, int32_t batch, int64_t t_max,
+                      int32_t* device_status, mla_stream_t stream);
 
 /*
  * Test hook: the selected-position gather of attendAbsorbed (takeAxis on

@@ -5,6 +5,7 @@
 #include <string.h>
 #include <stdint.h>
 
+#include "e4m3.cuh"
 #include "mla_internal.h"
 
 namespace mla {
@@ -662,6 +663,327 @@ int mla_rollback_lengths(const int32_t* kv_len_before, const int32_t* keep, cons
   return cuda_status(launch_rollback_lengths(kv_len_before, keep, kv_len, kv_len_out, batch, device_status,
                                              (cudaStream_t)stream),
                      "rollback_lengths launch");
+}
+
+// ------------------------------------------------------------ 8-bit cache
+
+// Checks shared by the entry points that take an 8-bit cache; `shift` receives log2(scale_block).
+static int check_q8(const char* what, const uint8_t* codes, int64_t row_stride, int64_t batch_stride,
+                    const uint8_t* scales, int64_t scales_batch_stride, int32_t scale_block, int32_t rank,
+                    int32_t* shift) {
+  MLA_CHECK(codes && scales, "%s: NULL cache pointer", what);
+  MLA_CHECK(row_stride >= rank && batch_stride >= 0 && scales_batch_stride >= 0, "%s: cache strides too small", what);
+  MLA_CHECK(scale_block > 0 && scale_block <= kMaxScaleBlock && (scale_block & (scale_block - 1)) == 0,
+            "%s: scale_block %d must be a power of two up to %d", what, scale_block, kMaxScaleBlock);
+  *shift = 0;
+  while ((1 << *shift) < scale_block) ++*shift;
+  return MLA_OK;
+}
+
+int mla_append_compressed_q8(const void* latent_raw, int64_t latent_raw_row_stride, int64_t latent_raw_token_stride,
+                             const void* rope_raw, int64_t rope_raw_row_stride, int64_t rope_raw_token_stride,
+                             int dtype, const void* norm_weight, float eps, float theta, const int32_t* row_offsets,
+                             uint8_t* codes, int64_t codes_row_stride, int64_t codes_batch_stride, uint8_t* scales,
+                             int64_t scales_batch_stride, int32_t scale_block, void* rope, int64_t rope_row_stride,
+                             int64_t rope_batch_stride, int rope_dtype, const int32_t* kv_start,
+                             const int32_t* kv_len, int32_t* kv_len_out, int32_t batch, int32_t s_new, int32_t rank,
+                             int32_t rope_dim, int64_t t_max, int32_t* device_status, mla_stream_t stream) {
+  g_detail[0] = 0;
+  MLA_CHECK(latent_raw && norm_weight && kv_len && (rope_dim == 0 || (rope_raw && rope)), "append_q8: NULL pointer");
+  MLA_CHECK(valid_dtype(dtype) && valid_dtype(rope_dtype), "append_q8: bad dtype");
+  MLA_CHECK(batch > 0 && s_new > 0 && rank > 0 && rope_dim >= 0 && t_max > 0, "append_q8: sizes must be positive");
+  MLA_CHECK(batch <= 65535, "append_q8: at most 65535 batch rows");
+  MLA_CHECK(t_max < (1LL << 31), "append_q8: t_max must fit int32");
+  MLA_CHECK(rank <= kMaxAppendRank, "append_q8: rank %d > %d", rank, kMaxAppendRank);
+  MLA_CHECK((rope_dim & 1) == 0 && rope_dim <= kMaxRotaryDims, "append_q8: rope_dim must be even and <= %d",
+            kMaxRotaryDims);
+  MLA_CHECK(isfinite(eps) && eps >= 0.f, "append_q8: RMSNorm epsilon must be non-negative");
+  MLA_CHECK(isfinite(theta) && theta > 0.f, "append_q8: theta must be positive and finite");
+  MLA_CHECK(latent_raw_token_stride >= rank && latent_raw_row_stride >= 0, "append_q8: latent strides too small");
+  MLA_CHECK(rope_dim == 0 || (rope_raw_token_stride >= rope_dim && rope_raw_row_stride >= 0 &&
+                              rope_row_stride >= rope_dim && rope_batch_stride >= 0),
+            "append_q8: rope strides too small");
+  EncodeParams p;
+  memset(&p, 0, sizeof(p));
+  const int st = check_q8("append_q8", codes, codes_row_stride, codes_batch_stride, scales, scales_batch_stride,
+                          scale_block, rank, &p.block_shift);
+  if (st != MLA_OK) return st;
+  p.latent_raw = latent_raw;
+  p.lr_row_stride = latent_raw_row_stride;
+  p.lr_tok_stride = latent_raw_token_stride;
+  p.rope_raw = rope_raw;
+  p.rr_row_stride = rope_raw_row_stride;
+  p.rr_tok_stride = rope_raw_token_stride;
+  p.weight = norm_weight;
+  p.eps = eps;
+  p.row_offsets = row_offsets;
+  p.codes = codes;
+  p.codes_row_stride = codes_row_stride;
+  p.codes_batch_stride = codes_batch_stride;
+  p.scales = scales;
+  p.scales_batch_stride = scales_batch_stride;
+  p.rope = rope;
+  p.rope_row_stride = rope_row_stride;
+  p.rope_batch_stride = rope_batch_stride;
+  p.kv_start = kv_start;
+  p.kv_len = kv_len;
+  p.kv_len_out = kv_len_out;
+  p.batch = batch;
+  p.s_new = s_new;
+  p.rank = rank;
+  p.rope_dim = rope_dim;
+  p.t_max = t_max;
+  p.status = device_status;
+  if (rope_dim > 0) rope_inverse_frequencies(theta, rope_dim, p.inv_freq);
+  const int64_t evec = dtype == MLA_DTYPE_F32 ? 4 : 8;   // elements of 16 bytes
+  const bool vec = rank % 8 == 0 && aligned16(latent_raw) && aligned16(norm_weight) &&
+                   latent_raw_row_stride % evec == 0 && latent_raw_token_stride % evec == 0 &&
+                   (reinterpret_cast<uintptr_t>(codes) & 7u) == 0 && codes_row_stride % 8 == 0 &&
+                   codes_batch_stride % 8 == 0;
+  return cuda_status(launch_append_q8(p, dtype, rope_dtype, vec, (cudaStream_t)stream), "append_q8 launch");
+}
+
+static int convert_params(EncodeParams& p, const char* what, const void* latent, int64_t latent_row_stride,
+                          int64_t latent_batch_stride, int dtype, const uint8_t* codes, int64_t codes_row_stride,
+                          int64_t codes_batch_stride, const uint8_t* scales, int64_t scales_batch_stride,
+                          int32_t scale_block, const int32_t* kv_start, const int32_t* kv_len, int32_t batch,
+                          int32_t rank, int64_t t_max, int32_t* device_status) {
+  MLA_CHECK(latent && kv_len, "%s: NULL pointer", what);
+  MLA_CHECK(valid_dtype(dtype), "%s: bad dtype %d", what, dtype);
+  MLA_CHECK(batch > 0 && rank > 0 && t_max > 0, "%s: sizes must be positive", what);
+  MLA_CHECK(batch <= 65535, "%s: at most 65535 batch rows", what);
+  MLA_CHECK(t_max < (1LL << 31), "%s: t_max must fit int32", what);
+  MLA_CHECK(latent_row_stride >= rank && latent_batch_stride >= 0, "%s: latent strides too small", what);
+  memset(&p, 0, sizeof(p));
+  const int st = check_q8(what, codes, codes_row_stride, codes_batch_stride, scales, scales_batch_stride, scale_block,
+                          rank, &p.block_shift);
+  if (st != MLA_OK) return st;
+  p.codes = const_cast<uint8_t*>(codes);
+  p.codes_row_stride = codes_row_stride;
+  p.codes_batch_stride = codes_batch_stride;
+  p.scales = const_cast<uint8_t*>(scales);
+  p.scales_batch_stride = scales_batch_stride;
+  p.kv_start = kv_start;
+  p.kv_len = kv_len;
+  p.batch = batch;
+  p.rank = rank;
+  p.t_max = t_max;
+  p.status = device_status;
+  return MLA_OK;
+}
+
+int mla_quantize_cache(const void* latent, int64_t latent_row_stride, int64_t latent_batch_stride, int dtype,
+                       uint8_t* codes, int64_t codes_row_stride, int64_t codes_batch_stride, uint8_t* scales,
+                       int64_t scales_batch_stride, int32_t scale_block, const int32_t* kv_start,
+                       const int32_t* kv_len, int32_t batch, int32_t rank, int64_t t_max, int32_t* device_status,
+                       mla_stream_t stream) {
+  g_detail[0] = 0;
+  EncodeParams p;
+  const int st = convert_params(p, "quantize", latent, latent_row_stride, latent_batch_stride, dtype, codes,
+                                codes_row_stride, codes_batch_stride, scales, scales_batch_stride, scale_block,
+                                kv_start, kv_len, batch, rank, t_max, device_status);
+  if (st != MLA_OK) return st;
+  p.latent_raw = latent;
+  p.lr_row_stride = latent_batch_stride;
+  p.lr_tok_stride = latent_row_stride;
+  const int64_t evec = dtype == MLA_DTYPE_F32 ? 4 : 8;
+  const bool vec = rank % 8 == 0 && aligned16(latent) && latent_row_stride % evec == 0 &&
+                   latent_batch_stride % evec == 0 && (reinterpret_cast<uintptr_t>(codes) & 7u) == 0 &&
+                   codes_row_stride % 8 == 0 && codes_batch_stride % 8 == 0;
+  return cuda_status(launch_quantize(p, dtype, vec, (cudaStream_t)stream), "quantize launch");
+}
+
+int mla_dequantize_cache(const uint8_t* codes, int64_t codes_row_stride, int64_t codes_batch_stride,
+                         const uint8_t* scales, int64_t scales_batch_stride, int32_t scale_block, void* latent,
+                         int64_t latent_row_stride, int64_t latent_batch_stride, int dtype, const int32_t* kv_start,
+                         const int32_t* kv_len, int32_t batch, int32_t rank, int64_t t_max, int32_t* device_status,
+                         mla_stream_t stream) {
+  g_detail[0] = 0;
+  EncodeParams p;
+  const int st = convert_params(p, "dequantize", latent, latent_row_stride, latent_batch_stride, dtype, codes,
+                                codes_row_stride, codes_batch_stride, scales, scales_batch_stride, scale_block,
+                                kv_start, kv_len, batch, rank, t_max, device_status);
+  if (st != MLA_OK) return st;
+  p.latent_out = latent;
+  p.lo_row_stride = latent_row_stride;
+  p.lo_batch_stride = latent_batch_stride;
+  const int64_t evec = dtype == MLA_DTYPE_F32 ? 4 : 8;
+  const bool vec = rank % 16 == 0 && aligned16(codes) && codes_row_stride % 16 == 0 && codes_batch_stride % 16 == 0 &&
+                   aligned16(latent) && latent_row_stride % evec == 0 && latent_batch_stride % evec == 0;
+  return cuda_status(launch_dequantize(p, dtype, vec, (cudaStream_t)stream), "dequantize launch");
+}
+
+int mla_decode_attend_q8(const void* q, int64_t q_row_stride, int64_t q_head_stride, const uint8_t* codes,
+                         int64_t codes_row_stride, int64_t codes_batch_stride, const uint8_t* scales,
+                         int64_t scales_batch_stride, int32_t scale_block, const void* rope, int64_t rope_row_stride,
+                         int64_t rope_batch_stride, int dtype, const int32_t* kv_start, const int32_t* kv_len,
+                         int32_t batch, int32_t s_q, int32_t heads, int32_t rank, int32_t rope_dim, int64_t t_max,
+                         const int32_t* selected_positions, const int32_t* selected_counts, int32_t k_max,
+                         float softmax_scale, void* ctx_out, int64_t ctx_row_stride, int64_t ctx_head_stride,
+                         int out_dtype, float* lse_out, void* workspace, size_t workspace_bytes,
+                         int32_t* device_status, mla_stream_t stream) {
+  g_detail[0] = 0;
+  DecodeGeometry g;
+  int st = decode_geometry(g, q, q_row_stride, q_head_stride, codes, codes_row_stride, codes_batch_stride, rope,
+                           rope_row_stride, rope_batch_stride, dtype, kv_start, kv_len, batch, s_q, heads, rank,
+                           rope_dim, t_max, selected_positions, selected_counts, k_max, softmax_scale, ctx_out,
+                           ctx_row_stride, ctx_head_stride, lse_out, device_status, true);
+  if (st != MLA_OK) return st;
+  st = check_q8("decode_q8", codes, codes_row_stride, codes_batch_stride, scales, scales_batch_stride, scale_block,
+                rank, &g.block_shift);
+  if (st != MLA_OK) return st;
+  g.codes = codes;
+  g.codes_row_stride = codes_row_stride;
+  g.codes_batch_stride = codes_batch_stride;
+  g.scales = scales;
+  g.scales_batch_stride = scales_batch_stride;
+  MLA_CHECK(valid_dtype(out_dtype), "decode_q8: bad out_dtype %d", out_dtype);
+  if (dtype == MLA_DTYPE_BF16 && !tc_decode_shape(heads, rank, rope_dim, dtype))
+    return fail(MLA_ERR_UNSUPPORTED, "decode_q8: bf16 is served for heads 64 or 128, rank 512, rope_dim 64 "
+                                     "(got heads %d, rank %d, rope_dim %d)", heads, rank, rope_dim);
+  const size_t need = mla_decode_workspace_size(batch, s_q, heads, rank, rope_dim, t_max, k_max,
+                                                selected_positions != nullptr, dtype);
+  MLA_CHECK(workspace_bytes >= need && (need == 0 || workspace),
+            "decode_q8: workspace of %zu bytes < %zu needed", workspace_bytes, need);
+  MLA_CHECK((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0,
+            "decode_q8: workspace must be 256-byte aligned");
+  if (dtype == MLA_DTYPE_BF16) {
+    const int64_t ovec = out_dtype == MLA_DTYPE_F32 ? 4 : 8;
+    MLA_CHECK(aligned16(q) && aligned16(codes) && aligned16(rope) && aligned16(ctx_out),
+              "decode_q8: q, codes, rope and ctx_out must be 16-byte aligned");
+    MLA_CHECK(q_row_stride % 8 == 0 && q_head_stride % 8 == 0 && codes_row_stride % 16 == 0 &&
+                  codes_batch_stride % 16 == 0 && rope_row_stride % 8 == 0 && rope_batch_stride % 8 == 0 &&
+                  ctx_row_stride % ovec == 0 && ctx_head_stride % ovec == 0,
+              "decode_q8: strides must be multiples of 16 bytes");
+    MLA_CHECK((int64_t)batch * s_q <= (1 << 20), "decode_q8: at most 2^20 query rows");
+    return cuda_status(launch_tc_decode(g, out_dtype, workspace, workspace_bytes, (cudaStream_t)stream),
+                       "decode_q8 (tensor core) launch");
+  }
+  MLA_CHECK((int64_t)batch * s_q <= 65535 && heads <= 65535, "decode_q8: f32 serves at most 65535 query rows and heads");
+  return cuda_status(launch_simt_decode(g, dtype, out_dtype, workspace, workspace_bytes, (cudaStream_t)stream),
+                     "decode_q8 launch");
+}
+
+// ------------------------------------------------------------ attention weights and eviction
+
+static int key_weights(const char* what, DecodeGeometry& g, int dtype, const float* lse, float decay, int32_t n_new,
+                       float* weights, int64_t weights_batch_stride, mla_stream_t stream) {
+  MLA_CHECK(g.q && lse && weights, "%s: NULL q, lse or weights", what);
+  MLA_CHECK(g.q_head_stride >= g.rank + g.rope_dim && g.q_row_stride >= 0, "%s: q strides too small", what);
+  MLA_CHECK(decay >= 0.f && decay <= 1.f, "%s: decay must lie in [0, 1]", what);
+  MLA_CHECK(n_new >= 0, "%s: n_new must be non-negative", what);
+  MLA_CHECK(weights_batch_stride >= 0, "%s: weights_batch_stride must be non-negative", what);
+  MLA_CHECK(g.batch <= 65535, "%s: at most 65535 batch rows", what);
+  KeyWeightParams p{g, lse, weights, weights_batch_stride, decay, n_new};
+  if (dtype == MLA_DTYPE_F32)
+    return cuda_status(launch_simt_key_weights(p, (cudaStream_t)stream), "key weights launch");
+  if (!tc_decode_shape(g.heads, g.rank, g.rope_dim, dtype))
+    return fail(MLA_ERR_UNSUPPORTED, "%s: bf16 is served for heads 64 or 128, rank 512, rope_dim 64 "
+                                     "(got heads %d, rank %d, rope_dim %d)", what, g.heads, g.rank, g.rope_dim);
+  const int64_t lvec = g.codes ? 16 : 8;
+  MLA_CHECK(aligned16(g.q) && aligned16(g.latent) && aligned16(g.rope),
+            "%s: q, the cache and rope must be 16-byte aligned", what);
+  MLA_CHECK(g.q_row_stride % 8 == 0 && g.q_head_stride % 8 == 0 && g.latent_row_stride % lvec == 0 &&
+                g.latent_batch_stride % lvec == 0 && g.rope_row_stride % 8 == 0 && g.rope_batch_stride % 8 == 0,
+            "%s: strides must be multiples of 16 bytes", what);
+  MLA_CHECK(g.codes || (g.latent_batch_stride == 0) == (g.rope_batch_stride == 0),
+            "%s: latent and rope batch strides must both be zero (packed rows) or both non-zero", what);
+  return cuda_status(launch_tc_key_weights(p, (cudaStream_t)stream), "key weights (tensor core) launch");
+}
+
+int mla_key_weights(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* latent,
+                    int64_t latent_row_stride, int64_t latent_batch_stride, const void* rope, int64_t rope_row_stride,
+                    int64_t rope_batch_stride, int dtype, const int32_t* kv_start, const int32_t* kv_len,
+                    int32_t batch, int32_t s_q, int32_t heads, int32_t rank, int32_t rope_dim, int64_t t_max,
+                    const float* lse, float softmax_scale, float decay, int32_t n_new, float* weights,
+                    int64_t weights_batch_stride, int32_t* device_status, mla_stream_t stream) {
+  g_detail[0] = 0;
+  DecodeGeometry g;
+  const int st = decode_geometry(g, q, q_row_stride, q_head_stride, latent, latent_row_stride, latent_batch_stride,
+                                 rope, rope_row_stride, rope_batch_stride, dtype, kv_start, kv_len, batch, s_q, heads,
+                                 rank, rope_dim, t_max, nullptr, nullptr, 0, softmax_scale, nullptr, 0, 0, nullptr,
+                                 device_status, false);
+  if (st != MLA_OK) return st;
+  MLA_CHECK(isfinite(softmax_scale) && softmax_scale > 0.f, "key_weights: softmax_scale must be positive");
+  return key_weights("key_weights", g, dtype, lse, decay, n_new, weights, weights_batch_stride, stream);
+}
+
+int mla_key_weights_q8(const void* q, int64_t q_row_stride, int64_t q_head_stride, const uint8_t* codes,
+                       int64_t codes_row_stride, int64_t codes_batch_stride, const uint8_t* scales,
+                       int64_t scales_batch_stride, int32_t scale_block, const void* rope, int64_t rope_row_stride,
+                       int64_t rope_batch_stride, int dtype, const int32_t* kv_start, const int32_t* kv_len,
+                       int32_t batch, int32_t s_q, int32_t heads, int32_t rank, int32_t rope_dim, int64_t t_max,
+                       const float* lse, float softmax_scale, float decay, int32_t n_new, float* weights,
+                       int64_t weights_batch_stride, int32_t* device_status, mla_stream_t stream) {
+  g_detail[0] = 0;
+  DecodeGeometry g;
+  int st = decode_geometry(g, q, q_row_stride, q_head_stride, codes, codes_row_stride, codes_batch_stride, rope,
+                           rope_row_stride, rope_batch_stride, dtype, kv_start, kv_len, batch, s_q, heads, rank,
+                           rope_dim, t_max, nullptr, nullptr, 0, softmax_scale, nullptr, 0, 0, nullptr, device_status,
+                           false);
+  if (st != MLA_OK) return st;
+  st = check_q8("key_weights_q8", codes, codes_row_stride, codes_batch_stride, scales, scales_batch_stride,
+                scale_block, rank, &g.block_shift);
+  if (st != MLA_OK) return st;
+  g.codes = codes;
+  g.codes_row_stride = codes_row_stride;
+  g.codes_batch_stride = codes_batch_stride;
+  g.scales = scales;
+  g.scales_batch_stride = scales_batch_stride;
+  MLA_CHECK(isfinite(softmax_scale) && softmax_scale > 0.f, "key_weights_q8: softmax_scale must be positive");
+  return key_weights("key_weights_q8", g, dtype, lse, decay, n_new, weights, weights_batch_stride, stream);
+}
+
+int mla_evict_plan(const float* weights, int64_t weights_batch_stride, const int32_t* kv_start, const int32_t* kv_len,
+                   int32_t batch, int64_t t_max, int32_t n_keep, int32_t n_sink, int32_t n_recent, int32_t* kept,
+                   int64_t kept_row_stride, int32_t* counts, int32_t* kv_len_out, int32_t* device_status,
+                   mla_stream_t stream) {
+  g_detail[0] = 0;
+  MLA_CHECK(weights && kv_len && kept && counts, "evict_plan: NULL pointer");
+  MLA_CHECK(batch > 0 && t_max > 0 && n_keep > 0, "evict_plan: batch, t_max and n_keep must be positive");
+  MLA_CHECK(batch <= 65535, "evict_plan: at most 65535 batch rows");
+  MLA_CHECK(t_max < (1LL << 31), "evict_plan: t_max must fit int32");
+  MLA_CHECK(n_sink >= 0 && n_recent >= 0 && (int64_t)n_sink + n_recent <= n_keep,
+            "evict_plan: n_sink %d and n_recent %d must be non-negative and fit n_keep %d", n_sink, n_recent, n_keep);
+  MLA_CHECK(weights_batch_stride >= 0 && kept_row_stride >= (batch > 1 ? n_keep : 0),
+            "evict_plan: strides too small");
+  EvictParams p{weights, weights_batch_stride, kv_start, kv_len, t_max, batch, n_keep, n_sink, n_recent, kept,
+                kept_row_stride, counts, kv_len_out, device_status};
+  return cuda_status(launch_evict_plan(p, (cudaStream_t)stream), "evict_plan launch");
+}
+
+int mla_cache_compact(const mla_state_array* arrays, int32_t n_arrays, const int32_t* kv_start, const int32_t* kept,
+                      int64_t kept_row_stride, const int32_t* counts, int32_t n_keep, int32_t batch, int64_t t_max,
+                      int32_t* device_status, mla_stream_t stream) {
+  g_detail[0] = 0;
+  MLA_CHECK(arrays && kept && counts, "cache_compact: NULL pointer");
+  MLA_CHECK(n_arrays > 0 && n_arrays <= kMaxStateArrays, "cache_compact: 1 to %d arrays", kMaxStateArrays);
+  MLA_CHECK(batch > 0 && batch <= 65535 && n_keep > 0 && t_max > 0 && t_max < (1LL << 31),
+            "cache_compact: batch, n_keep and t_max must be positive (batch <= 65535, t_max in int32)");
+  MLA_CHECK(kept_row_stride >= (batch > 1 ? n_keep : 0), "cache_compact: kept_row_stride < n_keep");
+  CompactParams p;
+  memset(&p, 0, sizeof(p));
+  for (int32_t i = 0; i < n_arrays; ++i) {
+    const mla_state_array& a = arrays[i];
+    MLA_CHECK(a.data, "cache_compact: array %d is NULL", i);
+    MLA_CHECK(a.row_bytes > 0 && a.token_stride_bytes >= a.row_bytes && a.batch_stride_bytes >= 0,
+              "cache_compact: array %d: strides too small", i);
+    int unit = 16;
+    while (unit > 1 && (reinterpret_cast<uintptr_t>(a.data) % unit || a.row_bytes % unit ||
+                        a.token_stride_bytes % unit || a.batch_stride_bytes % unit))
+      unit >>= 1;
+    p.a[i] = CompactArray{static_cast<uint8_t*>(a.data), a.token_stride_bytes, a.batch_stride_bytes, a.row_bytes, unit};
+  }
+  p.n_arrays = n_arrays;
+  p.kv_start = kv_start;
+  p.kept = kept;
+  p.kept_stride = kept_row_stride;
+  p.counts = counts;
+  p.n_keep = n_keep;
+  p.batch = batch;
+  p.t_max = t_max;
+  p.status = device_status;
+  return cuda_status(launch_compact(p, (cudaStream_t)stream), "cache_compact launch");
 }
 
 // ------------------------------------------------------------ reconstructed prefill

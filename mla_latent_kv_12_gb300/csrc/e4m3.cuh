@@ -1,0 +1,85 @@
+// The 8-bit latent: e4m3 codes (OCP 8-bit float: 1 sign, 4 exponent and 3
+// mantissa bits, bias 7, largest value 448, no infinity, NaN = 0x7F / 0xFF) in
+// units of a power of two 2^(e - 127) per block of buffer rows, e one byte in
+// [64, 134].
+//
+// Powers of two make every conversion but the first rounding exact: a code
+// times 2^(e - 127) has 4 significant bits and an exponent between -72 and 15,
+// so it is a normal bf16 (and f32), and moving a code to a larger unit only
+// loses what falls below e4m3's smallest step.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <stdint.h>
+
+namespace mla {
+
+constexpr int kMinExponent = 64, kMaxExponent = 134;   // 448 * 2^(134 - 127) = 57344, inside the fp16 range
+constexpr int kMaxScaleBlock = 64;                     // rows per exponent
+
+__host__ __device__ __forceinline__ int clamp_exponent(int e) {
+  return e < kMinExponent ? kMinExponent : (e > kMaxExponent ? kMaxExponent : e);
+}
+
+// The smallest exponent byte whose unit holds `amax` (>= 0): amax = f * 2^k with
+// 1 <= f < 2 fits 448 = 1.75 * 2^8 units when f <= 1.75 at unit 2^(k - 8), else at 2^(k - 7).
+__device__ __forceinline__ int exponent_for(float amax) {
+  const uint32_t bits = __float_as_uint(amax);
+  return clamp_exponent((int)(bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0));
+}
+
+__device__ __forceinline__ float unit_of(int e) { return __uint_as_float((uint32_t)e << 23); }
+__device__ __forceinline__ float inverse_unit_of(int e) { return __uint_as_float((uint32_t)(254 - e) << 23); }
+
+// Nearest e4m3 (ties to even), saturating at +-448; NaN becomes the NaN code.
+__device__ __forceinline__ uint16_t encode_e4m3x2(float lo, float hi) {
+  return (uint16_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint8_t encode_e4m3(float x) {
+  return (uint8_t)__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+}
+
+// code * unit in f32, exact: the code's exponent and mantissa bits placed at an
+// f32's read as the value times 2^-120 (also below the smallest normal e4m3).
+__device__ __forceinline__ float decode_e4m3(uint32_t code, float unit) {
+  const float mag = __uint_as_float((code & 0x7Fu) << 20) * 0x1p120f;
+  const float v = (code & 0x80u) ? -mag : mag;
+  return (code & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : v * unit;
+}
+
+// Sixteen codes to sixteen bf16 values (eight packed pairs), exact.  A code's
+// bits placed at a bf16's exponent and mantissa read as the value times
+// 2^-120; one packed multiplication by `mul2` = 2^(e - 7) in both halves
+// (bf16_unit) gives the value.  NaN codes would read as 480: a carry test
+// over all sixteen finds them, and a rare pass puts NaN there.
+__device__ __forceinline__ uint32_t bf16_unit(int e) { return (uint32_t)(e + 120) * 0x00800080u; }
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ void decode_e4m3x16(const uint4 codes, uint32_t mul2, uint32_t (&out)[8]) {
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+  uint32_t carry = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    carry |= (w[j] & 0x7F7F7F7Fu) + 0x01010101u;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t p = __byte_perm(w[j], 0, k ? 0x3424 : 0x1404);   // a code in the high byte of each half
+      out[2 * j + k] = mul_bf16x2(((p & 0x7F007F00u) >> 4) | (p & 0x80008000u), mul2);
+    }
+  }
+  if (carry & 0x80808080u) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t p = __byte_perm(w[j >> 1], 0, (j & 1) ? 0x3424 : 0x1404);
+      if ((p & 0x7F00u) == 0x7F00u) out[j] = (out[j] & 0xFFFF0000u) | 0x7FC0u;
+      if ((p & 0x7F000000u) == 0x7F000000u) out[j] = (out[j] & 0xFFFFu) | 0x7FC00000u;
+    }
+  }
+}
+
+}  // namespace mla

@@ -1,0 +1,369 @@
+// Eviction by accumulated attention weight: which tokens of a row stay, and
+// their compaction to the front of the row's window, in place.
+//
+// Plan.  A cluster of 1..8 CTAs per row.  Between the sinks and the recent
+// tokens the n_keep - n_sink - n_recent heaviest stay: their rank key is the
+// order-preserving map of the f32 bits to uint32, complemented (ascending key
+// = descending weight), and a radix selection (digits of 11, 11 and 10 bits)
+// finds the largest kept key and how many of its equals are kept.  Each CTA
+// holds its slice's keys in shared memory where they fit, so the weights
+// are read once; the digit histograms are summed over the cluster through
+// distributed shared memory, every CTA taking the same digit.  Bound by the latency of
+// the passes, not by the 4 bytes per token.
+//
+// Compaction.  Kept positions ascend, so row j's source kept[j] >= j: rows are
+// moved in chunks of consecutive j, each read whole before any of it is
+// written, and a chunk's writes only reach rows that no later chunk reads.  The
+// next chunk's loads are issued before the current one's stores (its sources
+// lie behind them), so the memory stays busy across the barrier.  Rows of a
+// window are one dependent chain; the parallelism is over batch rows and 64-byte
+// slices of a token's bytes, and over the CTAs of a cluster (which share each
+// chunk, with a cluster barrier) when those are few.
+#include "mla_internal.h"
+#include "tc_common.cuh"
+#include "tc_host.h"
+
+namespace mla {
+namespace {
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
+constexpr int kMaxHeldKeys = 40 * 1024;   // 160 KB of shared memory
+
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ int load_peer(const int* local, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(tc::mapa(tc::smem_u32(local), rank)) : "memory");
+  return v;
+}
+
+// Heavier tokens have smaller keys.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  const uint32_t bits = __float_as_uint(w);
+  return ~(bits ^ ((bits >> 31) ? 0xFFFFFFFFu : 0x80000000u));
+}
+
+// Exclusive prefix of `v` over the block's threads and the block's total.
+__device__ __forceinline__ int block_prefix(int v, int* warp_s, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) warp_s[warp] = inc;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanWarps; ++w) {
+    if (w < warp) before += warp_s[w];
+    total += warp_s[w];
+  }
+  __syncthreads();
+  return before + inc - v;
+}
+
+__global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __grid_constant__ EvictParams p, int held) {
+  extern __shared__ uint32_t keys_s[];   // `held` keys of this CTA's slice
+  __shared__ int hist[kBins];
+  __shared__ int warp_s[kPlanWarps];
+  __shared__ int tot_s[2];               // this CTA's kept and tied tokens
+  __shared__ int digit_s, rest_s;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const uint32_t crank = tc::cluster_ctarank();
+  const int ncta = (int)cluster_size();
+  const int b = blockIdx.x / ncta;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int len = p.kv_len[b], start = p.kv_start ? p.kv_start[b] : 0;
+  const bool fits = len >= 0 && start >= 0 && (int64_t)start + len <= p.t_max;
+  if (!fits || len <= p.n_keep) {   // the same in every CTA of the cluster
+    if (crank == 0 && threadIdx.x == 0) {
+      p.counts[b] = -1;
+      if (p.kv_len_out) p.kv_len_out[b] = len;
+      if (!fits && p.status) atomicOr(p.status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    return;
+  }
+  const float* w = p.weights + b * p.weights_batch_stride + start;
+  int32_t* kept = p.kept + b * p.kept_stride;
+  // candidates: window positions [n_sink, len - n_recent); this CTA's slice [lo, hi)
+  const int take = p.n_keep - p.n_sink - p.n_recent;
+  const int first = p.n_sink, last = len - p.n_recent;
+  const int span = ((last - first + ncta - 1) / ncta + 31) & ~31;
+  const int lo = min(last, first + (int)crank * span), hi = min(last, lo + span);
+  const bool in_smem = hi - lo <= held;
+  auto key_at = [&](int i) { return in_smem ? keys_s[i - lo] : weight_key(w[i]); };
+
+  uint32_t prefix = 0;
+  int rest = take;   // the rest-th smallest key among those with the prefix is looked for
+  if (take > 0) {
+    int known = 0;   // leading key bits fixed so far
+    for (int pass = 0; pass < 3; ++pass) {
+      const int width = pass < 2 ? 11 : 10, shift = 32 - known - width;
+      for (int i = threadIdx.x; i < kBins; i += kPlanThreads) hist[i] = 0;
+      __syncthreads();
+      constexpr int kLoads = 8;   // independent loads in flight per thread
+      for (int base = lo; base < hi; base += kPlanThreads * kLoads) {
+        uint32_t key[kLoads];
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+          const int i = base + u * kPlanThreads + threadIdx.x;
+          key[u] = 0;
+          if (i < hi) key[u] = pass == 0 ? weight_key(w[i]) : key_at(i);
+        }
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+          const int i = base + u * kPlanThreads + threadIdx.x;
+          if (pass == 0 && in_smem && i < hi) keys_s[i - lo] = key[u];
+          const bool counts = i < hi && (pass == 0 || (key[u] >> (32 - known)) == prefix);
+          const int digit = (int)((key[u] >> shift) & ((1u << width) - 1u));
+          // lanes that all hold one digit (weights that underflowed, say) add once
+          const uint32_t who = __ballot_sync(0xffffffffu, counts);
+          if (who == 0) continue;
+          const int leader = __ffs(who) - 1;
+          const int d0 = __shfl_sync(0xffffffffu, digit, leader);
+          if (__all_sync(0xffffffffu, !counts || digit == d0)) {
+            if (lane == leader) atomicAdd(&hist[d0], __popc(who));
+          } else if (counts) {
+            atomicAdd(&hist[digit], 1);
+          }
+        }
+      }
+      tc::cluster_sync();   // every CTA's histogram is complete
+      // thread t sums bins 4t .. 4t+3 over the cluster; the one whose bins hold the rest-th key takes it
+      const int nb = 1 << width, b0 = 4 * threadIdx.x;
+      int h[4] = {0, 0, 0, 0};
+      if (b0 < nb)
+        for (int c = 0; c < ncta; ++c)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) h[k] += load_peer(&hist[b0 + k], (uint32_t)c);
+      int all;
+      int before = block_prefix(h[0] + h[1] + h[2] + h[3], warp_s, all);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (before < rest && rest <= before + h[k]) {   // exactly one thread and bin
+          digit_s = b0 + k;
+          rest_s = rest - before;
+        }
+        before += h[k];
+      }
+      tc::cluster_sync();   // the histograms are read (they are cleared next pass); digit_s is written
+      prefix = (prefix << width) | (uint32_t)digit_s;
+      rest = rest_s;
+      known += width;
+    }
+  }
+  // ---- kept: keys below `prefix`, and the first `rest` positions that equal it.
+  // Warp w owns a contiguous part of the slice, so that ranks follow positions.
+  const int wspan = ((hi - lo + kPlanWarps - 1) / kPlanWarps + 31) & ~31;
+  const int wlo = min(hi, lo + warp * wspan), whi = min(hi, wlo + wspan);
+  int n_less = 0, n_tie = 0;
+  if (take > 0)
+    for (int i0 = wlo; i0 < whi; i0 += 32) {
+      const int i = i0 + lane;
+      const uint32_t key = i < whi ? key_at(i) : 0xFFFFFFFFu;
+      n_less += __popc(__ballot_sync(0xffffffffu, i < whi && key < prefix));
+      n_tie += __popc(__ballot_sync(0xffffffffu, i < whi && key == prefix));
+    }
+  int cta_less, cta_tie;
+  int before_less = block_prefix(lane == 0 ? n_less : 0, warp_s, cta_less);
+  int before_tie = block_prefix(lane == 0 ? n_tie : 0, warp_s, cta_tie);
+  if (threadIdx.x == 0) tot_s[0] = cta_less, tot_s[1] = cta_tie;
+  tc::cluster_sync();   // every CTA's totals are complete; every CTA has read kv_len
+  for (int c = 0; c < (int)crank; ++c) {
+    before_less += load_peer(&tot_s[0], (uint32_t)c);
+    before_tie += load_peer(&tot_s[1], (uint32_t)c);
+  }
+  before_less = __shfl_sync(0xffffffffu, before_less, 0);
+  before_tie = __shfl_sync(0xffffffffu, before_tie, 0);
+  if (take > 0) {
+    int out = p.n_sink + before_less + min(before_tie, rest), ties = before_tie;
+    const uint32_t below = (1u << lane) - 1u;
+    for (int i0 = wlo; i0 < whi; i0 += 32) {
+      const int i = i0 + lane;
+      const uint32_t key = i < whi ? key_at(i) : 0xFFFFFFFFu;
+      const uint32_t tie = __ballot_sync(0xffffffffu, i < whi && key == prefix);
+      const bool stays = i < whi && (key < prefix || (key == prefix && ties + __popc(tie & below) < rest));
+      const uint32_t who = __ballot_sync(0xffffffffu, stays);
+      if (stays) kept[out + __popc(who & below)] = i;
+      out += __popc(who);
+      ties += __popc(tie);
+    }
+  }
+  const int me = (int)crank * kPlanThreads + threadIdx.x;
+  for (int j = me; j < p.n_sink; j += ncta * kPlanThreads) kept[j] = j;
+  for (int j = me; j < p.n_recent; j += ncta * kPlanThreads) kept[p.n_keep - p.n_recent + j] = last + j;
+  if (crank == 0 && threadIdx.x == 0) {
+    p.counts[b] = p.n_keep;
+    if (p.kv_len_out) p.kv_len_out[b] = p.n_keep;
+  }
+  tc::cluster_sync();   // no CTA leaves while another may still read its shared memory
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ------------------------------------------------------------------ compaction
+
+constexpr int kMoveThreads = 512;
+constexpr int kMoves = 4;          // units in flight per thread and chunk
+constexpr int kSliceBytes = 64;    // of a token's bytes moved by one CTA
+
+struct Slice {
+  uint8_t* data;       // the slice's first byte of buffer row kv_start[b]
+  int64_t stride;      // bytes between buffer rows
+  int units;           // per row
+};
+
+template <typename V>
+__device__ __forceinline__ void move_rows(const Slice s, const CompactParams& p, const int32_t* kept, int count,
+                                          int start, int crank, int ncta, bool flags) {
+  // Thread i of the cluster moves unit i % units of rows i / units + k * rows_per_step
+  const int rows_cta = kMoveThreads / s.units;              // rows per step of this CTA
+  const int row0 = threadIdx.x / s.units, part = threadIdx.x % s.units;
+  const bool active = row0 < rows_cta;
+  const int step = rows_cta * ncta, chunk = step * kMoves;
+  auto row_of = [&](int c, int u) { return c * chunk + u * step + crank * rows_cta + row0; };
+  // The position of row j if it is one to move: above its predecessor's (so >= j), inside the buffer.
+  int pos[kMoves];
+  auto load_positions = [&](int c) {
+    int cur[kMoves], prev[kMoves];
+#pragma unroll
+    for (int u = 0; u < kMoves; ++u) {
+      const int j = row_of(c, u);
+      const bool in = active && j < count;
+      cur[u] = in ? __ldg(kept + j) : -1;
+      prev[u] = in && j > 0 ? __ldg(kept + j - 1) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kMoves; ++u) {
+      const int j = row_of(c, u);
+      const bool in = active && j < count;
+      const bool good = in && cur[u] >= j && cur[u] > prev[u] && (int64_t)start + cur[u] < p.t_max;
+      if (in && !good && flags && p.status) atomicOr(p.status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
+      pos[u] = good && cur[u] != j ? cur[u] : -1;   // a row already in place stays
+    }
+  };
+  V v[kMoves], next[kMoves];
+  bool moved[kMoves], next_moved[kMoves];
+  auto load_rows = [&](V(&dst)[kMoves], bool(&m)[kMoves]) {
+#pragma unroll
+    for (int u = 0; u < kMoves; ++u) {
+      m[u] = pos[u] >= 0;
+      if (m[u]) dst[u] = *(reinterpret_cast<const V*>(s.data + (int64_t)pos[u] * s.stride) + part);
+    }
+  };
+  const int n_chunks = (count + chunk - 1) / chunk;
+  load_positions(0);
+  load_rows(v, moved);
+  load_positions(1);
+  for (int c = 0; c < n_chunks; ++c) {
+    // every thread of the cluster has read its rows of chunk c
+    if (ncta > 1) tc::cluster_sync(); else __syncthreads();
+    load_rows(next, next_moved);   // chunk c + 1: its sources lie behind every row written below
+    load_positions(c + 2);
+#pragma unroll
+    for (int u = 0; u < kMoves; ++u) {
+      if (moved[u]) *(reinterpret_cast<V*>(s.data + (int64_t)row_of(c, u) * s.stride) + part) = v[u];
+      v[u] = next[u];
+      moved[u] = next_moved[u];
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kMoveThreads) compact_kernel(const __grid_constant__ CompactParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int ncta = (int)cluster_size();
+  const int crank = (int)tc::cluster_ctarank();
+  const int b = blockIdx.y;
+  int slice = blockIdx.x / ncta;
+  const bool flags = slice == 0;
+  const int count = p.counts[b], start = p.kv_start ? p.kv_start[b] : 0;
+  const bool good = count >= -1 && count <= p.n_keep;
+  const bool fits = start >= 0 && (int64_t)start + count <= p.t_max;
+  if (!good || !fits || count <= 0) {   // the same in the whole cluster
+    if (flags && crank == 0 && threadIdx.x == 0 && p.status) {
+      if (!good) atomicOr(p.status, MLA_DEVICE_BAD_SELECTION_COUNT);
+      else if (!fits) atomicOr(p.status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
+    }
+  } else {
+    // this CTA's array and slice
+    int k = 0;
+    auto slices_of = [&](int i) { return (p.a[i].row_bytes + kSliceBytes - 1) / kSliceBytes; };
+    while (slice >= slices_of(k)) slice -= slices_of(k++);
+    const CompactArray& a = p.a[k];
+    const int bytes = min(kSliceBytes, a.row_bytes - slice * kSliceBytes);
+    const Slice s{a.data + b * a.batch_bytes_stride + (int64_t)start * a.row_bytes_stride + slice * kSliceBytes,
+                  a.row_bytes_stride, bytes / a.unit};
+    const int32_t* kept = p.kept + b * p.kept_stride;
+    switch (a.unit) {
+      case 16: move_rows<uint4>(s, p, kept, count, start, crank, ncta, flags); break;
+      case 8: move_rows<uint2>(s, p, kept, count, start, crank, ncta, flags); break;
+      case 4: move_rows<uint32_t>(s, p, kept, count, start, crank, ncta, flags); break;
+      case 2: move_rows<uint16_t>(s, p, kept, count, start, crank, ncta, flags); break;
+      default: move_rows<uint8_t>(s, p, kept, count, start, crank, ncta, flags); break;
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, int threads, int smem, int ncta, cudaStream_t stream,
+                           Args... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)ncta;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_evict_plan(const EvictParams& p, cudaStream_t stream) {
+  // CTAs per row: one per 4096 candidates of the longest possible row, at most
+  // 8, and few enough that all rows run at once.
+  const int64_t most = p.t_max < 4096 ? 1 : p.t_max / 4096;
+  int ncta = 1;
+  while (ncta * 2 <= kMaxCluster && ncta * 2 <= most && (int64_t)ncta * 2 * p.batch <= device_sm_count()) ncta *= 2;
+  // a row's slice is at most ceil(t_max / ncta), rounded up to 32
+  const int64_t slice = (((p.t_max + ncta - 1) / ncta) + 31) & ~31LL;
+  const int held = (int)(slice < kMaxHeldKeys ? slice : 0);
+  if (held * 4 > 0) {
+    const cudaError_t ea = set_max_dynamic_smem(evict_plan_kernel, kMaxHeldKeys * 4);
+    if (ea != cudaSuccess) return ea;
+  }
+  return launch_cluster(evict_plan_kernel, dim3((unsigned)(p.batch * ncta)), kPlanThreads, held * 4, ncta, stream, p,
+                        held);
+}
+
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
+  int64_t slices = 0;
+  for (int i = 0; i < p.n_arrays; ++i) slices += (p.a[i].row_bytes + kSliceBytes - 1) / kSliceBytes;
+  // CTAs per slice: enough to fill the GPU twice, while each still has a chunk of rows
+  const int64_t chunks = (p.n_keep + kMoveThreads * kMoves / 4 - 1) / (kMoveThreads * kMoves / 4);
+  int ncta = 1;
+  while (ncta * 2 <= kMaxCluster && ncta * 2 <= chunks && slices * p.batch * ncta * 2 <= 2 * device_sm_count()) ncta *= 2;
+  if (slices * ncta > 0x7fffffffLL) return cudaErrorInvalidValue;
+  return launch_cluster(compact_kernel, dim3((unsigned)(slices * ncta), (unsigned)p.batch), kMoveThreads, 0, ncta,
+                        stream, p);
+}
+
+}  // namespace mla

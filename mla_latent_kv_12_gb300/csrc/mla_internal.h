@@ -46,6 +46,13 @@ struct DecodeGeometry {
   int64_t ctx_row_stride, ctx_head_stride;
   float* lse_out;
   int32_t* device_status;
+  // 8-bit cache (null codes: `latent` is read): e4m3 codes with byte strides,
+  // and one exponent byte per 2^block_shift buffer rows.
+  const uint8_t* codes;
+  int64_t codes_row_stride, codes_batch_stride;
+  const uint8_t* scales;
+  int64_t scales_batch_stride;
+  int32_t block_shift;
 };
 
 // CUDA-core decode of the f32 path (any shape; f32 q and cache).
@@ -135,6 +142,84 @@ struct AppendParams {
   float inv_freq[kMaxRotaryDims / 2];
 };
 cudaError_t launch_append(const AppendParams& p, int in_dtype, int cache_dtype, cudaStream_t stream);
+
+// Writing and reading an 8-bit latent cache (append, quantise, dequantise).
+struct EncodeParams {
+  const void* latent_raw;   // append: new tokens; quantise: the latent buffer
+  int64_t lr_row_stride, lr_tok_stride;
+  const void* rope_raw;
+  int64_t rr_row_stride, rr_tok_stride;
+  const void* weight;
+  float eps;
+  const int32_t* row_offsets;
+  uint8_t* codes;
+  int64_t codes_row_stride, codes_batch_stride;
+  uint8_t* scales;
+  int64_t scales_batch_stride;
+  int32_t block_shift;
+  void* rope;
+  int64_t rope_row_stride, rope_batch_stride;
+  void* latent_out;         // dequantise
+  int64_t lo_row_stride, lo_batch_stride;
+  const int32_t* kv_start;
+  const int32_t* kv_len;
+  int32_t* kv_len_out;
+  int32_t batch, s_new, rank, rope_dim;
+  int64_t t_max;
+  int32_t* status;
+  int32_t tile_rows, lengths_here;   // set by the launcher
+  float inv_freq[kMaxRotaryDims / 2];
+};
+cudaError_t launch_append_q8(const EncodeParams& p, int in_dtype, int rope_dtype, bool vec, cudaStream_t stream);
+cudaError_t launch_quantize(const EncodeParams& p, int dtype, bool vec, cudaStream_t stream);
+cudaError_t launch_dequantize(const EncodeParams& p, int dtype, bool vec, cudaStream_t stream);
+
+// Attention weight of every cached key, accumulated over heads and query tokens.
+struct KeyWeightParams {
+  DecodeGeometry g;         // q, cache, windows (ctx_out, lse_out and the selection unused)
+  const float* lse;
+  float* weights;
+  int64_t weights_batch_stride;
+  float decay;
+  int32_t n_new;
+};
+cudaError_t launch_simt_key_weights(const KeyWeightParams& p, cudaStream_t stream);
+cudaError_t launch_tc_key_weights(const KeyWeightParams& p, cudaStream_t stream);
+
+// Eviction: the kept positions of each row, and the in-place compaction.
+struct EvictParams {
+  const float* weights;
+  int64_t weights_batch_stride;
+  const int32_t* kv_start;
+  const int32_t* kv_len;
+  int64_t t_max;
+  int32_t batch, n_keep, n_sink, n_recent;
+  int32_t* kept;
+  int64_t kept_stride;
+  int32_t* counts;
+  int32_t* kv_len_out;
+  int32_t* status;
+};
+cudaError_t launch_evict_plan(const EvictParams& p, cudaStream_t stream);
+constexpr int kMaxStateArrays = 8;
+struct CompactArray {
+  uint8_t* data;
+  int64_t row_bytes_stride, batch_bytes_stride;
+  int32_t row_bytes;
+  int32_t unit;             // bytes moved together: 16, 8, 4, 2 or 1
+};
+struct CompactParams {
+  CompactArray a[kMaxStateArrays];
+  int32_t n_arrays;
+  const int32_t* kv_start;
+  const int32_t* kept;
+  int64_t kept_stride;
+  const int32_t* counts;
+  int32_t n_keep, batch;
+  int64_t t_max;
+  int32_t* status;
+};
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
 
 // Deterministic top-k selection of positions from per-row f32 scores.
 struct SelectParams {

@@ -7,6 +7,7 @@
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
+#include "e4m3.cuh"
 #include "mla_internal.h"
 
 namespace mla {
@@ -65,6 +66,16 @@ __device__ __forceinline__ RowKeys row_keys(const DecodeGeometry& g, int n) {
   return k;
 }
 
+// A window of an 8-bit cache must lie in the buffer and start on a whole block.
+__device__ __forceinline__ bool q8_window_ok(const DecodeGeometry& g, int b) {
+  const int start = g.kv_start ? g.kv_start[b] : 0, len = g.kv_len[b];
+  const bool fits = len >= 0 && start >= 0 && (int64_t)start + len <= g.t_max;
+  const bool ok = fits && (start & ((1 << g.block_shift) - 1)) == 0;
+  if (!ok && g.device_status)
+    atomicOr(g.device_status, fits ? MLA_DEVICE_BAD_BLOCK_START : MLA_DEVICE_INDEX_OUT_OF_RANGE);
+  return ok;
+}
+
 constexpr int kDecodeWarps = 4;
 constexpr int kMaxD = 1280;            // rank + rope
 constexpr int kMaxRank = 1024;
@@ -72,7 +83,8 @@ constexpr int kMaxRankPerLane = kMaxRank / 32;
 
 // grid (splits, heads, n_q); 4 warps.  Split s of row n covers entries
 // [s*chunk, (s+1)*chunk) of that row's key list, chunk = ceil(count/splits).
-template <typename T, typename TO>
+// kQ8: the latent comes from e4m3 codes and their block's exponent.
+template <typename T, typename TO, bool kQ8 = false>
 __global__ void __launch_bounds__(kDecodeWarps * 32)
     simt_decode_kernel(const __grid_constant__ DecodeGeometry g, float* __restrict__ ws, int splits) {
   const int split = blockIdx.x, h = blockIdx.y, n = blockIdx.z;
@@ -86,13 +98,16 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
   for (int d = threadIdx.x; d < D; d += blockDim.x) q_s[d] = to_f(qrow[d]);
   __syncthreads();
 
-  const RowKeys rk = row_keys(g, n);
+  RowKeys rk = row_keys(g, n);
+  if (kQ8 && !q8_window_ok(g, n / g.s_q)) rk.count = 0;
   const int chunk = (rk.count + splits - 1) / splits;
   const int lo = split * chunk;
   const int hi = min(rk.count, lo + chunk);
 
-  const T* lat = static_cast<const T*>(g.latent) + rk.batch_off_lat;
+  const T* lat = kQ8 ? nullptr : static_cast<const T*>(g.latent) + rk.batch_off_lat;
   const T* rop = static_cast<const T*>(g.rope) + rk.batch_off_rope;
+  const uint8_t* codes = kQ8 ? g.codes + (n / g.s_q) * g.codes_batch_stride : nullptr;
+  const uint8_t* scales = kQ8 ? g.scales + (n / g.s_q) * g.scales_batch_stride : nullptr;
 
   float m = -CUDART_INF_F, l = 0.f;
   float acc[kMaxRankPerLane];
@@ -109,7 +124,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
       }
     }
     const int64_t row = (int64_t)rk.start + t;
-    const T* lrow = lat + row * g.latent_row_stride;
+    const T* lrow = kQ8 ? nullptr : lat + row * g.latent_row_stride;
+    const uint8_t* crow = kQ8 ? codes + row * g.codes_row_stride : nullptr;
+    const float unit = kQ8 ? unit_of(clamp_exponent(scales[row >> g.block_shift])) : 1.f;
     const T* rrow = rop + row * g.rope_row_stride;
     float c[kMaxRankPerLane];
     float part = 0.f;
@@ -118,7 +135,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
       const int d = lane + 32 * j;
       c[j] = 0.f;
       if (d < g.rank) {
-        c[j] = to_f(lrow[d]);
+        if constexpr (kQ8) c[j] = decode_e4m3(crow[d], unit); else c[j] = to_f(lrow[d]);
         part = fmaf(q_s[d], c[j], part);
       }
     }
@@ -155,8 +172,10 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
     L += wgt[w] * l_s[w];
   }
   const int64_t slot = ((int64_t)n * splits + split) * g.heads + h;
+  // an 8-bit cache's NaN codes: a sum of NaN is no empty one
+  const bool some = kQ8 ? L != 0.f : L > 0.f;
   if (splits == 1) {
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = some ? 1.f / L : 0.f;
     TO* out = static_cast<TO*>(g.ctx_out) + (int64_t)n * g.ctx_row_stride + (int64_t)h * g.ctx_head_stride;
     for (int d = threadIdx.x; d < g.rank; d += blockDim.x) {
       float o = 0.f;
@@ -165,7 +184,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
       out[d] = cvt<TO>(o * inv);
     }
     if (threadIdx.x == 0 && g.lse_out)
-      g.lse_out[(int64_t)n * g.heads + h] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -CUDART_INF_F;
+      g.lse_out[(int64_t)n * g.heads + h] = some ? (M + log2f(L)) * 0.69314718055994531f : -CUDART_INF_F;
   } else {
     float* o_ws = ws + slot * g.rank;
     for (int d = threadIdx.x; d < g.rank; d += blockDim.x) {
@@ -177,7 +196,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
     const int64_t nslots = (int64_t)gridDim.z * splits * g.heads;
     if (threadIdx.x == 0) {
       float* ml = ws + nslots * g.rank;
-      ml[2 * slot] = (L > 0.f) ? M : -CUDART_INF_F;
+      ml[2 * slot] = !some ? -CUDART_INF_F : (kQ8 && M == -CUDART_INF_F) ? 0.f : M;
       ml[2 * slot + 1] = L;
     }
   }
@@ -201,7 +220,7 @@ __global__ void __launch_bounds__(128)
     const float ms = ml[2 * slot];
     if (ms != -CUDART_INF_F) L += exp2f(ms - M) * ml[2 * slot + 1];
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L != 0.f ? 1.f / L : 0.f;
   TO* out = static_cast<TO*>(g.ctx_out) + (int64_t)n * g.ctx_row_stride + (int64_t)h * g.ctx_head_stride;
   for (int d = threadIdx.x; d < g.rank; d += blockDim.x) {
     float o = 0.f;
@@ -213,7 +232,7 @@ __global__ void __launch_bounds__(128)
     out[d] = cvt<TO>(o * inv);
   }
   if (threadIdx.x == 0 && g.lse_out)
-    g.lse_out[(int64_t)n * g.heads + h] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -CUDART_INF_F;
+    g.lse_out[(int64_t)n * g.heads + h] = L != 0.f ? (M + log2f(L)) * 0.69314718055994531f : -CUDART_INF_F;
 }
 
 // ---------------------------------------------------------------- absorption
@@ -283,6 +302,66 @@ __global__ void __launch_bounds__(256) simt_project_kernel(const __grid_constant
   }
 }
 
+// ---------------------------------------------------------------- attention weight per key
+// grid (ceil(t_max / warps) capped, batch); one warp per window key: its row
+// stays in registers while every query row and head is scored against it, and
+// the probabilities are summed in one order.  Any shape, f32 arithmetic.
+constexpr int kWeightWarps = 8;
+constexpr int kMaxDPerLane = kMaxD / 32;
+
+template <bool kQ8>
+__global__ void __launch_bounds__(kWeightWarps * 32) simt_key_weights_kernel(const __grid_constant__ KeyWeightParams p) {
+  const DecodeGeometry& g = p.g;
+  const int b = blockIdx.y;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int start = g.kv_start ? g.kv_start[b] : 0, len = g.kv_len[b];
+  const bool fits = len >= 0 && start >= 0 && (int64_t)start + len <= g.t_max;
+  const bool ok = fits && (!kQ8 || (start & ((1 << g.block_shift) - 1)) == 0);
+  if (!ok) {
+    if (blockIdx.x == 0 && threadIdx.x == 0 && g.device_status)
+      atomicOr(g.device_status, fits ? MLA_DEVICE_BAD_BLOCK_START : MLA_DEVICE_INDEX_OUT_OF_RANGE);
+    return;
+  }
+  const int D = g.rank + g.rope_dim;
+  for (int64_t t = (int64_t)blockIdx.x * kWeightWarps + warp; t < len; t += (int64_t)gridDim.x * kWeightWarps) {
+    const int64_t row = start + t;
+    const float* lrow = kQ8 ? nullptr : static_cast<const float*>(g.latent) + b * g.latent_batch_stride + row * g.latent_row_stride;
+    const uint8_t* crow = kQ8 ? g.codes + b * g.codes_batch_stride + row * g.codes_row_stride : nullptr;
+    const float unit = kQ8 ? unit_of(clamp_exponent(g.scales[b * g.scales_batch_stride + (row >> g.block_shift)])) : 1.f;
+    const float* rrow = static_cast<const float*>(g.rope) + b * g.rope_batch_stride + row * g.rope_row_stride;
+    float key[kMaxDPerLane];
+#pragma unroll
+    for (int j = 0; j < kMaxDPerLane; ++j) {
+      const int d = lane + 32 * j;
+      key[j] = 0.f;
+      if (d < g.rank) {
+        if constexpr (kQ8) key[j] = decode_e4m3(crow[d], unit); else key[j] = lrow[d];
+      } else if (d < D) {
+        key[j] = rrow[d - g.rank];
+      }
+    }
+    float add = 0.f;
+    for (int i = 0; i < g.s_q; ++i) {
+      if (t > (int64_t)len - g.s_q + i) continue;   // this token does not see the key
+      const int64_t n = (int64_t)b * g.s_q + i;
+      for (int h = 0; h < g.heads; ++h) {
+        const float* q = static_cast<const float*>(g.q) + n * g.q_row_stride + h * g.q_head_stride;
+        float part = 0.f;
+#pragma unroll
+        for (int j = 0; j < kMaxDPerLane; ++j) {
+          const int d = lane + 32 * j;
+          if (d < D) part = fmaf(q[d], key[j], part);
+        }
+        add += exp2f(warp_sum(part) * g.scale_log2 - p.lse[n * g.heads + h] * 1.4426950408889634f);
+      }
+    }
+    if (lane == 0) {
+      float* w = p.weights + b * p.weights_batch_stride + row;
+      *w = (t < (int64_t)len - p.n_new && p.decay != 0.f ? p.decay * *w : 0.f) + add;
+    }
+  }
+}
+
 // ---------------------------------------------------------------- gather hook
 // grid (ceil(k_max/8), n_q); warp per output slot; raw element copies.
 template <typename T>
@@ -348,7 +427,22 @@ cudaError_t launch_simt_decode(const DecodeGeometry& g, int dtype, int out_dtype
   simt_decode_kernel<T, TO><<<grid, kDecodeWarps * 32, 0, stream>>>(g, ws, splits); \
   if (splits > 1) simt_combine_kernel<TO><<<dim3(g.heads, n_q), 128, 0, stream>>>(g, ws, splits);
   if (dtype != MLA_DTYPE_F32) return cudaErrorInvalidValue;
-  if (out_dtype == MLA_DTYPE_F32) { MLA_SIMT_DECODE(float, float) } else { MLA_SIMT_DECODE(float, __nv_bfloat16) }
+  if (g.codes != nullptr) {
+    if (out_dtype == MLA_DTYPE_F32)
+      simt_decode_kernel<float, float, true><<<grid, kDecodeWarps * 32, 0, stream>>>(g, ws, splits);
+    else
+      simt_decode_kernel<float, __nv_bfloat16, true><<<grid, kDecodeWarps * 32, 0, stream>>>(g, ws, splits);
+    if (splits > 1) {
+      if (out_dtype == MLA_DTYPE_F32)
+        simt_combine_kernel<float><<<dim3(g.heads, n_q), 128, 0, stream>>>(g, ws, splits);
+      else
+        simt_combine_kernel<__nv_bfloat16><<<dim3(g.heads, n_q), 128, 0, stream>>>(g, ws, splits);
+    }
+  } else if (out_dtype == MLA_DTYPE_F32) {
+    MLA_SIMT_DECODE(float, float)
+  } else {
+    MLA_SIMT_DECODE(float, __nv_bfloat16)
+  }
 #undef MLA_SIMT_DECODE
   return cudaGetLastError();
 }
@@ -369,6 +463,16 @@ cudaError_t launch_simt_project(const ProjectParams& p, int dtype, int out_dtype
     simt_project_kernel<float, float><<<grid, 256, smem, stream>>>(p);
   else
     simt_project_kernel<float, __nv_bfloat16><<<grid, 256, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_simt_key_weights(const KeyWeightParams& p, cudaStream_t stream) {
+  const int64_t gx = (p.g.t_max + kWeightWarps - 1) / kWeightWarps;
+  const dim3 grid((unsigned)(gx < 65535 ? gx : 65535), (unsigned)p.g.batch);
+  if (p.g.codes)
+    simt_key_weights_kernel<true><<<grid, kWeightWarps * 32, 0, stream>>>(p);
+  else
+    simt_key_weights_kernel<false><<<grid, kWeightWarps * 32, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

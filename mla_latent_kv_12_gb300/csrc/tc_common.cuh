@@ -178,6 +178,12 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+// x clamped to [-limit, limit]; NaN stays NaN.
+__device__ __forceinline__ float clamp_nan(float x, float limit) {
+  float d;
+  asm("{\n .reg .f32 t;\n max.NaN.f32 t, %1, %3;\n min.NaN.f32 %0, t, %2;\n}" : "=f"(d) : "f"(x), "f"(limit), "f"(-limit));
+  return d;
+}
 // (a0 + b0, a1 + b1) as one packed f32x2 addition.
 __device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
   uint64_t x, y, r;

@@ -42,6 +42,7 @@
 #include <cuda_fp16.h>
 #include <math_constants.h>
 
+#include "e4m3.cuh"
 #include "mla_internal.h"
 #include "tc_common.cuh"
 #include "tc_host.h"
@@ -68,6 +69,10 @@ constexpr int HEADS = 128, RANK = 512, DV = 256;  // DV: latent dims per CTA
 // more threads the dense kernel gets fewer registers and ran 3 % slower)
 constexpr int THREADS = 352, THREADS_GATHER = THREADS + 96;
 constexpr int kGatherWarp = 11;   // first extra gather warp
+// The instances for an 8-bit cache: the producer and three more warps fetch
+// the codes of each tile and write their bf16 values into the stage ring.
+constexpr int THREADS_Q8 = THREADS + 96;
+constexpr int kConvertWarps = 4;
 // Dynamic shared memory: the stage ring, then send[2] and receive[2].  The
 // 1024-byte alignment of the extern declaration places it on a 1024-byte
 // boundary after the static variables (checked at run time).
@@ -137,6 +142,13 @@ struct TcDecodeArgs {
   // kernel, which writes only the query and lets its dependants start only
   // after its own wait, so every other input is complete when this grid starts.
   int32_t early_inputs;
+  // 8-bit cache (null codes: `latent`); strides in bytes
+  const uint8_t* codes;
+  int64_t codes_row_stride, codes_batch_stride;
+  const uint8_t* scales;
+  int64_t scales_batch_stride;
+  int32_t block_shift;
+  int64_t t_max;
 };
 
 // ------------------------------------------------------------------ helpers
@@ -274,6 +286,16 @@ __device__ __forceinline__ void gather_key_group(const TcDecodeArgs& a, const CU
 // units.  Bad selection counts give 0 and are flagged where `flag` is set.
 __device__ __forceinline__ int row_keys(const TcDecodeArgs& a, int n, bool flag) {
   int keys = row_limit(a, n);
+  if (a.codes) {
+    // the 8-bit cache is read by plain loads: a window outside the buffer, or
+    // one that does not start on a whole block, is no window
+    const int b = n / a.s_q, start = a.kv_start ? a.kv_start[b] : 0, len = a.kv_len[b];
+    const bool fits = len >= 0 && start >= 0 && (int64_t)start + len <= a.t_max;
+    if (!fits || (start & ((1 << a.block_shift) - 1)) != 0) {
+      if (flag && a.status) atomicOr(a.status, fits ? MLA_DEVICE_BAD_BLOCK_START : MLA_DEVICE_INDEX_OUT_OF_RANGE);
+      return 0;
+    }
+  }
   if (a.sel) {
     const int c = a.sel_count[n];
     if (c != -1) {
@@ -419,7 +441,12 @@ __global__ void __launch_bounds__(1024) tc_plan_kernel(const __grid_constant__ T
 // MMAs instead of delaying them; single rows lose by the added P.V latency).
 // Without deadlock: the next tile's scores wait on the P.V STAGES tiles back
 // (its stage) and on the exchange of this tile's, in both CTAs, never on this P.V.
-template <int kPrefetchAhead, int kThreads, bool kLateP>
+// kQ8: the latent is held in 8 bits.  Four warps take the producer's place:
+// each thread fetches 16-byte pieces of codes a tile ahead (plain loads, so a
+// window and a selection are the same work), decodes them (e4m3.cuh: exact in
+// bf16, units applied) and writes them where the TMA box would have put them;
+// the rest of the kernel is the same.
+template <int kPrefetchAhead, int kThreads, bool kLateP, bool kQ8 = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_decode_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_constant__ CUtensorMap rope_map,
                      const __grid_constant__ CUtensorMap lat_rows_map, const __grid_constant__ CUtensorMap rope_rows_map,
@@ -456,14 +483,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const bool gather = a.sel != nullptr;
 
   if (threadIdx.x == 0) {
-    tma_prefetch_desc(&lat_map);
-    tma_prefetch_desc(&rope_map);
-    if (gather && a.gather_tma) {
-      tma_prefetch_desc(&lat_rows_map);
-      tma_prefetch_desc(&rope_rows_map);
+    if constexpr (!kQ8) {
+      tma_prefetch_desc(&lat_map);
+      tma_prefetch_desc(&rope_map);
+      if (gather && a.gather_tma) {
+        tma_prefetch_desc(&lat_rows_map);
+        tma_prefetch_desc(&rope_rows_map);
+      }
     }
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full_bar[s], (gather && !a.gather_tma) ? 32 : 1);
+      mbar_init(&full_bar[s], kQ8 ? kConvertWarps : (gather && !a.gather_tma) ? 32 : 1);
       mbar_init(&empty_bar[s], 1);
     }
     mbar_init(&s_full, 1);
@@ -515,7 +544,108 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (a.status) atomicOr(a.status, MLA_DEVICE_TIMEOUT);
   };
 
-  if (warp == 0) {
+  if (kQ8 && (warp == 0 || warp >= kGatherWarp)) {
+    // ============================================================ 8-bit producers
+    // Half a warp takes one key at a time, 16 of this CTA's 256 latent dims per
+    // lane: eight keys of each tile per thread (8i + 2w + half), and two
+    // 16-byte pieces of rope keys (lane group g: the half-warp's key g and g + 4).
+    const int cw = warp == 0 ? 0 : 1 + (warp - kGatherWarp);
+    const int c = lane & 15, key0 = 2 * cw + (lane >> 4);
+    const int rg = c >> 2, rp = c & 3;
+    int stage = 0;
+    uint32_t phase = 0;
+    int fills = 0;
+    int u, n, t0, t1;
+    bool whole;
+    while (!aborted() && it.next(u, t0, t1, whole)) {
+      if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
+      const int b = n / a.s_q;
+      const int start = a.plan_in_kernel ? row_start_s[n] : (a.kv_start ? a.kv_start[b] : 0);
+      const int limit = a.plan_in_kernel ? row_limit_s[n] : row_limit(a, n);
+      const int keys = keys_p[n];
+      const int32_t* list = (gather && a.sel_count[n] != -1) ? a.sel + (int64_t)n * a.k_max : nullptr;
+      const uint8_t* codes = a.codes + b * a.codes_batch_stride + dim_base + 16 * c;
+      const uint8_t* scales = a.scales + b * a.scales_batch_stride;
+      const __nv_bfloat16* ropes = a.rope + b * a.rope_batch_stride + 32 * (int)rank + 8 * rp;
+      // Window position of entry e, or -1: past the row's entries, or (flagged
+      // once, by the CTA and lane that own it) outside the visible window.
+      auto position = [&](int e, bool flag) -> int {
+        if (e >= keys) return -1;
+        if (!list) return e;
+        const int p = __ldg(list + e);
+        if (p >= 0 && p < limit) return p;
+        if (flag && a.status) atomicOr(a.status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
+        return -1;
+      };
+      uint4 code[8], rope[2];
+      int unit[8];   // the key's exponent byte
+      auto load_key = [&](int i, int pos) {
+        code[i] = make_uint4(0, 0, 0, 0);
+        unit[i] = 127;
+        if (pos >= 0) {
+          const int64_t row = (int64_t)start + pos;
+          code[i] = __ldg(reinterpret_cast<const uint4*>(codes + row * a.codes_row_stride));
+          unit[i] = __ldg(scales + (row >> a.block_shift));
+        }
+      };
+      auto load_rope = [&](int j, int pos) {
+        rope[j] = make_uint4(0, 0, 0, 0);
+        if (pos >= 0)
+          rope[j] = __ldg(reinterpret_cast<const uint4*>(ropes + ((int64_t)start + pos) * a.rope_row_stride));
+      };
+      const bool owner = rank == 0 && c == 0;   // flags a bad position of its keys
+#pragma unroll
+      for (int i = 0; i < 8; ++i) load_key(i, position(t0 * BN + 8 * i + key0, owner));
+#pragma unroll
+      for (int j = 0; j < 2; ++j) load_rope(j, position(t0 * BN + 8 * (4 * j + rg) + key0, false));
+      for (int t = t0; t < t1 && !aborted(); ++t) {
+        // the next tile's positions: read before the wait, used as this tile's registers free
+        int pos[8], rpos[2];
+        const bool more = t + 1 < t1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) pos[i] = more ? position((t + 1) * BN + 8 * i + key0, owner) : -1;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) rpos[j] = more ? position((t + 1) * BN + 8 * (4 * j + rg) + key0, false) : -1;
+        if (!list && t + kPrefetchAhead < t1) {
+          // a line of a later tile's codes, and of its rope keys, into L2
+          const int e = (t + kPrefetchAhead) * BN + (cw * 32 + lane) / 2;
+          if (e < keys) {
+            const int64_t row = (int64_t)start + e;
+            prefetch_l2(a.codes + b * a.codes_batch_stride + row * a.codes_row_stride + dim_base + 128 * (lane & 1));
+            if ((lane & 1) == 0)
+              prefetch_l2(a.rope + b * a.rope_batch_stride + row * a.rope_row_stride + 32 * (int)rank);
+          }
+        }
+        if (fills++ >= STAGES && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
+        uint8_t* st = stages + stage * STAGE_BYTES;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 8 * i + key0;
+          uint32_t v[8];
+          decode_e4m3x16(code[i], bf16_unit(clamp_exponent(unit[i])), v);
+          load_key(i, pos[i]);
+          // dims 16c .. 16c+15: 16-byte pieces 2(c % 4) and the next of box c / 4,
+          // at piece ^ (r % 8) (128-byte swizzle).  Odd boxes store their second
+          // piece first, so that eight neighbouring lanes hit eight different banks groups.
+          uint8_t* box = st + (c >> 2) * CHUNK_BYTES + r * 128;
+          const int first = (c >> 2) & 1, piece = 2 * (c & 3);
+          const uint4 lo = make_uint4(v[0], v[1], v[2], v[3]), hi = make_uint4(v[4], v[5], v[6], v[7]);
+          *reinterpret_cast<uint4*>(box + (((piece + first) ^ (r & 7)) << 4)) = first ? hi : lo;
+          *reinterpret_cast<uint4*>(box + (((piece + 1 - first) ^ (r & 7)) << 4)) = first ? lo : hi;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int r = 8 * (4 * j + rg) + key0;
+          *reinterpret_cast<uint4*>(st + 4 * CHUNK_BYTES + r * 64 + ((rp ^ ((r >> 1) & 3)) << 4)) = rope[j];
+          load_rope(j, rpos[j]);
+        }
+        fence_proxy_async_smem();   // generic-proxy writes, read by the MMAs
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full_bar[stage]);
+        if (++stage == STAGES) stage = 0, phase ^= 1u;
+      }
+    }
+  } else if (!kQ8 && warp == 0) {
     // ============================================================ producer
     int stage = 0;
     uint32_t phase = 0;
@@ -639,7 +769,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!mbar_wait_warp(&q_full, seg & 1u, kWaitLimit)) { fail(); break; }
       for (int t = t0; t < t1; ++t) {
         if (!mbar_wait_warp(&full_bar[stage], phase, kWaitLimit)) { fail(); break; }
-        if (!gather && t == (keys - 1) / BN && (keys % BN) != 0) {
+        if (!kQ8 && !gather && t == (keys - 1) / BN && (keys % BN) != 0) {
           // Tail tile: clear the rows past the window so that P = 0 never meets
           // a non-finite value left in the caller's buffer.
           const int valid = keys % BN;
@@ -652,7 +782,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (gather && !a.gather_tma) fence_proxy_async_smem();
+        if (!kQ8 && gather && !a.gather_tma) fence_proxy_async_smem();
         if (tile > 0 && !mbar_wait_warp(&s_free, (tile - 1) & 1u, kWaitLimit)) { fail(); break; }
         tc_fence_after();
         // 16 latent K-steps, then this CTA's two rope K-steps.  Descriptors
@@ -725,7 +855,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0) mma_commit(&pv_drain);
     __syncwarp();
     mbar_wait_warp(&pv_drain, 0, kWaitLimit);
-  } else if (kThreads > THREADS && warp >= kGatherWarp) {
+  } else if (!kQ8 && kThreads > THREADS && warp >= kGatherWarp) {
     // ============================================================ extra gather warps
     // Their share of the TMA row gathers of every tile (selected positions
     // only), following the producer's tiles, stages and stage waits.
@@ -866,7 +996,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             half_max = fmax3(half_max, fabsf(lo_raw), fabsf(hi_raw));
             // sent already scaled (log2 units): the softmax then only adds
             const float2 sc = mul_f32x2(make_float2(lo_raw, hi_raw), make_float2(a.scale_log2, a.scale_log2));
-            const __half2 hv = __floats2half2_rn(fminf(fmaxf(sc.x, -65504.f), 65504.f), fminf(fmaxf(sc.y, -65504.f), 65504.f));
+            // (an 8-bit cache's NaN codes stay NaN: clamp_nan keeps them)
+            const __half2 hv = kQ8 ? __floats2half2_rn(clamp_nan(sc.x, 65504.f), clamp_nan(sc.y, 65504.f))
+                                   : __floats2half2_rn(fminf(fmaxf(sc.x, -65504.f), 65504.f), fminf(fmaxf(sc.y, -65504.f), 65504.f));
             w[q] = *reinterpret_cast<const uint32_t*>(&hv);
           }
           *reinterpret_cast<uint4*>(xo + (c * 128 + h) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -1099,7 +1231,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (h >= a.heads) {
         // a padding row: nothing to store
       } else if (whole) {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l != 0.f ? 1.f / l : 0.f;   // 0: no entry; NaN stays NaN
         const int64_t off = (int64_t)n * a.ctx_row_stride + (int64_t)h * a.ctx_head_stride + dim_base;
         if (a.out_f32) {
           drain_o([&](int c, const uint32_t(&o)[32]) {
@@ -1121,7 +1253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           });
         }
         if (rank == 0 && a.lse)
-          a.lse[(int64_t)n * a.heads + h] = l > 0.f ? (m_used + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+          a.lse[(int64_t)n * a.heads + h] = l != 0.f ? (m_used + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
       } else {
         // Partial as [slot][RANK/8][H] entries of 8 fp16 dims: this piece's
         // context normalised by its own sum (O / l, an average of latent
@@ -1130,7 +1262,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // vector, a warp 512 B contiguous.  Stored with an evict-last L2
         // policy: the combine reads them after the whole decode, and the
         // cache stream would otherwise push the early pieces out to DRAM.
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        // m of the piece: -inf marks an empty one, so a sum of NaN alone gets a finite one
+        const float m_piece = l == 0.f ? -CUDART_INF_F : (kQ8 && m_used == -CUDART_INF_F) ? 0.f : m_used;
         const uint64_t keep = l2_policy_evict_last();
         uint4* dst = a.ws_o + (slot * (RANK / 8) + dim_base / 8) * HEADS + h;
         float vmax = 0.f;
@@ -1150,7 +1284,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         });
         if (!(vmax <= 65504.f) && a.status) atomicOr(a.status, MLA_DEVICE_VALUE_RANGE);
         if (rank == 0) {
-          st_global_f32_policy(a.ws_ml + (slot * 2) * HEADS + h, l > 0.f ? m_used : -CUDART_INF_F, keep);
+          st_global_f32_policy(a.ws_ml + (slot * 2) * HEADS + h, m_piece, keep);
           st_global_f32_policy(a.ws_ml + (slot * 2 + 1) * HEADS + h, l, keep);
         }
       }
@@ -1280,7 +1414,7 @@ __global__ void __launch_bounds__(128) tc_combine_kernel(const __grid_constant__
           for (int j = 0; j < CDIMS; ++j) acc[j] = (w != 0.f) ? fmaf(w, x[j], acc[j]) : acc[j];
         }
       }
-      const float inv = L > 0.f ? 1.f / L : 0.f;
+      const float inv = L != 0.f ? 1.f / L : 0.f;
 #pragma unroll
       for (int j = 0; j < CDIMS; ++j) acc[j] *= inv;
     }
@@ -1296,7 +1430,7 @@ __global__ void __launch_bounds__(128) tc_combine_kernel(const __grid_constant__
                      pack_bf16x2(acc[6], acc[7]));
     }
     if (blockIdx.y == 0 && a.lse)
-      a.lse[(int64_t)n * a.heads + h] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -CUDART_INF_F;
+      a.lse[(int64_t)n * a.heads + h] = L != 0.f ? (M + log2f(L)) * 0.69314718055994531f : -CUDART_INF_F;
   }
 }
 
@@ -1643,12 +1777,22 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
   a.batch_in_map = (g.latent_batch_stride != 0 || g.rope_batch_stride != 0) ? 1 : 0;
   a.plan_in_kernel = n_q <= kMaxRowsInKernelPlan ? 1 : 0;
   a.early_inputs = (tail != nullptr && a.plan_in_kernel) ? 1 : 0;
+  a.codes = g.codes;
+  a.codes_row_stride = g.codes_row_stride;
+  a.codes_batch_stride = g.codes_batch_stride;
+  a.scales = g.scales;
+  a.scales_batch_stride = g.scales_batch_stride;
+  a.block_shift = g.block_shift;
+  a.t_max = g.t_max;
+  a.gather_tma = 0;
+  a.lat_rows_per_batch = a.rope_rows_per_batch = 0;
 
   // Tensor maps over [B_buf, t_max, dims] (the batch axis has extent 1 for a
   // packed-flat cache whose batch stride is 0).
   const uint64_t bmap = a.batch_in_map ? (uint64_t)g.batch : 1;
-  CUtensorMap lat_map, rope_map;
-  {
+  const bool q8 = g.codes != nullptr;   // read by plain loads: no maps
+  CUtensorMap lat_map = {}, rope_map = {};
+  if (!q8) {
     const uint64_t dims[3] = {(uint64_t)g.rank, (uint64_t)g.t_max, bmap};
     const uint64_t bstride = a.batch_in_map ? (uint64_t)g.latent_batch_stride * 2
                                             : (uint64_t)g.t_max * g.latent_row_stride * 2;
@@ -1656,7 +1800,7 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
     const uint32_t box[3] = {64, BN, 1};
     if (!encode_tmap_bf16(&lat_map, g.latent, 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  {
+  if (!q8) {
     const uint64_t dims[3] = {(uint64_t)g.rope_dim, (uint64_t)g.t_max, bmap};
     const uint64_t bstride = a.batch_in_map ? (uint64_t)g.rope_batch_stride * 2
                                             : (uint64_t)g.t_max * g.rope_row_stride * 2;
@@ -1668,9 +1812,7 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
   // Row maps for gathers: the cache as [rows, dims] with one-row boxes; a
   // batch row's rows start at b * (batch stride / row stride).
   CUtensorMap lat_rows_map = lat_map, rope_rows_map = rope_map;
-  a.gather_tma = 0;
-  a.lat_rows_per_batch = a.rope_rows_per_batch = 0;
-  if (g.sel != nullptr && g.latent_batch_stride % g.latent_row_stride == 0 &&
+  if (!q8 && g.sel != nullptr && g.latent_batch_stride % g.latent_row_stride == 0 &&
       g.rope_batch_stride % g.rope_row_stride == 0) {
     a.lat_rows_per_batch = a.batch_in_map ? (int32_t)(g.latent_batch_stride / g.latent_row_stride) : 0;
     a.rope_rows_per_batch = a.batch_in_map ? (int32_t)(g.rope_batch_stride / g.rope_row_stride) : 0;
@@ -1686,7 +1828,9 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
   const bool lockstep = a.width > 1;
   // (the prefetch distance only serves the dense path; gathers take the
   // instance with the extra gather warps)
-  auto* const decode_kernel = a.gather_tma ? tc_decode_kernel<kPrefetchAheadRow, THREADS_GATHER, false>
+  auto* const decode_kernel = q8 && lockstep ? tc_decode_kernel<kPrefetchAheadGroup, THREADS_Q8, true, true>
+                              : q8         ? tc_decode_kernel<kPrefetchAheadRow, THREADS_Q8, false, true>
+                              : a.gather_tma ? tc_decode_kernel<kPrefetchAheadRow, THREADS_GATHER, false>
                               : lockstep   ? tc_decode_kernel<kPrefetchAheadGroup, THREADS, true>
                                            : tc_decode_kernel<kPrefetchAheadRow, THREADS, false>;
   {
@@ -1698,7 +1842,7 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
     e = launch_pdl(tc_plan_kernel, dim3(1), dim3(1024), 0, stream, a);
     if (e != cudaSuccess) return e;
   }
-  e = launch_pdl(decode_kernel, dim3(2 * nclusters), dim3(a.gather_tma ? THREADS_GATHER : THREADS), SMEM_BYTES, stream,
+  e = launch_pdl(decode_kernel, dim3(2 * nclusters), dim3(q8 ? THREADS_Q8 : a.gather_tma ? THREADS_GATHER : THREADS), SMEM_BYTES, stream,
                  lat_map, rope_map, lat_rows_map, rope_rows_map, a);
   if (e != cudaSuccess) return e;
   if (tail == nullptr) {

@@ -1,0 +1,464 @@
+// Accumulated attention weight of every cached key on the tensor cores:
+//   W_t <- decay W_t + sum_{i, h} 2^(s_{i,h,t} scale log2(e) - lse_{i,h} log2(e)).
+//
+// The scores are one GEMM per query token, S[128 heads x 64 keys] =
+// Q[128 x 576] . K^T, with the probabilities normalised by a given lse, so
+// nothing has to be known about other keys: each tile of 64 keys is finished
+// on its own.  The whole query of a token fits TMEM as the MMA's A operand (288
+// columns of packed bf16) beside two score buffers (2 x 64), so a CTA scores
+// all 576 features itself and no SM pair is needed.  At one query token it is
+// bound by the cache read (1152 or 641 bytes against 147 kflop per key: 0.17
+// or 0.09 ns at the measured copy rate, 0.076 ns at the measured bf16 rate).
+//
+//  * One persistent CTA per SM takes an equal range of the flattened tiles of
+//    all rows.  With several query tokens a range is walked in chunks that
+//    stay in L2, once per token: the weights of a key are always updated by
+//    the same thread, in token order (no atomics, the same bits every time).
+//  * bf16 cache: warp 0 loads [64 keys x 576] tiles by TMA into a three-stage
+//    ring (nine boxes of 64 dims, 128-byte swizzle).  8-bit cache: warps 6..13
+//    fetch codes a tile ahead by plain loads and write decoded bf16 into
+//    the same layout.
+//  * Warp 1 issues the 36 MMAs of a tile.  Warps 2..5 (one thread per head)
+//    load each token's query into TMEM, turn scores into probabilities and
+//    sum them over their 32 heads with a shuffle tree that halves the keys per
+//    lane at every step; the four warps' sums meet in shared memory.
+#include <cuda_bf16.h>
+
+#include "e4m3.cuh"
+#include "mla_internal.h"
+#include "tc_common.cuh"
+#include "tc_host.h"
+
+namespace mla {
+namespace {
+
+using namespace tc;
+
+constexpr int BN = 64;                    // keys per tile
+constexpr int BOX_BYTES = BN * 128;       // [64 keys][64 dims] bf16
+constexpr int BOXES = 9;                  // 8 of latent dims, 1 of rope dims
+constexpr int STAGE_BYTES = BOXES * BOX_BYTES;
+constexpr int STAGES = 3;
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES;
+constexpr uint32_t TM_Q = 0, TM_S = 288;  // TMEM columns
+constexpr int kThreads = 192, kThreadsQ8 = 448;
+constexpr int kConvertWarp = 6, kConvertWarps = 8;
+constexpr long long kWaitLimit = 1LL << 32;   // clock cycles (~2 s)
+// Tiles that several query tokens share before the next ones are read: 152
+// CTAs x 8 tiles x 72 KB = 88 MB stays in the 129 MB L2.
+constexpr int kChunkTiles = 8;
+// Tiles ahead of the conversion that an 8-bit cache is pulled into L2.
+constexpr int kPrefetchAhead = 3;
+
+struct WeightArgs {
+  DecodeGeometry g;
+  const float* lse;
+  float* weights;
+  int64_t weights_batch_stride;
+  float decay;
+  int32_t n_new;
+  int32_t batch_in_map;
+};
+
+__device__ __forceinline__ int window_tiles(const DecodeGeometry& g, int b, bool flag) {
+  const int start = g.kv_start ? g.kv_start[b] : 0, len = g.kv_len[b];
+  const bool fits = len >= 0 && start >= 0 && (int64_t)start + len <= g.t_max;
+  const bool ok = fits && (!g.codes || (start & ((1 << g.block_shift) - 1)) == 0);
+  if (!ok) {
+    if (flag && g.device_status)
+      atomicOr(g.device_status, fits ? MLA_DEVICE_BAD_BLOCK_START : MLA_DEVICE_INDEX_OUT_OF_RANGE);
+    return 0;
+  }
+  return (len + BN - 1) / BN;
+}
+
+// A CTA's share of the work: passes of one query token over tiles [t0, t1) of one batch row.
+struct Passes {
+  int b, t, left, row_tiles;   // current row, next tile, tiles left in the CTA's range, tiles of the row
+  int i, t0, t1;               // token, current chunk
+  __device__ void init(int b0, int first, int count, const DecodeGeometry& g) {
+    b = b0;
+    t = first;
+    left = count;
+    row_tiles = count > 0 ? window_tiles(g, b, false) : 0;
+    i = g.s_q;                 // no chunk yet
+    t0 = t1 = 0;
+  }
+  // The next pass; `fresh`: its query is not the previous pass's.
+  __device__ bool next(const DecodeGeometry& g, bool& fresh) {
+    fresh = true;
+    if (i + 1 < g.s_q) {
+      ++i;
+      return true;
+    }
+    if (left <= 0) return false;
+    const int was = i == g.s_q ? -1 : b;
+    while (t >= row_tiles) {
+      ++b;
+      t = 0;
+      row_tiles = window_tiles(g, b, false);
+    }
+    int n = min(left, row_tiles - t);
+    if (g.s_q > 1) n = min(n, kChunkTiles);
+    i = 0;
+    t0 = t;
+    t1 = t + n;
+    t += n;
+    left -= n;
+    fresh = g.s_q > 1 || was != b;
+    return true;
+  }
+};
+
+template <bool kQ8>
+__global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
+    tc_key_weights_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_constant__ CUtensorMap rope_map,
+                          const __grid_constant__ WeightArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if ((smem_u32(smem_raw) & 1023u) != 0) {   // the same in every CTA: nothing waits on anything yet
+    if (threadIdx.x == 0 && a.g.device_status) atomicOr(a.g.device_status, MLA_DEVICE_LAYOUT);
+    return;
+  }
+  uint8_t* stages = smem_raw;
+  __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES], s_full[2], s_free[2], q_full, drain;
+  __shared__ uint32_t tmem_base_s;
+  __shared__ volatile int abort_s;
+  __shared__ int first_row_s, first_tile_s, count_s;
+  __shared__ __align__(16) float part_s[2][4][BN];   // stored as float2
+  const DecodeGeometry& g = a.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    if constexpr (!kQ8) {
+      tma_prefetch_desc(&lat_map);
+      tma_prefetch_desc(&rope_map);
+    }
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full_bar[s], kQ8 ? kConvertWarps : 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(&s_full[k], 1);
+      mbar_init(&s_free[k], 4);
+    }
+    mbar_init(&q_full, 4);
+    mbar_init(&drain, 1);
+    abort_s = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_base_s, 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  if (warp == 0) {
+    // This CTA's tiles of the flattened sequence: the rows' tiles are counted
+    // (32 rows at a time), then walked again to the range's first row.
+    int total = 0;
+    for (int b0 = 0; b0 < g.batch; b0 += 32)
+      total += b0 + lane < g.batch ? window_tiles(g, b0 + lane, blockIdx.x == 0) : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const int per = (total + gridDim.x - 1) / (int)gridDim.x;
+    const long long begin = (long long)per * blockIdx.x;
+    const int count = (int)max(0LL, min((long long)per, (long long)total - begin));
+    if (lane == 0) count_s = count;
+    int before = 0;
+    for (int b0 = 0; count > 0 && b0 < g.batch; b0 += 32) {
+      const int mine = b0 + lane < g.batch ? window_tiles(g, b0 + lane, false) : 0;
+      int inc = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      const int lo = before + inc - mine;
+      const bool here = begin >= lo && begin < before + inc;
+      if (here) {
+        first_row_s = b0 + lane;
+        first_tile_s = (int)(begin - lo);
+      }
+      if (__any_sync(0xffffffffu, here)) break;
+      before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_s;
+  auto aborted = [&]() -> bool { return __any_sync(0xffffffffu, abort_s != 0); };
+  auto fail = [&]() {
+    abort_s = 1;
+    if (g.device_status) atomicOr(g.device_status, MLA_DEVICE_TIMEOUT);
+  };
+  Passes it;
+  it.init(count_s > 0 ? first_row_s : 0, count_s > 0 ? first_tile_s : 0, count_s, g);
+  bool fresh;
+
+  if (!kQ8 && warp == 0) {
+    // ============================================================ TMA producer
+    int stage = 0, fills = 0;
+    uint32_t phase = 0;
+    while (!aborted() && it.next(g, fresh)) {
+      const int start = g.kv_start ? g.kv_start[it.b] : 0;
+      const int z = a.batch_in_map ? it.b : 0;
+      for (int t = it.t0; t < it.t1; ++t) {
+        if (fills++ >= STAGES && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&full_bar[stage], STAGE_BYTES);
+          uint8_t* st = stages + stage * STAGE_BYTES;
+          for (int c = 0; c < 8; ++c)
+            tma_load_3d(st + c * BOX_BYTES, &lat_map, &full_bar[stage], 64 * c, start + t * BN, z);
+          tma_load_3d(st + 8 * BOX_BYTES, &rope_map, &full_bar[stage], 0, start + t * BN, z);
+        }
+        __syncwarp();
+        if (++stage == STAGES) stage = 0, phase ^= 1u;
+      }
+    }
+    // every issued load lands before this CTA may exit: fill k of a stage completes its phase k
+    for (int k = fills > STAGES ? fills - STAGES : 0; k < fills; ++k)
+      mbar_wait_warp(&full_bar[k % STAGES], (uint32_t)(k / STAGES) & 1u, kWaitLimit);
+  } else if (kQ8 && warp >= kConvertWarp) {
+    // ============================================================ 8-bit producers
+    // A warp takes one key at a time, 16 latent dims per lane: keys 8i + w of a
+    // tile; and two 16-byte pieces of rope keys (lane group g: key 8g + w and 8(g + 4) + w).
+    const int cw = warp - kConvertWarp;
+    const int rg = lane >> 3, rp = lane & 7;
+    int stage = 0, fills = 0;
+    uint32_t phase = 0;
+    while (!aborted() && it.next(g, fresh)) {
+      const int b = it.b, len = g.kv_len[b];
+      const int64_t start = g.kv_start ? g.kv_start[b] : 0;
+      const uint8_t* codes = g.codes + b * g.codes_batch_stride + 16 * lane;
+      const uint8_t* scales = g.scales + b * g.scales_batch_stride;
+      const __nv_bfloat16* ropes = static_cast<const __nv_bfloat16*>(g.rope) + b * g.rope_batch_stride + 8 * rp;
+      uint4 code[8], rope[2];
+      int unit[8];
+      auto load_key = [&](int i, int e) {
+        code[i] = make_uint4(0, 0, 0, 0);
+        unit[i] = 127;
+        if (e < len) {
+          code[i] = __ldg(reinterpret_cast<const uint4*>(codes + (start + e) * g.codes_row_stride));
+          unit[i] = __ldg(scales + ((start + e) >> g.block_shift));
+        }
+      };
+      auto load_rope = [&](int j, int e) {
+        rope[j] = make_uint4(0, 0, 0, 0);
+        if (e < len) rope[j] = __ldg(reinterpret_cast<const uint4*>(ropes + (start + e) * g.rope_row_stride));
+      };
+#pragma unroll
+      for (int i = 0; i < 8; ++i) load_key(i, it.t0 * BN + 8 * i + cw);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) load_rope(j, it.t0 * BN + 8 * (4 * j + rg) + cw);
+      for (int t = it.t0; t < it.t1; ++t) {
+        const int after = t + 1 < it.t1 ? (t + 1) * BN : len;   // `len`: nothing more to load
+        if (t + kPrefetchAhead < it.t1) {
+          const int tid = cw * 32 + lane;   // 256 threads: four lines of codes per key, one of rope keys
+          const int e = (t + kPrefetchAhead) * BN + (tid >> 2);
+          if (e < len) {
+            prefetch_l2(g.codes + b * g.codes_batch_stride + (start + e) * g.codes_row_stride + 128 * (tid & 3));
+            if ((tid & 3) == 0)
+              prefetch_l2(static_cast<const __nv_bfloat16*>(g.rope) + b * g.rope_batch_stride + (start + e) * g.rope_row_stride);
+          }
+        }
+        if (fills++ >= STAGES && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
+        uint8_t* st = stages + stage * STAGE_BYTES;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 8 * i + cw;
+          uint32_t v[8];
+          decode_e4m3x16(code[i], bf16_unit(clamp_exponent(unit[i])), v);
+          load_key(i, after + r);
+          // dims 16 lane .. +15: pieces 2(lane % 4) and the next of box lane / 4, at piece ^ (r % 8);
+          // odd boxes store their second piece first (eight lanes, eight bank groups)
+          uint8_t* box = st + (lane >> 2) * BOX_BYTES + r * 128;
+          const int first = (lane >> 2) & 1, piece = 2 * (lane & 3);
+          const uint4 lo = make_uint4(v[0], v[1], v[2], v[3]), hi = make_uint4(v[4], v[5], v[6], v[7]);
+          *reinterpret_cast<uint4*>(box + (((piece + first) ^ (r & 7)) << 4)) = first ? hi : lo;
+          *reinterpret_cast<uint4*>(box + (((piece + 1 - first) ^ (r & 7)) << 4)) = first ? lo : hi;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int r = 8 * (4 * j + rg) + cw;
+          *reinterpret_cast<uint4*>(st + 8 * BOX_BYTES + r * 128 + ((rp ^ (r & 7)) << 4)) = rope[j];
+          load_rope(j, after + r);
+        }
+        fence_proxy_async_smem();   // generic-proxy writes, read by the MMAs
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full_bar[stage]);
+        if (++stage == STAGES) stage = 0, phase ^= 1u;
+      }
+    }
+  } else if (warp == 1) {
+    // ============================================================ MMA issuer
+    const uint32_t idesc = idesc_bf16_f32(128, BN, 0, 0);
+    int stage = 0;
+    uint32_t phase = 0, tile = 0, queries = 0;
+    while (!aborted() && it.next(g, fresh)) {
+      if (fresh && !mbar_wait_warp(&q_full, queries++ & 1u, kWaitLimit)) { fail(); break; }
+      for (int t = it.t0; t < it.t1; ++t, ++tile) {
+        const uint32_t buf = tile & 1u;
+        if (tile >= 2 && !mbar_wait_warp(&s_free[buf], ((tile >> 1) - 1) & 1u, kWaitLimit)) { fail(); break; }
+        if (!mbar_wait_warp(&full_bar[stage], phase, kWaitLimit)) { fail(); break; }
+        tc_fence_after();
+        const uint64_t d0 = smem_desc(smem_u32(stages + stage * STAGE_BYTES), 16, 1024, kSwizzle128B);
+        if (elect_one()) {
+#pragma unroll
+          for (int c = 0; c < BOXES; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ts(tmem + TM_S + buf * BN, tmem + TM_Q + c * 32 + k * 8,
+                     d0 + (uint64_t)((c * BOX_BYTES + k * 32) >> 4), idesc, (c | k) != 0);
+          mma_commit(&empty_bar[stage]);
+          mma_commit(&s_full[buf]);
+        }
+        __syncwarp();
+        if (++stage == STAGES) stage = 0, phase ^= 1u;
+      }
+    }
+    if (lane == 0) mma_commit(&drain);   // every MMA completes before TMEM is released
+    __syncwarp();
+    mbar_wait_warp(&drain, 0, kWaitLimit);
+  } else if (warp >= 2 && warp < 6) {
+    // ============================================================ probabilities and sums
+    const int quarter = warp & 3;
+    const int h = 32 * quarter + lane;
+    const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
+    const bool real = h < g.heads;
+    const int k_mine = threadIdx.x - 64;      // key of the tile whose weight this thread updates (warps 2, 3)
+    uint32_t tile = 0;
+    float lse2 = 0.f;
+    // The four warps meet in a barrier at every tile, so they leave together.
+    bool stop = false;
+    while (!stop && it.next(g, fresh)) {
+      const int b = it.b, len = g.kv_len[b];
+      const int64_t start = g.kv_start ? g.kv_start[b] : 0;
+      const int limit = min(len, len - g.s_q + it.i + 1);
+      if (fresh) {
+        // This head's query into TMEM: every MMA of the previous pass has
+        // completed (its last scores were read here).  Padding rows are zero.
+        const int64_t n = (int64_t)b * g.s_q + it.i;
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(g.q) + n * g.q_row_stride +
+                                                        (int64_t)h * g.q_head_stride);
+        lse2 = real ? a.lse[n * g.heads + h] * 1.4426950408889634f : 0.f;
+#pragma unroll
+        for (int c = 0; c < BOXES; c += 3) {
+          uint4 qv[24];
+#pragma unroll
+          for (int v = 0; v < 24; ++v) qv[v] = real ? __ldg(q + 8 * c + v) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int d = 0; d < 3; ++d) {
+            uint32_t r[32];
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              r[4 * v] = qv[8 * d + v].x, r[4 * v + 1] = qv[8 * d + v].y, r[4 * v + 2] = qv[8 * d + v].z,
+              r[4 * v + 3] = qv[8 * d + v].w;
+            tmem_st32(tmem + TM_Q + (c + d) * 32 + lane_off, r);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full);
+      }
+      float* w_row = a.weights + b * a.weights_batch_stride + start;
+      for (int t = it.t0; t < it.t1; ++t, ++tile) {
+        const uint32_t buf = tile & 1u;
+        const int key = t * BN + k_mine;
+        // the weight so far, read ahead of the scores; the first token's pass decays it
+        float old = 0.f;
+        if (k_mine < BN && key < len) {
+          if (it.i > 0)
+            old = w_row[key];
+          else if (a.decay != 0.f && key < (int64_t)len - a.n_new)
+            old = a.decay * w_row[key];
+        }
+        const bool arrived = mbar_wait_warp(&s_full[buf], (tile >> 1) & 1u, kWaitLimit);
+        tc_fence_after();
+        uint32_t s0[32], s1[32];
+        tmem_ld32(tmem + TM_S + buf * BN + lane_off, s0);
+        tmem_ld32(tmem + TM_S + buf * BN + 32 + lane_off, s1);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[buf]);
+        float p[BN];
+#pragma unroll
+        for (int k = 0; k < BN; ++k)
+          p[k] = ex2_approx(fmaf(__uint_as_float(k < 32 ? s0[k] : s1[k - 32]), g.scale_log2, -lse2));
+        if ((t + 1) * BN > limit) {
+          // keys that this token does not see, and rows past the window (which may hold anything)
+#pragma unroll
+          for (int k = 0; k < BN; ++k) p[k] = t * BN + k < limit ? p[k] : 0.f;
+        }
+        // Sum over the warp's heads: each step halves the keys a lane holds.
+        // Lane l ends with keys 2l and 2l + 1.
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const bool upper = (lane & o) != 0;
+#pragma unroll
+          for (int k = 0; k < 2 * o; ++k) {
+            const float keep = upper ? p[k + 2 * o] : p[k], send = upper ? p[k] : p[k + 2 * o];
+            p[k] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+          }
+        }
+        // (64 heads: quarters 2 and 3 hold padding rows only)
+        *reinterpret_cast<float2*>(&part_s[buf][quarter][2 * lane]) = real ? make_float2(p[0], p[1]) : make_float2(0.f, 0.f);
+        // (a buffer is rewritten two tiles later, behind the next tile's barrier)
+        stop = named_sync_or(1, 128, !arrived || abort_s != 0);
+        if (stop) {
+          if (!arrived) fail();
+          break;
+        }
+        if (k_mine < BN && key < len)
+          w_row[key] = old + ((part_s[buf][0][k_mine] + part_s[buf][1][k_mine]) +
+                              (part_s[buf][2][k_mine] + part_s[buf][3][k_mine]));
+      }
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  pdl_trigger();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_tc_key_weights(const KeyWeightParams& p, cudaStream_t stream) {
+  WeightArgs a;
+  a.g = p.g;
+  a.lse = p.lse;
+  a.weights = p.weights;
+  a.weights_batch_stride = p.weights_batch_stride;
+  a.decay = p.decay;
+  a.n_new = p.n_new;
+  const DecodeGeometry& g = p.g;
+  a.batch_in_map = (g.latent_batch_stride != 0 || g.rope_batch_stride != 0) ? 1 : 0;
+  const bool q8 = g.codes != nullptr;
+  CUtensorMap lat_map = {}, rope_map = {};
+  if (!q8) {
+    const uint64_t bmap = a.batch_in_map ? (uint64_t)g.batch : 1;
+    const uint32_t box[3] = {64, BN, 1};
+    const uint64_t ld[3] = {(uint64_t)g.rank, (uint64_t)g.t_max, bmap};
+    const uint64_t ls[2] = {(uint64_t)g.latent_row_stride * 2,
+                            (a.batch_in_map ? (uint64_t)g.latent_batch_stride : (uint64_t)g.t_max * g.latent_row_stride) * 2};
+    const uint64_t rd[3] = {(uint64_t)g.rope_dim, (uint64_t)g.t_max, bmap};
+    const uint64_t rs[2] = {(uint64_t)g.rope_row_stride * 2,
+                            (a.batch_in_map ? (uint64_t)g.rope_batch_stride : (uint64_t)g.t_max * g.rope_row_stride) * 2};
+    if (!encode_tmap_bf16(&lat_map, g.latent, 3, ld, ls, box) || !encode_tmap_bf16(&rope_map, g.rope, 3, rd, rs, box))
+      return cudaErrorInvalidValue;
+  }
+  auto* const kernel = q8 ? tc_key_weights_kernel<true> : tc_key_weights_kernel<false>;
+  const cudaError_t ea = set_max_dynamic_smem(kernel, SMEM_BYTES);
+  if (ea != cudaSuccess) return ea;
+  const cudaError_t e = launch_pdl(kernel, dim3((unsigned)device_sm_count()), dim3(q8 ? kThreadsQ8 : kThreads), SMEM_BYTES,
+                                   stream, lat_map, rope_map, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace mla

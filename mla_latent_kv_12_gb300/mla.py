@@ -22,6 +22,7 @@ DEVICE_TIMEOUT = 1 << 5
 DEVICE_LAYOUT = 1 << 6
 DEVICE_SCORE_RANGE = 1 << 7
 DEVICE_VALUE_RANGE = 1 << 8
+DEVICE_BAD_BLOCK_START = 1 << 9
 FP16_SCORE_LIMIT = 256.0
 
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
@@ -34,6 +35,8 @@ EXPORTS = (
     "mla_decode_step_workspace_size", "mla_append_compressed", "mla_select_topk",
     "mla_selftest_bounded_wait", "mla_plan_rollback", "mla_plan_filter", "mla_plan_merge",
     "mla_cache_shift_rows", "mla_rollback_lengths", "mla_reconstruct_kv", "mla_prefill_attend",
+    "mla_append_compressed_q8", "mla_quantize_cache", "mla_dequantize_cache", "mla_decode_attend_q8",
+    "mla_key_weights", "mla_key_weights_q8", "mla_evict_plan", "mla_cache_compact",
 )
 
 
@@ -42,6 +45,12 @@ class MLAError(RuntimeError):
         super().__init__(f"mla status {status}: {detail}")
         self.status = status
         self.detail = detail
+
+
+class StateArray(ctypes.Structure):
+    """``mla_state_array``: one state array of a cache, sizes in bytes."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride_bytes", ctypes.c_int64),
+                ("batch_stride_bytes", ctypes.c_int64), ("row_bytes", ctypes.c_int32)]
 
 
 def _load() -> ctypes.CDLL:
@@ -103,7 +112,25 @@ def _load() -> ctypes.CDLL:
                                                ctypes.c_int, vp, vp]),
                        ("mla_prefill_attend", [vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, i64,
                                                ctypes.c_int, ctypes.c_int, vp, vp, i32, i32, i32, i32, i32, i32,
-                                               i64, f32, vp, i64, ctypes.c_int, vp, vp, vp])):
+                                               i64, f32, vp, i64, ctypes.c_int, vp, vp, vp]),
+                       ("mla_append_compressed_q8", [vp, i64, i64, vp, i64, i64, ctypes.c_int, vp, f32, f32, vp, vp,
+                                                     i64, i64, vp, i64, i32, vp, i64, i64, ctypes.c_int, vp, vp, vp,
+                                                     i32, i32, i32, i32, i64, vp, vp]),
+                       ("mla_quantize_cache", [vp, i64, i64, ctypes.c_int, vp, i64, i64, vp, i64, i32, vp, vp, i32,
+                                               i32, i64, vp, vp]),
+                       ("mla_dequantize_cache", [vp, i64, i64, vp, i64, i32, vp, i64, i64, ctypes.c_int, vp, vp, i32,
+                                                 i32, i64, vp, vp]),
+                       ("mla_decode_attend_q8", [vp, i64, i64, vp, i64, i64, vp, i64, i32, vp, i64, i64, ctypes.c_int,
+                                                 vp, vp, i32, i32, i32, i32, i32, i64, vp, vp, i32, f32, vp, i64, i64,
+                                                 ctypes.c_int, vp, vp, sz, vp, vp]),
+                       ("mla_key_weights", [vp, i64, i64, vp, i64, i64, vp, i64, i64, ctypes.c_int, vp, vp, i32, i32,
+                                            i32, i32, i32, i64, vp, f32, f32, i32, vp, i64, vp, vp]),
+                       ("mla_key_weights_q8", [vp, i64, i64, vp, i64, i64, vp, i64, i32, vp, i64, i64, ctypes.c_int,
+                                               vp, vp, i32, i32, i32, i32, i32, i64, vp, f32, f32, i32, vp, i64, vp,
+                                               vp]),
+                       ("mla_evict_plan", [vp, i64, vp, vp, i32, i64, i32, i32, i32, vp, i64, vp, vp, vp, vp]),
+                       ("mla_cache_compact", [ctypes.POINTER(StateArray), i32, vp, vp, i64, vp, i32, i32, i64, vp,
+                                              vp])):
         getattr(lib, name).restype = ctypes.c_int
         getattr(lib, name).argtypes = args
     lib.mla_gather_selected.restype = ctypes.c_int
@@ -390,3 +417,178 @@ def prefill_attend(q_nope: torch.Tensor, q_rope: torch.Tensor, k_nope: torch.Ten
 def default_scale(nope: int, rope_dim: int) -> float:
     """The page's softmax scale ``1/sqrt(qk_nope + qk_rope)``, as the library computes it."""
     return float(lib.mla_default_softmax_scale(nope, rope_dim))
+
+
+# ---------------------------------------------------------------- 8-bit cache
+
+def _batch_stride(t: torch.Tensor) -> int:
+    """Batch stride of a cache view: 0 for the packed-flat layout (one buffer row list for every batch row)."""
+    return t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _check_codes(codes: torch.Tensor, scales: torch.Tensor, scale_block: int) -> None:
+    """``codes`` ``[B_buf, T_max, rank]`` and ``scales`` ``[B_buf, >= ceil(T_max / scale_block)]``, one byte each."""
+    assert codes.dim() == 3 and codes.element_size() == 1 and codes.stride(2) == 1
+    assert scales.dim() == 2 and scales.element_size() == 1 and scales.stride(1) == 1
+    assert scales.shape[0] == codes.shape[0] and scales.shape[1] * scale_block >= codes.shape[1]
+
+
+def _check_lengths(*tensors: Optional[torch.Tensor]) -> None:
+    for t in tensors:
+        assert t is None or (t.dtype == torch.int32 and t.is_contiguous())
+
+
+def append_compressed_q8(latent_raw: torch.Tensor, rope_raw: torch.Tensor, norm_weight: torch.Tensor, eps: float,
+                         theta: float, codes: torch.Tensor, scales: torch.Tensor, scale_block: int,
+                         rope: torch.Tensor, kv_start, kv_len, kv_len_out: Optional[torch.Tensor] = None,
+                         row_offsets: Optional[torch.Tensor] = None, device_status=None, stream=None):
+    """``append_compressed`` into an 8-bit cache: ``codes`` ``[B_buf, T_max, rank]`` and ``scales`` ``[B_buf,
+    blocks]`` of one byte each (uint8, or float8_e4m3fn / float8_e8m0fnu), one exponent per ``scale_block``
+    buffer rows; ``rope`` ``[B_buf, T_max, rope]`` in f32 or bf16."""
+    B, S, rank = latent_raw.shape
+    _check_codes(codes, scales, scale_block)
+    _check_lengths(kv_start, kv_len, kv_len_out, row_offsets)
+    assert latent_raw.stride(2) == 1 and rope_raw.stride(2) == 1 and rope.stride(2) == 1 and norm_weight.is_contiguous()
+    assert rope_raw.dtype == latent_raw.dtype == norm_weight.dtype and codes.shape[2] == rank
+    assert rope.shape[:2] == codes.shape[:2] and kv_len.numel() == B
+    _check(lib.mla_append_compressed_q8(
+        _ptr(latent_raw), latent_raw.stride(0), latent_raw.stride(1), _ptr(rope_raw), rope_raw.stride(0),
+        rope_raw.stride(1), _dt(latent_raw), _ptr(norm_weight), float(eps), float(theta), _ptr(row_offsets),
+        _ptr(codes), codes.stride(1), _batch_stride(codes), _ptr(scales), _batch_stride(scales), int(scale_block),
+        _ptr(rope), rope.stride(1), _batch_stride(rope), _dt(rope), _ptr(kv_start), _ptr(kv_len), _ptr(kv_len_out),
+        B, S, rank, rope.shape[2], codes.shape[1], _ptr(device_status), _stream(stream)))
+
+
+def quantize_cache(latent: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, scale_block: int, kv_start, kv_len,
+                   device_status=None, stream=None) -> torch.Tensor:
+    """The windows of ``latent`` ``[B_buf, T_max, rank]`` (f32 or bf16) into ``codes`` / ``scales``."""
+    _check_codes(codes, scales, scale_block)
+    _check_lengths(kv_start, kv_len)
+    assert latent.shape == codes.shape and latent.stride(2) == 1
+    _check(lib.mla_quantize_cache(_ptr(latent), latent.stride(1), _batch_stride(latent), _dt(latent), _ptr(codes),
+                                  codes.stride(1), _batch_stride(codes), _ptr(scales), _batch_stride(scales),
+                                  int(scale_block), _ptr(kv_start), _ptr(kv_len), kv_len.numel(), codes.shape[2],
+                                  codes.shape[1], _ptr(device_status), _stream(stream)))
+    return codes
+
+
+def dequantize_cache(codes: torch.Tensor, scales: torch.Tensor, scale_block: int, latent: torch.Tensor, kv_start,
+                     kv_len, device_status=None, stream=None) -> torch.Tensor:
+    """The windows of an 8-bit cache back into ``latent`` ``[B_buf, T_max, rank]`` (f32 or bf16), exact."""
+    _check_codes(codes, scales, scale_block)
+    _check_lengths(kv_start, kv_len)
+    assert latent.shape == codes.shape and latent.stride(2) == 1
+    _check(lib.mla_dequantize_cache(_ptr(codes), codes.stride(1), _batch_stride(codes), _ptr(scales),
+                                    _batch_stride(scales), int(scale_block), _ptr(latent), latent.stride(1),
+                                    _batch_stride(latent), _dt(latent), _ptr(kv_start), _ptr(kv_len), kv_len.numel(),
+                                    codes.shape[2], codes.shape[1], _ptr(device_status), _stream(stream)))
+    return latent
+
+
+def decode_attend_q8(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, scale_block: int, rope: torch.Tensor,
+                     kv_start, kv_len, batch: int, s_q: int, softmax_scale: float, ctx_out: torch.Tensor,
+                     lse_out: Optional[torch.Tensor] = None, sel: Optional[torch.Tensor] = None,
+                     sel_count: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     device_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """``decode_attend`` over an 8-bit cache (views as in ``append_compressed_q8``; ``rope`` in the query's type).
+    The workspace is that of ``decode_workspace_size`` for the query's type."""
+    _, heads, width = q.shape
+    _check_codes(codes, scales, scale_block)
+    _check_lengths(kv_start, kv_len, sel_count)
+    rank, rope_dim = codes.shape[2], rope.shape[2]
+    t_max = codes.shape[1]
+    k_max = sel.shape[1] if sel is not None else 0
+    assert q.stride(2) == 1 and rope.stride(2) == 1 and ctx_out.stride(2) == 1 and width == rank + rope_dim
+    assert q.shape[0] == batch * s_q and kv_len.numel() == batch and ctx_out.shape == (batch * s_q, heads, rank)
+    assert rope.dtype == q.dtype and rope.shape[:2] == codes.shape[:2]
+    assert lse_out is None or (lse_out.dtype == torch.float32 and lse_out.is_contiguous())
+    assert sel is None or (sel.dtype == torch.int32 and sel.is_contiguous() and sel.shape[0] == batch * s_q)
+    if workspace is None:
+        nbytes = decode_workspace_size(batch, s_q, heads, rank, rope_dim, t_max, k_max, sel is not None, q.dtype)
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
+    _check(lib.mla_decode_attend_q8(
+        _ptr(q), q.stride(0), q.stride(1), _ptr(codes), codes.stride(1), _batch_stride(codes), _ptr(scales),
+        _batch_stride(scales), int(scale_block), _ptr(rope), rope.stride(1), _batch_stride(rope), _dt(q),
+        _ptr(kv_start), _ptr(kv_len), batch, s_q, heads, rank, rope_dim, t_max, _ptr(sel), _ptr(sel_count), k_max,
+        float(softmax_scale), _ptr(ctx_out), ctx_out.stride(0), ctx_out.stride(1), _dt(ctx_out), _ptr(lse_out),
+        _ptr(workspace), workspace.numel(), _ptr(device_status), _stream(stream)))
+    return ctx_out
+
+
+# ---------------------------------------------------------------- attention weights and eviction
+
+def _check_weights(q, rope, lse, weights, kv_start, kv_len, batch, s_q, t_max, rank) -> None:
+    _check_lengths(kv_start, kv_len)
+    assert q.shape[0] == batch * s_q and kv_len.numel() == batch and q.shape[2] == rank + rope.shape[2]
+    assert q.stride(2) == 1 and rope.stride(2) == 1 and rope.dtype == q.dtype
+    assert lse.dtype == torch.float32 and lse.is_contiguous() and lse.numel() == q.shape[0] * q.shape[1]
+    assert weights.dtype == torch.float32 and weights.dim() == 2 and weights.stride(1) == 1
+    assert weights.shape[1] >= t_max
+
+
+def key_weights(q: torch.Tensor, latent: torch.Tensor, rope: torch.Tensor, lse: torch.Tensor, kv_start, kv_len,
+                batch: int, s_q: int, softmax_scale: float, weights: torch.Tensor, decay: float = 1.0, n_new: int = 0,
+                device_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Adds the attention weight that each cached key received from ``q`` (all heads and tokens) to ``weights``
+    ``[B_buf, T_max]`` f32, decayed first; the ``n_new`` newest keys start from zero.  ``q`` and the cache as for
+    ``decode_attend``, ``lse`` its ``lse_out``."""
+    t_max, rank = latent.shape[1], latent.shape[2]
+    assert latent.stride(2) == 1 and latent.dtype == q.dtype and rope.shape[:2] == latent.shape[:2]
+    assert weights.shape[0] == latent.shape[0]
+    _check_weights(q, rope, lse, weights, kv_start, kv_len, batch, s_q, t_max, rank)
+    _check(lib.mla_key_weights(
+        _ptr(q), q.stride(0), q.stride(1), _ptr(latent), latent.stride(1), _batch_stride(latent), _ptr(rope),
+        rope.stride(1), _batch_stride(rope), _dt(q), _ptr(kv_start), _ptr(kv_len), batch, s_q, q.shape[1], rank,
+        rope.shape[2], t_max, _ptr(lse), float(softmax_scale), float(decay), int(n_new), _ptr(weights),
+        _batch_stride(weights), _ptr(device_status), _stream(stream)))
+    return weights
+
+
+def key_weights_q8(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, scale_block: int, rope: torch.Tensor,
+                   lse: torch.Tensor, kv_start, kv_len, batch: int, s_q: int, softmax_scale: float,
+                   weights: torch.Tensor, decay: float = 1.0, n_new: int = 0,
+                   device_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """``key_weights`` over an 8-bit cache."""
+    t_max, rank = codes.shape[1], codes.shape[2]
+    _check_codes(codes, scales, scale_block)
+    assert rope.shape[:2] == codes.shape[:2] and weights.shape[0] == codes.shape[0]
+    _check_weights(q, rope, lse, weights, kv_start, kv_len, batch, s_q, t_max, rank)
+    _check(lib.mla_key_weights_q8(
+        _ptr(q), q.stride(0), q.stride(1), _ptr(codes), codes.stride(1), _batch_stride(codes), _ptr(scales),
+        _batch_stride(scales), int(scale_block), _ptr(rope), rope.stride(1), _batch_stride(rope), _dt(q),
+        _ptr(kv_start), _ptr(kv_len), batch, s_q, q.shape[1], rank, rope.shape[2], t_max, _ptr(lse),
+        float(softmax_scale), float(decay), int(n_new), _ptr(weights), _batch_stride(weights), _ptr(device_status),
+        _stream(stream)))
+    return weights
+
+
+def evict_plan(weights: torch.Tensor, kv_start, kv_len, n_keep: int, n_sink: int, n_recent: int, kept: torch.Tensor,
+               counts: torch.Tensor, kv_len_out: Optional[torch.Tensor] = None, device_status=None,
+               stream=None) -> torch.Tensor:
+    """Window positions that stay, ascending: ``kept`` ``[B, >= n_keep]`` int32, ``counts`` ``[B]`` (``n_keep``, or
+    -1 for a row within its budget).  ``weights`` ``[B_buf, T_max]`` f32."""
+    assert weights.dtype == torch.float32 and weights.dim() == 2 and weights.stride(1) == 1
+    assert kept.dtype == torch.int32 and kept.dim() == 2 and kept.stride(1) == 1 and kept.shape[1] >= n_keep
+    _check_lengths(kv_start, kv_len, counts, kv_len_out)
+    batch = kv_len.numel()
+    assert kept.shape[0] == counts.numel() == batch
+    _check(lib.mla_evict_plan(_ptr(weights), _batch_stride(weights), _ptr(kv_start), _ptr(kv_len), batch,
+                              weights.shape[1], int(n_keep), int(n_sink), int(n_recent), _ptr(kept), kept.stride(0),
+                              _ptr(counts), _ptr(kv_len_out), _ptr(device_status), _stream(stream)))
+    return kept
+
+
+def cache_compact(arrays, kv_start, kept: torch.Tensor, counts: torch.Tensor, device_status=None, stream=None) -> None:
+    """Moves each row's kept tokens to the front of its window in every array of ``arrays`` (``[B_buf, T_max, F]``
+    views of any dtype, last dim contiguous; one launch), in place and in order."""
+    assert kept.dtype == torch.int32 and kept.dim() == 2 and kept.stride(1) == 1
+    _check_lengths(kv_start, counts)
+    t_max = arrays[0].shape[1]
+    states = (StateArray * len(arrays))()
+    for s, a in zip(states, arrays):
+        assert a.dim() == 3 and a.stride(2) == 1 and a.shape[:2] == arrays[0].shape[:2]
+        size = a.element_size()
+        s.data, s.row_bytes = a.data_ptr(), a.shape[2] * size
+        s.token_stride_bytes, s.batch_stride_bytes = a.stride(1) * size, _batch_stride(a) * size
+    _check(lib.mla_cache_compact(states, len(arrays), _ptr(kv_start), _ptr(kept), kept.stride(0), _ptr(counts),
+                                 kept.shape[1], counts.numel(), t_max, _ptr(device_status), _stream(stream)))

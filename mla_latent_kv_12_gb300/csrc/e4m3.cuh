@@ -51,8 +51,11 @@ __device__ __forceinline__ float decode_e4m3(uint32_t code, float unit) {
 // Sixteen codes to sixteen bf16 values (eight packed pairs), exact.  A code's
 // bits placed at a bf16's exponent and mantissa read as the value times
 // 2^-120; one packed multiplication by `mul2` = 2^(e - 7) in both halves
-// (bf16_unit) gives the value.  NaN codes would read as 480: a carry test
-// over all sixteen finds them, and a rare pass puts NaN there.
+// (bf16_unit) gives the value.  The high byte of a bf16 is (sign, 4 zeros, 3
+// exponent bits), the low one (exponent bit, 3 mantissa bits, 4 zeros): both
+// are masked shifts of the whole word, and a byte permutation pairs them.
+// NaN codes would read as 480: the returned word has bit 7 of a byte set iff
+// some code is NaN (the carry of magnitude 0x7F + 1), and the caller mends those.
 __device__ __forceinline__ uint32_t bf16_unit(int e) { return (uint32_t)(e + 120) * 0x00800080u; }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -60,25 +63,28 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-__device__ __forceinline__ void decode_e4m3x16(const uint4 codes, uint32_t mul2, uint32_t (&out)[8]) {
+__device__ __forceinline__ uint32_t decode_e4m3x16(const uint4 codes, uint32_t mul2, uint32_t (&out)[8]) {
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
   uint32_t carry = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     carry |= (w[j] & 0x7F7F7F7Fu) + 0x01010101u;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t p = __byte_perm(w[j], 0, k ? 0x3424 : 0x1404);   // a code in the high byte of each half
-      out[2 * j + k] = mul_bf16x2(((p & 0x7F007F00u) >> 4) | (p & 0x80008000u), mul2);
-    }
+    const uint32_t high = ((w[j] >> 4) & 0x07070707u) | (w[j] & 0x80808080u);
+    const uint32_t low = (w[j] << 4) & 0xF0F0F0F0u;
+    out[2 * j] = mul_bf16x2(__byte_perm(low, high, 0x5140), mul2);
+    out[2 * j + 1] = mul_bf16x2(__byte_perm(low, high, 0x7362), mul2);
   }
-  if (carry & 0x80808080u) {
+  return carry & 0x80808080u;
+}
+
+// Puts NaN where `codes` have it.
+__device__ __forceinline__ void mend_nan_e4m3x16(const uint4 codes, uint32_t (&out)[8]) {
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t p = __byte_perm(w[j >> 1], 0, (j & 1) ? 0x3424 : 0x1404);
-      if ((p & 0x7F00u) == 0x7F00u) out[j] = (out[j] & 0xFFFF0000u) | 0x7FC0u;
-      if ((p & 0x7F000000u) == 0x7F000000u) out[j] = (out[j] & 0xFFFFu) | 0x7FC00000u;
-    }
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t two = w[j >> 1] >> (16 * (j & 1));
+    if ((two & 0x7Fu) == 0x7Fu) out[j] = (out[j] & 0xFFFF0000u) | 0x7FC0u;
+    if ((two & 0x7F00u) == 0x7F00u) out[j] = (out[j] & 0xFFFFu) | 0x7FC00000u;
   }
 }
 

@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(kWarps * 32) decode_rows_kernel(const __grid_c
       if constexpr (kVec) {
         for (int i = 16 * lane; i < p.rank; i += 512) {
           uint32_t v[8];
-          decode_e4m3x16(*reinterpret_cast<const uint4*>(row + i), bf16_unit(e), v);
+          const uint4 c = *reinterpret_cast<const uint4*>(row + i);
+          if (decode_e4m3x16(c, bf16_unit(e), v)) mend_nan_e4m3x16(c, v);
           uint4* d = reinterpret_cast<uint4*>(dst + i);
           if constexpr (sizeof(TO) == 2) {
             d[0] = make_uint4(v[0], v[1], v[2], v[3]);

@@ -42,8 +42,8 @@
 #include <cuda_fp16.h>
 #include <math_constants.h>
 
-#include "e4m3.cuh"
 #include "mla_internal.h"
+#include "q8_tiles.cuh"
 #include "tc_common.cuh"
 #include "tc_host.h"
 
@@ -69,14 +69,18 @@ constexpr int HEADS = 128, RANK = 512, DV = 256;  // DV: latent dims per CTA
 // more threads the dense kernel gets fewer registers and ran 3 % slower)
 constexpr int THREADS = 352, THREADS_GATHER = THREADS + 96;
 constexpr int kGatherWarp = 11;   // first extra gather warp
-// The instances for an 8-bit cache: the producer and three more warps fetch
-// the codes of each tile and write their bf16 values into the stage ring.
-constexpr int THREADS_Q8 = THREADS + 96;
-constexpr int kConvertWarps = 4;
+// The instances for an 8-bit cache: four more warps, one per SM sub-partition,
+// fetch the codes of each tile and write their bf16 values into the stage
+// ring (three stages: the fourth's memory holds the fetch's two slots).
+constexpr int THREADS_Q8 = THREADS + 128;
+constexpr int kConvertWarps = 4, kConvertThreads = 32 * kConvertWarps;
+constexpr int STAGES_Q8 = 3;
+constexpr int SLOT_BYTES = kPieces * 16 * kConvertThreads;
 // Dynamic shared memory: the stage ring, then send[2] and receive[2].  The
 // 1024-byte alignment of the extern declaration places it on a 1024-byte
 // boundary after the static variables (checked at run time).
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 4 * XH_BYTES;
+constexpr int SMEM_BYTES_Q8 = STAGES_Q8 * STAGE_BYTES + 4 * XH_BYTES + 2 * SLOT_BYTES;
 constexpr uint32_t TM_O = 0, TM_Q = 256, TM_S = 400, TM_P = 464;  // TMEM columns (Q: 128 + 16)
 constexpr long long kWaitLimit = 1LL << 32;  // clock cycles (~2 s)
 constexpr float kRescaleThreshold = 8.0f;    // log2 units
@@ -441,16 +445,15 @@ __global__ void __launch_bounds__(1024) tc_plan_kernel(const __grid_constant__ T
 // MMAs instead of delaying them; single rows lose by the added P.V latency).
 // Without deadlock: the next tile's scores wait on the P.V STAGES tiles back
 // (its stage) and on the exchange of this tile's, in both CTAs, never on this P.V.
-// kQ8: the latent is held in 8 bits.  Four warps take the producer's place:
-// each thread fetches 16-byte pieces of codes a tile ahead (plain loads, so a
-// window and a selection are the same work), decodes them (e4m3.cuh: exact in
-// bf16, units applied) and writes them where the TMA box would have put them;
-// the rest of the kernel is the same.
+// kQ8: the latent is held in 8 bits: four warps fetch and decode it
+// (q8_tiles.cuh: exact in bf16, units applied) and write it where the TMA boxes
+// would have put it; the rest of the kernel is the same.
 template <int kPrefetchAhead, int kThreads, bool kLateP, bool kQ8 = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_decode_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_constant__ CUtensorMap rope_map,
                      const __grid_constant__ CUtensorMap lat_rows_map, const __grid_constant__ CUtensorMap rope_rows_map,
                      const __grid_constant__ TcDecodeArgs a) {
+  constexpr int kStages = kQ8 ? STAGES_Q8 : STAGES;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if ((smem_u32(smem_raw) & 1023u) != 0) {   // the same in every CTA: nothing waits on anything yet
     if (threadIdx.x == 0 && a.status) atomicOr(a.status, MLA_DEVICE_LAYOUT);
@@ -461,10 +464,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // Exchange buffers, each [8][128 heads][16 B] of fp16 scores: xin[b] is written
   // by the peer's remote stores, xout[b] holds this CTA's own half for its
   // softmax warps.
-  uint8_t* xin = smem + STAGES * STAGE_BYTES;        // 2 x XH_BYTES
+  uint8_t* xin = smem + kStages * STAGE_BYTES;        // 2 x XH_BYTES
   uint8_t* xout = xin + 2 * XH_BYTES;                // 2 x XH_BYTES
 
-  __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES];
+  __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];
   __shared__ __align__(8) uint64_t s_full, s_free, p_full, q_full, o_free, mma_drain, pv_drain;
   __shared__ __align__(8) uint64_t x_full[2], x_free[2], xo_free[2];  // per exchange buffer
   __shared__ uint32_t tmem_base_s;
@@ -491,7 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&rope_rows_map);
       }
     }
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(&full_bar[s], kQ8 ? kConvertWarps : (gather && !a.gather_tma) ? 32 : 1);
       mbar_init(&empty_bar[s], 1);
     }
@@ -544,14 +547,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (a.status) atomicOr(a.status, MLA_DEVICE_TIMEOUT);
   };
 
-  if (kQ8 && (warp == 0 || warp >= kGatherWarp)) {
+  if (kQ8 && warp >= kGatherWarp) {
     // ============================================================ 8-bit producers
-    // Half a warp takes one key at a time, 16 of this CTA's 256 latent dims per
-    // lane: eight keys of each tile per thread (8i + 2w + half), and two
-    // 16-byte pieces of rope keys (lane group g: the half-warp's key g and g + 4).
-    const int cw = warp == 0 ? 0 : 1 + (warp - kGatherWarp);
-    const int c = lane & 15, key0 = 2 * cw + (lane >> 4);
-    const int rg = c >> 2, rp = c & 3;
+    // Half a warp takes one key at a time, 16 of this CTA's 256 latent dims per lane.
+    const int cw = warp - kGatherWarp, c = lane & 15;
+    Q8Fetch<16> fetch;
+    fetch.slot0 = smem_u32(xout + 2 * XH_BYTES) + (cw * 32 + lane) * 16;
+    fetch.slot_bytes = SLOT_BYTES;
+    fetch.piece_bytes = 16 * kConvertThreads;
+    fetch.key0 = 2 * cw + (lane >> 4);
+    fetch.rope_group = c >> 2;
+    fetch.peers = lane & 16;
+    fetch.mine = lane & 7;
+    // Dims 16c .. 16c + 15 are pieces 2(c % 4) and the next of box c / 4; rope
+    // piece c % 4 of 64-byte rows (64-byte swizzle: piece ^ (row / 2 % 4)).
+    const int k0 = fetch.key0, piece = 2 * (c & 3);
+    const uint32_t box = smem_u32(stages) + (c >> 2) * CHUNK_BYTES + k0 * 128;
+    const uint32_t box0 = box + ((piece ^ k0) << 4), box1 = box + (((piece + 1) ^ k0) << 4);
+    const uint32_t rope0 = smem_u32(stages) + 4 * CHUNK_BYTES + (8 * fetch.rope_group + k0) * 64 +
+                           (((c & 3) ^ ((k0 >> 1) & 3)) << 4);
     int stage = 0;
     uint32_t phase = 0;
     int fills = 0;
@@ -560,100 +574,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     while (!aborted() && it.next(u, t0, t1, whole)) {
       if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
       const int b = n / a.s_q;
-      const int start = a.plan_in_kernel ? row_start_s[n] : (a.kv_start ? a.kv_start[b] : 0);
-      const int limit = a.plan_in_kernel ? row_limit_s[n] : row_limit(a, n);
-      const int keys = keys_p[n];
-      const int32_t* list = (gather && a.sel_count[n] != -1) ? a.sel + (int64_t)n * a.k_max : nullptr;
-      const uint8_t* codes = a.codes + b * a.codes_batch_stride + dim_base + 16 * c;
-      const uint8_t* scales = a.scales + b * a.scales_batch_stride;
-      const __nv_bfloat16* ropes = a.rope + b * a.rope_batch_stride + 32 * (int)rank + 8 * rp;
-      // Window position of entry e, or -1: past the row's entries, or (flagged
-      // once, by the CTA and lane that own it) outside the visible window.
-      auto position = [&](int e, bool flag) -> int {
-        if (e >= keys) return -1;
-        if (!list) return e;
-        const int p = __ldg(list + e);
-        if (p >= 0 && p < limit) return p;
-        if (flag && a.status) atomicOr(a.status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
-        return -1;
-      };
-      uint4 code[8], rope[2];
-      int unit[8];   // the key's exponent byte
-      auto load_key = [&](int i, int pos) {
-        code[i] = make_uint4(0, 0, 0, 0);
-        unit[i] = 127;
-        if (pos >= 0) {
-          const int64_t row = (int64_t)start + pos;
-          code[i] = __ldg(reinterpret_cast<const uint4*>(codes + row * a.codes_row_stride));
-          unit[i] = __ldg(scales + (row >> a.block_shift));
-        }
-      };
-      auto load_rope = [&](int j, int pos) {
-        rope[j] = make_uint4(0, 0, 0, 0);
-        if (pos >= 0)
-          rope[j] = __ldg(reinterpret_cast<const uint4*>(ropes + ((int64_t)start + pos) * a.rope_row_stride));
-      };
-      const bool owner = rank == 0 && c == 0;   // flags a bad position of its keys
-#pragma unroll
-      for (int i = 0; i < 8; ++i) load_key(i, position(t0 * BN + 8 * i + key0, owner));
-#pragma unroll
-      for (int j = 0; j < 2; ++j) load_rope(j, position(t0 * BN + 8 * (4 * j + rg) + key0, false));
-      for (int t = t0; t < t1 && !aborted(); ++t) {
-        // the next tile's positions: read before the wait, used as this tile's registers free
-        int pos[8], rpos[2];
-        const bool more = t + 1 < t1;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) pos[i] = more ? position((t + 1) * BN + 8 * i + key0, owner) : -1;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) rpos[j] = more ? position((t + 1) * BN + 8 * (4 * j + rg) + key0, false) : -1;
-        if (!list && t + kPrefetchAhead < t1) {
-          // a line of a later tile's codes, and of its rope keys, into L2
-          const int e = (t + kPrefetchAhead) * BN + (cw * 32 + lane) / 2;
-          if (e < keys) {
-            const int64_t row = (int64_t)start + e;
-            prefetch_l2(a.codes + b * a.codes_batch_stride + row * a.codes_row_stride + dim_base + 128 * (lane & 1));
-            if ((lane & 1) == 0)
-              prefetch_l2(a.rope + b * a.rope_batch_stride + row * a.rope_row_stride + 32 * (int)rank);
-          }
-        }
-        if (fills++ >= STAGES && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
-        uint8_t* st = stages + stage * STAGE_BYTES;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 8 * i + key0;
-          uint32_t v[8];
-          decode_e4m3x16(code[i], bf16_unit(clamp_exponent(unit[i])), v);
-          load_key(i, pos[i]);
-          // dims 16c .. 16c+15: 16-byte pieces 2(c % 4) and the next of box c / 4,
-          // at piece ^ (r % 8) (128-byte swizzle).  Odd boxes store their second
-          // piece first, so that eight neighbouring lanes hit eight different banks groups.
-          uint8_t* box = st + (c >> 2) * CHUNK_BYTES + r * 128;
-          const int first = (c >> 2) & 1, piece = 2 * (c & 3);
-          const uint4 lo = make_uint4(v[0], v[1], v[2], v[3]), hi = make_uint4(v[4], v[5], v[6], v[7]);
-          *reinterpret_cast<uint4*>(box + (((piece + first) ^ (r & 7)) << 4)) = first ? hi : lo;
-          *reinterpret_cast<uint4*>(box + (((piece + 1 - first) ^ (r & 7)) << 4)) = first ? lo : hi;
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int r = 8 * (4 * j + rg) + key0;
-          *reinterpret_cast<uint4*>(st + 4 * CHUNK_BYTES + r * 64 + ((rp ^ ((r >> 1) & 3)) << 4)) = rope[j];
-          load_rope(j, rpos[j]);
-        }
+      Q8Rows rows;
+      rows.codes = a.codes + b * a.codes_batch_stride + dim_base + 16 * c;
+      rows.codes_stride = a.codes_row_stride;
+      rows.scales = a.scales + b * a.scales_batch_stride;
+      rows.shift = a.block_shift;
+      rows.rope = a.rope + b * a.rope_batch_stride + 32 * (int)rank + 8 * (c & 3);
+      rows.rope_stride = a.rope_row_stride;
+      rows.start = a.plan_in_kernel ? row_start_s[n] : (a.kv_start ? a.kv_start[b] : 0);
+      rows.limit = a.plan_in_kernel ? row_limit_s[n] : row_limit(a, n);
+      rows.entries = keys_p[n];
+      rows.list = (gather && a.sel_count[n] != -1) ? a.sel + (int64_t)n * a.k_max : nullptr;
+      rows.status = rank == 0 && c < 8 ? a.status : nullptr;   // one lane per entry flags it
+      // The pipeline: tile t is converted while the copies of t + 1 and (from
+      // its end on) t + 2 are in flight; exponents come with the copies, list
+      // positions a tile before them.
+      int pos = fetch.my_position(rows, t0);
+      int e_now = fetch.my_exponent(rows, pos);
+      fetch.issue(rows, 0, pos);
+      cp_async_commit();
+      pos = fetch.my_position(rows, t0 + 1);
+      int e_next = fetch.my_exponent(rows, pos);
+      if (t0 + 1 < t1) fetch.issue(rows, 1, pos);
+      cp_async_commit();
+      pos = fetch.my_position(rows, t0 + 2);
+      for (int t = t0; t < t1; ++t) {
+        const int slot = (t - t0) & 1;
+        if (fills++ >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
+        cp_async_wait<1>();   // this tile's pieces
+        const uint32_t off = stage * STAGE_BYTES;
+        fetch.convert(slot, e_now, box0 + off, box1 + off, rope0 + off, rope0 + off + 4 * 8 * 64, (c & 4) != 0);
         fence_proxy_async_smem();   // generic-proxy writes, read by the MMAs
         __syncwarp();
         if (lane == 0) mbar_arrive(&full_bar[stage]);
-        if (++stage == STAGES) stage = 0, phase ^= 1u;
+        e_now = e_next;
+        if (t + 2 < t1) {
+          e_next = fetch.my_exponent(rows, pos);
+          fetch.issue(rows, slot, pos);
+          pos = fetch.my_position(rows, t + 3);
+        }
+        cp_async_commit();
+        if (++stage == kStages) stage = 0, phase ^= 1u;
       }
+      cp_async_wait<0>();   // the slots are free for the next segment
     }
-  } else if (!kQ8 && warp == 0) {
+  } else if (kQ8 && warp == 0) {
+    // (no producer warp: the fetch is the converting warps' own)
+  } else if (warp == 0) {
     // ============================================================ producer
     int stage = 0;
     uint32_t phase = 0;
-    uint32_t issued_phase[STAGES];
-    bool issued[STAGES];
+    uint32_t issued_phase[kStages];
+    bool issued[kStages];
 #pragma unroll
-    for (int s = 0; s < STAGES; ++s) issued[s] = false, issued_phase[s] = 0;
-    int fills = 0;   // the ring's first STAGES fills need no free slot
+    for (int s = 0; s < kStages; ++s) issued[s] = false, issued_phase[s] = 0;
+    int fills = 0;   // the ring's first kStages fills need no free slot
     int u, n, t0, t1;
     bool whole;
     while (!aborted() && it.next(u, t0, t1, whole)) {
@@ -666,13 +641,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int32_t* list = (gather && a.sel_count[n] != -1) ? a.sel + (int64_t)n * a.k_max : nullptr;
       if (!gather && lane == 0) {
         // the segment's first tiles that the loop's look-ahead will not cover
-        for (int t = t0 + STAGES; t < t0 + kPrefetchAhead && t < t1; ++t) {
+        for (int t = t0 + kStages; t < t0 + kPrefetchAhead && t < t1; ++t) {
           for (int c = 0; c < 4; ++c) tma_prefetch_l2_3d(&lat_map, dim_base + 64 * c, start + t * BN, zb);
           tma_prefetch_l2_3d(&rope_map, 32 * (int)rank, start + t * BN, zb);
         }
       }
       for (int t = t0; t < t1 && !aborted(); ++t) {
-        if (fills++ >= STAGES && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
+        if (fills++ >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
         if (!gather) {
           if (lane == 0) {
             mbar_arrive_expect_tx(&full_bar[stage], STAGE_TX);
@@ -746,11 +721,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         issued[stage] = true;
         issued_phase[stage] = phase;
-        if (++stage == STAGES) stage = 0, phase ^= 1u;
+        if (++stage == kStages) stage = 0, phase ^= 1u;
       }
     }
     // Drain: every issued fill must land before this CTA may exit.
-    for (int s = 0; s < STAGES; ++s)
+    for (int s = 0; s < kStages; ++s)
       if (issued[s]) mbar_wait(&full_bar[s], issued_phase[s], kWaitLimit);
   } else if (warp == 1) {
     // ============================================================ score MMA issuer
@@ -809,7 +784,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         ++tile;
-        if (++stage == STAGES) stage = 0, phase ^= 1u;
+        if (++stage == kStages) stage = 0, phase ^= 1u;
       }
       if (aborted()) break;
       ++seg;
@@ -847,7 +822,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         ++tile;
-        if (++stage == STAGES) stage = 0;
+        if (++stage == kStages) stage = 0;
       }
       if (aborted()) break;
       ++seg;
@@ -875,12 +850,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int keys = keys_p[n];
         const int32_t* list = a.sel_count[n] != -1 ? a.sel + (int64_t)n * a.k_max : nullptr;
         for (int t = t0; t < t1 && !aborted(); ++t) {
-          if (fills++ >= STAGES && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
+          if (fills++ >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
           const int g = issuer + kIssuers * lane;
           if (g < BN / 4)
             gather_key_group(a, &lat_rows_map, &rope_rows_map, stages + stage * STAGE_BYTES, &full_bar[stage], g, t,
                              b, start, limit, keys, list, rank, dim_base);
-          if (++stage == STAGES) stage = 0, phase ^= 1u;
+          if (++stage == kStages) stage = 0, phase ^= 1u;
         }
       }
     }
@@ -1029,12 +1004,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     x_free_peer[1] = mapa(smem_u32(&x_free[1]), peer);
     uint32_t tile = 0, seg = 0;
     // P.V(k) has completed once its commit arrives on the stage barrier
-    // empty_bar[k % STAGES] (that barrier's (k / STAGES)-th completion).  P.V's
-    // complete in order, and when P.V(k) is waited for, P.V(k - STAGES) has
-    // been waited for already and P.V(k + STAGES) cannot have started, so the
+    // empty_bar[k % kStages] (that barrier's (k / kStages)-th completion).  P.V's
+    // complete in order, and when P.V(k) is waited for, P.V(k - kStages) has
+    // been waited for already and P.V(k + kStages) cannot have started, so the
     // phase parity identifies the completion.
     auto wait_pv = [&](uint32_t k) -> bool {
-      return mbar_wait_warp(&empty_bar[k % STAGES], (k / STAGES) & 1u, kWaitLimit);
+      return mbar_wait_warp(&empty_bar[k % kStages], (k / kStages) & 1u, kWaitLimit);
     };
     int u, n, t0, t1;
     bool whole;
@@ -1833,8 +1808,9 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
                               : a.gather_tma ? tc_decode_kernel<kPrefetchAheadRow, THREADS_GATHER, false>
                               : lockstep   ? tc_decode_kernel<kPrefetchAheadGroup, THREADS, true>
                                            : tc_decode_kernel<kPrefetchAheadRow, THREADS, false>;
+  const int smem_bytes = q8 ? SMEM_BYTES_Q8 : SMEM_BYTES;
   {
-    const cudaError_t ea = set_max_dynamic_smem(decode_kernel, SMEM_BYTES);
+    const cudaError_t ea = set_max_dynamic_smem(decode_kernel, smem_bytes);
     if (ea != cudaSuccess) return ea;
   }
   cudaError_t e = cudaSuccess;
@@ -1842,7 +1818,7 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
     e = launch_pdl(tc_plan_kernel, dim3(1), dim3(1024), 0, stream, a);
     if (e != cudaSuccess) return e;
   }
-  e = launch_pdl(decode_kernel, dim3(2 * nclusters), dim3(q8 ? THREADS_Q8 : a.gather_tma ? THREADS_GATHER : THREADS), SMEM_BYTES, stream,
+  e = launch_pdl(decode_kernel, dim3(2 * nclusters), dim3(q8 ? THREADS_Q8 : a.gather_tma ? THREADS_GATHER : THREADS), smem_bytes, stream,
                  lat_map, rope_map, lat_rows_map, rope_rows_map, a);
   if (e != cudaSuccess) return e;
   if (tail == nullptr) {

@@ -16,16 +16,15 @@
 //    the same thread, in token order (no atomics, the same bits every time).
 //  * bf16 cache: warp 0 loads [64 keys x 576] tiles by TMA into a three-stage
 //    ring (nine boxes of 64 dims, 128-byte swizzle).  8-bit cache: warps 6..13
-//    fetch codes a tile ahead by plain loads and write decoded bf16 into
-//    the same layout.
+//    fetch codes and write decoded bf16 into the same layout (q8_tiles.cuh).
 //  * Warp 1 issues the 36 MMAs of a tile.  Warps 2..5 (one thread per head)
 //    load each token's query into TMEM, turn scores into probabilities and
 //    sum them over their 32 heads with a shuffle tree that halves the keys per
 //    lane at every step; the four warps' sums meet in shared memory.
 #include <cuda_bf16.h>
 
-#include "e4m3.cuh"
 #include "mla_internal.h"
+#include "q8_tiles.cuh"
 #include "tc_common.cuh"
 #include "tc_host.h"
 
@@ -38,17 +37,16 @@ constexpr int BN = 64;                    // keys per tile
 constexpr int BOX_BYTES = BN * 128;       // [64 keys][64 dims] bf16
 constexpr int BOXES = 9;                  // 8 of latent dims, 1 of rope dims
 constexpr int STAGE_BYTES = BOXES * BOX_BYTES;
-constexpr int STAGES = 3;
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES;
+constexpr int STAGES = 3, STAGES_Q8 = 2;   // 8-bit: the third stage's memory holds the fetch's slots
 constexpr uint32_t TM_Q = 0, TM_S = 288;  // TMEM columns
 constexpr int kThreads = 192, kThreadsQ8 = 448;
-constexpr int kConvertWarp = 6, kConvertWarps = 8;
+constexpr int kConvertWarp = 6, kConvertWarps = 8, kConvertThreads = 32 * kConvertWarps;
+constexpr int SLOT_BYTES = kPieces * 16 * kConvertThreads;
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES, SMEM_BYTES_Q8 = STAGES_Q8 * STAGE_BYTES + 2 * SLOT_BYTES;
 constexpr long long kWaitLimit = 1LL << 32;   // clock cycles (~2 s)
 // Tiles that several query tokens share before the next ones are read: 152
 // CTAs x 8 tiles x 72 KB = 88 MB stays in the 129 MB L2.
 constexpr int kChunkTiles = 8;
-// Tiles ahead of the conversion that an 8-bit cache is pulled into L2.
-constexpr int kPrefetchAhead = 3;
 
 struct WeightArgs {
   DecodeGeometry g;
@@ -114,13 +112,14 @@ template <bool kQ8>
 __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
     tc_key_weights_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_constant__ CUtensorMap rope_map,
                           const __grid_constant__ WeightArgs a) {
+  constexpr int kStages = kQ8 ? STAGES_Q8 : STAGES;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if ((smem_u32(smem_raw) & 1023u) != 0) {   // the same in every CTA: nothing waits on anything yet
     if (threadIdx.x == 0 && a.g.device_status) atomicOr(a.g.device_status, MLA_DEVICE_LAYOUT);
     return;
   }
   uint8_t* stages = smem_raw;
-  __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES], s_full[2], s_free[2], q_full, drain;
+  __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages], s_full[2], s_free[2], q_full, drain;
   __shared__ uint32_t tmem_base_s;
   __shared__ volatile int abort_s;
   __shared__ int first_row_s, first_tile_s, count_s;
@@ -133,7 +132,7 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
       tma_prefetch_desc(&lat_map);
       tma_prefetch_desc(&rope_map);
     }
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(&full_bar[s], kQ8 ? kConvertWarps : 1);
       mbar_init(&empty_bar[s], 1);
     }
@@ -203,7 +202,7 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
       const int start = g.kv_start ? g.kv_start[it.b] : 0;
       const int z = a.batch_in_map ? it.b : 0;
       for (int t = it.t0; t < it.t1; ++t) {
-        if (fills++ >= STAGES && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
+        if (fills++ >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
         if (lane == 0) {
           mbar_arrive_expect_tx(&full_bar[stage], STAGE_BYTES);
           uint8_t* st = stages + stage * STAGE_BYTES;
@@ -212,82 +211,72 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
           tma_load_3d(st + 8 * BOX_BYTES, &rope_map, &full_bar[stage], 0, start + t * BN, z);
         }
         __syncwarp();
-        if (++stage == STAGES) stage = 0, phase ^= 1u;
+        if (++stage == kStages) stage = 0, phase ^= 1u;
       }
     }
     // every issued load lands before this CTA may exit: fill k of a stage completes its phase k
-    for (int k = fills > STAGES ? fills - STAGES : 0; k < fills; ++k)
-      mbar_wait_warp(&full_bar[k % STAGES], (uint32_t)(k / STAGES) & 1u, kWaitLimit);
+    for (int k = fills > kStages ? fills - kStages : 0; k < fills; ++k)
+      mbar_wait_warp(&full_bar[k % kStages], (uint32_t)(k / kStages) & 1u, kWaitLimit);
   } else if (kQ8 && warp >= kConvertWarp) {
     // ============================================================ 8-bit producers
-    // A warp takes one key at a time, 16 latent dims per lane: keys 8i + w of a
-    // tile; and two 16-byte pieces of rope keys (lane group g: key 8g + w and 8(g + 4) + w).
+    // A warp takes one key at a time, 16 latent dims per lane.
     const int cw = warp - kConvertWarp;
-    const int rg = lane >> 3, rp = lane & 7;
+    Q8Fetch<32> fetch;
+    fetch.slot0 = smem_u32(stages + kStages * STAGE_BYTES) + (cw * 32 + lane) * 16;
+    fetch.slot_bytes = SLOT_BYTES;
+    fetch.piece_bytes = 16 * kConvertThreads;
+    fetch.key0 = cw;
+    fetch.rope_group = lane >> 3;
+    fetch.peers = 0;
+    fetch.mine = lane & 7;
+    // Dims 16 lane .. +15 are pieces 2(lane % 4) and the next of box lane / 4; rope piece lane % 8 of box 8.
+    const int piece = 2 * (lane & 3);
+    const uint32_t box = smem_u32(stages) + (lane >> 2) * BOX_BYTES + cw * 128;
+    const uint32_t box0 = box + ((piece ^ cw) << 4), box1 = box + (((piece + 1) ^ cw) << 4);
+    const uint32_t rope0 = smem_u32(stages) + 8 * BOX_BYTES + (8 * fetch.rope_group + cw) * 128 + (((lane & 7) ^ cw) << 4);
     int stage = 0, fills = 0;
     uint32_t phase = 0;
     while (!aborted() && it.next(g, fresh)) {
-      const int b = it.b, len = g.kv_len[b];
-      const int64_t start = g.kv_start ? g.kv_start[b] : 0;
-      const uint8_t* codes = g.codes + b * g.codes_batch_stride + 16 * lane;
-      const uint8_t* scales = g.scales + b * g.scales_batch_stride;
-      const __nv_bfloat16* ropes = static_cast<const __nv_bfloat16*>(g.rope) + b * g.rope_batch_stride + 8 * rp;
-      uint4 code[8], rope[2];
-      int unit[8];
-      auto load_key = [&](int i, int e) {
-        code[i] = make_uint4(0, 0, 0, 0);
-        unit[i] = 127;
-        if (e < len) {
-          code[i] = __ldg(reinterpret_cast<const uint4*>(codes + (start + e) * g.codes_row_stride));
-          unit[i] = __ldg(scales + ((start + e) >> g.block_shift));
-        }
-      };
-      auto load_rope = [&](int j, int e) {
-        rope[j] = make_uint4(0, 0, 0, 0);
-        if (e < len) rope[j] = __ldg(reinterpret_cast<const uint4*>(ropes + (start + e) * g.rope_row_stride));
-      };
-#pragma unroll
-      for (int i = 0; i < 8; ++i) load_key(i, it.t0 * BN + 8 * i + cw);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) load_rope(j, it.t0 * BN + 8 * (4 * j + rg) + cw);
-      for (int t = it.t0; t < it.t1; ++t) {
-        const int after = t + 1 < it.t1 ? (t + 1) * BN : len;   // `len`: nothing more to load
-        if (t + kPrefetchAhead < it.t1) {
-          const int tid = cw * 32 + lane;   // 256 threads: four lines of codes per key, one of rope keys
-          const int e = (t + kPrefetchAhead) * BN + (tid >> 2);
-          if (e < len) {
-            prefetch_l2(g.codes + b * g.codes_batch_stride + (start + e) * g.codes_row_stride + 128 * (tid & 3));
-            if ((tid & 3) == 0)
-              prefetch_l2(static_cast<const __nv_bfloat16*>(g.rope) + b * g.rope_batch_stride + (start + e) * g.rope_row_stride);
-          }
-        }
-        if (fills++ >= STAGES && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
-        uint8_t* st = stages + stage * STAGE_BYTES;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 8 * i + cw;
-          uint32_t v[8];
-          decode_e4m3x16(code[i], bf16_unit(clamp_exponent(unit[i])), v);
-          load_key(i, after + r);
-          // dims 16 lane .. +15: pieces 2(lane % 4) and the next of box lane / 4, at piece ^ (r % 8);
-          // odd boxes store their second piece first (eight lanes, eight bank groups)
-          uint8_t* box = st + (lane >> 2) * BOX_BYTES + r * 128;
-          const int first = (lane >> 2) & 1, piece = 2 * (lane & 3);
-          const uint4 lo = make_uint4(v[0], v[1], v[2], v[3]), hi = make_uint4(v[4], v[5], v[6], v[7]);
-          *reinterpret_cast<uint4*>(box + (((piece + first) ^ (r & 7)) << 4)) = first ? hi : lo;
-          *reinterpret_cast<uint4*>(box + (((piece + 1 - first) ^ (r & 7)) << 4)) = first ? lo : hi;
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int r = 8 * (4 * j + rg) + cw;
-          *reinterpret_cast<uint4*>(st + 8 * BOX_BYTES + r * 128 + ((rp ^ (r & 7)) << 4)) = rope[j];
-          load_rope(j, after + r);
-        }
+      const int b = it.b, t0 = it.t0, t1 = it.t1;
+      Q8Rows rows;
+      rows.codes = g.codes + b * g.codes_batch_stride + 16 * lane;
+      rows.codes_stride = g.codes_row_stride;
+      rows.scales = g.scales + b * g.scales_batch_stride;
+      rows.shift = g.block_shift;
+      rows.rope = static_cast<const __nv_bfloat16*>(g.rope) + b * g.rope_batch_stride + 8 * (lane & 7);
+      rows.rope_stride = g.rope_row_stride;
+      rows.start = g.kv_start ? g.kv_start[b] : 0;
+      rows.entries = rows.limit = g.kv_len[b];
+      rows.list = nullptr;
+      rows.status = nullptr;
+      // Tile t is converted while the copies of t + 1 and (from its end on) t + 2 are in flight.
+      int pos = fetch.my_position(rows, t0);
+      int e_now = fetch.my_exponent(rows, pos);
+      fetch.issue(rows, 0, pos);
+      cp_async_commit();
+      pos = fetch.my_position(rows, t0 + 1);
+      int e_next = fetch.my_exponent(rows, pos);
+      if (t0 + 1 < t1) fetch.issue(rows, 1, pos);
+      cp_async_commit();
+      for (int t = t0; t < t1; ++t) {
+        const int slot = (t - t0) & 1;
+        if (fills++ >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
+        cp_async_wait<1>();   // this tile's pieces
+        const uint32_t off = stage * STAGE_BYTES;
+        fetch.convert(slot, e_now, box0 + off, box1 + off, rope0 + off, rope0 + off + 4 * 8 * 128, (lane & 4) != 0);
         fence_proxy_async_smem();   // generic-proxy writes, read by the MMAs
         __syncwarp();
         if (lane == 0) mbar_arrive(&full_bar[stage]);
-        if (++stage == STAGES) stage = 0, phase ^= 1u;
+        e_now = e_next;
+        if (t + 2 < t1) {
+          pos = fetch.my_position(rows, t + 2);
+          e_next = fetch.my_exponent(rows, pos);
+          fetch.issue(rows, slot, pos);
+        }
+        cp_async_commit();
+        if (++stage == kStages) stage = 0, phase ^= 1u;
       }
+      cp_async_wait<0>();   // the slots are free for the next pass
     }
   } else if (warp == 1) {
     // ============================================================ MMA issuer
@@ -313,7 +302,7 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
           mma_commit(&s_full[buf]);
         }
         __syncwarp();
-        if (++stage == STAGES) stage = 0, phase ^= 1u;
+        if (++stage == kStages) stage = 0, phase ^= 1u;
       }
     }
     if (lane == 0) mma_commit(&drain);   // every MMA completes before TMEM is released
@@ -454,9 +443,10 @@ cudaError_t launch_tc_key_weights(const KeyWeightParams& p, cudaStream_t stream)
       return cudaErrorInvalidValue;
   }
   auto* const kernel = q8 ? tc_key_weights_kernel<true> : tc_key_weights_kernel<false>;
-  const cudaError_t ea = set_max_dynamic_smem(kernel, SMEM_BYTES);
+  const int smem = q8 ? SMEM_BYTES_Q8 : SMEM_BYTES;
+  const cudaError_t ea = set_max_dynamic_smem(kernel, smem);
   if (ea != cudaSuccess) return ea;
-  const cudaError_t e = launch_pdl(kernel, dim3((unsigned)device_sm_count()), dim3(q8 ? kThreadsQ8 : kThreads), SMEM_BYTES,
+  const cudaError_t e = launch_pdl(kernel, dim3((unsigned)device_sm_count()), dim3(q8 ? kThreadsQ8 : kThreads), smem,
                                    stream, lat_map, rope_map, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -3,16 +3,15 @@
 // swizzled shared-memory layout that a TMA load of a bf16 cache would leave.
 //
 // The fetch runs two tiles ahead: every thread copies its own 16-byte pieces
-// with cp.async into one of two private slots (10 pieces: eight of codes, two
-// of rope keys), so nothing but its own wait_group lies between the copy and
-// the conversion, and a window and a selection are the same work.  The loops
-// are rolled: with eight pieces unrolled beside the softmax's code the
-// instruction cache missed on most of them (a ragged decode of 32 rows took
-// 398 us that way).
+// with cp.async into one of two private slots, so nothing but its own
+// wait_group lies between the copy and the conversion, and a window and a
+// selection are the same work.  (Codes fetched into registers a tile ahead took
+// 398 us on a ragged decode of 32 rows: its code, unrolled over the register
+// array beside the softmax's, missed the instruction cache.)
 //
-// kLanes lanes (16 or 32) take one key, 16 dims each; a group of warps takes
-// eight keys at once: piece i of a thread belongs to key 8i + key0.  Keys of
-// one thread differ by multiples of 8, so its place in the 128-byte swizzle
+// kLanes lanes (16 or 32) take one key, 16 dims each, and kThreads threads
+// take 64 / kIters keys at once: piece i of a thread belongs to key i * kStep +
+// key0.  kStep is a multiple of 8, so a thread's place in the 128-byte swizzle
 // (piece ^ (row % 8)) is fixed.
 #pragma once
 
@@ -22,7 +21,6 @@
 namespace mla {
 
 constexpr int kTileKeys = 64;
-constexpr int kPieces = 10;   // 16-byte pieces per thread and slot
 
 // The cache row range of a pass, with the pointers moved to this thread's pieces.
 struct Q8Rows {
@@ -38,14 +36,19 @@ struct Q8Rows {
   int32_t* status;               // non-NULL: flag positions outside the window
 };
 
-template <int kLanes>
+template <int kLanes, int kThreads>
 struct Q8Fetch {
+  static constexpr int kStep = kThreads / kLanes;         // keys taken at once
+  static constexpr int kIters = kTileKeys / kStep;        // pieces of codes per thread and tile
+  static constexpr int kRopeIters = kIters / 4;           // and of rope keys
+  static constexpr int kPieceBytes = 16 * kThreads;
+  static constexpr int kSlotBytes = (kIters + kRopeIters) * kPieceBytes;
+  static_assert(kStep % 8 == 0 && kIters >= 4 && kIters <= 8, "fixed swizzle; lanes to look the keys up");
   uint32_t slot0;                // shared address of this thread's first piece
-  uint32_t slot_bytes, piece_bytes;
-  int key0;                      // key of piece i is 8i + key0
-  int rope_group;                // rope pieces belong to this thread's keys rope_group and rope_group + 4
+  int key0;                      // key of piece i is i * kStep + key0
+  int rope_group;                // rope piece j belongs to this thread's key 4j + rope_group
   int peers;                     // first lane of the lanes that share this lane's keys
-  int mine;                      // piece whose position and exponent this lane looks up (lane % 8)
+  int mine;                      // piece whose position and exponent this lane looks up (lane % kIters)
 
   // Window position of entry e, -1 for none (past the entries, or outside the window: skipped and flagged).
   __device__ __forceinline__ int position(const Q8Rows& r, int e) const {
@@ -57,58 +60,78 @@ struct Q8Fetch {
     return -1;
   }
   __device__ __forceinline__ int my_position(const Q8Rows& r, int tile) const {
-    return position(r, tile * kTileKeys + 8 * mine + key0);
+    return position(r, tile * kTileKeys + kStep * mine + key0);
   }
   // Exponent byte of the key at `pos` (any value for no key).
   __device__ __forceinline__ int my_exponent(const Q8Rows& r, int pos) const {
     return pos >= 0 ? __ldg(r.scales + (((int64_t)r.start + pos) >> r.shift)) : kMinExponent;
   }
   // Copies of one tile into slot s; `pos` from my_position.
-  __device__ __forceinline__ void issue(const Q8Rows& r, int s, int pos) const {
-    const uint32_t dst = slot0 + s * slot_bytes;
-#pragma unroll 2
-    for (int i = 0; i < 8; ++i) {
-      const int p = __shfl_sync(0xffffffffu, pos, peers + i);
-      tc::cp_async_16(dst + i * piece_bytes, r.codes + (int64_t)(r.start + max(p, 0)) * r.codes_stride, p >= 0 ? 16u : 0u);
+  __device__ __forceinline__ void issue(const Q8Rows& r, int tile, int s, int pos) const {
+    const uint32_t dst = slot0 + s * kSlotBytes;
+    if (!r.list && (tile + 1) * kTileKeys <= r.entries) {   // a whole tile of a window: rows at one distance
+      const int64_t row = (int64_t)r.start + tile * kTileKeys + key0;
+      const uint8_t* c = r.codes + row * r.codes_stride;
+      const __nv_bfloat16* k = r.rope + (row + rope_group * kStep) * r.rope_stride;
+#pragma unroll
+      for (int i = 0; i < kIters; ++i, c += kStep * r.codes_stride) tc::cp_async_16(dst + i * kPieceBytes, c, 16u);
+#pragma unroll
+      for (int j = 0; j < kRopeIters; ++j, k += 4 * kStep * r.rope_stride)
+        tc::cp_async_16(dst + (kIters + j) * kPieceBytes, k, 16u);
+      return;
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int i = 0; i < kIters; ++i) {
+      const int p = __shfl_sync(0xffffffffu, pos, peers + i);
+      tc::cp_async_16(dst + i * kPieceBytes, r.codes + (int64_t)(r.start + max(p, 0)) * r.codes_stride, p >= 0 ? 16u : 0u);
+    }
+#pragma unroll
+    for (int j = 0; j < kRopeIters; ++j) {
       const int p = __shfl_sync(0xffffffffu, pos, peers + 4 * j + rope_group);
-      tc::cp_async_16(dst + (8 + j) * piece_bytes, r.rope + (int64_t)(r.start + max(p, 0)) * r.rope_stride,
+      tc::cp_async_16(dst + (kIters + j) * kPieceBytes, r.rope + (int64_t)(r.start + max(p, 0)) * r.rope_stride,
                       p >= 0 ? 16u : 0u);
     }
   }
-  // Slot s as bf16 values: box `box0` / `box1` receive dims 0..7 and 8..15 of
-  // the thread's 16 (shared addresses for key0; keys 8 apart lie 1024 bytes
-  // apart), `rope0` / `rope1` the rope pieces.  `exponent` from my_exponent.
-  __device__ __forceinline__ void convert(int s, int exponent, uint32_t box0, uint32_t box1, uint32_t rope0,
-                                          uint32_t rope1, bool swap) const {
-    const uint32_t src = slot0 + s * slot_bytes;
+  // Slot s as bf16 values.  A piece's 16 dims are two 16-byte pieces of bf16:
+  // `half0` (0 or 8) picks the eight codes decoded first, stored at `box0`, the
+  // others at `box1` (shared addresses for key0; rows lie 128 bytes
+  // apart): half of the lanes take their second eight first, so that eight
+  // lanes of a store hit eight bank groups.  `rope` receives the first
+  // rope piece (rows of rope keys kRopeRow bytes apart).  `exponent` from my_exponent.
+  template <int kRopeRow>
+  __device__ __forceinline__ void convert(int s, int exponent, uint32_t half0, uint32_t box0, uint32_t box1,
+                                          uint32_t rope) const {
+    const uint32_t src = slot0 + s * kSlotBytes, src0 = src + half0, src1 = src + (half0 ^ 8u);
     const uint32_t unit = bf16_unit(clamp_exponent(exponent));
-#pragma unroll 2
-    for (int i = 0; i < 8; ++i) {
+    uint32_t nan = 0;
+#pragma unroll
+    for (int i = 0; i < kIters; ++i) {
       const uint32_t mul2 = __shfl_sync(0xffffffffu, unit, peers + i);
-      const uint4 c = ld_shared_16(src + i * piece_bytes);
+      const uint2 c0 = ld_shared_8(src0 + i * kPieceBytes), c1 = ld_shared_8(src1 + i * kPieceBytes);
       uint32_t v[8];
-      const uint32_t nan = decode_e4m3x16(c, mul2, v);
-      // half of the lanes store their second piece first (eight lanes, eight bank groups)
-      st_shared_16(swap ? box1 : box0, swap ? make_uint4(v[4], v[5], v[6], v[7]) : make_uint4(v[0], v[1], v[2], v[3]));
-      st_shared_16(swap ? box0 : box1, swap ? make_uint4(v[0], v[1], v[2], v[3]) : make_uint4(v[4], v[5], v[6], v[7]));
-      if (nan) {
-#pragma unroll 1
-        for (int k = 0; k < 16; ++k) {
-          uint32_t code;
-          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(code) : "r"(src + i * piece_bytes + k) : "memory");
-          if ((code & 0x7Fu) == 0x7Fu) tc::st_shared_u16((k < 8 ? box0 : box1) + 2 * (k & 7), 0x7FC0u);
-        }
-      }
-      box0 += 1024;
-      box1 += 1024;
+      nan |= decode_e4m3x16(make_uint4(c0.x, c0.y, c1.x, c1.y), mul2, v);
+      st_shared_16(box0 + i * kStep * 128, make_uint4(v[0], v[1], v[2], v[3]));
+      st_shared_16(box1 + i * kStep * 128, make_uint4(v[4], v[5], v[6], v[7]));
     }
-    st_shared_16(rope0, ld_shared_16(src + 8 * piece_bytes));
-    st_shared_16(rope1, ld_shared_16(src + 9 * piece_bytes));
+#pragma unroll
+    for (int j = 0; j < kRopeIters; ++j)
+      st_shared_16(rope + 4 * j * kStep * kRopeRow, ld_shared_16(src + (kIters + j) * kPieceBytes));
+    if (nan) {   // rare: look for the NaN codes again, one by one
+#pragma unroll 1
+      for (int k = 0; k < 16 * kIters; ++k) {
+        const int i = k >> 4, j = k & 7;
+        uint32_t code;
+        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(code) : "r"(((k & 8) ? src1 : src0) + i * kPieceBytes + j) : "memory");
+        if ((code & 0x7Fu) == 0x7Fu) tc::st_shared_u16(((k & 8) ? box1 : box0) + i * kStep * 128 + 2 * j, 0x7FC0u);
+      }
+    }
   }
 
+  static __device__ __forceinline__ uint2 ld_shared_8(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+  }
   static __device__ __forceinline__ uint4 ld_shared_16(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");

@@ -69,18 +69,23 @@ constexpr int HEADS = 128, RANK = 512, DV = 256;  // DV: latent dims per CTA
 // more threads the dense kernel gets fewer registers and ran 3 % slower)
 constexpr int THREADS = 352, THREADS_GATHER = THREADS + 96;
 constexpr int kGatherWarp = 11;   // first extra gather warp
-// The instances for an 8-bit cache: four more warps, one per SM sub-partition,
-// fetch the codes of each tile and write their bf16 values into the stage
-// ring (three stages: the fourth's memory holds the fetch's two slots).
-constexpr int THREADS_Q8 = THREADS + 128;
-constexpr int kConvertWarps = 4, kConvertThreads = 32 * kConvertWarps;
+// The instances for an 8-bit cache: eight warps fetch the codes of each tile
+// and write their bf16 values into the stage ring (three stages: the fourth's
+// memory holds the fetch's two slots).  Roles are whole warpgroups, whose
+// registers are redistributed at their start: the softmax and exchange
+// warps take what the MMA and converting warps do not need.  The shares (per
+// thread and warpgroup) add up to the launch's 5 x 96.
+constexpr int THREADS_Q8 = 640;
+constexpr int kConvertWarps = 8;
 constexpr int STAGES_Q8 = 3;
-constexpr int SLOT_BYTES = kPieces * 16 * kConvertThreads;
+constexpr int kRegsSoftmax = 144, kRegsExchange = 136, kRegsIssue = 40, kRegsConvert = 80;
+static_assert(kRegsSoftmax + kRegsExchange + kRegsIssue + 2 * kRegsConvert <= 5 * 96, "more registers than the launch has");
+using DecodeFetch = Q8Fetch<16, 32 * kConvertWarps>;
 // Dynamic shared memory: the stage ring, then send[2] and receive[2].  The
 // 1024-byte alignment of the extern declaration places it on a 1024-byte
 // boundary after the static variables (checked at run time).
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 4 * XH_BYTES;
-constexpr int SMEM_BYTES_Q8 = STAGES_Q8 * STAGE_BYTES + 4 * XH_BYTES + 2 * SLOT_BYTES;
+constexpr int SMEM_BYTES_Q8 = STAGES_Q8 * STAGE_BYTES + 4 * XH_BYTES + 2 * DecodeFetch::kSlotBytes;
 constexpr uint32_t TM_O = 0, TM_Q = 256, TM_S = 400, TM_P = 464;  // TMEM columns (Q: 128 + 16)
 constexpr long long kWaitLimit = 1LL << 32;  // clock cycles (~2 s)
 constexpr float kRescaleThreshold = 8.0f;    // log2 units
@@ -478,6 +483,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   auto aborted = [&]() -> bool { return __any_sync(0xffffffffu, abort_s != 0); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // Warps of each role (the first of four, one per TMEM lane quarter, for softmax and exchange).
+  constexpr int kSoftmaxWarp = kQ8 ? 0 : 2, kExchangeWarp = kQ8 ? 4 : 6, kScoreWarp = kQ8 ? 8 : 1, kPvWarp = kQ8 ? 9 : 10;
+  constexpr int kConvertWarp = 12;
   const uint32_t rank = cluster_ctarank();
   const uint32_t peer = rank ^ 1u;
   const int dim_base = 256 * (int)rank;     // first latent dim of this CTA
@@ -514,7 +522,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     abort_s = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == kScoreWarp) {
     tmem_alloc(&tmem_base_s, 512);
     tmem_relinquish();
   }
@@ -547,24 +555,137 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (a.status) atomicOr(a.status, MLA_DEVICE_TIMEOUT);
   };
 
-  if (kQ8 && warp >= kGatherWarp) {
+  // The MMA issuers, one warp each.
+  auto issue_scores = [&]() {
+    // ============================================================ score MMA issuer
+    // S(t) as soon as tile t has landed and the exchange warps have read S(t-1);
+    // the P.V issuer (warp 10) runs independently, so scores run ahead.
+    const uint32_t idesc_s = idesc_bf16_f32(128, BN, 0, 0);
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t tile = 0;      // global tile counter (S phases)
+    uint32_t seg = 0;       // segment counter (q_full phases)
+    int u, n, t0, t1;
+    bool whole;
+    while (!aborted() && it.next(u, t0, t1, whole)) {
+      if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
+      const int keys = keys_p[n];
+      if (!mbar_wait_warp(&q_full, seg & 1u, kWaitLimit)) { fail(); break; }
+      for (int t = t0; t < t1; ++t) {
+        if (!mbar_wait_warp(&full_bar[stage], phase, kWaitLimit)) { fail(); break; }
+        if (!kQ8 && !gather && t == (keys - 1) / BN && (keys % BN) != 0) {
+          // Tail tile: clear the rows past the window so that P = 0 never meets
+          // a non-finite value left in the caller's buffer.
+          const int valid = keys % BN;
+          uint8_t* st = stages + stage * STAGE_BYTES;
+          for (int q16 = lane; q16 < (BN - valid) * 4 * 8; q16 += 32) {
+            const int c = q16 / ((BN - valid) * 8), rem = q16 % ((BN - valid) * 8);
+            const int r = valid + rem / 8, uu = rem % 8;
+            *reinterpret_cast<uint4*>(st + c * CHUNK_BYTES + r * 128 + uu * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (!kQ8 && gather && !a.gather_tma) fence_proxy_async_smem();
+        if (tile > 0 && !mbar_wait_warp(&s_free, (tile - 1) & 1u, kWaitLimit)) { fail(); break; }
+        tc_fence_after();
+        // 16 latent K-steps, then this CTA's two rope K-steps.  Descriptors
+        // differ only in the start address (16-byte units, low bits); one
+        // elected lane of the converged warp issues them with constant
+        // offsets (a lane-0 branch with per-MMA descriptor arithmetic issues
+        // the N=64 MMAs at about half the rate).
+        const uint64_t d0 = smem_desc(smem_u32(stages + stage * STAGE_BYTES), 16, 1024, kSwizzle128B);
+        // this CTA's 32 rope dims: 64-byte rows, 8-row groups 512 bytes apart
+        const uint64_t d_rope =
+            smem_desc(smem_u32(stages + stage * STAGE_BYTES + 4 * CHUNK_BYTES), 16, 512, kSwizzle64B);
+        if (elect_one()) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ts(tmem + TM_S, tmem + TM_Q + c * 32 + k * 8, d0 + (uint64_t)((c * CHUNK_BYTES + k * 32) >> 4),
+                     idesc_s, (c | k) != 0);
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            mma_ts(tmem + TM_S, tmem + TM_Q + 128 + k * 8, d_rope + (uint64_t)((k * 32) >> 4), idesc_s, 1u);
+          mma_commit(&s_full);
+        }
+        __syncwarp();
+        ++tile;
+        if (++stage == kStages) stage = 0, phase ^= 1u;
+      }
+      if (aborted()) break;
+      ++seg;
+    }
+    // All score MMAs complete before TMEM is released.
+    if (lane == 0) mma_commit(&mma_drain);
+    __syncwarp();
+    mbar_wait_warp(&mma_drain, 0, kWaitLimit);
+  };
+  auto issue_pv = [&]() {
+    // ============================================================ P.V MMA issuer
+    const uint32_t idesc_pv = idesc_bf16_f32(128, DV, 0, 1);
+    int stage = 0;
+    uint32_t tile = 0, seg = 0;
+    int u, n, t0, t1;
+    bool whole;
+    while (!aborted() && it.next(u, t0, t1, whole)) {
+      if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
+      for (int t = t0; t < t1; ++t) {
+        const bool first = (t == t0);
+        // O is overwritten by a segment's first P.V: the previous segment's
+        // epilogue must have read it.
+        if (first && seg > 0 && !mbar_wait_warp(&o_free, (seg - 1) & 1u, kWaitLimit)) { fail(); break; }
+        if (!mbar_wait_warp(&p_full, tile & 1u, kWaitLimit)) { fail(); break; }
+        tc_fence_after();
+        const uint64_t d0 = smem_desc(smem_u32(stages + stage * STAGE_BYTES), CHUNK_BYTES, 1024, kSwizzle128B);
+        const uint32_t acc0 = first ? 0u : 1u;
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < BN / 16; ++k)
+            mma_ts(tmem + TM_O, tmem + TM_P + k * 8, d0 + (uint64_t)((k * 2048) >> 4), idesc_pv,
+                   k == 0 ? acc0 : 1u);
+          // one commit: the stage barrier also tells the softmax warps that
+          // this P.V has completed (a second commit costs its own latency)
+          mma_commit(&empty_bar[stage]);
+        }
+        __syncwarp();
+        ++tile;
+        if (++stage == kStages) stage = 0;
+      }
+      if (aborted()) break;
+      ++seg;
+    }
+    if (lane == 0) mma_commit(&pv_drain);
+    __syncwarp();
+    mbar_wait_warp(&pv_drain, 0, kWaitLimit);
+  };
+
+  if (kQ8 && warp >= kScoreWarp && warp < kConvertWarp) {
+    // One warpgroup: both issuers and two warps without a role (a whole
+    // warpgroup executes the same setmaxnreg).
+    reg_dealloc<kRegsIssue>();
+    if (warp == kScoreWarp) issue_scores();
+    if (warp == kPvWarp) issue_pv();
+  } else if (kQ8 && warp >= kConvertWarp) {
+    reg_dealloc<kRegsConvert>();
     // ============================================================ 8-bit producers
     // Half a warp takes one key at a time, 16 of this CTA's 256 latent dims per lane.
-    const int cw = warp - kGatherWarp, c = lane & 15;
-    Q8Fetch<16> fetch;
+    const int cw = warp - kConvertWarp, c = lane & 15;
+    DecodeFetch fetch;
     fetch.slot0 = smem_u32(xout + 2 * XH_BYTES) + (cw * 32 + lane) * 16;
-    fetch.slot_bytes = SLOT_BYTES;
-    fetch.piece_bytes = 16 * kConvertThreads;
     fetch.key0 = 2 * cw + (lane >> 4);
     fetch.rope_group = c >> 2;
     fetch.peers = lane & 16;
-    fetch.mine = lane & 7;
+    fetch.mine = lane % DecodeFetch::kIters;
     // Dims 16c .. 16c + 15 are pieces 2(c % 4) and the next of box c / 4; rope
     // piece c % 4 of 64-byte rows (64-byte swizzle: piece ^ (row / 2 % 4)).
-    const int k0 = fetch.key0, piece = 2 * (c & 3);
-    const uint32_t box = smem_u32(stages) + (c >> 2) * CHUNK_BYTES + k0 * 128;
-    const uint32_t box0 = box + ((piece ^ k0) << 4), box1 = box + (((piece + 1) ^ k0) << 4);
-    const uint32_t rope0 = smem_u32(stages) + 4 * CHUNK_BYTES + (8 * fetch.rope_group + k0) * 64 +
+    const int row = fetch.key0, k0 = row & 7, piece = 2 * (c & 3);
+    const uint32_t box = smem_u32(stages) + (c >> 2) * CHUNK_BYTES + row * 128;
+    const uint32_t odd = (c >> 2) & 1, half0 = 8 * odd;   // lanes of odd boxes take their second piece first
+    const uint32_t box0 = box + (((piece + odd) ^ k0) << 4), box1 = box + (((piece + 1 - odd) ^ k0) << 4);
+    const uint32_t rope0 = smem_u32(stages) + 4 * CHUNK_BYTES + (DecodeFetch::kStep * fetch.rope_group + row) * 64 +
                            (((c & 3) ^ ((k0 >> 1) & 3)) << 4);
     int stage = 0;
     uint32_t phase = 0;
@@ -585,17 +706,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       rows.limit = a.plan_in_kernel ? row_limit_s[n] : row_limit(a, n);
       rows.entries = keys_p[n];
       rows.list = (gather && a.sel_count[n] != -1) ? a.sel + (int64_t)n * a.k_max : nullptr;
-      rows.status = rank == 0 && c < 8 ? a.status : nullptr;   // one lane per entry flags it
+      rows.status = rank == 0 && c < DecodeFetch::kIters ? a.status : nullptr;   // one lane per entry flags it
       // The pipeline: tile t is converted while the copies of t + 1 and (from
       // its end on) t + 2 are in flight; exponents come with the copies, list
       // positions a tile before them.
       int pos = fetch.my_position(rows, t0);
       int e_now = fetch.my_exponent(rows, pos);
-      fetch.issue(rows, 0, pos);
+      fetch.issue(rows, t0, 0, pos);
       cp_async_commit();
       pos = fetch.my_position(rows, t0 + 1);
       int e_next = fetch.my_exponent(rows, pos);
-      if (t0 + 1 < t1) fetch.issue(rows, 1, pos);
+      if (t0 + 1 < t1) fetch.issue(rows, t0 + 1, 1, pos);
       cp_async_commit();
       pos = fetch.my_position(rows, t0 + 2);
       for (int t = t0; t < t1; ++t) {
@@ -603,14 +724,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (fills++ >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
         cp_async_wait<1>();   // this tile's pieces
         const uint32_t off = stage * STAGE_BYTES;
-        fetch.convert(slot, e_now, box0 + off, box1 + off, rope0 + off, rope0 + off + 4 * 8 * 64, (c & 4) != 0);
+        fetch.convert<64>(slot, e_now, half0, box0 + off, box1 + off, rope0 + off);
         fence_proxy_async_smem();   // generic-proxy writes, read by the MMAs
         __syncwarp();
         if (lane == 0) mbar_arrive(&full_bar[stage]);
         e_now = e_next;
         if (t + 2 < t1) {
           e_next = fetch.my_exponent(rows, pos);
-          fetch.issue(rows, slot, pos);
+          fetch.issue(rows, t + 2, slot, pos);
           pos = fetch.my_position(rows, t + 3);
         }
         cp_async_commit();
@@ -618,9 +739,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       cp_async_wait<0>();   // the slots are free for the next segment
     }
-  } else if (kQ8 && warp == 0) {
-    // (no producer warp: the fetch is the converting warps' own)
-  } else if (warp == 0) {
+  } else if (!kQ8 && warp == 0) {
     // ============================================================ producer
     int stage = 0;
     uint32_t phase = 0;
@@ -727,109 +846,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // Drain: every issued fill must land before this CTA may exit.
     for (int s = 0; s < kStages; ++s)
       if (issued[s]) mbar_wait(&full_bar[s], issued_phase[s], kWaitLimit);
-  } else if (warp == 1) {
-    // ============================================================ score MMA issuer
-    // S(t) as soon as tile t has landed and the exchange warps have read S(t-1);
-    // the P.V issuer (warp 10) runs independently, so scores run ahead.
-    const uint32_t idesc_s = idesc_bf16_f32(128, BN, 0, 0);
-    int stage = 0;
-    uint32_t phase = 0;
-    uint32_t tile = 0;      // global tile counter (S phases)
-    uint32_t seg = 0;       // segment counter (q_full phases)
-    int u, n, t0, t1;
-    bool whole;
-    while (!aborted() && it.next(u, t0, t1, whole)) {
-      if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
-      const int keys = keys_p[n];
-      if (!mbar_wait_warp(&q_full, seg & 1u, kWaitLimit)) { fail(); break; }
-      for (int t = t0; t < t1; ++t) {
-        if (!mbar_wait_warp(&full_bar[stage], phase, kWaitLimit)) { fail(); break; }
-        if (!kQ8 && !gather && t == (keys - 1) / BN && (keys % BN) != 0) {
-          // Tail tile: clear the rows past the window so that P = 0 never meets
-          // a non-finite value left in the caller's buffer.
-          const int valid = keys % BN;
-          uint8_t* st = stages + stage * STAGE_BYTES;
-          for (int q16 = lane; q16 < (BN - valid) * 4 * 8; q16 += 32) {
-            const int c = q16 / ((BN - valid) * 8), rem = q16 % ((BN - valid) * 8);
-            const int r = valid + rem / 8, uu = rem % 8;
-            *reinterpret_cast<uint4*>(st + c * CHUNK_BYTES + r * 128 + uu * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        if (!kQ8 && gather && !a.gather_tma) fence_proxy_async_smem();
-        if (tile > 0 && !mbar_wait_warp(&s_free, (tile - 1) & 1u, kWaitLimit)) { fail(); break; }
-        tc_fence_after();
-        // 16 latent K-steps, then this CTA's two rope K-steps.  Descriptors
-        // differ only in the start address (16-byte units, low bits); one
-        // elected lane of the converged warp issues them with constant
-        // offsets (a lane-0 branch with per-MMA descriptor arithmetic issues
-        // the N=64 MMAs at about half the rate).
-        const uint64_t d0 = smem_desc(smem_u32(stages + stage * STAGE_BYTES), 16, 1024, kSwizzle128B);
-        // this CTA's 32 rope dims: 64-byte rows, 8-row groups 512 bytes apart
-        const uint64_t d_rope =
-            smem_desc(smem_u32(stages + stage * STAGE_BYTES + 4 * CHUNK_BYTES), 16, 512, kSwizzle64B);
-        if (elect_one()) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ts(tmem + TM_S, tmem + TM_Q + c * 32 + k * 8, d0 + (uint64_t)((c * CHUNK_BYTES + k * 32) >> 4),
-                     idesc_s, (c | k) != 0);
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            mma_ts(tmem + TM_S, tmem + TM_Q + 128 + k * 8, d_rope + (uint64_t)((k * 32) >> 4), idesc_s, 1u);
-          mma_commit(&s_full);
-        }
-        __syncwarp();
-        ++tile;
-        if (++stage == kStages) stage = 0, phase ^= 1u;
-      }
-      if (aborted()) break;
-      ++seg;
-    }
-    // All score MMAs complete before TMEM is released.
-    if (lane == 0) mma_commit(&mma_drain);
-    __syncwarp();
-    mbar_wait_warp(&mma_drain, 0, kWaitLimit);
-  } else if (warp == 10) {
-    // ============================================================ P.V MMA issuer
-    const uint32_t idesc_pv = idesc_bf16_f32(128, DV, 0, 1);
-    int stage = 0;
-    uint32_t tile = 0, seg = 0;
-    int u, n, t0, t1;
-    bool whole;
-    while (!aborted() && it.next(u, t0, t1, whole)) {
-      if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
-      for (int t = t0; t < t1; ++t) {
-        const bool first = (t == t0);
-        // O is overwritten by a segment's first P.V: the previous segment's
-        // epilogue must have read it.
-        if (first && seg > 0 && !mbar_wait_warp(&o_free, (seg - 1) & 1u, kWaitLimit)) { fail(); break; }
-        if (!mbar_wait_warp(&p_full, tile & 1u, kWaitLimit)) { fail(); break; }
-        tc_fence_after();
-        const uint64_t d0 = smem_desc(smem_u32(stages + stage * STAGE_BYTES), CHUNK_BYTES, 1024, kSwizzle128B);
-        const uint32_t acc0 = first ? 0u : 1u;
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < BN / 16; ++k)
-            mma_ts(tmem + TM_O, tmem + TM_P + k * 8, d0 + (uint64_t)((k * 2048) >> 4), idesc_pv,
-                   k == 0 ? acc0 : 1u);
-          // one commit: the stage barrier also tells the softmax warps that
-          // this P.V has completed (a second commit costs its own latency)
-          mma_commit(&empty_bar[stage]);
-        }
-        __syncwarp();
-        ++tile;
-        if (++stage == kStages) stage = 0;
-      }
-      if (aborted()) break;
-      ++seg;
-    }
-    if (lane == 0) mma_commit(&pv_drain);
-    __syncwarp();
-    mbar_wait_warp(&pv_drain, 0, kWaitLimit);
+  } else if (!kQ8 && warp == kScoreWarp) {
+    issue_scores();
+  } else if (!kQ8 && warp == kPvWarp) {
+    issue_pv();
   } else if (!kQ8 && kThreads > THREADS && warp >= kGatherWarp) {
     // ============================================================ extra gather warps
     // Their share of the TMA row gathers of every tile (selected positions
@@ -859,8 +879,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp >= 6 && warp < 10) {
+  } else if (warp >= kExchangeWarp && warp < kExchangeWarp + 4) {
     // ============================================================ exchange warps
+    if constexpr (kQ8) reg_alloc<kRegsExchange>();
     // Read this CTA's partial scores from TMEM, round them to fp16 (saturating)
     // and send them to the peer with remote stores, one tile ahead of the
     // softmax warps (two send and two receive buffers).
@@ -995,6 +1016,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       atomicOr(a.status, MLA_DEVICE_SCORE_RANGE);
   } else {
     // ============================================================ softmax / epilogue
+    static_assert(kSoftmaxWarp % 4 == kExchangeWarp % 4, "both take TMEM lane quarter warp % 4");
+    if constexpr (kQ8) reg_alloc<kRegsSoftmax>();
     if (a.early_inputs) pdl_wait();   // the query comes from the launch before this one
     const int quarter = warp & 3;
     const int h = 32 * quarter + lane;                    // head = TMEM lane
@@ -1275,7 +1298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync();   // the peer no longer writes into this CTA's shared memory
-  if (warp == 1) {
+  if (warp == kScoreWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -41,8 +41,8 @@ constexpr int STAGES = 3, STAGES_Q8 = 2;   // 8-bit: the third stage's memory ho
 constexpr uint32_t TM_Q = 0, TM_S = 288;  // TMEM columns
 constexpr int kThreads = 192, kThreadsQ8 = 448;
 constexpr int kConvertWarp = 6, kConvertWarps = 8, kConvertThreads = 32 * kConvertWarps;
-constexpr int SLOT_BYTES = kPieces * 16 * kConvertThreads;
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES, SMEM_BYTES_Q8 = STAGES_Q8 * STAGE_BYTES + 2 * SLOT_BYTES;
+using WeightFetch = Q8Fetch<32, kConvertThreads>;
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES, SMEM_BYTES_Q8 = STAGES_Q8 * STAGE_BYTES + 2 * WeightFetch::kSlotBytes;
 constexpr long long kWaitLimit = 1LL << 32;   // clock cycles (~2 s)
 // Tiles that several query tokens share before the next ones are read: 152
 // CTAs x 8 tiles x 72 KB = 88 MB stays in the 129 MB L2.
@@ -221,19 +221,18 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
     // ============================================================ 8-bit producers
     // A warp takes one key at a time, 16 latent dims per lane.
     const int cw = warp - kConvertWarp;
-    Q8Fetch<32> fetch;
+    WeightFetch fetch;
     fetch.slot0 = smem_u32(stages + kStages * STAGE_BYTES) + (cw * 32 + lane) * 16;
-    fetch.slot_bytes = SLOT_BYTES;
-    fetch.piece_bytes = 16 * kConvertThreads;
     fetch.key0 = cw;
     fetch.rope_group = lane >> 3;
     fetch.peers = 0;
-    fetch.mine = lane & 7;
+    fetch.mine = lane % WeightFetch::kIters;
     // Dims 16 lane .. +15 are pieces 2(lane % 4) and the next of box lane / 4; rope piece lane % 8 of box 8.
     const int piece = 2 * (lane & 3);
     const uint32_t box = smem_u32(stages) + (lane >> 2) * BOX_BYTES + cw * 128;
-    const uint32_t box0 = box + ((piece ^ cw) << 4), box1 = box + (((piece + 1) ^ cw) << 4);
-    const uint32_t rope0 = smem_u32(stages) + 8 * BOX_BYTES + (8 * fetch.rope_group + cw) * 128 + (((lane & 7) ^ cw) << 4);
+    const uint32_t odd = (lane >> 2) & 1, half0 = 8 * odd;   // lanes of odd boxes take their second piece first
+    const uint32_t box0 = box + (((piece + odd) ^ cw) << 4), box1 = box + (((piece + 1 - odd) ^ cw) << 4);
+    const uint32_t rope0 = smem_u32(stages) + 8 * BOX_BYTES + (WeightFetch::kStep * fetch.rope_group + cw) * 128 + (((lane & 7) ^ cw) << 4);
     int stage = 0, fills = 0;
     uint32_t phase = 0;
     while (!aborted() && it.next(g, fresh)) {
@@ -252,18 +251,18 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
       // Tile t is converted while the copies of t + 1 and (from its end on) t + 2 are in flight.
       int pos = fetch.my_position(rows, t0);
       int e_now = fetch.my_exponent(rows, pos);
-      fetch.issue(rows, 0, pos);
+      fetch.issue(rows, t0, 0, pos);
       cp_async_commit();
       pos = fetch.my_position(rows, t0 + 1);
       int e_next = fetch.my_exponent(rows, pos);
-      if (t0 + 1 < t1) fetch.issue(rows, 1, pos);
+      if (t0 + 1 < t1) fetch.issue(rows, t0 + 1, 1, pos);
       cp_async_commit();
       for (int t = t0; t < t1; ++t) {
         const int slot = (t - t0) & 1;
         if (fills++ >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
         cp_async_wait<1>();   // this tile's pieces
         const uint32_t off = stage * STAGE_BYTES;
-        fetch.convert(slot, e_now, box0 + off, box1 + off, rope0 + off, rope0 + off + 4 * 8 * 128, (lane & 4) != 0);
+        fetch.convert<128>(slot, e_now, half0, box0 + off, box1 + off, rope0 + off);
         fence_proxy_async_smem();   // generic-proxy writes, read by the MMAs
         __syncwarp();
         if (lane == 0) mbar_arrive(&full_bar[stage]);
@@ -271,7 +270,7 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
         if (t + 2 < t1) {
           pos = fetch.my_position(rows, t + 2);
           e_next = fetch.my_exponent(rows, pos);
-          fetch.issue(rows, slot, pos);
+          fetch.issue(rows, t + 2, slot, pos);
         }
         cp_async_commit();
         if (++stage == kStages) stage = 0, phase ^= 1u;

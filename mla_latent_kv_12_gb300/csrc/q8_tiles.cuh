@@ -2,17 +2,22 @@
 // the codes, exponents and rope keys of 64 keys, and their bf16 values in the
 // swizzled shared-memory layout that a TMA load of a bf16 cache would leave.
 //
-// The fetch runs two tiles ahead: every thread copies its own 16-byte pieces
-// with cp.async into one of two private slots, so nothing but its own
+// The fetch runs two tiles ahead: every warp copies its own 16-byte pieces
+// with cp.async into one of two slots of its own, so nothing but its own
 // wait_group lies between the copy and the conversion, and a window and a
 // selection are the same work.  (Codes fetched into registers a tile ahead took
 // 398 us on a ragged decode of 32 rows: its code, unrolled over the register
 // array beside the softmax's, missed the instruction cache.)
 //
-// kLanes lanes (16 or 32) take one key, 16 dims each, and kThreads threads
-// take 64 / kIters keys at once: piece i of a thread belongs to key i * kStep +
-// key0.  kStep is a multiple of 8, so a thread's place in the 128-byte swizzle
-// (piece ^ (row % 8)) is fixed.
+// kLanes lanes (16 or 32) take one key and kThreads threads take 64 / kIters
+// keys at once: piece i of a thread belongs to key i * kStep + key0.  Lane c
+// copies the key's codes 16c .. 16c + 15, and decodes the eight codes from 8c
+// on and the eight from 8 (kLanes + c) on: two 16-byte pieces of bf16, c % 8
+// of boxes c / 8 and (kLanes + c) / 8, so that every eight lanes of a load or a
+// store cover all banks.  (Sixteen neighbouring codes per lane cost 128 more
+// shared-memory wavefronts per tile; the ragged decode went from 175 to 167 us.)
+// kStep is a multiple of 8, so a thread's place in the 128-byte swizzle (piece
+// ^ (row % 8)) is fixed.
 #pragma once
 
 #include "e4m3.cuh"
@@ -45,6 +50,7 @@ struct Q8Fetch {
   static constexpr int kSlotBytes = (kIters + kRopeIters) * kPieceBytes;
   static_assert(kStep % 8 == 0 && kIters >= 4 && kIters <= 8, "fixed swizzle; lanes to look the keys up");
   uint32_t slot0;                // shared address of this thread's first piece
+  uint32_t codes0;               // and of the codes that it decodes
   int key0;                      // key of piece i is i * kStep + key0
   int rope_group;                // rope piece j belongs to this thread's key 4j + rope_group
   int peers;                     // first lane of the lanes that share this lane's keys
@@ -92,17 +98,15 @@ struct Q8Fetch {
                       p >= 0 ? 16u : 0u);
     }
   }
-  // Slot s as bf16 values.  A piece's 16 dims are two 16-byte pieces of bf16:
-  // `half0` (0 or 8) picks the eight codes decoded first, stored at `box0`, the
-  // others at `box1` (shared addresses for key0; rows lie 128 bytes
-  // apart): half of the lanes take their second eight first, so that eight
-  // lanes of a store hit eight bank groups.  `rope` receives the first
-  // rope piece (rows of rope keys kRopeRow bytes apart).  `exponent` from my_exponent.
-  template <int kRopeRow>
-  __device__ __forceinline__ void convert(int s, int exponent, uint32_t half0, uint32_t box0, uint32_t box1,
-                                          uint32_t rope) const {
-    const uint32_t src = slot0 + s * kSlotBytes, src0 = src + half0, src1 = src + (half0 ^ 8u);
+  // Slot s as bf16 values, its first eight dims at shared address `box`, the
+  // others kBox bytes behind, rows 128 bytes apart; `rope` receives the first
+  // rope piece (rows of rope keys kRopeRow bytes apart).  `exponent` from
+  // my_exponent.
+  template <int kBox, int kRopeRow>
+  __device__ __forceinline__ void convert(int s, int exponent, uint32_t box, uint32_t rope) const {
+    const uint32_t src = slot0 + s * kSlotBytes, src0 = codes0 + s * kSlotBytes, src1 = src0 + 8 * kLanes;
     const uint32_t unit = bf16_unit(clamp_exponent(exponent));
+    __syncwarp();   // the warp's copies have landed (each lane has waited for its own)
     uint32_t nan = 0;
 #pragma unroll
     for (int i = 0; i < kIters; ++i) {
@@ -110,8 +114,8 @@ struct Q8Fetch {
       const uint2 c0 = ld_shared_8(src0 + i * kPieceBytes), c1 = ld_shared_8(src1 + i * kPieceBytes);
       uint32_t v[8];
       nan |= decode_e4m3x16(make_uint4(c0.x, c0.y, c1.x, c1.y), mul2, v);
-      st_shared_16(box0 + i * kStep * 128, make_uint4(v[0], v[1], v[2], v[3]));
-      st_shared_16(box1 + i * kStep * 128, make_uint4(v[4], v[5], v[6], v[7]));
+      st_shared_16(box + i * kStep * 128, make_uint4(v[0], v[1], v[2], v[3]));
+      st_shared_16(box + kBox + i * kStep * 128, make_uint4(v[4], v[5], v[6], v[7]));
     }
 #pragma unroll
     for (int j = 0; j < kRopeIters; ++j)
@@ -122,7 +126,7 @@ struct Q8Fetch {
         const int i = k >> 4, j = k & 7;
         uint32_t code;
         asm volatile("ld.shared.u8 %0, [%1];" : "=r"(code) : "r"(((k & 8) ? src1 : src0) + i * kPieceBytes + j) : "memory");
-        if ((code & 0x7Fu) == 0x7Fu) tc::st_shared_u16(((k & 8) ? box1 : box0) + i * kStep * 128 + 2 * j, 0x7FC0u);
+        if ((code & 0x7Fu) == 0x7Fu) tc::st_shared_u16(box + ((k & 8) ? kBox : 0) + i * kStep * 128 + 2 * j, 0x7FC0u);
       }
     }
   }

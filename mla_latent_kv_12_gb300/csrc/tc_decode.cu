@@ -671,20 +671,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (kQ8 && warp >= kConvertWarp) {
     reg_dealloc<kRegsConvert>();
     // ============================================================ 8-bit producers
-    // Half a warp takes one key at a time, 16 of this CTA's 256 latent dims per lane.
+    // Half a warp takes one key at a time.
     const int cw = warp - kConvertWarp, c = lane & 15;
     DecodeFetch fetch;
     fetch.slot0 = smem_u32(xout + 2 * XH_BYTES) + (cw * 32 + lane) * 16;
+    fetch.codes0 = fetch.slot0 - 16 * c + 8 * c;
     fetch.key0 = 2 * cw + (lane >> 4);
     fetch.rope_group = c >> 2;
     fetch.peers = lane & 16;
     fetch.mine = lane % DecodeFetch::kIters;
-    // Dims 16c .. 16c + 15 are pieces 2(c % 4) and the next of box c / 4; rope
-    // piece c % 4 of 64-byte rows (64-byte swizzle: piece ^ (row / 2 % 4)).
-    const int row = fetch.key0, k0 = row & 7, piece = 2 * (c & 3);
-    const uint32_t box = smem_u32(stages) + (c >> 2) * CHUNK_BYTES + row * 128;
-    const uint32_t odd = (c >> 2) & 1, half0 = 8 * odd;   // lanes of odd boxes take their second piece first
-    const uint32_t box0 = box + (((piece + odd) ^ k0) << 4), box1 = box + (((piece + 1 - odd) ^ k0) << 4);
+    // rope piece c % 4 of 64-byte rows (64-byte swizzle: piece ^ (row / 2 % 4))
+    const int row = fetch.key0, k0 = row & 7;
+    const uint32_t box0 = smem_u32(stages) + (c >> 3) * CHUNK_BYTES + row * 128 + (((c & 7) ^ k0) << 4);
     const uint32_t rope0 = smem_u32(stages) + 4 * CHUNK_BYTES + (DecodeFetch::kStep * fetch.rope_group + row) * 64 +
                            (((c & 3) ^ ((k0 >> 1) & 3)) << 4);
     int stage = 0;
@@ -724,7 +722,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (fills++ >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
         cp_async_wait<1>();   // this tile's pieces
         const uint32_t off = stage * STAGE_BYTES;
-        fetch.convert<64>(slot, e_now, half0, box0 + off, box1 + off, rope0 + off);
+        fetch.convert<2 * CHUNK_BYTES, 64>(slot, e_now, box0 + off, rope0 + off);
         fence_proxy_async_smem();   // generic-proxy writes, read by the MMAs
         __syncwarp();
         if (lane == 0) mbar_arrive(&full_bar[stage]);

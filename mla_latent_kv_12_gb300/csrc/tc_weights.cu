@@ -219,19 +219,17 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
       mbar_wait_warp(&full_bar[k % kStages], (uint32_t)(k / kStages) & 1u, kWaitLimit);
   } else if (kQ8 && warp >= kConvertWarp) {
     // ============================================================ 8-bit producers
-    // A warp takes one key at a time, 16 latent dims per lane.
+    // A warp takes one key at a time.
     const int cw = warp - kConvertWarp;
     WeightFetch fetch;
     fetch.slot0 = smem_u32(stages + kStages * STAGE_BYTES) + (cw * 32 + lane) * 16;
+    fetch.codes0 = fetch.slot0 - 16 * lane + 8 * lane;
     fetch.key0 = cw;
     fetch.rope_group = lane >> 3;
     fetch.peers = 0;
     fetch.mine = lane % WeightFetch::kIters;
-    // Dims 16 lane .. +15 are pieces 2(lane % 4) and the next of box lane / 4; rope piece lane % 8 of box 8.
-    const int piece = 2 * (lane & 3);
-    const uint32_t box = smem_u32(stages) + (lane >> 2) * BOX_BYTES + cw * 128;
-    const uint32_t odd = (lane >> 2) & 1, half0 = 8 * odd;   // lanes of odd boxes take their second piece first
-    const uint32_t box0 = box + (((piece + odd) ^ cw) << 4), box1 = box + (((piece + 1 - odd) ^ cw) << 4);
+    // rope piece lane % 8 of box 8
+    const uint32_t box0 = smem_u32(stages) + (lane >> 3) * BOX_BYTES + cw * 128 + (((lane & 7) ^ cw) << 4);
     const uint32_t rope0 = smem_u32(stages) + 8 * BOX_BYTES + (WeightFetch::kStep * fetch.rope_group + cw) * 128 + (((lane & 7) ^ cw) << 4);
     int stage = 0, fills = 0;
     uint32_t phase = 0;
@@ -262,7 +260,7 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
         if (fills++ >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
         cp_async_wait<1>();   // this tile's pieces
         const uint32_t off = stage * STAGE_BYTES;
-        fetch.convert<128>(slot, e_now, half0, box0 + off, box1 + off, rope0 + off);
+        fetch.convert<4 * BOX_BYTES, 128>(slot, e_now, box0 + off, rope0 + off);
         fence_proxy_async_smem();   // generic-proxy writes, read by the MMAs
         __syncwarp();
         if (lane == 0) mbar_arrive(&full_bar[stage]);

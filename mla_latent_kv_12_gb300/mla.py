@@ -420,22 +420,45 @@ def default_scale(nope: int, rope_dim: int) -> float:
 
 
 # ---------------------------------------------------------------- 8-bit cache
+#
+# These calls run once per layer and token, so their checks are written to be
+# cheap: each tensor's shape and strides are taken once.
 
-def _batch_stride(t: torch.Tensor) -> int:
-    """Batch stride of a cache view: 0 for the packed-flat layout (one buffer row list for every batch row)."""
-    return t.stride(0) if t.shape[0] > 1 else 0
-
-
-def _check_codes(codes: torch.Tensor, scales: torch.Tensor, scale_block: int) -> None:
-    """``codes`` ``[B_buf, T_max, rank]`` and ``scales`` ``[B_buf, >= ceil(T_max / scale_block)]``, one byte each."""
-    assert codes.dim() == 3 and codes.element_size() == 1 and codes.stride(2) == 1
-    assert scales.dim() == 2 and scales.element_size() == 1 and scales.stride(1) == 1
-    assert scales.shape[0] == codes.shape[0] and scales.shape[1] * scale_block >= codes.shape[1]
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _check_lengths(*tensors: Optional[torch.Tensor]) -> None:
+def _launch_stream(stream, *tensors: Optional[torch.Tensor]) -> int:
+    """The stream's handle, after a check that every tensor lives on the current CUDA device."""
+    device = torch.cuda.current_device()
     for t in tensors:
-        assert t is None or (t.dtype == torch.int32 and t.is_contiguous())
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"a tensor on {t.device} in a call on cuda:{device}")
+    return _raw_stream(device) if stream is None else stream.cuda_stream
+
+
+def _check_int32(*tensors: Optional[torch.Tensor]) -> None:
+    for t in tensors:
+        assert t is None or (t.dtype is torch.int32 and t.is_contiguous()), "lengths, starts and counts: contiguous int32"
+
+
+def _cache_strides(t: torch.Tensor):
+    """``(row stride, batch stride)`` of a ``[B_buf, T_max, F]`` view, rows contiguous; the batch stride is 0 for
+    the packed-flat layout (``B_buf == 1``)."""
+    batch, row, last = t.stride()
+    assert last == 1, "the last axis must be contiguous"
+    return row, (batch if t.shape[0] > 1 else 0)
+
+
+def _q8_strides(codes: torch.Tensor, scales: torch.Tensor, scale_block: int):
+    """``(T_max, rank, codes row stride, codes batch stride, scales batch stride)`` of ``codes`` ``[B_buf, T_max,
+    rank]`` and ``scales`` ``[B_buf, >= ceil(T_max / scale_block)]``, one byte each."""
+    rows, t_max, rank = codes.shape
+    n, blocks = scales.shape
+    batch, last = scales.stride()
+    assert codes.element_size() == 1 and scales.element_size() == 1, "codes and scales hold one byte each"
+    assert n == rows and last == 1 and blocks * scale_block >= t_max, "scales: [B_buf, >= ceil(T_max / scale_block)]"
+    row, batch_c = _cache_strides(codes)
+    return t_max, rank, row, batch_c, (batch if rows > 1 else 0)
 
 
 def append_compressed_q8(latent_raw: torch.Tensor, rope_raw: torch.Tensor, norm_weight: torch.Tensor, eps: float,
@@ -446,42 +469,52 @@ def append_compressed_q8(latent_raw: torch.Tensor, rope_raw: torch.Tensor, norm_
     blocks]`` of one byte each (uint8, or float8_e4m3fn / float8_e8m0fnu), one exponent per ``scale_block``
     buffer rows; ``rope`` ``[B_buf, T_max, rope]`` in f32 or bf16."""
     B, S, rank = latent_raw.shape
-    _check_codes(codes, scales, scale_block)
-    _check_lengths(kv_start, kv_len, kv_len_out, row_offsets)
-    assert latent_raw.stride(2) == 1 and rope_raw.stride(2) == 1 and rope.stride(2) == 1 and norm_weight.is_contiguous()
-    assert rope_raw.dtype == latent_raw.dtype == norm_weight.dtype and codes.shape[2] == rank
-    assert rope.shape[:2] == codes.shape[:2] and kv_len.numel() == B
+    l_batch, l_token, l_last = latent_raw.stride()
+    r_batch, r_token, r_last = rope_raw.stride()
+    t_max, width, c_row, c_batch, s_batch = _q8_strides(codes, scales, scale_block)
+    k_row, k_batch = _cache_strides(rope)
+    rows, t_rope, rope_dim = rope.shape
+    dtype = latent_raw.dtype
+    assert l_last == 1 and r_last == 1 and norm_weight.is_contiguous() and width == rank == norm_weight.numel()
+    assert rope_raw.dtype is dtype and norm_weight.dtype is dtype and rope_raw.shape == (B, S, rope_dim)
+    assert rows == codes.shape[0] and t_rope == t_max and kv_len.numel() == B and (rows == 1 or rows == B)
+    _check_int32(kv_start, kv_len, kv_len_out, row_offsets)
+    handle = _launch_stream(stream, latent_raw, rope_raw, norm_weight, codes, scales, rope, kv_start, kv_len, kv_len_out,
+                            row_offsets, device_status)
     _check(lib.mla_append_compressed_q8(
-        _ptr(latent_raw), latent_raw.stride(0), latent_raw.stride(1), _ptr(rope_raw), rope_raw.stride(0),
-        rope_raw.stride(1), _dt(latent_raw), _ptr(norm_weight), float(eps), float(theta), _ptr(row_offsets),
-        _ptr(codes), codes.stride(1), _batch_stride(codes), _ptr(scales), _batch_stride(scales), int(scale_block),
-        _ptr(rope), rope.stride(1), _batch_stride(rope), _dt(rope), _ptr(kv_start), _ptr(kv_len), _ptr(kv_len_out),
-        B, S, rank, rope.shape[2], codes.shape[1], _ptr(device_status), _stream(stream)))
+        latent_raw.data_ptr(), l_batch, l_token, rope_raw.data_ptr(), r_batch, r_token, _dt(latent_raw),
+        norm_weight.data_ptr(), eps, theta, _ptr(row_offsets), codes.data_ptr(), c_row, c_batch, scales.data_ptr(),
+        s_batch, scale_block, rope.data_ptr(), k_row, k_batch, _dt(rope), _ptr(kv_start), kv_len.data_ptr(),
+        _ptr(kv_len_out), B, S, rank, rope_dim, t_max, _ptr(device_status), handle))
 
 
 def quantize_cache(latent: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, scale_block: int, kv_start, kv_len,
                    device_status=None, stream=None) -> torch.Tensor:
     """The windows of ``latent`` ``[B_buf, T_max, rank]`` (f32 or bf16) into ``codes`` / ``scales``."""
-    _check_codes(codes, scales, scale_block)
-    _check_lengths(kv_start, kv_len)
-    assert latent.shape == codes.shape and latent.stride(2) == 1
-    _check(lib.mla_quantize_cache(_ptr(latent), latent.stride(1), _batch_stride(latent), _dt(latent), _ptr(codes),
-                                  codes.stride(1), _batch_stride(codes), _ptr(scales), _batch_stride(scales),
-                                  int(scale_block), _ptr(kv_start), _ptr(kv_len), kv_len.numel(), codes.shape[2],
-                                  codes.shape[1], _ptr(device_status), _stream(stream)))
+    t_max, rank, c_row, c_batch, s_batch = _q8_strides(codes, scales, scale_block)
+    l_row, l_batch = _cache_strides(latent)
+    batch = kv_len.numel()
+    assert latent.shape == codes.shape and latent.shape[0] in (1, batch)
+    _check_int32(kv_start, kv_len)
+    handle = _launch_stream(stream, latent, codes, scales, kv_start, kv_len, device_status)
+    _check(lib.mla_quantize_cache(latent.data_ptr(), l_row, l_batch, _dt(latent), codes.data_ptr(), c_row, c_batch,
+                                  scales.data_ptr(), s_batch, scale_block, _ptr(kv_start), kv_len.data_ptr(), batch, rank,
+                                  t_max, _ptr(device_status), handle))
     return codes
 
 
 def dequantize_cache(codes: torch.Tensor, scales: torch.Tensor, scale_block: int, latent: torch.Tensor, kv_start,
                      kv_len, device_status=None, stream=None) -> torch.Tensor:
     """The windows of an 8-bit cache back into ``latent`` ``[B_buf, T_max, rank]`` (f32 or bf16), exact."""
-    _check_codes(codes, scales, scale_block)
-    _check_lengths(kv_start, kv_len)
-    assert latent.shape == codes.shape and latent.stride(2) == 1
-    _check(lib.mla_dequantize_cache(_ptr(codes), codes.stride(1), _batch_stride(codes), _ptr(scales),
-                                    _batch_stride(scales), int(scale_block), _ptr(latent), latent.stride(1),
-                                    _batch_stride(latent), _dt(latent), _ptr(kv_start), _ptr(kv_len), kv_len.numel(),
-                                    codes.shape[2], codes.shape[1], _ptr(device_status), _stream(stream)))
+    t_max, rank, c_row, c_batch, s_batch = _q8_strides(codes, scales, scale_block)
+    l_row, l_batch = _cache_strides(latent)
+    batch = kv_len.numel()
+    assert latent.shape == codes.shape and latent.shape[0] in (1, batch)
+    _check_int32(kv_start, kv_len)
+    handle = _launch_stream(stream, latent, codes, scales, kv_start, kv_len, device_status)
+    _check(lib.mla_dequantize_cache(codes.data_ptr(), c_row, c_batch, scales.data_ptr(), s_batch, scale_block,
+                                    latent.data_ptr(), l_row, l_batch, _dt(latent), _ptr(kv_start), kv_len.data_ptr(),
+                                    batch, rank, t_max, _ptr(device_status), handle))
     return latent
 
 
@@ -492,38 +525,55 @@ def decode_attend_q8(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
                      device_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """``decode_attend`` over an 8-bit cache (views as in ``append_compressed_q8``; ``rope`` in the query's type).
     The workspace is that of ``decode_workspace_size`` for the query's type."""
-    _, heads, width = q.shape
-    _check_codes(codes, scales, scale_block)
-    _check_lengths(kv_start, kv_len, sel_count)
-    rank, rope_dim = codes.shape[2], rope.shape[2]
-    t_max = codes.shape[1]
-    k_max = sel.shape[1] if sel is not None else 0
-    assert q.stride(2) == 1 and rope.stride(2) == 1 and ctx_out.stride(2) == 1 and width == rank + rope_dim
-    assert q.shape[0] == batch * s_q and kv_len.numel() == batch and ctx_out.shape == (batch * s_q, heads, rank)
-    assert rope.dtype == q.dtype and rope.shape[:2] == codes.shape[:2]
-    assert lse_out is None or (lse_out.dtype == torch.float32 and lse_out.is_contiguous())
-    assert sel is None or (sel.dtype == torch.int32 and sel.is_contiguous() and sel.shape[0] == batch * s_q)
+    n_q, heads, width = q.shape
+    q_row, q_head, q_last = q.stride()
+    x_row, x_head, x_last = ctx_out.stride()
+    t_max, rank, c_row, c_batch, s_batch = _q8_strides(codes, scales, scale_block)
+    k_row, k_batch = _cache_strides(rope)
+    rows, t_rope, rope_dim = rope.shape
+    assert q_last == 1 and x_last == 1 and width == rank + rope_dim and n_q == batch * s_q
+    assert ctx_out.shape == (n_q, heads, rank) and rope.dtype is q.dtype and t_rope == t_max
+    assert rows == codes.shape[0] and (rows == 1 or rows == batch) and kv_len.numel() == batch
+    _check_int32(kv_start, kv_len)
+    if lse_out is not None:
+        assert lse_out.dtype is torch.float32 and lse_out.is_contiguous() and lse_out.numel() == n_q * heads
+    k_max = 0
+    if sel is not None:
+        k_max = sel.shape[1]
+        assert sel.shape[0] == n_q and sel_count is not None and sel_count.numel() == n_q
+        _check_int32(sel, sel_count)
     if workspace is None:
         nbytes = decode_workspace_size(batch, s_q, heads, rank, rope_dim, t_max, k_max, sel is not None, q.dtype)
         workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
+    assert workspace.element_size() == 1 and workspace.is_contiguous()
+    handle = _launch_stream(stream, q, codes, scales, rope, kv_start, kv_len, ctx_out, lse_out, sel, sel_count, workspace,
+                            device_status)
     _check(lib.mla_decode_attend_q8(
-        _ptr(q), q.stride(0), q.stride(1), _ptr(codes), codes.stride(1), _batch_stride(codes), _ptr(scales),
-        _batch_stride(scales), int(scale_block), _ptr(rope), rope.stride(1), _batch_stride(rope), _dt(q),
-        _ptr(kv_start), _ptr(kv_len), batch, s_q, heads, rank, rope_dim, t_max, _ptr(sel), _ptr(sel_count), k_max,
-        float(softmax_scale), _ptr(ctx_out), ctx_out.stride(0), ctx_out.stride(1), _dt(ctx_out), _ptr(lse_out),
-        _ptr(workspace), workspace.numel(), _ptr(device_status), _stream(stream)))
+        q.data_ptr(), q_row, q_head, codes.data_ptr(), c_row, c_batch, scales.data_ptr(), s_batch, scale_block,
+        rope.data_ptr(), k_row, k_batch, _dt(q), _ptr(kv_start), kv_len.data_ptr(), batch, s_q, heads, rank, rope_dim,
+        t_max, _ptr(sel), _ptr(sel_count), k_max, softmax_scale, ctx_out.data_ptr(), x_row, x_head, _dt(ctx_out),
+        _ptr(lse_out), workspace.data_ptr(), workspace.numel(), _ptr(device_status), handle))
     return ctx_out
 
 
 # ---------------------------------------------------------------- attention weights and eviction
 
-def _check_weights(q, rope, lse, weights, kv_start, kv_len, batch, s_q, t_max, rank) -> None:
-    _check_lengths(kv_start, kv_len)
-    assert q.shape[0] == batch * s_q and kv_len.numel() == batch and q.shape[2] == rank + rope.shape[2]
-    assert q.stride(2) == 1 and rope.stride(2) == 1 and rope.dtype == q.dtype
-    assert lse.dtype == torch.float32 and lse.is_contiguous() and lse.numel() == q.shape[0] * q.shape[1]
-    assert weights.dtype == torch.float32 and weights.dim() == 2 and weights.stride(1) == 1
-    assert weights.shape[1] >= t_max
+def _weight_strides(q: torch.Tensor, lse: torch.Tensor, weights: torch.Tensor, rope: torch.Tensor, kv_start, kv_len,
+                    batch: int, s_q: int, rows: int, t_max: int, rank: int):
+    """Checks shared by both forms; ``(heads, q row stride, q head stride, rope_dim, rope strides, weights batch
+    stride)``."""
+    n_q, heads, width = q.shape
+    q_row, q_head, q_last = q.stride()
+    k_rows, t_rope, rope_dim = rope.shape
+    k_row, k_batch = _cache_strides(rope)
+    w_batch, w_last = weights.stride()
+    w_rows, w_cols = weights.shape
+    assert q_last == 1 and n_q == batch * s_q and width == rank + rope_dim and rope.dtype is q.dtype
+    assert k_rows == rows and t_rope == t_max and (rows == 1 or rows == batch) and kv_len.numel() == batch
+    assert lse.dtype is torch.float32 and lse.is_contiguous() and lse.numel() == n_q * heads
+    assert weights.dtype is torch.float32 and w_last == 1 and w_rows == rows and w_cols >= t_max
+    _check_int32(kv_start, kv_len)
+    return heads, q_row, q_head, rope_dim, k_row, k_batch, (w_batch if rows > 1 else 0)
 
 
 def key_weights(q: torch.Tensor, latent: torch.Tensor, rope: torch.Tensor, lse: torch.Tensor, kv_start, kv_len,
@@ -532,15 +582,16 @@ def key_weights(q: torch.Tensor, latent: torch.Tensor, rope: torch.Tensor, lse: 
     """Adds the attention weight that each cached key received from ``q`` (all heads and tokens) to ``weights``
     ``[B_buf, T_max]`` f32, decayed first; the ``n_new`` newest keys start from zero.  ``q`` and the cache as for
     ``decode_attend``, ``lse`` its ``lse_out``."""
-    t_max, rank = latent.shape[1], latent.shape[2]
-    assert latent.stride(2) == 1 and latent.dtype == q.dtype and rope.shape[:2] == latent.shape[:2]
-    assert weights.shape[0] == latent.shape[0]
-    _check_weights(q, rope, lse, weights, kv_start, kv_len, batch, s_q, t_max, rank)
+    rows, t_max, rank = latent.shape
+    l_row, l_batch = _cache_strides(latent)
+    assert latent.dtype is q.dtype
+    heads, q_row, q_head, rope_dim, k_row, k_batch, w_batch = _weight_strides(q, lse, weights, rope, kv_start, kv_len,
+                                                                              batch, s_q, rows, t_max, rank)
+    handle = _launch_stream(stream, q, latent, rope, lse, kv_start, kv_len, weights, device_status)
     _check(lib.mla_key_weights(
-        _ptr(q), q.stride(0), q.stride(1), _ptr(latent), latent.stride(1), _batch_stride(latent), _ptr(rope),
-        rope.stride(1), _batch_stride(rope), _dt(q), _ptr(kv_start), _ptr(kv_len), batch, s_q, q.shape[1], rank,
-        rope.shape[2], t_max, _ptr(lse), float(softmax_scale), float(decay), int(n_new), _ptr(weights),
-        _batch_stride(weights), _ptr(device_status), _stream(stream)))
+        q.data_ptr(), q_row, q_head, latent.data_ptr(), l_row, l_batch, rope.data_ptr(), k_row, k_batch, _dt(q),
+        _ptr(kv_start), kv_len.data_ptr(), batch, s_q, heads, rank, rope_dim, t_max, lse.data_ptr(), softmax_scale, decay,
+        n_new, weights.data_ptr(), w_batch, _ptr(device_status), handle))
     return weights
 
 
@@ -549,16 +600,14 @@ def key_weights_q8(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, s
                    weights: torch.Tensor, decay: float = 1.0, n_new: int = 0,
                    device_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """``key_weights`` over an 8-bit cache."""
-    t_max, rank = codes.shape[1], codes.shape[2]
-    _check_codes(codes, scales, scale_block)
-    assert rope.shape[:2] == codes.shape[:2] and weights.shape[0] == codes.shape[0]
-    _check_weights(q, rope, lse, weights, kv_start, kv_len, batch, s_q, t_max, rank)
+    t_max, rank, c_row, c_batch, s_batch = _q8_strides(codes, scales, scale_block)
+    heads, q_row, q_head, rope_dim, k_row, k_batch, w_batch = _weight_strides(q, lse, weights, rope, kv_start, kv_len,
+                                                                              batch, s_q, codes.shape[0], t_max, rank)
+    handle = _launch_stream(stream, q, codes, scales, rope, lse, kv_start, kv_len, weights, device_status)
     _check(lib.mla_key_weights_q8(
-        _ptr(q), q.stride(0), q.stride(1), _ptr(codes), codes.stride(1), _batch_stride(codes), _ptr(scales),
-        _batch_stride(scales), int(scale_block), _ptr(rope), rope.stride(1), _batch_stride(rope), _dt(q),
-        _ptr(kv_start), _ptr(kv_len), batch, s_q, q.shape[1], rank, rope.shape[2], t_max, _ptr(lse),
-        float(softmax_scale), float(decay), int(n_new), _ptr(weights), _batch_stride(weights), _ptr(device_status),
-        _stream(stream)))
+        q.data_ptr(), q_row, q_head, codes.data_ptr(), c_row, c_batch, scales.data_ptr(), s_batch, scale_block,
+        rope.data_ptr(), k_row, k_batch, _dt(q), _ptr(kv_start), kv_len.data_ptr(), batch, s_q, heads, rank, rope_dim,
+        t_max, lse.data_ptr(), softmax_scale, decay, n_new, weights.data_ptr(), w_batch, _ptr(device_status), handle))
     return weights
 
 
@@ -567,28 +616,38 @@ def evict_plan(weights: torch.Tensor, kv_start, kv_len, n_keep: int, n_sink: int
                stream=None) -> torch.Tensor:
     """Window positions that stay, ascending: ``kept`` ``[B, >= n_keep]`` int32, ``counts`` ``[B]`` (``n_keep``, or
     -1 for a row within its budget).  ``weights`` ``[B_buf, T_max]`` f32."""
-    assert weights.dtype == torch.float32 and weights.dim() == 2 and weights.stride(1) == 1
-    assert kept.dtype == torch.int32 and kept.dim() == 2 and kept.stride(1) == 1 and kept.shape[1] >= n_keep
-    _check_lengths(kv_start, kv_len, counts, kv_len_out)
+    rows, t_max = weights.shape
+    w_batch, w_last = weights.stride()
+    n, width = kept.shape
+    k_row, k_last = kept.stride()
     batch = kv_len.numel()
-    assert kept.shape[0] == counts.numel() == batch
-    _check(lib.mla_evict_plan(_ptr(weights), _batch_stride(weights), _ptr(kv_start), _ptr(kv_len), batch,
-                              weights.shape[1], int(n_keep), int(n_sink), int(n_recent), _ptr(kept), kept.stride(0),
-                              _ptr(counts), _ptr(kv_len_out), _ptr(device_status), _stream(stream)))
+    assert weights.dtype is torch.float32 and w_last == 1 and (rows == 1 or rows == batch)
+    assert kept.dtype is torch.int32 and k_last == 1 and width >= n_keep and n == batch == counts.numel()
+    _check_int32(kv_start, kv_len, counts, kv_len_out)
+    handle = _launch_stream(stream, weights, kv_start, kv_len, kept, counts, kv_len_out, device_status)
+    _check(lib.mla_evict_plan(weights.data_ptr(), w_batch if rows > 1 else 0, _ptr(kv_start), kv_len.data_ptr(), batch,
+                              t_max, n_keep, n_sink, n_recent, kept.data_ptr(), k_row, counts.data_ptr(), _ptr(kv_len_out),
+                              _ptr(device_status), handle))
     return kept
 
 
 def cache_compact(arrays, kv_start, kept: torch.Tensor, counts: torch.Tensor, device_status=None, stream=None) -> None:
     """Moves each row's kept tokens to the front of its window in every array of ``arrays`` (``[B_buf, T_max, F]``
     views of any dtype, last dim contiguous; one launch), in place and in order."""
-    assert kept.dtype == torch.int32 and kept.dim() == 2 and kept.stride(1) == 1
-    _check_lengths(kv_start, counts)
-    t_max = arrays[0].shape[1]
+    n, width = kept.shape
+    k_row, k_last = kept.stride()
+    batch = counts.numel()
+    rows, t_max, _ = arrays[0].shape
+    assert kept.dtype is torch.int32 and k_last == 1 and n == batch and (rows == 1 or rows == batch)
+    _check_int32(kv_start, counts)
     states = (StateArray * len(arrays))()
     for s, a in zip(states, arrays):
-        assert a.dim() == 3 and a.stride(2) == 1 and a.shape[:2] == arrays[0].shape[:2]
+        a_rows, a_len, features = a.shape
+        a_row, a_batch = _cache_strides(a)
         size = a.element_size()
-        s.data, s.row_bytes = a.data_ptr(), a.shape[2] * size
-        s.token_stride_bytes, s.batch_stride_bytes = a.stride(1) * size, _batch_stride(a) * size
-    _check(lib.mla_cache_compact(states, len(arrays), _ptr(kv_start), _ptr(kept), kept.stride(0), _ptr(counts),
-                                 kept.shape[1], counts.numel(), t_max, _ptr(device_status), _stream(stream)))
+        assert a_rows == rows and a_len == t_max
+        s.data, s.token_stride_bytes, s.row_bytes = a.data_ptr(), a_row * size, features * size
+        s.batch_stride_bytes = a_batch * size
+    handle = _launch_stream(stream, kv_start, kept, counts, device_status, *arrays)
+    _check(lib.mla_cache_compact(states, len(arrays), _ptr(kv_start), kept.data_ptr(), k_row, counts.data_ptr(), width,
+                                 batch, t_max, _ptr(device_status), handle))

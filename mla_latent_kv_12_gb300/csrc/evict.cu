@@ -12,13 +12,13 @@
 // the passes, not by the 4 bytes per token.
 //
 // Compaction.  Kept positions ascend, so row j's source kept[j] >= j: rows are
-// moved in chunks of consecutive j, each read whole before any of it is
-// written, and a chunk's writes only reach rows that no later chunk reads.  The
-// next chunk's loads are issued before the current one's stores (its sources
-// lie behind them), so the memory stays busy across the barrier.  Rows of a
-// window are one dependent chain; the parallelism is over batch rows and 64-byte
-// slices of a token's bytes, and over the CTAs of a cluster (which share each
-// chunk, with a cluster barrier) when those are few.
+// moved in chunks of consecutive j, and a chunk is written only when all
+// chunks up to it have been read.  Later chunks read rows behind all of its
+// own, so their loads are issued ahead (kDepth chunks, in registers) and the memory
+// stays busy across the barriers.  Rows of a window are one dependent chain;
+// the parallelism is over batch rows and 64-byte slices of a token's bytes, and
+// over the CTAs of a cluster (which share each chunk, with a cluster barrier)
+// when those are few.
 #include "mla_internal.h"
 #include "tc_common.cuh"
 #include "tc_host.h"
@@ -26,7 +26,7 @@
 namespace mla {
 namespace {
 
-constexpr int kPlanThreads = 512;
+constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
@@ -60,13 +60,15 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_s, int& total) {
   }
   if (lane == 31) warp_s[warp] = inc;
   __syncthreads();
-  int before = 0;
-  total = 0;
+  static_assert(kPlanWarps == 32, "one warp's sum per lane");
+  const int mine = warp_s[lane];
+  int all = mine, before = lane < warp ? mine : 0;
 #pragma unroll
-  for (int w = 0; w < kPlanWarps; ++w) {
-    if (w < warp) before += warp_s[w];
-    total += warp_s[w];
+  for (int o = 16; o > 0; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
   }
+  total = all;
   __syncthreads();
   return before + inc - v;
 }
@@ -126,30 +128,37 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
           if (pass == 0 && in_smem && i < hi) keys_s[i - lo] = key[u];
           const bool counts = i < hi && (pass == 0 || (key[u] >> (32 - known)) == prefix);
           const int digit = (int)((key[u] >> shift) & ((1u << width) - 1u));
-          // lanes that all hold one digit (weights that underflowed, say) add once
-          const uint32_t who = __ballot_sync(0xffffffffu, counts);
-          if (who == 0) continue;
-          const int leader = __ffs(who) - 1;
-          const int d0 = __shfl_sync(0xffffffffu, digit, leader);
-          if (__all_sync(0xffffffffu, !counts || digit == d0)) {
-            if (lane == leader) atomicAdd(&hist[d0], __popc(who));
-          } else if (counts) {
-            atomicAdd(&hist[digit], 1);
+          // Lanes with the digit of the first one that counts add once, and so
+          // do those with the first one's of the others (many weights share a
+          // value, zero above all, and equal addresses are added one by one);
+          // the rest add for themselves.
+          uint32_t who = __ballot_sync(0xffffffffu, counts);
+          bool left = counts;
+#pragma unroll
+          for (int round = 0; round < 2; ++round) {
+            if (who == 0) break;
+            const int leader = __ffs(who) - 1;
+            const int common = __shfl_sync(0xffffffffu, digit, leader);   // (by every lane: not behind a condition)
+            const uint32_t same = __ballot_sync(0xffffffffu, left && digit == common);
+            if (lane == leader) atomicAdd(&hist[digit], __popc(same));
+            left = left && !((same >> lane) & 1u);
+            who &= ~same;
           }
+          if (left) atomicAdd(&hist[digit], 1);
         }
       }
       tc::cluster_sync();   // every CTA's histogram is complete
-      // thread t sums bins 4t .. 4t+3 over the cluster; the one whose bins hold the rest-th key takes it
-      const int nb = 1 << width, b0 = 4 * threadIdx.x;
-      int h[4] = {0, 0, 0, 0};
+      // thread t sums bins 2t and 2t + 1 over the cluster; the one whose bins hold the rest-th key takes it
+      const int nb = 1 << width, b0 = 2 * threadIdx.x;
+      int h[2] = {0, 0};
       if (b0 < nb)
         for (int c = 0; c < ncta; ++c)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) h[k] += load_peer(&hist[b0 + k], (uint32_t)c);
+          for (int k = 0; k < 2; ++k) h[k] += load_peer(&hist[b0 + k], (uint32_t)c);
       int all;
-      int before = block_prefix(h[0] + h[1] + h[2] + h[3], warp_s, all);
+      int before = block_prefix(h[0] + h[1], warp_s, all);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 2; ++k) {
         if (before < rest && rest <= before + h[k]) {   // exactly one thread and bin
           digit_s = b0 + k;
           rest_s = rest - before;
@@ -168,6 +177,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
   const int wlo = min(hi, lo + warp * wspan), whi = min(hi, wlo + wspan);
   int n_less = 0, n_tie = 0;
   if (take > 0)
+#pragma unroll 4
     for (int i0 = wlo; i0 < whi; i0 += 32) {
       const int i = i0 + lane;
       const uint32_t key = i < whi ? key_at(i) : 0xFFFFFFFFu;
@@ -188,6 +198,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
   if (take > 0) {
     int out = p.n_sink + before_less + min(before_tie, rest), ties = before_tie;
     const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
     for (int i0 = wlo; i0 < whi; i0 += 32) {
       const int i = i0 + lane;
       const uint32_t key = i < whi ? key_at(i) : 0xFFFFFFFFu;
@@ -213,7 +224,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
 // ------------------------------------------------------------------ compaction
 
 constexpr int kMoveThreads = 512;
-constexpr int kMoves = 4;          // units in flight per thread and chunk
+constexpr int kMoves = 2;          // units per thread and chunk
+constexpr int kDepth = 4;          // chunks in flight
 constexpr int kSliceBytes = 64;    // of a token's bytes moved by one CTA
 
 struct Slice {
@@ -222,14 +234,20 @@ struct Slice {
   int units;           // per row
 };
 
+// A word that depends on every byte of v (its value does not matter).
+__device__ __forceinline__ uint32_t word_of(uint4 v) { return v.x ^ v.y ^ v.z ^ v.w; }
+__device__ __forceinline__ uint32_t word_of(uint2 v) { return v.x ^ v.y; }
+__device__ __forceinline__ uint32_t word_of(uint32_t v) { return v; }
+
 template <typename V>
 __device__ __forceinline__ void move_rows(const Slice s, const CompactParams& p, const int32_t* kept, int count,
-                                          int start, int crank, int ncta, bool flags) {
+                                          int start, int crank, int ncta, bool flags, uint32_t* arrived) {
   // Thread i of the cluster moves unit i % units of rows i / units + k * rows_per_step
   const int rows_cta = kMoveThreads / s.units;              // rows per step of this CTA
   const int row0 = threadIdx.x / s.units, part = threadIdx.x % s.units;
   const bool active = row0 < rows_cta;
   const int step = rows_cta * ncta, chunk = step * kMoves;
+  const int n_chunks = (count + chunk - 1) / chunk;
   auto row_of = [&](int c, int u) { return c * chunk + u * step + crank * rows_cta + row0; };
   // The position of row j if it is one to move: above its predecessor's (so >= j), inside the buffer.
   int pos[kMoves];
@@ -238,47 +256,58 @@ __device__ __forceinline__ void move_rows(const Slice s, const CompactParams& p,
 #pragma unroll
     for (int u = 0; u < kMoves; ++u) {
       const int j = row_of(c, u);
-      const bool in = active && j < count;
+      const bool in = active && c < n_chunks && j < count;
       cur[u] = in ? __ldg(kept + j) : -1;
       prev[u] = in && j > 0 ? __ldg(kept + j - 1) : -1;
     }
 #pragma unroll
     for (int u = 0; u < kMoves; ++u) {
       const int j = row_of(c, u);
-      const bool in = active && j < count;
+      const bool in = active && c < n_chunks && j < count;
       const bool good = in && cur[u] >= j && cur[u] > prev[u] && (int64_t)start + cur[u] < p.t_max;
       if (in && !good && flags && p.status) atomicOr(p.status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
       pos[u] = good && cur[u] != j ? cur[u] : -1;   // a row already in place stays
     }
   };
-  V v[kMoves], next[kMoves];
-  bool moved[kMoves], next_moved[kMoves];
+  V v[kDepth][kMoves];
+  bool moved[kDepth][kMoves];
   auto load_rows = [&](V(&dst)[kMoves], bool(&m)[kMoves]) {
 #pragma unroll
     for (int u = 0; u < kMoves; ++u) {
       m[u] = pos[u] >= 0;
+      dst[u] = V{};
       if (m[u]) dst[u] = *(reinterpret_cast<const V*>(s.data + (int64_t)pos[u] * s.stride) + part);
     }
   };
-  const int n_chunks = (count + chunk - 1) / chunk;
   load_positions(0);
-  load_rows(v, moved);
-  load_positions(1);
-  for (int c = 0; c < n_chunks; ++c) {
-    // every thread of the cluster has read its rows of chunk c
-    if (ncta > 1) tc::cluster_sync(); else __syncthreads();
-    load_rows(next, next_moved);   // chunk c + 1: its sources lie behind every row written below
-    load_positions(c + 2);
 #pragma unroll
-    for (int u = 0; u < kMoves; ++u) {
-      if (moved[u]) *(reinterpret_cast<V*>(s.data + (int64_t)row_of(c, u) * s.stride) + part) = v[u];
-      v[u] = next[u];
-      moved[u] = next_moved[u];
+  for (int d = 0; d < kDepth; ++d) {
+    load_rows(v[d], moved[d]);
+    load_positions(d + 1);
+  }
+  for (int c0 = 0; c0 < n_chunks; c0 += kDepth) {
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      const int c = c0 + d;
+      if (c >= n_chunks) break;   // the same in the whole cluster
+      // Every thread of the cluster holds its rows of chunk c: the store of a
+      // word made of them waits for them before the barrier.
+      uint32_t word = 0;
+#pragma unroll
+      for (int u = 0; u < kMoves; ++u) word ^= word_of(v[d][u]);
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(tc::smem_u32(arrived)), "r"(word) : "memory");
+      if (ncta > 1) tc::cluster_sync(); else __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kMoves; ++u)
+        if (moved[d][u]) *(reinterpret_cast<V*>(s.data + (int64_t)row_of(c, u) * s.stride) + part) = v[d][u];
+      load_rows(v[d], moved[d]);   // chunk c + kDepth
+      load_positions(c + kDepth + 1);
     }
   }
 }
 
-__global__ void __launch_bounds__(kMoveThreads) compact_kernel(const __grid_constant__ CompactParams p) {
+__global__ void __launch_bounds__(kMoveThreads, 2) compact_kernel(const __grid_constant__ CompactParams p) {
+  __shared__ uint32_t arrived_s[kMoveThreads];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int ncta = (int)cluster_size();
   const int crank = (int)tc::cluster_ctarank();
@@ -304,11 +333,11 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const __grid_cons
                   a.row_bytes_stride, bytes / a.unit};
     const int32_t* kept = p.kept + b * p.kept_stride;
     switch (a.unit) {
-      case 16: move_rows<uint4>(s, p, kept, count, start, crank, ncta, flags); break;
-      case 8: move_rows<uint2>(s, p, kept, count, start, crank, ncta, flags); break;
-      case 4: move_rows<uint32_t>(s, p, kept, count, start, crank, ncta, flags); break;
-      case 2: move_rows<uint16_t>(s, p, kept, count, start, crank, ncta, flags); break;
-      default: move_rows<uint8_t>(s, p, kept, count, start, crank, ncta, flags); break;
+      case 16: move_rows<uint4>(s, p, kept, count, start, crank, ncta, flags, arrived_s + threadIdx.x); break;
+      case 8: move_rows<uint2>(s, p, kept, count, start, crank, ncta, flags, arrived_s + threadIdx.x); break;
+      case 4: move_rows<uint32_t>(s, p, kept, count, start, crank, ncta, flags, arrived_s + threadIdx.x); break;
+      case 2: move_rows<uint16_t>(s, p, kept, count, start, crank, ncta, flags, arrived_s + threadIdx.x); break;
+      default: move_rows<uint8_t>(s, p, kept, count, start, crank, ncta, flags, arrived_s + threadIdx.x); break;
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -358,7 +387,8 @@ cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
   int64_t slices = 0;
   for (int i = 0; i < p.n_arrays; ++i) slices += (p.a[i].row_bytes + kSliceBytes - 1) / kSliceBytes;
   // CTAs per slice: enough to fill the GPU twice, while each still has a chunk of rows
-  const int64_t chunks = (p.n_keep + kMoveThreads * kMoves / 4 - 1) / (kMoveThreads * kMoves / 4);
+  const int64_t chunk = kMoveThreads * kMoves / (kSliceBytes / 16);
+  const int64_t chunks = (p.n_keep + chunk - 1) / chunk;
   int ncta = 1;
   while (ncta * 2 <= kMaxCluster && ncta * 2 <= chunks && slices * p.batch * ncta * 2 <= 2 * device_sm_count()) ncta *= 2;
   if (slices * ncta > 0x7fffffffLL) return cudaErrorInvalidValue;

@@ -2,13 +2,16 @@
 // RoPE, 8-bit codes), and conversion of cache windows between bf16 / f32 and
 // 8 bits.
 //
-// Rows are taken in tiles of max(block, 16) buffer rows that start on whole
-// blocks, one CTA per tile, one warp per token at a time.  The unit of a block is
-// known only once the largest magnitude of all its tokens is, so a tile is
-// walked twice: the first walk reduces each token (sum of squares, largest
-// magnitude), the second, after a barrier, encodes; it reads the tokens again
-// from L1 / L2, which costs no memory traffic.  Bound by memory: 2 * rank +
-// 2 * rope bytes in and rank + 2 * rope bytes out per bf16 token.
+// The unit of a block is known only once the largest magnitude of all its tokens
+// is.  Rows are taken in tiles that start on whole blocks, one CTA per tile.
+// encode_kernel (ranks up to 512 of aligned rows) takes 64 rows, four
+// neighbouring ones per warp, and holds them in registers: a warp's loads are
+// all in flight together, its tokens are reduced, and then encoded -- after a
+// barrier where a block spans warps, at once where it does not (blocks of up
+// to four tokens).  encode_walk_kernel serves every other shape: it walks a
+// tile of max(block, 16) rows twice, the second time from L1 / L2.  Bound by
+// memory: 2 * rank + 2 * rope bytes in and rank + 2 * rope bytes out per bf16
+// token.
 #include <cuda_bf16.h>
 
 #include "e4m3.cuh"
@@ -74,32 +77,281 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// The rows that a batch row's call writes, and the state of its tile walk.
+template <bool kNorm>
+struct EncodeRow {
+  int len, start;
+  int64_t pos0;        // position of the first new token
+  bool ok;
+  int64_t lo, hi;      // rows written: [lo, hi)
+  __device__ EncodeRow(const EncodeParams& p, int b, bool flag) {
+    len = p.kv_len[b];
+    start = p.kv_start ? p.kv_start[b] : 0;
+    pos0 = !kNorm ? 0 : (p.row_offsets ? (int64_t)p.row_offsets[b] : (int64_t)len);
+    const bool aligned = (start & ((1 << p.block_shift) - 1)) == 0;
+    const bool fits = len >= 0 && start >= 0 && pos0 >= 0 && (int64_t)start + len + (kNorm ? p.s_new : 0) <= p.t_max;
+    ok = fits && aligned;
+    if (!ok && flag && p.status) atomicOr(p.status, fits ? MLA_DEVICE_BAD_BLOCK_START : MLA_DEVICE_INDEX_OUT_OF_RANGE);
+    lo = kNorm ? (int64_t)start + len : start;
+    hi = kNorm ? lo + p.s_new : (int64_t)start + len;
+  }
+  __device__ int64_t tiles(int tile_rows) const { return ok && hi > lo ? (hi - 1) / tile_rows - lo / tile_rows + 1 : 0; }
+};
+
+// The exponent of block k of a tile at buffer row `base`, from the largest
+// magnitude of its new tokens: never below that of tokens the block holds
+// already (rows [max(block start, start), lo); `old` receives their exponent
+// byte, else -1).  Written to the cache.
+template <bool kNorm>
+__device__ __forceinline__ int block_exponent(const EncodeParams& p, const EncodeRow<kNorm>& row, uint8_t* scales,
+                                              int64_t base, int k, float amax, int& old) {
+  uint8_t* at = scales + (base >> p.block_shift) + k;
+  int e = exponent_for(amax);
+  old = -1;
+  if (kNorm && base + ((int64_t)k << p.block_shift) < row.lo && row.start < row.lo) {
+    old = *at;
+    e = max(e, clamp_exponent(old));
+  }
+  if (!(amax <= 448.f * 128.f) && p.status) atomicOr(p.status, MLA_DEVICE_VALUE_RANGE);
+  *at = (uint8_t)e;
+  return e;
+}
+
+// The rope key of new token t, pairs from `lane` on (every 32nd): rotated at its position, into buffer row `row`.
+template <typename TI, typename TR>
+__device__ __forceinline__ void append_rope(const EncodeParams& p, int b, int64_t t, int64_t row, int64_t pos, int lane) {
+  const TI* rr = static_cast<const TI*>(p.rope_raw) + b * p.rr_row_stride + t * p.rr_tok_stride;
+  TR* dr = static_cast<TR*>(p.rope) + b * p.rope_batch_stride + row * p.rope_row_stride;
+  const int half = p.rope_dim >> 1;
+  for (int j = lane; j < half; j += 32) {
+    float re, im;
+    rope_rotate_pair(to_f(rr[2 * j]), to_f(rr[2 * j + 1]), pos, p.inv_freq[j], re, im);
+    put(dr + j, re);
+    put(dr + half + j, im);
+  }
+}
+
+// The codes of rows [first, lo), which a block held before, move from unit `old` to unit `e`.
+template <int kThreads>
+__device__ __forceinline__ void move_codes(const EncodeParams& p, uint8_t* codes, int64_t first, int64_t lo, int old,
+                                           int e) {
+  const float unit = unit_of(clamp_exponent(old)), to_units = inverse_unit_of(e);
+  for (int64_t r = first + (threadIdx.x >> 5); r < lo; r += kThreads / 32) {
+    uint8_t* dst = codes + r * p.codes_row_stride;
+    for (int i = threadIdx.x & 31; i < p.rank; i += 32) dst[i] = encode_e4m3(decode_e4m3(dst[i], unit) * to_units);
+  }
+}
+
+__device__ __forceinline__ uint2 encode8(const float (&x)[8]) {
+  return make_uint2(encode_e4m3x2(x[0], x[1]) | (uint32_t)encode_e4m3x2(x[2], x[3]) << 16,
+                    encode_e4m3x2(x[4], x[5]) | (uint32_t)encode_e4m3x2(x[6], x[7]) << 16);
+}
+
+// Eight consecutive raw values as loaded.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 a;
+  __device__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[2 * j] = __uint_as_float(w[j] << 16), v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ void load(const float* p) { a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1]; }
+  __device__ void get(float (&v)[8]) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
+
+// Tiles of 64 rows, four neighbouring ones per warp; lane l holds elements
+// 8l .. 8l + 7 and 256 + those of each.
+constexpr int kHeldWarps = 16, kHeldRows = 4, kHeldTile = kHeldWarps * kHeldRows, kHeldRank = 512;
+static_assert(kHeldTile >= kMaxScaleBlock, "a tile holds whole blocks");
+
+template <bool kNorm, typename TI, typename TR>
+__global__ void __launch_bounds__(kHeldWarps * 32, sizeof(TI) == 2 ? 2 : 1) encode_kernel(const __grid_constant__ EncodeParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ uint32_t amax_s[kHeldTile];   // per block of the tile, f32 bits (non-negative: ordered as integers)
+  __shared__ int exp_s[kHeldTile], old_s;
+  const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const EncodeRow<kNorm> row(p, b, blockIdx.x == 0 && threadIdx.x == 0);
+  uint8_t* codes = p.codes + b * p.codes_batch_stride;
+  uint8_t* scales = p.scales + b * p.scales_batch_stride;
+  const TI* src = static_cast<const TI*>(p.latent_raw) + b * p.lr_row_stride;
+  const TI* gain = static_cast<const TI*>(p.weight);
+  const int block = 1 << p.block_shift, n_blocks = kHeldTile >> p.block_shift;
+  const bool warp_blocks = block <= kHeldRows;   // no block spans warps
+  const int64_t n_tiles = row.tiles(kHeldTile);
+  const int half = p.rope_dim >> 1;
+  bool live[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) live[c] = 256 * c + 8 * lane < p.rank;
+
+  for (int64_t tile = blockIdx.x; tile < n_tiles; tile += gridDim.x) {
+    const int64_t base = (row.lo / kHeldTile + tile) * kHeldTile;
+    const int r_lo = (int)max((int64_t)0, row.lo - base), r_hi = (int)min((int64_t)kHeldTile, row.hi - base);
+    const int r0 = kHeldRows * warp;   // this warp's first row
+    auto mine = [&](int k) { return r0 + k >= r_lo && r0 + k < r_hi; };
+    Raw8<TI> raw[kHeldRows][2];
+    float ra[kHeldRows], rb[kHeldRows];   // this lane's rope pair (j = lane)
+#pragma unroll
+    for (int k = 0; k < kHeldRows; ++k) {
+      if (!mine(k)) continue;
+      const int64_t t = kNorm ? base + r0 + k - row.lo : base + r0 + k;
+      const TI* x = src + t * p.lr_tok_stride + 8 * lane;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (live[c]) raw[k][c].load(x + 256 * c);
+      if (kNorm && lane < half) {
+        const TI* rr = static_cast<const TI*>(p.rope_raw) + b * p.rr_row_stride + t * p.rr_tok_stride;
+        ra[k] = to_f(rr[2 * lane]);
+        rb[k] = to_f(rr[2 * lane + 1]);
+      }
+    }
+    Raw8<TI> g[2];
+    if constexpr (kNorm) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (live[c]) g[c].load(gain + 256 * c + 8 * lane);
+    }
+    if (!warp_blocks) {
+      for (int k = threadIdx.x; k < n_blocks; k += kHeldWarps * 32) amax_s[k] = 0;
+      __syncthreads();
+    }
+    // The values of group c of token k: normalised and weighted.
+    float inv[kHeldRows], amax[kHeldRows];
+    auto values = [&](int k, int c, float(&v)[8]) {
+      raw[k][c].get(v);
+      if constexpr (kNorm) {
+        float w[8];
+        g[c].get(w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = v[j] * inv[k] * w[j];
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < kHeldRows; ++k) {
+      amax[k] = 0.f;
+      if (!mine(k)) continue;
+      if constexpr (kNorm) {
+        float sq = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (live[c]) {
+            float v[8];
+            raw[k][c].get(v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sq = fmaf(v[j], v[j], sq);
+          }
+        inv[k] = rsqrtf(warp_sum(sq) / (float)p.rank + p.eps);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (live[c]) {
+          float v[8];
+          values(k, c, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) amax[k] = fmaxf(amax[k], fabsf(v[j]));
+        }
+      amax[k] = warp_max(amax[k]);
+      if (!warp_blocks && lane == 0) atomicMax(&amax_s[(r0 + k) >> p.block_shift], __float_as_uint(amax[k]));
+    }
+    if (warp_blocks) {
+      // lane k: block k of the warp's rows
+      if (lane < kHeldRows >> p.block_shift) {
+        const int k_lo = lane << p.block_shift;
+        float m = 0.f;
+#pragma unroll
+        for (int k = 0; k < kHeldRows; ++k)
+          if (k >= k_lo && k < k_lo + block) m = fmaxf(m, amax[k]);
+        const int bk = (r0 + k_lo) >> p.block_shift;
+        if (r0 + k_lo + block > r_lo && r0 + k_lo < r_hi) {
+          int old;
+          exp_s[bk] = block_exponent<kNorm>(p, row, scales, base, bk, m, old);
+          if (bk == (r_lo >> p.block_shift)) old_s = old;
+        }
+      }
+      __syncwarp();
+    } else {
+      __syncthreads();
+      for (int k = threadIdx.x; k < n_blocks; k += kHeldWarps * 32) {
+        const int k_lo = k << p.block_shift;
+        if (k_lo + block <= r_lo || k_lo >= r_hi) continue;
+        int old;
+        exp_s[k] = block_exponent<kNorm>(p, row, scales, base, k, __uint_as_float(amax_s[k]), old);
+        if (k == (r_lo >> p.block_shift)) old_s = old;
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < kHeldRows; ++k) {
+      if (!mine(k)) continue;
+      const float to_units = inverse_unit_of(exp_s[(r0 + k) >> p.block_shift]);
+      uint8_t* dst = codes + (base + r0 + k) * p.codes_row_stride + 8 * lane;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (live[c]) {
+          float v[8];
+          values(k, c, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] *= to_units;   // a power of two: exact
+          *reinterpret_cast<uint2*>(dst + 256 * c) = encode8(v);
+        }
+    }
+    if constexpr (kNorm) {
+#pragma unroll
+      for (int k = 0; k < kHeldRows; ++k) {
+        if (!mine(k)) continue;
+        const int64_t t = base + r0 + k - row.lo;
+        if (lane < half) {
+          TR* dr = static_cast<TR*>(p.rope) + b * p.rope_batch_stride + (base + r0 + k) * p.rope_row_stride;
+          float re, im;
+          rope_rotate_pair(ra[k], rb[k], row.pos0 + t, p.inv_freq[lane], re, im);
+          put(dr + lane, re);
+          put(dr + half + lane, im);
+        }
+        append_rope<TI, TR>(p, b, t, base + r0 + k, row.pos0 + t, lane + 32);   // wider rope keys
+      }
+      // tokens that the first block held before: their codes move to the larger unit
+      __syncthreads();
+      const int k0 = r_lo >> p.block_shift, old = old_s, e = exp_s[k0];
+      if (old >= 0 && clamp_exponent(old) != e)
+        move_codes<kHeldWarps * 32>(p, codes, max(base + ((int64_t)k0 << p.block_shift), (int64_t)row.start), row.lo, old, e);
+    }
+    __syncthreads();   // the tile's shared state is read before the next one overwrites it
+  }
+  if constexpr (kNorm) {
+    // one CTA per row: every thread has read the length before it may be overwritten
+    if (p.lengths_here && blockIdx.x == 0) {
+      __syncthreads();
+      if (threadIdx.x == 0) p.kv_len_out[b] = row.ok ? row.len + p.s_new : row.len;
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // kNorm: new tokens of an append (normalised, weighted, with their rope key);
 // otherwise the tokens of each row's window of a latent buffer.
 template <bool kNorm, bool kVec, typename TI, typename TR>
-__global__ void __launch_bounds__(kWarps * 32) encode_kernel(const __grid_constant__ EncodeParams p) {
+__global__ void __launch_bounds__(kWarps * 32) encode_walk_kernel(const __grid_constant__ EncodeParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ uint32_t amax_s[kMaxScaleBlock];   // per block of the tile, f32 bits (non-negative: ordered as integers)
   __shared__ int exp_s[kMaxScaleBlock], old_exp_s[kMaxScaleBlock];
   __shared__ float inv_s[kMaxScaleBlock];       // per row of the tile
   const int b = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int len = p.kv_len[b];
-  const int start = p.kv_start ? p.kv_start[b] : 0;
-  const int64_t pos0 = !kNorm ? 0 : (p.row_offsets ? (int64_t)p.row_offsets[b] : (int64_t)len);
+  const EncodeRow<kNorm> row_of(p, b, blockIdx.x == 0 && threadIdx.x == 0);
+  const int64_t lo = row_of.lo, hi = row_of.hi;
   const int block = 1 << p.block_shift;
-  const bool aligned = (start & (block - 1)) == 0;
-  const bool fits = len >= 0 && start >= 0 && pos0 >= 0 &&
-                    (int64_t)start + len + (kNorm ? p.s_new : 0) <= p.t_max;
-  const bool ok = fits && aligned;
-  if (!ok && blockIdx.x == 0 && threadIdx.x == 0 && p.status)
-    atomicOr(p.status, fits ? MLA_DEVICE_BAD_BLOCK_START : MLA_DEVICE_INDEX_OUT_OF_RANGE);
-  // the rows written: [lo, hi)
-  const int64_t lo = kNorm ? (int64_t)start + len : start;
-  const int64_t hi = kNorm ? lo + p.s_new : (int64_t)start + len;
   const int tile_rows = p.tile_rows;
   const int64_t tile0 = lo / tile_rows;
-  const int64_t n_tiles = ok && hi > lo ? (hi - 1) / tile_rows - tile0 + 1 : 0;
+  const int64_t n_tiles = row_of.tiles(tile_rows);
   uint8_t* codes = p.codes + b * p.codes_batch_stride;
   uint8_t* scales = p.scales + b * p.scales_batch_stride;
   const TI* src = static_cast<const TI*>(p.latent_raw) + b * p.lr_row_stride;
@@ -150,17 +402,7 @@ __global__ void __launch_bounds__(kWarps * 32) encode_kernel(const __grid_consta
     for (int k = threadIdx.x; k < n_blocks; k += kWarps * 32) {
       const int k_lo = k << p.block_shift, k_hi = k_lo + block;
       if (k_hi <= r_lo || k_lo >= r_hi) continue;
-      const float amax = __uint_as_float(amax_s[k]);
-      int e = exponent_for(amax), old = -1;
-      uint8_t* at = scales + (base >> p.block_shift) + k;
-      if (kNorm && base + k_lo < lo && start < lo) {   // rows [max(block start, start), lo) hold tokens
-        old = *at;
-        e = max(e, clamp_exponent(old));
-      }
-      if (!(amax <= 448.f * 128.f) && p.status) atomicOr(p.status, MLA_DEVICE_VALUE_RANGE);
-      exp_s[k] = e;
-      old_exp_s[k] = old;
-      *at = (uint8_t)e;
+      exp_s[k] = block_exponent<kNorm>(p, row_of, scales, base, k, __uint_as_float(amax_s[k]), old_exp_s[k]);
     }
     __syncthreads();
     for (int r = r_lo + warp; r < r_hi; r += kWarps) {
@@ -176,46 +418,28 @@ __global__ void __launch_bounds__(kWarps * 32) encode_kernel(const __grid_consta
         for (int j = 0; j < 8; ++j)
           if (j < n) x[j] = (kNorm ? v[j] * inv * g[j] : v[j]) * to_units;   // a power of two: exact
         if constexpr (kVec) {
-          const uint32_t w0 = encode_e4m3x2(x[0], x[1]) | (uint32_t)encode_e4m3x2(x[2], x[3]) << 16;
-          const uint32_t w1 = encode_e4m3x2(x[4], x[5]) | (uint32_t)encode_e4m3x2(x[6], x[7]) << 16;
-          *reinterpret_cast<uint2*>(dst + i) = make_uint2(w0, w1);
+          *reinterpret_cast<uint2*>(dst + i) = encode8(x);
         } else {
           dst[i] = encode_e4m3(x[0]);
         }
       });
       if constexpr (kNorm) {
-        const int64_t t = base + r - lo;
-        const TI* rr = static_cast<const TI*>(p.rope_raw) + b * p.rr_row_stride + t * p.rr_tok_stride;
-        TR* dr = static_cast<TR*>(p.rope) + b * p.rope_batch_stride + (base + r) * p.rope_row_stride;
-        const int half = p.rope_dim >> 1;
-        for (int j = lane; j < half; j += 32) {
-          float re, im;
-          rope_rotate_pair(to_f(rr[2 * j]), to_f(rr[2 * j + 1]), pos0 + t, p.inv_freq[j], re, im);
-          put(dr + j, re);
-          put(dr + half + j, im);
-        }
+        append_rope<TI, TR>(p, b, base + r - lo, base + r, row_of.pos0 + (base + r - lo), lane);
       }
     }
     if constexpr (kNorm) {
       // tokens that the first block held before: their codes move to the larger unit
-      const int k0 = r_lo >> p.block_shift;
-      const int old = old_exp_s[k0], e = exp_s[k0];
-      if (old >= 0 && clamp_exponent(old) != e) {
-        const float unit = unit_of(clamp_exponent(old)), to_units = inverse_unit_of(e);
-        const int64_t first = max(base + ((int64_t)k0 << p.block_shift), (int64_t)start);
-        for (int64_t r = first + warp; r < lo; r += kWarps) {
-          uint8_t* dst = codes + r * p.codes_row_stride;
-          for (int i = lane; i < p.rank; i += 32) dst[i] = encode_e4m3(decode_e4m3(dst[i], unit) * to_units);
-        }
-      }
+      const int k0 = r_lo >> p.block_shift, old = old_exp_s[k0], e = exp_s[k0];
+      if (old >= 0 && clamp_exponent(old) != e)
+        move_codes<kWarps * 32>(p, codes, max(base + ((int64_t)k0 << p.block_shift), (int64_t)row_of.start), lo, old, e);
     }
     __syncthreads();   // the tile's shared state is read before the next one overwrites it
   }
   if constexpr (kNorm) {
     // one CTA per row: every thread has read the length before it may be overwritten
-    if (p.lengths_here) {
+    if (p.lengths_here && blockIdx.x == 0) {
       __syncthreads();
-      if (threadIdx.x == 0) p.kv_len_out[b] = ok ? len + p.s_new : len;
+      if (threadIdx.x == 0) p.kv_len_out[b] = row_of.ok ? row_of.len + p.s_new : row_of.len;
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -282,25 +506,33 @@ __global__ void __launch_bounds__(kWarps * 32) decode_rows_kernel(const __grid_c
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+bool held_shape(const EncodeParams& p, bool vec) { return vec && p.rank <= kHeldRank; }
+int tile_rows_of(const EncodeParams& p, bool vec) {
+  if (held_shape(p, vec)) return kHeldTile;
+  return (1 << p.block_shift) > kMinTileRows ? (1 << p.block_shift) : kMinTileRows;
+}
+
 template <bool kNorm, typename TI, typename TR>
 cudaError_t launch_encode_t(const EncodeParams& p, bool vec, dim3 grid, cudaStream_t stream) {
-  const dim3 block(kWarps * 32);
-  return vec ? launch_pdl(encode_kernel<kNorm, true, TI, TR>, grid, block, 0, stream, p)
-             : launch_pdl(encode_kernel<kNorm, false, TI, TR>, grid, block, 0, stream, p);
+  const dim3 held(kHeldWarps * 32), walk(kWarps * 32);
+  if (held_shape(p, vec)) return launch_pdl(encode_kernel<kNorm, TI, TR>, grid, held, 0, stream, p);
+  return vec ? launch_pdl(encode_walk_kernel<kNorm, true, TI, TR>, grid, walk, 0, stream, p)
+             : launch_pdl(encode_walk_kernel<kNorm, false, TI, TR>, grid, walk, 0, stream, p);
 }
 
 }  // namespace
 
 cudaError_t launch_append_q8(const EncodeParams& p_in, int in_dtype, int rope_dtype, bool vec, cudaStream_t stream) {
   EncodeParams p = p_in;
-  p.tile_rows = (1 << p.block_shift) > kMinTileRows ? (1 << p.block_shift) : kMinTileRows;
-  // Tiles that s_new rows can touch.  Up to two are walked by one CTA per row,
-  // which then writes the row's new length itself (a decode step's append is
-  // one launch); more are spread over CTAs and the lengths take a launch of
-  // their own.
+  p.tile_rows = tile_rows_of(p, vec);
+  // Tiles that s_new rows can touch.  Up to two are walked by one CTA per row (a
+  // decode step's append); more are spread over CTAs.  The new lengths are
+  // written by the row's first CTA unless they may overwrite the lengths that
+  // other CTAs of the row still have to read: then by a launch of their own.
   const int64_t tiles = ((int64_t)p.s_new + p.tile_rows - 2) / p.tile_rows + 1;
   const unsigned gx = tiles <= 2 ? 1u : (unsigned)(tiles < 65535 ? tiles : 65535);
-  p.lengths_here = gx == 1 && p.kv_len_out != nullptr;
+  const bool apart = p.kv_len_out + p.batch <= p.kv_len || p.kv_len + p.batch <= p.kv_len_out;
+  p.lengths_here = p.kv_len_out != nullptr && (gx == 1 || apart);
   const dim3 grid(gx, (unsigned)p.batch);
   cudaError_t e;
   if (in_dtype == MLA_DTYPE_F32)
@@ -317,7 +549,7 @@ cudaError_t launch_append_q8(const EncodeParams& p_in, int in_dtype, int rope_dt
 
 cudaError_t launch_quantize(const EncodeParams& p_in, int dtype, bool vec, cudaStream_t stream) {
   EncodeParams p = p_in;
-  p.tile_rows = (1 << p.block_shift) > kMinTileRows ? (1 << p.block_shift) : kMinTileRows;
+  p.tile_rows = tile_rows_of(p, vec);
   const int64_t tiles = (p.t_max + p.tile_rows - 1) / p.tile_rows;
   const dim3 grid((unsigned)(tiles < 65535 ? tiles : 65535), (unsigned)p.batch);
   const cudaError_t e = dtype == MLA_DTYPE_F32

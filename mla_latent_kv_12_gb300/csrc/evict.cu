@@ -37,9 +37,9 @@ __device__ __forceinline__ uint32_t cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ int load_peer(const int* local, uint32_t rank) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(tc::mapa(tc::smem_u32(local), rank)) : "memory");
+__device__ __forceinline__ int2 load_peer2(const int* local, uint32_t rank) {   // 8-byte aligned
+  int2 v;
+  asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(tc::mapa(tc::smem_u32(local), rank)) : "memory");
   return v;
 }
 
@@ -75,10 +75,9 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_s, int& total) {
 
 __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __grid_constant__ EvictParams p, int held) {
   extern __shared__ uint32_t keys_s[];   // `held` keys of this CTA's slice
-  __shared__ int hist[kBins];
+  __shared__ __align__(8) int hist_s[3][kBins];   // one per pass: a peer may still read the previous one
   __shared__ int warp_s[kPlanWarps];
-  __shared__ int tot_s[2];               // this CTA's kept and tied tokens
-  __shared__ int digit_s, rest_s;
+  __shared__ int digit_s, rest_s, less_s, tie_s;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t crank = tc::cluster_ctarank();
   const int ncta = (int)cluster_size();
@@ -107,12 +106,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
 
   uint32_t prefix = 0;
   int rest = take;   // the rest-th smallest key among those with the prefix is looked for
+  int peers_less = 0, peers_tie = 0;   // keys below `prefix`, and equal to it, in the earlier CTAs' slices
   if (take > 0) {
+    for (int i = threadIdx.x; i < 3 * kBins; i += kPlanThreads) hist_s[0][i] = 0;
+    __syncthreads();
     int known = 0;   // leading key bits fixed so far
     for (int pass = 0; pass < 3; ++pass) {
       const int width = pass < 2 ? 11 : 10, shift = 32 - known - width;
-      for (int i = threadIdx.x; i < kBins; i += kPlanThreads) hist[i] = 0;
-      __syncthreads();
+      int* hist = hist_s[pass];
       constexpr int kLoads = 8;   // independent loads in flight per thread
       for (int base = lo; base < hi; base += kPlanThreads * kLoads) {
         uint32_t key[kLoads];
@@ -150,27 +151,42 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
       tc::cluster_sync();   // every CTA's histogram is complete
       // thread t sums bins 2t and 2t + 1 over the cluster; the one whose bins hold the rest-th key takes it
       const int nb = 1 << width, b0 = 2 * threadIdx.x;
-      int h[2] = {0, 0};
-      if (b0 < nb)
-        for (int c = 0; c < ncta; ++c)
+      int h[2] = {0, 0}, e[2] = {0, 0};   // the cluster's, and the earlier CTAs'
+      if (b0 < nb) {
+        int2 part[kMaxCluster];   // all loads in flight together
 #pragma unroll
-          for (int k = 0; k < 2; ++k) h[k] += load_peer(&hist[b0 + k], (uint32_t)c);
+        for (int c = 0; c < kMaxCluster; ++c)
+          part[c] = c < ncta ? load_peer2(&hist[b0], (uint32_t)c) : make_int2(0, 0);
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+          h[0] += part[c].x, h[1] += part[c].y;
+          if (c < (int)crank) e[0] += part[c].x, e[1] += part[c].y;
+        }
+      }
       int all;
-      int before = block_prefix(h[0] + h[1], warp_s, all);
+      int before = block_prefix(h[0] + h[1], warp_s, all), less = block_prefix(e[0] + e[1], warp_s, all);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         if (before < rest && rest <= before + h[k]) {   // exactly one thread and bin
           digit_s = b0 + k;
           rest_s = rest - before;
+          less_s = less;
+          tie_s = e[k];
         }
         before += h[k];
+        less += e[k];
       }
-      tc::cluster_sync();   // the histograms are read (they are cleared next pass); digit_s is written
+      __syncthreads();
       prefix = (prefix << width) | (uint32_t)digit_s;
       rest = rest_s;
+      peers_less += less_s;
+      peers_tie = tie_s;
       known += width;
+      __syncthreads();   // (read before the next pass writes them)
     }
   }
+  // The last reads of other CTAs' shared memory are done: no CTA leaves before all have arrived here.
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   // ---- kept: keys below `prefix`, and the first `rest` positions that equal it.
   // Warp w owns a contiguous part of the slice, so that ranks follow positions.
   const int wspan = ((hi - lo + kPlanWarps - 1) / kPlanWarps + 31) & ~31;
@@ -187,12 +203,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
   int cta_less, cta_tie;
   int before_less = block_prefix(lane == 0 ? n_less : 0, warp_s, cta_less);
   int before_tie = block_prefix(lane == 0 ? n_tie : 0, warp_s, cta_tie);
-  if (threadIdx.x == 0) tot_s[0] = cta_less, tot_s[1] = cta_tie;
-  tc::cluster_sync();   // every CTA's totals are complete; every CTA has read kv_len
-  for (int c = 0; c < (int)crank; ++c) {
-    before_less += load_peer(&tot_s[0], (uint32_t)c);
-    before_tie += load_peer(&tot_s[1], (uint32_t)c);
-  }
+  before_less += peers_less;
+  before_tie += peers_tie;
   before_less = __shfl_sync(0xffffffffu, before_less, 0);
   before_tie = __shfl_sync(0xffffffffu, before_tie, 0);
   if (take > 0) {
@@ -213,19 +225,25 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
   const int me = (int)crank * kPlanThreads + threadIdx.x;
   for (int j = me; j < p.n_sink; j += ncta * kPlanThreads) kept[j] = j;
   for (int j = me; j < p.n_recent; j += ncta * kPlanThreads) kept[p.n_keep - p.n_recent + j] = last + j;
-  if (crank == 0 && threadIdx.x == 0) {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (crank == 0 && threadIdx.x == 0) {   // every CTA has read kv_len, which kv_len_out may alias
     p.counts[b] = p.n_keep;
     if (p.kv_len_out) p.kv_len_out[b] = p.n_keep;
   }
-  tc::cluster_sync();   // no CTA leaves while another may still read its shared memory
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ compaction
 
 constexpr int kMoveThreads = 512;
-constexpr int kMoves = 2;          // units per thread and chunk
-constexpr int kDepth = 4;          // chunks in flight
+// Units per thread and chunk, chunks in flight, threads and slice width: of the
+// sweep (moves, depth, bytes, threads) on a bf16 batch of 8 rows halved from
+// 32768 tokens (plan and compaction): (2, 4, 64, 512) 112 us, (1, 8, 64, 512)
+// 136, (4, 2, 64, 512) 95, (8, 1, 64, 512) 99, (4, 2, 128, 512) 134, (4, 2, 32,
+// 512) 99, (4, 2, 64, 1024) 106: fewer barriers against more in flight.
+constexpr int kMoves = 4;
+constexpr int kDepth = 2;
 constexpr int kSliceBytes = 64;    // of a token's bytes moved by one CTA
 
 struct Slice {

@@ -10,6 +10,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <stdint.h>
 
@@ -46,6 +47,38 @@ __device__ __forceinline__ float decode_e4m3(uint32_t code, float unit) {
   const float mag = __uint_as_float((code & 0x7Fu) << 20) * 0x1p120f;
   const float v = (code & 0x80u) ? -mag : mag;
   return (code & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : v * unit;
+}
+
+// Eight codes to eight fp16 values (four packed pairs): the hardware's exact
+// conversion (NaN codes become NaN) and one packed multiplication by the unit
+// `mul2` = 2^(e - 127) in both halves.  Exact for e >= kMinExponentF16: a code's
+// least bit is at least 2^-9.  Below, values round to multiples of 2^-24.
+constexpr int kMinExponentF16 = 127 - 15;
+__device__ __forceinline__ uint32_t f16_unit(int e) {
+  const __half h = __float2half_rn(__uint_as_float((uint32_t)e << 23));   // subnormal below 2^-14, 0 below 2^-25
+  return (uint32_t)__half_as_ushort(h) * 0x00010001u;
+}
+__device__ __forceinline__ void decode_e4m3x8_f16(const uint2 codes, uint32_t mul2, uint32_t (&out)[4]) {
+  const uint32_t w[2] = {codes.x, codes.y};
+  const __half2 unit = *reinterpret_cast<const __half2*>(&mul2);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint32_t lo, hi;
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+        : "=r"(lo), "=r"(hi) : "r"(w[j]));
+    const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&lo), unit), y = __hmul2(*reinterpret_cast<const __half2*>(&hi), unit);
+    out[2 * j] = *reinterpret_cast<const uint32_t*>(&x);
+    out[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+
+// Two bf16 values as fp16, saturating (exact from 2^-14 to 65504 in magnitude).
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v) {
+  const float lo = __uint_as_float(v << 16), hi = __uint_as_float(v & 0xFFFF0000u);
+  // (written so that NaN stays NaN)
+  const __half2 h = __floats2half2_rn(lo > 65504.f ? 65504.f : lo < -65504.f ? -65504.f : lo,
+                                      hi > 65504.f ? 65504.f : hi < -65504.f ? -65504.f : hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Sixteen codes to sixteen bf16 values (eight packed pairs), exact.  A code's

@@ -1,5 +1,5 @@
-// Tiles of an 8-bit cache as the bf16 operand tiles of tcgen05 MMAs: fetch of
-// the codes, exponents and rope keys of 64 keys, and their bf16 values in the
+// Tiles of an 8-bit cache as the fp16 operand tiles of tcgen05 MMAs: fetch of
+// the codes, exponents and rope keys of 64 keys, and their fp16 values in the
 // swizzled shared-memory layout that a TMA load of a bf16 cache would leave.
 //
 // The fetch runs two tiles ahead: every warp copies its own 16-byte pieces
@@ -72,25 +72,33 @@ struct Q8Fetch {
   __device__ __forceinline__ int my_exponent(const Q8Rows& r, int pos) const {
     return pos >= 0 ? __ldg(r.scales + (((int64_t)r.start + pos) >> r.shift)) : kMinExponent;
   }
-  // Copies of one tile into slot s; `pos` from my_position.
-  __device__ __forceinline__ void issue(const Q8Rows& r, int tile, int s, int pos) const {
+  // Flags a unit in which fp16 loses bits (the smallest one is that of zeros).
+  __device__ __forceinline__ void check_exponent(int32_t* status, int e) const {
+    if (e < kMinExponentF16 && e > kMinExponent && status) atomicOr(status, MLA_DEVICE_VALUE_RANGE);
+  }
+  // Copies of a window tile's codes into slot s: rows at one distance, zeros past the entries.
+  __device__ __forceinline__ void issue_window(const Q8Rows& r, int tile, int s) const {
+    const int e0 = tile * kTileKeys + key0;
+    const uint8_t* c = r.codes + ((int64_t)r.start + e0) * r.codes_stride;
     const uint32_t dst = slot0 + s * kSlotBytes;
-    if (!r.list && (tile + 1) * kTileKeys <= r.entries) {   // a whole tile of a window: rows at one distance
-      const int64_t row = (int64_t)r.start + tile * kTileKeys + key0;
-      const uint8_t* c = r.codes + row * r.codes_stride;
-      const __nv_bfloat16* k = r.rope + (row + rope_group * kStep) * r.rope_stride;
 #pragma unroll
-      for (int i = 0; i < kIters; ++i, c += kStep * r.codes_stride) tc::cp_async_16(dst + i * kPieceBytes, c, 16u);
-#pragma unroll
-      for (int j = 0; j < kRopeIters; ++j, k += 4 * kStep * r.rope_stride)
-        tc::cp_async_16(dst + (kIters + j) * kPieceBytes, k, 16u);
-      return;
+    for (int i = 0; i < kIters; ++i, c += kStep * r.codes_stride) {
+      const bool in = e0 + i * kStep < r.entries;
+      tc::cp_async_16(dst + i * kPieceBytes, in ? c : r.codes, in ? 16u : 0u);
     }
+  }
+  // Copies of one tile's codes into slot s; `pos` from my_position.
+  __device__ __forceinline__ void issue_codes(const Q8Rows& r, int s, int pos) const {
+    const uint32_t dst = slot0 + s * kSlotBytes;
 #pragma unroll
     for (int i = 0; i < kIters; ++i) {
       const int p = __shfl_sync(0xffffffffu, pos, peers + i);
       tc::cp_async_16(dst + i * kPieceBytes, r.codes + (int64_t)(r.start + max(p, 0)) * r.codes_stride, p >= 0 ? 16u : 0u);
     }
+  }
+  // And of its rope keys.
+  __device__ __forceinline__ void issue_rope(const Q8Rows& r, int s, int pos) const {
+    const uint32_t dst = slot0 + s * kSlotBytes;
 #pragma unroll
     for (int j = 0; j < kRopeIters; ++j) {
       const int p = __shfl_sync(0xffffffffu, pos, peers + 4 * j + rope_group);
@@ -98,36 +106,30 @@ struct Q8Fetch {
                       p >= 0 ? 16u : 0u);
     }
   }
-  // Slot s as bf16 values, its first eight dims at shared address `box`, the
-  // others kBox bytes behind, rows 128 bytes apart; `rope` receives the first
-  // rope piece (rows of rope keys kRopeRow bytes apart).  `exponent` from
+  // The rope pieces that issue() copied, into the stage: `rope` is the place of the first one, rows kRow bytes apart.
+  template <int kRow>
+  __device__ __forceinline__ void copy_rope(int s, uint32_t rope) const {
+#pragma unroll
+    for (int j = 0; j < kRopeIters; ++j)
+      st_shared_16(rope + 4 * j * kStep * kRow, ld_shared_16(slot0 + s * kSlotBytes + (kIters + j) * kPieceBytes));
+  }
+  // Slot s as fp16 values: this lane's first eight dims at shared address `box`,
+  // the others kBox bytes behind, rows 128 bytes apart.  `exponent` from
   // my_exponent.
-  template <int kBox, int kRopeRow>
-  __device__ __forceinline__ void convert(int s, int exponent, uint32_t box, uint32_t rope) const {
-    const uint32_t src = slot0 + s * kSlotBytes, src0 = codes0 + s * kSlotBytes, src1 = src0 + 8 * kLanes;
-    const uint32_t unit = bf16_unit(clamp_exponent(exponent));
+  template <int kBox>
+  __device__ __forceinline__ void convert(int s, int exponent, uint32_t box) const {
+    const uint32_t src0 = codes0 + s * kSlotBytes, src1 = src0 + 8 * kLanes;
+    const uint32_t unit = f16_unit(clamp_exponent(exponent));
     __syncwarp();   // the warp's copies have landed (each lane has waited for its own)
-    uint32_t nan = 0;
 #pragma unroll
     for (int i = 0; i < kIters; ++i) {
       const uint32_t mul2 = __shfl_sync(0xffffffffu, unit, peers + i);
       const uint2 c0 = ld_shared_8(src0 + i * kPieceBytes), c1 = ld_shared_8(src1 + i * kPieceBytes);
-      uint32_t v[8];
-      nan |= decode_e4m3x16(make_uint4(c0.x, c0.y, c1.x, c1.y), mul2, v);
+      uint32_t v[4];
+      decode_e4m3x8_f16(c0, mul2, v);
       st_shared_16(box + i * kStep * 128, make_uint4(v[0], v[1], v[2], v[3]));
-      st_shared_16(box + kBox + i * kStep * 128, make_uint4(v[4], v[5], v[6], v[7]));
-    }
-#pragma unroll
-    for (int j = 0; j < kRopeIters; ++j)
-      st_shared_16(rope + 4 * j * kStep * kRopeRow, ld_shared_16(src + (kIters + j) * kPieceBytes));
-    if (nan) {   // rare: look for the NaN codes again, one by one
-#pragma unroll 1
-      for (int k = 0; k < 16 * kIters; ++k) {
-        const int i = k >> 4, j = k & 7;
-        uint32_t code;
-        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(code) : "r"(((k & 8) ? src1 : src0) + i * kPieceBytes + j) : "memory");
-        if ((code & 0x7Fu) == 0x7Fu) tc::st_shared_u16(box + ((k & 8) ? kBox : 0) + i * kStep * 128 + 2 * j, 0x7FC0u);
-      }
+      decode_e4m3x8_f16(c1, mul2, v);
+      st_shared_16(box + kBox + i * kStep * 128, make_uint4(v[0], v[1], v[2], v[3]));
     }
   }
 

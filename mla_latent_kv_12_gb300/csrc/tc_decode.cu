@@ -69,16 +69,20 @@ constexpr int HEADS = 128, RANK = 512, DV = 256;  // DV: latent dims per CTA
 // more threads the dense kernel gets fewer registers and ran 3 % slower)
 constexpr int THREADS = 352, THREADS_GATHER = THREADS + 96;
 constexpr int kGatherWarp = 11;   // first extra gather warp
-// The instances for an 8-bit cache: eight warps fetch the codes of each tile
-// and write their bf16 values into the stage ring (three stages: the fourth's
-// memory holds the fetch's two slots).  Roles are whole warpgroups, whose
-// registers are redistributed at their start: the softmax and exchange
-// warps take what the MMA and converting warps do not need.  The shares (per
-// thread and warpgroup) add up to the launch's 5 x 96.
+// The instance for an 8-bit cache: eight warps fetch the codes of each tile
+// and write their fp16 values into the stage ring (q8_tiles.cuh): three
+// stages, the fourth's memory holds the fetch's two slots.  (Four stages, one
+// slot of codes refilled by halves and rope keys by TMA: the ragged decode of
+// 32 rows 175 us against 165, verify 601 against 554.  The SM's issue slots are
+// what the roles share, and converting further ahead slows the softmax.)
+// Roles are whole warpgroups, whose registers are redistributed at their
+// start: the softmax and exchange warps take what the MMA and converting warps
+// do not need.  The shares (per thread and warpgroup) add up to the launch's
+// 5 x 96.
 constexpr int THREADS_Q8 = 640;
 constexpr int kConvertWarps = 8;
 constexpr int STAGES_Q8 = 3;
-constexpr int kRegsSoftmax = 144, kRegsExchange = 136, kRegsIssue = 40, kRegsConvert = 80;
+constexpr int kRegsSoftmax = 144, kRegsExchange = 128, kRegsIssue = 48, kRegsConvert = 80;
 static_assert(kRegsSoftmax + kRegsExchange + kRegsIssue + 2 * kRegsConvert <= 5 * 96, "more registers than the launch has");
 using DecodeFetch = Q8Fetch<16, 32 * kConvertWarps>;
 // Dynamic shared memory: the stage ring, then send[2] and receive[2].  The
@@ -450,9 +454,13 @@ __global__ void __launch_bounds__(1024) tc_plan_kernel(const __grid_constant__ T
 // MMAs instead of delaying them; single rows lose by the added P.V latency).
 // Without deadlock: the next tile's scores wait on the P.V STAGES tiles back
 // (its stage) and on the exchange of this tile's, in both CTAs, never on this P.V.
-// kQ8: the latent is held in 8 bits: four warps fetch and decode it
-// (q8_tiles.cuh: exact in bf16, units applied) and write it where the TMA boxes
-// would have put it; the rest of the kernel is the same.
+// kQ8: the latent is held in 8 bits: eight warps decode it into fp16
+// (q8_tiles.cuh) and write it where the TMA boxes of a bf16 cache would have put
+// it; the latent part of the query and P are fp16 too (an MMA's operands have
+// one type; the rope MMAs stay bf16), the rest of the kernel is the same.  fp16
+// takes 21 instructions for 16 codes where bf16, which the hardware does not
+// convert to, takes 51: the converting warps share the issue slots with the
+// softmax (ragged decode 174 -> 165 us, verify 628 -> 554 us).
 template <int kPrefetchAhead, int kThreads, bool kLateP, bool kQ8 = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_decode_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_constant__ CUtensorMap rope_map,
@@ -560,7 +568,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ============================================================ score MMA issuer
     // S(t) as soon as tile t has landed and the exchange warps have read S(t-1);
     // the P.V issuer (warp 10) runs independently, so scores run ahead.
-    const uint32_t idesc_s = idesc_bf16_f32(128, BN, 0, 0);
+    const uint32_t idesc_rope = idesc_bf16_f32(128, BN, 0, 0);
+    const uint32_t idesc_s = kQ8 ? idesc_f16_f32(128, BN, 0, 0) : idesc_rope;
     int stage = 0;
     uint32_t phase = 0;
     uint32_t tile = 0;      // global tile counter (S phases)
@@ -608,7 +617,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            mma_ts(tmem + TM_S, tmem + TM_Q + 128 + k * 8, d_rope + (uint64_t)((k * 32) >> 4), idesc_s, 1u);
+            mma_ts(tmem + TM_S, tmem + TM_Q + 128 + k * 8, d_rope + (uint64_t)((k * 32) >> 4), idesc_rope, 1u);
           mma_commit(&s_full);
         }
         __syncwarp();
@@ -625,7 +634,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   };
   auto issue_pv = [&]() {
     // ============================================================ P.V MMA issuer
-    const uint32_t idesc_pv = idesc_bf16_f32(128, DV, 0, 1);
+    const uint32_t idesc_pv = kQ8 ? idesc_f16_f32(128, DV, 0, 1) : idesc_bf16_f32(128, DV, 0, 1);
     int stage = 0;
     uint32_t tile = 0, seg = 0;
     int u, n, t0, t1;
@@ -705,37 +714,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       rows.entries = keys_p[n];
       rows.list = (gather && a.sel_count[n] != -1) ? a.sel + (int64_t)n * a.k_max : nullptr;
       rows.status = rank == 0 && c < DecodeFetch::kIters ? a.status : nullptr;   // one lane per entry flags it
-      // The pipeline: tile t is converted while the copies of t + 1 and (from
-      // its end on) t + 2 are in flight; exponents come with the copies, list
-      // positions a tile before them.
+      // Tile t is converted while the copies of t + 1 and (from its end on)
+      // t + 2 are in flight; exponents come with the copies, list positions a
+      // tile before them.  (Copies and loads are issued behind the fence, which
+      // waits for loads in flight.)
+      auto issue = [&](int t, int slot, int p) {
+        if (rows.list) fetch.issue_codes(rows, slot, p); else fetch.issue_window(rows, t, slot);
+        fetch.issue_rope(rows, slot, p);
+      };
       int pos = fetch.my_position(rows, t0);
       int e_now = fetch.my_exponent(rows, pos);
-      fetch.issue(rows, t0, 0, pos);
+      issue(t0, 0, pos);
       cp_async_commit();
       pos = fetch.my_position(rows, t0 + 1);
       int e_next = fetch.my_exponent(rows, pos);
-      if (t0 + 1 < t1) fetch.issue(rows, t0 + 1, 1, pos);
+      if (t0 + 1 < t1) issue(t0 + 1, 1, pos);
       cp_async_commit();
       pos = fetch.my_position(rows, t0 + 2);
       for (int t = t0; t < t1; ++t) {
         const int slot = (t - t0) & 1;
         if (fills++ >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
+        fetch.check_exponent(rows.status, e_now);
         cp_async_wait<1>();   // this tile's pieces
         const uint32_t off = stage * STAGE_BYTES;
-        fetch.convert<2 * CHUNK_BYTES, 64>(slot, e_now, box0 + off, rope0 + off);
+        fetch.template convert<2 * CHUNK_BYTES>(slot, e_now, box0 + off);
+        fetch.template copy_rope<64>(slot, rope0 + off);
         fence_proxy_async_smem();   // generic-proxy writes, read by the MMAs
         __syncwarp();
         if (lane == 0) mbar_arrive(&full_bar[stage]);
         e_now = e_next;
         if (t + 2 < t1) {
           e_next = fetch.my_exponent(rows, pos);
-          fetch.issue(rows, t + 2, slot, pos);
+          issue(t + 2, slot, pos);
           pos = fetch.my_position(rows, t + 3);
         }
         cp_async_commit();
         if (++stage == kStages) stage = 0, phase ^= 1u;
       }
       cp_async_wait<0>();   // the slots are free for the next segment
+      __syncwarp();
     }
   } else if (!kQ8 && warp == 0) {
     // ============================================================ producer
@@ -922,6 +939,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int v = 0; v < 8; ++v)
               r[4 * v] = qv[8 * c + v].x, r[4 * v + 1] = qv[8 * c + v].y, r[4 * v + 2] = qv[8 * c + v].z,
               r[4 * v + 3] = qv[8 * c + v].w;
+            if constexpr (kQ8) {
+#pragma unroll
+              for (int v = 0; v < 32; ++v) r[v] = bf16x2_to_f16x2(r[v]);
+            }
             tmem_st32(tmem + TM_Q + c * 32 + lane_off, r);
           }
           uint32_t r[16];
@@ -979,6 +1000,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // the peer's receive buffer: no staging round trip, no bulk copy.
         uint8_t* xo = xout + b * XH_BYTES;
         const uint32_t xi = xin_peer + b * XH_BYTES;
+        if constexpr (kQ8) {
+          // Scores that fp16 cannot hold are rare: the tile's largest magnitude
+          // decides once whether they are clamped (NaN stays NaN).
+          float top = 0.f;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) top = fmax3(top, fabsf(__uint_as_float(sa[k])), fabsf(__uint_as_float(sb[k])));
+          half_max = fmaxf(half_max, top);
+          if (__any_sync(0xffffffffu, !(top * a.scale_log2 < 65504.f))) {
+            const float limit = 65504.f / a.scale_log2;   // (rounds back to 65504 in fp16)
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              sa[k] = __float_as_uint(clamp_nan(__uint_as_float(sa[k]), limit));
+              sb[k] = __float_as_uint(clamp_nan(__uint_as_float(sb[k]), limit));
+            }
+          }
+        }
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           uint32_t w[4];
@@ -987,11 +1024,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int k = 8 * c + 2 * q;   // scores k, k+1
             const float lo_raw = __uint_as_float(k < 32 ? sa[k] : sb[k - 32]);
             const float hi_raw = __uint_as_float(k < 32 ? sa[k + 1] : sb[k - 31]);
-            half_max = fmax3(half_max, fabsf(lo_raw), fabsf(hi_raw));
+            if constexpr (!kQ8) half_max = fmax3(half_max, fabsf(lo_raw), fabsf(hi_raw));
             // sent already scaled (log2 units): the softmax then only adds
             const float2 sc = mul_f32x2(make_float2(lo_raw, hi_raw), make_float2(a.scale_log2, a.scale_log2));
-            // (an 8-bit cache's NaN codes stay NaN: clamp_nan keeps them)
-            const __half2 hv = kQ8 ? __floats2half2_rn(clamp_nan(sc.x, 65504.f), clamp_nan(sc.y, 65504.f))
+            const __half2 hv = kQ8 ? __floats2half2_rn(sc.x, sc.y)
                                    : __floats2half2_rn(fminf(fmaxf(sc.x, -65504.f), 65504.f), fminf(fmaxf(sc.y, -65504.f), 65504.f));
             w[q] = *reinterpret_cast<const uint32_t*>(&hv);
           }
@@ -1167,8 +1203,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const float p0 = ex2_approx(xs.x);
           const float p1 = ex2_approx(xs.y);
           ps2[(k >> 1) & 7] = add_f32x2(ps2[(k >> 1) & 7], make_float2(p0, p1));
-          const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
-          pk[k >> 1] = *reinterpret_cast<const uint32_t*>(&pb);
+          if constexpr (kQ8) {   // (p is at most 2^kRescaleThreshold)
+            const __half2 ph = __floats2half2_rn(p0, p1);
+            pk[k >> 1] = *reinterpret_cast<const uint32_t*>(&ph);
+          } else {
+            const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
+            pk[k >> 1] = *reinterpret_cast<const uint32_t*>(&pb);
+          }
         }
         ps2[0] = add_f32x2(add_f32x2(ps2[0], ps2[1]), add_f32x2(ps2[2], ps2[3]));
         ps2[4] = add_f32x2(add_f32x2(ps2[4], ps2[5]), add_f32x2(ps2[6], ps2[7]));
@@ -1786,7 +1827,7 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
   // Tensor maps over [B_buf, t_max, dims] (the batch axis has extent 1 for a
   // packed-flat cache whose batch stride is 0).
   const uint64_t bmap = a.batch_in_map ? (uint64_t)g.batch : 1;
-  const bool q8 = g.codes != nullptr;   // read by plain loads: no maps
+  const bool q8 = g.codes != nullptr;   // copied row by row: no maps
   CUtensorMap lat_map = {}, rope_map = {};
   if (!q8) {
     const uint64_t dims[3] = {(uint64_t)g.rank, (uint64_t)g.t_max, bmap};
@@ -1824,8 +1865,9 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
   const bool lockstep = a.width > 1;
   // (the prefetch distance only serves the dense path; gathers take the
   // instance with the extra gather warps)
-  auto* const decode_kernel = q8 && lockstep ? tc_decode_kernel<kPrefetchAheadGroup, THREADS_Q8, true, true>
-                              : q8         ? tc_decode_kernel<kPrefetchAheadRow, THREADS_Q8, false, true>
+  // (an 8-bit cache is served by one instance: announcing P late, as the
+  // lockstep groups do, costs it 11 %)
+  auto* const decode_kernel = q8 ? tc_decode_kernel<kPrefetchAheadRow, THREADS_Q8, false, true>
                               : a.gather_tma ? tc_decode_kernel<kPrefetchAheadRow, THREADS_GATHER, false>
                               : lockstep   ? tc_decode_kernel<kPrefetchAheadGroup, THREADS, true>
                                            : tc_decode_kernel<kPrefetchAheadRow, THREADS, false>;

@@ -245,22 +245,28 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
       rows.start = g.kv_start ? g.kv_start[b] : 0;
       rows.entries = rows.limit = g.kv_len[b];
       rows.list = nullptr;
-      rows.status = nullptr;
+      rows.status = lane < WeightFetch::kIters ? g.device_status : nullptr;
       // Tile t is converted while the copies of t + 1 and (from its end on) t + 2 are in flight.
+      auto issue = [&](int t, int slot, int p) {
+        fetch.issue_window(rows, t, slot);
+        fetch.issue_rope(rows, slot, p);
+      };
       int pos = fetch.my_position(rows, t0);
       int e_now = fetch.my_exponent(rows, pos);
-      fetch.issue(rows, t0, 0, pos);
+      issue(t0, 0, pos);
       cp_async_commit();
       pos = fetch.my_position(rows, t0 + 1);
       int e_next = fetch.my_exponent(rows, pos);
-      if (t0 + 1 < t1) fetch.issue(rows, t0 + 1, 1, pos);
+      if (t0 + 1 < t1) issue(t0 + 1, 1, pos);
       cp_async_commit();
       for (int t = t0; t < t1; ++t) {
         const int slot = (t - t0) & 1;
         if (fills++ >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
         cp_async_wait<1>();   // this tile's pieces
         const uint32_t off = stage * STAGE_BYTES;
-        fetch.convert<4 * BOX_BYTES, 128>(slot, e_now, box0 + off, rope0 + off);
+        fetch.check_exponent(rows.status, e_now);
+        fetch.convert<4 * BOX_BYTES>(slot, e_now, box0 + off);
+        fetch.copy_rope<128>(slot, rope0 + off);
         fence_proxy_async_smem();   // generic-proxy writes, read by the MMAs
         __syncwarp();
         if (lane == 0) mbar_arrive(&full_bar[stage]);
@@ -268,7 +274,7 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
         if (t + 2 < t1) {
           pos = fetch.my_position(rows, t + 2);
           e_next = fetch.my_exponent(rows, pos);
-          fetch.issue(rows, t + 2, slot, pos);
+          issue(t + 2, slot, pos);
         }
         cp_async_commit();
         if (++stage == kStages) stage = 0, phase ^= 1u;
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
     }
   } else if (warp == 1) {
     // ============================================================ MMA issuer
-    const uint32_t idesc = idesc_bf16_f32(128, BN, 0, 0);
+    const uint32_t idesc_rope = idesc_bf16_f32(128, BN, 0, 0), idesc = kQ8 ? idesc_f16_f32(128, BN, 0, 0) : idesc_rope;
     int stage = 0;
     uint32_t phase = 0, tile = 0, queries = 0;
     while (!aborted() && it.next(g, fresh)) {
@@ -294,7 +300,7 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               mma_ts(tmem + TM_S + buf * BN, tmem + TM_Q + c * 32 + k * 8,
-                     d0 + (uint64_t)((c * BOX_BYTES + k * 32) >> 4), idesc, (c | k) != 0);
+                     d0 + (uint64_t)((c * BOX_BYTES + k * 32) >> 4), c < 8 ? idesc : idesc_rope, (c | k) != 0);
           mma_commit(&empty_bar[stage]);
           mma_commit(&s_full[buf]);
         }
@@ -339,6 +345,12 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
             for (int v = 0; v < 8; ++v)
               r[4 * v] = qv[8 * d + v].x, r[4 * v + 1] = qv[8 * d + v].y, r[4 * v + 2] = qv[8 * d + v].z,
               r[4 * v + 3] = qv[8 * d + v].w;
+            if constexpr (kQ8) {
+              if (c + d < 8) {
+#pragma unroll
+                for (int v = 0; v < 32; ++v) r[v] = bf16x2_to_f16x2(r[v]);
+              }
+            }
             tmem_st32(tmem + TM_Q + (c + d) * 32 + lane_off, r);
           }
         }

@@ -341,12 +341,6 @@ def test_attend(mla, heads, s_q, block, T, lengths, starts):
     mla.decode_attend_q8(q, codes, scales, block, rope, start, length, B, s_q, SCALE, ctx, lse, device_status=st)
     assert int(st) & ~mla.DEVICE_SCORE_RANGE == 0
     check_attend(ctx, lse, case, block, s_q)
-    # the same bits as the bf16 decode over the dequantised cache
-    lat = torch.zeros(B, T, 512, dtype=torch.bfloat16, device=DEV)
-    mla.dequantize_cache(codes, scales, block, lat, start, length)
-    ctx2, lse2 = torch.empty_like(ctx), torch.empty_like(lse)
-    mla.decode_attend(q, lat, rope, start, length, B, s_q, SCALE, ctx2, lse2)
-    assert torch.equal(ctx, ctx2) and torch.equal(lse, lse2)
 
 
 @pytest.mark.parametrize("s_q", [1, 2])

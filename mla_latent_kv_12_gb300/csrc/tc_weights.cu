@@ -44,9 +44,12 @@ constexpr int kConvertWarp = 6, kConvertWarps = 8, kConvertThreads = 32 * kConve
 using WeightFetch = Q8Fetch<32, kConvertThreads>;
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES, SMEM_BYTES_Q8 = STAGES_Q8 * STAGE_BYTES + 2 * WeightFetch::kSlotBytes;
 constexpr long long kWaitLimit = 1LL << 32;   // clock cycles (~2 s)
-// Tiles that several query tokens share before the next ones are read: 152
-// CTAs x 8 tiles x 72 KB = 88 MB stays in the 129 MB L2.
-constexpr int kChunkTiles = 8;
+// Tiles that several query tokens share before the next ones are read, so that
+// they stay in the 129 MB L2: 152 CTAs x 8 tiles x 72 KB = 88 MB, 152 x 15 x 40
+// KB = 91 MB of an 8-bit cache.  (A pass begins with a drained pipeline and its
+// query's load.)
+constexpr int kChunkTiles = 8, kChunkTilesQ8 = 15;
+constexpr int kWeightsAhead = 8;   // tiles ahead that weights are pulled into L2
 
 struct WeightArgs {
   DecodeGeometry g;
@@ -97,7 +100,7 @@ struct Passes {
       row_tiles = window_tiles(g, b, false);
     }
     int n = min(left, row_tiles - t);
-    if (g.s_q > 1) n = min(n, kChunkTiles);
+    if (g.s_q > 1) n = min(n, g.codes ? kChunkTilesQ8 : kChunkTiles);
     i = 0;
     t0 = t;
     t1 = t + n;
@@ -318,6 +321,7 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
     const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
     const bool real = h < g.heads;
     const int k_mine = threadIdx.x - 64;      // key of the tile whose weight this thread updates (warps 2, 3)
+    constexpr int kQueryBoxes = kQ8 ? 3 : 5;   // (the registers of a thread: 128 and 254)
     uint32_t tile = 0;
     float lse2 = 0.f;
     // The four warps meet in a barrier at every tile, so they leave together.
@@ -334,12 +338,14 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
                                                         (int64_t)h * g.q_head_stride);
         lse2 = real ? a.lse[n * g.heads + h] * 1.4426950408889634f : 0.f;
 #pragma unroll
-        for (int c = 0; c < BOXES; c += 3) {
-          uint4 qv[24];
+        for (int c = 0; c < BOXES; c += kQueryBoxes) {
+          uint4 qv[8 * kQueryBoxes];   // these loads are in flight together
 #pragma unroll
-          for (int v = 0; v < 24; ++v) qv[v] = real ? __ldg(q + 8 * c + v) : make_uint4(0, 0, 0, 0);
+          for (int v = 0; v < 8 * kQueryBoxes; ++v)
+            qv[v] = real && 8 * c + v < 8 * BOXES ? __ldg(q + 8 * c + v) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int d = 0; d < 3; ++d) {
+          for (int d = 0; d < kQueryBoxes; ++d) {
+            if (c + d >= BOXES) break;
             uint32_t r[32];
 #pragma unroll
             for (int v = 0; v < 8; ++v)
@@ -358,19 +364,36 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full);
+        // The queries that the next passes may need, into L2: the row's next
+        // token, and the next row's first one.
+        if (real) {
+          const int64_t next = it.i + 1 < g.s_q ? n + 1 : (int64_t)b * g.s_q, row = (int64_t)(b + 1) * g.s_q;
+#pragma unroll
+          for (int l = 0; l < BOXES; ++l) {
+            prefetch_l2(static_cast<const __nv_bfloat16*>(g.q) + next * g.q_row_stride + (int64_t)h * g.q_head_stride + 64 * l);
+            if (b + 1 < g.batch && it.left > 0)
+              prefetch_l2(static_cast<const __nv_bfloat16*>(g.q) + row * g.q_row_stride + (int64_t)h * g.q_head_stride + 64 * l);
+          }
+        }
       }
       float* w_row = a.weights + b * a.weights_batch_stride + start;
+      // The weight so far of this thread's key of tile t, read a tile ahead of
+      // its use, its lines pulled into L2 before that (read in the tile's own
+      // iteration, the latency of a cold line bound the kernel).  The first token's pass
+      // decays it, from the n_new newest keys on with 0.
+      const int64_t kept_keys = it.i > 0 ? len : a.decay != 0.f ? (int64_t)len - a.n_new : 0;
+      const float factor = it.i > 0 ? 1.f : a.decay;
+      auto weight_of = [&](int t) -> float {
+        const int key = t * BN + k_mine;
+        return t < it.t1 && k_mine < BN && key < kept_keys ? w_row[key] : 0.f;
+      };
+      float old_next = weight_of(it.t0);
       for (int t = it.t0; t < it.t1; ++t, ++tile) {
         const uint32_t buf = tile & 1u;
         const int key = t * BN + k_mine;
-        // the weight so far, read ahead of the scores; the first token's pass decays it
-        float old = 0.f;
-        if (k_mine < BN && key < len) {
-          if (it.i > 0)
-            old = w_row[key];
-          else if (a.decay != 0.f && key < (int64_t)len - a.n_new)
-            old = a.decay * w_row[key];
-        }
+        const float old = old_next;
+        old_next = weight_of(t + 1);
+        if (k_mine < BN && (k_mine & 31) == 0 && key + kWeightsAhead * BN < len) prefetch_l2(w_row + key + kWeightsAhead * BN);
         const bool arrived = mbar_wait_warp(&s_full[buf], (tile >> 1) & 1u, kWaitLimit);
         tc_fence_after();
         uint32_t s0[32], s1[32];
@@ -409,7 +432,7 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
           break;
         }
         if (k_mine < BN && key < len)
-          w_row[key] = old + ((part_s[buf][0][k_mine] + part_s[buf][1][k_mine]) +
+          w_row[key] = factor * old + ((part_s[buf][0][k_mine] + part_s[buf][1][k_mine]) +
                               (part_s[buf][2][k_mine] + part_s[buf][3][k_mine]));
       }
     }

@@ -49,34 +49,32 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return ~(bits ^ ((bits >> 31) ? 0xFFFFFFFFu : 0x80000000u));
 }
 
-// Exclusive prefix of `v` over the block's threads and the block's total.
-__device__ __forceinline__ int block_prefix(int v, int* warp_s, int& total) {
+// Exclusive prefixes of two counts over the block's threads (both below 2^31:
+// one scan of the pair packed in 64 bits).
+__device__ __forceinline__ int2 block_prefix(int a, int b, unsigned long long* warp_s) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int inc = v;
+  const unsigned long long v = (unsigned long long)(uint32_t)b << 32 | (uint32_t)a;
+  unsigned long long inc = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, inc, o);
+    const unsigned long long x = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += x;
   }
   if (lane == 31) warp_s[warp] = inc;
   __syncthreads();
   static_assert(kPlanWarps == 32, "one warp's sum per lane");
-  const int mine = warp_s[lane];
-  int all = mine, before = lane < warp ? mine : 0;
+  unsigned long long before = lane < warp ? warp_s[lane] : 0ull;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
-  total = all;
+  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
   __syncthreads();
-  return before + inc - v;
+  const unsigned long long r = before + inc - v;
+  return make_int2((int)(uint32_t)r, (int)(uint32_t)(r >> 32));
 }
 
 __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __grid_constant__ EvictParams p, int held) {
   extern __shared__ uint32_t keys_s[];   // `held` keys of this CTA's slice
   __shared__ __align__(8) int hist_s[3][kBins];   // one per pass: a peer may still read the previous one
-  __shared__ int warp_s[kPlanWarps];
+  __shared__ unsigned long long warp_s[kPlanWarps];
   __shared__ int digit_s, rest_s, less_s, tie_s;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t crank = tc::cluster_ctarank();
@@ -163,8 +161,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
           if (c < (int)crank) e[0] += part[c].x, e[1] += part[c].y;
         }
       }
-      int all;
-      int before = block_prefix(h[0] + h[1], warp_s, all), less = block_prefix(e[0] + e[1], warp_s, all);
+      const int2 sums = block_prefix(h[0] + h[1], e[0] + e[1], warp_s);
+      int before = sums.x, less = sums.y;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         if (before < rest && rest <= before + h[k]) {   // exactly one thread and bin
@@ -200,13 +198,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
       n_less += __popc(__ballot_sync(0xffffffffu, i < whi && key < prefix));
       n_tie += __popc(__ballot_sync(0xffffffffu, i < whi && key == prefix));
     }
-  int cta_less, cta_tie;
-  int before_less = block_prefix(lane == 0 ? n_less : 0, warp_s, cta_less);
-  int before_tie = block_prefix(lane == 0 ? n_tie : 0, warp_s, cta_tie);
-  before_less += peers_less;
-  before_tie += peers_tie;
-  before_less = __shfl_sync(0xffffffffu, before_less, 0);
-  before_tie = __shfl_sync(0xffffffffu, before_tie, 0);
+  const int2 sums = block_prefix(lane == 0 ? n_less : 0, lane == 0 ? n_tie : 0, warp_s);
+  const int before_less = __shfl_sync(0xffffffffu, sums.x, 0) + peers_less;
+  const int before_tie = __shfl_sync(0xffffffffu, sums.y, 0) + peers_tie;
   if (take > 0) {
     int out = p.n_sink + before_less + min(before_tie, rest), ties = before_tie;
     const uint32_t below = (1u << lane) - 1u;

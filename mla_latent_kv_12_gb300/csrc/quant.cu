@@ -17,6 +17,7 @@
 #include "e4m3.cuh"
 #include "mla_internal.h"
 #include "rope_math.cuh"
+#include "tc_common.cuh"
 #include "tc_host.h"
 
 namespace mla {
@@ -147,27 +148,38 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8]) {
                     encode_e4m3x2(x[4], x[5]) | (uint32_t)encode_e4m3x2(x[6], x[7]) << 16);
 }
 
-// Eight consecutive raw values as loaded.
+// Eight consecutive raw values as loaded, and as four pairs.
 template <typename T>
 struct Raw8;
 template <>
 struct Raw8<__nv_bfloat16> {
   uint4 a;
   __device__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
-  __device__ void get(float (&v)[8]) const {
+  __device__ void get(float2 (&v)[4]) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[2 * j] = __uint_as_float(w[j] << 16), v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    for (int j = 0; j < 4; ++j) v[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
   }
 };
 template <>
 struct Raw8<float> {
   float4 a, b;
   __device__ void load(const float* p) { a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1]; }
-  __device__ void get(float (&v)[8]) const {
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  __device__ void get(float2 (&v)[4]) const {
+    v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w), v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
   }
 };
+// (a0 b0 + c0, a1 b1 + c1) as one packed f32x2 operation.
+__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
+  uint64_t x, y, z, r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c.x), "f"(c.y));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(r));
+  return d;
+}
 
 // Tiles of 64 rows, four neighbouring ones per warp; lane l holds elements
 // 8l .. 8l + 7 and 256 + those of each.
@@ -224,42 +236,37 @@ __global__ void __launch_bounds__(kHeldWarps * 32, sizeof(TI) == 2 ? 2 : 1) enco
       for (int k = threadIdx.x; k < n_blocks; k += kHeldWarps * 32) amax_s[k] = 0;
       __syncthreads();
     }
-    // The values of group c of token k: normalised and weighted.
+    // A token's value is x inv g.  Its largest magnitude is taken as inv
+    // max |x g| (half a unit in the last place of the exact one either way, as
+    // the values themselves), in one walk with the sum of squares.
     float inv[kHeldRows], amax[kHeldRows];
-    auto values = [&](int k, int c, float(&v)[8]) {
-      raw[k][c].get(v);
-      if constexpr (kNorm) {
-        float w[8];
-        g[c].get(w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = v[j] * inv[k] * w[j];
-      }
-    };
 #pragma unroll
     for (int k = 0; k < kHeldRows; ++k) {
       amax[k] = 0.f;
+      inv[k] = 1.f;
       if (!mine(k)) continue;
-      if constexpr (kNorm) {
-        float sq = 0.f;
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          if (live[c]) {
-            float v[8];
-            raw[k][c].get(v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sq = fmaf(v[j], v[j], sq);
-          }
-        inv[k] = rsqrtf(warp_sum(sq) / (float)p.rank + p.eps);
-      }
+      float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
       for (int c = 0; c < 2; ++c)
         if (live[c]) {
-          float v[8];
-          values(k, c, v);
+          float2 v[4], w[4];
+          raw[k][c].get(v);
+          if constexpr (kNorm) g[c].get(w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) amax[k] = fmaxf(amax[k], fabsf(v[j]));
+          for (int j = 0; j < 4; ++j) {
+            float2 x = v[j];
+            if constexpr (kNorm) {
+              sq = fma_f32x2(x, x, sq);
+              x = tc::mul_f32x2(x, w[j]);
+            }
+            amax[k] = tc::fmax3(amax[k], fabsf(x.x), fabsf(x.y));
+          }
         }
       amax[k] = warp_max(amax[k]);
+      if constexpr (kNorm) {
+        inv[k] = rsqrtf(warp_sum(sq.x + sq.y) / (float)p.rank + p.eps);
+        amax[k] *= inv[k];
+      }
       if (!warp_blocks && lane == 0) atomicMax(&amax_s[(r0 + k) >> p.block_shift], __float_as_uint(amax[k]));
     }
     if (warp_blocks) {
@@ -292,16 +299,22 @@ __global__ void __launch_bounds__(kHeldWarps * 32, sizeof(TI) == 2 ? 2 : 1) enco
 #pragma unroll
     for (int k = 0; k < kHeldRows; ++k) {
       if (!mine(k)) continue;
-      const float to_units = inverse_unit_of(exp_s[(r0 + k) >> p.block_shift]);
+      // in units: (x inv) g 2^(127 - e), the power of two taken with inv (exact)
+      const float f = inv[k] * inverse_unit_of(exp_s[(r0 + k) >> p.block_shift]);
       uint8_t* dst = codes + (base + r0 + k) * p.codes_row_stride + 8 * lane;
 #pragma unroll
       for (int c = 0; c < 2; ++c)
         if (live[c]) {
-          float v[8];
-          values(k, c, v);
+          float2 v[4], w[4];
+          raw[k][c].get(v);
+          if constexpr (kNorm) g[c].get(w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] *= to_units;   // a power of two: exact
-          *reinterpret_cast<uint2*>(dst + 256 * c) = encode8(v);
+          for (int j = 0; j < 4; ++j) {
+            v[j] = tc::mul_f32x2(v[j], make_float2(f, f));
+            if constexpr (kNorm) v[j] = tc::mul_f32x2(v[j], w[j]);
+          }
+          const float x[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
+          *reinterpret_cast<uint2*>(dst + 256 * c) = encode8(x);
         }
     }
     if constexpr (kNorm) {

@@ -71,6 +71,19 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+// Four sums over the warp at once, every lane receiving all of them: the first
+// two steps halve the sums a lane carries.
+__device__ __forceinline__ void warp_sum4(float (&v)[4]) {
+  const int lane = threadIdx.x & 31;
+  const bool b4 = lane & 16, b3 = lane & 8;
+  float x = (b4 ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, b4 ? v[0] : v[2], 16);
+  const float y = (b4 ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, b4 ? v[1] : v[3], 16);
+  x = (b3 ? y : x) + __shfl_xor_sync(0xffffffffu, b3 ? x : y, 8);   // lanes 0-7: v[0], 8-15: v[1], 16-23: v[2], 24-31: v[3]
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = __shfl_sync(0xffffffffu, x, 8 * k);
+}
 // NaN is passed over (it has a code of its own), so it does not set a unit.
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -239,35 +252,42 @@ __global__ void __launch_bounds__(kHeldWarps * 32, sizeof(TI) == 2 ? 2 : 1) enco
     // A token's value is x inv g.  Its largest magnitude is taken as inv
     // max |x g| (half a unit in the last place of the exact one either way, as
     // the values themselves), in one walk with the sum of squares.
-    float inv[kHeldRows], amax[kHeldRows];
+    float inv[kHeldRows], amax[kHeldRows], sum[kHeldRows];
+#pragma unroll
+    for (int k = 0; k < kHeldRows; ++k) inv[k] = 1.f, amax[k] = 0.f, sum[k] = 0.f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      if (!live[c]) continue;
+      float2 w[4];
+      if constexpr (kNorm) g[c].get(w);
+#pragma unroll
+      for (int k = 0; k < kHeldRows; ++k) {
+        if (!mine(k)) continue;
+        float2 v[4], sq = make_float2(0.f, 0.f);
+        raw[k][c].get(v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float2 x = v[j];
+          if constexpr (kNorm) {
+            sq = fma_f32x2(x, x, sq);
+            x = tc::mul_f32x2(x, w[j]);
+          }
+          amax[k] = tc::fmax3(amax[k], fabsf(x.x), fabsf(x.y));
+        }
+        sum[k] += sq.x + sq.y;
+      }
+    }
+    if constexpr (kNorm) {
+      warp_sum4(sum);
+#pragma unroll
+      for (int k = 0; k < kHeldRows; ++k) inv[k] = rsqrtf(sum[k] / (float)p.rank + p.eps);
+    }
 #pragma unroll
     for (int k = 0; k < kHeldRows; ++k) {
-      amax[k] = 0.f;
-      inv[k] = 1.f;
-      if (!mine(k)) continue;
-      float2 sq = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-        if (live[c]) {
-          float2 v[4], w[4];
-          raw[k][c].get(v);
-          if constexpr (kNorm) g[c].get(w);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float2 x = v[j];
-            if constexpr (kNorm) {
-              sq = fma_f32x2(x, x, sq);
-              x = tc::mul_f32x2(x, w[j]);
-            }
-            amax[k] = tc::fmax3(amax[k], fabsf(x.x), fabsf(x.y));
-          }
-        }
-      amax[k] = warp_max(amax[k]);
-      if constexpr (kNorm) {
-        inv[k] = rsqrtf(warp_sum(sq.x + sq.y) / (float)p.rank + p.eps);
-        amax[k] *= inv[k];
-      }
-      if (!warp_blocks && lane == 0) atomicMax(&amax_s[(r0 + k) >> p.block_shift], __float_as_uint(amax[k]));
+      // (non-negative: ordered as integers)
+      amax[k] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax[k])));
+      if constexpr (kNorm) amax[k] *= inv[k];
+      if (!warp_blocks && lane == 0 && mine(k)) atomicMax(&amax_s[(r0 + k) >> p.block_shift], __float_as_uint(amax[k]));
     }
     if (warp_blocks) {
       // lane k: block k of the warp's rows
@@ -296,26 +316,29 @@ __global__ void __launch_bounds__(kHeldWarps * 32, sizeof(TI) == 2 ? 2 : 1) enco
       }
       __syncthreads();
     }
+    // in units: (x inv) g 2^(127 - e), the power of two taken with inv (exact)
 #pragma unroll
-    for (int k = 0; k < kHeldRows; ++k) {
-      if (!mine(k)) continue;
-      // in units: (x inv) g 2^(127 - e), the power of two taken with inv (exact)
-      const float f = inv[k] * inverse_unit_of(exp_s[(r0 + k) >> p.block_shift]);
-      uint8_t* dst = codes + (base + r0 + k) * p.codes_row_stride + 8 * lane;
+    for (int k = 0; k < kHeldRows; ++k)
+      if (mine(k)) inv[k] *= inverse_unit_of(exp_s[(r0 + k) >> p.block_shift]);
+    uint8_t* dst = codes + (base + r0) * p.codes_row_stride + 8 * lane;
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        if (live[c]) {
-          float2 v[4], w[4];
-          raw[k][c].get(v);
-          if constexpr (kNorm) g[c].get(w);
+    for (int c = 0; c < 2; ++c) {
+      if (!live[c]) continue;
+      float2 w[4];
+      if constexpr (kNorm) g[c].get(w);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            v[j] = tc::mul_f32x2(v[j], make_float2(f, f));
-            if constexpr (kNorm) v[j] = tc::mul_f32x2(v[j], w[j]);
-          }
-          const float x[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
-          *reinterpret_cast<uint2*>(dst + 256 * c) = encode8(x);
+      for (int k = 0; k < kHeldRows; ++k) {
+        if (!mine(k)) continue;
+        float2 v[4];
+        raw[k][c].get(v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[j] = tc::mul_f32x2(v[j], make_float2(inv[k], inv[k]));
+          if constexpr (kNorm) v[j] = tc::mul_f32x2(v[j], w[j]);
         }
+        const float x[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
+        *reinterpret_cast<uint2*>(dst + k * p.codes_row_stride + 256 * c) = encode8(x);
+      }
     }
     if constexpr (kNorm) {
 #pragma unroll

@@ -80,7 +80,9 @@ typedef enum mla_dtype { MLA_DTYPE_F32 = 0, MLA_DTYPE_BF16 = 1 } mla_dtype;
                                                    range of the bf16 decode's
                                                    partials; saturated; or a latent
                                                    value to be held in 8 bits is
-                                                   beyond 57344; saturated          */
+                                                   beyond 57344; saturated; or an
+                                                   operand of an 8-bit cache's
+                                                   attention leaves the fp16 range  */
 #define MLA_DEVICE_BAD_BLOCK_START (1 << 9)     /* an 8-bit cache row whose kv_start is not
                                                    a whole number of scale blocks   */
 /* Largest |half score| (unscaled q . k over one CTA's 288 features) that the
@@ -530,7 +532,8 @@ int mla_prefill_attend(const void* q_nope, int64_t q_nope_row_stride, int64_t q_
  * rounded again to the larger unit (exact but for what falls below e4m3's
  * smallest step).  Codes round to nearest, ties to even.  A magnitude beyond
  * 57344 (or infinite) saturates and sets MLA_DEVICE_VALUE_RANGE; NaN stays
- * NaN and sets no unit.  kv_len_out may alias kv_len.  At most 65535 batch rows.
+ * NaN and sets no unit.  kv_len_out may alias kv_len and row_offsets.  At most
+ * 65535 batch rows.
  *
  * mla_quantize_cache: the windows of a latent buffer [b, r, rank] (dtype f32 or
  * bf16) into codes and exponents, rows outside the windows left as they
@@ -558,12 +561,19 @@ int mla_dequantize_cache(const uint8_t* codes, int64_t codes_row_stride, int64_t
 
 /*
  * mla_decode_attend over an 8-bit cache: the same attention over the held
- * values (no further rounding of them: over bf16 queries the result is that of
- * mla_decode_attend over the dequantised bf16 cache).  q and rope have
- * `dtype`.  bf16 is served for the shapes of mla_decode_attend, with codes and
- * rope 16-byte aligned, codes strides multiples of 16 and rope strides
- * multiples of 8 elements; f32 for any shape.  The workspace is that of
- * mla_decode_workspace_size for `dtype`.
+ * values.  q and rope have `dtype`.  bf16 is served for the shapes of
+ * mla_decode_attend, with codes and rope 16-byte aligned, codes strides
+ * multiples of 16 and rope strides multiples of 8 elements; f32 for any shape.
+ * The workspace is that of mla_decode_workspace_size for `dtype`.
+ *
+ * The bf16 path multiplies the latent, the latent part of q and the
+ * probabilities in fp16 (the rope part stays bf16).  Held values are exact in
+ * fp16 for units of 2^-15 and more; those of smaller units round to multiples
+ * of 2^-24 (zero for units of 2^-25 and less), and a block read with a unit
+ * below 2^-15 and above the smallest, 2^-63 (that of zeros), sets
+ * MLA_DEVICE_VALUE_RANGE.  Query values are exact from 2^-14 to 65504 in
+ * magnitude, multiples of 2^-24 below; larger ones saturate and set
+ * MLA_DEVICE_VALUE_RANGE.  mla_key_weights_q8 takes its operands the same way.
  */
 int mla_decode_attend_q8(const void* q, int64_t q_row_stride, int64_t q_head_stride, const uint8_t* codes,
                          int64_t codes_row_stride, int64_t codes_batch_stride, const uint8_t* scales,

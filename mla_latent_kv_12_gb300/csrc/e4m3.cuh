@@ -3,10 +3,12 @@
 // units of a power of two 2^(e - 127) per block of buffer rows, e one byte in
 // [64, 134].
 //
-// Powers of two make every conversion but the first rounding exact: a code
-// times 2^(e - 127) has 4 significant bits and an exponent between -72 and 15,
-// so it is a normal bf16 (and f32), and moving a code to a larger unit only
-// loses what falls below e4m3's smallest step.
+// Powers of two make the conversions to bf16 and f32 exact: a code times
+// 2^(e - 127) has 4 significant bits and an exponent between -72 and 15, so it
+// is a normal number of both, and moving a code to a larger unit only loses
+// what falls below e4m3's smallest step.  fp16, the tensor cores' operand, is
+// exact down to unit 2^-15 (a block whose largest magnitude is above 0.0068);
+// below it values round to multiples of 2^-24.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -55,7 +57,7 @@ __device__ __forceinline__ float decode_e4m3(uint32_t code, float unit) {
 // least bit is at least 2^-9.  Below, values round to multiples of 2^-24.
 constexpr int kMinExponentF16 = 127 - 15;
 __device__ __forceinline__ uint32_t f16_unit(int e) {
-  const __half h = __float2half_rn(__uint_as_float((uint32_t)e << 23));   // subnormal below 2^-14, 0 below 2^-25
+  const __half h = __float2half_rn(__uint_as_float((uint32_t)e << 23));   // subnormal below 2^-14, 0 from 2^-25 down
   return (uint32_t)__half_as_ushort(h) * 0x00010001u;
 }
 __device__ __forceinline__ void decode_e4m3x8_f16(const uint2 codes, uint32_t mul2, uint32_t (&out)[4]) {
@@ -72,13 +74,25 @@ __device__ __forceinline__ void decode_e4m3x8_f16(const uint2 codes, uint32_t mu
   }
 }
 
-// Two bf16 values as fp16, saturating (exact from 2^-14 to 65504 in magnitude).
+// Two bf16 values as fp16: exact from 2^-14 to 65280 in magnitude, multiples of
+// 2^-24 below, saturating above.
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v) {
   const float lo = __uint_as_float(v << 16), hi = __uint_as_float(v & 0xFFFF0000u);
   // (written so that NaN stays NaN)
   const __half2 h = __floats2half2_rn(lo > 65504.f ? 65504.f : lo < -65504.f ? -65504.f : lo,
                                       hi > 65504.f ? 65504.f : hi < -65504.f ? -65504.f : hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Running maximum of the magnitudes of bf16 pairs (both halves; NaN ignored),
+// and whether fp16 cannot hold it.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t top, uint32_t v) {
+  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&top),
+                                   __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ bool beyond_f16(uint32_t top) {
+  return __uint_as_float(top << 16) > 65504.f || __uint_as_float(top & 0xFFFF0000u) > 65504.f;
 }
 
 // Sixteen codes to sixteen bf16 values (eight packed pairs), exact.  A code's

@@ -563,12 +563,13 @@ cudaError_t launch_append_q8(const EncodeParams& p_in, int in_dtype, int rope_dt
   p.tile_rows = tile_rows_of(p, vec);
   // Tiles that s_new rows can touch.  Up to two are walked by one CTA per row (a
   // decode step's append); more are spread over CTAs.  The new lengths are
-  // written by the row's first CTA unless they may overwrite the lengths that
-  // other CTAs of the row still have to read: then by a launch of their own.
+  // written by the row's first CTA unless they may overwrite the lengths or
+  // offsets that other CTAs of the row still have to read: then by a launch of
+  // their own.
   const int64_t tiles = ((int64_t)p.s_new + p.tile_rows - 2) / p.tile_rows + 1;
   const unsigned gx = tiles <= 2 ? 1u : (unsigned)(tiles < 65535 ? tiles : 65535);
-  const bool apart = p.kv_len_out + p.batch <= p.kv_len || p.kv_len + p.batch <= p.kv_len_out;
-  p.lengths_here = p.kv_len_out != nullptr && (gx == 1 || apart);
+  auto apart = [&](const int32_t* x) { return !x || p.kv_len_out + p.batch <= x || x + p.batch <= p.kv_len_out; };
+  p.lengths_here = p.kv_len_out != nullptr && (gx == 1 || (apart(p.kv_len) && apart(p.row_offsets)));
   const dim3 grid(gx, (unsigned)p.batch);
   cudaError_t e;
   if (in_dtype == MLA_DTYPE_F32)

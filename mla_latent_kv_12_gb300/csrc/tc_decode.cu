@@ -77,13 +77,14 @@ constexpr int kGatherWarp = 11;   // first extra gather warp
 // what the roles share, and converting further ahead slows the softmax.)
 // Roles are whole warpgroups, whose registers are redistributed at their
 // start: the softmax and exchange warps take what the MMA and converting warps
-// do not need.  The shares (per thread and warpgroup) add up to the launch's
-// 5 x 96.
+// do not need.  The shares (per thread and warpgroup) add up to the launch's,
+// kRegsLaunch for each of the five.
 constexpr int THREADS_Q8 = 640;
 constexpr int kConvertWarps = 8;
 constexpr int STAGES_Q8 = 3;
+constexpr int kRegsLaunch = 96;
 constexpr int kRegsSoftmax = 144, kRegsExchange = 128, kRegsIssue = 48, kRegsConvert = 80;
-static_assert(kRegsSoftmax + kRegsExchange + kRegsIssue + 2 * kRegsConvert <= 5 * 96, "more registers than the launch has");
+static_assert(kRegsSoftmax + kRegsExchange + kRegsIssue + 2 * kRegsConvert <= 5 * kRegsLaunch, "more registers than the launch has");
 using DecodeFetch = Q8Fetch<16, 32 * kConvertWarps>;
 // Dynamic shared memory: the stage ring, then send[2] and receive[2].  The
 // 1024-byte alignment of the extern declaration places it on a 1024-byte
@@ -926,6 +927,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         {
           // all 36 loads in flight at once: 256 latent dims, then the 32 rope dims
           uint4 qv[36];
+          uint32_t q_top = 0;   // largest magnitudes that are converted to fp16
           const uint4* qlat = reinterpret_cast<const uint4*>(qrow + dim_base);
           const uint4* qrope = reinterpret_cast<const uint4*>(qrow + RANK + 32 * (int)rank);
 #pragma unroll
@@ -941,9 +943,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               r[4 * v + 3] = qv[8 * c + v].w;
             if constexpr (kQ8) {
 #pragma unroll
-              for (int v = 0; v < 32; ++v) r[v] = bf16x2_to_f16x2(r[v]);
+              for (int v = 0; v < 32; ++v) q_top = max_abs_bf16x2(q_top, r[v]), r[v] = bf16x2_to_f16x2(r[v]);
             }
             tmem_st32(tmem + TM_Q + c * 32 + lane_off, r);
+          }
+          if constexpr (kQ8) {
+            if (beyond_f16(q_top) && a.status) atomicOr(a.status, MLA_DEVICE_VALUE_RANGE);
           }
           uint32_t r[16];
 #pragma unroll
@@ -1872,6 +1877,15 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
                               : lockstep   ? tc_decode_kernel<kPrefetchAheadGroup, THREADS, true>
                                            : tc_decode_kernel<kPrefetchAheadRow, THREADS, false>;
   const int smem_bytes = q8 ? SMEM_BYTES_Q8 : SMEM_BYTES;
+  if (q8) {
+    // The warpgroups' register shares wait for one another: a build with fewer
+    // registers than they add up to must not be launched.
+    static const int regs = [&] {
+      cudaFuncAttributes attr;
+      return cudaFuncGetAttributes(&attr, decode_kernel) == cudaSuccess ? attr.numRegs : 0;
+    }();
+    if (regs < kRegsLaunch) return cudaErrorInvalidConfiguration;
+  }
   {
     const cudaError_t ea = set_max_dynamic_smem(decode_kernel, smem_bytes);
     if (ea != cudaSuccess) return ea;

@@ -5,7 +5,7 @@
 // Q[128 x 576] . K^T, with the probabilities normalised by a given lse, so
 // nothing has to be known about other keys: each tile of 64 keys is finished
 // on its own.  The whole query of a token fits TMEM as the MMA's A operand (288
-// columns of packed bf16) beside two score buffers (2 x 64), so a CTA scores
+// columns of packed 16-bit pairs) beside two score buffers (2 x 64), so a CTA scores
 // all 576 features itself and no SM pair is needed.  At one query token it is
 // bound by the cache read (1152 or 641 bytes against 147 kflop per key: 0.17
 // or 0.09 ns at the measured copy rate, 0.076 ns at the measured bf16 rate).
@@ -16,7 +16,8 @@
 //    the same thread, in token order (no atomics, the same bits every time).
 //  * bf16 cache: warp 0 loads [64 keys x 576] tiles by TMA into a three-stage
 //    ring (nine boxes of 64 dims, 128-byte swizzle).  8-bit cache: warps 6..13
-//    fetch codes and write decoded bf16 into the same layout (q8_tiles.cuh).
+//    fetch codes and write their fp16 values into the same layout
+//    (q8_tiles.cuh); the latent part of the query is converted to fp16 too.
 //  * Warp 1 issues the 36 MMAs of a tile.  Warps 2..5 (one thread per head)
 //    load each token's query into TMEM, turn scores into probabilities and
 //    sum them over their 32 heads with a shuffle tree that halves the keys per
@@ -337,6 +338,7 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
         const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(g.q) + n * g.q_row_stride +
                                                         (int64_t)h * g.q_head_stride);
         lse2 = real ? a.lse[n * g.heads + h] * 1.4426950408889634f : 0.f;
+        uint32_t q_top = 0;   // largest magnitudes that are converted to fp16
 #pragma unroll
         for (int c = 0; c < BOXES; c += kQueryBoxes) {
           uint4 qv[8 * kQueryBoxes];   // these loads are in flight together
@@ -354,12 +356,13 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
             if constexpr (kQ8) {
               if (c + d < 8) {
 #pragma unroll
-                for (int v = 0; v < 32; ++v) r[v] = bf16x2_to_f16x2(r[v]);
+                for (int v = 0; v < 32; ++v) q_top = max_abs_bf16x2(q_top, r[v]), r[v] = bf16x2_to_f16x2(r[v]);
               }
             }
             tmem_st32(tmem + TM_Q + (c + d) * 32 + lane_off, r);
           }
         }
+        if (kQ8 && beyond_f16(q_top) && g.device_status) atomicOr(g.device_status, MLA_DEVICE_VALUE_RANGE);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();

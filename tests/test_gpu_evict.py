@@ -335,3 +335,86 @@ def test_append_attend_weights_evict(mla):
                 assert torch.equal(a[b, lo:lo + len(at)].contiguous().view(torch.uint8),
                                    o[b, lo + torch.from_numpy(at).to(DEV)].contiguous().view(torch.uint8))
     assert evicted >= 6 and int(st) & ~mla.DEVICE_SCORE_RANGE == 0
+
+
+def test_key_weights_fp16_operand_range(mla):
+    """As the attention over an 8-bit cache: small units and large query values are flagged, and rounded as documented."""
+    g = gen(92)
+    B, T = 2, 200
+    q, codes, scales, rope, start, length = attend_case(g, B, 1, 128, T, 1, [T] * B, [0] * B)
+    scales[0], scales[1] = 112, 105
+
+    def run(n, w):
+        st = status()
+        mla.key_weights_q8(q, codes, scales, 1, rope, lse, start, n, B, 1, SCALE, w, decay=0.0, device_status=st)
+        return int(st)
+    lat = [np.round(R.held64(codes[b].cpu().numpy(), scales[b].cpu().numpy(), 1) * 2.0 ** 24) * 2.0 ** -24 for b in range(B)]
+    lse = make_lse(q, lat, rope, start, length, 1)
+    w = torch.zeros(B, T, device=DEV)
+    assert run(i32([T, 0]), w) == 0 and run(i32([T, T]), w) == mla.DEVICE_VALUE_RANGE
+    check_weights(w, torch.zeros_like(w), q, lat, rope, lse, start, length, 1, 0.0, 0)
+    scales.fill_(120)
+    codes[..., 3] = 0
+    want, got = torch.zeros_like(w), torch.zeros_like(w)
+    assert run(length, want) == 0
+    q[1, 5, 3] = 65536.0
+    assert run(length, got) == mla.DEVICE_VALUE_RANGE and torch.equal(got, want)
+
+
+def cycle(mla, s, stream=None):
+    """One serving step over state ``s``: append, attend, weights, eviction."""
+    mla.append_compressed_q8(s["raw"], s["raw_rope"], s["gain"], EPS, THETA, s["codes"], s["scales"], 1, s["rope"], None,
+                             s["length"], kv_len_out=s["length"], row_offsets=s["offset"], stream=stream)
+    mla.decode_attend_q8(s["q"], s["codes"], s["scales"], 1, s["rope"], None, s["length"], 2, 1, SCALE, s["ctx"], s["lse"],
+                         workspace=s["ws"], stream=stream)
+    mla.key_weights_q8(s["q"], s["codes"], s["scales"], 1, s["rope"], s["lse"], None, s["length"], 2, 1, SCALE, s["weights"],
+                       n_new=1, stream=stream)
+    mla.evict_plan(s["weights"], None, s["length"], 300, 4, 32, s["kept"], s["counts"], kv_len_out=s["length"], stream=stream)
+    mla.cache_compact([s["codes"], s["rope"], s["scales"].unsqueeze(-1), s["weights"].unsqueeze(-1)], None, s["kept"],
+                      s["counts"], stream=stream)
+
+
+def cycle_state(mla, seed):
+    g = gen(seed)
+    codes, scales = random_cache(g, 2, 400, 512, 1)
+    return dict(codes=codes, scales=scales, rope=normal(g, 2, 400, 64).bfloat16(), weights=torch.rand(2, 400, generator=g, device=DEV),
+                raw=normal(g, 2, 1, 512).bfloat16(), raw_rope=normal(g, 2, 1, 64).bfloat16(), gain=torch.ones(512, device=DEV).bfloat16(),
+                q=normal(g, 2, 128, 576).bfloat16() * 0.2, length=i32([299, 250]), offset=i32([900, 250]),
+                ctx=torch.empty(2, 128, 512, dtype=torch.bfloat16, device=DEV), lse=torch.empty(2, 128, device=DEV),
+                kept=torch.zeros(2, 300, dtype=torch.int32, device=DEV), counts=i32([0, 0]),
+                ws=torch.empty(mla.decode_workspace_size(2, 1, 128, 512, 64, 400), dtype=torch.uint8, device=DEV))
+
+
+def same_state(a, b):
+    return all(torch.equal(a[k].contiguous().view(torch.uint8), b[k].contiguous().view(torch.uint8)) for k in a if k != "ws")
+
+
+def test_cycles_on_two_streams_and_in_two_graphs(mla):
+    """Two caches stepped at once on two streams, and by two captured graphs replayed in turn, against one after the
+    other: the same bits."""
+    steps = 5
+    want = [cycle_state(mla, k) for k in (1, 2)]
+    for s in want:
+        for _ in range(steps):
+            cycle(mla, s)
+    assert want[0]["length"].tolist() == [300, 255] and want[0]["counts"].tolist() == [300, -1]
+    got = [cycle_state(mla, k) for k in (1, 2)]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(steps):
+        for s, side in zip(got, sides):
+            cycle(mla, s, side)
+    torch.cuda.synchronize()
+    assert all(same_state(a, b) for a, b in zip(got, want))
+    got = [cycle_state(mla, k) for k in (1, 2)]
+    graphs = []
+    for s in got:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            cycle(mla, s)
+        graphs.append(graph)
+    for _ in range(steps):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    assert all(same_state(a, b) for a, b in zip(got, want))

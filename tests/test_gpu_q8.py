@@ -527,3 +527,55 @@ def test_capture_replay_and_other_stream(mla):
     torch.cuda.synchronize()
     assert length.tolist() == [504, 7]
     check_attend(ctx, lse, (q, codes, scales, rope, start, length), block, 1)
+
+
+def test_append_lengths_over_the_offsets(mla):
+    """New lengths written over the offsets tensor, rows of several tiles: every tile reads the old offsets."""
+    g = gen(83)
+    B, T, s_new, block = 3, 900, 700, 16
+    codes, scales = random_cache(g, B, T, 512, block)
+    rope = normal(g, B, T, 64).bfloat16()
+    raw, raw_rope = normal(g, B, s_new, 512).bfloat16(), normal(g, B, s_new, 64).bfloat16()
+    gain = torch.ones(512, device=DEV).bfloat16()
+    length, offset = i32([0, 100, 33]), i32([7, 5000, 33])
+    off0 = offset.tolist()
+    before = codes.cpu().numpy(), scales.cpu().numpy(), R.as64(rope)
+    mla.append_compressed_q8(raw, raw_rope, gain, EPS, THETA, codes, scales, block, rope, None, length,
+                             kv_len_out=offset, row_offsets=offset)
+    assert offset.tolist() == [700, 800, 733] and length.tolist() == [0, 100, 33]
+    check_append(raw, raw_rope, gain, before, (codes.cpu().numpy(), scales.cpu().numpy(), R.as64(rope)), block,
+                 [0] * B, [0, 100, 33], off0, s_new, torch.bfloat16)
+
+
+def test_attend_fp16_operand_range(mla):
+    """Held values of units below 2^-15 are rounded to multiples of 2^-24 and flagged; so is a query value beyond
+    65504, which saturates.  Each row has few keys (one piece), its rope scores spread the probabilities."""
+    g = gen(84)
+    B, T = 3, 100
+    q, codes, scales, rope, start, length = attend_case(g, B, 1, 128, T, 1, [T] * B, [0] * B)
+    scales[0], scales[1], scales[2] = 112, 111, 105        # units 2^-15, 2^-16, 2^-22
+    ctx, lse = torch.empty(B, 128, 512, device=DEV), torch.empty(B, 128, device=DEV)
+
+    def run(n, **kw):
+        st = status()
+        mla.decode_attend_q8(q, codes, scales, 1, rope, start, n, B, 1, SCALE, ctx, lse, device_status=st, **kw)
+        return int(st) & ~mla.DEVICE_SCORE_RANGE
+    assert run(i32([T, 0, 0])) == 0
+    assert run(i32([0, T, 0])) == mla.DEVICE_VALUE_RANGE and run(i32([0, 0, 1])) == mla.DEVICE_VALUE_RANGE
+    assert run(i32([T, T, T])) == mla.DEVICE_VALUE_RANGE
+    for b in range(B):
+        lat = np.round(R.held64(codes[b].cpu().numpy(), scales[b].cpu().numpy(), 1) * 2.0 ** 24) * 2.0 ** -24
+        c, l = R.attend64(R.as64(q[b]), lat, R.as64(rope[b]), SCALE)
+        # p rounds to fp16 (2^-11), the exchanged scores to fp16 within the bf16 bound on the lse: 2e-2 of each weight
+        assert np.abs(R.as64(ctx[b]) - c).max() <= (2e-2 + 2.0 ** -11) * np.abs(lat).max()
+        assert np.abs(R.as64(lse[b]) - l).max() <= 2e-2
+    # the query: feature 3 meets zero latents, so the scores are those of any finite value
+    scales.fill_(120)
+    codes[..., 3] = 0
+    assert run(length) == 0
+    want = ctx.clone()
+    q[1, 5, 3] = 65280.0                                   # the largest bf16 that fp16 holds
+    assert run(length) == 0 and torch.equal(ctx, want)
+    for big in (65536.0, -1e30, float("inf")):
+        q[1, 5, 3] = big
+        assert run(length) == mla.DEVICE_VALUE_RANGE and torch.equal(ctx, want)

@@ -949,6 +949,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if constexpr (kQ8) {
             if (beyond_f16(q_top) && a.status) atomicOr(a.status, MLA_DEVICE_VALUE_RANGE);
+            __syncwarp();   // (the TMEM stores are the whole warp's)
           }
           uint32_t r[16];
 #pragma unroll

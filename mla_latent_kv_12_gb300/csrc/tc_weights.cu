@@ -283,6 +283,21 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
         cp_async_commit();
         if (++stage == kStages) stage = 0, phase ^= 1u;
       }
+      if (t0 == 0 && g.device_status) {
+        // Once per query row: values that fp16 cannot hold.  These warps run
+        // ahead of the others, whose registers are full (checked as they are
+        // converted, four tokens took 165 us on 8 rows of 16384 keys, here 145).
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(g.q) + ((int64_t)b * g.s_q + it.i) * g.q_row_stride;
+        uint32_t top = 0;
+#pragma unroll 4
+        for (int h = cw; h < g.heads; h += kConvertWarps)
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(q + (int64_t)h * g.q_head_stride) + 32 * v + lane);
+            top = max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(top, x.x), x.y), x.z), x.w);
+          }
+        if (beyond_f16(top)) atomicOr(g.device_status, MLA_DEVICE_VALUE_RANGE);
+      }
       cp_async_wait<0>();   // the slots are free for the next pass
     }
   } else if (warp == 1) {
@@ -338,7 +353,6 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
         const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(g.q) + n * g.q_row_stride +
                                                         (int64_t)h * g.q_head_stride);
         lse2 = real ? a.lse[n * g.heads + h] * 1.4426950408889634f : 0.f;
-        uint32_t q_top = 0;   // largest magnitudes that are converted to fp16
 #pragma unroll
         for (int c = 0; c < BOXES; c += kQueryBoxes) {
           uint4 qv[8 * kQueryBoxes];   // these loads are in flight together
@@ -356,13 +370,12 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
             if constexpr (kQ8) {
               if (c + d < 8) {
 #pragma unroll
-                for (int v = 0; v < 32; ++v) q_top = max_abs_bf16x2(q_top, r[v]), r[v] = bf16x2_to_f16x2(r[v]);
+                for (int v = 0; v < 32; ++v) r[v] = bf16x2_to_f16x2(r[v]);
               }
             }
             tmem_st32(tmem + TM_Q + (c + d) * 32 + lane_off, r);
           }
         }
-        if (kQ8 && beyond_f16(q_top) && g.device_status) atomicOr(g.device_status, MLA_DEVICE_VALUE_RANGE);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();

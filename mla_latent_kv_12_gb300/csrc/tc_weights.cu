@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
     const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
     const bool real = h < g.heads;
     const int k_mine = threadIdx.x - 64;      // key of the tile whose weight this thread updates (warps 2, 3)
-    constexpr int kQueryBoxes = kQ8 ? 3 : 5;   // (the registers of a thread: 128 and 254)
+    constexpr int kQueryBoxes = kQ8 ? 5 : 9;   // (the registers of a thread: 128 and 254)
     uint32_t tile = 0;
     float lse2 = 0.f;
     // The four warps meet in a barrier at every tile, so they leave together.
@@ -347,35 +347,31 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
       const int64_t start = g.kv_start ? g.kv_start[b] : 0;
       const int limit = min(len, len - g.s_q + it.i + 1);
       if (fresh) {
-        // This head's query into TMEM: every MMA of the previous pass has
+        // The warp's 32 heads of the query into TMEM: every MMA of the previous pass has
         // completed (its last scores were read here).  Padding rows are zero.
         const int64_t n = (int64_t)b * g.s_q + it.i;
-        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(g.q) + n * g.q_row_stride +
-                                                        (int64_t)h * g.q_head_stride);
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(g.q) + n * g.q_row_stride +
+                                 (int64_t)(32 * quarter + (lane >> 2)) * g.q_head_stride + 4 * (lane & 3);
         lse2 = real ? a.lse[n * g.heads + h] * 1.4426950408889634f : 0.f;
 #pragma unroll
-        for (int c = 0; c < BOXES; c += kQueryBoxes) {
-          uint4 qv[8 * kQueryBoxes];   // these loads are in flight together
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
-          for (int v = 0; v < 8 * kQueryBoxes; ++v)
-            qv[v] = real && 8 * c + v < 8 * BOXES ? __ldg(q + 8 * c + v) : make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < BOXES; c += kQueryBoxes) {
+            uint32_t r[kQueryBoxes][16];   // these loads are in flight together
 #pragma unroll
-          for (int d = 0; d < kQueryBoxes; ++d) {
-            if (c + d >= BOXES) break;
-            uint32_t r[32];
+            for (int d = 0; d < kQueryBoxes && c + d < BOXES; ++d)
+              load_rows_16x256b<4>(q + (int64_t)(16 * half) * g.q_head_stride + 64 * (c + d), g.q_head_stride, real, r[d]);
 #pragma unroll
-            for (int v = 0; v < 8; ++v)
-              r[4 * v] = qv[8 * d + v].x, r[4 * v + 1] = qv[8 * d + v].y, r[4 * v + 2] = qv[8 * d + v].z,
-              r[4 * v + 3] = qv[8 * d + v].w;
-            if constexpr (kQ8) {
-              if (c + d < 8) {
+            for (int d = 0; d < kQueryBoxes && c + d < BOXES; ++d) {
+              if constexpr (kQ8) {
+                if (c + d < 8) {
 #pragma unroll
-                for (int v = 0; v < 32; ++v) r[v] = bf16x2_to_f16x2(r[v]);
+                  for (int v = 0; v < 16; ++v) r[d][v] = bf16x2_to_f16x2(r[d][v]);
+                }
               }
+              tmem_st_16x256b_x4(tmem + TM_Q + (c + d) * 32 + lane_off + ((uint32_t)(16 * half) << 16), r[d]);
             }
-            tmem_st32(tmem + TM_Q + (c + d) * 32 + lane_off, r);
           }
-        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();

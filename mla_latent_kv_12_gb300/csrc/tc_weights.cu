@@ -15,13 +15,14 @@
 //    stay in L2, once per token: the weights of a key are always updated by
 //    the same thread, in token order (no atomics, the same bits every time).
 //  * bf16 cache: warp 0 loads [64 keys x 576] tiles by TMA into a three-stage
-//    ring (nine boxes of 64 dims, 128-byte swizzle).  8-bit cache: warps 6..13
-//    fetch codes and write their fp16 values into the same layout
+//    ring (nine boxes of 64 dims, 128-byte swizzle).  8-bit cache: warps
+//    10..17 fetch codes and write their fp16 values into the same layout
 //    (q8_tiles.cuh); the latent part of the query is converted to fp16 too.
-//  * Warp 1 issues the 36 MMAs of a tile.  Warps 2..5 (one thread per head)
-//    load each token's query into TMEM, turn scores into probabilities and
-//    sum them over their 32 heads with a shuffle tree that halves the keys per
-//    lane at every step; the four warps' sums meet in shared memory.
+//  * Warp 1 issues the 36 MMAs of a tile.  Warps 2..9 load each token's query
+//    into TMEM; two groups of four (one thread per head) take the tiles in
+//    turn, turn scores into probabilities and sum them over a warp's 32 heads
+//    with a shuffle tree that halves the keys per lane at every step; the four
+//    warps' sums meet in shared memory.
 #include <cuda_bf16.h>
 
 #include "mla_internal.h"
@@ -40,8 +41,9 @@ constexpr int BOXES = 9;                  // 8 of latent dims, 1 of rope dims
 constexpr int STAGE_BYTES = BOXES * BOX_BYTES;
 constexpr int STAGES = 3, STAGES_Q8 = 2;   // 8-bit: the third stage's memory holds the fetch's slots
 constexpr uint32_t TM_Q = 0, TM_S = 288;  // TMEM columns
-constexpr int kThreads = 192, kThreadsQ8 = 448;
-constexpr int kConvertWarp = 6, kConvertWarps = 8, kConvertThreads = 32 * kConvertWarps;
+constexpr int kSumWarp = 2, kSumGroups = 2;   // two groups of four warps
+constexpr int kConvertWarp = kSumWarp + 4 * kSumGroups, kConvertWarps = 8, kConvertThreads = 32 * kConvertWarps;
+constexpr int kThreads = 32 * kConvertWarp, kThreadsQ8 = kThreads + kConvertThreads;
 using WeightFetch = Q8Fetch<32, kConvertThreads>;
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES, SMEM_BYTES_Q8 = STAGES_Q8 * STAGE_BYTES + 2 * WeightFetch::kSlotBytes;
 constexpr long long kWaitLimit = 1LL << 32;   // clock cycles (~2 s)
@@ -127,7 +129,7 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
   __shared__ uint32_t tmem_base_s;
   __shared__ volatile int abort_s;
   __shared__ int first_row_s, first_tile_s, count_s;
-  __shared__ __align__(16) float part_s[2][4][BN];   // stored as float2
+  __shared__ float part_s[kSumGroups][4][BN];
   const DecodeGeometry& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -144,7 +146,7 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
       mbar_init(&s_full[k], 1);
       mbar_init(&s_free[k], 4);
     }
-    mbar_init(&q_full, 4);
+    mbar_init(&q_full, 4 * kSumGroups);
     mbar_init(&drain, 1);
     abort_s = 0;
     fence_mbar_init();
@@ -330,62 +332,69 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
     if (lane == 0) mma_commit(&drain);   // every MMA completes before TMEM is released
     __syncwarp();
     mbar_wait_warp(&drain, 0, kWaitLimit);
-  } else if (warp >= 2 && warp < 6) {
+  } else if (warp >= kSumWarp && warp < kConvertWarp) {
     // ============================================================ probabilities and sums
-    const int quarter = warp & 3;
+    const int group = (warp - kSumWarp) >> 2, quarter = warp & 3;
     const int h = 32 * quarter + lane;
     const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
     const bool real = h < g.heads;
-    const int k_mine = threadIdx.x - 64;      // key of the tile whose weight this thread updates (warps 2, 3)
-    constexpr int kQueryBoxes = kQ8 ? 5 : 9;   // (the registers of a thread: 128 and 254)
+    const int k_mine = threadIdx.x - 32 * (kSumWarp + 4 * group);   // key of a tile whose weight this thread updates (first two warps)
+    constexpr int kQueryBoxes = kQ8 ? 3 : 5;   // (the registers of a thread: 96 and 168)
     uint32_t tile = 0;
     float lse2 = 0.f;
-    // The four warps meet in a barrier at every tile, so they leave together.
-    bool stop = false;
+    // A group's warps meet in barriers at every pass and tile, so they leave together.
+    bool stop = false, arrived = true;
+    auto leave = [&]() -> bool {
+      stop = named_sync_or(1 + group, 128, !arrived || abort_s != 0);
+      if (stop && !arrived) fail();
+      return stop;
+    };
     while (!stop && it.next(g, fresh)) {
       const int b = it.b, len = g.kv_len[b];
       const int64_t start = g.kv_start ? g.kv_start[b] : 0;
       const int limit = min(len, len - g.s_q + it.i + 1);
       if (fresh) {
-        // The warp's 32 heads of the query into TMEM: every MMA of the previous pass has
-        // completed (its last scores were read here).  Padding rows are zero.
+        // The query into TMEM, of each warp's 32 heads 16 by either group.
+        // Padding rows are zero.
         const int64_t n = (int64_t)b * g.s_q + it.i;
         const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(g.q) + n * g.q_row_stride +
-                                 (int64_t)(32 * quarter + (lane >> 2)) * g.q_head_stride + 4 * (lane & 3);
+                                 (int64_t)(32 * quarter + 16 * group + (lane >> 2)) * g.q_head_stride + 4 * (lane & 3);
         lse2 = real ? a.lse[n * g.heads + h] * 1.4426950408889634f : 0.f;
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+        for (int c = 0; c < BOXES; c += kQueryBoxes) {
+          uint32_t r[kQueryBoxes][16];   // these loads are in flight together
 #pragma unroll
-          for (int c = 0; c < BOXES; c += kQueryBoxes) {
-            uint32_t r[kQueryBoxes][16];   // these loads are in flight together
-#pragma unroll
-            for (int d = 0; d < kQueryBoxes && c + d < BOXES; ++d)
-              load_rows_16x256b<4>(q + (int64_t)(16 * half) * g.q_head_stride + 64 * (c + d), g.q_head_stride, real, r[d]);
-#pragma unroll
-            for (int d = 0; d < kQueryBoxes && c + d < BOXES; ++d) {
-              if constexpr (kQ8) {
-                if (c + d < 8) {
-#pragma unroll
-                  for (int v = 0; v < 16; ++v) r[d][v] = bf16x2_to_f16x2(r[d][v]);
-                }
-              }
-              tmem_st_16x256b_x4(tmem + TM_Q + (c + d) * 32 + lane_off + ((uint32_t)(16 * half) << 16), r[d]);
-            }
+          for (int d = 0; d < kQueryBoxes && c + d < BOXES; ++d)
+            load_rows_16x256b<4>(q + 64 * (c + d), g.q_head_stride, real, r[d]);
+          if (c == 0) {
+            // every MMA of the previous passes has completed once its last scores are there
+            if (tile > 0) arrived = mbar_wait_warp(&s_full[(tile - 1) & 1u], ((tile - 1) >> 1) & 1u, kWaitLimit);
+            if (leave()) break;
+            tc_fence_after();
           }
+#pragma unroll
+          for (int d = 0; d < kQueryBoxes && c + d < BOXES; ++d) {
+            if constexpr (kQ8) {
+              if (c + d < 8) {
+#pragma unroll
+                for (int v = 0; v < 16; ++v) r[d][v] = bf16x2_to_f16x2(r[d][v]);
+              }
+            }
+            tmem_st_16x256b_x4(tmem + TM_Q + (c + d) * 32 + lane_off + ((uint32_t)(16 * group) << 16), r[d]);
+          }
+        }
+        if (stop) break;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full);
         // The queries that the next passes may need, into L2: the row's next
-        // token, and the next row's first one.
-        if (real) {
-          const int64_t next = it.i + 1 < g.s_q ? n + 1 : (int64_t)b * g.s_q, row = (int64_t)(b + 1) * g.s_q;
+        // token (one group), and the next row's first one (the other).
+        const int64_t ahead = group == 0 ? (it.i + 1 < g.s_q ? n + 1 : (int64_t)b * g.s_q) : (int64_t)(b + 1) * g.s_q;
+        if (real && (group == 0 || (b + 1 < g.batch && it.left > 0))) {
 #pragma unroll
-          for (int l = 0; l < BOXES; ++l) {
-            prefetch_l2(static_cast<const __nv_bfloat16*>(g.q) + next * g.q_row_stride + (int64_t)h * g.q_head_stride + 64 * l);
-            if (b + 1 < g.batch && it.left > 0)
-              prefetch_l2(static_cast<const __nv_bfloat16*>(g.q) + row * g.q_row_stride + (int64_t)h * g.q_head_stride + 64 * l);
-          }
+          for (int l = 0; l < BOXES; ++l)
+            prefetch_l2(static_cast<const __nv_bfloat16*>(g.q) + ahead * g.q_row_stride + (int64_t)h * g.q_head_stride + 64 * l);
         }
       }
       float* w_row = a.weights + b * a.weights_batch_stride + start;
@@ -399,53 +408,57 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
         const int key = t * BN + k_mine;
         return t < it.t1 && k_mine < BN && key < kept_keys ? w_row[key] : 0.f;
       };
-      float old_next = weight_of(it.t0);
-      for (int t = it.t0; t < it.t1; ++t, ++tile) {
-        const uint32_t buf = tile & 1u;
+      // Group t % 2 takes tile t of a row in every token's pass: a weight has one owner.
+      const int first = it.t0 + ((it.t0 ^ group) & 1);
+      float old_next = weight_of(first);
+      const uint32_t tile0 = tile;
+      tile += it.t1 - it.t0;
+      for (int t = first; t < it.t1; t += kSumGroups) {
+        const uint32_t my_tile = tile0 + (t - it.t0), buf = my_tile & 1u;
         const int key = t * BN + k_mine;
         const float old = old_next;
-        old_next = weight_of(t + 1);
+        old_next = weight_of(t + kSumGroups);
         if (k_mine < BN && (k_mine & 31) == 0 && key + kWeightsAhead * BN < len) prefetch_l2(w_row + key + kWeightsAhead * BN);
-        const bool arrived = mbar_wait_warp(&s_full[buf], (tile >> 1) & 1u, kWaitLimit);
+        arrived = mbar_wait_warp(&s_full[buf], (my_tile >> 1) & 1u, kWaitLimit);
         tc_fence_after();
-        uint32_t s0[32], s1[32];
-        tmem_ld32(tmem + TM_S + buf * BN + lane_off, s0);
-        tmem_ld32(tmem + TM_S + buf * BN + 32 + lane_off, s1);
+        uint32_t s[2][32];
+        tmem_ld32(tmem + TM_S + buf * BN + lane_off, s[0]);
+        tmem_ld32(tmem + TM_S + buf * BN + 32 + lane_off, s[1]);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_free[buf]);
-        float p[BN];
+        float sum[2];
 #pragma unroll
-        for (int k = 0; k < BN; ++k)
-          p[k] = ex2_approx(fmaf(__uint_as_float(k < 32 ? s0[k] : s1[k - 32]), g.scale_log2, -lse2));
-        if ((t + 1) * BN > limit) {
-          // keys that this token does not see, and rows past the window (which may hold anything)
+        for (int k2 = 0; k2 < 2; ++k2) {
+          float p[32];
 #pragma unroll
-          for (int k = 0; k < BN; ++k) p[k] = t * BN + k < limit ? p[k] : 0.f;
-        }
-        // Sum over the warp's heads: each step halves the keys a lane holds.
-        // Lane l ends with keys 2l and 2l + 1.
+          for (int k = 0; k < 32; ++k) p[k] = ex2_approx(fmaf(__uint_as_float(s[k2][k]), g.scale_log2, -lse2));
+          if ((t + 1) * BN > limit) {
+            // keys that this token does not see, and rows past the window (which may hold anything)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          const bool upper = (lane & o) != 0;
-#pragma unroll
-          for (int k = 0; k < 2 * o; ++k) {
-            const float keep = upper ? p[k + 2 * o] : p[k], send = upper ? p[k] : p[k + 2 * o];
-            p[k] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            for (int k = 0; k < 32; ++k) p[k] = t * BN + 32 * k2 + k < limit ? p[k] : 0.f;
           }
+          // Sum over the warp's heads: each step halves the keys a lane holds.
+          // Lane l ends with key 32 k2 + l.
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            const bool upper = (lane & o) != 0;
+#pragma unroll
+            for (int k = 0; k < o; ++k) {
+              const float keep = upper ? p[k + o] : p[k], send = upper ? p[k] : p[k + o];
+              p[k] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            }
+          }
+          sum[k2] = real ? p[0] : 0.f;   // (64 heads: quarters 2 and 3 hold padding rows only)
         }
-        // (64 heads: quarters 2 and 3 hold padding rows only)
-        *reinterpret_cast<float2*>(&part_s[buf][quarter][2 * lane]) = real ? make_float2(p[0], p[1]) : make_float2(0.f, 0.f);
-        // (a buffer is rewritten two tiles later, behind the next tile's barrier)
-        stop = named_sync_or(1, 128, !arrived || abort_s != 0);
-        if (stop) {
-          if (!arrived) fail();
-          break;
-        }
+        named_sync(1 + kSumGroups + group, 128);   // the previous tile's sums have been read
+        part_s[group][quarter][lane] = sum[0];
+        part_s[group][quarter][32 + lane] = sum[1];
+        if (leave()) break;
         if (k_mine < BN && key < len)
-          w_row[key] = factor * old + ((part_s[buf][0][k_mine] + part_s[buf][1][k_mine]) +
-                              (part_s[buf][2][k_mine] + part_s[buf][3][k_mine]));
+          w_row[key] = factor * old + ((part_s[group][0][k_mine] + part_s[group][1][k_mine]) +
+                                       (part_s[group][2][k_mine] + part_s[group][3][k_mine]));
       }
     }
   }

@@ -111,7 +111,7 @@ struct Q8Fetch {
   __device__ __forceinline__ void copy_rope(int s, uint32_t rope) const {
 #pragma unroll
     for (int j = 0; j < kRopeIters; ++j)
-      st_shared_16(rope + 4 * j * kStep * kRow, ld_shared_16(slot0 + s * kSlotBytes + (kIters + j) * kPieceBytes));
+      st_shared_16(rope + 4 * j * kStep * kRow, tc::ld_shared_16(slot0 + s * kSlotBytes + (kIters + j) * kPieceBytes));
   }
   // Slot s as fp16 values: this lane's first eight dims at shared address `box`,
   // the others kBox bytes behind, rows 128 bytes apart.  `exponent` from
@@ -136,11 +136,6 @@ struct Q8Fetch {
   static __device__ __forceinline__ uint2 ld_shared_8(uint32_t a) {
     uint2 v;
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-    return v;
-  }
-  static __device__ __forceinline__ uint4 ld_shared_16(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
     return v;
   }
   static __device__ __forceinline__ void st_shared_16(uint32_t a, uint4 v) {

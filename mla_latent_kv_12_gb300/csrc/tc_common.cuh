@@ -102,6 +102,12 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, l
 }
 
 
+// 16-byte shared-memory load.
+__device__ __forceinline__ uint4 ld_shared_16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
 // Arrive on the local barrier and raise its expected transaction bytes.
 __device__ __forceinline__ void mbar_arrive_expect_tx_u32(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
@@ -427,33 +433,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
         "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
-}
-
-// Stores of 16 lanes (from the address's lane on, 0 or 16 of the warp's quarter)
-// by 256-bit column groups: of group j, thread t holds the 32-bit columns 2 (t
-// % 4) and 2 (t % 4) + 1 of lane t / 4 in r[4j], r[4j + 1], and those of lane t
-// / 4 + 8 in r[4j + 2], r[4j + 3].
-__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-// 16 kGroups bf16 dims of 16 rows in that layout: `p` is row lane / 4, dim 4
-// (lane % 4), `stride` the elements between rows.  A load covers 32 whole bytes
-// of eight rows.  (A thread that loads its own row, 16 bytes of 32 rows per
-// load, is bound by the cache's line lookups.)
-template <int kGroups>
-__device__ __forceinline__ void load_rows_16x256b(const __nv_bfloat16* p, int64_t stride, bool real, uint32_t (&r)[4 * kGroups]) {
-#pragma unroll
-  for (int j = 0; j < kGroups; ++j)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint2 v = real ? __ldg(reinterpret_cast<const uint2*>(p + 8 * k * stride + 16 * j)) : make_uint2(0, 0);
-      r[4 * j + 2 * k] = v.x;
-      r[4 * j + 2 * k + 1] = v.y;
-    }
 }
 
 // ------------------------------------------------------------------ descriptors

@@ -61,7 +61,7 @@ struct WeightArgs {
   int64_t weights_batch_stride;
   float decay;
   int32_t n_new;
-  int32_t batch_in_map;
+  int32_t batch_in_map, rows_in_map;   // whether the cache's batch axis and the query's row axis are mapped
 };
 
 __device__ __forceinline__ int window_tiles(const DecodeGeometry& g, int b, bool flag) {
@@ -116,8 +116,8 @@ struct Passes {
 
 template <bool kQ8>
 __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
-    tc_key_weights_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_constant__ CUtensorMap rope_map,
-                          const __grid_constant__ WeightArgs a) {
+    tc_key_weights_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap lat_map,
+                          const __grid_constant__ CUtensorMap rope_map, const __grid_constant__ WeightArgs a) {
   constexpr int kStages = kQ8 ? STAGES_Q8 : STAGES;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if ((smem_u32(smem_raw) & 1023u) != 0) {   // the same in every CTA: nothing waits on anything yet
@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+    tma_prefetch_desc(&q_map);
     if constexpr (!kQ8) {
       tma_prefetch_desc(&lat_map);
       tma_prefetch_desc(&rope_map);
@@ -196,6 +197,13 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
     abort_s = 1;
     if (g.device_status) atomicOr(g.device_status, MLA_DEVICE_TIMEOUT);
   };
+  // One half (64 heads) of a pass's query into a stage: the boxes of a tile.
+  auto load_query = [&](int stage, int row, int half) {
+    mbar_arrive_expect_tx(&full_bar[stage], STAGE_BYTES);
+    for (int c = 0; c < BOXES; ++c)
+      tma_load_3d(stages + stage * STAGE_BYTES + c * BOX_BYTES, &q_map, &full_bar[stage], 64 * c, 64 * half,
+                  a.rows_in_map ? row : 0);
+  };
   Passes it;
   it.init(count_s > 0 ? first_row_s : 0, count_s > 0 ? first_tile_s : 0, count_s, g);
   bool fresh;
@@ -207,8 +215,17 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
     while (!aborted() && it.next(g, fresh)) {
       const int start = g.kv_start ? g.kv_start[it.b] : 0;
       const int z = a.batch_in_map ? it.b : 0;
-      for (int t = it.t0; t < it.t1; ++t) {
-        if (fills++ >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
+      bool ok = true;
+      for (int half = 0; fresh && ok && half < 2; ++half) {
+        if (fills >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); ok = false; break; }
+        ++fills;
+        if (lane == 0) load_query(stage, it.b * g.s_q + it.i, half);
+        __syncwarp();
+        if (++stage == kStages) stage = 0, phase ^= 1u;
+      }
+      for (int t = it.t0; ok && t < it.t1; ++t) {
+        if (fills >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
+        ++fills;   // (counts what was issued)
         if (lane == 0) {
           mbar_arrive_expect_tx(&full_bar[stage], STAGE_BYTES);
           uint8_t* st = stages + stage * STAGE_BYTES;
@@ -265,9 +282,20 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
       int e_next = fetch.my_exponent(rows, pos);
       if (t0 + 1 < t1) issue(t0 + 1, 1, pos);
       cp_async_commit();
-      for (int t = t0; t < t1; ++t) {
+      bool ok = true;
+      for (int half = 0; fresh && ok && half < 2; ++half) {
+        if (fills >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); ok = false; break; }
+        ++fills;
+        if (lane == 0) {
+          if (cw == 0) load_query(stage, b * g.s_q + it.i, half); else mbar_arrive(&full_bar[stage]);
+        }
+        __syncwarp();
+        if (++stage == kStages) stage = 0, phase ^= 1u;
+      }
+      for (int t = t0; ok && t < t1; ++t) {
         const int slot = (t - t0) & 1;
-        if (fills++ >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
+        if (fills >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
+        ++fills;
         cp_async_wait<1>();   // this tile's pieces
         const uint32_t off = stage * STAGE_BYTES;
         fetch.check_exponent(rows.status, e_now);
@@ -302,13 +330,23 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
       }
       cp_async_wait<0>();   // the slots are free for the next pass
     }
+    // (query loads land before this CTA may exit)
+    for (int k = fills > kStages ? fills - kStages : 0; k < fills; ++k)
+      mbar_wait_warp(&full_bar[k % kStages], (uint32_t)(k / kStages) & 1u, kWaitLimit);
   } else if (warp == 1) {
     // ============================================================ MMA issuer
     const uint32_t idesc_rope = idesc_bf16_f32(128, BN, 0, 0), idesc = kQ8 ? idesc_f16_f32(128, BN, 0, 0) : idesc_rope;
     int stage = 0;
     uint32_t phase = 0, tile = 0, queries = 0;
     while (!aborted() && it.next(g, fresh)) {
-      if (fresh && !mbar_wait_warp(&q_full, queries++ & 1u, kWaitLimit)) { fail(); break; }
+      if (fresh) {
+        if (!mbar_wait_warp(&q_full, queries++ & 1u, kWaitLimit)) { fail(); break; }
+        for (int half = 0; half < 2; ++half) {   // the query's stages have been read
+          if (lane == 0) mbar_arrive(&empty_bar[stage]);
+          if (++stage == kStages) stage = 0, phase ^= 1u;
+        }
+        __syncwarp();
+      }
       for (int t = it.t0; t < it.t1; ++t, ++tile) {
         const uint32_t buf = tile & 1u;
         if (tile >= 2 && !mbar_wait_warp(&s_free[buf], ((tile >> 1) - 1) & 1u, kWaitLimit)) { fail(); break; }
@@ -339,8 +377,7 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
     const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
     const bool real = h < g.heads;
     const int k_mine = threadIdx.x - 32 * (kSumWarp + 4 * group);   // key of a tile whose weight this thread updates (first two warps)
-    constexpr int kQueryBoxes = kQ8 ? 3 : 5;   // (the registers of a thread: 96 and 168)
-    uint32_t tile = 0;
+    uint32_t tile = 0, fill = 0;   // tiles and ring fills of all passes so far
     float lse2 = 0.f;
     // A group's warps meet in barriers at every pass and tile, so they leave together.
     bool stop = false, arrived = true;
@@ -354,48 +391,34 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
       const int64_t start = g.kv_start ? g.kv_start[b] : 0;
       const int limit = min(len, len - g.s_q + it.i + 1);
       if (fresh) {
-        // The query into TMEM, of each warp's 32 heads 16 by either group.
-        // Padding rows are zero.
-        const int64_t n = (int64_t)b * g.s_q + it.i;
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(g.q) + n * g.q_row_stride +
-                                 (int64_t)(32 * quarter + 16 * group + (lane >> 2)) * g.q_head_stride + 4 * (lane & 3);
-        lse2 = real ? a.lse[n * g.heads + h] * 1.4426950408889634f : 0.f;
+        // The query into TMEM, a head per thread, every other box by either
+        // group (rows of padding heads arrive as zeros).  Every MMA of the
+        // previous passes has completed once its last scores are there.
+        lse2 = real ? a.lse[((int64_t)b * g.s_q + it.i) * g.heads + h] * 1.4426950408889634f : 0.f;
+        const uint32_t k = fill + (quarter >> 1);
+        arrived = tile == 0 || mbar_wait_warp(&s_full[(tile - 1) & 1u], ((tile - 1) >> 1) & 1u, kWaitLimit);
+        arrived = mbar_wait_warp(&full_bar[k % kStages], (k / kStages) & 1u, kWaitLimit) && arrived;
+        if (leave()) break;
+        tc_fence_after();
+        const uint32_t row = smem_u32(stages) + (k % kStages) * STAGE_BYTES + (h & 63) * 128;
+        for (int c = group; c < BOXES; c += kSumGroups) {
+          uint32_t r[32];
 #pragma unroll
-        for (int c = 0; c < BOXES; c += kQueryBoxes) {
-          uint32_t r[kQueryBoxes][16];   // these loads are in flight together
-#pragma unroll
-          for (int d = 0; d < kQueryBoxes && c + d < BOXES; ++d)
-            load_rows_16x256b<4>(q + 64 * (c + d), g.q_head_stride, real, r[d]);
-          if (c == 0) {
-            // every MMA of the previous passes has completed once its last scores are there
-            if (tile > 0) arrived = mbar_wait_warp(&s_full[(tile - 1) & 1u], ((tile - 1) >> 1) & 1u, kWaitLimit);
-            if (leave()) break;
-            tc_fence_after();
+          for (int v = 0; v < 8; ++v) {
+            const uint4 x = ld_shared_16(row + c * BOX_BYTES + ((v ^ (h & 7)) << 4));
+            r[4 * v] = x.x, r[4 * v + 1] = x.y, r[4 * v + 2] = x.z, r[4 * v + 3] = x.w;
           }
+          if (kQ8 && c < 8) {
 #pragma unroll
-          for (int d = 0; d < kQueryBoxes && c + d < BOXES; ++d) {
-            if constexpr (kQ8) {
-              if (c + d < 8) {
-#pragma unroll
-                for (int v = 0; v < 16; ++v) r[d][v] = bf16x2_to_f16x2(r[d][v]);
-              }
-            }
-            tmem_st_16x256b_x4(tmem + TM_Q + (c + d) * 32 + lane_off + ((uint32_t)(16 * group) << 16), r[d]);
+            for (int v = 0; v < 32; ++v) r[v] = bf16x2_to_f16x2(r[v]);
           }
+          tmem_st32(tmem + TM_Q + c * 32 + lane_off, r);
         }
-        if (stop) break;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full);
-        // The queries that the next passes may need, into L2: the row's next
-        // token (one group), and the next row's first one (the other).
-        const int64_t ahead = group == 0 ? (it.i + 1 < g.s_q ? n + 1 : (int64_t)b * g.s_q) : (int64_t)(b + 1) * g.s_q;
-        if (real && (group == 0 || (b + 1 < g.batch && it.left > 0))) {
-#pragma unroll
-          for (int l = 0; l < BOXES; ++l)
-            prefetch_l2(static_cast<const __nv_bfloat16*>(g.q) + ahead * g.q_row_stride + (int64_t)h * g.q_head_stride + 64 * l);
-        }
+        fill += 2;
       }
       float* w_row = a.weights + b * a.weights_batch_stride + start;
       // The weight so far of this thread's key of tile t, read a tile ahead of
@@ -413,6 +436,7 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
       float old_next = weight_of(first);
       const uint32_t tile0 = tile;
       tile += it.t1 - it.t0;
+      fill += it.t1 - it.t0;
       for (int t = first; t < it.t1; t += kSumGroups) {
         const uint32_t my_tile = tile0 + (t - it.t0), buf = my_tile & 1u;
         const int key = t * BN + k_mine;
@@ -486,7 +510,13 @@ cudaError_t launch_tc_key_weights(const KeyWeightParams& p, cudaStream_t stream)
   const DecodeGeometry& g = p.g;
   a.batch_in_map = (g.latent_batch_stride != 0 || g.rope_batch_stride != 0) ? 1 : 0;
   const bool q8 = g.codes != nullptr;
-  CUtensorMap lat_map = {}, rope_map = {};
+  CUtensorMap q_map, lat_map = {}, rope_map = {};
+  const uint32_t q_box[3] = {64, 64, 1};
+  a.rows_in_map = g.q_row_stride != 0;
+  const uint64_t q_rows = a.rows_in_map ? (uint64_t)g.batch * g.s_q : 1;
+  const uint64_t qd[3] = {(uint64_t)(g.rank + g.rope_dim), (uint64_t)g.heads, q_rows};
+  const uint64_t qs[2] = {(uint64_t)g.q_head_stride * 2, (uint64_t)(a.rows_in_map ? g.q_row_stride : g.heads * g.q_head_stride) * 2};
+  if (!encode_tmap_bf16(&q_map, g.q, 3, qd, qs, q_box)) return cudaErrorInvalidValue;
   if (!q8) {
     const uint64_t bmap = a.batch_in_map ? (uint64_t)g.batch : 1;
     const uint32_t box[3] = {64, BN, 1};
@@ -504,7 +534,7 @@ cudaError_t launch_tc_key_weights(const KeyWeightParams& p, cudaStream_t stream)
   const cudaError_t ea = set_max_dynamic_smem(kernel, smem);
   if (ea != cudaSuccess) return ea;
   const cudaError_t e = launch_pdl(kernel, dim3((unsigned)device_sm_count()), dim3(q8 ? kThreadsQ8 : kThreads), smem,
-                                   stream, lat_map, rope_map, a);
+                                   stream, q_map, lat_map, rope_map, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

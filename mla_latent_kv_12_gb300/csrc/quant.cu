@@ -132,17 +132,44 @@ __device__ __forceinline__ int block_exponent(const EncodeParams& p, const Encod
 }
 
 // The rope key of new token t, pairs from `lane` on (every 32nd): rotated at its position, into buffer row `row`.
+// (`freq`: the inverse frequencies in shared memory; lanes that index the
+// parameters' constant bank apart are served one by one.)
 template <typename TI, typename TR>
-__device__ __forceinline__ void append_rope(const EncodeParams& p, int b, int64_t t, int64_t row, int64_t pos, int lane) {
+__device__ __forceinline__ void append_rope(const EncodeParams& p, const float* freq, int b, int64_t t, int64_t row,
+                                            int64_t pos, int lane) {
   const TI* rr = static_cast<const TI*>(p.rope_raw) + b * p.rr_row_stride + t * p.rr_tok_stride;
   TR* dr = static_cast<TR*>(p.rope) + b * p.rope_batch_stride + row * p.rope_row_stride;
   const int half = p.rope_dim >> 1;
   for (int j = lane; j < half; j += 32) {
     float re, im;
-    rope_rotate_pair(to_f(rr[2 * j]), to_f(rr[2 * j + 1]), pos, p.inv_freq[j], re, im);
+    rope_rotate_pair(to_f(rr[2 * j]), to_f(rr[2 * j + 1]), pos, freq[j], re, im);
     put(dr + j, re);
     put(dr + half + j, im);
   }
+}
+
+// Sine and cosine of |x| <= kSmallAngle without branches: x less the nearest
+// multiple of pi / 2, which is subtracted in three f32 parts with fused
+// multiply-adds (Cody and Waite; the first is exact: x and the multiple are both
+// multiples of 2^-24, their difference is below 1), then the Taylor sums, whose
+// remainders on [-pi/4, pi/4] are below 2^-28.  Absolute error below 1.2 * 2^-24
+// (against 64 bits over the range and next to the multiples of pi / 2).
+constexpr float kSmallAngle = 65536.f;
+__device__ __forceinline__ void sincos_small(float x, float& sine, float& cosine) {
+  const float shifted = fmaf(x, 0.6366197723675814f, 12582912.f);   // 1.5 * 2^23: the low bits are the nearest integer
+  const uint32_t quadrant = __float_as_uint(shifted);
+  const float k = shifted - 12582912.f;
+  float r = fmaf(-k, 0x1.921fb6p+0f, x);
+  r = fmaf(-k, -0x1.777a5cp-25f, r);
+  r = fmaf(-k, -0x1.ee59dap-50f, r);
+  const float z = r * r;
+  float s = fmaf(fmaf(fmaf(1.f / 362880, z, -1.f / 5040), z, 1.f / 120), z, -1.f / 6);
+  s = fmaf(r * z, s, r);
+  float c = fmaf(fmaf(fmaf(-1.f / 3628800, z, 1.f / 40320), z, -1.f / 720), z, 1.f / 24);
+  c = fmaf(fmaf(c, z, -0.5f), z, 1.f);
+  const bool swap = quadrant & 1u;
+  sine = __uint_as_float(__float_as_uint(swap ? c : s) ^ ((quadrant & 2u) << 30));
+  cosine = __uint_as_float(__float_as_uint(swap ? s : c) ^ (((quadrant + 1u) & 2u) << 30));
 }
 
 // The codes of rows [first, lo), which a block held before, move from unit `old` to unit `e`.
@@ -204,6 +231,7 @@ __global__ void __launch_bounds__(kHeldWarps * 32, sizeof(TI) == 2 ? 2 : 1) enco
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ uint32_t amax_s[kHeldTile];   // per block of the tile, f32 bits (non-negative: ordered as integers)
   __shared__ int exp_s[kHeldTile], old_s;
+  __shared__ float freq_s[kNorm ? kMaxRotaryDims / 2 : 1];
   const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const EncodeRow<kNorm> row(p, b, blockIdx.x == 0 && threadIdx.x == 0);
   uint8_t* codes = p.codes + b * p.codes_batch_stride;
@@ -214,6 +242,9 @@ __global__ void __launch_bounds__(kHeldWarps * 32, sizeof(TI) == 2 ? 2 : 1) enco
   const bool warp_blocks = block <= kHeldRows;   // no block spans warps
   const int64_t n_tiles = row.tiles(kHeldTile);
   const int half = p.rope_dim >> 1;
+  if constexpr (kNorm) {
+    if ((int)threadIdx.x < half) freq_s[threadIdx.x] = p.inv_freq[threadIdx.x];   // (read behind the tile's barriers)
+  }
   bool live[2];
 #pragma unroll
   for (int c = 0; c < 2; ++c) live[c] = 256 * c + 8 * lane < p.rank;
@@ -245,9 +276,42 @@ __global__ void __launch_bounds__(kHeldWarps * 32, sizeof(TI) == 2 ? 2 : 1) enco
       for (int c = 0; c < 2; ++c)
         if (live[c]) g[c].load(gain + 256 * c + 8 * lane);
     }
-    if (!warp_blocks) {
+    if (!warp_blocks)
       for (int k = threadIdx.x; k < n_blocks; k += kHeldWarps * 32) amax_s[k] = 0;
-      __syncthreads();
+    if (kNorm || !warp_blocks) __syncthreads();
+    // The rope keys first: their sines and cosines while the latents arrive.
+    if constexpr (kNorm) {
+      if (lane < half) {
+        const int64_t pos = row.pos0 + (base + r0 - row.lo);   // of the warp's first row
+        const float freq = freq_s[lane];
+        float sine[kHeldRows], cosine[kHeldRows], top = 0.f;
+#pragma unroll
+        for (int k = 0; k < kHeldRows; ++k) {
+          // (the angle of rope_angle; sine holds it first)
+          sine[k] = row.pos0 + p.s_new <= (1 << 24) ? __fmul_rn((float)(int)(pos + k), freq) : rope_angle(pos + k, freq);
+          top = fmaxf(top, fabsf(sine[k]));
+        }
+        if (top <= kSmallAngle) {
+#pragma unroll
+          for (int k = 0; k < kHeldRows; ++k) sincos_small(sine[k], sine[k], cosine[k]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < kHeldRows; ++k) sincosf(sine[k], &sine[k], &cosine[k]);
+        }
+        TR* dr = static_cast<TR*>(p.rope) + b * p.rope_batch_stride + (base + r0) * p.rope_row_stride + lane;
+#pragma unroll
+        for (int k = 0; k < kHeldRows; ++k, dr += p.rope_row_stride) {
+          if (!mine(k)) continue;
+          put(dr, ra[k] * cosine[k] - rb[k] * sine[k]);
+          put(dr + half, rb[k] * cosine[k] + ra[k] * sine[k]);
+        }
+      }
+      if (half > 32) {   // wider rope keys
+        for (int k = 0; k < kHeldRows; ++k) {
+          const int64_t t = base + r0 + k - row.lo;
+          if (mine(k)) append_rope<TI, TR>(p, freq_s, b, t, base + r0 + k, row.pos0 + t, lane + 32);
+        }
+      }
     }
     // A token's value is x inv g.  Its largest magnitude is taken as inv
     // max |x g| (half a unit in the last place of the exact one either way, as
@@ -341,19 +405,6 @@ __global__ void __launch_bounds__(kHeldWarps * 32, sizeof(TI) == 2 ? 2 : 1) enco
       }
     }
     if constexpr (kNorm) {
-#pragma unroll
-      for (int k = 0; k < kHeldRows; ++k) {
-        if (!mine(k)) continue;
-        const int64_t t = base + r0 + k - row.lo;
-        if (lane < half) {
-          TR* dr = static_cast<TR*>(p.rope) + b * p.rope_batch_stride + (base + r0 + k) * p.rope_row_stride;
-          float re, im;
-          rope_rotate_pair(ra[k], rb[k], row.pos0 + t, p.inv_freq[lane], re, im);
-          put(dr + lane, re);
-          put(dr + half + lane, im);
-        }
-        append_rope<TI, TR>(p, b, t, base + r0 + k, row.pos0 + t, lane + 32);   // wider rope keys
-      }
       // tokens that the first block held before: their codes move to the larger unit
       __syncthreads();
       const int k0 = r_lo >> p.block_shift, old = old_s, e = exp_s[k0];
@@ -380,9 +431,13 @@ __global__ void __launch_bounds__(kWarps * 32) encode_walk_kernel(const __grid_c
   __shared__ uint32_t amax_s[kMaxScaleBlock];   // per block of the tile, f32 bits (non-negative: ordered as integers)
   __shared__ int exp_s[kMaxScaleBlock], old_exp_s[kMaxScaleBlock];
   __shared__ float inv_s[kMaxScaleBlock];       // per row of the tile
+  __shared__ float freq_s[kNorm ? kMaxRotaryDims / 2 : 1];
   const int b = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const EncodeRow<kNorm> row_of(p, b, blockIdx.x == 0 && threadIdx.x == 0);
+  if constexpr (kNorm) {
+    if ((int)threadIdx.x < p.rope_dim >> 1) freq_s[threadIdx.x] = p.inv_freq[threadIdx.x];   // (read behind the tile's barriers)
+  }
   const int64_t lo = row_of.lo, hi = row_of.hi;
   const int block = 1 << p.block_shift;
   const int tile_rows = p.tile_rows;
@@ -460,7 +515,7 @@ __global__ void __launch_bounds__(kWarps * 32) encode_walk_kernel(const __grid_c
         }
       });
       if constexpr (kNorm) {
-        append_rope<TI, TR>(p, b, base + r - lo, base + r, row_of.pos0 + (base + r - lo), lane);
+        append_rope<TI, TR>(p, freq_s, b, base + r - lo, base + r, row_of.pos0 + (base + r - lo), lane);
       }
     }
     if constexpr (kNorm) {

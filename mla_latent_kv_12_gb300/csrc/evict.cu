@@ -5,7 +5,8 @@
 // tokens the n_keep - n_sink - n_recent heaviest stay: their rank key is the
 // order-preserving map of the f32 bits to uint32, complemented (ascending key
 // = descending weight), and a radix selection (digits of 11, 11 and 10 bits)
-// finds the largest kept key and how many of its equals are kept.  Each CTA
+// finds the largest kept key and how many of its equals are kept; it ends
+// early when all keys with the digits so far are kept.  Each CTA
 // holds its slice's keys in shared memory where they fit, so the weights
 // are read once; the digit histograms are summed over the cluster through
 // distributed shared memory, every CTA taking the same digit.  Bound by the latency of
@@ -75,8 +76,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
   extern __shared__ uint32_t keys_s[];   // `held` keys of this CTA's slice
   __shared__ __align__(8) int hist_s[3][kBins];   // one per pass: a peer may still read the previous one
   __shared__ unsigned long long warp_s[kPlanWarps];
-  __shared__ int digit_s, rest_s, less_s, tie_s;
+  __shared__ int digit_s, rest_s, less_s, tie_s, last_s;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // (the compaction's CTAs may take their places already: they wait for this grid's end)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t crank = tc::cluster_ctarank();
   const int ncta = (int)cluster_size();
   const int b = blockIdx.x / ncta;
@@ -89,7 +92,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
       if (p.kv_len_out) p.kv_len_out[b] = len;
       if (!fits && p.status) atomicOr(p.status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     return;
   }
   const float* w = p.weights + b * p.weights_batch_stride + start;
@@ -104,6 +106,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
 
   uint32_t prefix = 0;
   int rest = take;   // the rest-th smallest key among those with the prefix is looked for
+  int drop = 0;      // low key bits that need not be compared
   int peers_less = 0, peers_tie = 0;   // keys below `prefix`, and equal to it, in the earlier CTAs' slices
   if (take > 0) {
     for (int i = threadIdx.x; i < 3 * kBins; i += kPlanThreads) hist_s[0][i] = 0;
@@ -168,6 +171,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
         if (before < rest && rest <= before + h[k]) {   // exactly one thread and bin
           digit_s = b0 + k;
           rest_s = rest - before;
+          last_s = rest - before == h[k];   // all keys with this digit are kept
           less_s = less;
           tie_s = e[k];
         }
@@ -180,6 +184,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
       peers_less += less_s;
       peers_tie = tie_s;
       known += width;
+      drop = 32 - known;
+      if (last_s) break;   // (the same in the whole cluster)
       __syncthreads();   // (read before the next pass writes them)
     }
   }
@@ -194,7 +200,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
 #pragma unroll 4
     for (int i0 = wlo; i0 < whi; i0 += 32) {
       const int i = i0 + lane;
-      const uint32_t key = i < whi ? key_at(i) : 0xFFFFFFFFu;
+      const uint32_t key = i < whi ? key_at(i) >> drop : 0xFFFFFFFFu;
       n_less += __popc(__ballot_sync(0xffffffffu, i < whi && key < prefix));
       n_tie += __popc(__ballot_sync(0xffffffffu, i < whi && key == prefix));
     }
@@ -207,7 +213,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
 #pragma unroll 4
     for (int i0 = wlo; i0 < whi; i0 += 32) {
       const int i = i0 + lane;
-      const uint32_t key = i < whi ? key_at(i) : 0xFFFFFFFFu;
+      const uint32_t key = i < whi ? key_at(i) >> drop : 0xFFFFFFFFu;
       const uint32_t tie = __ballot_sync(0xffffffffu, i < whi && key == prefix);
       const bool stays = i < whi && (key < prefix || (key == prefix && ties + __popc(tie & below) < rest));
       const uint32_t who = __ballot_sync(0xffffffffu, stays);
@@ -225,7 +231,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
     p.counts[b] = p.n_keep;
     if (p.kv_len_out) p.kv_len_out[b] = p.n_keep;
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ compaction

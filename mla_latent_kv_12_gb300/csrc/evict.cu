@@ -130,23 +130,16 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
           if (pass == 0 && in_smem && i < hi) keys_s[i - lo] = key[u];
           const bool counts = i < hi && (pass == 0 || (key[u] >> (32 - known)) == prefix);
           const int digit = (int)((key[u] >> shift) & ((1u << width) - 1u));
-          // Lanes with the digit of the first one that counts add once, and so
-          // do those with the first one's of the others (many weights share a
-          // value, zero above all, and equal addresses are added one by one);
-          // the rest add for themselves.
-          uint32_t who = __ballot_sync(0xffffffffu, counts);
-          bool left = counts;
-#pragma unroll
-          for (int round = 0; round < 2; ++round) {
-            if (who == 0) break;
-            const int leader = __ffs(who) - 1;
-            const int common = __shfl_sync(0xffffffffu, digit, leader);   // (by every lane: not behind a condition)
-            const uint32_t same = __ballot_sync(0xffffffffu, left && digit == common);
-            if (lane == leader) atomicAdd(&hist[digit], __popc(same));
-            left = left && !((same >> lane) & 1u);
-            who &= ~same;
-          }
-          if (left) atomicAdd(&hist[digit], 1);
+          // Lanes with the digit of the first one that counts add once (many
+          // weights share a value, zero above all, and equal addresses are
+          // added one by one); the rest add for themselves.
+          const uint32_t who = __ballot_sync(0xffffffffu, counts);
+          if (who == 0) continue;   // (the same in the whole warp)
+          const int leader = __ffs(who) - 1;
+          const int common = __shfl_sync(0xffffffffu, digit, leader);   // (by every lane: not behind a condition)
+          const uint32_t same = __ballot_sync(0xffffffffu, counts && digit == common);
+          if (lane == leader) atomicAdd(&hist[digit], __popc(same));
+          if (counts && !((same >> lane) & 1u)) atomicAdd(&hist[digit], 1);
         }
       }
       tc::cluster_sync();   // every CTA's histogram is complete

@@ -640,14 +640,14 @@ def cache_compact(arrays, kv_start, kept: torch.Tensor, counts: torch.Tensor, de
     rows, t_max, _ = arrays[0].shape
     assert kept.dtype is torch.int32 and k_last == 1 and n == batch and (rows == 1 or rows == batch)
     _check_int32(kv_start, counts)
-    states = (StateArray * len(arrays))()
-    for s, a in zip(states, arrays):
+    states = []
+    for a in arrays:
         a_rows, a_len, features = a.shape
         a_row, a_batch = _cache_strides(a)
         size = a.element_size()
         assert a_rows == rows and a_len == t_max
-        s.data, s.token_stride_bytes, s.row_bytes = a.data_ptr(), a_row * size, features * size
-        s.batch_stride_bytes = a_batch * size
+        states.append((a.data_ptr(), a_row * size, a_batch * size, features * size))
+    states = (StateArray * len(states))(*states)
     handle = _launch_stream(stream, kv_start, kept, counts, device_status, *arrays)
     _check(lib.mla_cache_compact(states, len(arrays), _ptr(kv_start), kept.data_ptr(), k_row, counts.data_ptr(), width,
                                  batch, t_max, _ptr(device_status), handle))

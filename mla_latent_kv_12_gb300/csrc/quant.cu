@@ -11,7 +11,9 @@
 // to four tokens).  encode_walk_kernel serves every other shape: it walks a
 // tile of max(block, 16) rows twice, the second time from L1 / L2.  Bound by
 // memory: 2 * rank + 2 * rope bytes in and rank + 2 * rope bytes out per bf16
-// token.
+// token.  Measured: 16 x 16384 tokens quantised in 68 us (5.9 TB/s), 8 x 2048
+// appended in 14.7 us (2.0 TB/s: one wave of CTAs), 16 x 16384 dequantised in
+// 67 us (6.0 TB/s).
 #include <cuda_bf16.h>
 
 #include "e4m3.cuh"

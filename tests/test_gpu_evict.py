@@ -418,3 +418,56 @@ def test_cycles_on_two_streams_and_in_two_graphs(mla):
             graph.replay()
     torch.cuda.synchronize()
     assert all(same_state(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("layout", ["broadcast rows", "heads first", "wide heads"])
+def test_key_weights_query_layouts(mla, q8, layout):
+    g = gen(93)
+    B, s_q, T, block = 3, 2, 200, 8
+    q, codes, scales, rope, start, length = attend_case(g, B, s_q, 128, T, block, [200, 5, 131], [0, 8, 16])
+    if layout == "broadcast rows":
+        q = q[:1].expand(B * s_q, 128, 576)
+    elif layout == "heads first":
+        q = q.transpose(0, 1).contiguous().transpose(0, 1)
+    else:
+        wide = torch.full((B * s_q, 128, 592), float("nan"), dtype=torch.bfloat16, device=DEV)
+        wide[..., 8:584] = q
+        q = wide[..., 8:584]
+    latent = normal(g, B, T, 512).bfloat16()
+    lat = [R.held64(codes[b].cpu().numpy(), scales[b].cpu().numpy(), block) if q8 else R.as64(latent[b]) for b in range(B)]
+    lse = make_lse(q, lat, rope, start, length, s_q)
+    w = torch.exp(normal(g, B, T))
+    before, st = w.clone(), status()
+    if q8:
+        mla.key_weights_q8(q, codes, scales, block, rope, lse, start, length, B, s_q, SCALE, w, n_new=1, device_status=st)
+    else:
+        mla.key_weights(q, latent, rope, lse, start, length, B, s_q, SCALE, w, n_new=1, device_status=st)
+    assert int(st) == 0
+    check_weights(w, before, q, lat, rope, lse, start, length, s_q, 1.0, 1)
+    if q8:
+        ctx, lse2 = torch.empty(B * s_q, 128, 512, dtype=torch.bfloat16, device=DEV), torch.empty(B * s_q, 128, device=DEV)
+        mla.decode_attend_q8(q, codes, scales, block, rope, start, length, B, s_q, SCALE, ctx, lse2)
+        check_attend(ctx, lse2, (q, codes, scales, rope, start, length), block, s_q)
+
+
+def test_every_row_empty(mla):
+    """No key anywhere: nothing is written but empty results, and nothing is flagged."""
+    g = gen(94)
+    B, T, block = 3, 128, 16
+    q, codes, scales, rope, start, length = attend_case(g, B, 1, 128, T, block, [0, 0, 0], [0, 16, 32])
+    latent = normal(g, B, T, 512).bfloat16()
+    ctx, lse, st = torch.ones(B, 128, 512, dtype=torch.bfloat16, device=DEV), torch.ones(B, 128, device=DEV), status()
+    mla.decode_attend_q8(q, codes, scales, block, rope, start, length, B, 1, SCALE, ctx, lse, device_status=st)
+    assert (ctx == 0).all() and torch.isneginf(lse).all()
+    w = torch.rand(B, T, generator=g, device=DEV)
+    w0, c0, e0, l0 = w.clone(), codes.clone(), scales.clone(), latent.clone()
+    mla.key_weights_q8(q, codes, scales, block, rope, lse, start, length, B, 1, SCALE, w, n_new=1, device_status=st)
+    mla.key_weights(q, latent, rope, lse, start, length, B, 1, SCALE, w, n_new=1, device_status=st)
+    mla.quantize_cache(latent, codes, scales, block, start, length, device_status=st)
+    mla.dequantize_cache(codes, scales, block, latent, start, length, device_status=st)
+    kept, counts, out, plan_status = run_plan(mla, w, start, length, 4, 1, 1)
+    mla.cache_compact([codes, rope], start, kept, counts, device_status=st)
+    assert int(st) == 0 and plan_status == 0 and counts.tolist() == [-1] * 3 and out.tolist() == [0] * 3
+    for a, b in ((w, w0), (codes, c0), (scales, e0), (latent, l0)):
+        assert torch.equal(a, b)

@@ -17,6 +17,7 @@
 //    all rows.  With several query tokens a range is walked in chunks that
 //    stay in L2, once per token: the weights of a key are always updated by
 //    the same thread, in token order (no atomics, the same bits every time).
+//    Two tokens of 64 heads share the MMA's 128 rows and a pass.
 //  * bf16 cache: warp 0 loads [64 keys x 576] tiles by TMA into a three-stage
 //    ring (nine boxes of 64 dims, 128-byte swizzle).  8-bit cache: warps
 //    10..17 fetch codes and write their fp16 values into the same layout
@@ -79,10 +80,12 @@ __device__ __forceinline__ int window_tiles(const DecodeGeometry& g, int b, bool
   return (len + BN - 1) / BN;
 }
 
-// A CTA's share of the work: passes of one query token over tiles [t0, t1) of one batch row.
+// A CTA's share of the work: passes of one query token (two of 64 heads, which
+// share the MMA's 128 rows) over tiles [t0, t1) of one batch row.
 struct Passes {
   int b, t, left, row_tiles;   // current row, next tile, tiles left in the CTA's range, tiles of the row
-  int i, t0, t1;               // token, current chunk
+  int i, t0, t1;               // (first) token, current chunk
+  static __device__ int tokens(const DecodeGeometry& g) { return g.heads == 64 ? 2 : 1; }
   __device__ void init(int b0, int first, int count, const DecodeGeometry& g) {
     b = b0;
     t = first;
@@ -94,25 +97,25 @@ struct Passes {
   // The next pass; `fresh`: its query is not the previous pass's.
   __device__ bool next(const DecodeGeometry& g, bool& fresh) {
     fresh = true;
-    if (i + 1 < g.s_q) {
-      ++i;
+    if (i + tokens(g) < g.s_q) {
+      i += tokens(g);
       return true;
     }
     if (left <= 0) return false;
-    const int was = i == g.s_q ? -1 : b;
+    const int was = t1 == 0 ? -1 : b;
     while (t >= row_tiles) {
       ++b;
       t = 0;
       row_tiles = window_tiles(g, b, false);
     }
     int n = min(left, row_tiles - t);
-    if (g.s_q > 1) n = min(n, g.codes ? kChunkTilesQ8 : kChunkTiles);
+    if (g.s_q > tokens(g)) n = min(n, g.codes ? kChunkTilesQ8 : kChunkTiles);
     i = 0;
     t0 = t;
     t1 = t + n;
     t += n;
     left -= n;
-    fresh = g.s_q > 1 || was != b;
+    fresh = g.s_q > tokens(g) || was != b;
     return true;
   }
 };
@@ -200,11 +203,15 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
     abort_s = 1;
     if (g.device_status) atomicOr(g.device_status, MLA_DEVICE_TIMEOUT);
   };
-  // One half (64 heads) of a pass's query into a stage: the boxes of a tile.
-  auto load_query = [&](int stage, int row, int half) {
+  // One half (64 heads, of the second token where a pass has two) of a pass's
+  // query into a stage: the boxes of a tile.  (A second token that is not there
+  // is the first one again; its sums are dropped.)
+  auto load_query = [&](int stage, int b, int i, int half) {
+    const bool two = Passes::tokens(g) == 2;
+    const int row = b * g.s_q + (two && i + half < g.s_q ? i + half : i);
     mbar_arrive_expect_tx(&full_bar[stage], STAGE_BYTES);
     for (int c = 0; c < BOXES; ++c)
-      tma_load_3d(stages + stage * STAGE_BYTES + c * BOX_BYTES, &q_map, &full_bar[stage], 64 * c, 64 * half,
+      tma_load_3d(stages + stage * STAGE_BYTES + c * BOX_BYTES, &q_map, &full_bar[stage], 64 * c, two ? 0 : 64 * half,
                   a.rows_in_map ? row : 0);
   };
   Passes it;
@@ -222,7 +229,7 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
       for (int half = 0; fresh && ok && half < 2; ++half) {
         if (fills >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); ok = false; break; }
         ++fills;
-        if (lane == 0) load_query(stage, it.b * g.s_q + it.i, half);
+        if (lane == 0) load_query(stage, it.b, it.i, half);
         __syncwarp();
         if (++stage == kStages) stage = 0, phase ^= 1u;
       }
@@ -290,7 +297,7 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
         if (fills >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); ok = false; break; }
         ++fills;
         if (lane == 0) {
-          if (cw == 0) load_query(stage, b * g.s_q + it.i, half); else mbar_arrive(&full_bar[stage]);
+          if (cw == 0) load_query(stage, b, it.i, half); else mbar_arrive(&full_bar[stage]);
         }
         __syncwarp();
         if (++stage == kStages) stage = 0, phase ^= 1u;
@@ -321,12 +328,14 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
         // ahead of the others, whose registers are full (checked as they are
         // converted, four tokens took 165 us on 8 rows of 16384 keys, here 145).
         const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(g.q) + ((int64_t)b * g.s_q + it.i) * g.q_row_stride;
+        const int rows = min(Passes::tokens(g), g.s_q - it.i) * g.heads;
         uint32_t top = 0;
 #pragma unroll 4
-        for (int h = cw; h < g.heads; h += kConvertWarps)
+        for (int h = cw; h < rows; h += kConvertWarps)
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(q + (int64_t)h * g.q_head_stride) + 32 * v + lane);
+            const __nv_bfloat16* head = q + (h >= g.heads ? g.q_row_stride + (int64_t)(h - g.heads) * g.q_head_stride : (int64_t)h * g.q_head_stride);
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(head) + 32 * v + lane);
             top = max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(top, x.x), x.y), x.z), x.w);
           }
         if (beyond_f16(top)) atomicOr(g.device_status, MLA_DEVICE_VALUE_RANGE);
@@ -376,9 +385,9 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
   } else if (warp >= kSumWarp && warp < kConvertWarp) {
     // ============================================================ probabilities and sums
     const int group = (warp - kSumWarp) >> 2, quarter = warp & 3;
-    const int h = 32 * quarter + lane;
+    const int h = 32 * quarter + lane;   // MMA row
     const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
-    const bool real = h < g.heads;
+    const int token = h / g.heads;       // of the pass's tokens
     const int k_mine = threadIdx.x - 32 * (kSumWarp + 4 * group);   // key of a tile whose weight this thread updates (first two warps)
     uint32_t tile = 0, fill = 0;   // tiles and ring fills of all passes so far
     float lse2 = 0.f;
@@ -392,12 +401,13 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
     while (!stop && it.next(g, fresh)) {
       const int b = it.b, len = g.kv_len[b];
       const int64_t start = g.kv_start ? g.kv_start[b] : 0;
-      const int limit = min(len, len - g.s_q + it.i + 1);
+      const bool real = it.i + token < g.s_q;
+      const int limit = min(len, len - g.s_q + it.i + token + 1);
       if (fresh) {
         // The query into TMEM, a head per thread, every other box by either
-        // group (rows of padding heads arrive as zeros).  Every MMA of the
-        // previous passes has completed once its last scores are there.
-        lse2 = real ? a.lse[((int64_t)b * g.s_q + it.i) * g.heads + h] * 1.4426950408889634f : 0.f;
+        // group.  Every MMA of the previous passes has completed once its last
+        // scores are there.
+        lse2 = real ? a.lse[((int64_t)b * g.s_q + it.i) * g.heads + h] * 1.4426950408889634f : 0.f;   // (h: into the second token's)
         const uint32_t k = fill + (quarter >> 1);
         arrived = tile == 0 || mbar_wait_warp(&s_full[(tile - 1) & 1u], ((tile - 1) >> 1) & 1u, kWaitLimit);
         arrived = mbar_wait_warp(&full_bar[k % kStages], (k / kStages) & 1u, kWaitLimit) && arrived;
@@ -477,7 +487,7 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
               p[k] = keep + __shfl_xor_sync(0xffffffffu, send, o);
             }
           }
-          sum[k2] = real ? p[0] : 0.f;   // (64 heads: quarters 2 and 3 hold padding rows only)
+          sum[k2] = real ? p[0] : 0.f;
         }
         named_sync(1 + kSumGroups + group, 128);   // the previous tile's sums have been read
         part_s[group][quarter][lane] = sum[0];

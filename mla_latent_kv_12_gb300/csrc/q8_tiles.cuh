@@ -41,13 +41,13 @@ struct Q8Rows {
   int32_t* status;               // non-NULL: flag positions outside the window
 };
 
-template <int kLanes, int kThreads>
+template <int kLanes, int kThreads, bool kRopeInSlots>
 struct Q8Fetch {
   static constexpr int kStep = kThreads / kLanes;         // keys taken at once
   static constexpr int kIters = kTileKeys / kStep;        // pieces of codes per thread and tile
   static constexpr int kRopeIters = kIters / 4;           // and of rope keys
   static constexpr int kPieceBytes = 16 * kThreads;
-  static constexpr int kSlotBytes = (kIters + kRopeIters) * kPieceBytes;
+  static constexpr int kSlotBytes = (kIters + (kRopeInSlots ? kRopeIters : 0)) * kPieceBytes;
   static_assert(kStep % 8 == 0 && kIters >= 4 && kIters <= 8, "fixed swizzle; lanes to look the keys up");
   uint32_t slot0;                // shared address of this thread's first piece
   uint32_t codes0;               // and of the codes that it decodes
@@ -106,7 +106,13 @@ struct Q8Fetch {
                       p >= 0 ? 16u : 0u);
     }
   }
-  // The rope pieces that issue() copied, into the stage: `rope` is the place of the first one, rows kRow bytes apart.
+  // This thread's rope piece of one tile (one per thread), zeros for no key.
+  __device__ __forceinline__ uint4 load_rope(const Q8Rows& r, int pos) const {
+    static_assert(kRopeIters == 1 || kRopeInSlots, "one piece is held in registers");
+    const int p = __shfl_sync(0xffffffffu, pos, peers + rope_group);
+    return p >= 0 ? __ldg(reinterpret_cast<const uint4*>(r.rope + (int64_t)(r.start + p) * r.rope_stride)) : make_uint4(0, 0, 0, 0);
+  }
+  // The rope pieces that issue_rope() copied, into the stage: `rope` is the place of the first one, rows kRow bytes apart.
   template <int kRow>
   __device__ __forceinline__ void copy_rope(int s, uint32_t rope) const {
 #pragma unroll

@@ -81,16 +81,17 @@ constexpr int kGatherWarp = 11;   // first extra gather warp
 // kRegsLaunch for each of the five.
 constexpr int THREADS_Q8 = 640;
 constexpr int kConvertWarps = 8;
-constexpr int STAGES_Q8 = 3;
+constexpr int STAGES_Q8 = 4;
+constexpr int kTilesAhead = 6;    // tiles ahead that a window's rows are pulled into L2
 constexpr int kRegsLaunch = 96;
 constexpr int kRegsSoftmax = 144, kRegsExchange = 128, kRegsIssue = 48, kRegsConvert = 80;
 static_assert(kRegsSoftmax + kRegsExchange + kRegsIssue + 2 * kRegsConvert <= 5 * kRegsLaunch, "more registers than the launch has");
-using DecodeFetch = Q8Fetch<16, 32 * kConvertWarps>;
+using DecodeFetch = Q8Fetch<16, 32 * kConvertWarps, false>;
 // Dynamic shared memory: the stage ring, then send[2] and receive[2].  The
 // 1024-byte alignment of the extern declaration places it on a 1024-byte
 // boundary after the static variables (checked at run time).
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 4 * XH_BYTES;
-constexpr int SMEM_BYTES_Q8 = STAGES_Q8 * STAGE_BYTES + 4 * XH_BYTES + 2 * DecodeFetch::kSlotBytes;
+constexpr int SMEM_BYTES_Q8 = STAGES_Q8 * STAGE_BYTES + 3 * XH_BYTES + 2 * DecodeFetch::kSlotBytes;
 constexpr uint32_t TM_O = 0, TM_Q = 256, TM_S = 400, TM_P = 464;  // TMEM columns (Q: 128 + 16)
 constexpr long long kWaitLimit = 1LL << 32;  // clock cycles (~2 s)
 constexpr float kRescaleThreshold = 8.0f;    // log2 units
@@ -494,7 +495,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Warps of each role (the first of four, one per TMEM lane quarter, for softmax and exchange).
   constexpr int kSoftmaxWarp = kQ8 ? 0 : 2, kExchangeWarp = kQ8 ? 4 : 6, kScoreWarp = kQ8 ? 8 : 1, kPvWarp = kQ8 ? 9 : 10;
-  constexpr int kConvertWarp = 12;
+  constexpr int kRopeWarp = 10, kConvertWarp = 12;
   const uint32_t rank = cluster_ctarank();
   const uint32_t peer = rank ^ 1u;
   const int dim_base = 256 * (int)rank;     // first latent dim of this CTA
@@ -503,16 +504,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const bool gather = a.sel != nullptr;
 
   if (threadIdx.x == 0) {
+    if (!kQ8 || !gather) tma_prefetch_desc(&rope_map);
     if constexpr (!kQ8) {
       tma_prefetch_desc(&lat_map);
-      tma_prefetch_desc(&rope_map);
       if (gather && a.gather_tma) {
         tma_prefetch_desc(&lat_rows_map);
         tma_prefetch_desc(&rope_rows_map);
       }
     }
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full_bar[s], kQ8 ? kConvertWarps : (gather && !a.gather_tma) ? 32 : 1);
+      mbar_init(&full_bar[s], kQ8 ? kConvertWarps + 1 : (gather && !a.gather_tma) ? 32 : 1);
       mbar_init(&empty_bar[s], 1);
     }
     mbar_init(&s_full, 1);
@@ -672,19 +673,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_wait_warp(&pv_drain, 0, kWaitLimit);
   };
 
+  // The 8-bit cache's rope keys, which need no conversion: whole tiles of a
+  // window go to their stage by TMA, beside the converting warps, who write those of
+  // selections and of a window's last tile.  The rows of a later tile are
+  // pulled into L2.
+  auto load_rope_tiles = [&]() {
+    int stage = 0, fills = 0;
+    uint32_t phase = 0;
+    int u, n, t0, t1;
+    bool whole;
+    while (!aborted() && it.next(u, t0, t1, whole)) {
+      if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
+      const int b = n / a.s_q, keys = keys_p[n];
+      const int start = a.plan_in_kernel ? row_start_s[n] : (a.kv_start ? a.kv_start[b] : 0);
+      const bool window = !gather || a.sel_count[n] == -1;
+      const int z = a.batch_in_map ? b : 0;
+      for (int t = t0; t < t1; ++t) {
+        if (fills >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
+        ++fills;
+        if (lane == 0) {
+          if (window && (t + 1) * BN <= keys) {
+            mbar_arrive_expect_tx(&full_bar[stage], BN * 64);
+            tma_load_3d(stages + stage * STAGE_BYTES + 4 * CHUNK_BYTES, &rope_map, &full_bar[stage], 32 * (int)rank,
+                        start + t * BN, z);
+          } else {
+            mbar_arrive(&full_bar[stage]);
+          }
+          if (window && t + kTilesAhead < t1)
+            tma_prefetch_l2_3d(&rope_map, 32 * (int)rank, start + (t + kTilesAhead) * BN, z);
+        }
+        __syncwarp();
+        if (++stage == kStages) stage = 0, phase ^= 1u;
+      }
+    }
+    // every load lands before this CTA may exit
+    for (int k = fills > kStages ? fills - kStages : 0; k < fills; ++k)
+      mbar_wait_warp(&full_bar[k % kStages], (uint32_t)(k / kStages) & 1u, kWaitLimit);
+  };
+
   if (kQ8 && warp >= kScoreWarp && warp < kConvertWarp) {
-    // One warpgroup: both issuers and two warps without a role (a whole
-    // warpgroup executes the same setmaxnreg).
+    // One warpgroup: both issuers, the rope keys' warp and one without a role
+    // (a whole warpgroup executes the same setmaxnreg).
     reg_dealloc<kRegsIssue>();
     if (warp == kScoreWarp) issue_scores();
     if (warp == kPvWarp) issue_pv();
+    if (warp == kRopeWarp) load_rope_tiles();
   } else if (kQ8 && warp >= kConvertWarp) {
     reg_dealloc<kRegsConvert>();
     // ============================================================ 8-bit producers
     // Half a warp takes one key at a time.
     const int cw = warp - kConvertWarp, c = lane & 15;
     DecodeFetch fetch;
-    fetch.slot0 = smem_u32(xout + 2 * XH_BYTES) + (cw * 32 + lane) * 16;
+    fetch.slot0 = smem_u32(xout + XH_BYTES) + (cw * 32 + lane) * 16;
     fetch.codes0 = fetch.slot0 - 16 * c + 8 * c;
     fetch.key0 = 2 * cw + (lane >> 4);
     fetch.rope_group = c >> 2;
@@ -721,14 +761,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // waits for loads in flight.)
       auto issue = [&](int t, int slot, int p) {
         if (rows.list) fetch.issue_codes(rows, slot, p); else fetch.issue_window(rows, t, slot);
-        fetch.issue_rope(rows, slot, p);
       };
       int pos = fetch.my_position(rows, t0);
       int e_now = fetch.my_exponent(rows, pos);
+      const int rope_from = rows.list ? 0 : rows.entries / BN;   // first tile whose rope keys the rope warp does not load
+      uint4 rope_now = make_uint4(0, 0, 0, 0), rope_next = rope_now;
+      if (t0 >= rope_from) rope_now = fetch.load_rope(rows, pos);
       issue(t0, 0, pos);
       cp_async_commit();
       pos = fetch.my_position(rows, t0 + 1);
       int e_next = fetch.my_exponent(rows, pos);
+      if (t0 + 1 >= rope_from) rope_next = fetch.load_rope(rows, pos);
       if (t0 + 1 < t1) issue(t0 + 1, 1, pos);
       cp_async_commit();
       pos = fetch.my_position(rows, t0 + 2);
@@ -739,13 +782,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         cp_async_wait<1>();   // this tile's pieces
         const uint32_t off = stage * STAGE_BYTES;
         fetch.template convert<2 * CHUNK_BYTES>(slot, e_now, box0 + off);
-        fetch.template copy_rope<64>(slot, rope0 + off);
+        if (t >= rope_from) DecodeFetch::st_shared_16(rope0 + off, rope_now);
         fence_proxy_async_smem();   // generic-proxy writes, read by the MMAs
         __syncwarp();
         if (lane == 0) mbar_arrive(&full_bar[stage]);
         e_now = e_next;
+        rope_now = rope_next;
         if (t + 2 < t1) {
           e_next = fetch.my_exponent(rows, pos);
+          if (t + 2 >= rope_from) rope_next = fetch.load_rope(rows, pos);
           issue(t + 2, slot, pos);
           pos = fetch.my_position(rows, t + 3);
         }
@@ -990,7 +1035,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // (a signal only: the peer's reads of that buffer completed before its
           // arrive, so a CTA-scope wait suffices)
           if (!mbar_wait_warp(&x_free[b], (use - 1) & 1u, kWaitLimit)) { fail(); break; }
-          if (!mbar_wait_warp(&xo_free[b], (use - 1) & 1u, kWaitLimit)) { fail(); break; }
+          if (!kQ8 && !mbar_wait_warp(&xo_free[b], (use - 1) & 1u, kWaitLimit)) { fail(); break; }
         }
         if (!mbar_wait_warp(&s_full, tile & 1u, kWaitLimit)) { fail(); break; }
         tc_fence_after();
@@ -1004,7 +1049,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // Each 16-byte piece goes to our own softmax warps (xout) and, as an
         // asynchronous remote store that completes on the peer's x_full, into
         // the peer's receive buffer: no staging round trip, no bulk copy.
-        uint8_t* xo = xout + b * XH_BYTES;
+        uint8_t* xo = xout + (kQ8 ? 0 : b) * XH_BYTES;
         const uint32_t xi = xin_peer + b * XH_BYTES;
         if constexpr (kQ8) {
           // Scores that fp16 cannot hold are rare: the tile's largest magnitude
@@ -1022,9 +1067,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
+        uint32_t w[8][4];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          uint32_t w[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int k = 8 * c + 2 * q;   // scores k, k+1
@@ -1035,10 +1080,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const float2 sc = mul_f32x2(make_float2(lo_raw, hi_raw), make_float2(a.scale_log2, a.scale_log2));
             const __half2 hv = kQ8 ? __floats2half2_rn(sc.x, sc.y)
                                    : __floats2half2_rn(fminf(fmaxf(sc.x, -65504.f), 65504.f), fminf(fmaxf(sc.y, -65504.f), 65504.f));
-            w[q] = *reinterpret_cast<const uint32_t*>(&hv);
+            w[c][q] = *reinterpret_cast<const uint32_t*>(&hv);
           }
-          *reinterpret_cast<uint4*>(xo + (c * 128 + h) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-          st_async_v4(xi + (uint32_t)((c * 128 + h) * 16), w[0], w[1], w[2], w[3], x_full_peer[b]);
+          if constexpr (!kQ8) *reinterpret_cast<uint4*>(xo + (c * 128 + h) * 16) = make_uint4(w[c][0], w[c][1], w[c][2], w[c][3]);
+          st_async_v4(xi + (uint32_t)((c * 128 + h) * 16), w[c][0], w[c][1], w[c][2], w[c][3], x_full_peer[b]);
+        }
+        if constexpr (kQ8) {
+          // One buffer for our own half (the other's memory is the fourth
+          // stage's): the softmax warps have read the tile before, which they
+          // do first of all.
+          if (tile > 0 && !mbar_wait_warp(&xo_free[0], (tile - 1) & 1u, kWaitLimit)) { fail(); break; }
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4*>(xo + (c * 128 + h) * 16) = make_uint4(w[c][0], w[c][1], w[c][2], w[c][3]);
         }
         __syncwarp();
         // xout[b] is written by this warp; receive buffer b expects the peer's
@@ -1142,7 +1196,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // (finite) half.  A rolled loop with computed addresses: it runs at a
           // row's last tile only, where an unrolled masking pass would be
           // fetched cold into the instruction cache.
-          const uint32_t row = smem_u32(xout + b * XH_BYTES) + (uint32_t)h * 16u;
+          const uint32_t row = smem_u32(xout + (kQ8 ? 0 : b) * XH_BYTES) + (uint32_t)h * 16u;
           uint64_t inv = ~valid;
 #pragma unroll 1
           while (inv != 0ull) {
@@ -1153,7 +1207,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         float x[BN];
         {
-          const uint8_t* xo = xout + b * XH_BYTES;
+          const uint8_t* xo = xout + (kQ8 ? 0 : b) * XH_BYTES;
           const uint8_t* xi = xin + b * XH_BYTES;
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
@@ -1185,7 +1239,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // that dependency (a release arrive costs a cluster-scope fence per tile).
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive_relaxed_dep(&xo_free[b], __float_as_uint(mx));
+          mbar_arrive_relaxed_dep(&xo_free[kQ8 ? 0 : b], __float_as_uint(mx));
           mbar_arrive_remote_relaxed_dep(x_free_peer[b], __float_as_uint(mx));
         }
         // ---- online softmax with lazy rescaling: the reference moves only
@@ -1817,7 +1871,8 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
   a.width = (g.sel == nullptr && g.s_q > 1 && g.s_q <= 8) ? g.s_q : 1;
   a.n_units = n_q / a.width;
   a.min_tiles = kMinTilesPerGroup;
-  a.batch_in_map = (g.latent_batch_stride != 0 || g.rope_batch_stride != 0) ? 1 : 0;
+  const bool q8 = g.codes != nullptr;   // codes are copied row by row: only rope keys are mapped
+  a.batch_in_map = ((g.latent_batch_stride != 0 && !q8) || g.rope_batch_stride != 0) ? 1 : 0;
   a.plan_in_kernel = n_q <= kMaxRowsInKernelPlan ? 1 : 0;
   a.early_inputs = (tail != nullptr && a.plan_in_kernel) ? 1 : 0;
   a.codes = g.codes;
@@ -1833,8 +1888,7 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
   // Tensor maps over [B_buf, t_max, dims] (the batch axis has extent 1 for a
   // packed-flat cache whose batch stride is 0).
   const uint64_t bmap = a.batch_in_map ? (uint64_t)g.batch : 1;
-  const bool q8 = g.codes != nullptr;   // copied row by row: no maps
-  CUtensorMap lat_map = {}, rope_map = {};
+  CUtensorMap lat_map = {}, rope_map;
   if (!q8) {
     const uint64_t dims[3] = {(uint64_t)g.rank, (uint64_t)g.t_max, bmap};
     const uint64_t bstride = a.batch_in_map ? (uint64_t)g.latent_batch_stride * 2
@@ -1843,7 +1897,7 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
     const uint32_t box[3] = {64, BN, 1};
     if (!encode_tmap_bf16(&lat_map, g.latent, 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  if (!q8) {
+  {
     const uint64_t dims[3] = {(uint64_t)g.rope_dim, (uint64_t)g.t_max, bmap};
     const uint64_t bstride = a.batch_in_map ? (uint64_t)g.rope_batch_stride * 2
                                             : (uint64_t)g.t_max * g.rope_row_stride * 2;

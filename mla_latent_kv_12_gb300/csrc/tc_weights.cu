@@ -48,7 +48,7 @@ constexpr uint32_t TM_Q = 0, TM_S = 288;  // TMEM columns
 constexpr int kSumWarp = 2, kSumGroups = 2;   // two groups of four warps
 constexpr int kConvertWarp = kSumWarp + 4 * kSumGroups, kConvertWarps = 8, kConvertThreads = 32 * kConvertWarps;
 constexpr int kThreads = 32 * kConvertWarp, kThreadsQ8 = kThreads + kConvertThreads;
-using WeightFetch = Q8Fetch<32, kConvertThreads>;
+using WeightFetch = Q8Fetch<32, kConvertThreads, true>;
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES, SMEM_BYTES_Q8 = STAGES_Q8 * STAGE_BYTES + 2 * WeightFetch::kSlotBytes;
 constexpr long long kWaitLimit = 1LL << 32;   // clock cycles (~2 s)
 // Tiles that several query tokens share before the next ones are read, so that

@@ -1,6 +1,7 @@
 // Tiles of an 8-bit cache as the fp16 operand tiles of tcgen05 MMAs: fetch of
-// the codes, exponents and rope keys of 64 keys, and their fp16 values in the
-// swizzled shared-memory layout that a TMA load of a bf16 cache would leave.
+// the codes and exponents of 64 keys, and their fp16 values in the swizzled
+// shared-memory layout that a TMA load of a bf16 cache would leave.  (Rope keys
+// need no conversion: the kernels load those of whole tiles by TMA.)
 //
 // The fetch runs two tiles ahead: every warp copies its own 16-byte pieces
 // with cp.async into one of two slots of its own, so nothing but its own
@@ -41,13 +42,13 @@ struct Q8Rows {
   int32_t* status;               // non-NULL: flag positions outside the window
 };
 
-template <int kLanes, int kThreads, bool kRopeInSlots>
+template <int kLanes, int kThreads>
 struct Q8Fetch {
   static constexpr int kStep = kThreads / kLanes;         // keys taken at once
   static constexpr int kIters = kTileKeys / kStep;        // pieces of codes per thread and tile
   static constexpr int kRopeIters = kIters / 4;           // and of rope keys
   static constexpr int kPieceBytes = 16 * kThreads;
-  static constexpr int kSlotBytes = (kIters + (kRopeInSlots ? kRopeIters : 0)) * kPieceBytes;
+  static constexpr int kSlotBytes = kIters * kPieceBytes;
   static_assert(kStep % 8 == 0 && kIters >= 4 && kIters <= 8, "fixed swizzle; lanes to look the keys up");
   uint32_t slot0;                // shared address of this thread's first piece
   uint32_t codes0;               // and of the codes that it decodes
@@ -96,28 +97,11 @@ struct Q8Fetch {
       tc::cp_async_16(dst + i * kPieceBytes, r.codes + (int64_t)(r.start + max(p, 0)) * r.codes_stride, p >= 0 ? 16u : 0u);
     }
   }
-  // And of its rope keys.
-  __device__ __forceinline__ void issue_rope(const Q8Rows& r, int s, int pos) const {
-    const uint32_t dst = slot0 + s * kSlotBytes;
-#pragma unroll
-    for (int j = 0; j < kRopeIters; ++j) {
-      const int p = __shfl_sync(0xffffffffu, pos, peers + 4 * j + rope_group);
-      tc::cp_async_16(dst + (kIters + j) * kPieceBytes, r.rope + (int64_t)(r.start + max(p, 0)) * r.rope_stride,
-                      p >= 0 ? 16u : 0u);
-    }
-  }
   // This thread's rope piece of one tile (one per thread), zeros for no key.
   __device__ __forceinline__ uint4 load_rope(const Q8Rows& r, int pos) const {
-    static_assert(kRopeIters == 1 || kRopeInSlots, "one piece is held in registers");
+    static_assert(kRopeIters == 1, "one piece per thread");
     const int p = __shfl_sync(0xffffffffu, pos, peers + rope_group);
     return p >= 0 ? __ldg(reinterpret_cast<const uint4*>(r.rope + (int64_t)(r.start + p) * r.rope_stride)) : make_uint4(0, 0, 0, 0);
-  }
-  // The rope pieces that issue_rope() copied, into the stage: `rope` is the place of the first one, rows kRow bytes apart.
-  template <int kRow>
-  __device__ __forceinline__ void copy_rope(int s, uint32_t rope) const {
-#pragma unroll
-    for (int j = 0; j < kRopeIters; ++j)
-      st_shared_16(rope + 4 * j * kStep * kRow, tc::ld_shared_16(slot0 + s * kSlotBytes + (kIters + j) * kPieceBytes));
   }
   // Slot s as fp16 values: this lane's first eight dims at shared address `box`,
   // the others kBox bytes behind, rows 128 bytes apart.  `exponent` from

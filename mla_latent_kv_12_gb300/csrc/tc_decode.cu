@@ -86,7 +86,7 @@ constexpr int kTilesAhead = 6;    // tiles ahead that a window's rows are pulled
 constexpr int kRegsLaunch = 96;
 constexpr int kRegsSoftmax = 144, kRegsExchange = 128, kRegsIssue = 48, kRegsConvert = 80;
 static_assert(kRegsSoftmax + kRegsExchange + kRegsIssue + 2 * kRegsConvert <= 5 * kRegsLaunch, "more registers than the launch has");
-using DecodeFetch = Q8Fetch<16, 32 * kConvertWarps, false>;
+using DecodeFetch = Q8Fetch<16, 32 * kConvertWarps>;
 // Dynamic shared memory: the stage ring, then send[2] and receive[2].  The
 // 1024-byte alignment of the extern declaration places it on a 1024-byte
 // boundary after the static variables (checked at run time).

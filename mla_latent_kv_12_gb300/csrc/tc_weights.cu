@@ -21,7 +21,8 @@
 //  * bf16 cache: warp 0 loads [64 keys x 576] tiles by TMA into a three-stage
 //    ring (nine boxes of 64 dims, 128-byte swizzle).  8-bit cache: warps
 //    10..17 fetch codes and write their fp16 values into the same layout
-//    (q8_tiles.cuh); the latent part of the query is converted to fp16 too.
+//    (q8_tiles.cuh), warp 0 loads the rope boxes; the latent part of the query
+//    is converted to fp16 too.
 //  * Warp 1 issues the 36 MMAs of a tile.  Warps 2..9 load each token's query
 //    into TMEM; two groups of four (one thread per head) take the tiles in
 //    turn, turn scores into probabilities and sum them over a warp's 32 heads
@@ -48,7 +49,7 @@ constexpr uint32_t TM_Q = 0, TM_S = 288;  // TMEM columns
 constexpr int kSumWarp = 2, kSumGroups = 2;   // two groups of four warps
 constexpr int kConvertWarp = kSumWarp + 4 * kSumGroups, kConvertWarps = 8, kConvertThreads = 32 * kConvertWarps;
 constexpr int kThreads = 32 * kConvertWarp, kThreadsQ8 = kThreads + kConvertThreads;
-using WeightFetch = Q8Fetch<32, kConvertThreads, true>;
+using WeightFetch = Q8Fetch<32, kConvertThreads>;
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES, SMEM_BYTES_Q8 = STAGES_Q8 * STAGE_BYTES + 2 * WeightFetch::kSlotBytes;
 constexpr long long kWaitLimit = 1LL << 32;   // clock cycles (~2 s)
 // Tiles that several query tokens share before the next ones are read, so that
@@ -56,6 +57,7 @@ constexpr long long kWaitLimit = 1LL << 32;   // clock cycles (~2 s)
 // KB = 91 MB of an 8-bit cache.  (A pass begins with a drained pipeline and its
 // query's load.)
 constexpr int kChunkTiles = 8, kChunkTilesQ8 = 15;
+constexpr int kRopeAhead = 6;      // tiles ahead that an 8-bit cache's rope keys are pulled into L2
 constexpr int kWeightsAhead = 8;   // tiles ahead that weights are pulled into L2
 
 struct WeightArgs {
@@ -141,12 +143,10 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
 
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&q_map);
-    if constexpr (!kQ8) {
-      tma_prefetch_desc(&lat_map);
-      tma_prefetch_desc(&rope_map);
-    }
+    tma_prefetch_desc(&rope_map);
+    if constexpr (!kQ8) tma_prefetch_desc(&lat_map);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full_bar[s], kQ8 ? kConvertWarps : 1);
+      mbar_init(&full_bar[s], kQ8 ? kConvertWarps + 1 : 1);
       mbar_init(&empty_bar[s], 1);
     }
     for (int k = 0; k < 2; ++k) {
@@ -218,8 +218,8 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
   it.init(count_s > 0 ? first_row_s : 0, count_s > 0 ? first_tile_s : 0, count_s, g);
   bool fresh;
 
-  if (!kQ8 && warp == 0) {
-    // ============================================================ TMA producer
+  if (warp == 0) {
+    // ============================================================ TMA producer (8-bit: of queries and rope keys)
     int stage = 0, fills = 0;
     uint32_t phase = 0;
     while (!aborted() && it.next(g, fresh)) {
@@ -237,11 +237,13 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
         if (fills >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
         ++fills;   // (counts what was issued)
         if (lane == 0) {
-          mbar_arrive_expect_tx(&full_bar[stage], STAGE_BYTES);
+          mbar_arrive_expect_tx(&full_bar[stage], kQ8 ? BOX_BYTES : STAGE_BYTES);
           uint8_t* st = stages + stage * STAGE_BYTES;
-          for (int c = 0; c < 8; ++c)
-            tma_load_3d(st + c * BOX_BYTES, &lat_map, &full_bar[stage], 64 * c, start + t * BN, z);
+          if constexpr (!kQ8)
+            for (int c = 0; c < 8; ++c)
+              tma_load_3d(st + c * BOX_BYTES, &lat_map, &full_bar[stage], 64 * c, start + t * BN, z);
           tma_load_3d(st + 8 * BOX_BYTES, &rope_map, &full_bar[stage], 0, start + t * BN, z);
+          if (kQ8 && t + kRopeAhead < it.t1) tma_prefetch_l2_3d(&rope_map, 0, start + (t + kRopeAhead) * BN, z);
         }
         __syncwarp();
         if (++stage == kStages) stage = 0, phase ^= 1u;
@@ -258,12 +260,9 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
     fetch.slot0 = smem_u32(stages + kStages * STAGE_BYTES) + (cw * 32 + lane) * 16;
     fetch.codes0 = fetch.slot0 - 16 * lane + 8 * lane;
     fetch.key0 = cw;
-    fetch.rope_group = lane >> 3;
     fetch.peers = 0;
     fetch.mine = lane % WeightFetch::kIters;
-    // rope piece lane % 8 of box 8
     const uint32_t box0 = smem_u32(stages) + (lane >> 3) * BOX_BYTES + cw * 128 + (((lane & 7) ^ cw) << 4);
-    const uint32_t rope0 = smem_u32(stages) + 8 * BOX_BYTES + (WeightFetch::kStep * fetch.rope_group + cw) * 128 + (((lane & 7) ^ cw) << 4);
     int stage = 0, fills = 0;
     uint32_t phase = 0;
     while (!aborted() && it.next(g, fresh)) {
@@ -273,32 +272,24 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
       rows.codes_stride = g.codes_row_stride;
       rows.scales = g.scales + b * g.scales_batch_stride;
       rows.shift = g.block_shift;
-      rows.rope = static_cast<const __nv_bfloat16*>(g.rope) + b * g.rope_batch_stride + 8 * (lane & 7);
-      rows.rope_stride = g.rope_row_stride;
       rows.start = g.kv_start ? g.kv_start[b] : 0;
       rows.entries = rows.limit = g.kv_len[b];
       rows.list = nullptr;
       rows.status = lane < WeightFetch::kIters ? g.device_status : nullptr;
       // Tile t is converted while the copies of t + 1 and (from its end on) t + 2 are in flight.
-      auto issue = [&](int t, int slot, int p) {
-        fetch.issue_window(rows, t, slot);
-        fetch.issue_rope(rows, slot, p);
-      };
       int pos = fetch.my_position(rows, t0);
       int e_now = fetch.my_exponent(rows, pos);
-      issue(t0, 0, pos);
+      fetch.issue_window(rows, t0, 0);
       cp_async_commit();
       pos = fetch.my_position(rows, t0 + 1);
       int e_next = fetch.my_exponent(rows, pos);
-      if (t0 + 1 < t1) issue(t0 + 1, 1, pos);
+      if (t0 + 1 < t1) fetch.issue_window(rows, t0 + 1, 1);
       cp_async_commit();
       bool ok = true;
       for (int half = 0; fresh && ok && half < 2; ++half) {
         if (fills >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); ok = false; break; }
         ++fills;
-        if (lane == 0) {
-          if (cw == 0) load_query(stage, b, it.i, half); else mbar_arrive(&full_bar[stage]);
-        }
+        if (lane == 0) mbar_arrive(&full_bar[stage]);   // (a half of the query, loaded by warp 0)
         __syncwarp();
         if (++stage == kStages) stage = 0, phase ^= 1u;
       }
@@ -310,7 +301,6 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
         const uint32_t off = stage * STAGE_BYTES;
         fetch.check_exponent(rows.status, e_now);
         fetch.convert<4 * BOX_BYTES>(slot, e_now, box0 + off);
-        fetch.copy_rope<128>(slot, rope0 + off);
         fence_proxy_async_smem();   // generic-proxy writes, read by the MMAs
         __syncwarp();
         if (lane == 0) mbar_arrive(&full_bar[stage]);
@@ -318,7 +308,7 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
         if (t + 2 < t1) {
           pos = fetch.my_position(rows, t + 2);
           e_next = fetch.my_exponent(rows, pos);
-          issue(t + 2, slot, pos);
+          fetch.issue_window(rows, t + 2, slot);
         }
         cp_async_commit();
         if (++stage == kStages) stage = 0, phase ^= 1u;
@@ -342,9 +332,6 @@ __global__ void __launch_bounds__(kQ8 ? kThreadsQ8 : kThreads, 1)
       }
       cp_async_wait<0>();   // the slots are free for the next pass
     }
-    // (query loads land before this CTA may exit)
-    for (int k = fills > kStages ? fills - kStages : 0; k < fills; ++k)
-      mbar_wait_warp(&full_bar[k % kStages], (uint32_t)(k / kStages) & 1u, kWaitLimit);
   } else if (warp == 1) {
     // ============================================================ MMA issuer
     const uint32_t idesc_rope = idesc_bf16_f32(128, BN, 0, 0), idesc = kQ8 ? idesc_f16_f32(128, BN, 0, 0) : idesc_rope;
@@ -521,27 +508,27 @@ cudaError_t launch_tc_key_weights(const KeyWeightParams& p, cudaStream_t stream)
   a.decay = p.decay;
   a.n_new = p.n_new;
   const DecodeGeometry& g = p.g;
-  a.batch_in_map = (g.latent_batch_stride != 0 || g.rope_batch_stride != 0) ? 1 : 0;
-  const bool q8 = g.codes != nullptr;
-  CUtensorMap q_map, lat_map = {}, rope_map = {};
+  const bool q8 = g.codes != nullptr;   // codes are copied row by row: only rope keys are mapped
+  a.batch_in_map = ((g.latent_batch_stride != 0 && !q8) || g.rope_batch_stride != 0) ? 1 : 0;
+  CUtensorMap q_map, lat_map = {}, rope_map;
   const uint32_t q_box[3] = {64, 64, 1};
   a.rows_in_map = g.q_row_stride != 0;
   const uint64_t q_rows = a.rows_in_map ? (uint64_t)g.batch * g.s_q : 1;
   const uint64_t qd[3] = {(uint64_t)(g.rank + g.rope_dim), (uint64_t)g.heads, q_rows};
   const uint64_t qs[2] = {(uint64_t)g.q_head_stride * 2, (uint64_t)(a.rows_in_map ? g.q_row_stride : g.heads * g.q_head_stride) * 2};
   if (!encode_tmap_bf16(&q_map, g.q, 3, qd, qs, q_box)) return cudaErrorInvalidValue;
+  const uint64_t bmap = a.batch_in_map ? (uint64_t)g.batch : 1;
+  const uint32_t box[3] = {64, BN, 1};
   if (!q8) {
-    const uint64_t bmap = a.batch_in_map ? (uint64_t)g.batch : 1;
-    const uint32_t box[3] = {64, BN, 1};
     const uint64_t ld[3] = {(uint64_t)g.rank, (uint64_t)g.t_max, bmap};
     const uint64_t ls[2] = {(uint64_t)g.latent_row_stride * 2,
                             (a.batch_in_map ? (uint64_t)g.latent_batch_stride : (uint64_t)g.t_max * g.latent_row_stride) * 2};
-    const uint64_t rd[3] = {(uint64_t)g.rope_dim, (uint64_t)g.t_max, bmap};
-    const uint64_t rs[2] = {(uint64_t)g.rope_row_stride * 2,
-                            (a.batch_in_map ? (uint64_t)g.rope_batch_stride : (uint64_t)g.t_max * g.rope_row_stride) * 2};
-    if (!encode_tmap_bf16(&lat_map, g.latent, 3, ld, ls, box) || !encode_tmap_bf16(&rope_map, g.rope, 3, rd, rs, box))
-      return cudaErrorInvalidValue;
+    if (!encode_tmap_bf16(&lat_map, g.latent, 3, ld, ls, box)) return cudaErrorInvalidValue;
   }
+  const uint64_t rd[3] = {(uint64_t)g.rope_dim, (uint64_t)g.t_max, bmap};
+  const uint64_t rs[2] = {(uint64_t)g.rope_row_stride * 2,
+                          (a.batch_in_map ? (uint64_t)g.rope_batch_stride : (uint64_t)g.t_max * g.rope_row_stride) * 2};
+  if (!encode_tmap_bf16(&rope_map, g.rope, 3, rd, rs, box)) return cudaErrorInvalidValue;
   auto* const kernel = q8 ? tc_key_weights_kernel<true> : tc_key_weights_kernel<false>;
   const int smem = q8 ? SMEM_BYTES_Q8 : SMEM_BYTES;
   const cudaError_t ea = set_max_dynamic_smem(kernel, smem);

@@ -7,8 +7,8 @@
 // with cp.async into one of two slots of its own, so nothing but its own
 // wait_group lies between the copy and the conversion, and a window and a
 // selection are the same work.  (Codes fetched into registers a tile ahead took
-// 220 us on a ragged decode of 32 rows, 498,051 keys, against 165: the fence
-// that publishes a tile also waits for the loads in flight.)
+// 220 us on a ragged decode of 32 rows, 498,051 keys, against 165 then: the
+// fence that publishes a tile also waits for the loads in flight.)
 //
 // kLanes lanes (16 or 32) take one key and kThreads threads take 64 / kIters
 // keys at once: piece i of a thread belongs to key i * kStep + key0.  Lane c
@@ -46,14 +46,13 @@ template <int kLanes, int kThreads>
 struct Q8Fetch {
   static constexpr int kStep = kThreads / kLanes;         // keys taken at once
   static constexpr int kIters = kTileKeys / kStep;        // pieces of codes per thread and tile
-  static constexpr int kRopeIters = kIters / 4;           // and of rope keys
   static constexpr int kPieceBytes = 16 * kThreads;
   static constexpr int kSlotBytes = kIters * kPieceBytes;
   static_assert(kStep % 8 == 0 && kIters >= 4 && kIters <= 8, "fixed swizzle; lanes to look the keys up");
   uint32_t slot0;                // shared address of this thread's first piece
   uint32_t codes0;               // and of the codes that it decodes
   int key0;                      // key of piece i is i * kStep + key0
-  int rope_group;                // rope piece j belongs to this thread's key 4j + rope_group
+  int rope_group;                // this thread's rope piece belongs to its key rope_group
   int peers;                     // first lane of the lanes that share this lane's keys
   int mine;                      // piece whose position and exponent this lane looks up (lane % kIters)
 
@@ -99,7 +98,7 @@ struct Q8Fetch {
   }
   // This thread's rope piece of one tile (one per thread), zeros for no key.
   __device__ __forceinline__ uint4 load_rope(const Q8Rows& r, int pos) const {
-    static_assert(kRopeIters == 1, "one piece per thread");
+    static_assert(kIters == 4, "one piece per thread");
     const int p = __shfl_sync(0xffffffffu, pos, peers + rope_group);
     return p >= 0 ? __ldg(reinterpret_cast<const uint4*>(r.rope + (int64_t)(r.start + p) * r.rope_stride)) : make_uint4(0, 0, 0, 0);
   }

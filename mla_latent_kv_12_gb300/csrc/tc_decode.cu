@@ -70,19 +70,18 @@ constexpr int HEADS = 128, RANK = 512, DV = 256;  // DV: latent dims per CTA
 constexpr int THREADS = 352, THREADS_GATHER = THREADS + 96;
 constexpr int kGatherWarp = 11;   // first extra gather warp
 // The instance for an 8-bit cache: eight warps fetch the codes of each tile
-// and write their fp16 values into the stage ring (q8_tiles.cuh): three
-// stages, the fourth's memory holds the fetch's two slots.  (Four stages, one
-// slot of codes refilled by halves and rope keys by TMA: the ragged decode of
-// 32 rows 175 us against 165, verify 601 against 554.  The SM's issue slots are
-// what the roles share, and converting further ahead slows the softmax.)
+// and write their fp16 values into the stage ring (q8_tiles.cuh); one more warp
+// loads the rope keys by TMA.  The fetch's two slots take the memory of one of
+// the buffers for a CTA's own scores.  (Three stages, with rope keys in the
+// slots and both buffers: the ragged decode of 32 rows, 498,051 keys, 167 us
+// against 152, verify of 8 x 4 tokens of 65536 555 against 488.)
 // Roles are whole warpgroups, whose registers are redistributed at their
 // start: the softmax and exchange warps take what the MMA and converting warps
 // do not need.  The shares (per thread and warpgroup) add up to the launch's,
 // kRegsLaunch for each of the five.
 constexpr int THREADS_Q8 = 640;
 constexpr int kConvertWarps = 8;
-constexpr int STAGES_Q8 = 4;
-constexpr int kTilesAhead = 6;    // tiles ahead that a window's rows are pulled into L2
+constexpr int kTilesAhead = 6;    // tiles ahead that a window's rope keys are pulled into L2
 constexpr int kRegsLaunch = 96;
 constexpr int kRegsSoftmax = 144, kRegsExchange = 128, kRegsIssue = 48, kRegsConvert = 80;
 static_assert(kRegsSoftmax + kRegsExchange + kRegsIssue + 2 * kRegsConvert <= 5 * kRegsLaunch, "more registers than the launch has");
@@ -91,7 +90,7 @@ using DecodeFetch = Q8Fetch<16, 32 * kConvertWarps>;
 // 1024-byte alignment of the extern declaration places it on a 1024-byte
 // boundary after the static variables (checked at run time).
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 4 * XH_BYTES;
-constexpr int SMEM_BYTES_Q8 = STAGES_Q8 * STAGE_BYTES + 3 * XH_BYTES + 2 * DecodeFetch::kSlotBytes;
+constexpr int SMEM_BYTES_Q8 = STAGES * STAGE_BYTES + 3 * XH_BYTES + 2 * DecodeFetch::kSlotBytes;
 constexpr uint32_t TM_O = 0, TM_Q = 256, TM_S = 400, TM_P = 464;  // TMEM columns (Q: 128 + 16)
 constexpr long long kWaitLimit = 1LL << 32;  // clock cycles (~2 s)
 constexpr float kRescaleThreshold = 8.0f;    // log2 units
@@ -468,7 +467,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_decode_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_constant__ CUtensorMap rope_map,
                      const __grid_constant__ CUtensorMap lat_rows_map, const __grid_constant__ CUtensorMap rope_rows_map,
                      const __grid_constant__ TcDecodeArgs a) {
-  constexpr int kStages = kQ8 ? STAGES_Q8 : STAGES;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if ((smem_u32(smem_raw) & 1023u) != 0) {   // the same in every CTA: nothing waits on anything yet
     if (threadIdx.x == 0 && a.status) atomicOr(a.status, MLA_DEVICE_LAYOUT);
@@ -478,11 +476,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* stages = smem;
   // Exchange buffers, each [8][128 heads][16 B] of fp16 scores: xin[b] is written
   // by the peer's remote stores, xout[b] holds this CTA's own half for its
-  // softmax warps.
-  uint8_t* xin = smem + kStages * STAGE_BYTES;        // 2 x XH_BYTES
+  // softmax warps (8-bit cache: xout[0] alone).
+  uint8_t* xin = smem + STAGES * STAGE_BYTES;        // 2 x XH_BYTES
   uint8_t* xout = xin + 2 * XH_BYTES;                // 2 x XH_BYTES
 
-  __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];
+  __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES];
   __shared__ __align__(8) uint64_t s_full, s_free, p_full, q_full, o_free, mma_drain, pv_drain;
   __shared__ __align__(8) uint64_t x_full[2], x_free[2], xo_free[2];  // per exchange buffer
   __shared__ uint32_t tmem_base_s;
@@ -512,7 +510,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&rope_rows_map);
       }
     }
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full_bar[s], kQ8 ? kConvertWarps + 1 : (gather && !a.gather_tma) ? 32 : 1);
       mbar_init(&empty_bar[s], 1);
     }
@@ -624,7 +622,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         ++tile;
-        if (++stage == kStages) stage = 0, phase ^= 1u;
+        if (++stage == STAGES) stage = 0, phase ^= 1u;
       }
       if (aborted()) break;
       ++seg;
@@ -663,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         ++tile;
-        if (++stage == kStages) stage = 0;
+        if (++stage == STAGES) stage = 0;
       }
       if (aborted()) break;
       ++seg;
@@ -675,8 +673,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   // The 8-bit cache's rope keys, which need no conversion: whole tiles of a
   // window go to their stage by TMA, beside the converting warps, who write those of
-  // selections and of a window's last tile.  The rows of a later tile are
-  // pulled into L2.
+  // selections and of a window's last tile.
   auto load_rope_tiles = [&]() {
     int stage = 0, fills = 0;
     uint32_t phase = 0;
@@ -689,7 +686,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool window = !gather || a.sel_count[n] == -1;
       const int z = a.batch_in_map ? b : 0;
       for (int t = t0; t < t1; ++t) {
-        if (fills >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
+        if (fills >= STAGES && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
         ++fills;
         if (lane == 0) {
           if (window && (t + 1) * BN <= keys) {
@@ -703,12 +700,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tma_prefetch_l2_3d(&rope_map, 32 * (int)rank, start + (t + kTilesAhead) * BN, z);
         }
         __syncwarp();
-        if (++stage == kStages) stage = 0, phase ^= 1u;
+        if (++stage == STAGES) stage = 0, phase ^= 1u;
       }
     }
     // every load lands before this CTA may exit
-    for (int k = fills > kStages ? fills - kStages : 0; k < fills; ++k)
-      mbar_wait_warp(&full_bar[k % kStages], (uint32_t)(k / kStages) & 1u, kWaitLimit);
+    for (int k = fills > STAGES ? fills - STAGES : 0; k < fills; ++k)
+      mbar_wait_warp(&full_bar[k % STAGES], (uint32_t)(k / STAGES) & 1u, kWaitLimit);
   };
 
   if (kQ8 && warp >= kScoreWarp && warp < kConvertWarp) {
@@ -777,7 +774,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       pos = fetch.my_position(rows, t0 + 2);
       for (int t = t0; t < t1; ++t) {
         const int slot = (t - t0) & 1;
-        if (fills++ >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
+        if (fills++ >= STAGES && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
         fetch.check_exponent(rows.status, e_now);
         cp_async_wait<1>();   // this tile's pieces
         const uint32_t off = stage * STAGE_BYTES;
@@ -795,7 +792,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           pos = fetch.my_position(rows, t + 3);
         }
         cp_async_commit();
-        if (++stage == kStages) stage = 0, phase ^= 1u;
+        if (++stage == STAGES) stage = 0, phase ^= 1u;
       }
       cp_async_wait<0>();   // the slots are free for the next segment
       __syncwarp();
@@ -804,11 +801,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ============================================================ producer
     int stage = 0;
     uint32_t phase = 0;
-    uint32_t issued_phase[kStages];
-    bool issued[kStages];
+    uint32_t issued_phase[STAGES];
+    bool issued[STAGES];
 #pragma unroll
-    for (int s = 0; s < kStages; ++s) issued[s] = false, issued_phase[s] = 0;
-    int fills = 0;   // the ring's first kStages fills need no free slot
+    for (int s = 0; s < STAGES; ++s) issued[s] = false, issued_phase[s] = 0;
+    int fills = 0;   // the ring's first STAGES fills need no free slot
     int u, n, t0, t1;
     bool whole;
     while (!aborted() && it.next(u, t0, t1, whole)) {
@@ -821,13 +818,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int32_t* list = (gather && a.sel_count[n] != -1) ? a.sel + (int64_t)n * a.k_max : nullptr;
       if (!gather && lane == 0) {
         // the segment's first tiles that the loop's look-ahead will not cover
-        for (int t = t0 + kStages; t < t0 + kPrefetchAhead && t < t1; ++t) {
+        for (int t = t0 + STAGES; t < t0 + kPrefetchAhead && t < t1; ++t) {
           for (int c = 0; c < 4; ++c) tma_prefetch_l2_3d(&lat_map, dim_base + 64 * c, start + t * BN, zb);
           tma_prefetch_l2_3d(&rope_map, 32 * (int)rank, start + t * BN, zb);
         }
       }
       for (int t = t0; t < t1 && !aborted(); ++t) {
-        if (fills++ >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
+        if (fills++ >= STAGES && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
         if (!gather) {
           if (lane == 0) {
             mbar_arrive_expect_tx(&full_bar[stage], STAGE_TX);
@@ -901,11 +898,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         issued[stage] = true;
         issued_phase[stage] = phase;
-        if (++stage == kStages) stage = 0, phase ^= 1u;
+        if (++stage == STAGES) stage = 0, phase ^= 1u;
       }
     }
     // Drain: every issued fill must land before this CTA may exit.
-    for (int s = 0; s < kStages; ++s)
+    for (int s = 0; s < STAGES; ++s)
       if (issued[s]) mbar_wait(&full_bar[s], issued_phase[s], kWaitLimit);
   } else if (!kQ8 && warp == kScoreWarp) {
     issue_scores();
@@ -931,12 +928,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int keys = keys_p[n];
         const int32_t* list = a.sel_count[n] != -1 ? a.sel + (int64_t)n * a.k_max : nullptr;
         for (int t = t0; t < t1 && !aborted(); ++t) {
-          if (fills++ >= kStages && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
+          if (fills++ >= STAGES && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
           const int g = issuer + kIssuers * lane;
           if (g < BN / 4)
             gather_key_group(a, &lat_rows_map, &rope_rows_map, stages + stage * STAGE_BYTES, &full_bar[stage], g, t,
                              b, start, limit, keys, list, rank, dim_base);
-          if (++stage == kStages) stage = 0, phase ^= 1u;
+          if (++stage == STAGES) stage = 0, phase ^= 1u;
         }
       }
     }
@@ -1121,12 +1118,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     x_free_peer[1] = mapa(smem_u32(&x_free[1]), peer);
     uint32_t tile = 0, seg = 0;
     // P.V(k) has completed once its commit arrives on the stage barrier
-    // empty_bar[k % kStages] (that barrier's (k / kStages)-th completion).  P.V's
-    // complete in order, and when P.V(k) is waited for, P.V(k - kStages) has
-    // been waited for already and P.V(k + kStages) cannot have started, so the
+    // empty_bar[k % STAGES] (that barrier's (k / STAGES)-th completion).  P.V's
+    // complete in order, and when P.V(k) is waited for, P.V(k - STAGES) has
+    // been waited for already and P.V(k + STAGES) cannot have started, so the
     // phase parity identifies the completion.
     auto wait_pv = [&](uint32_t k) -> bool {
-      return mbar_wait_warp(&empty_bar[k % kStages], (k / kStages) & 1u, kWaitLimit);
+      return mbar_wait_warp(&empty_bar[k % STAGES], (k / STAGES) & 1u, kWaitLimit);
     };
     int u, n, t0, t1;
     bool whole;

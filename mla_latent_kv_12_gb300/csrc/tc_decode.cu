@@ -1048,7 +1048,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // the peer's receive buffer: no staging round trip, no bulk copy.
         uint8_t* xo = xout + (kQ8 ? 0 : b) * XH_BYTES;
         const uint32_t xi = xin_peer + b * XH_BYTES;
-        if constexpr (kQ8) {
+        if constexpr (!kQ8) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int k = 8 * c + 2 * q;   // scores k, k+1
+              const float lo_raw = __uint_as_float(k < 32 ? sa[k] : sb[k - 32]);
+              const float hi_raw = __uint_as_float(k < 32 ? sa[k + 1] : sb[k - 31]);
+              half_max = fmax3(half_max, fabsf(lo_raw), fabsf(hi_raw));
+              // sent already scaled (log2 units): the softmax then only adds
+              const float2 sc = mul_f32x2(make_float2(lo_raw, hi_raw), make_float2(a.scale_log2, a.scale_log2));
+              const __half2 hv = __floats2half2_rn(fminf(fmaxf(sc.x, -65504.f), 65504.f), fminf(fmaxf(sc.y, -65504.f), 65504.f));
+              w[q] = *reinterpret_cast<const uint32_t*>(&hv);
+            }
+            *reinterpret_cast<uint4*>(xo + (c * 128 + h) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+            st_async_v4(xi + (uint32_t)((c * 128 + h) * 16), w[0], w[1], w[2], w[3], x_full_peer[b]);
+          }
+        } else {
           // Scores that fp16 cannot hold are rare: the tile's largest magnitude
           // decides once whether they are clamped (NaN stays NaN).
           float top = 0.f;
@@ -1063,33 +1081,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               sb[k] = __float_as_uint(clamp_nan(__uint_as_float(sb[k]), limit));
             }
           }
-        }
-        uint32_t w[8][4];
+          uint4 w[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+          for (int c = 0; c < 8; ++c) {
+            uint32_t v[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int k = 8 * c + 2 * q;   // scores k, k+1
-            const float lo_raw = __uint_as_float(k < 32 ? sa[k] : sb[k - 32]);
-            const float hi_raw = __uint_as_float(k < 32 ? sa[k + 1] : sb[k - 31]);
-            if constexpr (!kQ8) half_max = fmax3(half_max, fabsf(lo_raw), fabsf(hi_raw));
-            // sent already scaled (log2 units): the softmax then only adds
-            const float2 sc = mul_f32x2(make_float2(lo_raw, hi_raw), make_float2(a.scale_log2, a.scale_log2));
-            const __half2 hv = kQ8 ? __floats2half2_rn(sc.x, sc.y)
-                                   : __floats2half2_rn(fminf(fmaxf(sc.x, -65504.f), 65504.f), fminf(fmaxf(sc.y, -65504.f), 65504.f));
-            w[c][q] = *reinterpret_cast<const uint32_t*>(&hv);
+            for (int q = 0; q < 4; ++q) {
+              const int k = 8 * c + 2 * q;
+              const float2 raw = make_float2(__uint_as_float(k < 32 ? sa[k] : sb[k - 32]), __uint_as_float(k < 32 ? sa[k + 1] : sb[k - 31]));
+              const float2 sc = mul_f32x2(raw, make_float2(a.scale_log2, a.scale_log2));
+              const __half2 hv = __floats2half2_rn(sc.x, sc.y);
+              v[q] = *reinterpret_cast<const uint32_t*>(&hv);
+            }
+            w[c] = make_uint4(v[0], v[1], v[2], v[3]);
+            st_async_v4(xi + (uint32_t)((c * 128 + h) * 16), w[c].x, w[c].y, w[c].z, w[c].w, x_full_peer[b]);
           }
-          if constexpr (!kQ8) *reinterpret_cast<uint4*>(xo + (c * 128 + h) * 16) = make_uint4(w[c][0], w[c][1], w[c][2], w[c][3]);
-          st_async_v4(xi + (uint32_t)((c * 128 + h) * 16), w[c][0], w[c][1], w[c][2], w[c][3], x_full_peer[b]);
-        }
-        if constexpr (kQ8) {
-          // One buffer for our own half (the other's memory is the fourth
-          // stage's): the softmax warps have read the tile before, which they
-          // do first of all.
+          // One buffer for our own half: the softmax warps have read the tile
+          // before, which they do first of all.
           if (tile > 0 && !mbar_wait_warp(&xo_free[0], (tile - 1) & 1u, kWaitLimit)) { fail(); break; }
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            *reinterpret_cast<uint4*>(xo + (c * 128 + h) * 16) = make_uint4(w[c][0], w[c][1], w[c][2], w[c][3]);
+          for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(xo + (c * 128 + h) * 16) = w[c];
         }
         __syncwarp();
         // xout[b] is written by this warp; receive buffer b expects the peer's

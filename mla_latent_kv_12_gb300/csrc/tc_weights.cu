@@ -9,9 +9,9 @@
 // all 576 features itself and no SM pair is needed.  At one query token it is
 // bound by the cache read (1152 or 641 bytes against 147 kflop per key: 0.17
 // or 0.09 ns at the measured copy rate, 0.076 ns at the measured bf16 rate):
-// 32 rows, 498,051 keys, take 95 to 103 us over bf16 (5.6 to 6.1 TB/s) and 87
-// us over 8 bits (3.7 TB/s; the N = 64 MMAs alone, without conversion and fetch,
-// 66); four tokens of 8 rows of 16384 keys 91 and 116 us.
+// 32 rows, 498,051 keys, take 95 to 103 us over bf16 (5.6 to 6.1 TB/s) and 85
+// us over 8 bits (3.8 TB/s; the N = 64 MMAs alone, without conversion and fetch,
+// 66); four tokens of 8 rows of 16384 keys 91 and 110 us.
 //
 //  * One persistent CTA per SM takes an equal range of the flattened tiles of
 //    all rows.  With several query tokens a range is walked in chunks that

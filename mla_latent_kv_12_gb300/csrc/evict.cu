@@ -10,8 +10,8 @@
 // holds its slice's keys in shared memory where they fit, so the weights
 // are read once; the digit histograms are summed over the cluster through
 // distributed shared memory, every CTA taking the same digit.  Bound by the
-// latency of the passes, not by the 4 bytes per token: 15 us for one row of
-// 8192, 17.5 us for 32 rows of up to 32768, 27 us for one of 131072.
+// latency of the passes, not by the 4 bytes per token: 12 us for one row of
+// 8192, 17 us for 32 rows of up to 32768, 25 us for one of 131072.
 //
 // Compaction.  Kept positions ascend, so row j's source kept[j] >= j: rows are
 // moved in chunks of consecutive j, and a chunk is written only when all
@@ -52,33 +52,26 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return ~(bits ^ ((bits >> 31) ? 0xFFFFFFFFu : 0x80000000u));
 }
 
-// Exclusive prefixes of two counts over the block's threads (both below 2^31:
-// one scan of the pair packed in 64 bits).
-__device__ __forceinline__ int2 block_prefix(int a, int b, unsigned long long* warp_s) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned long long v = (unsigned long long)(uint32_t)b << 32 | (uint32_t)a;
-  unsigned long long inc = v;
+__device__ __forceinline__ int warp_inclusive(int v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long x = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += x;
+    const int x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
   }
-  if (lane == 31) warp_s[warp] = inc;
-  __syncthreads();
-  static_assert(kPlanWarps == 32, "one warp's sum per lane");
-  unsigned long long before = lane < warp ? warp_s[lane] : 0ull;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-  __syncthreads();
-  const unsigned long long r = before + inc - v;
-  return make_int2((int)(uint32_t)r, (int)(uint32_t)(r >> 32));
+  return v;
 }
 
 __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __grid_constant__ EvictParams p, int held) {
   extern __shared__ uint32_t keys_s[];   // `held` keys of this CTA's slice
   __shared__ __align__(8) int hist_s[3][kBins];   // one per pass: a peer may still read the previous one
-  __shared__ unsigned long long warp_s[kPlanWarps];
-  __shared__ int digit_s, rest_s, less_s, tie_s, last_s;
+  // per pass (written once, so that no barrier keeps a reader from a later writer)
+  __shared__ int total_s[3][kPlanWarps], peers_s[3][kPlanWarps];   // of each warp's bins: the cluster's, and the earlier CTAs'
+  struct Found {
+    int digit, rest, less, tie, last;
+  };
+  __shared__ Found found_s[3];
+  __shared__ int less_s[kPlanWarps], tie_s[kPlanWarps];
+  static_assert(kPlanWarps == 32, "one warp's sum per lane");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // (the compaction's CTAs may take their places already: they wait for this grid's end)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -114,6 +107,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
     for (int i = threadIdx.x; i < 3 * kBins; i += kPlanThreads) hist_s[0][i] = 0;
     __syncthreads();
     int known = 0;   // leading key bits fixed so far
+#pragma unroll
     for (int pass = 0; pass < 3; ++pass) {
       const int width = pass < 2 ? 11 : 10, shift = 32 - known - width;
       int* hist = hist_s[pass];
@@ -128,6 +122,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
         }
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) {
+          if (base + u * kPlanThreads >= hi) break;   // (the same in the whole block)
           const int i = base + u * kPlanThreads + threadIdx.x;
           if (pass == 0 && in_smem && i < hi) keys_s[i - lo] = key[u];
           const bool counts = i < hi && (pass == 0 || (key[u] >> (32 - known)) == prefix);
@@ -145,7 +140,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
         }
       }
       tc::cluster_sync();   // every CTA's histogram is complete
-      // thread t sums bins 2t and 2t + 1 over the cluster; the one whose bins hold the rest-th key takes it
+      // thread t sums bins 2t and 2t + 1 over the cluster
       const int nb = 1 << width, b0 = 2 * threadIdx.x;
       int h[2] = {0, 0}, e[2] = {0, 0};   // the cluster's, and the earlier CTAs'
       if (b0 < nb) {
@@ -159,29 +154,33 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
           if (c < (int)crank) e[0] += part[c].x, e[1] += part[c].y;
         }
       }
-      const int2 sums = block_prefix(h[0] + h[1], e[0] + e[1], warp_s);
-      int before = sums.x, less = sums.y;
+      const int hs = h[0] + h[1], es = e[0] + e[1];
+      const int ht = __reduce_add_sync(0xffffffffu, hs), et = __reduce_add_sync(0xffffffffu, es);
+      if (lane == 0) total_s[pass][warp] = ht, peers_s[pass][warp] = et;
+      __syncthreads();
+      const int total = total_s[pass][lane], upto = warp_inclusive(total, lane);
+      const int holder = __ffs(__ballot_sync(0xffffffffu, upto >= rest)) - 1;   // the warp whose bins hold the rest-th key
+      if (warp == holder) {
+        int before = __shfl_sync(0xffffffffu, upto - total, holder) + warp_inclusive(hs, lane) - hs;
+        int less = __reduce_add_sync(0xffffffffu, lane < holder ? peers_s[pass][lane] : 0) + warp_inclusive(es, lane) - es;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (before < rest && rest <= before + h[k]) {   // exactly one thread and bin
-          digit_s = b0 + k;
-          rest_s = rest - before;
-          last_s = rest - before == h[k];   // all keys with this digit are kept
-          less_s = less;
-          tie_s = e[k];
+        for (int k = 0; k < 2; ++k) {
+          // (exactly one thread and bin; the last pass when all keys with this digit are kept)
+          if (before < rest && rest <= before + h[k])
+            found_s[pass] = Found{b0 + k, rest - before, less, e[k], rest - before == h[k]};
+          before += h[k];
+          less += e[k];
         }
-        before += h[k];
-        less += e[k];
       }
       __syncthreads();
-      prefix = (prefix << width) | (uint32_t)digit_s;
-      rest = rest_s;
-      peers_less += less_s;
-      peers_tie = tie_s;
+      const Found found = found_s[pass];
+      prefix = (prefix << width) | (uint32_t)found.digit;
+      rest = found.rest;
+      peers_less += found.less;
+      peers_tie = found.tie;
       known += width;
       drop = 32 - known;
-      if (last_s) break;   // (the same in the whole cluster)
-      __syncthreads();   // (read before the next pass writes them)
+      if (found.last) break;   // (the same in the whole cluster)
     }
   }
   // The last reads of other CTAs' shared memory are done: no CTA leaves before all have arrived here.
@@ -199,9 +198,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) evict_plan_kernel(const __gri
       n_less += __popc(__ballot_sync(0xffffffffu, i < whi && key < prefix));
       n_tie += __popc(__ballot_sync(0xffffffffu, i < whi && key == prefix));
     }
-  const int2 sums = block_prefix(lane == 0 ? n_less : 0, lane == 0 ? n_tie : 0, warp_s);
-  const int before_less = __shfl_sync(0xffffffffu, sums.x, 0) + peers_less;
-  const int before_tie = __shfl_sync(0xffffffffu, sums.y, 0) + peers_tie;
+  if (lane == 0) less_s[warp] = n_less, tie_s[warp] = n_tie;
+  __syncthreads();
+  const int before_less = __reduce_add_sync(0xffffffffu, lane < warp ? less_s[lane] : 0) + peers_less;
+  const int before_tie = __reduce_add_sync(0xffffffffu, lane < warp ? tie_s[lane] : 0) + peers_tie;
   if (take > 0) {
     int out = p.n_sink + before_less + min(before_tie, rest), ties = before_tie;
     const uint32_t below = (1u << lane) - 1u;
@@ -387,9 +387,9 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, int threads, int
 }  // namespace
 
 cudaError_t launch_evict_plan(const EvictParams& p, cudaStream_t stream) {
-  // CTAs per row: one per 4096 candidates of the longest possible row, at most
+  // CTAs per row: one per 2048 candidates of the longest possible row, at most
   // 8, and few enough that all rows run at once.
-  const int64_t most = p.t_max < 4096 ? 1 : p.t_max / 4096;
+  const int64_t most = p.t_max < 2048 ? 1 : p.t_max / 2048;
   int ncta = 1;
   while (ncta * 2 <= kMaxCluster && ncta * 2 <= most && (int64_t)ncta * 2 * p.batch <= device_sm_count()) ncta *= 2;
   // a row's slice is at most ceil(t_max / ncta), rounded up to 32

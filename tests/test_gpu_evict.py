@@ -471,3 +471,25 @@ def test_every_row_empty(mla):
     assert int(st) == 0 and plan_status == 0 and counts.tolist() == [-1] * 3 and out.tolist() == [0] * 3
     for a, b in ((w, w0), (codes, c0), (scales, e0), (latent, l0)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("shared", ["rope", "codes", "both"])
+def test_rows_that_share_a_buffer(mla, shared):
+    """Batch rows over one codes or rope buffer (a batch stride of zero), at different windows."""
+    g = gen(95)
+    B, T, block = 3, 300, 4
+    q, codes, scales, rope, start, length = attend_case(g, B, 1, 128, T, block, [300, 70, 129], [0, 8, 12])
+    if shared != "rope":
+        codes, scales = codes[:1].expand(B, T, 512), scales[:1].expand(B, -1)
+    if shared != "codes":
+        rope = rope[:1].expand(B, T, 64)
+    ctx, lse, st = torch.empty(B, 128, 512, dtype=torch.bfloat16, device=DEV), torch.empty(B, 128, device=DEV), status()
+    mla.decode_attend_q8(q, codes, scales, block, rope, start, length, B, 1, SCALE, ctx, lse, device_status=st)
+    check_attend(ctx, lse, (q, codes, scales, rope, start, length), block, 1)
+    lat = [R.held64(codes[b].cpu().numpy(), scales[b].cpu().numpy(), block) for b in range(B)]
+    exact = make_lse(q, lat, rope, start, length, 1)
+    w = torch.exp(normal(g, B, T))
+    before = w.clone()
+    mla.key_weights_q8(q, codes, scales, block, rope, exact, start, length, B, 1, SCALE, w, n_new=1, device_status=st)
+    check_weights(w, before, q, lat, rope, exact, start, length, 1, 1.0, 1)
+    assert int(st) & ~mla.DEVICE_SCORE_RANGE == 0

@@ -52,11 +52,13 @@ constexpr int kThreads = 32 * kConvertWarp, kThreadsQ8 = kThreads + kConvertThre
 using WeightFetch = Q8Fetch<32, kConvertThreads>;
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES, SMEM_BYTES_Q8 = STAGES_Q8 * STAGE_BYTES + 2 * WeightFetch::kSlotBytes;
 constexpr long long kWaitLimit = 1LL << 32;   // clock cycles (~2 s)
-// Tiles that several query tokens share before the next ones are read, so that
-// they stay in the 129 MB L2: 152 CTAs x 8 tiles x 72 KB = 88 MB, 152 x 15 x 40
-// KB = 91 MB of an 8-bit cache.  (A pass begins with a drained pipeline and its
-// query's load.)
-constexpr int kChunkTiles = 8, kChunkTilesQ8 = 15;
+// Tiles that several query tokens share before the next ones are read.  A pass
+// begins with a drained pipeline, so chunks are as long as the L2 (129 MB)
+// allows: 152 CTAs x 8 tiles x 72 KB = 88 MB; from 11 on full chunks are read
+// from memory again (four tokens of 8 rows of 14592 keys: 77 us with 8 or 10,
+// 91 with 12).  An 8-bit cache's passes are slower than its reads from memory:
+// chunks of 28 tiles (4 rows of 65536 keys: 179 us with 15, 169 with 28 and 60).
+constexpr int kChunkTiles = 8, kChunkTilesQ8 = 28;
 constexpr int kRopeAhead = 6;      // tiles ahead that an 8-bit cache's rope keys are pulled into L2
 constexpr int kWeightsAhead = 8;   // tiles ahead that weights are pulled into L2
 

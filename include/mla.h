@@ -530,10 +530,12 @@ int mla_prefill_attend(const void* q_nope, int64_t q_nope_row_stride, int64_t q_
  * the largest magnitude is at most 448; a block that already holds tokens of
  * the window keeps its unit or takes a larger one, and its codes are then
  * rounded again to the larger unit (exact but for what falls below e4m3's
- * smallest step).  Codes round to nearest, ties to even.  A magnitude beyond
- * 57344 (or infinite) saturates and sets MLA_DEVICE_VALUE_RANGE; NaN stays
- * NaN and sets no unit.  kv_len_out may alias kv_len and row_offsets.  At most
- * 65535 batch rows.
+ * smallest step).  Codes round to nearest, ties to even.  A normalised
+ * magnitude beyond 57344 (or infinite) saturates and sets
+ * MLA_DEVICE_VALUE_RANGE; NaN stays NaN, sets no unit and no flag.  (A token
+ * with a NaN element, and one of zeros at eps = 0, is NaN after the norm; one
+ * with an infinite element is NaN there and 0 elsewhere.)  kv_len_out may
+ * alias kv_len and row_offsets.  At most 65535 batch rows.
  *
  * mla_quantize_cache: the windows of a latent buffer [b, r, rank] (dtype f32 or
  * bf16) into codes and exponents, rows outside the windows left as they

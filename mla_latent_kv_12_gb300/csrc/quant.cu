@@ -352,7 +352,8 @@ __global__ void __launch_bounds__(kHeldWarps * 32, sizeof(TI) == 2 ? 2 : 1) enco
     for (int k = 0; k < kHeldRows; ++k) {
       // (non-negative: ordered as integers)
       amax[k] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax[k])));
-      if constexpr (kNorm) amax[k] *= inv[k];
+      // NaN sets no unit: a token with a NaN or infinite element, or of zeros at eps = 0, has no finite inv.
+      if constexpr (kNorm) amax[k] = fmaxf(amax[k] * inv[k], 0.f);
       if (!warp_blocks && lane == 0 && mine(k)) atomicMax(&amax_s[(r0 + k) >> p.block_shift], __float_as_uint(amax[k]));
     }
     if (warp_blocks) {

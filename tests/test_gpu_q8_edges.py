@@ -1,0 +1,98 @@
+"""The 8-bit cache where it can go wrong: non-finite tokens, dominant keys, wide rope keys, far positions, and
+weights from the attention's own lse."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import q8_reference as R
+from tests.test_gpu_q8 import DEV, EPS, THETA, gen, i32, normal, random_cache, status
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mla():
+    from mla_latent_kv_12_gb300 import mla
+    return mla
+
+
+# ---------------------------------------------------------------- append
+
+# encode_kernel serves aligned ranks up to 512, encode_walk_kernel the others
+SHAPES = [(512, torch.bfloat16), (512, torch.float32), (96, torch.bfloat16), (1024, torch.bfloat16), (33, torch.float32)]
+
+
+def normalised(raw, gain, eps):
+    with np.errstate(invalid="ignore", divide="ignore", over="ignore"):
+        return R.rms_norm64(R.as64(raw), R.as64(gain), eps)
+
+
+def append_into_partly_filled_blocks(mla, raw, gain, eps, block, slack=1e-5):
+    """Appends raw [2, s_new, rank] behind 37 tokens of row 0 and at the front of row 1, and checks every code
+    and exponent against 64 bits: a NaN value is held as NaN and sets no unit.  (The slack is that of the f32 norm,
+    as for other appends.)  Returns the status."""
+    B, s_new, rank = raw.shape
+    T = 160
+    codes, scales = random_cache(gen(block), B, T, rank, block)
+    rope = torch.zeros(B, T, 8, dtype=raw.dtype, device=DEV)
+    start, length = [block, 0], [37, 0]
+    codes0, scales0 = codes.cpu().numpy(), scales.cpu().numpy()
+    st = status()
+    mla.append_compressed_q8(raw, torch.zeros(B, s_new, 8, dtype=raw.dtype, device=DEV), gain, eps, THETA, codes, scales,
+                             block, rope, i32(start), i32(length), device_status=st)
+    codes1, scales1 = codes.cpu().numpy(), scales.cpu().numpy()
+    v = normalised(raw, gain, eps)
+    for b in range(B):
+        lo = start[b] + length[b]
+        hi = lo + s_new
+        same = np.r_[0:lo, hi:T]
+        for k in range(lo // block, (hi - 1) // block + 1):
+            r0, r1, old0 = max(lo, k * block), min(hi, (k + 1) * block), max(k * block, start[b])
+            want = v[b, r0 - lo:r1 - lo]
+            size = np.abs(want)
+            amax = size[~np.isnan(size)].max(initial=0.0)
+            allowed = {R.exponent64(amax * (1 - slack)), R.exponent64(amax * (1 + slack))}
+            if old0 < lo:
+                allowed = {max(a, int(scales0[b, k])) for a in allowed}
+            e = int(scales1[b, k])
+            assert e in allowed
+            units = want * 2.0 ** (127.0 - e)
+            got = R.codes64(codes1[b, r0:r1])
+            assert np.array_equal(np.isnan(got), np.isnan(units))
+            fine = np.isfinite(units)
+            assert (np.abs(got - units)[fine] <= (np.abs(R.nearest_e4m3(units) - units) + 2 * slack * np.abs(units))[fine]).all()
+            assert np.array_equal(got[np.isinf(units)], np.copysign(448.0, units[np.isinf(units)]))
+            if old0 < lo:
+                held = R.codes64(codes0[b, old0:lo]) * 2.0 ** (float(scales0[b, k]) - e)
+                assert np.array_equal(R.codes64(codes1[b, old0:lo]), R.nearest_e4m3(held))
+                same = np.setdiff1d(same, np.arange(old0, lo))
+        assert np.array_equal(codes1[b, same], codes0[b, same])
+    return int(st)
+
+
+@pytest.mark.parametrize("bad", ["nan", "inf", "-inf", "zero, eps 0"])
+@pytest.mark.parametrize("block", [1, 4, 8, 64])
+@pytest.mark.parametrize("rank,dtype", SHAPES)
+def test_append_of_a_token_without_a_norm(mla, rank, dtype, block, bad):
+    """One new token that is NaN after its norm leaves the unit, the tokens beside it and those held before alone."""
+    g = gen(rank + block)
+    raw = normal(g, 2, 6, rank).to(dtype)
+    gain = torch.exp(0.3 * normal(g, rank)).to(dtype)
+    eps = EPS
+    if bad == "zero, eps 0":
+        raw[0, 1], raw[1, 0], eps = 0.0, 0.0, 0.0
+    else:
+        raw[0, 1, 5] = raw[1, 0, rank - 1] = float(bad)
+    assert append_into_partly_filled_blocks(mla, raw, gain, eps, block) == 0
+
+
+@pytest.mark.parametrize("block", [1, 8])
+@pytest.mark.parametrize("rank,dtype", SHAPES)
+def test_append_of_infinite_values(mla, rank, dtype, block):
+    """An infinite norm weight: those values saturate at 57344 and are flagged."""
+    g = gen(rank + block)
+    gain = torch.ones(rank, device=DEV, dtype=dtype)
+    gain[7] = float("inf")
+    assert append_into_partly_filled_blocks(mla, normal(g, 2, 6, rank).to(dtype), gain, EPS, block) == mla.DEVICE_VALUE_RANGE

@@ -574,8 +574,13 @@ int mla_dequantize_cache(const uint8_t* codes, int64_t codes_row_stride, int64_t
  * of 2^-24 (zero for units of 2^-25 and less), and a block read with a unit
  * below 2^-15 and above the smallest, 2^-63 (that of zeros), sets
  * MLA_DEVICE_VALUE_RANGE.  Query values are exact from 2^-14 to 65504 in
- * magnitude, multiples of 2^-24 below; larger ones saturate and set
- * MLA_DEVICE_VALUE_RANGE.  mla_key_weights_q8 takes its operands the same way.
+ * magnitude, multiples of 2^-24 below (not flagged: a score q . k moves by at
+ * most 2^-25 times the sum of the key's latent magnitudes, before
+ * softmax_scale); larger ones saturate and set MLA_DEVICE_VALUE_RANGE.
+ * mla_key_weights_q8 takes its operands the same way.  Probabilities are
+ * taken relative to a key at most 2^8 lighter than the heaviest read so far in
+ * the row's piece; they round to 2^-11 of themselves down to 2^-21 of that
+ * key's, and to multiples of 2^-31 of it below.
  */
 int mla_decode_attend_q8(const void* q, int64_t q_row_stride, int64_t q_head_stride, const uint8_t* codes,
                          int64_t codes_row_stride, int64_t codes_batch_stride, const uint8_t* scales,

@@ -94,6 +94,14 @@ constexpr int SMEM_BYTES_Q8 = STAGES * STAGE_BYTES + 3 * XH_BYTES + 2 * DecodeFe
 constexpr uint32_t TM_O = 0, TM_Q = 256, TM_S = 400, TM_P = 464;  // TMEM columns (Q: 128 + 16)
 constexpr long long kWaitLimit = 1LL << 32;  // clock cycles (~2 s)
 constexpr float kRescaleThreshold = 8.0f;    // log2 units
+// The 8-bit instance's P is fp16, and p reaches 2^kRescaleThreshold: p is held
+// 2^kRaiseF16 times larger, up to 2^15, so that the keys lighter than the
+// reference by up to 2^21 keep all of fp16's bits (2^-11); below, p rounds to
+// multiples of 2^-31 of the reference's weight.  (Unraised, a key 2^22 lighter
+// than the heaviest of its piece was off by up to a tenth.)  The sum l holds the
+// same factor, and m less kRaiseF16 stands for it in the lse and the partials.
+constexpr float kRaiseF16 = 7.0f;
+static_assert(kRescaleThreshold + kRaiseF16 < 16.0f, "p in the fp16 range");
 // A group's tile range is at least this long: each split writes a 256 KB f32
 // partial, worth it only against a few 72 KB tiles of cache read.
 constexpr int kMinTilesPerGroup = 4;
@@ -1153,6 +1161,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int limit = a.plan_in_kernel ? row_limit_s[n] : row_limit(a, n);
       const int32_t* list = (gather && a.sel_count[n] != -1) ? a.sel + (int64_t)n * a.k_max : nullptr;
       float m_used = -CUDART_INF_F, l = 0.f;
+      constexpr float kRaise = kQ8 ? kRaiseF16 : 0.f;   // l is 2^kRaise times the sum relative to m_used
       bool first_tile = true;
       bool p_pending = false;   // kLateP: the previous tile's P is not yet announced
       // Selected positions of the lane's two entries of the next tile, read a
@@ -1253,13 +1262,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---- online softmax with lazy rescaling: the reference moves only
         // when the tile maximum exceeds it by more than the threshold (or on
         // the first visible entry); p = 2^(x - shift).
-        float alpha = 1.f, shift = 0.f;
+        float alpha = 1.f, shift = -kRaise;
         bool rescale = false;
         if (mx != -CUDART_INF_F && (mx > kRescaleThreshold || m_used == -CUDART_INF_F)) {
           alpha = (m_used == -CUDART_INF_F) ? 0.f : ex2_approx(-mx);
           rescale = !first_tile && m_used != -CUDART_INF_F;
           m_used = m_ref + mx;
-          shift = mx;
+          shift = mx - kRaise;
         }
         uint32_t pk[32];
         float2 ps2[8];
@@ -1271,7 +1280,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const float p0 = ex2_approx(xs.x);
           const float p1 = ex2_approx(xs.y);
           ps2[(k >> 1) & 7] = add_f32x2(ps2[(k >> 1) & 7], make_float2(p0, p1));
-          if constexpr (kQ8) {   // (p is at most 2^kRescaleThreshold)
+          if constexpr (kQ8) {   // (p is at most 2^(kRescaleThreshold + kRaiseF16))
             const __half2 ph = __floats2half2_rn(p0, p1);
             pk[k >> 1] = *reinterpret_cast<const uint32_t*>(&ph);
           } else {
@@ -1358,7 +1367,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           });
         }
         if (rank == 0 && a.lse)
-          a.lse[(int64_t)n * a.heads + h] = l != 0.f ? (m_used + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+          a.lse[(int64_t)n * a.heads + h] =
+              l != 0.f ? ((m_used - kRaise) + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
       } else {
         // Partial as [slot][RANK/8][H] entries of 8 fp16 dims: this piece's
         // context normalised by its own sum (O / l, an average of latent
@@ -1369,7 +1379,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // cache stream would otherwise push the early pieces out to DRAM.
         const float inv = l != 0.f ? 1.f / l : 0.f;
         // m of the piece: -inf marks an empty one, so a sum of NaN alone gets a finite one
-        const float m_piece = l == 0.f ? -CUDART_INF_F : (kQ8 && m_used == -CUDART_INF_F) ? 0.f : m_used;
+        const float m_piece = l == 0.f ? -CUDART_INF_F : (kQ8 && m_used == -CUDART_INF_F) ? 0.f : m_used - kRaise;
         const uint64_t keep = l2_policy_evict_last();
         uint4* dst = a.ws_o + (slot * (RANK / 8) + dim_base / 8) * HEADS + h;
         float vmax = 0.f;

@@ -96,3 +96,38 @@ def test_append_of_infinite_values(mla, rank, dtype, block):
     gain = torch.ones(rank, device=DEV, dtype=dtype)
     gain[7] = float("inf")
     assert append_into_partly_filled_blocks(mla, normal(g, 2, 6, rank).to(dtype), gain, EPS, block) == mla.DEVICE_VALUE_RANGE
+
+
+# ---------------------------------------------------------------- attention
+
+@pytest.mark.parametrize("gap", [21.625, 23.375, 26.625])
+def test_attend_light_keys_behind_a_heavy_one(mla, gap):
+    """One key 2^gap times heavier than 16384 equal ones, its latent zero: the context is that of the light keys.
+    80 rows over one buffer, so that a piece holds thousands of keys.
+
+    Scores are exact (one rope feature, log2 units).  p rounds to 2^-11 of itself, or to half of 2^-31 of the heavy
+    key's weight; a piece's context to fp16 (2^-11, 2^-25 below its normal range); sums of positive f32 values,
+    accumulated 16 keys a step, to 2^-23 per step and 2^-24 per tile."""
+    g = gen(int(8 * gap))
+    B, T, heads = 80, 16385, 64
+    codes, scales = random_cache(g, 1, T, 512, 1)
+    codes = codes & 0x7F                                  # positive latents: no cancellation
+    codes[0, 0] = 0
+    rope = torch.zeros(1, T, 64, dtype=torch.bfloat16, device=DEV)
+    rope[0, 0, 0] = gap
+    q = torch.zeros(B, heads, 576, dtype=torch.bfloat16, device=DEV)
+    q[..., 512] = 1.0
+    ctx, lse, st = torch.empty(B, heads, 512, device=DEV), torch.empty(B, heads, device=DEV), status()
+    mla.decode_attend_q8(q, codes, scales, 1, rope, None, i32([T] * B), B, 1, math.log(2.0), ctx, lse, device_status=st)
+    assert int(st) == 0
+    lat = R.held64(codes[0].cpu().numpy(), scales[0].cpu().numpy(), 1)
+    total = 2.0 ** gap + T - 1
+    want = lat.sum(0) / total
+    bound = max(2.0 ** -11, 2.0 ** (gap - 32)) + 2.0 ** -11 + T / 16 * 2.0 ** -23 + T / 64 * 2.0 ** -24 + 1e-5
+    got = R.as64(ctx)
+    assert (np.abs(got - want) <= bound * want + 2.0 ** -25).all()
+    # The sum takes one f32 addition per tile of 64 keys, each off by up to 2^-24 of it, always the same way here
+    # (the light keys add the same small number to a sum of 2^7): T / 64 * 2^-24 = 1.53e-5 in the logarithm.  Then
+    # three f32 operations on values up to 32 round to half of 2^-19 (m less 7 and log2 l added, the logarithm itself, the
+    # product with ln 2): 3 * 2^-20 = 2.9e-6.
+    assert np.abs(R.as64(lse) - math.log(total)).max() <= T / 64 * 2.0 ** -24 + 3 * 2.0 ** -20

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from tests import q8_reference as R
-from tests.test_gpu_q8 import DEV, EPS, THETA, gen, i32, normal, random_cache, status
+from tests.test_gpu_q8 import DEV, EPS, THETA, check_append, gen, i32, normal, random_cache, status
 
 pytestmark = pytest.mark.gpu
 
@@ -96,6 +96,28 @@ def test_append_of_infinite_values(mla, rank, dtype, block):
     gain = torch.ones(rank, device=DEV, dtype=dtype)
     gain[7] = float("inf")
     assert append_into_partly_filled_blocks(mla, normal(g, 2, 6, rank).to(dtype), gain, EPS, block) == mla.DEVICE_VALUE_RANGE
+
+
+@pytest.mark.parametrize("dtype,rope_dtype", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32)])
+@pytest.mark.parametrize("rank,rope_dim,s_new,block", [(512, 128, 7, 1), (256, 256, 70, 16), (512, 66, 7, 64), (512, 64, 130, 8),
+                                                      (33, 6, 7, 4), (1024, 256, 20, 16)])
+def test_append_wide_rope_keys_and_far_positions(mla, dtype, rope_dtype, rank, rope_dim, s_new, block):
+    """Rope keys of more than 64 values beside a latent held in registers; positions across 2^24, from where an f32
+    no longer holds them, and across 2^31."""
+    g = gen(rank + rope_dim)
+    B, T = 4, 420
+    codes, scales = random_cache(g, B, T, rank, block)
+    rope = normal(g, B, T, rope_dim).to(rope_dtype)
+    raw, raw_rope = normal(g, B, s_new, rank).to(dtype), normal(g, B, s_new, rope_dim).to(dtype)
+    gain = torch.exp(0.3 * normal(g, rank)).to(dtype)
+    start, length, offset = [0, block, 0, 2 * block], [5, 37, 0, 64], [2 ** 24 - 3, 2 ** 31 - 4, 65530, 2 ** 24 + 1]
+    before = codes.cpu().numpy(), scales.cpu().numpy(), R.as64(rope)
+    st = status()
+    mla.append_compressed_q8(raw, raw_rope, gain, EPS, THETA, codes, scales, block, rope, i32(start), i32(length),
+                             row_offsets=i32(offset), device_status=st)
+    assert int(st) == 0
+    check_append(raw, raw_rope, gain, before, (codes.cpu().numpy(), scales.cpu().numpy(), R.as64(rope)), block, start, length,
+                 offset, s_new, rope_dtype)
 
 
 # ---------------------------------------------------------------- attention

@@ -436,9 +436,15 @@ def _launch_stream(stream, *tensors: Optional[torch.Tensor]) -> int:
     return _raw_stream(device) if stream is None else stream.cuda_stream
 
 
-def _check_int32(*tensors: Optional[torch.Tensor]) -> None:
+def _check_int32(count: int, *tensors: Optional[torch.Tensor]) -> None:
+    """Lengths, starts, offsets and counts that the kernels read or write ``count`` of."""
     for t in tensors:
-        assert t is None or (t.dtype is torch.int32 and t.is_contiguous()), "lengths, starts and counts: contiguous int32"
+        assert t is None or (t.dtype is torch.int32 and t.is_contiguous() and t.numel() >= count), \
+            f"lengths, starts and counts: contiguous int32, at least {count}"
+
+
+def _check_status(status: Optional[torch.Tensor]) -> None:
+    assert status is None or status.numel() * status.element_size() >= 4, "device_status: one int32"
 
 
 def _cache_strides(t: torch.Tensor):
@@ -478,7 +484,8 @@ def append_compressed_q8(latent_raw: torch.Tensor, rope_raw: torch.Tensor, norm_
     assert l_last == 1 and r_last == 1 and norm_weight.is_contiguous() and width == rank == norm_weight.numel()
     assert rope_raw.dtype is dtype and norm_weight.dtype is dtype and rope_raw.shape == (B, S, rope_dim)
     assert rows == codes.shape[0] and t_rope == t_max and kv_len.numel() == B and (rows == 1 or rows == B)
-    _check_int32(kv_start, kv_len, kv_len_out, row_offsets)
+    _check_int32(B, kv_start, kv_len, kv_len_out, row_offsets)
+    _check_status(device_status)
     handle = _launch_stream(stream, latent_raw, rope_raw, norm_weight, codes, scales, rope, kv_start, kv_len, kv_len_out,
                             row_offsets, device_status)
     _check(lib.mla_append_compressed_q8(
@@ -495,7 +502,8 @@ def quantize_cache(latent: torch.Tensor, codes: torch.Tensor, scales: torch.Tens
     l_row, l_batch = _cache_strides(latent)
     batch = kv_len.numel()
     assert latent.shape == codes.shape and latent.shape[0] in (1, batch)
-    _check_int32(kv_start, kv_len)
+    _check_int32(batch, kv_start, kv_len)
+    _check_status(device_status)
     handle = _launch_stream(stream, latent, codes, scales, kv_start, kv_len, device_status)
     _check(lib.mla_quantize_cache(latent.data_ptr(), l_row, l_batch, _dt(latent), codes.data_ptr(), c_row, c_batch,
                                   scales.data_ptr(), s_batch, scale_block, _ptr(kv_start), kv_len.data_ptr(), batch, rank,
@@ -510,7 +518,8 @@ def dequantize_cache(codes: torch.Tensor, scales: torch.Tensor, scale_block: int
     l_row, l_batch = _cache_strides(latent)
     batch = kv_len.numel()
     assert latent.shape == codes.shape and latent.shape[0] in (1, batch)
-    _check_int32(kv_start, kv_len)
+    _check_int32(batch, kv_start, kv_len)
+    _check_status(device_status)
     handle = _launch_stream(stream, latent, codes, scales, kv_start, kv_len, device_status)
     _check(lib.mla_dequantize_cache(codes.data_ptr(), c_row, c_batch, scales.data_ptr(), s_batch, scale_block,
                                     latent.data_ptr(), l_row, l_batch, _dt(latent), _ptr(kv_start), kv_len.data_ptr(),
@@ -534,14 +543,15 @@ def decode_attend_q8(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     assert q_last == 1 and x_last == 1 and width == rank + rope_dim and n_q == batch * s_q
     assert ctx_out.shape == (n_q, heads, rank) and rope.dtype is q.dtype and t_rope == t_max
     assert rows == codes.shape[0] and (rows == 1 or rows == batch) and kv_len.numel() == batch
-    _check_int32(kv_start, kv_len)
+    _check_int32(batch, kv_start, kv_len)
+    _check_status(device_status)
     if lse_out is not None:
         assert lse_out.dtype is torch.float32 and lse_out.is_contiguous() and lse_out.numel() == n_q * heads
     k_max = 0
     if sel is not None:
         k_max = sel.shape[1]
         assert sel.shape[0] == n_q and sel_count is not None and sel_count.numel() == n_q
-        _check_int32(sel, sel_count)
+        _check_int32(n_q, sel, sel_count)
     if workspace is None:
         nbytes = decode_workspace_size(batch, s_q, heads, rank, rope_dim, t_max, k_max, sel is not None, q.dtype)
         workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
@@ -559,7 +569,7 @@ def decode_attend_q8(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
 # ---------------------------------------------------------------- attention weights and eviction
 
 def _weight_strides(q: torch.Tensor, lse: torch.Tensor, weights: torch.Tensor, rope: torch.Tensor, kv_start, kv_len,
-                    batch: int, s_q: int, rows: int, t_max: int, rank: int):
+                    batch: int, s_q: int, rows: int, t_max: int, rank: int, device_status):
     """Checks shared by both forms; ``(heads, q row stride, q head stride, rope_dim, rope strides, weights batch
     stride)``."""
     n_q, heads, width = q.shape
@@ -572,7 +582,8 @@ def _weight_strides(q: torch.Tensor, lse: torch.Tensor, weights: torch.Tensor, r
     assert k_rows == rows and t_rope == t_max and (rows == 1 or rows == batch) and kv_len.numel() == batch
     assert lse.dtype is torch.float32 and lse.is_contiguous() and lse.numel() == n_q * heads
     assert weights.dtype is torch.float32 and w_last == 1 and w_rows == rows and w_cols >= t_max
-    _check_int32(kv_start, kv_len)
+    _check_int32(batch, kv_start, kv_len)
+    _check_status(device_status)
     return heads, q_row, q_head, rope_dim, k_row, k_batch, (w_batch if rows > 1 else 0)
 
 
@@ -586,7 +597,8 @@ def key_weights(q: torch.Tensor, latent: torch.Tensor, rope: torch.Tensor, lse: 
     l_row, l_batch = _cache_strides(latent)
     assert latent.dtype is q.dtype
     heads, q_row, q_head, rope_dim, k_row, k_batch, w_batch = _weight_strides(q, lse, weights, rope, kv_start, kv_len,
-                                                                              batch, s_q, rows, t_max, rank)
+                                                                              batch, s_q, rows, t_max, rank,
+                                                                              device_status)
     handle = _launch_stream(stream, q, latent, rope, lse, kv_start, kv_len, weights, device_status)
     _check(lib.mla_key_weights(
         q.data_ptr(), q_row, q_head, latent.data_ptr(), l_row, l_batch, rope.data_ptr(), k_row, k_batch, _dt(q),
@@ -602,7 +614,8 @@ def key_weights_q8(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, s
     """``key_weights`` over an 8-bit cache."""
     t_max, rank, c_row, c_batch, s_batch = _q8_strides(codes, scales, scale_block)
     heads, q_row, q_head, rope_dim, k_row, k_batch, w_batch = _weight_strides(q, lse, weights, rope, kv_start, kv_len,
-                                                                              batch, s_q, codes.shape[0], t_max, rank)
+                                                                              batch, s_q, codes.shape[0], t_max, rank,
+                                                                              device_status)
     handle = _launch_stream(stream, q, codes, scales, rope, lse, kv_start, kv_len, weights, device_status)
     _check(lib.mla_key_weights_q8(
         q.data_ptr(), q_row, q_head, codes.data_ptr(), c_row, c_batch, scales.data_ptr(), s_batch, scale_block,
@@ -623,7 +636,8 @@ def evict_plan(weights: torch.Tensor, kv_start, kv_len, n_keep: int, n_sink: int
     batch = kv_len.numel()
     assert weights.dtype is torch.float32 and w_last == 1 and (rows == 1 or rows == batch)
     assert kept.dtype is torch.int32 and k_last == 1 and width >= n_keep and n == batch == counts.numel()
-    _check_int32(kv_start, kv_len, counts, kv_len_out)
+    _check_int32(batch, kv_start, kv_len, counts, kv_len_out)
+    _check_status(device_status)
     handle = _launch_stream(stream, weights, kv_start, kv_len, kept, counts, kv_len_out, device_status)
     _check(lib.mla_evict_plan(weights.data_ptr(), w_batch if rows > 1 else 0, _ptr(kv_start), kv_len.data_ptr(), batch,
                               t_max, n_keep, n_sink, n_recent, kept.data_ptr(), k_row, counts.data_ptr(), _ptr(kv_len_out),
@@ -639,7 +653,8 @@ def cache_compact(arrays, kv_start, kept: torch.Tensor, counts: torch.Tensor, de
     batch = counts.numel()
     rows, t_max, _ = arrays[0].shape
     assert kept.dtype is torch.int32 and k_last == 1 and n == batch and (rows == 1 or rows == batch)
-    _check_int32(kv_start, counts)
+    _check_int32(batch, kv_start, counts)
+    _check_status(device_status)
     states = []
     for a in arrays:
         a_rows, a_len, features = a.shape

@@ -167,6 +167,15 @@ def status_string(status: int) -> str:
     return lib.mla_status_string(status).decode()
 
 
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace of one call.  The allocator hands memory freed on the current stream to that stream's next call: on
+    another stream it is told to wait for the kernels that use it."""
+    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 # ---------------------------------------------------------------- entry points
 
 def rope_partial_interleaved(x: torch.Tensor, out: torch.Tensor, rotary_dims: int, theta: float,
@@ -221,7 +230,7 @@ def decode_attend(q: torch.Tensor, latent: torch.Tensor, rope: torch.Tensor, kv_
     if workspace is None:
         nbytes = decode_workspace_size(batch, s_q, heads, rank, rope_dim, t_max, k_max,
                                        sel is not None, latent.dtype)
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(max(nbytes, 1), q.device, stream)
     _check(lib.mla_decode_attend(
         _ptr(q), q.stride(0), q.stride(1), _ptr(latent), latent.stride(1), lat_bs,
         _ptr(rope), rope.stride(1), rope_bs, _dt(latent), _ptr(kv_start), _ptr(kv_len),
@@ -266,7 +275,7 @@ def decode_step(q_nope: torch.Tensor, q_rope: torch.Tensor, theta: float, kv_b_p
     if workspace is None:
         nbytes = decode_step_workspace_size(batch, s_q, heads, nope, v_dim, rank, rope_dim, t_max, k_max,
                                             sel is not None, latent.dtype)
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=latent.device)
+        workspace = _scratch(max(nbytes, 256), latent.device, stream)
     _check(lib.mla_decode_step(
         _ptr(q_nope), q_nope.stride(0), q_nope.stride(1), _ptr(q_rope), q_rope.stride(0), q_rope.stride(1),
         _ptr(row_offsets), int(position_offset), float(theta), _ptr(kv_b_proj),
@@ -554,7 +563,7 @@ def decode_attend_q8(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
         _check_int32(n_q, sel, sel_count)
     if workspace is None:
         nbytes = decode_workspace_size(batch, s_q, heads, rank, rope_dim, t_max, k_max, sel is not None, q.dtype)
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(max(nbytes, 1), q.device, stream)
     assert workspace.element_size() == 1 and workspace.is_contiguous()
     handle = _launch_stream(stream, q, codes, scales, rope, kv_start, kv_len, ctx_out, lse_out, sel, sel_count, workspace,
                             device_status)

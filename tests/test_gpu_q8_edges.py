@@ -153,3 +153,40 @@ def test_attend_light_keys_behind_a_heavy_one(mla, gap):
     # three f32 operations on values up to 32 round to half of 2^-19 (m less 7 and log2 l added, the logarithm itself, the
     # product with ln 2): 3 * 2^-20 = 2.9e-6.
     assert np.abs(R.as64(lse) - math.log(total)).max() <= T / 64 * 2.0 ** -24 + 3 * 2.0 ** -20
+
+
+@pytest.mark.parametrize("q8", [True, False])
+def test_own_workspace_outlives_a_call_on_another_stream(mla, q8, monkeypatch):
+    """A call on a side stream that is still busy: its workspace is not handed to the current stream meanwhile."""
+    g = gen(3)
+    B, T, heads = 2, 3000, 128
+    codes, scales = random_cache(g, B, T, 512, 16)
+    latent, rope = normal(g, B, T, 512).bfloat16(), normal(g, B, T, 64).bfloat16()
+    q = normal(g, B, heads, 576).bfloat16() * 0.1
+    ctx, lse, length = torch.empty(B, heads, 512, device=DEV), torch.empty(B, heads, device=DEV), i32([T, 5])
+    taken, empty = [], torch.empty
+
+    def spy(*args, **kw):
+        t = empty(*args, **kw)
+        taken.append((t.data_ptr(), t.numel()))
+        return t
+
+    def call(stream):
+        if q8:
+            mla.decode_attend_q8(q, codes, scales, 16, rope, None, length, B, 1, 0.07, ctx, lse, stream=stream)
+        else:
+            mla.decode_attend(q, latent, rope, None, length, B, 1, 0.07, ctx, lse, stream=stream)
+    call(None)                              # (a kernel's first launch loads its code, which waits for the device)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)      # 0.2 s
+    monkeypatch.setattr(torch, "empty", spy)
+    call(side)
+    monkeypatch.undo()
+    (ptr, size), = taken
+    others = [empty(size, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    assert not side.query() and all(t.data_ptr() != ptr for t in others)
+    side.synchronize()
+    assert torch.isfinite(ctx).all()

@@ -15,6 +15,7 @@
 // appended in 14.7 us (2.0 TB/s: one wave of CTAs), 16 x 16384 dequantised in
 // 67 us (6.0 TB/s).
 #include <cuda_bf16.h>
+#include <float.h>
 
 #include "e4m3.cuh"
 #include "mla_internal.h"
@@ -383,10 +384,17 @@ __global__ void __launch_bounds__(kHeldWarps * 32, sizeof(TI) == 2 ? 2 : 1) enco
       }
       __syncthreads();
     }
-    // in units: (x inv) g 2^(127 - e), the power of two taken with inv (exact)
+    // in units: (x inv) g 2^(127 - e), the power of two taken with inv: exact, but
+    // that the product of a finite inv stays finite.  (It passes f32's range for
+    // tokens below 2^-65 at eps = 0 whose weights are so small, or 0, that the
+    // block takes one of the smallest units: a weight of 0 must give 0, and
+    // values of at most 2^-45 may be coded smaller than they are.)
 #pragma unroll
-    for (int k = 0; k < kHeldRows; ++k)
-      if (mine(k)) inv[k] *= inverse_unit_of(exp_s[(r0 + k) >> p.block_shift]);
+    for (int k = 0; k < kHeldRows; ++k) {
+      if (!mine(k)) continue;
+      const float units = inv[k] * inverse_unit_of(exp_s[(r0 + k) >> p.block_shift]);
+      inv[k] = kNorm && fabsf(inv[k]) <= FLT_MAX ? fminf(units, FLT_MAX) : units;
+    }
     uint8_t* dst = codes + (base + r0) * p.codes_row_stride + 8 * lane;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {

@@ -98,6 +98,14 @@ def test_append_of_infinite_values(mla, rank, dtype, block):
     assert append_into_partly_filled_blocks(mla, normal(g, 2, 6, rank).to(dtype), gain, EPS, block) == mla.DEVICE_VALUE_RANGE
 
 
+@pytest.mark.parametrize("block", [1, 8])
+@pytest.mark.parametrize("rank,dtype", SHAPES)
+def test_append_of_tiny_tokens_under_zero_weights(mla, rank, dtype, block):
+    """Tokens of 1e-21 at eps = 0 have an inverse norm of 1e21: times a weight of 0 they are 0, not NaN."""
+    raw = torch.full((2, 6, rank), 1e-21, device=DEV, dtype=dtype)
+    assert append_into_partly_filled_blocks(mla, raw, torch.zeros(rank, device=DEV, dtype=dtype), 0.0, block) == 0
+
+
 @pytest.mark.parametrize("dtype,rope_dtype", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32)])
 @pytest.mark.parametrize("rank,rope_dim,s_new,block", [(512, 128, 7, 1), (256, 256, 70, 16), (512, 66, 7, 64), (512, 64, 130, 8),
                                                       (33, 6, 7, 4), (1024, 256, 20, 16)])

@@ -523,7 +523,12 @@ int mla_prefill_attend(const void* q_nope, int64_t q_nope_row_stride, int64_t q_
  * MLA_DEVICE_BAD_BLOCK_START, one whose window does not lie in [0, t_max)
  * sets MLA_DEVICE_INDEX_OUT_OF_RANGE, and either is skipped (attention: no
  * visible key).  The selection, scores, outputs, workspace and errors of the
- * entry points below are those of their bf16 / f32 counterparts.
+ * entry points below are those of their bf16 / f32 counterparts.  An 8-bit
+ * cache rolls back by its lengths (mla_rollback_lengths): a block that keeps
+ * tokens keeps its unit, one that keeps none takes a new one with its next
+ * tokens.  The right-aligned row operations (mla_cache_shift_rows) move f32 and
+ * bf16 elements by any number of columns and know nothing of exponents: they
+ * do not serve it.
  *
  * mla_append_compressed_q8: mla_append_compressed into an 8-bit cache.  The
  * normalised f32 values of a block's tokens take the smallest unit in which
@@ -601,7 +606,10 @@ int mla_decode_attend_q8(const void* q, int64_t q_row_stride, int64_t q_head_str
  *   W <- (t < kv_len[b] - n_new ? decay * W : 0)
  *        + sum over tokens i < s_q that see t and heads h of exp(s[n, h, t] - lse[n, h]),
  * n = b*s_q + i, s the scaled score of mla_decode_attend over the dense causal
- * window and lse [n_q, heads] its lse_out.  The n_new newest keys start from
+ * window and lse [n_q, heads] its lse_out.  (The scores are f32 sums.  The lse
+ * of the bf16 attention comes from scores exchanged in fp16 and may be off by up
+ * to 2e-2, so the weights that a head and token hand out may sum to 0.98 to
+ * 1.02.)  The n_new newest keys start from
  * zero (the tokens appended since the last call: buffer rows behind a window
  * may hold weights of evicted keys).  decay in [0, 1]; 0 does not read W.
  * Weights outside the windows are left as they were.  Sums are f32 in a fixed

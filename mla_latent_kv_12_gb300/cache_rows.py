@@ -5,7 +5,9 @@ state array of a layer (latent, rope, indexer keys) as ``[B, width, F]`` with
 row ``b``'s tokens in its last ``row_offsets[b]`` columns.  Its
 ``specRoundRollback``, ``filter`` and ``mergeRows`` are planned on the host by
 the library (integer bookkeeping) and carried out by one row-gather launch per
-state array into new device arrays of the planned width.
+state array into new device arrays of the planned width.  The arrays are f32 or
+bf16; an 8-bit cache, whose exponents belong to blocks of buffer rows, keeps the
+window layout and rolls back by its lengths (``mla.rollback_lengths``).
 """
 from __future__ import annotations
 

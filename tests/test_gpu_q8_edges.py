@@ -7,7 +7,8 @@ import pytest
 import torch
 
 from tests import q8_reference as R
-from tests.test_gpu_q8 import DEV, EPS, THETA, check_append, gen, i32, normal, random_cache, status
+from tests.test_gpu_q8 import (DEV, EPS, SCALE, THETA, attend_case, check_append, gen, i32, normal, random_cache,
+                               status)
 
 pytestmark = pytest.mark.gpu
 
@@ -106,6 +107,27 @@ def test_append_of_tiny_tokens_under_zero_weights(mla, rank, dtype, block):
     assert append_into_partly_filled_blocks(mla, raw, torch.zeros(rank, device=DEV, dtype=dtype), 0.0, block) == 0
 
 
+def test_append_after_a_rollback(mla):
+    """A block that keeps tokens keeps its unit, one that keeps none takes that of its next tokens."""
+    g = gen(12)
+    codes, scales = torch.zeros(2, 32, 512, dtype=torch.uint8, device=DEV), torch.zeros(2, 4, dtype=torch.uint8, device=DEV)
+    rope, n = torch.zeros(2, 32, 8, device=DEV), i32([0, 0])
+
+    def append(s_new, size):
+        mla.append_compressed_q8(normal(g, 2, s_new, 512), torch.zeros(2, s_new, 8, device=DEV),
+                                 torch.full((512,), size, device=DEV), EPS, THETA, codes, scales, 8, rope, None, n, kv_len_out=n)
+    append(8, 1.0)
+    before = n.clone()
+    append(8, 100.0)
+    large = scales[:, 1].tolist()
+    mla.rollback_lengths(before, i32([0, 3]), n)
+    assert n.tolist() == [8, 11]
+    append(2, 1.0)
+    assert n.tolist() == [10, 13]
+    # unit 2^k holds rms 1 (a largest magnitude of 2.5 to 7 among 512 values), 2^(k + 6) or more rms 100
+    assert int(scales[0, 1]) <= large[0] - 5 and int(scales[1, 1]) == large[1]
+
+
 @pytest.mark.parametrize("dtype,rope_dtype", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32)])
 @pytest.mark.parametrize("rank,rope_dim,s_new,block", [(512, 128, 7, 1), (256, 256, 70, 16), (512, 66, 7, 64), (512, 64, 130, 8),
                                                       (33, 6, 7, 4), (1024, 256, 20, 16)])
@@ -198,3 +220,29 @@ def test_own_workspace_outlives_a_call_on_another_stream(mla, q8, monkeypatch):
     assert not side.query() and all(t.data_ptr() != ptr for t in others)
     side.synchronize()
     assert torch.isfinite(ctx).all()
+
+
+@pytest.mark.parametrize("q8", [True, False])
+def test_weights_from_the_attentions_own_lse(mla, q8):
+    """attend, then weights from its lse: that is off by up to 2e-2 (the bound of its tests), the weights by the
+    exponential of that, and by 1e-4 of their own (as with an exact lse)."""
+    g = gen(96)
+    B, T, heads, block = 2, 1500, 128, 8
+    q, codes, scales, rope, start, length = attend_case(g, B, 1, heads, T, block, [1500, 700], [0, 8])
+    latent, ctx = normal(g, B, T, 512).bfloat16(), torch.empty(B, heads, 512, device=DEV)
+    lse, w = torch.empty(B, heads, device=DEV), torch.zeros(B, T, device=DEV)
+    if q8:
+        mla.decode_attend_q8(q, codes, scales, block, rope, start, length, B, 1, SCALE, ctx, lse)
+        mla.key_weights_q8(q, codes, scales, block, rope, lse, start, length, B, 1, SCALE, w)
+    else:
+        mla.decode_attend(q, latent, rope, start, length, B, 1, SCALE, ctx, lse)
+        mla.key_weights(q, latent, rope, lse, start, length, B, 1, SCALE, w)
+    got, bound = R.as64(w), math.expm1(2e-2) + 1e-4
+    for b in range(B):
+        lo, n = int(start[b]), int(length[b])
+        lat = R.held64(codes[b].cpu().numpy(), scales[b].cpu().numpy(), block)[lo:lo + n] if q8 else R.as64(latent[b, lo:lo + n])
+        keys = R.as64(rope[b, lo:lo + n])
+        exact = R.attend64(R.as64(q[b]), lat, keys, SCALE)[1]
+        want = R.key_weights64(R.as64(q[b:b + 1]), lat, keys, exact[None], np.zeros(n), SCALE, 0.0, 0)
+        assert (np.abs(got[b, lo:lo + n] - want) <= bound * want).all()
+        assert abs(got[b].sum() - heads) <= bound * heads

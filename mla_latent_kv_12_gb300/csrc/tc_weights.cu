@@ -14,9 +14,10 @@
 // 66); four tokens of 8 rows of 16384 keys 91 and 110 us.
 //
 //  * One persistent CTA per SM takes an equal range of the flattened tiles of
-//    all rows.  With several query tokens a range is walked in chunks that
-//    stay in L2, once per token: the weights of a key are always updated by
-//    the same thread, in token order (no atomics, the same bits every time).
+//    all rows.  With several query tokens a range is walked in chunks (of a bf16
+//    cache: that stay in L2), once per token: the weights of a key are always
+//    updated by the same thread, in token order (no atomics, the same bits
+//    every time).
 //    Two tokens of 64 heads share the MMA's 128 rows and a pass.
 //  * bf16 cache: warp 0 loads [64 keys x 576] tiles by TMA into a three-stage
 //    ring (nine boxes of 64 dims, 128-byte swizzle).  8-bit cache: warps
@@ -52,12 +53,16 @@ constexpr int kThreads = 32 * kConvertWarp, kThreadsQ8 = kThreads + kConvertThre
 using WeightFetch = Q8Fetch<32, kConvertThreads>;
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES, SMEM_BYTES_Q8 = STAGES_Q8 * STAGE_BYTES + 2 * WeightFetch::kSlotBytes;
 constexpr long long kWaitLimit = 1LL << 32;   // clock cycles (~2 s)
-// Tiles that several query tokens share before the next ones are read.  A pass
-// begins with a drained pipeline, so chunks are as long as the L2 (129 MB)
-// allows: 152 CTAs x 8 tiles x 72 KB = 88 MB; from 11 on full chunks are read
+// Tiles that several query tokens walk before the next ones.  A pass begins
+// with a drained pipeline, so chunks are long.  Over bf16 as long as the L2 (129
+// MB) allows: 152 CTAs x 8 tiles x 72 KB = 88 MB; from 11 on full chunks are read
 // from memory again (four tokens of 8 rows of 14592 keys: 77 us with 8 or 10,
-// 91 with 12).  An 8-bit cache's passes are slower than its reads from memory:
-// chunks of 28 tiles (4 rows of 65536 keys: 179 us with 15, 169 with 28 and 60).
+// 91 with 12).  Over 8 bits a pass is slower than its reads from memory, and
+// its chunks do not stay in L2 (28 tiles x 40 KB x 152 CTAs = 175 MB): with 8 / 15
+// / 20 / 28 / 60 tiles four tokens of 8 rows of 65536 keys (54 tiles per CTA)
+// take 369 / 323 / 306 / 296 / 280 us, of 4 such rows 210 / 179 / 181 / 166 /
+// 167, three of 5 rows of 40001 132 / 120 / 113 / 112 / 112, two of 6 rows of
+// 30011 89 / 83 / 75 / 75 / 75.
 constexpr int kChunkTiles = 8, kChunkTilesQ8 = 28;
 constexpr int kRopeAhead = 6;      // tiles ahead that an 8-bit cache's rope keys are pulled into L2
 constexpr int kWeightsAhead = 8;   // tiles ahead that weights are pulled into L2

@@ -246,3 +246,36 @@ def test_weights_from_the_attentions_own_lse(mla, q8):
         want = R.key_weights64(R.as64(q[b:b + 1]), lat, keys, exact[None], np.zeros(n), SCALE, 0.0, 0)
         assert (np.abs(got[b, lo:lo + n] - want) <= bound * want).all()
         assert abs(got[b].sum() - heads) <= bound * heads
+
+
+@pytest.mark.parametrize("order", ["rising", "falling", "heavy last"])
+def test_attend_moves_its_reference(mla, order):
+    """Scores that rise by a quarter (log2 units) from tile to tile, fall so, or jump by 60 at the last key: the reference
+    moves and the context is rescaled, or most keys are far lighter than it.
+
+    Exact scores; roundings as for light keys behind a heavy one, 2^-32 of the heaviest weight per key for those below
+    fp16's normal range, and 2^-21 for each of at most 9 rescales."""
+    g = gen(len(order))
+    B, T, heads = 80, 16385, 64
+    codes, scales = random_cache(g, 1, T, 512, 1)
+    codes = codes & 0x7F
+    score = torch.arange(T, device=DEV) // 64 * 0.25                  # up to 64: 8 bits
+    if order == "falling":
+        score = score.flip(0)
+    elif order == "heavy last":
+        score = torch.where(torch.arange(T, device=DEV) == T - 1, 60.0, 0.0)
+    rope = torch.zeros(1, T, 64, dtype=torch.bfloat16, device=DEV)
+    rope[0, :, 0] = score
+    q = torch.zeros(B, heads, 576, dtype=torch.bfloat16, device=DEV)
+    q[..., 512] = 1.0
+    ctx, lse, st = torch.empty(B, heads, 512, device=DEV), torch.empty(B, heads, device=DEV), status()
+    mla.decode_attend_q8(q, codes, scales, 1, rope, None, i32([T] * B), B, 1, math.log(2.0), ctx, lse, device_status=st)
+    assert int(st) == 0
+    lat = R.held64(codes[0].cpu().numpy(), scales[0].cpu().numpy(), 1)
+    p = np.exp2(R.as64(rope[0, :, 0]) - R.as64(score).max())
+    want = p @ lat / p.sum()
+    bound = 2 * 2.0 ** -11 + T / 16 * 2.0 ** -23 + T / 64 * 2.0 ** -24 + 9 * 2.0 ** -21 + 1e-5
+    assert (np.abs(R.as64(ctx) - want) <= bound * want + lat.sum(0) * 2.0 ** -32 / p.sum() + 2.0 ** -25).all()
+    # the lse: additions and three f32 operations on values up to 64 (2^-19 each, and as much for the rescales)
+    exact = (R.as64(score).max() + math.log2(p.sum())) * math.log(2.0)
+    assert np.abs(R.as64(lse) - exact).max() <= T / 64 * 2.0 ** -24 + 4 * 2.0 ** -18

@@ -324,7 +324,9 @@ def _plan(s):
 def _commit(s):
     if own:
         from mla_latent_kv_12_gb300 import mla
-        mla.commit_paged(s["arrays"], s["table"], s["len"], s["path"], s["accepted"], kv_len_out=s["len_out"],
+        if "pools" not in s:
+            s["pools"] = mla.PagedArrays(s["arrays"])
+        mla.commit_paged(s["pools"], s["table"], s["len"], s["path"], s["accepted"], kv_len_out=s["len_out"],
                          device_status=s["status"])
     else:
         step = torch.arange(s["path"].shape[1], device=DEV)[None, :]

@@ -680,6 +680,101 @@ int mla_cache_compact(const mla_state_array* arrays, int32_t n_arrays, const int
                       int32_t* device_status, mla_stream_t stream);
 
 /*
+ * The paged cache (no counterpart on the pages): the cache of a server that
+ * hands memory to its sequences page by page, and verifies trees of drafted
+ * tokens over it.
+ *
+ * A pool holds num_pages pages of page_size rows: row r of page p is
+ * latent[p*latent_page_stride + r*latent_row_stride + 0:rank] and
+ * rope[p*rope_page_stride + r*rope_row_stride + 0:rope_dim].  Key t of batch
+ * row b is row t % page_size of page page_table[b*page_table_stride +
+ * t / page_size]; a row has at most table_width pages (table_width *
+ * page_size < 2^31).  Table entries behind a row's last key are not read.
+ * Rows may share pages that none of them writes (a common prefix).
+ * New tokens: row b has token_counts[b] new tokens, 0 .. s (NULL: s for every
+ * row), where s is the call's s_new / s_q / n_nodes; a padded batch gives its
+ * unused rows and tokens a count of 0.
+ * A length that is negative or passes the table, or a count outside 0 .. s,
+ * sets MLA_DEVICE_INDEX_OUT_OF_RANGE and the row is skipped (attention: no
+ * visible key).  A page outside [0, num_pages) that a row needs sets it too:
+ * nothing outside the pool is read or written, a token of such a page is not
+ * written, and what the attention of that row returns is not specified.
+ *
+ * mla_append_paged: mla_append_compressed into pages.  Token t < count of row b
+ * becomes key kv_len[b] + t, its rope key rotated at positions[b*s_new + t]
+ * (NULL: at its key index; a negative position sets
+ * MLA_DEVICE_INDEX_OUT_OF_RANGE and the token is not written).
+ * kv_len_out[b] (may be NULL, may be kv_len) receives kv_len[b] + count.
+ *
+ * mla_tree_plan: node j < count of row b hangs below node parents[b *
+ * parents_row_stride + j] < j (a stride of 0: one tree for every row), or (-1) below the row's last cached key; another
+ * value sets MLA_DEVICE_INDEX_OUT_OF_RANGE and counts as -1.  positions[b *
+ * n_nodes + j] = kv_len[b] + the node's depth (kv_len NULL: 0), and
+ * tree_mask[(b*n_nodes + j)*words + w], words = ceil(n_nodes / 64), has bit
+ * i % 64 of word i / 64 set for the node itself and its ancestors i.  A node
+ * j >= count gets position kv_len[b] and an empty mask.  n_nodes <=
+ * MLA_MAX_TREE_NODES.
+ *
+ * mla_decode_attend_paged: mla_decode_attend over pages.  The row's last count
+ * keys are its new tokens.  Token i < count sees the keys t <= kv_len[b] -
+ * count + i; with tree_mask (s_q <= MLA_MAX_TREE_NODES) the keys t <
+ * kv_len[b] - count and the keys kv_len[b] - count + j of the nodes j < count
+ * whose bit is set (any bits, a tree or not).  Keys that a token does not see
+ * have no part in its result, whatever they hold.  A token i >= count sees no
+ * key; its selection is not read.  Selections are as in mla_decode_attend and
+ * exclude tree_mask (list the ancestors instead).  The workspace is that of
+ * mla_decode_workspace_size with t_max = table_width * page_size.
+ * bf16 is served for the shapes of mla_decode_attend, with pool pointers
+ * 16-byte aligned and strides multiples of 16 bytes.  Page sizes that are
+ * multiples of 16 rows are read by TMA boxes; others, and selections, row by
+ * row, which needs page strides that are whole numbers of rows and pools of
+ * fewer than 2^31 rows (else MLA_ERR_UNSUPPORTED).  f32 for any shape, at most
+ * 65535 query rows.
+ *
+ * mla_commit_paged: after verification, moves the accepted path of each row's
+ * tree to the end of its sequence: for j < counts[b], key kv_len[b] + j of every
+ * listed array receives key kv_len[b] + path[b*path_row_stride + j], in place
+ * and in order, and kv_len_out[b] (may be NULL, may be kv_len) receives
+ * kv_len[b] + counts[b].  kv_len is the length before the tree was appended;
+ * path holds node numbers from the top down, so ascending, at most path_width
+ * <= MLA_MAX_TREE_NODES.  Rotations are those of the nodes' depths, which stay
+ * right.  A node that is not above its predecessor, below j or behind the table
+ * sets MLA_DEVICE_INDEX_OUT_OF_RANGE and is not moved; the row's length grows
+ * all the same.  `arrays` is a HOST array of n_arrays <= MLA_MAX_COMMIT_ARRAYS
+ * pools (all layers at once); batch_stride_bytes is the stride between pages.
+ * Rows of one call must not share the pages that they write.
+ * At most 65535 batch rows in mla_tree_plan and mla_commit_paged.
+ */
+#define MLA_MAX_TREE_NODES 1024
+#define MLA_MAX_COMMIT_ARRAYS 256
+int mla_append_paged(const void* latent_raw, int64_t latent_raw_row_stride, int64_t latent_raw_token_stride,
+                     const void* rope_raw, int64_t rope_raw_row_stride, int64_t rope_raw_token_stride, int dtype,
+                     const void* norm_weight, float eps, float theta, const int32_t* positions, void* latent,
+                     int64_t latent_row_stride, int64_t latent_page_stride, void* rope, int64_t rope_row_stride,
+                     int64_t rope_page_stride, int cache_dtype, const int32_t* page_table, int64_t page_table_stride,
+                     int32_t table_width, int32_t page_size, int32_t num_pages, const int32_t* kv_len,
+                     const int32_t* token_counts, int32_t* kv_len_out, int32_t batch, int32_t s_new, int32_t rank,
+                     int32_t rope_dim, int32_t* device_status, mla_stream_t stream);
+int mla_tree_plan(const int32_t* parents, int64_t parents_row_stride, const int32_t* kv_len,
+                  const int32_t* token_counts, int32_t batch, int32_t n_nodes, int32_t* positions, uint64_t* tree_mask,
+                  int32_t* device_status, mla_stream_t stream);
+int mla_decode_attend_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* latent,
+                            int64_t latent_row_stride, int64_t latent_page_stride, const void* rope,
+                            int64_t rope_row_stride, int64_t rope_page_stride, int dtype, const int32_t* page_table,
+                            int64_t page_table_stride, int32_t table_width, int32_t page_size, int32_t num_pages,
+                            const int32_t* kv_len, const int32_t* token_counts, const uint64_t* tree_mask,
+                            int32_t batch, int32_t s_q, int32_t heads, int32_t rank, int32_t rope_dim,
+                            const int32_t* selected_positions, const int32_t* selected_counts, int32_t k_max,
+                            float softmax_scale, void* ctx_out, int64_t ctx_row_stride, int64_t ctx_head_stride,
+                            int out_dtype, float* lse_out, void* workspace, size_t workspace_bytes,
+                            int32_t* device_status, mla_stream_t stream);
+int mla_commit_paged(const mla_state_array* arrays, int32_t n_arrays, const int32_t* page_table,
+                     int64_t page_table_stride, int32_t table_width, int32_t page_size, int32_t num_pages,
+                     const int32_t* kv_len, const int32_t* path, int64_t path_row_stride, int32_t path_width,
+                     const int32_t* counts, int32_t* kv_len_out, int32_t batch, int32_t* device_status,
+                     mla_stream_t stream);
+
+/*
  * Test hook: the selected-position gather of attendAbsorbed (takeAxis on
  * latent and rope), bit-exact.  out[n, j, 0:rank+rope_dim] = latent || rope of
  * window key selected_positions[n*k_max + j] of query row n, for j < count;

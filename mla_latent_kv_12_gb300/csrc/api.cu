@@ -986,6 +986,217 @@ int mla_cache_compact(const mla_state_array* arrays, int32_t n_arrays, const int
   return cuda_status(launch_compact(p, (cudaStream_t)stream), "cache_compact launch");
 }
 
+// ------------------------------------------------------------ paged cache
+
+// Checks shared by the entry points of the paged cache.
+static int check_table(const char* what, const int32_t* table, int64_t stride, int32_t width, int32_t page_size,
+                       int32_t num_pages, int32_t batch) {
+  MLA_CHECK(table, "%s: NULL page_table", what);
+  MLA_CHECK(batch > 0 && width > 0 && page_size > 0 && num_pages > 0,
+            "%s: batch, table_width, page_size and num_pages must be positive", what);
+  MLA_CHECK(stride >= (batch > 1 ? width : 0), "%s: page_table_stride < table_width", what);
+  MLA_CHECK((int64_t)width * page_size < (1LL << 31), "%s: table_width * page_size must fit int32", what);
+  return MLA_OK;
+}
+
+// kv_len_out is kv_len itself or does not overlap what the call reads.
+static bool lengths_apart(const int32_t* out, const int32_t* kv_len, const int32_t* counts, int32_t batch) {
+  auto apart = [&](const int32_t* a) { return !a || out + batch <= a || a + batch <= out; };
+  return !out || ((out == kv_len || apart(kv_len)) && apart(counts));
+}
+
+int mla_append_paged(const void* latent_raw, int64_t latent_raw_row_stride, int64_t latent_raw_token_stride,
+                     const void* rope_raw, int64_t rope_raw_row_stride, int64_t rope_raw_token_stride, int dtype,
+                     const void* norm_weight, float eps, float theta, const int32_t* positions, void* latent,
+                     int64_t latent_row_stride, int64_t latent_page_stride, void* rope, int64_t rope_row_stride,
+                     int64_t rope_page_stride, int cache_dtype, const int32_t* page_table, int64_t page_table_stride,
+                     int32_t table_width, int32_t page_size, int32_t num_pages, const int32_t* kv_len,
+                     const int32_t* token_counts, int32_t* kv_len_out, int32_t batch, int32_t s_new, int32_t rank,
+                     int32_t rope_dim, int32_t* device_status, mla_stream_t stream) {
+  g_detail[0] = 0;
+  MLA_CHECK(latent_raw && norm_weight && latent && kv_len && (rope_dim == 0 || (rope_raw && rope)),
+            "append_paged: NULL pointer");
+  MLA_CHECK(valid_dtype(dtype) && valid_dtype(cache_dtype), "append_paged: bad dtype");
+  MLA_CHECK(s_new > 0 && rank > 0 && rope_dim >= 0, "append_paged: sizes must be positive");
+  const int st = check_table("append_paged", page_table, page_table_stride, table_width, page_size, num_pages, batch);
+  if (st != MLA_OK) return st;
+  MLA_CHECK(rank <= kMaxAppendRank, "append_paged: rank %d > %d", rank, kMaxAppendRank);
+  MLA_CHECK((rope_dim & 1) == 0 && rope_dim <= kMaxRotaryDims, "append_paged: rope_dim must be even and <= %d",
+            kMaxRotaryDims);
+  MLA_CHECK(isfinite(eps) && eps >= 0.f, "append_paged: RMSNorm epsilon must be non-negative");
+  MLA_CHECK(isfinite(theta) && theta > 0.f, "append_paged: theta must be positive and finite");
+  MLA_CHECK(latent_raw_token_stride >= rank && latent_raw_row_stride >= 0 && latent_row_stride >= rank &&
+                latent_page_stride >= 0,
+            "append_paged: latent strides too small");
+  MLA_CHECK(rope_dim == 0 || (rope_raw_token_stride >= rope_dim && rope_raw_row_stride >= 0 &&
+                              rope_row_stride >= rope_dim && rope_page_stride >= 0),
+            "append_paged: rope strides too small");
+  MLA_CHECK(lengths_apart(kv_len_out, kv_len, token_counts, batch),
+            "append_paged: kv_len_out must be kv_len or apart from kv_len and token_counts");
+  AppendPagedParams p;
+  memset(&p, 0, sizeof(p));
+  p.latent_raw = latent_raw;
+  p.lr_row_stride = latent_raw_row_stride;
+  p.lr_tok_stride = latent_raw_token_stride;
+  p.rope_raw = rope_raw;
+  p.rr_row_stride = rope_raw_row_stride;
+  p.rr_tok_stride = rope_raw_token_stride;
+  p.weight = norm_weight;
+  p.eps = eps;
+  p.positions = positions;
+  p.latent = latent;
+  p.l_row_stride = latent_row_stride;
+  p.l_page_stride = latent_page_stride;
+  p.rope = rope;
+  p.r_row_stride = rope_row_stride;
+  p.r_page_stride = rope_page_stride;
+  p.table = page_table;
+  p.table_stride = page_table_stride;
+  p.table_width = table_width;
+  p.page_size = page_size;
+  p.num_pages = num_pages;
+  p.kv_len = kv_len;
+  p.counts = token_counts;
+  p.kv_len_out = kv_len_out;
+  p.batch = batch;
+  p.s_new = s_new;
+  p.rank = rank;
+  p.rope_dim = rope_dim;
+  p.status = device_status;
+  if (rope_dim > 0) rope_inverse_frequencies(theta, rope_dim, p.inv_freq);
+  return cuda_status(launch_append_paged(p, dtype, cache_dtype, (cudaStream_t)stream), "append_paged launch");
+}
+
+int mla_tree_plan(const int32_t* parents, int64_t parents_row_stride, const int32_t* kv_len,
+                  const int32_t* token_counts, int32_t batch, int32_t n_nodes, int32_t* positions, uint64_t* tree_mask,
+                  int32_t* device_status, mla_stream_t stream) {
+  g_detail[0] = 0;
+  MLA_CHECK(parents && positions && tree_mask, "tree_plan: NULL pointer");
+  MLA_CHECK(batch > 0 && batch <= 65535, "tree_plan: 1 to 65535 batch rows");
+  MLA_CHECK(n_nodes > 0 && n_nodes <= kMaxTreeNodes, "tree_plan: 1 to %d nodes", kMaxTreeNodes);
+  MLA_CHECK(parents_row_stride >= 0, "tree_plan: parents_row_stride must be non-negative");
+  MLA_CHECK((reinterpret_cast<uintptr_t>(tree_mask) & 7u) == 0, "tree_plan: tree_mask must be 8-byte aligned");
+  const TreePlanParams p{parents, parents_row_stride, kv_len, token_counts, positions, tree_mask, batch, n_nodes,
+                         device_status};
+  return cuda_status(launch_tree_plan(p, (cudaStream_t)stream), "tree_plan launch");
+}
+
+int mla_decode_attend_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* latent,
+                            int64_t latent_row_stride, int64_t latent_page_stride, const void* rope,
+                            int64_t rope_row_stride, int64_t rope_page_stride, int dtype, const int32_t* page_table,
+                            int64_t page_table_stride, int32_t table_width, int32_t page_size, int32_t num_pages,
+                            const int32_t* kv_len, const int32_t* token_counts, const uint64_t* tree_mask,
+                            int32_t batch, int32_t s_q, int32_t heads, int32_t rank, int32_t rope_dim,
+                            const int32_t* selected_positions, const int32_t* selected_counts, int32_t k_max,
+                            float softmax_scale, void* ctx_out, int64_t ctx_row_stride, int64_t ctx_head_stride,
+                            int out_dtype, float* lse_out, void* workspace, size_t workspace_bytes,
+                            int32_t* device_status, mla_stream_t stream) {
+  g_detail[0] = 0;
+  int st = check_table("decode_paged", page_table, page_table_stride, table_width, page_size, num_pages, batch);
+  if (st != MLA_OK) return st;
+  const int64_t t_max = (int64_t)table_width * page_size;
+  DecodeGeometry g;
+  st = decode_geometry(g, q, q_row_stride, q_head_stride, latent, latent_row_stride, 0, rope, rope_row_stride, 0, dtype,
+                       nullptr, kv_len, batch, s_q, heads, rank, rope_dim, t_max, selected_positions, selected_counts,
+                       k_max, softmax_scale, ctx_out, ctx_row_stride, ctx_head_stride, lse_out, device_status, true);
+  if (st != MLA_OK) return st;
+  MLA_CHECK(valid_dtype(out_dtype), "decode_paged: bad out_dtype %d", out_dtype);
+  MLA_CHECK(latent_page_stride >= 0 && rope_page_stride >= 0, "decode_paged: page strides must be non-negative");
+  MLA_CHECK(!tree_mask || s_q <= kMaxTreeNodes, "decode_paged: trees of at most %d nodes", kMaxTreeNodes);
+  MLA_CHECK((reinterpret_cast<uintptr_t>(tree_mask) & 7u) == 0, "decode_paged: tree_mask must be 8-byte aligned");
+  if (tree_mask && selected_positions)
+    return fail(MLA_ERR_UNSUPPORTED, "decode_paged: a selection lists a node's ancestors itself; it takes no tree_mask");
+  g.table = page_table;
+  g.table_stride = page_table_stride;
+  g.table_width = table_width;
+  g.page_size = page_size;
+  g.num_pages = num_pages;
+  g.latent_page_stride = latent_page_stride;
+  g.rope_page_stride = rope_page_stride;
+  g.counts = token_counts;
+  g.tree = tree_mask;
+  g.tree_words = tree_mask ? (s_q + 63) / 64 : 0;
+  if (dtype == MLA_DTYPE_BF16 && !tc_decode_shape(heads, rank, rope_dim, dtype))
+    return fail(MLA_ERR_UNSUPPORTED, "decode_paged: bf16 is served for heads 64 or 128, rank 512, rope_dim 64 "
+                                     "(got heads %d, rank %d, rope_dim %d)", heads, rank, rope_dim);
+  const size_t need = mla_decode_workspace_size(batch, s_q, heads, rank, rope_dim, t_max, k_max,
+                                                selected_positions != nullptr, dtype);
+  MLA_CHECK(workspace_bytes >= need && (need == 0 || workspace),
+            "decode_paged: workspace of %zu bytes < %zu needed", workspace_bytes, need);
+  MLA_CHECK((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0,
+            "decode_paged: workspace must be 256-byte aligned");
+  if (dtype == MLA_DTYPE_F32) {
+    if ((int64_t)batch * s_q > 65535)
+      return fail(MLA_ERR_UNSUPPORTED, "decode_paged: f32 is served for at most 65535 query rows");
+    return cuda_status(launch_simt_decode(g, dtype, out_dtype, workspace, workspace_bytes, (cudaStream_t)stream),
+                       "decode_paged launch");
+  }
+  const int64_t ovec = out_dtype == MLA_DTYPE_F32 ? 4 : 8;
+  MLA_CHECK(aligned16(q) && aligned16(latent) && aligned16(rope) && aligned16(ctx_out),
+            "decode_paged: q, latent, rope and ctx_out must be 16-byte aligned");
+  MLA_CHECK(q_row_stride % 8 == 0 && q_head_stride % 8 == 0 && latent_row_stride % 8 == 0 &&
+                latent_page_stride % 8 == 0 && rope_row_stride % 8 == 0 && rope_page_stride % 8 == 0 &&
+                ctx_row_stride % ovec == 0 && ctx_head_stride % ovec == 0,
+            "decode_paged: strides must be multiples of 16 bytes");
+  MLA_CHECK((int64_t)batch * s_q <= (1 << 20), "decode_paged: at most 2^20 query rows");
+  MLA_CHECK(num_pages == 1 || (latent_page_stride > 0 && rope_page_stride > 0),
+            "decode_paged: page strides must be positive");
+  if (selected_positions || page_size % 16 != 0) {
+    const int64_t lp = latent_page_stride / latent_row_stride, rp = rope_page_stride / rope_row_stride;
+    if (latent_page_stride % latent_row_stride != 0 || rope_page_stride % rope_row_stride != 0 ||
+        lp * (num_pages - 1) + page_size >= (1LL << 31) || rp * (num_pages - 1) + page_size >= (1LL << 31))
+      return fail(MLA_ERR_UNSUPPORTED, "decode_paged: selections and page sizes that are no multiple of 16 need page "
+                                       "strides of whole rows and fewer than 2^31 rows");
+  }
+  return cuda_status(launch_tc_decode(g, out_dtype, workspace, workspace_bytes, (cudaStream_t)stream),
+                     "decode_paged (tensor core) launch");
+}
+
+int mla_commit_paged(const mla_state_array* arrays, int32_t n_arrays, const int32_t* page_table,
+                     int64_t page_table_stride, int32_t table_width, int32_t page_size, int32_t num_pages,
+                     const int32_t* kv_len, const int32_t* path, int64_t path_row_stride, int32_t path_width,
+                     const int32_t* counts, int32_t* kv_len_out, int32_t batch, int32_t* device_status,
+                     mla_stream_t stream) {
+  g_detail[0] = 0;
+  MLA_CHECK(arrays && kv_len && path && counts, "commit_paged: NULL pointer");
+  MLA_CHECK(n_arrays > 0 && n_arrays <= kMaxCommitArrays, "commit_paged: 1 to %d arrays", kMaxCommitArrays);
+  const int st = check_table("commit_paged", page_table, page_table_stride, table_width, page_size, num_pages, batch);
+  if (st != MLA_OK) return st;
+  MLA_CHECK(batch <= 65535, "commit_paged: at most 65535 batch rows");
+  MLA_CHECK(path_width > 0 && path_width <= kMaxTreeNodes, "commit_paged: paths of 1 to %d nodes", kMaxTreeNodes);
+  MLA_CHECK(path_row_stride >= 0, "commit_paged: path_row_stride must be non-negative");
+  MLA_CHECK(lengths_apart(kv_len_out, kv_len, counts, batch),
+            "commit_paged: kv_len_out must be kv_len or apart from kv_len and counts");
+  CommitParams p;
+  memset(&p, 0, sizeof(p));
+  for (int32_t i = 0; i < n_arrays; ++i) {
+    const mla_state_array& a = arrays[i];
+    MLA_CHECK(a.data, "commit_paged: array %d is NULL", i);
+    MLA_CHECK(a.row_bytes > 0 && a.token_stride_bytes >= a.row_bytes && a.batch_stride_bytes >= 0,
+              "commit_paged: array %d: strides too small", i);
+    int unit = 16;
+    while (unit > 1 && (reinterpret_cast<uintptr_t>(a.data) % unit || a.row_bytes % unit ||
+                        a.token_stride_bytes % unit || a.batch_stride_bytes % unit))
+      unit >>= 1;
+    p.a[i] = CommitArray{static_cast<uint8_t*>(a.data), a.token_stride_bytes, a.batch_stride_bytes, a.row_bytes, unit};
+  }
+  p.n_arrays = n_arrays;
+  p.table = page_table;
+  p.table_stride = page_table_stride;
+  p.table_width = table_width;
+  p.page_size = page_size;
+  p.num_pages = num_pages;
+  p.kv_len = kv_len;
+  p.path = path;
+  p.path_stride = path_row_stride;
+  p.counts = counts;
+  p.path_width = path_width;
+  p.kv_len_out = kv_len_out;
+  p.batch = batch;
+  p.status = device_status;
+  return cuda_status(launch_commit_paged(p, (cudaStream_t)stream), "commit_paged launch");
+}
+
 // ------------------------------------------------------------ reconstructed prefill
 
 int mla_reconstruct_kv(const void* latent, int64_t latent_row_stride, int64_t n_rows, const void* kv_b_proj,

@@ -53,6 +53,14 @@ struct DecodeGeometry {
   const uint8_t* scales;
   int64_t scales_batch_stride;
   int32_t block_shift;
+  // Paged cache (null table: windows): pages of page_size rows; no kv_start, no batch strides.
+  const int32_t* table;
+  int64_t table_stride;
+  int32_t table_width, page_size, num_pages;
+  int64_t latent_page_stride, rope_page_stride;
+  const int32_t* counts;      // [batch] new tokens of each row (null: s_q)
+  const uint64_t* tree;       // [n_q][tree_words] ancestor masks (null: tokens in a row)
+  int32_t tree_words;
 };
 
 // CUDA-core decode of the f32 path (any shape; f32 q and cache).
@@ -220,6 +228,70 @@ struct CompactParams {
   int32_t* status;
 };
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
+
+// Writing a paged cache: append, tree plan, commit of an accepted path.
+struct AppendPagedParams {
+  const void* latent_raw;
+  int64_t lr_row_stride, lr_tok_stride;
+  const void* rope_raw;
+  int64_t rr_row_stride, rr_tok_stride;
+  const void* weight;
+  float eps;
+  const int32_t* positions;   // [batch][s_new] (null: the token's key index)
+  void* latent;
+  int64_t l_row_stride, l_page_stride;
+  void* rope;
+  int64_t r_row_stride, r_page_stride;
+  const int32_t* table;
+  int64_t table_stride;
+  int32_t table_width, page_size, num_pages;
+  const int32_t* kv_len;
+  const int32_t* counts;
+  int32_t* kv_len_out;
+  int32_t batch, s_new, rank, rope_dim;
+  int32_t* status;
+  int32_t lengths_here;       // set by the launcher: the kernel writes kv_len_out
+  float inv_freq[kMaxRotaryDims / 2];
+};
+cudaError_t launch_append_paged(AppendPagedParams p, int in_dtype, int cache_dtype, cudaStream_t stream);
+
+constexpr int kMaxTreeNodes = 1024;
+struct TreePlanParams {
+  const int32_t* parents;
+  int64_t parents_stride;
+  const int32_t* kv_len;
+  const int32_t* counts;
+  int32_t* positions;
+  uint64_t* mask;
+  int32_t batch, n_nodes;
+  int32_t* status;
+};
+cudaError_t launch_tree_plan(const TreePlanParams& p, cudaStream_t stream);
+
+constexpr int kMaxCommitArrays = 256;
+struct CommitArray {
+  uint8_t* data;
+  int64_t row_bytes_stride, page_bytes_stride;
+  int32_t row_bytes;
+  int32_t unit;               // bytes moved together: 16, 8, 4, 2 or 1
+};
+struct CommitParams {
+  CommitArray a[kMaxCommitArrays];
+  int32_t n_arrays;
+  const int32_t* table;
+  int64_t table_stride;
+  int32_t table_width, page_size, num_pages;
+  const int32_t* kv_len;
+  const int32_t* path;
+  int64_t path_stride;
+  const int32_t* counts;
+  int32_t path_width;
+  int32_t* kv_len_out;
+  int32_t batch;
+  int32_t* status;
+  int32_t lengths_here;
+};
+cudaError_t launch_commit_paged(CommitParams& p, cudaStream_t stream);
 
 // Deterministic top-k selection of positions from per-row f32 scores.
 struct SelectParams {

@@ -9,6 +9,7 @@
 
 #include "e4m3.cuh"
 #include "mla_internal.h"
+#include "paged.cuh"
 
 namespace mla {
 namespace {
@@ -76,6 +77,32 @@ __device__ __forceinline__ bool q8_window_ok(const DecodeGeometry& g, int b) {
   return ok;
 }
 
+// A row of a paged cache: the keys that a token sees (in a tree some of
+// [0, limit) are not), and the first of the row's new tokens.
+__device__ __forceinline__ RowKeys paged_row_keys(const DecodeGeometry& g, int n, int& first) {
+  RowKeys k;
+  const int b = n / g.s_q, i = n % g.s_q;
+  const int len = g.kv_len[b], count = paged_count(g.counts, b, g.s_q);
+  const bool fits = len >= 0 && len <= g.t_max && count >= 0;
+  if (!fits && g.device_status) atomicOr(g.device_status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
+  first = len - count;
+  k.start = 0;
+  k.limit = fits ? paged_limit(len, count, i, g.tree ? g.tree + (int64_t)n * g.tree_words : nullptr, g.tree_words) : 0;
+  k.count = k.limit;
+  k.list = nullptr;
+  k.batch_off_lat = k.batch_off_rope = 0;
+  if (g.sel != nullptr && k.limit > 0) {   // the selection of a token that sees nothing is not read
+    const int32_t c = g.sel_count[n];
+    if (c != -1) {
+      const bool good = c > 0 && c <= g.k_max;
+      if (!good && g.device_status) atomicOr(g.device_status, MLA_DEVICE_BAD_SELECTION_COUNT);
+      k.count = good ? c : 0;
+      k.list = g.sel + (int64_t)n * g.k_max;
+    }
+  }
+  return k;
+}
+
 constexpr int kDecodeWarps = 4;
 constexpr int kMaxD = 1280;            // rank + rope
 constexpr int kMaxRank = 1024;
@@ -84,7 +111,9 @@ constexpr int kMaxRankPerLane = kMaxRank / 32;
 // grid (splits, heads, n_q); 4 warps.  Split s of row n covers entries
 // [s*chunk, (s+1)*chunk) of that row's key list, chunk = ceil(count/splits).
 // kQ8: the latent comes from e4m3 codes and their block's exponent.
-template <typename T, typename TO, bool kQ8 = false>
+// kPaged: the rows are found through the page table, and a tree's token passes
+// over the keys that it does not see.
+template <typename T, typename TO, bool kQ8 = false, bool kPaged = false>
 __global__ void __launch_bounds__(kDecodeWarps * 32)
     simt_decode_kernel(const __grid_constant__ DecodeGeometry g, float* __restrict__ ws, int splits) {
   const int split = blockIdx.x, h = blockIdx.y, n = blockIdx.z;
@@ -98,7 +127,11 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
   for (int d = threadIdx.x; d < D; d += blockDim.x) q_s[d] = to_f(qrow[d]);
   __syncthreads();
 
-  RowKeys rk = row_keys(g, n);
+  int first = 0;
+  RowKeys rk;
+  if constexpr (kPaged) rk = paged_row_keys(g, n, first); else rk = row_keys(g, n);
+  const int32_t* table = kPaged ? g.table + (n / g.s_q) * g.table_stride : nullptr;
+  const uint64_t* mask = kPaged && g.tree ? g.tree + (int64_t)n * g.tree_words : nullptr;
   if (kQ8 && !q8_window_ok(g, n / g.s_q)) rk.count = 0;
   const int chunk = (rk.count + splits - 1) / splits;
   const int lo = split * chunk;
@@ -128,6 +161,17 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
     const uint8_t* crow = kQ8 ? codes + row * g.codes_row_stride : nullptr;
     const float unit = kQ8 ? unit_of(clamp_exponent(scales[row >> g.block_shift])) : 1.f;
     const T* rrow = rop + row * g.rope_row_stride;
+    if constexpr (kPaged) {
+      const int node = t - first;
+      if (mask && node >= 0 && !((mask[node >> 6] >> (node & 63)) & 1)) continue;
+      const int at = t / g.page_size, in_page = t - at * g.page_size, page = table[at];
+      if (page < 0 || page >= g.num_pages) {
+        if (lane == 0 && g.device_status) atomicOr(g.device_status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
+        continue;
+      }
+      lrow = lat + page * g.latent_page_stride + in_page * g.latent_row_stride;
+      rrow = rop + page * g.rope_page_stride + in_page * g.rope_row_stride;
+    }
     float c[kMaxRankPerLane];
     float part = 0.f;
 #pragma unroll
@@ -169,11 +213,12 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
 #pragma unroll
   for (int w = 0; w < kDecodeWarps; ++w) {
     wgt[w] = (m_s[w] == -CUDART_INF_F) ? 0.f : exp2f(m_s[w] - M);
+    if (kPaged && l_s[w] != l_s[w]) wgt[w] = 1.f;   // scores of NaN alone: their sum stays NaN
     L += wgt[w] * l_s[w];
   }
   const int64_t slot = ((int64_t)n * splits + split) * g.heads + h;
   // an 8-bit cache's NaN codes: a sum of NaN is no empty one
-  const bool some = kQ8 ? L != 0.f : L > 0.f;
+  const bool some = kQ8 || kPaged ? L != 0.f : L > 0.f;
   if (splits == 1) {
     const float inv = some ? 1.f / L : 0.f;
     TO* out = static_cast<TO*>(g.ctx_out) + (int64_t)n * g.ctx_row_stride + (int64_t)h * g.ctx_head_stride;
@@ -196,7 +241,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
     const int64_t nslots = (int64_t)gridDim.z * splits * g.heads;
     if (threadIdx.x == 0) {
       float* ml = ws + nslots * g.rank;
-      ml[2 * slot] = !some ? -CUDART_INF_F : (kQ8 && M == -CUDART_INF_F) ? 0.f : M;
+      ml[2 * slot] = !some ? -CUDART_INF_F : ((kQ8 || kPaged) && M == -CUDART_INF_F) ? 0.f : M;
       ml[2 * slot + 1] = L;
     }
   }
@@ -427,8 +472,12 @@ cudaError_t launch_simt_decode(const DecodeGeometry& g, int dtype, int out_dtype
   simt_decode_kernel<T, TO><<<grid, kDecodeWarps * 32, 0, stream>>>(g, ws, splits); \
   if (splits > 1) simt_combine_kernel<TO><<<dim3(g.heads, n_q), 128, 0, stream>>>(g, ws, splits);
   if (dtype != MLA_DTYPE_F32) return cudaErrorInvalidValue;
-  if (g.codes != nullptr) {
-    if (out_dtype == MLA_DTYPE_F32)
+  if (g.codes != nullptr || g.table != nullptr) {
+    if (g.table != nullptr && out_dtype == MLA_DTYPE_F32)
+      simt_decode_kernel<float, float, false, true><<<grid, kDecodeWarps * 32, 0, stream>>>(g, ws, splits);
+    else if (g.table != nullptr)
+      simt_decode_kernel<float, __nv_bfloat16, false, true><<<grid, kDecodeWarps * 32, 0, stream>>>(g, ws, splits);
+    else if (out_dtype == MLA_DTYPE_F32)
       simt_decode_kernel<float, float, true><<<grid, kDecodeWarps * 32, 0, stream>>>(g, ws, splits);
     else
       simt_decode_kernel<float, __nv_bfloat16, true><<<grid, kDecodeWarps * 32, 0, stream>>>(g, ws, splits);

@@ -43,6 +43,7 @@
 #include <math_constants.h>
 
 #include "mla_internal.h"
+#include "paged.cuh"
 #include "q8_tiles.cuh"
 #include "tc_common.cuh"
 #include "tc_host.h"
@@ -171,13 +172,35 @@ struct TcDecodeArgs {
   int64_t scales_batch_stride;
   int32_t block_shift;
   int64_t t_max;
+  // Paged cache (null table: windows): a row's keys by pages of page_size rows, read in boxes of
+  // box_rows rows, or row by row (lat_rows_per_batch, rope_rows_per_batch: between pages).
+  const int32_t* table;
+  int64_t table_stride;
+  int32_t page_size, num_pages, box_rows;
+  const int32_t* counts;
+  const uint64_t* tree;
+  int32_t tree_words;
 };
 
 // ------------------------------------------------------------------ helpers
 
+__device__ __forceinline__ const uint64_t* tree_of(const TcDecodeArgs& a, int n) {
+  return a.tree ? a.tree + (int64_t)n * a.tree_words : nullptr;
+}
+
+// The first of the new tokens' keys of a paged row.
+__device__ __forceinline__ int paged_first(const TcDecodeArgs& a, int n) {
+  const int b = n / a.s_q;
+  return a.kv_len[b] - paged_count(a.counts, b, a.s_q);
+}
+
 __device__ __forceinline__ int row_limit(const TcDecodeArgs& a, int n) {
   const int b = n / a.s_q, i = n % a.s_q;
   const int len = a.kv_len[b];
+  if (a.table) {
+    const int count = paged_count(a.counts, b, a.s_q);
+    return len < 0 || len > a.t_max || count < 0 ? 0 : paged_limit(len, count, i, tree_of(a, n), a.tree_words);
+  }
   int lim = len - a.s_q + i + 1;
   lim = lim < 0 ? 0 : (lim > len ? len : lim);
   return lim;
@@ -261,6 +284,7 @@ __device__ __forceinline__ int last_group_of(const int32_t* prefix, int u, int p
 __device__ __forceinline__ bool member_segment(const TcDecodeArgs& a, const int32_t* keys, int u, int member,
                                                int& n, int& t0, int& t1) {
   n = u * a.width + member;
+  if (n >= a.n_q) return false;   // the last unit may have fewer rows
   const int tiles = (keys[n] + BN - 1) / BN;
   if (t1 > tiles) t1 = tiles;
   return t0 < t1;
@@ -302,12 +326,51 @@ __device__ __forceinline__ void gather_key_group(const TcDecodeArgs& a, const CU
   tma_gather4(dst + 4 * CHUNK_BYTES + g * 4 * 64, rope_rows_map, bar, 32 * (int)rank, rr[0], rr[1], rr[2], rr[3]);
 }
 
+// The same over pages: the four rows are found through the row's page table.
+// Entries past the count, or that name a key out of range, load the row's first
+// key; a page outside the pool (flagged) is read as page 0.
+__device__ __forceinline__ void gather_paged_group(const TcDecodeArgs& a, const CUtensorMap* lat_rows_map,
+                                                   const CUtensorMap* rope_rows_map, uint8_t* dst, uint64_t* bar, int g,
+                                                   int t, int limit, int keys, const int32_t* table,
+                                                   const int32_t* list, uint32_t rank, int dim_base) {
+  int lr[4], rr[4], pos[4], page[4], row[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int e = t * BN + 4 * g + j;
+    pos[j] = e < keys ? (list ? __ldg(list + e) : e) : 0;
+  }
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (pos[j] < 0 || pos[j] >= limit) bad = true, pos[j] = 0;
+    const int at = pos[j] / a.page_size;
+    row[j] = pos[j] - at * a.page_size;
+    page[j] = __ldg(table + at);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (page[j] < 0 || page[j] >= a.num_pages) bad = true, page[j] = 0;
+    lr[j] = page[j] * a.lat_rows_per_batch + row[j];
+    rr[j] = page[j] * a.rope_rows_per_batch + row[j];
+  }
+  if (bad && a.status && rank == 0) atomicOr(a.status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
+  for (int c = 0; c < 4; ++c)
+    tma_gather4(dst + c * CHUNK_BYTES + g * 4 * 128, lat_rows_map, bar, dim_base + 64 * c, lr[0], lr[1], lr[2], lr[3]);
+  tma_gather4(dst + 4 * CHUNK_BYTES + g * 4 * 64, rope_rows_map, bar, 32 * (int)rank, rr[0], rr[1], rr[2], rr[3]);
+}
+
 // ------------------------------------------------------------------ planner
 // Per query row the number of visible entries; the planner (or the decode
 // prologue) turns them into tiles and the exclusive prefix of tiles over work
 // units.  Bad selection counts give 0 and are flagged where `flag` is set.
 __device__ __forceinline__ int row_keys(const TcDecodeArgs& a, int n, bool flag) {
   int keys = row_limit(a, n);
+  if (a.table) {
+    const int b = n / a.s_q, len = a.kv_len[b];
+    if (flag && a.status && (len < 0 || len > a.t_max || paged_count(a.counts, b, a.s_q) < 0))
+      atomicOr(a.status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
+    if (keys == 0) return 0;   // the selection of a token that sees nothing is not read
+  }
   if (a.codes) {
     // the 8-bit cache is read by plain loads: a window outside the buffer, or
     // one that does not start on a whole block, is no window
@@ -336,7 +399,8 @@ __device__ __forceinline__ int row_keys(const TcDecodeArgs& a, int n, bool flag)
 // thread of the block, blockDim >= n_q): visible entries per query row, then per
 // unit its tiles (the longest of its `width` rows) and their exclusive prefix,
 // scanned by warp 0 (four units per lane, in unit order).
-// With start_s / limit_s, also each row's first cache row and window limit.
+// With start_s / limit_s, also each row's first cache row (of a paged row: the
+// first of its new tokens' keys) and window limit.
 __device__ __forceinline__ void plan_rows(const TcDecodeArgs& a, int32_t* keys_s, int32_t* prefix_s, bool flag,
                                           int32_t* start_s = nullptr, int32_t* limit_s = nullptr) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -344,7 +408,7 @@ __device__ __forceinline__ void plan_rows(const TcDecodeArgs& a, int32_t* keys_s
     const int n = threadIdx.x;
     keys_s[n] = row_keys(a, n, flag);
     if (start_s) {
-      start_s[n] = a.kv_start ? a.kv_start[n / a.s_q] : 0;
+      start_s[n] = a.table ? paged_first(a, n) : a.kv_start ? a.kv_start[n / a.s_q] : 0;
       limit_s[n] = row_limit(a, n);
     }
   }
@@ -357,7 +421,8 @@ __device__ __forceinline__ void plan_rows(const TcDecodeArgs& a, int32_t* keys_s
       const int u = 32 * j + lane;
       int tiles = 0;
       if (u < a.n_units)
-        for (int i = 0; i < a.width; ++i) tiles = max(tiles, (keys_s[u * a.width + i] + BN - 1) / BN);
+        for (int i = 0; i < a.width && u * a.width + i < a.n_q; ++i)
+          tiles = max(tiles, (keys_s[u * a.width + i] + BN - 1) / BN);
       tl[j] = tiles;
       raw += tiles;
     }
@@ -397,7 +462,7 @@ __global__ void __launch_bounds__(1024) tc_plan_kernel(const __grid_constant__ T
   int raw = 0;
   for (int u = threadIdx.x; u < a.n_units; u += 1024) {
     int tiles = 0;
-    for (int i = 0; i < a.width; ++i) {
+    for (int i = 0; i < a.width && u * a.width + i < a.n_q; ++i) {
       const int n = u * a.width + i;
       const int keys = row_keys(a, n, true);
       a.keys[n] = keys;
@@ -418,7 +483,7 @@ __global__ void __launch_bounds__(1024) tc_plan_kernel(const __grid_constant__ T
     int ext = 0;
     if (u < a.n_units) {
       int tiles = 0;
-      for (int i = 0; i < a.width; ++i) {
+      for (int i = 0; i < a.width && u * a.width + i < a.n_q; ++i) {
         const int t = (a.keys[u * a.width + i] + BN - 1) / BN;
         tiles = t > tiles ? t : tiles;
       }
@@ -470,7 +535,12 @@ __global__ void __launch_bounds__(1024) tc_plan_kernel(const __grid_constant__ T
 // takes 21 instructions for 16 codes where bf16, which the hardware does not
 // convert to, takes 51: the converting warps share the issue slots with the
 // softmax (ragged decode 174 -> 165 us, verify 628 -> 554 us).
-template <int kPrefetchAhead, int kThreads, bool kLateP, bool kQ8 = false>
+// kPaged: the keys come from pages (boxes of a page's rows, or in the instance
+// with the extra gather warps row by row), and a token of a tree sees some keys
+// of its last tiles only.  Rows of a tile that its token does not see are
+// cleared before the scores: a probability of 0 must not meet what another
+// token, or nobody, left there.
+template <int kPrefetchAhead, int kThreads, bool kLateP, bool kQ8 = false, bool kPaged = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_decode_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_constant__ CUtensorMap rope_map,
                      const __grid_constant__ CUtensorMap lat_rows_map, const __grid_constant__ CUtensorMap rope_rows_map,
@@ -507,7 +577,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int dim_base = 256 * (int)rank;     // first latent dim of this CTA
   const int cluster = blockIdx.x >> 1;
   const int group = cluster / a.width, member = cluster % a.width;
-  const bool gather = a.sel != nullptr;
+  constexpr bool kPagedGather = kPaged && kThreads > THREADS;
+  const bool gather = kPaged ? kPagedGather : a.sel != nullptr;
 
   if (threadIdx.x == 0) {
     if (!kQ8 || !gather) tma_prefetch_desc(&rope_map);
@@ -587,10 +658,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     while (!aborted() && it.next(u, t0, t1, whole)) {
       if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
       const int keys = keys_p[n];
+      const uint64_t* mask = kPaged ? tree_of(a, n) : nullptr;
+      const int first = !kPaged || !mask ? keys : a.plan_in_kernel ? row_start_s[n] : paged_first(a, n);
       if (!mbar_wait_warp(&q_full, seg & 1u, kWaitLimit)) { fail(); break; }
       for (int t = t0; t < t1; ++t) {
+        uint64_t seen = ~0ull;
+        if (kPaged && (t + 1) * BN > min(keys, first)) seen = paged_seen(t * BN, keys, first, mask, a.tree_words);
         if (!mbar_wait_warp(&full_bar[stage], phase, kWaitLimit)) { fail(); break; }
-        if (!kQ8 && !gather && t == (keys - 1) / BN && (keys % BN) != 0) {
+        if (kPaged && seen != ~0ull) {
+          uint8_t* st = stages + stage * STAGE_BYTES;
+#pragma unroll 1
+          for (int q16 = lane; q16 < BN * 36; q16 += 32) {
+            const int r = q16 / 36, v = q16 - 36 * r;
+            if (seen >> r & 1) continue;
+            *reinterpret_cast<uint4*>(st + (v < 32 ? (v >> 3) * CHUNK_BYTES + r * 128 + (v & 7) * 16
+                                                   : 4 * CHUNK_BYTES + r * 64 + (v - 32) * 16)) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (!kPaged && !kQ8 && !gather && t == (keys - 1) / BN && (keys % BN) != 0) {
           // Tail tile: clear the rows past the window so that P = 0 never meets
           // a non-finite value left in the caller's buffer.
           const int valid = keys % BN;
@@ -603,7 +690,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (!kQ8 && gather && !a.gather_tma) fence_proxy_async_smem();
+        if (!kPaged && !kQ8 && gather && !a.gather_tma) fence_proxy_async_smem();
         if (tile > 0 && !mbar_wait_warp(&s_free, (tile - 1) & 1u, kWaitLimit)) { fail(); break; }
         tc_fence_after();
         // 16 latent K-steps, then this CTA's two rope K-steps.  Descriptors
@@ -823,8 +910,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int limit = a.plan_in_kernel ? row_limit_s[n] : row_limit(a, n);
       const int keys = keys_p[n];
       const int zb = a.batch_in_map ? b : 0;
-      const int32_t* list = (gather && a.sel_count[n] != -1) ? a.sel + (int64_t)n * a.k_max : nullptr;
-      if (!gather && lane == 0) {
+      const int32_t* list = (gather && (!kPaged || a.sel) && a.sel_count[n] != -1) ? a.sel + (int64_t)n * a.k_max : nullptr;
+      const int32_t* table = kPaged ? a.table + b * a.table_stride : nullptr;
+      // Pages: a tile is boxes of a.box_rows rows (a divisor of 64 and of the page size), one per lane.
+      const int boxes = kPaged ? BN / a.box_rows : 0;
+      auto box_at = [&](int t, int& page, int& row) {   // this lane's box of tile t; page -1: no key in it
+        const int key = t * BN + lane * a.box_rows, at = key / a.page_size;
+        page = -1;
+        row = key - at * a.page_size;
+        if (lane < boxes && key < keys) {
+          page = __ldg(table + at);
+          if (page < 0 || page >= a.num_pages) {   // flagged, and read as zeros: no such page in the map
+            page = a.num_pages;
+            if (a.status && rank == 0) atomicOr(a.status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
+          }
+        }
+      };
+      auto prefetch_box = [&](int t) {
+        int page, row;
+        box_at(t, page, row);
+        if (page < 0 || page >= a.num_pages) return;
+        for (int c = 0; c < 4; ++c) tma_prefetch_l2_3d(&lat_map, dim_base + 64 * c, row, page);
+        tma_prefetch_l2_3d(&rope_map, 32 * (int)rank, row, page);
+      };
+      int page = -1, row = 0;
+      if (kPaged && !gather) {
+        box_at(t0, page, row);
+        for (int t = t0 + STAGES; t < t0 + kPrefetchAhead && t < t1; ++t) prefetch_box(t);
+      }
+      if (!kPaged && !gather && lane == 0) {
         // the segment's first tiles that the loop's look-ahead will not cover
         for (int t = t0 + STAGES; t < t0 + kPrefetchAhead && t < t1; ++t) {
           for (int c = 0; c < 4; ++c) tma_prefetch_l2_3d(&lat_map, dim_base + 64 * c, start + t * BN, zb);
@@ -833,7 +947,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       for (int t = t0; t < t1 && !aborted(); ++t) {
         if (fills++ >= STAGES && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
-        if (!gather) {
+        if (kPaged && !gather) {
+          const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
+          if (lane == 0) mbar_arrive_expect_tx(&full_bar[stage], __popc(there) * a.box_rows * (STAGE_BYTES / BN));
+          __syncwarp();
+          if (page >= 0) {
+            uint8_t* dst = stages + stage * STAGE_BYTES + lane * a.box_rows * 128;
+            for (int c = 0; c < 4; ++c)
+              tma_load_3d(dst + c * CHUNK_BYTES, &lat_map, &full_bar[stage], dim_base + 64 * c, row, page);
+            tma_load_3d(dst + 4 * CHUNK_BYTES - lane * a.box_rows * 64, &rope_map, &full_bar[stage], 32 * (int)rank, row,
+                        page);
+          }
+          if (t + 1 < t1) box_at(t + 1, page, row);
+          if (t + kPrefetchAhead < t1) prefetch_box(t + kPrefetchAhead);
+          __syncwarp();
+        } else if (!gather) {
           if (lane == 0) {
             mbar_arrive_expect_tx(&full_bar[stage], STAGE_TX);
             uint8_t* dst = stages + stage * STAGE_BYTES;
@@ -859,9 +987,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive_expect_tx(&full_bar[stage], STAGE_TX);
           __syncwarp();
           constexpr int kIssuers = 1 + (kThreads - THREADS) / 32;
-          if (kIssuers * lane < BN / 4)
-            gather_key_group(a, &lat_rows_map, &rope_rows_map, stages + stage * STAGE_BYTES, &full_bar[stage],
-                             kIssuers * lane, t, b, start, limit, keys, list, rank, dim_base);
+          if (kIssuers * lane < BN / 4) {
+            if constexpr (kPaged)
+              gather_paged_group(a, &lat_rows_map, &rope_rows_map, stages + stage * STAGE_BYTES, &full_bar[stage],
+                                 kIssuers * lane, t, limit, keys, table, list, rank, dim_base);
+            else
+              gather_key_group(a, &lat_rows_map, &rope_rows_map, stages + stage * STAGE_BYTES, &full_bar[stage],
+                               kIssuers * lane, t, b, start, limit, keys, list, rank, dim_base);
+          }
         } else {
           // Row gather: lane L owns keys L and L+32 of the tile.
           const int e0 = t * BN + lane, e1 = e0 + 32;
@@ -934,13 +1067,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int start = a.plan_in_kernel ? row_start_s[n] : (a.kv_start ? a.kv_start[b] : 0);
         const int limit = a.plan_in_kernel ? row_limit_s[n] : row_limit(a, n);
         const int keys = keys_p[n];
-        const int32_t* list = a.sel_count[n] != -1 ? a.sel + (int64_t)n * a.k_max : nullptr;
+        const int32_t* list = (!kPaged || a.sel) && a.sel_count[n] != -1 ? a.sel + (int64_t)n * a.k_max : nullptr;
         for (int t = t0; t < t1 && !aborted(); ++t) {
           if (fills++ >= STAGES && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
           const int g = issuer + kIssuers * lane;
-          if (g < BN / 4)
-            gather_key_group(a, &lat_rows_map, &rope_rows_map, stages + stage * STAGE_BYTES, &full_bar[stage], g, t,
-                             b, start, limit, keys, list, rank, dim_base);
+          if (g < BN / 4) {
+            if constexpr (kPaged)
+              gather_paged_group(a, &lat_rows_map, &rope_rows_map, stages + stage * STAGE_BYTES, &full_bar[stage], g, t,
+                                 limit, keys, a.table + b * a.table_stride, list, rank, dim_base);
+            else
+              gather_key_group(a, &lat_rows_map, &rope_rows_map, stages + stage * STAGE_BYTES, &full_bar[stage], g, t,
+                               b, start, limit, keys, list, rank, dim_base);
+          }
           if (++stage == STAGES) stage = 0, phase ^= 1u;
         }
       }
@@ -1159,7 +1297,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       const int keys = keys_p[n];
       const int limit = a.plan_in_kernel ? row_limit_s[n] : row_limit(a, n);
-      const int32_t* list = (gather && a.sel_count[n] != -1) ? a.sel + (int64_t)n * a.k_max : nullptr;
+      const int32_t* list = (gather && (!kPaged || a.sel) && a.sel_count[n] != -1) ? a.sel + (int64_t)n * a.k_max : nullptr;
+      const uint64_t* mask = kPaged ? tree_of(a, n) : nullptr;
+      const int first = !kPaged || !mask ? keys : a.plan_in_kernel ? row_start_s[n] : paged_first(a, n);
       float m_used = -CUDART_INF_F, l = 0.f;
       constexpr float kRaise = kQ8 ? kRaiseF16 : 0.f;   // l is 2^kRaise times the sum relative to m_used
       bool first_tile = true;
@@ -1176,7 +1316,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---- validity of this tile's 64 entries (lane L: entries L, L+32);
         // a whole tile of a dense row needs no check (warp-uniform test)
         uint64_t valid = ~0ull;
-        if (list != nullptr || (t + 1) * BN > keys) {
+        if (kPaged && list == nullptr) {
+          if ((t + 1) * BN > min(keys, first)) valid = paged_seen(t * BN, keys, first, mask, a.tree_words);
+        } else if (list != nullptr || (t + 1) * BN > keys) {
           const int e0 = t * BN + lane, e1 = e0 + 32;
           bool v0 = e0 < keys, v1 = e1 < keys;
           if (list) {
@@ -1887,7 +2029,9 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
   // A dense multi-token verify serves each batch row's tokens with a group of
   // clusters in lockstep; everything else is one query row per unit.
   a.width = (g.sel == nullptr && g.s_q > 1 && g.s_q <= 8) ? g.s_q : 1;
-  a.n_units = n_q / a.width;
+  const bool paged = g.table != nullptr;
+  if (paged && g.sel == nullptr && g.s_q > 8) a.width = 8;
+  a.n_units = (n_q + a.width - 1) / a.width;
   a.min_tiles = kMinTilesPerGroup;
   const bool q8 = g.codes != nullptr;   // codes are copied row by row: only rope keys are mapped
   a.batch_in_map = ((g.latent_batch_stride != 0 && !q8) || g.rope_batch_stride != 0) ? 1 : 0;
@@ -1902,12 +2046,36 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
   a.t_max = g.t_max;
   a.gather_tma = 0;
   a.lat_rows_per_batch = a.rope_rows_per_batch = 0;
+  a.table = g.table;
+  a.table_stride = g.table_stride;
+  a.page_size = g.page_size;
+  a.num_pages = g.num_pages;
+  a.counts = g.counts;
+  a.tree = g.tree;
+  a.tree_words = g.tree_words;
+  // the largest box that divides a tile and a page
+  a.box_rows = BN;
+  while (paged && g.page_size % a.box_rows != 0) a.box_rows >>= 1;
+  // Boxes of 16 rows and more; smaller ones take as long to issue as single rows.
+  const bool paged_rows = paged && (g.sel != nullptr || a.box_rows < 16);
 
   // Tensor maps over [B_buf, t_max, dims] (the batch axis has extent 1 for a
   // packed-flat cache whose batch stride is 0).
   const uint64_t bmap = a.batch_in_map ? (uint64_t)g.batch : 1;
-  CUtensorMap lat_map = {}, rope_map;
-  if (!q8) {
+  CUtensorMap lat_map = {}, rope_map = {};
+  if (paged && !paged_rows) {
+    // [pages, page rows, dims]
+    const uint64_t ldims[3] = {(uint64_t)g.rank, (uint64_t)g.page_size, (uint64_t)g.num_pages};
+    const uint64_t rdims[3] = {(uint64_t)g.rope_dim, (uint64_t)g.page_size, (uint64_t)g.num_pages};
+    // (one page: its stride has no meaning)
+    const uint64_t lstrides[2] = {(uint64_t)g.latent_row_stride * 2, (uint64_t)(g.num_pages > 1 ? g.latent_page_stride : g.latent_row_stride * g.page_size) * 2};
+    const uint64_t rstrides[2] = {(uint64_t)g.rope_row_stride * 2, (uint64_t)(g.num_pages > 1 ? g.rope_page_stride : g.rope_row_stride * g.page_size) * 2};
+    const uint32_t lbox[3] = {64, (uint32_t)a.box_rows, 1}, rbox[3] = {32, (uint32_t)a.box_rows, 1};
+    if (!encode_tmap_bf16(&lat_map, g.latent, 3, ldims, lstrides, lbox) ||
+        !encode_tmap_bf16(&rope_map, g.rope, 3, rdims, rstrides, rbox, CU_TENSOR_MAP_SWIZZLE_64B))
+      return cudaErrorInvalidValue;
+  }
+  if (!q8 && !paged) {
     const uint64_t dims[3] = {(uint64_t)g.rank, (uint64_t)g.t_max, bmap};
     const uint64_t bstride = a.batch_in_map ? (uint64_t)g.latent_batch_stride * 2
                                             : (uint64_t)g.t_max * g.latent_row_stride * 2;
@@ -1915,7 +2083,7 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
     const uint32_t box[3] = {64, BN, 1};
     if (!encode_tmap_bf16(&lat_map, g.latent, 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  {
+  if (!paged) {
     const uint64_t dims[3] = {(uint64_t)g.rope_dim, (uint64_t)g.t_max, bmap};
     const uint64_t bstride = a.batch_in_map ? (uint64_t)g.rope_batch_stride * 2
                                             : (uint64_t)g.t_max * g.rope_row_stride * 2;
@@ -1927,7 +2095,7 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
   // Row maps for gathers: the cache as [rows, dims] with one-row boxes; a
   // batch row's rows start at b * (batch stride / row stride).
   CUtensorMap lat_rows_map = lat_map, rope_rows_map = rope_map;
-  if (!q8 && g.sel != nullptr && g.latent_batch_stride % g.latent_row_stride == 0 &&
+  if (!q8 && !paged && g.sel != nullptr && g.latent_batch_stride % g.latent_row_stride == 0 &&
       g.rope_batch_stride % g.rope_row_stride == 0) {
     a.lat_rows_per_batch = a.batch_in_map ? (int32_t)(g.latent_batch_stride / g.latent_row_stride) : 0;
     a.rope_rows_per_batch = a.batch_in_map ? (int32_t)(g.rope_batch_stride / g.rope_row_stride) : 0;
@@ -1940,12 +2108,29 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
         encode_tmap_bf16(&rope_rows_map, g.rope, 2, rd, rs, rbox, CU_TENSOR_MAP_SWIZZLE_64B))
       a.gather_tma = 1;
   }
+  if (paged_rows) {
+    a.lat_rows_per_batch = (int32_t)(g.latent_page_stride / g.latent_row_stride);
+    a.rope_rows_per_batch = (int32_t)(g.rope_page_stride / g.rope_row_stride);
+    const uint64_t ld[2] = {(uint64_t)g.rank, (uint64_t)(g.num_pages - 1) * a.lat_rows_per_batch + g.page_size};
+    const uint64_t rd[2] = {(uint64_t)g.rope_dim, (uint64_t)(g.num_pages - 1) * a.rope_rows_per_batch + g.page_size};
+    const uint64_t ls[1] = {(uint64_t)g.latent_row_stride * 2}, rs[1] = {(uint64_t)g.rope_row_stride * 2};
+    const uint32_t box[2] = {64, 1}, rbox[2] = {32, 1};
+    if (!encode_tmap_bf16(&lat_rows_map, g.latent, 2, ld, ls, box) ||
+        !encode_tmap_bf16(&rope_rows_map, g.rope, 2, rd, rs, rbox, CU_TENSOR_MAP_SWIZZLE_64B))
+      return cudaErrorInvalidValue;
+    lat_map = lat_rows_map;   // (unused, but prefetched)
+    rope_map = rope_rows_map;
+    a.gather_tma = 1;
+  }
   const bool lockstep = a.width > 1;
   // (the prefetch distance only serves the dense path; gathers take the
   // instance with the extra gather warps)
   // (an 8-bit cache is served by one instance: announcing P late, as the
   // lockstep groups do, costs it 11 %)
-  auto* const decode_kernel = q8 ? tc_decode_kernel<kPrefetchAheadRow, THREADS_Q8, false, true>
+  auto* const decode_kernel = paged_rows ? tc_decode_kernel<kPrefetchAheadRow, THREADS_GATHER, false, false, true>
+                              : paged && lockstep ? tc_decode_kernel<kPrefetchAheadGroup, THREADS, true, false, true>
+                              : paged ? tc_decode_kernel<kPrefetchAheadRow, THREADS, false, false, true>
+                              : q8 ? tc_decode_kernel<kPrefetchAheadRow, THREADS_Q8, false, true>
                               : a.gather_tma ? tc_decode_kernel<kPrefetchAheadRow, THREADS_GATHER, false>
                               : lockstep   ? tc_decode_kernel<kPrefetchAheadGroup, THREADS, true>
                                            : tc_decode_kernel<kPrefetchAheadRow, THREADS, false>;

@@ -726,7 +726,7 @@ int mla_cache_compact(const mla_state_array* arrays, int32_t n_arrays, const int
  * mla_decode_workspace_size with t_max = table_width * page_size.
  * bf16 is served for the shapes of mla_decode_attend, with pool pointers
  * 16-byte aligned and strides multiples of 16 bytes.  Page sizes that are
- * multiples of 16 rows are read by TMA boxes; others, and selections, row by
+ * multiples of 8 rows are read by TMA boxes; others, and selections, row by
  * row, which needs page strides that are whole numbers of rows and pools of
  * fewer than 2^31 rows (else MLA_ERR_UNSUPPORTED).  f32 for any shape, at most
  * 65535 query rows.

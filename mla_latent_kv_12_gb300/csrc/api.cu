@@ -1141,14 +1141,16 @@ int mla_decode_attend_paged(const void* q, int64_t q_row_stride, int64_t q_head_
   MLA_CHECK((int64_t)batch * s_q <= (1 << 20), "decode_paged: at most 2^20 query rows");
   MLA_CHECK(num_pages == 1 || (latent_page_stride > 0 && rope_page_stride > 0),
             "decode_paged: page strides must be positive");
-  if (selected_positions || page_size % 16 != 0) {
+  if (selected_positions || page_size % 8 != 0) {
     const int64_t lp = latent_page_stride / latent_row_stride, rp = rope_page_stride / rope_row_stride;
     if (latent_page_stride % latent_row_stride != 0 || rope_page_stride % rope_row_stride != 0 ||
         lp * (num_pages - 1) + page_size >= (1LL << 31) || rp * (num_pages - 1) + page_size >= (1LL << 31))
-      return fail(MLA_ERR_UNSUPPORTED, "decode_paged: selections and page sizes that are no multiple of 16 need page "
+      return fail(MLA_ERR_UNSUPPORTED, "decode_paged: selections and page sizes that are no multiple of 8 need page "
                                        "strides of whole rows and fewer than 2^31 rows");
+    return cuda_status(launch_tc_decode(g, out_dtype, workspace, workspace_bytes, (cudaStream_t)stream),
+                       "decode_paged (rows) launch");
   }
-  return cuda_status(launch_tc_decode(g, out_dtype, workspace, workspace_bytes, (cudaStream_t)stream),
+  return cuda_status(launch_tc_paged(g, out_dtype, workspace, workspace_bytes, (cudaStream_t)stream),
                      "decode_paged (tensor core) launch");
 }
 

@@ -82,6 +82,11 @@ size_t tc_decode_workspace(int32_t n_q);
 cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* workspace,
                              size_t workspace_bytes, cudaStream_t stream, const DecodeTail* tail = nullptr);
 
+// The same over a paged cache whose pages are a multiple of 8 rows (no selection); launch_tc_decode
+// serves the others, row by row.
+cudaError_t launch_tc_paged(const DecodeGeometry& g, int out_dtype, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream);
+
 struct AbsorbParams {
   const void* q_nope;
   int64_t q_row_stride, q_head_stride;

@@ -43,17 +43,16 @@
 #include <math_constants.h>
 
 #include "mla_internal.h"
-#include "paged.cuh"
 #include "q8_tiles.cuh"
 #include "tc_common.cuh"
 #include "tc_host.h"
+#include "tc_split.cuh"
 
 namespace mla {
 namespace {
 
 using namespace tc;
 
-constexpr int BN = 64;                    // keys per tile
 constexpr int STAGES = 4;
 // A stage holds one tile of this CTA's features: four [64 keys x 64 latent
 // dims] boxes (128-byte rows, 128-byte swizzle) and its 32 rope dims
@@ -63,7 +62,6 @@ constexpr int ROPE_BYTES = BN * 64;
 constexpr int STAGE_BYTES = 4 * CHUNK_BYTES + ROPE_BYTES;
 constexpr int STAGE_TX = STAGE_BYTES;     // bytes one tile's loads deliver into a stage
 constexpr int XH_BYTES = 128 * BN * 2;    // fp16 partial scores of one tile (one send / receive buffer)
-constexpr int HEADS = 128, RANK = 512, DV = 256;  // DV: latent dims per CTA
 // producer, score MMA, 4 softmax, 4 exchange and P.V MMA warps; the kernel
 // instance for TMA row gathers of selected positions adds three warps that
 // share each tile's gathers with the producer (its own instance: compiled for
@@ -93,8 +91,6 @@ using DecodeFetch = Q8Fetch<16, 32 * kConvertWarps>;
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 4 * XH_BYTES;
 constexpr int SMEM_BYTES_Q8 = STAGES * STAGE_BYTES + 3 * XH_BYTES + 2 * DecodeFetch::kSlotBytes;
 constexpr uint32_t TM_O = 0, TM_Q = 256, TM_S = 400, TM_P = 464;  // TMEM columns (Q: 128 + 16)
-constexpr long long kWaitLimit = 1LL << 32;  // clock cycles (~2 s)
-constexpr float kRescaleThreshold = 8.0f;    // log2 units
 // The 8-bit instance's P is fp16, and p reaches 2^kRescaleThreshold: p is held
 // 2^kRaiseF16 times larger, up to 2^15, so that the keys lighter than the
 // reference by up to 2^21 keep all of fp16's bits (2^-11); below, p rounds to
@@ -103,20 +99,6 @@ constexpr float kRescaleThreshold = 8.0f;    // log2 units
 // same factor, and m less kRaiseF16 stands for it in the lse and the partials.
 constexpr float kRaiseF16 = 7.0f;
 static_assert(kRescaleThreshold + kRaiseF16 < 16.0f, "p in the fp16 range");
-// A group's tile range is at least this long: each split writes a 256 KB f32
-// partial, worth it only against a few 72 KB tiles of cache read.
-constexpr int kMinTilesPerGroup = 4;
-// Each work unit with tiles is charged this many tiles' worth of time for
-// its start: a segment boundary drains the pair's pipeline (the next query
-// enters TMEM only once the previous segment's last scores are read, then
-// its first scores and exchange run before the softmax resumes), which costs
-// several tiles of streaming.  The charge sits in the split plan ahead of the
-// unit's tiles, so a group whose range holds more unit starts gets fewer
-// tiles.  It applies when the groups stream at least kChargeMinSpan tiles
-// each: with a few tiles per group (a short or selected-position batch) every
-// group pays one start anyway, and a charge would only idle groups.
-constexpr int kUnitStartCharge = 10;
-constexpr int kChargeMinSpan = 32;
 // Tiles of the current row pulled into L2 ahead of their load (the decode
 // kernel's template parameter): farther for a lockstep group (the group's
 // pairs all read each tile, three of them from L2), nearer for a single row,
@@ -124,172 +106,6 @@ constexpr int kChargeMinSpan = 32;
 // compile-time distance: with a run-time one the lockstep verify decode ran
 // 3 % slower.
 constexpr int kPrefetchAheadGroup = 8, kPrefetchAheadRow = 3;
-constexpr int kQueryPrefetchTiles = 4;   // the next segment's query is pulled into L2 this many tiles before
-// Up to this many query rows, every CTA plans the split itself in its prologue
-// (no planner launch); larger batches use the planner kernel.
-constexpr int kMaxRowsInKernelPlan = 128;
-
-struct TcDecodeArgs {
-  const __nv_bfloat16* q;
-  int64_t q_row_stride, q_head_stride;
-  const __nv_bfloat16* latent;
-  int64_t latent_row_stride, latent_batch_stride;
-  const __nv_bfloat16* rope;
-  int64_t rope_row_stride, rope_batch_stride;
-  const int32_t* kv_start;
-  const int32_t* kv_len;
-  int32_t s_q, n_q;
-  int32_t heads;       // 64 or 128; rows h >= heads of the MMA's M side are zero padding
-  const int32_t* sel;
-  const int32_t* sel_count;
-  int32_t k_max;
-  float scale_log2;
-  void* ctx;
-  int64_t ctx_row_stride, ctx_head_stride;
-  int32_t out_f32;
-  float* lse;
-  int32_t* status;
-  int32_t* prefix;     // [n_units + 2] the split plan: prefix over work units, then the start charge
-  int32_t* keys;       // [n_q] visible entries per query row (planner)
-  uint4* ws_o;         // [slots][RANK/8][H] partial context, 8 fp16 dims per entry (O / l of the piece)
-  float* ws_ml;        // [slots][2][H] partial (m, l), log2 domain
-  int32_t num_clusters;
-  int32_t width;       // query rows per work unit = clusters per group
-  int32_t n_units;     // n_q / width
-  int32_t min_tiles;   // smallest tile range given to a group
-  int32_t batch_in_map;  // 1: use batch coordinate b in the tensor maps
-  int32_t gather_tma;    // 1: selected rows come by TMA gather4 (else cp.async)
-  int32_t lat_rows_per_batch, rope_rows_per_batch;  // batch stride in rows (gather maps)
-  int32_t plan_in_kernel;  // 1: n_q <= kMaxRowsInKernelPlan, each CTA plans (CTA 0 also stores the plan)
-  // 1 inside a fused step: the launch before the decode kernel is the absorb
-  // kernel, which writes only the query and lets its dependants start only
-  // after its own wait, so every other input is complete when this grid starts.
-  int32_t early_inputs;
-  // 8-bit cache (null codes: `latent`); strides in bytes
-  const uint8_t* codes;
-  int64_t codes_row_stride, codes_batch_stride;
-  const uint8_t* scales;
-  int64_t scales_batch_stride;
-  int32_t block_shift;
-  int64_t t_max;
-  // Paged cache (null table: windows): a row's keys by pages of page_size rows, read in boxes of
-  // box_rows rows, or row by row (lat_rows_per_batch, rope_rows_per_batch: between pages).
-  const int32_t* table;
-  int64_t table_stride;
-  int32_t page_size, num_pages, box_rows;
-  const int32_t* counts;
-  const uint64_t* tree;
-  int32_t tree_words;
-};
-
-// ------------------------------------------------------------------ helpers
-
-__device__ __forceinline__ const uint64_t* tree_of(const TcDecodeArgs& a, int n) {
-  return a.tree ? a.tree + (int64_t)n * a.tree_words : nullptr;
-}
-
-// The first of the new tokens' keys of a paged row.
-__device__ __forceinline__ int paged_first(const TcDecodeArgs& a, int n) {
-  const int b = n / a.s_q;
-  return a.kv_len[b] - paged_count(a.counts, b, a.s_q);
-}
-
-__device__ __forceinline__ int row_limit(const TcDecodeArgs& a, int n) {
-  const int b = n / a.s_q, i = n % a.s_q;
-  const int len = a.kv_len[b];
-  if (a.table) {
-    const int count = paged_count(a.counts, b, a.s_q);
-    return len < 0 || len > a.t_max || count < 0 ? 0 : paged_limit(len, count, i, tree_of(a, n), a.tree_words);
-  }
-  int lim = len - a.s_q + i + 1;
-  lim = lim < 0 ? 0 : (lim > len ? len : lim);
-  return lim;
-}
-
-// Work units are query rows, or -- for a dense multi-token verify -- whole
-// batch rows whose `width` = s_q tokens are served by a group of `width`
-// clusters in lockstep (member i takes token i), so the tokens of a batch row
-// read each cache tile at the same time and three of four reads hit L2.
-// The units' tiles form one flattened sequence cut into equal ranges, one per
-// group (at least `min_tiles` each, so a short sequence uses fewer groups).
-// In that sequence each unit with tiles occupies charge + tiles positions,
-// its tiles at the end: prefix[0..n_units] holds these extents' exclusive
-// prefix and prefix[n_units + 1] the charge, so unit u's tile j sits at
-// position prefix[u] + charge + j.
-__device__ __forceinline__ int group_span(const TcDecodeArgs& a, int total) {
-  const int ngroups = a.num_clusters / a.width;
-  const int per = (total + ngroups - 1) / ngroups;
-  return per > a.min_tiles ? per : a.min_tiles;
-}
-
-// The start charge of a plan whose units hold `raw` tiles in all.
-__device__ __forceinline__ int unit_start_charge(const TcDecodeArgs& a, int raw) {
-  const int ngroups = a.num_clusters / a.width;
-  return (raw + ngroups - 1) / ngroups >= kChargeMinSpan ? kUnitStartCharge : 0;
-}
-
-struct WorkIter {
-  const int32_t* prefix;
-  int n, t, t_begin, t_end, charge;
-  __device__ void init(const TcDecodeArgs& a, const int32_t* unit_prefix, int group) {
-    prefix = unit_prefix;
-    charge = prefix[a.n_units + 1];
-    const int total = prefix[a.n_units];
-    const int per = group_span(a, total);
-    const int ngroups = a.num_clusters / a.width;
-    const long long b0 = group < ngroups ? (long long)group * per : total;
-    t_begin = (int)min((long long)total, b0);
-    t_end = (int)min((long long)total, (long long)t_begin + per);
-    // first unit with prefix[n+1] > t_begin
-    int lo = 0, hi = a.n_units - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (prefix[mid + 1] > t_begin) hi = mid; else lo = mid + 1;
-    }
-    n = lo;
-    t = t_begin;
-  }
-  // Next segment: unit u, unit-local tiles [t0, t1); `whole` if all of the
-  // unit's tiles lie inside this group's range.  A unit whose start charge
-  // alone falls in the range is no segment.
-  __device__ bool next(int& u, int& t0, int& t1, bool& whole) {
-    while (t < t_end) {
-      while (prefix[n + 1] <= t) ++n;
-      const int rs = prefix[n] + charge, re = prefix[n + 1];   // the unit's tiles
-      const int s = max(t, rs), e = min(t_end, re);
-      t = e;
-      if (s >= e) continue;
-      u = n;
-      t0 = s - rs;
-      t1 = e - rs;
-      whole = rs >= t_begin && re <= t_end;
-      return true;
-    }
-    return false;
-  }
-};
-
-// The groups whose ranges hold unit u's tiles: [first, last] (a unit with
-// tiles; `charge` = prefix[n_units + 1]).
-__device__ __forceinline__ int first_group_of(const int32_t* prefix, int u, int per, int charge) {
-  return (prefix[u] + charge) / per;
-}
-__device__ __forceinline__ int last_group_of(const int32_t* prefix, int u, int per) {
-  return (prefix[u + 1] - 1) / per;
-}
-
-// A member's share of a unit segment: its query row n and the segment's tiles
-// clipped to that row's own tiles (a verify token sees a shorter prefix than
-// the last token).  False if nothing is left.
-__device__ __forceinline__ bool member_segment(const TcDecodeArgs& a, const int32_t* keys, int u, int member,
-                                               int& n, int& t0, int& t1) {
-  n = u * a.width + member;
-  if (n >= a.n_q) return false;   // the last unit may have fewer rows
-  const int tiles = (keys[n] + BN - 1) / BN;
-  if (t1 > tiles) t1 = tiles;
-  return t0 < t1;
-}
-
 // TMA row gather of key group g (keys 4g..4g+3) of tile t into a stage: one
 // gather4 per 64-dim latent chunk and one for this CTA's 32 rope dims.
 // Entries past the count or out of range load the window's first row
@@ -360,96 +176,6 @@ __device__ __forceinline__ void gather_paged_group(const TcDecodeArgs& a, const 
 }
 
 // ------------------------------------------------------------------ planner
-// Per query row the number of visible entries; the planner (or the decode
-// prologue) turns them into tiles and the exclusive prefix of tiles over work
-// units.  Bad selection counts give 0 and are flagged where `flag` is set.
-__device__ __forceinline__ int row_keys(const TcDecodeArgs& a, int n, bool flag) {
-  int keys = row_limit(a, n);
-  if (a.table) {
-    const int b = n / a.s_q, len = a.kv_len[b];
-    if (flag && a.status && (len < 0 || len > a.t_max || paged_count(a.counts, b, a.s_q) < 0))
-      atomicOr(a.status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
-    if (keys == 0) return 0;   // the selection of a token that sees nothing is not read
-  }
-  if (a.codes) {
-    // the 8-bit cache is read by plain loads: a window outside the buffer, or
-    // one that does not start on a whole block, is no window
-    const int b = n / a.s_q, start = a.kv_start ? a.kv_start[b] : 0, len = a.kv_len[b];
-    const bool fits = len >= 0 && start >= 0 && (int64_t)start + len <= a.t_max;
-    if (!fits || (start & ((1 << a.block_shift) - 1)) != 0) {
-      if (flag && a.status) atomicOr(a.status, fits ? MLA_DEVICE_BAD_BLOCK_START : MLA_DEVICE_INDEX_OUT_OF_RANGE);
-      return 0;
-    }
-  }
-  if (a.sel) {
-    const int c = a.sel_count[n];
-    if (c != -1) {
-      if (c <= 0 || c > a.k_max) {
-        keys = 0;
-        if (flag && a.status) atomicOr(a.status, MLA_DEVICE_BAD_SELECTION_COUNT);
-      } else {
-        keys = c;
-      }
-    }
-  }
-  return keys;
-}
-
-// The split plan inside a kernel (n_q <= kMaxRowsInKernelPlan; called by every
-// thread of the block, blockDim >= n_q): visible entries per query row, then per
-// unit its tiles (the longest of its `width` rows) and their exclusive prefix,
-// scanned by warp 0 (four units per lane, in unit order).
-// With start_s / limit_s, also each row's first cache row (of a paged row: the
-// first of its new tokens' keys) and window limit.
-__device__ __forceinline__ void plan_rows(const TcDecodeArgs& a, int32_t* keys_s, int32_t* prefix_s, bool flag,
-                                          int32_t* start_s = nullptr, int32_t* limit_s = nullptr) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x < a.n_q) {
-    const int n = threadIdx.x;
-    keys_s[n] = row_keys(a, n, flag);
-    if (start_s) {
-      start_s[n] = a.table ? paged_first(a, n) : a.kv_start ? a.kv_start[n / a.s_q] : 0;
-      limit_s[n] = row_limit(a, n);
-    }
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int tl[kMaxRowsInKernelPlan / 32];
-    int raw = 0;
-#pragma unroll
-    for (int j = 0; j < kMaxRowsInKernelPlan / 32; ++j) {
-      const int u = 32 * j + lane;
-      int tiles = 0;
-      if (u < a.n_units)
-        for (int i = 0; i < a.width && u * a.width + i < a.n_q; ++i)
-          tiles = max(tiles, (keys_s[u * a.width + i] + BN - 1) / BN);
-      tl[j] = tiles;
-      raw += tiles;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) raw += __shfl_xor_sync(0xffffffffu, raw, o);
-    const int charge = unit_start_charge(a, raw);
-    int carry = 0;
-#pragma unroll
-    for (int j = 0; j < kMaxRowsInKernelPlan / 32; ++j) {
-      const int u = 32 * j + lane;
-      const int ext = tl[j] > 0 ? tl[j] + charge : 0;   // the unit's extent in the plan
-      int v = ext;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += x;
-      }
-      if (u < a.n_units) prefix_s[u] = carry + v - ext;
-      carry += __shfl_sync(0xffffffffu, v, 31);
-    }
-    if (lane == 0) {
-      prefix_s[a.n_units] = carry;
-      prefix_s[a.n_units + 1] = charge;
-    }
-  }
-  __syncthreads();
-}
 
 __global__ void __launch_bounds__(1024) tc_plan_kernel(const __grid_constant__ TcDecodeArgs a) {
   pdl_wait();
@@ -535,11 +261,12 @@ __global__ void __launch_bounds__(1024) tc_plan_kernel(const __grid_constant__ T
 // takes 21 instructions for 16 codes where bf16, which the hardware does not
 // convert to, takes 51: the converting warps share the issue slots with the
 // softmax (ragged decode 174 -> 165 us, verify 628 -> 554 us).
-// kPaged: the keys come from pages (boxes of a page's rows, or in the instance
-// with the extra gather warps row by row), and a token of a tree sees some keys
-// of its last tiles only.  Rows of a tile that its token does not see are
-// cleared before the scores: a probability of 0 must not meet what another
-// token, or nobody, left there.
+// kPaged: the instance with the extra gather warps over pages, row by row
+// (tc_paged.cu reads whole pieces of pages): selections, and page sizes that
+// such pieces do not fit.  A token of a tree sees some keys of its last tiles
+// only; rows of a tile that its token does not see are cleared before the
+// scores: a probability of 0 must not meet what another token, or nobody, left
+// there.
 template <int kPrefetchAhead, int kThreads, bool kLateP, bool kQ8 = false, bool kPaged = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_decode_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_constant__ CUtensorMap rope_map,
@@ -577,8 +304,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int dim_base = 256 * (int)rank;     // first latent dim of this CTA
   const int cluster = blockIdx.x >> 1;
   const int group = cluster / a.width, member = cluster % a.width;
-  constexpr bool kPagedGather = kPaged && kThreads > THREADS;
-  const bool gather = kPaged ? kPagedGather : a.sel != nullptr;
+  static_assert(!kPaged || kThreads == THREADS_GATHER, "pages are read row by row");
+  const bool gather = kPaged || a.sel != nullptr;
 
   if (threadIdx.x == 0) {
     if (!kQ8 || !gather) tma_prefetch_desc(&rope_map);
@@ -659,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
       const int keys = keys_p[n];
       const uint64_t* mask = kPaged ? tree_of(a, n) : nullptr;
-      const int first = !kPaged || !mask ? keys : a.plan_in_kernel ? row_start_s[n] : paged_first(a, n);
+      const int first = !kPaged || !mask ? keys : a.plan_in_kernel ? row_start_s[n] : paged_first(a, n / a.s_q);
       if (!mbar_wait_warp(&q_full, seg & 1u, kWaitLimit)) { fail(); break; }
       for (int t = t0; t < t1; ++t) {
         uint64_t seen = ~0ull;
@@ -677,7 +404,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (!kPaged && !kQ8 && !gather && t == (keys - 1) / BN && (keys % BN) != 0) {
+        if (!kQ8 && !gather && t == (keys - 1) / BN && (keys % BN) != 0) {
           // Tail tile: clear the rows past the window so that P = 0 never meets
           // a non-finite value left in the caller's buffer.
           const int valid = keys % BN;
@@ -690,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (!kPaged && !kQ8 && gather && !a.gather_tma) fence_proxy_async_smem();
+        if (!kQ8 && gather && !a.gather_tma) fence_proxy_async_smem();
         if (tile > 0 && !mbar_wait_warp(&s_free, (tile - 1) & 1u, kWaitLimit)) { fail(); break; }
         tc_fence_after();
         // 16 latent K-steps, then this CTA's two rope K-steps.  Descriptors
@@ -912,33 +639,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int zb = a.batch_in_map ? b : 0;
       const int32_t* list = (gather && (!kPaged || a.sel) && a.sel_count[n] != -1) ? a.sel + (int64_t)n * a.k_max : nullptr;
       const int32_t* table = kPaged ? a.table + b * a.table_stride : nullptr;
-      // Pages: a tile is boxes of a.box_rows rows (a divisor of 64 and of the page size), one per lane.
-      const int boxes = kPaged ? BN / a.box_rows : 0;
-      auto box_at = [&](int t, int& page, int& row) {   // this lane's box of tile t; page -1: no key in it
-        const int key = t * BN + lane * a.box_rows, at = key / a.page_size;
-        page = -1;
-        row = key - at * a.page_size;
-        if (lane < boxes && key < keys) {
-          page = __ldg(table + at);
-          if (page < 0 || page >= a.num_pages) {   // flagged, and read as zeros: no such page in the map
-            page = a.num_pages;
-            if (a.status && rank == 0) atomicOr(a.status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
-          }
-        }
-      };
-      auto prefetch_box = [&](int t) {
-        int page, row;
-        box_at(t, page, row);
-        if (page < 0 || page >= a.num_pages) return;
-        for (int c = 0; c < 4; ++c) tma_prefetch_l2_3d(&lat_map, dim_base + 64 * c, row, page);
-        tma_prefetch_l2_3d(&rope_map, 32 * (int)rank, row, page);
-      };
-      int page = -1, row = 0;
-      if (kPaged && !gather) {
-        box_at(t0, page, row);
-        for (int t = t0 + STAGES; t < t0 + kPrefetchAhead && t < t1; ++t) prefetch_box(t);
-      }
-      if (!kPaged && !gather && lane == 0) {
+      if (!gather && lane == 0) {
         // the segment's first tiles that the loop's look-ahead will not cover
         for (int t = t0 + STAGES; t < t0 + kPrefetchAhead && t < t1; ++t) {
           for (int c = 0; c < 4; ++c) tma_prefetch_l2_3d(&lat_map, dim_base + 64 * c, start + t * BN, zb);
@@ -947,21 +648,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       for (int t = t0; t < t1 && !aborted(); ++t) {
         if (fills++ >= STAGES && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
-        if (kPaged && !gather) {
-          const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
-          if (lane == 0) mbar_arrive_expect_tx(&full_bar[stage], __popc(there) * a.box_rows * (STAGE_BYTES / BN));
-          __syncwarp();
-          if (page >= 0) {
-            uint8_t* dst = stages + stage * STAGE_BYTES + lane * a.box_rows * 128;
-            for (int c = 0; c < 4; ++c)
-              tma_load_3d(dst + c * CHUNK_BYTES, &lat_map, &full_bar[stage], dim_base + 64 * c, row, page);
-            tma_load_3d(dst + 4 * CHUNK_BYTES - lane * a.box_rows * 64, &rope_map, &full_bar[stage], 32 * (int)rank, row,
-                        page);
-          }
-          if (t + 1 < t1) box_at(t + 1, page, row);
-          if (t + kPrefetchAhead < t1) prefetch_box(t + kPrefetchAhead);
-          __syncwarp();
-        } else if (!gather) {
+        if (!gather) {
           if (lane == 0) {
             mbar_arrive_expect_tx(&full_bar[stage], STAGE_TX);
             uint8_t* dst = stages + stage * STAGE_BYTES;
@@ -1299,7 +986,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int limit = a.plan_in_kernel ? row_limit_s[n] : row_limit(a, n);
       const int32_t* list = (gather && (!kPaged || a.sel) && a.sel_count[n] != -1) ? a.sel + (int64_t)n * a.k_max : nullptr;
       const uint64_t* mask = kPaged ? tree_of(a, n) : nullptr;
-      const int first = !kPaged || !mask ? keys : a.plan_in_kernel ? row_start_s[n] : paged_first(a, n);
+      const int first = !kPaged || !mask ? keys : a.plan_in_kernel ? row_start_s[n] : paged_first(a, n / a.s_q);
       float m_used = -CUDART_INF_F, l = 0.f;
       constexpr float kRaise = kQ8 ? kRaiseF16 : 0.f;   // l is 2^kRaise times the sum relative to m_used
       bool first_tile = true;
@@ -1622,8 +1309,17 @@ __global__ void __launch_bounds__(128) tc_combine_kernel(const __grid_constant__
     c1 = last_group_of(prefix, u, per);
   }
   pdl_wait();
-  if (h >= a.heads) return;
-  const int64_t orow = (int64_t)n * a.ctx_row_stride + (int64_t)h * a.ctx_head_stride + d0;
+  // the token and head of MMA row h (two tokens of 64 heads, or padding from a.heads on)
+  int64_t token = n;
+  int head = h;
+  if (a.tokens == 2) {
+    const int i = 2 * (n % a.s_q) + (h >> 6);
+    if (i >= a.tok_q) return;
+    token = (int64_t)(n / a.s_q) * a.tok_q + i;
+    head = h & 63;
+  }
+  if (head >= a.heads) return;
+  const int64_t orow = token * a.ctx_row_stride + (int64_t)head * a.ctx_head_stride + d0;
   float acc[CDIMS];
 #pragma unroll
   for (int j = 0; j < CDIMS; ++j) acc[j] = 0.f;
@@ -1687,7 +1383,7 @@ __global__ void __launch_bounds__(128) tc_combine_kernel(const __grid_constant__
                      pack_bf16x2(acc[6], acc[7]));
     }
     if (blockIdx.y == 0 && a.lse)
-      a.lse[(int64_t)n * a.heads + h] = L != 0.f ? (M + log2f(L)) * 0.69314718055994531f : -CUDART_INF_F;
+      a.lse[token * a.heads + head] = L != 0.f ? (M + log2f(L)) * 0.69314718055994531f : -CUDART_INF_F;
   }
 }
 
@@ -1984,14 +1680,37 @@ size_t tc_decode_workspace(int32_t n_q) {
          align256(slots * HEADS * RANK * 2) + align256(slots * HEADS * 2 * 4);
 }
 
+void tc::lay_out_workspace(TcDecodeArgs& a, void* workspace) {
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  size_t off = 0;
+  a.prefix = reinterpret_cast<int32_t*>(ws + off);
+  off += align256((size_t)(a.n_q + 2) * 4);
+  a.keys = reinterpret_cast<int32_t*>(ws + off);
+  off += align256((size_t)a.n_q * 4);
+  const size_t slots = (size_t)a.n_q + tc_decode_clusters();
+  a.ws_o = reinterpret_cast<uint4*>(ws + off);
+  off += align256(slots * HEADS * RANK * 2);
+  a.ws_ml = reinterpret_cast<float*>(ws + off);
+}
+
+cudaError_t tc::launch_split_plan(const TcDecodeArgs& a, cudaStream_t stream) {
+  return launch_pdl(tc_plan_kernel, dim3(1), dim3(1024), 0, stream, a);
+}
+
+cudaError_t tc::launch_split_combine(const TcDecodeArgs& a, cudaStream_t stream) {
+  // batch 16 (128 registers, 4 CTAs per SM) while the grid fits one wave
+  // at that occupancy, else 4
+  auto* const combine = a.n_q <= kCombineWideRows ? tc_combine_kernel<16> : tc_combine_kernel<4>;
+  return launch_pdl(combine, dim3(a.n_q, RANK / CDIMS), dim3(HEADS), 0, stream, a);
+}
+
 cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* workspace, size_t workspace_bytes,
                              cudaStream_t stream, const DecodeTail* tail) {
   const int n_q = g.batch * g.s_q;
   const int nclusters = tc_decode_clusters();
   if (workspace_bytes < tc_decode_workspace(n_q)) return cudaErrorInvalidValue;
   if (g.heads != 64 && g.heads != HEADS) return cudaErrorInvalidValue;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  TcDecodeArgs a;
+  TcDecodeArgs a = {};
   a.q = static_cast<const __nv_bfloat16*>(g.q);
   a.q_row_stride = g.q_row_stride;
   a.q_head_stride = g.q_head_stride;
@@ -2016,22 +1735,14 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
   a.out_f32 = out_dtype == MLA_DTYPE_F32;
   a.lse = g.lse_out;
   a.status = g.device_status;
-  size_t off = 0;
-  a.prefix = reinterpret_cast<int32_t*>(ws + off);
-  off += align256((size_t)(n_q + 2) * 4);
-  a.keys = reinterpret_cast<int32_t*>(ws + off);
-  off += align256((size_t)n_q * 4);
-  const size_t slots = (size_t)n_q + nclusters;
-  a.ws_o = reinterpret_cast<uint4*>(ws + off);
-  off += align256(slots * HEADS * RANK * 2);
-  a.ws_ml = reinterpret_cast<float*>(ws + off);
+  lay_out_workspace(a, workspace);
   a.num_clusters = nclusters;
   // A dense multi-token verify serves each batch row's tokens with a group of
   // clusters in lockstep; everything else is one query row per unit.
   a.width = (g.sel == nullptr && g.s_q > 1 && g.s_q <= 8) ? g.s_q : 1;
-  const bool paged = g.table != nullptr;
-  if (paged && g.sel == nullptr && g.s_q > 8) a.width = 8;
-  a.n_units = (n_q + a.width - 1) / a.width;
+  const bool paged = g.table != nullptr;   // (row by row: tokens apart)
+  if (paged) a.width = 1;
+  a.n_units = n_q / a.width;
   a.min_tiles = kMinTilesPerGroup;
   const bool q8 = g.codes != nullptr;   // codes are copied row by row: only rope keys are mapped
   a.batch_in_map = ((g.latent_batch_stride != 0 && !q8) || g.rope_batch_stride != 0) ? 1 : 0;
@@ -2044,6 +1755,8 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
   a.scales_batch_stride = g.scales_batch_stride;
   a.block_shift = g.block_shift;
   a.t_max = g.t_max;
+  a.tokens = 1;
+  a.tok_q = g.s_q;
   a.gather_tma = 0;
   a.lat_rows_per_batch = a.rope_rows_per_batch = 0;
   a.table = g.table;
@@ -2053,28 +1766,11 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
   a.counts = g.counts;
   a.tree = g.tree;
   a.tree_words = g.tree_words;
-  // the largest box that divides a tile and a page
-  a.box_rows = BN;
-  while (paged && g.page_size % a.box_rows != 0) a.box_rows >>= 1;
-  // Boxes of 16 rows and more; smaller ones take as long to issue as single rows.
-  const bool paged_rows = paged && (g.sel != nullptr || a.box_rows < 16);
 
   // Tensor maps over [B_buf, t_max, dims] (the batch axis has extent 1 for a
   // packed-flat cache whose batch stride is 0).
   const uint64_t bmap = a.batch_in_map ? (uint64_t)g.batch : 1;
   CUtensorMap lat_map = {}, rope_map = {};
-  if (paged && !paged_rows) {
-    // [pages, page rows, dims]
-    const uint64_t ldims[3] = {(uint64_t)g.rank, (uint64_t)g.page_size, (uint64_t)g.num_pages};
-    const uint64_t rdims[3] = {(uint64_t)g.rope_dim, (uint64_t)g.page_size, (uint64_t)g.num_pages};
-    // (one page: its stride has no meaning)
-    const uint64_t lstrides[2] = {(uint64_t)g.latent_row_stride * 2, (uint64_t)(g.num_pages > 1 ? g.latent_page_stride : g.latent_row_stride * g.page_size) * 2};
-    const uint64_t rstrides[2] = {(uint64_t)g.rope_row_stride * 2, (uint64_t)(g.num_pages > 1 ? g.rope_page_stride : g.rope_row_stride * g.page_size) * 2};
-    const uint32_t lbox[3] = {64, (uint32_t)a.box_rows, 1}, rbox[3] = {32, (uint32_t)a.box_rows, 1};
-    if (!encode_tmap_bf16(&lat_map, g.latent, 3, ldims, lstrides, lbox) ||
-        !encode_tmap_bf16(&rope_map, g.rope, 3, rdims, rstrides, rbox, CU_TENSOR_MAP_SWIZZLE_64B))
-      return cudaErrorInvalidValue;
-  }
   if (!q8 && !paged) {
     const uint64_t dims[3] = {(uint64_t)g.rank, (uint64_t)g.t_max, bmap};
     const uint64_t bstride = a.batch_in_map ? (uint64_t)g.latent_batch_stride * 2
@@ -2108,7 +1804,7 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
         encode_tmap_bf16(&rope_rows_map, g.rope, 2, rd, rs, rbox, CU_TENSOR_MAP_SWIZZLE_64B))
       a.gather_tma = 1;
   }
-  if (paged_rows) {
+  if (paged) {   // the pool's rows
     a.lat_rows_per_batch = (int32_t)(g.latent_page_stride / g.latent_row_stride);
     a.rope_rows_per_batch = (int32_t)(g.rope_page_stride / g.rope_row_stride);
     const uint64_t ld[2] = {(uint64_t)g.rank, (uint64_t)(g.num_pages - 1) * a.lat_rows_per_batch + g.page_size};
@@ -2118,7 +1814,7 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
     if (!encode_tmap_bf16(&lat_rows_map, g.latent, 2, ld, ls, box) ||
         !encode_tmap_bf16(&rope_rows_map, g.rope, 2, rd, rs, rbox, CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorInvalidValue;
-    lat_map = lat_rows_map;   // (unused, but prefetched)
+    lat_map = lat_rows_map;   // (not loaded from, but prefetched)
     rope_map = rope_rows_map;
     a.gather_tma = 1;
   }
@@ -2127,9 +1823,7 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
   // instance with the extra gather warps)
   // (an 8-bit cache is served by one instance: announcing P late, as the
   // lockstep groups do, costs it 11 %)
-  auto* const decode_kernel = paged_rows ? tc_decode_kernel<kPrefetchAheadRow, THREADS_GATHER, false, false, true>
-                              : paged && lockstep ? tc_decode_kernel<kPrefetchAheadGroup, THREADS, true, false, true>
-                              : paged ? tc_decode_kernel<kPrefetchAheadRow, THREADS, false, false, true>
+  auto* const decode_kernel = paged ? tc_decode_kernel<kPrefetchAheadRow, THREADS_GATHER, false, false, true>
                               : q8 ? tc_decode_kernel<kPrefetchAheadRow, THREADS_Q8, false, true>
                               : a.gather_tma ? tc_decode_kernel<kPrefetchAheadRow, THREADS_GATHER, false>
                               : lockstep   ? tc_decode_kernel<kPrefetchAheadGroup, THREADS, true>
@@ -2150,17 +1844,14 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
   }
   cudaError_t e = cudaSuccess;
   if (!a.plan_in_kernel) {
-    e = launch_pdl(tc_plan_kernel, dim3(1), dim3(1024), 0, stream, a);
+    e = launch_split_plan(a, stream);
     if (e != cudaSuccess) return e;
   }
   e = launch_pdl(decode_kernel, dim3(2 * nclusters), dim3(q8 ? THREADS_Q8 : a.gather_tma ? THREADS_GATHER : THREADS), smem_bytes, stream,
                  lat_map, rope_map, lat_rows_map, rope_rows_map, a);
   if (e != cudaSuccess) return e;
   if (tail == nullptr) {
-    // batch 16 (128 registers, 4 CTAs per SM) while the grid fits one wave
-    // at that occupancy, else 4
-    auto* const combine = n_q <= kCombineWideRows ? tc_combine_kernel<16> : tc_combine_kernel<4>;
-    e = launch_pdl(combine, dim3(n_q, RANK / CDIMS), dim3(HEADS), 0, stream, a);
+    e = launch_split_combine(a, stream);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
   }

@@ -43,10 +43,10 @@ bool encode_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64
     set_error_detail("cuTensorMapEncodeTiled is not available from the driver");
     return false;
   }
-  cuuint64_t gdim[3];
-  cuuint64_t gstride[2];
-  cuuint32_t bdim[3];
-  cuuint32_t estride[3] = {1, 1, 1};
+  cuuint64_t gdim[5];
+  cuuint64_t gstride[4];
+  cuuint32_t bdim[5];
+  cuuint32_t estride[5] = {1, 1, 1, 1, 1};
   for (int i = 0; i < rank; ++i) {
     gdim[i] = dims[i];
     bdim[i] = box[i];

@@ -10,7 +10,7 @@
 
 namespace mla {
 
-// Encodes a bf16 tensor map of rank 2 or 3 with 128-byte swizzle (or the
+// Encodes a bf16 tensor map of rank 2 to 5 with 128-byte swizzle (or the
 // given swizzle).  dims[0] is the contiguous axis; strides_bytes[i] is the
 // byte stride of dims[i+1].  Returns false (and sets the error detail) on
 // failure.

@@ -1,0 +1,856 @@
+// Tensor-core attention over a paged latent||rope cache: one token, a row of
+// drafted tokens, a tree of them or a prompt chunk per batch row (bf16, 128 or
+// 64 heads, rank 512, rope 64, pages of a multiple of 8 rows).
+//
+// Like the window decode (tc_decode.cu), a cluster of two CTAs owns a stream of
+// (query row, 64-key tile) work: each CTA scores half of the 576 features of a
+// tile, the fp16 halves cross by st.async, and each CTA accumulates the context
+// over its 256 latent dims in TMEM.  What differs:
+//  * Pages.  A tile is 64 / box_rows boxes, each inside one page.  The pool is
+//    mapped as [pages][groups of 8 rows][8 chunks of 64 dims][8 rows][64 dims],
+//    so that one copy brings a box of all the CTA's dims: groups of 8 rows x 4
+//    chunks of 1024 bytes, 128-byte swizzle, which both MMAs read through their
+//    descriptors' strides (scores: 4096 bytes between groups of 8 keys; P.V:
+//    1024 between chunks of 64 dims).
+//  * Two groups of four softmax warps take the tiles in turn.  A tile's scores
+//    are summed and their maximum taken before the reference that the tile
+//    before left is known; the reference is handed on before the exponentials,
+//    so these phases of two tiles overlap.  Each group keeps its own sum, and
+//    the two are joined at the end of a segment, whose context they store half
+//    each.
+//  * kPair: two tokens of 64 heads share the MMA's 128 rows.
+//  * Masks.  A tile that a token sees in part has its scores masked; rows that no
+//    token of the query row sees are cleared before the scores (a probability
+//    of 0 must not meet what another token, or nobody, left there).  With two
+//    tokens, a key that only one of them sees may not be cleared: its elements
+//    that are not finite are replaced by 0 and the token that does see it gets
+//    NaN.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math_constants.h>
+#include <stdlib.h>
+
+#include "mla_internal.h"
+#include "tc_common.cuh"
+#include "tc_host.h"
+#include "tc_split.cuh"
+
+namespace mla {
+namespace {
+
+using namespace tc;
+
+constexpr int STAGES = 5;
+// A stage: 8 groups of 8 keys, each 4 chunks of [8 keys x 64 latent dims], then [64 keys x 32 rope dims] (64-byte swizzle).
+constexpr int GROUP_BYTES = 4 * 1024;
+constexpr int LATENT_BYTES = 8 * GROUP_BYTES;
+constexpr int STAGE_BYTES = LATENT_BYTES + BN * 64;
+constexpr int XH_BYTES = 128 * BN * 2;    // fp16 partial scores of one tile
+constexpr int QROPE_BYTES = 128 * 64;     // the query's 32 rope dims (64-byte rows, 64-byte swizzle)
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 2 * XH_BYTES + QROPE_BYTES;
+// TMEM columns: context, the query's latent dims, scores, probabilities, this CTA's half of the scores in fp16.
+constexpr uint32_t TM_O = 0, TM_Q = 256, TM_S = 384, TM_P = 448, TM_X = 480;
+// Warpgroups: two of softmax warps, the exchange, and the issuers (loads, score MMA, P.V MMA, L2 prefetch).
+constexpr int THREADS = 512;
+constexpr int kExchangeWarp = 8, kLoadWarp = 12, kScoreWarp = 13, kPvWarp = 14, kPrefetchWarp = 15;
+// Registers per thread of each warpgroup; their sum fits the launch's.
+constexpr int kRegsLaunch = 128;
+constexpr int kRegsSoftmax = 152, kRegsIssue = 72;
+static_assert(2 * kRegsSoftmax + kRegsLaunch + kRegsIssue <= 4 * kRegsLaunch, "more registers than the launch has");
+// Tiles pulled into L2 ahead of their load: farther for a lockstep group.
+constexpr int kPrefetchAheadGroup = 8, kPrefetchAheadRow = 3;
+
+__device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, uint64_t* bar, int x, int y, int z, int w, int v) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v)
+      : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_l2_5d(const void* tmap, int x, int y, int z, int w, int v) {
+  asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %3, %4, %5}];"
+               ::"l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v)
+               : "memory");
+}
+
+// bf16 pairs with infinities and NaN replaced by 0; `found` is set if there was one.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w, bool& found) {
+  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u, found = true;
+  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu, found = true;
+  return w;
+}
+
+template <int kPrefetchAhead, bool kPair>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    tc_paged_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_constant__ CUtensorMap rope_map,
+                    const __grid_constant__ TcDecodeArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if ((smem_u32(smem_raw) & 1023u) != 0) {   // the same in every CTA: nothing waits on anything yet
+    if (threadIdx.x == 0 && a.status) atomicOr(a.status, MLA_DEVICE_LAYOUT);
+    return;
+  }
+  uint8_t* stages = smem_raw;
+  // The peer's halves of the scores, [8][128 heads][16 B] in fp16, one buffer per softmax group.
+  uint8_t* xin = smem_raw + STAGES * STAGE_BYTES;
+  uint8_t* qrope_s = xin + 2 * XH_BYTES;
+
+  __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES];
+  __shared__ __align__(8) uint64_t s_full, s_free, p_full, q_full, o_free, mma_drain, pv_drain, seg_done;
+  __shared__ __align__(8) uint64_t x_full[2], x_free[2], xo_free;
+  __shared__ __align__(8) uint64_t ref_full[2][4];      // per softmax group and lane quarter: its reference is in ref_s
+  __shared__ __align__(8) uint64_t poison_full[4];      // kPair
+  __shared__ uint64_t poison_s[4];
+  __shared__ float ref_s[2][128], sum_s[2][128], sum_ref_s[2][128];
+  __shared__ uint32_t tmem_base_s;
+  __shared__ volatile int abort_s, loaded_s;   // loaded_s: tiles whose loads have been issued
+  __shared__ int32_t plan_keys_s[kMaxRowsInKernelPlan], plan_prefix_s[kMaxRowsInKernelPlan + 2];
+  __shared__ int32_t row_first_s[kMaxRowsInKernelPlan], limit_s[2 * kMaxRowsInKernelPlan];
+  auto aborted = [&]() -> bool { return __any_sync(0xffffffffu, abort_s != 0); };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const uint32_t peer = rank ^ 1u;
+  const int dim_base = 256 * (int)rank;     // first latent dim of this CTA
+  const int cluster = blockIdx.x >> 1;
+  const int group = cluster / a.width, member = cluster % a.width;
+  constexpr int kTokens = kPair ? 2 : 1;
+
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&lat_map);
+    tma_prefetch_desc(&rope_map);
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    mbar_init(&s_full, 1);
+    mbar_init(&s_free, 4);      // the exchange warps have read S
+    mbar_init(&p_full, 4);      // one arrival per softmax warp of the tile's group
+    mbar_init(&q_full, 4);      // the exchange warps have written this segment's query into TMEM
+    mbar_init(&o_free, 8);
+    mbar_init(&seg_done, 8);    // the softmax warps have published their sums
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&x_full[b], 4);   // our exchange warps have stored our half + the peer's bytes into xin[b]
+      mbar_init(&x_free[b], 4);   // the peer's softmax warps have read xin[b]
+      for (int q = 0; q < 4; ++q) mbar_init(&ref_full[b][q], 1);
+    }
+    for (int k = 0; k < 4; ++k) mbar_init(&poison_full[k], 1);
+    mbar_init(&xo_free, 4);     // our softmax warps have read our half
+    mbar_init(&mma_drain, 1);
+    mbar_init(&pv_drain, 1);
+    abort_s = 0;
+    loaded_s = 0;
+    fence_mbar_init();
+  }
+  if (warp == kScoreWarp) {
+    tmem_alloc(&tmem_base_s, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // peer barriers initialised before any remote arrive
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_s;
+  pdl_wait();
+
+  const int32_t* keys_p = a.keys;
+  const int32_t* prefix_p = a.prefix;
+  if (a.plan_in_kernel) {
+    plan_rows(a, plan_keys_s, plan_prefix_s, blockIdx.x == 0, row_first_s, limit_s);
+    keys_p = plan_keys_s;
+    prefix_p = plan_prefix_s;
+  }
+  WorkIter it;
+  it.init(a, prefix_p, group);
+
+  auto fail = [&]() {
+    abort_s = 1;
+    if (a.status) atomicOr(a.status, MLA_DEVICE_TIMEOUT);
+  };
+  // What token k of query row n sees: keys [0, limit), in a tree from `first` on by its mask.
+  struct Sight {
+    int limit, first;
+    const uint64_t* mask;
+    __device__ bool whole(int t) const { return (t + 1) * BN <= min(limit, first); }
+  };
+  // A token that sees nothing beside one that does is scored like that one (and its result dropped).
+  auto limit_of = [&](int n, int k) {
+    return a.plan_in_kernel ? limit_s[kTokens * n + k] : token_limit(a, n / a.s_q, (n % a.s_q) * kTokens + k);
+  };
+  auto sight_of = [&](int n, int k) {
+    Sight s;
+    s.limit = limit_of(n, k);
+    if (kPair && s.limit == 0) s.limit = limit_of(n, k ^= 1);
+    const int b = n / a.s_q, i = (n % a.s_q) * kTokens + k;
+    s.mask = i < a.tok_q ? tree_of(a, b * a.tok_q + i) : nullptr;
+    s.first = !s.mask ? s.limit : a.plan_in_kernel ? row_first_s[n] : paged_first(a, b);
+    return s;
+  };
+  auto seen_of = [&](const Sight& s, int t) {
+    return s.whole(t) ? ~0ull : paged_seen(t * BN, s.limit, s.first, s.mask, a.tree_words);
+  };
+
+  if (warp >= kLoadWarp) {
+    reg_dealloc<kRegsIssue>();
+    if (warp == kLoadWarp || warp == kPrefetchWarp) {
+      // ============================================================ loads, and L2 prefetch a few tiles ahead of them
+      const bool loads = warp == kLoadWarp;
+      int stage = 0;
+      uint32_t phase = 0;
+      int fills = 0;   // the ring's first STAGES fills need no free slot
+      const int boxes = BN / a.box_rows;   // 1, 2, 4 or 8 of a tile, one per lane
+      const int groups = a.box_rows >> 3;
+      int u, n, t0, t1;
+      bool whole;
+      while (!aborted() && it.next(u, t0, t1, whole)) {
+        if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
+        const int keys = keys_p[n];
+        const int32_t* table = a.table + (n / a.s_q) * a.table_stride;
+        // Lane l holds the page (-1: no key in the box) and first row there of box 32 * block + l, and of the
+        // block behind it.
+        int block = -2, page = -1, row = 0, page_next = -1, row_next = 0;
+        auto fetch = [&](int blk, int& pg, int& rw) {
+          const int key = (32 * blk + lane) * a.box_rows, at = key / a.page_size;
+          rw = key - at * a.page_size;
+          pg = key < keys ? __ldg(table + at) : -1;
+          if (key < keys && (pg < 0 || pg >= a.num_pages)) {   // flagged, and read as zeros: no such page in the map
+            pg = a.num_pages;
+            if (a.status && rank == 0) atomicOr(a.status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
+          }
+        };
+        auto box_of = [&](int t, int& pg, int& rw) {   // this lane's box of tile t
+          const int blk = (t * boxes) >> 5;
+          if (blk != block) {
+            if (blk == block + 1) page = page_next, row = row_next; else fetch(blk, page, row);
+            fetch(blk + 1, page_next, row_next);
+            block = blk;
+          }
+          const int from = (t * boxes + lane) & 31;
+          pg = __shfl_sync(0xffffffffu, page, from);
+          rw = __shfl_sync(0xffffffffu, row, from);
+          if (lane >= boxes) pg = -1;
+        };
+        auto prefetch_tile = [&](int t) {
+          int pg, rw;
+          box_of(t, pg, rw);
+          if (pg >= 0 && pg < a.num_pages) {
+            tma_prefetch_l2_5d(&lat_map, 0, 0, 4 * (int)rank, rw >> 3, pg);
+            tma_prefetch_l2_3d(&rope_map, 32 * (int)rank, rw, pg);
+          }
+          __syncwarp();
+        };
+        // the segment's first tiles that the loop's look-ahead will not cover
+        if (!loads)
+          for (int t = t0 + STAGES; t < t0 + kPrefetchAhead && t < t1; ++t) prefetch_tile(t);
+        for (int t = t0; t < t1 && !aborted(); ++t) {
+          if (loads) {
+            if (fills >= STAGES && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
+            int pg, rw;
+            box_of(t, pg, rw);
+            const uint32_t there = __ballot_sync(0xffffffffu, pg >= 0);
+            if (lane == 0) mbar_arrive_expect_tx(&full_bar[stage], __popc(there) * a.box_rows * (STAGE_BYTES / BN));
+            __syncwarp();
+            if (pg >= 0) {
+              uint8_t* dst = stages + stage * STAGE_BYTES;
+              tma_load_5d(dst + lane * groups * GROUP_BYTES, &lat_map, &full_bar[stage], 0, 0, 4 * (int)rank, rw >> 3, pg);
+              tma_load_3d(dst + LATENT_BYTES + lane * a.box_rows * 64, &rope_map, &full_bar[stage], 32 * (int)rank, rw, pg);
+            }
+            __syncwarp();
+            if (lane == 0) loaded_s = fills + 1;
+          } else {
+            // with the loads of tile t, or at once if those are farther already (a counter, not the stage's barrier: a
+            // late reader of a barrier's parity could miss a phase)
+            const long long begin = clock64();
+            while (loaded_s <= fills && !abort_s && clock64() - begin < kWaitLimit) __nanosleep(100);
+            __syncwarp();
+            if (t + kPrefetchAhead < t1) prefetch_tile(t + kPrefetchAhead);
+          }
+          ++fills;
+          if (++stage == STAGES) stage = 0, phase ^= 1u;
+        }
+      }
+      // Drain: every issued fill must land before this CTA may exit.
+      for (int k = fills > STAGES ? fills - STAGES : 0; loads && k < fills; ++k)
+        mbar_wait_warp(&full_bar[k % STAGES], (uint32_t)(k / STAGES) & 1u, kWaitLimit);
+    } else if (warp == kScoreWarp) {
+      // ============================================================ score MMA issuer
+      const uint32_t idesc_s = idesc_bf16_f32(128, BN, 0, 0);
+      int stage = 0;
+      uint32_t phase = 0, tile = 0, seg = 0;
+      int u, n, t0, t1;
+      bool whole;
+      while (!aborted() && it.next(u, t0, t1, whole)) {
+        if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
+        const Sight s0 = sight_of(n, 0), s1 = kPair ? sight_of(n, 1) : s0;
+        if (!mbar_wait_warp(&q_full, seg & 1u, kWaitLimit)) { fail(); break; }
+        for (int t = t0; t < t1; ++t) {
+          const uint64_t seen0 = seen_of(s0, t), seen1 = kPair ? seen_of(s1, t) : seen0;
+          if (!mbar_wait_warp(&full_bar[stage], phase, kWaitLimit)) { fail(); break; }
+          if ((seen0 & seen1) != ~0ull) {
+            const uint64_t any = seen0 | seen1, one = seen0 ^ seen1;
+            uint8_t* st = stages + stage * STAGE_BYTES;
+            uint64_t poison = 0;
+#pragma unroll 1
+            for (int i = lane; i < BN * 36; i += 32) {
+              const int r = i / 36, v = i - 36 * r;
+              uint4* at = reinterpret_cast<uint4*>(st + (v < 32 ? (r >> 3) * GROUP_BYTES + (v >> 3) * 1024 + (r & 7) * 128 + (v & 7) * 16
+                                                                : LATENT_BYTES + r * 64 + (v - 32) * 16));
+              if (!(any >> r & 1)) {
+                *at = make_uint4(0, 0, 0, 0);
+              } else if (kPair && (one >> r & 1)) {
+                uint4 w = *at;
+                bool found = false;
+                w = make_uint4(finite_pair(w.x, found), finite_pair(w.y, found), finite_pair(w.z, found), finite_pair(w.w, found));
+                if (found) *at = w, poison |= 1ull << r;
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (kPair && one != 0ull) {
+              const uint32_t lo = __reduce_or_sync(0xffffffffu, (uint32_t)poison);
+              const uint32_t hi = __reduce_or_sync(0xffffffffu, (uint32_t)(poison >> 32));
+              // (four slots: tile t + 4 gets here only after the softmax has read tile t's)
+              if (tile > 0 && !mbar_wait_warp(&s_free, (tile - 1) & 1u, kWaitLimit)) { fail(); break; }
+              if (lane == 0) {
+                poison_s[tile & 3] = (uint64_t)hi << 32 | lo;
+                mbar_arrive(&poison_full[tile & 3]);
+              }
+            }
+          }
+          if (tile > 0 && !mbar_wait_warp(&s_free, (tile - 1) & 1u, kWaitLimit)) { fail(); break; }
+          tc_fence_after();
+          // 16 latent K-steps, then this CTA's two rope K-steps
+          const uint64_t d0 = smem_desc(smem_u32(stages + stage * STAGE_BYTES), 16, GROUP_BYTES, kSwizzle128B);
+          const uint64_t d_rope = smem_desc(smem_u32(stages + stage * STAGE_BYTES + LATENT_BYTES), 16, 512, kSwizzle64B);
+          const uint64_t a_rope = smem_desc(smem_u32(qrope_s), 16, 512, kSwizzle64B);
+          if (elect_one()) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_ts(tmem + TM_S, tmem + TM_Q + c * 32 + k * 8, d0 + (uint64_t)((c * 1024 + k * 32) >> 4), idesc_s, (c | k) != 0);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              mma_ss(tmem + TM_S, a_rope + (uint64_t)((k * 32) >> 4), d_rope + (uint64_t)((k * 32) >> 4), idesc_s, 1u);
+            mma_commit(&s_full);
+          }
+          __syncwarp();
+          ++tile;
+          if (++stage == STAGES) stage = 0, phase ^= 1u;
+        }
+        if (aborted()) break;
+        ++seg;
+      }
+      // All score MMAs complete before TMEM is released.
+      if (lane == 0) mma_commit(&mma_drain);
+      __syncwarp();
+      mbar_wait_warp(&mma_drain, 0, kWaitLimit);
+    } else if (warp == kPvWarp) {
+      // ============================================================ P.V MMA issuer
+      const uint32_t idesc_pv = idesc_bf16_f32(128, DV, 0, 1);
+      int stage = 0;
+      uint32_t tile = 0, seg = 0;
+      int u, n, t0, t1;
+      bool whole;
+      while (!aborted() && it.next(u, t0, t1, whole)) {
+        if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
+        for (int t = t0; t < t1; ++t) {
+          const bool first = (t == t0);
+          // O is overwritten by a segment's first P.V: the previous segment's epilogue must have read it.
+          if (first && seg > 0 && !mbar_wait_warp(&o_free, (seg - 1) & 1u, kWaitLimit)) { fail(); break; }
+          if (!mbar_wait_warp(&p_full, tile & 1u, kWaitLimit)) { fail(); break; }
+          tc_fence_after();
+          const uint64_t d0 = smem_desc(smem_u32(stages + stage * STAGE_BYTES), 1024, GROUP_BYTES, kSwizzle128B);
+          const uint32_t acc0 = first ? 0u : 1u;
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < BN / 16; ++k)
+              mma_ts(tmem + TM_O, tmem + TM_P + k * 8, d0 + (uint64_t)((k * 2 * GROUP_BYTES) >> 4), idesc_pv, k == 0 ? acc0 : 1u);
+            // one commit: the stage barrier also tells the softmax warps that this P.V has completed
+            mma_commit(&empty_bar[stage]);
+          }
+          __syncwarp();
+          ++tile;
+          if (++stage == STAGES) stage = 0;
+        }
+        if (aborted()) break;
+        ++seg;
+      }
+      if (lane == 0) mma_commit(&pv_drain);
+      __syncwarp();
+      mbar_wait_warp(&pv_drain, 0, kWaitLimit);
+    }
+  } else if (warp >= kExchangeWarp) {
+    // ============================================================ exchange warps
+    const int quarter = warp & 3;
+    const int h = 32 * quarter + lane;     // MMA row
+    const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
+    const bool issuer = (h == 0);
+    const uint32_t xin_peer = mapa(smem_u32(xin), peer);
+    uint32_t x_full_peer[2];
+    x_full_peer[0] = mapa(smem_u32(&x_full[0]), peer);
+    x_full_peer[1] = mapa(smem_u32(&x_full[1]), peer);
+    // This MMA row's query of row n, or null (padding, or a token that the batch row does not have).
+    auto query_of = [&](int n) -> const __nv_bfloat16* {
+      const int b = n / a.s_q, i = (n % a.s_q) * kTokens + (kPair ? h >> 6 : 0), head = kPair ? h & 63 : h;
+      if (i >= a.tok_q || head >= a.heads) return nullptr;
+      return a.q + ((int64_t)b * a.tok_q + i) * a.q_row_stride + (int64_t)head * a.q_head_stride;
+    };
+    uint32_t tile = 0;
+    float half_max = 0.f;   // largest |half score| sent (checked against the fp16 exchange's range)
+    int u, n, t0, t1;
+    bool whole;
+    while (!aborted() && it.next(u, t0, t1, whole)) {
+      if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
+      {
+        // The query into TMEM: every score MMA of the previous segment has completed (its last scores were read
+        // here), while the softmax warps may still be finishing that segment.
+        const __nv_bfloat16* qrow = query_of(n);
+        uint4 qv[36];   // all 36 loads in flight at once: 256 latent dims, then the 32 rope dims
+        const uint4* qlat = reinterpret_cast<const uint4*>(qrow + dim_base);
+        const uint4* qrope = reinterpret_cast<const uint4*>(qrow + RANK + 32 * (int)rank);
+#pragma unroll
+        for (int v = 0; v < 32; ++v) qv[v] = qrow ? __ldg(qlat + v) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) qv[32 + v] = qrow ? __ldg(qrope + v) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[32];
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            r[4 * v] = qv[8 * c + v].x, r[4 * v + 1] = qv[8 * c + v].y, r[4 * v + 2] = qv[8 * c + v].z, r[4 * v + 3] = qv[8 * c + v].w;
+          tmem_st32(tmem + TM_Q + c * 32 + lane_off, r);
+        }
+        // the rope dims as a K-major tile in shared memory (piece v of row h at v ^ (h / 2 % 4))
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          *reinterpret_cast<uint4*>(qrope_s + h * 64 + ((v ^ ((h >> 1) & 3)) << 4)) = qv[32 + v];
+        fence_proxy_async_smem();
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full);
+      }
+      // A few tiles before this segment ends, the next segment's query row is pulled into L2.
+      const int t_pf = t1 - kQueryPrefetchTiles > t0 ? t1 - kQueryPrefetchTiles : t0;
+      for (int t = t0; t < t1; ++t) {
+        if (t == t_pf) {
+          WorkIter peek = it;
+          int un, nn, tn0, tn1;
+          bool wn;
+          while (peek.next(un, tn0, tn1, wn)) {
+            if (!member_segment(a, keys_p, un, member, nn, tn0, tn1)) continue;
+            if (const __nv_bfloat16* qnext = query_of(nn)) {
+#pragma unroll
+              for (int l = 0; l < 4; ++l) prefetch_l2(qnext + dim_base + 64 * l);
+              prefetch_l2(qnext + RANK + 32 * (int)rank);
+            }
+            break;
+          }
+        }
+        const uint32_t b = tile & 1u, use = tile >> 1;
+        // the peer has read our copy of tile - 2
+        if (tile >= 2 && !mbar_wait_warp(&x_free[b], (use - 1) & 1u, kWaitLimit)) { fail(); break; }
+        if (!mbar_wait_warp(&s_full, tile & 1u, kWaitLimit)) { fail(); break; }
+        tc_fence_after();
+        uint32_t sa[32], sb[32];
+        tmem_ld32(tmem + TM_S + lane_off, sa);
+        tmem_ld32(tmem + TM_S + 32 + lane_off, sb);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free);
+        // Scores that fp16 cannot hold are rare: the tile's largest magnitude decides once whether they are clamped
+        // (NaN stays NaN).
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) top = fmax3(top, fabsf(__uint_as_float(sa[k])), fabsf(__uint_as_float(sb[k])));
+        half_max = fmaxf(half_max, top);
+        if (__any_sync(0xffffffffu, !(top * a.scale_log2 < 65504.f))) {
+          const float limit = 65504.f / a.scale_log2;   // (rounds back to 65504 in fp16)
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            sa[k] = __float_as_uint(clamp_nan(__uint_as_float(sa[k]), limit));
+            sb[k] = __float_as_uint(clamp_nan(__uint_as_float(sb[k]), limit));
+          }
+        }
+        const uint32_t xi = xin_peer + b * XH_BYTES;
+        uint32_t w[32];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int k = 8 * c + 2 * q;   // scores k, k+1
+            const float2 raw = make_float2(__uint_as_float(k < 32 ? sa[k] : sb[k - 32]), __uint_as_float(k < 32 ? sa[k + 1] : sb[k - 31]));
+            // sent already scaled (log2 units): the softmax then only adds
+            const float2 sc = mul_f32x2(raw, make_float2(a.scale_log2, a.scale_log2));
+            const __half2 hv = __floats2half2_rn(sc.x, sc.y);
+            w[4 * c + q] = *reinterpret_cast<const uint32_t*>(&hv);
+          }
+          st_async_v4(xi + (uint32_t)((c * 128 + h) * 16), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3], x_full_peer[b]);
+        }
+        // our own half, once the softmax warps have read the tile before's
+        if (tile > 0 && !mbar_wait_warp(&xo_free, (tile - 1) & 1u, kWaitLimit)) { fail(); break; }
+        tc_fence_after();
+        tmem_st32(tmem + TM_X + lane_off, w);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        // receive buffer b expects the peer's XH_BYTES for this tile (announced by one of the four arrivals).
+        if (issuer)
+          mbar_arrive_expect_tx_u32(smem_u32(&x_full[b]), XH_BYTES);
+        else if (lane == 0)
+          mbar_arrive(&x_full[b]);
+        ++tile;
+      }
+    }
+    // Rows without a query score 0; a key that no token sees holds zeros.
+    if (__any_sync(0xffffffffu, !(half_max <= MLA_FP16_SCORE_LIMIT)) && lane == 0 && a.status)
+      atomicOr(a.status, MLA_DEVICE_SCORE_RANGE);
+  } else {
+    // ============================================================ softmax / epilogue
+    reg_alloc<kRegsSoftmax>();
+    const int quarter = warp & 3;
+    const uint32_t me = warp >> 2;                        // this group takes the tiles with parity `me`
+    const int h = 32 * quarter + lane;                    // MMA row = TMEM lane
+    const int k_token = kPair ? h >> 6 : 0, head = kPair ? h & 63 : h;
+    const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
+    const uint32_t x_free_peer = mapa(smem_u32(&x_free[me]), peer);
+    uint8_t* const xi = xin + me * XH_BYTES;
+    uint32_t tile = 0, seg = 0, poison_phase = 0;
+    // P.V(k) has completed once its commit arrives on empty_bar[k % STAGES].  Each group waits for every other one
+    // at least, and P.V(k + STAGES) cannot have started, so the phase parity identifies the completion.
+    auto wait_pv = [&](uint32_t k) -> bool {
+      return mbar_wait_warp(&empty_bar[k % STAGES], (k / STAGES) & 1u, kWaitLimit);
+    };
+    int u, n, t0, t1;
+    bool whole;
+    while (!aborted() && it.next(u, t0, t1, whole)) {
+      const bool any = member_segment(a, keys_p, u, member, n, t0, t1);
+      const int64_t slot = ((int64_t)u + group) * a.width + member;
+      if (!any) {
+        // Nothing of this row in the group's range: an empty partial (weight 0).
+        if (!whole && rank == 0 && me == 0 && head < a.heads) {
+          a.ws_ml[(slot * 2) * HEADS + h] = -CUDART_INF_F;
+          a.ws_ml[(slot * 2 + 1) * HEADS + h] = 0.f;
+        }
+        continue;
+      }
+      const Sight sight = sight_of(n, k_token), other = kPair ? sight_of(n, k_token ^ 1) : sight;
+      float m = -CUDART_INF_F, l = 0.f;   // this group's sum l is relative to 2^m
+      for (int t = t0; t < t1; ++t, ++tile) {
+        if ((tile & 1u) != me) continue;
+        const uint64_t valid = seen_of(sight, t);
+        uint64_t poison = 0;
+        if (kPair && (!sight.whole(t) || !other.whole(t)) && (valid ^ seen_of(other, t)) != 0ull) {
+          const uint32_t k = tile & 3u;
+          if (!mbar_wait_warp(&poison_full[k], poison_phase >> k & 1u, kWaitLimit)) { fail(); break; }
+          poison_phase ^= 1u << k;
+          poison = poison_s[k] & valid;
+        }
+        // ---- both halves present: our own (stored by the exchange warps) and the peer's remote stores
+        if (!mbar_wait_warp(&x_full[me], (tile >> 1) & 1u, kWaitLimit)) { fail(); break; }
+        tc_fence_after();
+        uint32_t own[32];
+        tmem_ld32(tmem + TM_X + lane_off, own);
+        if (valid != ~0ull || poison != 0ull) {
+          // Keys that this token does not see: the peer's half becomes fp16 -inf, so that the score is -inf whatever
+          // our own (finite) half; a seen key that is not finite: NaN.  A rolled loop with computed addresses: it
+          // runs at a row's last tiles only.
+          const uint32_t row = smem_u32(xi) + (uint32_t)h * 16u;
+          uint64_t inv = ~valid | poison;
+#pragma unroll 1
+          while (inv != 0ull) {
+            const int k = __ffsll((long long)inv) - 1;
+            inv &= inv - 1ull;
+            st_shared_u16(row + (uint32_t)((k >> 3) * 128 * 16 + (k & 7) * 2), (poison >> k & 1) ? 0x7E00u : 0xFC00u);
+          }
+        }
+        tmem_wait_ld_regs(own);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&xo_free);
+        float x[BN];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 i4 = *reinterpret_cast<const uint4*>(xi + (c * 128 + h) * 16);
+          const uint32_t iw[4] = {i4.x, i4.y, i4.z, i4.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            x[8 * c + 2 * q] = add_f16lo(iw[q], add_f16lo(own[4 * c + q], 0.f));
+            x[8 * c + 2 * q + 1] = add_f16hi(iw[q], add_f16hi(own[4 * c + q], 0.f));
+          }
+        }
+        // ---- tile maximum (three-input max tree)
+        float mx;
+        {
+          float m21[22];
+#pragma unroll
+          for (int k = 0; k < 21; ++k) m21[k] = fmax3(x[3 * k], x[3 * k + 1], x[3 * k + 2]);
+          m21[21] = x[63];
+          float m7[8];
+#pragma unroll
+          for (int k = 0; k < 7; ++k) m7[k] = fmax3(m21[3 * k], m21[3 * k + 1], m21[3 * k + 2]);
+          m7[7] = m21[21];
+          mx = fmax3(fmax3(m7[0], m7[1], m7[2]), fmax3(m7[3], m7[4], m7[5]), fmaxf(m7[6], m7[7]));
+        }
+        // Every score above fed mx, so the warp holds all of this tile's data: the buffer is freed with a relaxed
+        // arrive ordered by that dependency.
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote_relaxed_dep(x_free_peer, __float_as_uint(mx));
+        // ---- the reference: handed over by the other group from the tile before; it moves only when the tile's
+        // maximum exceeds it by more than the threshold (or on the first visible entry)
+        float m_ref = -CUDART_INF_F;
+        if (t > t0) {
+          if (!mbar_wait_warp(&ref_full[me ^ 1u][quarter], ((tile - 1) >> 1) & 1u, kWaitLimit)) { fail(); break; }
+          m_ref = ref_s[me ^ 1u][h];
+        }
+        const bool moved = mx != -CUDART_INF_F && (m_ref == -CUDART_INF_F || mx > m_ref + kRescaleThreshold);
+        const float m_new = moved ? mx : m_ref;
+        ref_s[me][h] = m_new;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ref_full[me][quarter]);
+        const bool rescale = moved && m_ref != -CUDART_INF_F;
+        if (m != m_new) {
+          if (m != -CUDART_INF_F) l *= ex2_approx(m - m_new);   // (a sum without a reference is 0, or NaN)
+          m = m_new;
+        }
+        // ---- p = 2^(x - m)
+        const float shift = m_new == -CUDART_INF_F ? 0.f : -m_new;
+        uint32_t pk[32];
+        float2 ps2[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ps2[k] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < BN; k += 2) {
+          const float2 xs = add_f32x2(make_float2(x[k], x[k + 1]), make_float2(shift, shift));
+          const float p0 = ex2_approx(xs.x);
+          const float p1 = ex2_approx(xs.y);
+          ps2[(k >> 1) & 7] = add_f32x2(ps2[(k >> 1) & 7], make_float2(p0, p1));
+          const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
+          pk[k >> 1] = *reinterpret_cast<const uint32_t*>(&pb);
+        }
+        ps2[0] = add_f32x2(add_f32x2(ps2[0], ps2[1]), add_f32x2(ps2[2], ps2[3]));
+        ps2[4] = add_f32x2(add_f32x2(ps2[4], ps2[5]), add_f32x2(ps2[6], ps2[7]));
+        ps2[0] = add_f32x2(ps2[0], ps2[4]);
+        l += ps2[0].x + ps2[0].y;
+        // ---- P into TMEM once the previous P.V has consumed it (and O is stable)
+        if (tile > 0 && !wait_pv(tile - 1)) { fail(); break; }
+        tc_fence_after();
+        // tcgen05.ld / st are warp-collective: the whole warp takes the
+        // rescale pass when any of its rows needs it, the others with factor 1.
+        if (__any_sync(0xffffffffu, rescale)) {
+          const float f = rescale ? ex2_approx(m_ref - m_new) : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < DV / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tmem + TM_O + c * 32 + lane_off, o);
+            tmem_wait_ld_regs(o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st32(tmem + TM_O + c * 32 + lane_off, o);
+          }
+        }
+        tmem_st32(tmem + TM_P + lane_off, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full);
+      }
+      if (aborted()) break;
+      // ---- both groups' sums (their slots are free once every warp has left the segment before)
+      if (seg > 0 && !mbar_wait_warp(&o_free, (seg - 1) & 1u, kWaitLimit)) { fail(); break; }
+      sum_s[me][h] = l;
+      sum_ref_s[me][h] = m;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_done);
+      if (!mbar_wait_warp(&seg_done, seg & 1u, kWaitLimit)) { fail(); break; }
+      {
+        const float l2 = sum_s[me ^ 1u][h], m2 = sum_ref_s[me ^ 1u][h];
+        const float top = fmaxf(m, m2);   // the segment's last reference, which O is relative to
+        l = (m == top ? l : m == -CUDART_INF_F ? l : l * ex2_approx(m - top)) +
+            (m2 == top ? l2 : m2 == -CUDART_INF_F ? l2 : l2 * ex2_approx(m2 - top));
+        m = top;
+      }
+      // ---- epilogue: the segment's last P.V, then this group's half of the context
+      if (!wait_pv(tile - 1)) { fail(); break; }
+      tc_fence_after();
+      const bool blind = kPair && limit_of(n, k_token) == 0;
+      if (blind) l = 0.f;
+      const int c0 = (DV / 64) * (int)me;   // of DV / 32 chunks of 32 columns
+      auto drain_o = [&](auto&& store_chunk) {
+        uint32_t oa[32], ob[32];
+        auto blank = [&](uint32_t(&o)[32]) {
+          if (!blind) return;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0;
+        };
+        tmem_ld32(tmem + TM_O + c0 * 32 + lane_off, oa);
+#pragma unroll 1
+        for (int c = c0; c < c0 + DV / 64; c += 2) {
+          tmem_wait_ld_regs(oa);
+          tmem_ld32(tmem + TM_O + (c + 1) * 32 + lane_off, ob);
+          blank(oa);
+          store_chunk(c, oa);
+          tmem_wait_ld_regs(ob);
+          if (c + 2 < c0 + DV / 64) tmem_ld32(tmem + TM_O + (c + 2) * 32 + lane_off, oa);
+          blank(ob);
+          store_chunk(c + 1, ob);
+        }
+      };
+      const int i = (n % a.s_q) * kTokens + k_token;
+      const int64_t token = (int64_t)(n / a.s_q) * a.tok_q + i;
+      const float inv = l != 0.f ? 1.f / l : 0.f;   // 0: no entry; NaN stays NaN
+      if (head >= a.heads || i >= a.tok_q) {
+        // a padding row: nothing to store
+      } else if (whole) {
+        const int64_t off = token * a.ctx_row_stride + (int64_t)head * a.ctx_head_stride + dim_base;
+        if (a.out_f32) {
+          drain_o([&](int c, const uint32_t(&o)[32]) {
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.ctx) + off + c * 32);
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
+                                   __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
+          });
+        } else {
+          drain_o([&](int c, const uint32_t(&o)[32]) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.ctx) + off + c * 32);
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              dst[v] = make_uint4(pack_bf16x2(__uint_as_float(o[8 * v]) * inv, __uint_as_float(o[8 * v + 1]) * inv),
+                                  pack_bf16x2(__uint_as_float(o[8 * v + 2]) * inv, __uint_as_float(o[8 * v + 3]) * inv),
+                                  pack_bf16x2(__uint_as_float(o[8 * v + 4]) * inv, __uint_as_float(o[8 * v + 5]) * inv),
+                                  pack_bf16x2(__uint_as_float(o[8 * v + 6]) * inv, __uint_as_float(o[8 * v + 7]) * inv));
+          });
+        }
+        if (rank == 0 && me == 0 && a.lse)
+          a.lse[token * a.heads + head] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+      } else {
+        // Partial: this piece's context normalised by its own sum in fp16, (m, l) in f32 beside it, kept in L2.
+        const float m_piece = l == 0.f ? -CUDART_INF_F : m == -CUDART_INF_F ? 0.f : m;   // -inf marks an empty one
+        const uint64_t keep = l2_policy_evict_last();
+        uint4* dst = a.ws_o + (slot * (RANK / 8) + dim_base / 8) * HEADS + h;
+        float vmax = 0.f;
+        drain_o([&](int c, const uint32_t(&o)[32]) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float x0 = __uint_as_float(o[8 * q + 2 * j]) * inv, x1 = __uint_as_float(o[8 * q + 2 * j + 1]) * inv;
+              vmax = fmaxf(vmax, fmaxf(fabsf(x0), fabsf(x1)));   // beyond 65504 the fp16 value is infinite
+              const __half2 hv = __floats2half2_rn(x0, x1);
+              w[j] = *reinterpret_cast<const uint32_t*>(&hv);
+            }
+            st_global_v4_policy(dst + (int64_t)(4 * c + q) * HEADS, make_uint4(w[0], w[1], w[2], w[3]), keep);
+          }
+        });
+        if (!(vmax <= 65504.f) && a.status) atomicOr(a.status, MLA_DEVICE_VALUE_RANGE);
+        if (rank == 0 && me == 0) {
+          st_global_f32_policy(a.ws_ml + (slot * 2) * HEADS + h, m_piece, keep);
+          st_global_f32_policy(a.ws_ml + (slot * 2 + 1) * HEADS + h, l, keep);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_free);
+      ++seg;
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  pdl_trigger();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // the peer no longer writes into this CTA's shared memory
+  if (warp == kScoreWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_tc_paged(const DecodeGeometry& g, int out_dtype, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream) {
+  if (workspace_bytes < tc_decode_workspace(g.batch * g.s_q)) return cudaErrorInvalidValue;
+  if (g.heads != 64 && g.heads != HEADS) return cudaErrorInvalidValue;
+  TcDecodeArgs a = {};
+  a.q = static_cast<const __nv_bfloat16*>(g.q);
+  a.q_row_stride = g.q_row_stride;
+  a.q_head_stride = g.q_head_stride;
+  a.kv_len = g.kv_len;
+  a.tok_q = g.s_q;
+  a.tokens = g.heads == 64 && g.s_q > 1 ? 2 : 1;
+  a.s_q = (g.s_q + a.tokens - 1) / a.tokens;
+  a.n_q = g.batch * a.s_q;
+  a.heads = g.heads;
+  a.scale_log2 = g.scale_log2;
+  a.ctx = g.ctx_out;
+  a.ctx_row_stride = g.ctx_row_stride;
+  a.ctx_head_stride = g.ctx_head_stride;
+  a.out_f32 = out_dtype == MLA_DTYPE_F32;
+  a.lse = g.lse_out;
+  a.status = g.device_status;
+  a.t_max = g.t_max;
+  a.table = g.table;
+  a.table_stride = g.table_stride;
+  a.page_size = g.page_size;
+  a.num_pages = g.num_pages;
+  a.counts = g.counts;
+  a.tree = g.tree;
+  a.tree_words = g.tree_words;
+  a.num_clusters = device_sm_count() / 2;
+  a.width = a.s_q < 8 ? a.s_q : 8;
+  if (const char* w = getenv("MLA_W")) a.width = a.s_q < atoi(w) ? a.s_q : atoi(w);
+  a.n_units = (a.n_q + a.width - 1) / a.width;
+  a.min_tiles = kMinTilesPerGroup;
+  a.plan_in_kernel = a.n_q <= kMaxRowsInKernelPlan ? 1 : 0;
+  a.box_rows = BN;   // the largest box that divides a tile and a page
+  while (g.page_size % a.box_rows != 0) a.box_rows >>= 1;
+  if (a.box_rows < 8) return cudaErrorInvalidValue;
+  lay_out_workspace(a, workspace);
+
+  CUtensorMap lat_map, rope_map;
+  {
+    const uint64_t row = (uint64_t)g.latent_row_stride * 2;
+    const uint64_t page = g.num_pages > 1 ? (uint64_t)g.latent_page_stride * 2 : row * g.page_size;   // (one page: no stride)
+    const uint64_t dims[5] = {64, 8, RANK / 64, (uint64_t)g.page_size / 8, (uint64_t)g.num_pages};
+    const uint64_t strides[4] = {row, 128, 8 * row, page};
+    const uint32_t box[5] = {64, 8, 4, (uint32_t)a.box_rows / 8, 1};
+    if (!encode_tmap_bf16(&lat_map, g.latent, 5, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  {
+    const uint64_t row = (uint64_t)g.rope_row_stride * 2;
+    const uint64_t page = g.num_pages > 1 ? (uint64_t)g.rope_page_stride * 2 : row * g.page_size;
+    const uint64_t dims[3] = {(uint64_t)g.rope_dim, (uint64_t)g.page_size, (uint64_t)g.num_pages};
+    const uint64_t strides[2] = {row, page};
+    const uint32_t box[3] = {32, (uint32_t)a.box_rows, 1};
+    if (!encode_tmap_bf16(&rope_map, g.rope, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B)) return cudaErrorInvalidValue;
+  }
+  const bool lockstep = a.width > 1;
+  auto* const kernel = a.tokens == 2 ? (lockstep ? tc_paged_kernel<kPrefetchAheadGroup, true> : tc_paged_kernel<kPrefetchAheadRow, true>)
+                                     : (lockstep ? tc_paged_kernel<kPrefetchAheadGroup, false> : tc_paged_kernel<kPrefetchAheadRow, false>);
+  {
+    // The warpgroups' register shares wait for one another: a build with other
+    // registers than they add up to must not be launched.
+    static const bool fits = [] {
+      for (auto* k : {tc_paged_kernel<kPrefetchAheadGroup, true>, tc_paged_kernel<kPrefetchAheadRow, true>,
+                      tc_paged_kernel<kPrefetchAheadGroup, false>, tc_paged_kernel<kPrefetchAheadRow, false>}) {
+        cudaFuncAttributes attr;
+        if (cudaFuncGetAttributes(&attr, k) != cudaSuccess || attr.numRegs < kRegsLaunch) return false;
+      }
+      return true;
+    }();
+    if (!fits) return cudaErrorInvalidConfiguration;
+    const cudaError_t ea = set_max_dynamic_smem(kernel, SMEM_BYTES);
+    if (ea != cudaSuccess) return ea;
+  }
+  cudaError_t e = a.plan_in_kernel ? cudaSuccess : launch_split_plan(a, stream);
+  if (e == cudaSuccess) e = launch_pdl(kernel, dim3(2 * a.num_clusters), dim3(THREADS), SMEM_BYTES, stream, lat_map, rope_map, a);
+  if (e == cudaSuccess) e = launch_split_combine(a, stream);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace mla

@@ -704,8 +704,8 @@ def test_two_graphs_replayed(mla):
 
 
 def test_pages_and_windows_give_the_same(mla):
-    """A cache in contiguous windows seen as pages of one row after another: the same bits where the split is the
-    same (one token), and the windows' causal verify against a chain as a tree."""
+    """A cache in contiguous windows seen as pages of one row after another (the kernels add in different orders: the
+    bf16 bounds, twice over), and a chain as a tree against tokens in a row (the same bits)."""
     g = gen(8)
     B, T, heads = 3, 640, 128
     latent, rope = normal(g, B, T, 512).bfloat16(), normal(g, B, T, 64).bfloat16()
@@ -717,10 +717,11 @@ def test_pages_and_windows_give_the_same(mla):
         table = torch.arange(B * 10, device=DEV, dtype=torch.int32).view(B, 10)
         pools = latent.view(-1, 64, 512), rope.view(-1, 64, 64)
         mla.decode_attend_paged(q, *pools, table, lens, B, s_q, SCALE, got)
-        assert torch.equal(got, want)
+        assert (got.float() - want.float()).abs().max() <= 4e-2
+        assert (got.float() - want.float()).norm() <= 1e-2 * want.float().norm()
         parents = torch.arange(-1, s_q - 1, device=DEV, dtype=torch.int32).expand(B, s_q)
         pos = torch.zeros(B, s_q, dtype=torch.int32, device=DEV)
         mask = torch.zeros(B * s_q, 1, dtype=torch.int64, device=DEV)
         mla.tree_plan(parents, None, pos, mask)
         mla.decode_attend_paged(q, *pools, table, lens, B, s_q, SCALE, tree, tree_mask=mask)
-        assert torch.equal(tree, want)
+        assert torch.equal(tree, got)

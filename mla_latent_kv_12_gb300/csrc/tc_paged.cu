@@ -46,17 +46,17 @@ constexpr int GROUP_BYTES = 4 * 1024;
 constexpr int LATENT_BYTES = 8 * GROUP_BYTES;
 constexpr int STAGE_BYTES = LATENT_BYTES + BN * 64;
 constexpr int XH_BYTES = 128 * BN * 2;    // fp16 partial scores of one tile
-constexpr int QROPE_BYTES = 128 * 64;     // the query's 32 rope dims (64-byte rows, 64-byte swizzle)
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 2 * XH_BYTES + QROPE_BYTES;
-// TMEM columns: context, the query's latent dims, scores, probabilities, this CTA's half of the scores in fp16.
-constexpr uint32_t TM_O = 0, TM_Q = 256, TM_S = 384, TM_P = 448, TM_X = 480;
-// Warpgroups: two of softmax warps, the exchange, and the issuers (loads, score MMA, P.V MMA, L2 prefetch).
-constexpr int THREADS = 512;
-constexpr int kExchangeWarp = 8, kLoadWarp = 12, kScoreWarp = 13, kPvWarp = 14, kPrefetchWarp = 15;
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 2 * XH_BYTES;
+constexpr uint32_t TM_O = 0, TM_Q = 256, TM_S = 400, TM_P = 464;  // TMEM columns (Q: 128 + 16)
+// Warpgroups: the softmax groups, and the issuers (loads, score MMA, P.V MMA, L2 prefetch).
+constexpr uint32_t kGroups = 3;
+constexpr uint32_t kSlots = 2 * kGroups;   // of masks handed from the score warp to the groups
+constexpr int THREADS = 128 * (kGroups + 1);
+constexpr int kLoadWarp = 4 * kGroups, kScoreWarp = kLoadWarp + 1, kPvWarp = kLoadWarp + 2, kPrefetchWarp = kLoadWarp + 3;
 // Registers per thread of each warpgroup; their sum fits the launch's.
 constexpr int kRegsLaunch = 128;
-constexpr int kRegsSoftmax = 152, kRegsIssue = 72;
-static_assert(2 * kRegsSoftmax + kRegsLaunch + kRegsIssue <= 4 * kRegsLaunch, "more registers than the launch has");
+constexpr int kRegsSoftmax = 144, kRegsIssue = 72;
+static_assert(kGroups * kRegsSoftmax + kRegsIssue <= (kGroups + 1) * kRegsLaunch, "more registers than the launch has");
 // Tiles pulled into L2 ahead of their load: farther for a lockstep group.
 constexpr int kPrefetchAheadGroup = 8, kPrefetchAheadRow = 3;
 
@@ -90,17 +90,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     return;
   }
   uint8_t* stages = smem_raw;
-  // The peer's halves of the scores, [8][128 heads][16 B] in fp16, one buffer per softmax group.
+  // The peer's halves of the scores, [8][128 rows][16 B] in fp16, tiles in turn.
   uint8_t* xin = smem_raw + STAGES * STAGE_BYTES;
-  uint8_t* qrope_s = xin + 2 * XH_BYTES;
 
   __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES];
-  __shared__ __align__(8) uint64_t s_full, s_free, p_full, q_full, o_free, mma_drain, pv_drain, seg_done;
-  __shared__ __align__(8) uint64_t x_full[2], x_free[2], xo_free;
-  __shared__ __align__(8) uint64_t ref_full[2][4];      // per softmax group and lane quarter: its reference is in ref_s
-  __shared__ __align__(8) uint64_t poison_full[4];      // kPair
-  __shared__ uint64_t poison_s[4];
-  __shared__ float ref_s[2][128], sum_s[2][128], sum_ref_s[2][128];
+  __shared__ __align__(8) uint64_t p_full, q_full, o_free, mma_drain, pv_drain, seg_done;
+  // One barrier per softmax group: its waits then follow its own tiles, whatever the others' progress.
+  __shared__ __align__(8) uint64_t s_full[kGroups], s_free[kGroups], x_full[kGroups], x_free[kGroups];
+  __shared__ __align__(8) uint64_t ref_full[kGroups][4];   // per lane quarter: the group's reference is in ref_s
+  __shared__ __align__(8) uint64_t poison_full[kSlots];    // kPair
+  __shared__ uint64_t poison_s[kSlots];
+  __shared__ float ref_s[kGroups][128], sum_s[kGroups][128], sum_ref_s[kGroups][128];
   __shared__ uint32_t tmem_base_s;
   __shared__ volatile int abort_s, loaded_s;   // loaded_s: tiles whose loads have been issued
   __shared__ int32_t plan_keys_s[kMaxRowsInKernelPlan], plan_prefix_s[kMaxRowsInKernelPlan + 2];
@@ -122,19 +122,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(&full_bar[s], 1);
       mbar_init(&empty_bar[s], 1);
     }
-    mbar_init(&s_full, 1);
-    mbar_init(&s_free, 4);      // the exchange warps have read S
-    mbar_init(&p_full, 4);      // one arrival per softmax warp of the tile's group
-    mbar_init(&q_full, 4);      // the exchange warps have written this segment's query into TMEM
-    mbar_init(&o_free, 8);
-    mbar_init(&seg_done, 8);    // the softmax warps have published their sums
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&x_full[b], 4);   // our exchange warps have stored our half + the peer's bytes into xin[b]
-      mbar_init(&x_free[b], 4);   // the peer's softmax warps have read xin[b]
+    mbar_init(&p_full, 4);      // one arrival per warp of the tile's group
+    mbar_init(&q_full, 4);      // a group has written this segment's query into TMEM
+    mbar_init(&o_free, 4 * kGroups);
+    mbar_init(&seg_done, 4 * kGroups);   // the sums are published
+    for (uint32_t b = 0; b < kGroups; ++b) {
+      mbar_init(&s_full[b], 1);
+      mbar_init(&s_free[b], 4);   // the group has read S
+      mbar_init(&x_full[b], 1);   // the peer's bytes of the group's tile, announced by one of its threads
+      mbar_init(&x_free[b], 4);   // the peer's group has read them
       for (int q = 0; q < 4; ++q) mbar_init(&ref_full[b][q], 1);
     }
-    for (int k = 0; k < 4; ++k) mbar_init(&poison_full[k], 1);
-    mbar_init(&xo_free, 4);     // our softmax warps have read our half
+    for (uint32_t k = 0; k < kSlots; ++k) mbar_init(&poison_full[k], 1);
     mbar_init(&mma_drain, 1);
     mbar_init(&pv_drain, 1);
     abort_s = 0;
@@ -243,10 +242,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           for (int t = t0 + STAGES; t < t0 + kPrefetchAhead && t < t1; ++t) prefetch_tile(t);
         for (int t = t0; t < t1 && !aborted(); ++t) {
           if (loads) {
-            if (fills >= STAGES && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
             int pg, rw;
             box_of(t, pg, rw);
             const uint32_t there = __ballot_sync(0xffffffffu, pg >= 0);
+            if (fills >= STAGES && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
             if (lane == 0) mbar_arrive_expect_tx(&full_bar[stage], __popc(there) * a.box_rows * (STAGE_BYTES / BN));
             __syncwarp();
             if (pg >= 0) {
@@ -308,20 +307,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (kPair && one != 0ull) {
               const uint32_t lo = __reduce_or_sync(0xffffffffu, (uint32_t)poison);
               const uint32_t hi = __reduce_or_sync(0xffffffffu, (uint32_t)(poison >> 32));
-              // (four slots: tile t + 4 gets here only after the softmax has read tile t's)
-              if (tile > 0 && !mbar_wait_warp(&s_free, (tile - 1) & 1u, kWaitLimit)) { fail(); break; }
+              // (tile t + kSlots gets here only once the group of tile t has read S of t + kGroups)
+              if (tile > 0 && !mbar_wait_warp(&s_free[(tile - 1) % kGroups], (tile - 1) / kGroups & 1u, kWaitLimit)) { fail(); break; }
               if (lane == 0) {
-                poison_s[tile & 3] = (uint64_t)hi << 32 | lo;
-                mbar_arrive(&poison_full[tile & 3]);
+                poison_s[tile % kSlots] = (uint64_t)hi << 32 | lo;
+                mbar_arrive(&poison_full[tile % kSlots]);
               }
             }
           }
-          if (tile > 0 && !mbar_wait_warp(&s_free, (tile - 1) & 1u, kWaitLimit)) { fail(); break; }
+          if (tile > 0 && !mbar_wait_warp(&s_free[(tile - 1) % kGroups], (tile - 1) / kGroups & 1u, kWaitLimit)) { fail(); break; }
           tc_fence_after();
           // 16 latent K-steps, then this CTA's two rope K-steps
           const uint64_t d0 = smem_desc(smem_u32(stages + stage * STAGE_BYTES), 16, GROUP_BYTES, kSwizzle128B);
           const uint64_t d_rope = smem_desc(smem_u32(stages + stage * STAGE_BYTES + LATENT_BYTES), 16, 512, kSwizzle64B);
-          const uint64_t a_rope = smem_desc(smem_u32(qrope_s), 16, 512, kSwizzle64B);
           if (elect_one()) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -331,8 +329,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             }
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-              mma_ss(tmem + TM_S, a_rope + (uint64_t)((k * 32) >> 4), d_rope + (uint64_t)((k * 32) >> 4), idesc_s, 1u);
-            mma_commit(&s_full);
+              mma_ts(tmem + TM_S, tmem + TM_Q + 128 + k * 8, d_rope + (uint64_t)((k * 32) >> 4), idesc_s, 1u);
+            mma_commit(&s_full[tile % kGroups]);
           }
           __syncwarp();
           ++tile;
@@ -380,151 +378,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       __syncwarp();
       mbar_wait_warp(&pv_drain, 0, kWaitLimit);
     }
-  } else if (warp >= kExchangeWarp) {
-    // ============================================================ exchange warps
-    const int quarter = warp & 3;
-    const int h = 32 * quarter + lane;     // MMA row
-    const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
-    const bool issuer = (h == 0);
-    const uint32_t xin_peer = mapa(smem_u32(xin), peer);
-    uint32_t x_full_peer[2];
-    x_full_peer[0] = mapa(smem_u32(&x_full[0]), peer);
-    x_full_peer[1] = mapa(smem_u32(&x_full[1]), peer);
-    // This MMA row's query of row n, or null (padding, or a token that the batch row does not have).
-    auto query_of = [&](int n) -> const __nv_bfloat16* {
-      const int b = n / a.s_q, i = (n % a.s_q) * kTokens + (kPair ? h >> 6 : 0), head = kPair ? h & 63 : h;
-      if (i >= a.tok_q || head >= a.heads) return nullptr;
-      return a.q + ((int64_t)b * a.tok_q + i) * a.q_row_stride + (int64_t)head * a.q_head_stride;
-    };
-    uint32_t tile = 0;
-    float half_max = 0.f;   // largest |half score| sent (checked against the fp16 exchange's range)
-    int u, n, t0, t1;
-    bool whole;
-    while (!aborted() && it.next(u, t0, t1, whole)) {
-      if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
-      {
-        // The query into TMEM: every score MMA of the previous segment has completed (its last scores were read
-        // here), while the softmax warps may still be finishing that segment.
-        const __nv_bfloat16* qrow = query_of(n);
-        uint4 qv[36];   // all 36 loads in flight at once: 256 latent dims, then the 32 rope dims
-        const uint4* qlat = reinterpret_cast<const uint4*>(qrow + dim_base);
-        const uint4* qrope = reinterpret_cast<const uint4*>(qrow + RANK + 32 * (int)rank);
-#pragma unroll
-        for (int v = 0; v < 32; ++v) qv[v] = qrow ? __ldg(qlat + v) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) qv[32 + v] = qrow ? __ldg(qrope + v) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r[32];
-#pragma unroll
-          for (int v = 0; v < 8; ++v)
-            r[4 * v] = qv[8 * c + v].x, r[4 * v + 1] = qv[8 * c + v].y, r[4 * v + 2] = qv[8 * c + v].z, r[4 * v + 3] = qv[8 * c + v].w;
-          tmem_st32(tmem + TM_Q + c * 32 + lane_off, r);
-        }
-        // the rope dims as a K-major tile in shared memory (piece v of row h at v ^ (h / 2 % 4))
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          *reinterpret_cast<uint4*>(qrope_s + h * 64 + ((v ^ ((h >> 1) & 3)) << 4)) = qv[32 + v];
-        fence_proxy_async_smem();
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full);
-      }
-      // A few tiles before this segment ends, the next segment's query row is pulled into L2.
-      const int t_pf = t1 - kQueryPrefetchTiles > t0 ? t1 - kQueryPrefetchTiles : t0;
-      for (int t = t0; t < t1; ++t) {
-        if (t == t_pf) {
-          WorkIter peek = it;
-          int un, nn, tn0, tn1;
-          bool wn;
-          while (peek.next(un, tn0, tn1, wn)) {
-            if (!member_segment(a, keys_p, un, member, nn, tn0, tn1)) continue;
-            if (const __nv_bfloat16* qnext = query_of(nn)) {
-#pragma unroll
-              for (int l = 0; l < 4; ++l) prefetch_l2(qnext + dim_base + 64 * l);
-              prefetch_l2(qnext + RANK + 32 * (int)rank);
-            }
-            break;
-          }
-        }
-        const uint32_t b = tile & 1u, use = tile >> 1;
-        // the peer has read our copy of tile - 2
-        if (tile >= 2 && !mbar_wait_warp(&x_free[b], (use - 1) & 1u, kWaitLimit)) { fail(); break; }
-        if (!mbar_wait_warp(&s_full, tile & 1u, kWaitLimit)) { fail(); break; }
-        tc_fence_after();
-        uint32_t sa[32], sb[32];
-        tmem_ld32(tmem + TM_S + lane_off, sa);
-        tmem_ld32(tmem + TM_S + 32 + lane_off, sb);
-        tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free);
-        // Scores that fp16 cannot hold are rare: the tile's largest magnitude decides once whether they are clamped
-        // (NaN stays NaN).
-        float top = 0.f;
-#pragma unroll
-        for (int k = 0; k < 32; ++k) top = fmax3(top, fabsf(__uint_as_float(sa[k])), fabsf(__uint_as_float(sb[k])));
-        half_max = fmaxf(half_max, top);
-        if (__any_sync(0xffffffffu, !(top * a.scale_log2 < 65504.f))) {
-          const float limit = 65504.f / a.scale_log2;   // (rounds back to 65504 in fp16)
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            sa[k] = __float_as_uint(clamp_nan(__uint_as_float(sa[k]), limit));
-            sb[k] = __float_as_uint(clamp_nan(__uint_as_float(sb[k]), limit));
-          }
-        }
-        const uint32_t xi = xin_peer + b * XH_BYTES;
-        uint32_t w[32];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int k = 8 * c + 2 * q;   // scores k, k+1
-            const float2 raw = make_float2(__uint_as_float(k < 32 ? sa[k] : sb[k - 32]), __uint_as_float(k < 32 ? sa[k + 1] : sb[k - 31]));
-            // sent already scaled (log2 units): the softmax then only adds
-            const float2 sc = mul_f32x2(raw, make_float2(a.scale_log2, a.scale_log2));
-            const __half2 hv = __floats2half2_rn(sc.x, sc.y);
-            w[4 * c + q] = *reinterpret_cast<const uint32_t*>(&hv);
-          }
-          st_async_v4(xi + (uint32_t)((c * 128 + h) * 16), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3], x_full_peer[b]);
-        }
-        // our own half, once the softmax warps have read the tile before's
-        if (tile > 0 && !mbar_wait_warp(&xo_free, (tile - 1) & 1u, kWaitLimit)) { fail(); break; }
-        tc_fence_after();
-        tmem_st32(tmem + TM_X + lane_off, w);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        // receive buffer b expects the peer's XH_BYTES for this tile (announced by one of the four arrivals).
-        if (issuer)
-          mbar_arrive_expect_tx_u32(smem_u32(&x_full[b]), XH_BYTES);
-        else if (lane == 0)
-          mbar_arrive(&x_full[b]);
-        ++tile;
-      }
-    }
-    // Rows without a query score 0; a key that no token sees holds zeros.
-    if (__any_sync(0xffffffffu, !(half_max <= MLA_FP16_SCORE_LIMIT)) && lane == 0 && a.status)
-      atomicOr(a.status, MLA_DEVICE_SCORE_RANGE);
   } else {
-    // ============================================================ softmax / epilogue
+    // ============================================================ exchange, softmax, epilogue
     reg_alloc<kRegsSoftmax>();
     const int quarter = warp & 3;
-    const uint32_t me = warp >> 2;                        // this group takes the tiles with parity `me`
+    const uint32_t me = warp >> 2;                        // this group takes the tiles me, me + kGroups, ...
     const int h = 32 * quarter + lane;                    // MMA row = TMEM lane
     const int k_token = kPair ? h >> 6 : 0, head = kPair ? h & 63 : h;
     const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
-    const uint32_t x_free_peer = mapa(smem_u32(&x_free[me]), peer);
-    uint8_t* const xi = xin + me * XH_BYTES;
-    uint32_t tile = 0, seg = 0, poison_phase = 0;
-    // P.V(k) has completed once its commit arrives on empty_bar[k % STAGES].  Each group waits for every other one
-    // at least, and P.V(k + STAGES) cannot have started, so the phase parity identifies the completion.
+    const uint32_t before = (me + kGroups - 1) % kGroups; // the group of the tile before
+    const uint32_t xin_peer = mapa(smem_u32(xin), peer) + (uint32_t)h * 16u;
+    const uint32_t x_full_peer = mapa(smem_u32(&x_full[me]), peer), x_free_peer = mapa(smem_u32(&x_free[me]), peer);
+    uint32_t tile = 0, seg = 0, poison_phase = 0, use = 0;   // use: tiles of this group so far
+    float half_max = 0.f;   // largest |half score| sent (checked against the fp16 exchange's range)
+    // P.V(k) has completed once its commit arrives on empty_bar[k % STAGES].  Each group waits for one of every
+    // kGroups < STAGES at least, and P.V(k + STAGES) cannot have started, so the phase parity identifies the completion.
     auto wait_pv = [&](uint32_t k) -> bool {
       return mbar_wait_warp(&empty_bar[k % STAGES], (k / STAGES) & 1u, kWaitLimit);
     };
+    // This MMA row's query of row n, or null (padding, or a token that the batch row does not have).
+    auto query_of = [&](int n) -> const __nv_bfloat16* {
+      const int b = n / a.s_q, i = (n % a.s_q) * kTokens + k_token;
+      if (i >= a.tok_q || head >= a.heads) return nullptr;
+      return a.q + ((int64_t)b * a.tok_q + i) * a.q_row_stride + (int64_t)head * a.q_head_stride + dim_base;
+    };
+    auto load_query = [&](int n) {
+      const __nv_bfloat16* qrow = query_of(n);
+      uint4 qv[36];   // all 36 loads in flight at once: 256 latent dims, then the 32 rope dims
+      const uint4* qlat = reinterpret_cast<const uint4*>(qrow);
+      const uint4* qrope = qlat + (RANK - dim_base + 32 * (int)rank) / 8;
+#pragma unroll
+      for (int v = 0; v < 32; ++v) qv[v] = qrow ? __ldg(qlat + v) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) qv[32 + v] = qrow ? __ldg(qrope + v) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t r[32];
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+          r[4 * v] = qv[8 * c + v].x, r[4 * v + 1] = qv[8 * c + v].y, r[4 * v + 2] = qv[8 * c + v].z, r[4 * v + 3] = qv[8 * c + v].w;
+        tmem_st32(tmem + TM_Q + c * 32 + lane_off, r);
+      }
+      uint32_t r[16];
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        r[4 * v] = qv[32 + v].x, r[4 * v + 1] = qv[32 + v].y, r[4 * v + 2] = qv[32 + v].z, r[4 * v + 3] = qv[32 + v].w;
+      tmem_st16(tmem + TM_Q + 128 + lane_off, r);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full);
+    };
+    // This member's next segment behind `it`, or -1.
+    auto next_row = [&]() {
+      WorkIter peek = it;
+      int u, n, t0, t1;
+      bool whole;
+      while (peek.next(u, t0, t1, whole))
+        if (member_segment(a, keys_p, u, member, n, t0, t1)) return n;
+      return -1;
+    };
     int u, n, t0, t1;
     bool whole;
+    if (me == 0) {
+      const int first_row = next_row();
+      if (first_row >= 0) load_query(first_row);
+    }
     while (!aborted() && it.next(u, t0, t1, whole)) {
       const bool any = member_segment(a, keys_p, u, member, n, t0, t1);
       const int64_t slot = ((int64_t)u + group) * a.width + member;
@@ -537,27 +456,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         continue;
       }
       const Sight sight = sight_of(n, k_token), other = kPair ? sight_of(n, k_token ^ 1) : sight;
+      const int t_pf = t1 - kQueryPrefetchTiles > t0 ? t1 - kQueryPrefetchTiles : t0;
       float m = -CUDART_INF_F, l = 0.f;   // this group's sum l is relative to 2^m
       for (int t = t0; t < t1; ++t, ++tile) {
-        if ((tile & 1u) != me) continue;
+        if (tile % kGroups != me) continue;
+        // A few tiles before this segment ends, the next segment's query row is pulled into L2.
+        if (t >= t_pf && t < t_pf + (int)kGroups) {
+          const int nn = next_row();
+          if (const __nv_bfloat16* qnext = nn >= 0 ? query_of(nn) : nullptr) {
+#pragma unroll
+            for (int l4 = 0; l4 < 4; ++l4) prefetch_l2(qnext + 64 * l4);
+            prefetch_l2(qnext + RANK - dim_base + 32 * (int)rank);
+          }
+        }
         const uint64_t valid = seen_of(sight, t);
+        // ---- this CTA's partial scores, in f32 and log2 units
+        if (!mbar_wait_warp(&s_full[me], use & 1u, kWaitLimit)) { fail(); break; }
+        tc_fence_after();
+        float x[BN];
+        {
+          uint32_t sa[32], sb[32];
+          tmem_ld32(tmem + TM_S + lane_off, sa);
+          tmem_ld32(tmem + TM_S + 32 + lane_off, sb);
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_free[me]);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(sa[k]), x[32 + k] = __uint_as_float(sb[k]);
+        }
+        // Scores that fp16 cannot hold are rare: the tile's largest magnitude decides once whether they are clamped
+        // (NaN stays NaN).
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) top = fmax3(top, fabsf(x[k]), fabsf(x[32 + k]));
+        half_max = fmaxf(half_max, top);
+        if (__any_sync(0xffffffffu, !(top * a.scale_log2 < 65504.f))) {
+          const float limit = 65504.f / a.scale_log2;   // (rounds back to 65504 in fp16)
+#pragma unroll
+          for (int k = 0; k < BN; ++k) x[k] = clamp_nan(x[k], limit);
+        }
+        // ---- sent to the peer in fp16, once it has read the tile two back
+        const uint32_t xb = (tile & 1u) * XH_BYTES;
+        if (tile >= 2 && !mbar_wait_warp(&x_free[(tile - 2) % kGroups], (tile - 2) / kGroups & 1u, kWaitLimit)) { fail(); break; }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t w[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int k = 8 * c + 2 * q;
+            const float2 sc = mul_f32x2(make_float2(x[k], x[k + 1]), make_float2(a.scale_log2, a.scale_log2));
+            x[k] = sc.x, x[k + 1] = sc.y;
+            const __half2 hv = __floats2half2_rn(sc.x, sc.y);
+            w[q] = *reinterpret_cast<const uint32_t*>(&hv);
+          }
+          st_async_v4(xin_peer + xb + (uint32_t)(c * 128 * 16), w[0], w[1], w[2], w[3], x_full_peer);
+        }
+        if (h == 0) mbar_arrive_expect_tx(&x_full[me], XH_BYTES);
         uint64_t poison = 0;
         if (kPair && (!sight.whole(t) || !other.whole(t)) && (valid ^ seen_of(other, t)) != 0ull) {
-          const uint32_t k = tile & 3u;
+          const uint32_t k = tile % kSlots;
           if (!mbar_wait_warp(&poison_full[k], poison_phase >> k & 1u, kWaitLimit)) { fail(); break; }
           poison_phase ^= 1u << k;
           poison = poison_s[k] & valid;
         }
-        // ---- both halves present: our own (stored by the exchange warps) and the peer's remote stores
-        if (!mbar_wait_warp(&x_full[me], (tile >> 1) & 1u, kWaitLimit)) { fail(); break; }
-        tc_fence_after();
-        uint32_t own[32];
-        tmem_ld32(tmem + TM_X + lane_off, own);
+        // ---- the peer's half (its remote stores complete as transaction bytes on this barrier)
+        if (!mbar_wait_warp(&x_full[me], use & 1u, kWaitLimit)) { fail(); break; }
+        ++use;
+        const uint8_t* const xi = xin + xb + h * 16;
         if (valid != ~0ull || poison != 0ull) {
           // Keys that this token does not see: the peer's half becomes fp16 -inf, so that the score is -inf whatever
           // our own (finite) half; a seen key that is not finite: NaN.  A rolled loop with computed addresses: it
           // runs at a row's last tiles only.
-          const uint32_t row = smem_u32(xi) + (uint32_t)h * 16u;
+          const uint32_t row = smem_u32(xi);
           uint64_t inv = ~valid | poison;
 #pragma unroll 1
           while (inv != 0ull) {
@@ -566,19 +537,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             st_shared_u16(row + (uint32_t)((k >> 3) * 128 * 16 + (k & 7) * 2), (poison >> k & 1) ? 0x7E00u : 0xFC00u);
           }
         }
-        tmem_wait_ld_regs(own);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&xo_free);
-        float x[BN];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          const uint4 i4 = *reinterpret_cast<const uint4*>(xi + (c * 128 + h) * 16);
+          const uint4 i4 = *reinterpret_cast<const uint4*>(xi + c * 128 * 16);
           const uint32_t iw[4] = {i4.x, i4.y, i4.z, i4.w};
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            x[8 * c + 2 * q] = add_f16lo(iw[q], add_f16lo(own[4 * c + q], 0.f));
-            x[8 * c + 2 * q + 1] = add_f16hi(iw[q], add_f16hi(own[4 * c + q], 0.f));
+            x[8 * c + 2 * q] = add_f16lo(iw[q], x[8 * c + 2 * q]);
+            x[8 * c + 2 * q + 1] = add_f16hi(iw[q], x[8 * c + 2 * q + 1]);
           }
         }
         // ---- tile maximum (three-input max tree)
@@ -598,12 +564,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         // arrive ordered by that dependency.
         __syncwarp();
         if (lane == 0) mbar_arrive_remote_relaxed_dep(x_free_peer, __float_as_uint(mx));
-        // ---- the reference: handed over by the other group from the tile before; it moves only when the tile's
+        // ---- the reference: handed over by the group of the tile before; it moves only when the tile's
         // maximum exceeds it by more than the threshold (or on the first visible entry)
         float m_ref = -CUDART_INF_F;
         if (t > t0) {
-          if (!mbar_wait_warp(&ref_full[me ^ 1u][quarter], ((tile - 1) >> 1) & 1u, kWaitLimit)) { fail(); break; }
-          m_ref = ref_s[me ^ 1u][h];
+          if (!mbar_wait_warp(&ref_full[before][quarter], (tile - 1) / kGroups & 1u, kWaitLimit)) { fail(); break; }
+          m_ref = ref_s[before][h];
         }
         const bool moved = mx != -CUDART_INF_F && (m_ref == -CUDART_INF_F || mx > m_ref + kRescaleThreshold);
         const float m_new = moved ? mx : m_ref;
@@ -658,7 +624,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (lane == 0) mbar_arrive(&p_full);
       }
       if (aborted()) break;
-      // ---- both groups' sums (their slots are free once every warp has left the segment before)
+      // ---- the next segment's query, as soon as the last scores of this one are read (by the group that will read
+      // its first scores)
+      if (tile % kGroups == me) {
+        const int nn = next_row();
+        if (nn >= 0) {
+          if (!mbar_wait_warp(&s_free[(tile - 1) % kGroups], (tile - 1) / kGroups & 1u, kWaitLimit)) { fail(); break; }
+          tc_fence_after();
+          load_query(nn);
+        }
+      }
+      // ---- the groups' sums (their slots are free once every warp has left the segment before)
       if (seg > 0 && !mbar_wait_warp(&o_free, (seg - 1) & 1u, kWaitLimit)) { fail(); break; }
       sum_s[me][h] = l;
       sum_ref_s[me][h] = m;
@@ -666,10 +642,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (lane == 0) mbar_arrive(&seg_done);
       if (!mbar_wait_warp(&seg_done, seg & 1u, kWaitLimit)) { fail(); break; }
       {
-        const float l2 = sum_s[me ^ 1u][h], m2 = sum_ref_s[me ^ 1u][h];
-        const float top = fmaxf(m, m2);   // the segment's last reference, which O is relative to
-        l = (m == top ? l : m == -CUDART_INF_F ? l : l * ex2_approx(m - top)) +
-            (m2 == top ? l2 : m2 == -CUDART_INF_F ? l2 : l2 * ex2_approx(m2 - top));
+        float top = m;   // the segment's last reference, which O is relative to, is the largest
+#pragma unroll
+        for (uint32_t g = 0; g < kGroups; ++g) top = fmaxf(top, sum_ref_s[g][h]);
+        l = 0.f;
+#pragma unroll
+        for (uint32_t g = 0; g < kGroups; ++g) {
+          const float lg = sum_s[g][h], mg = sum_ref_s[g][h];
+          l += mg == top || mg == -CUDART_INF_F ? lg : lg * ex2_approx(mg - top);   // (without a reference: 0, or NaN)
+        }
         m = top;
       }
       // ---- epilogue: the segment's last P.V, then this group's half of the context
@@ -677,25 +658,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       tc_fence_after();
       const bool blind = kPair && limit_of(n, k_token) == 0;
       if (blind) l = 0.f;
-      const int c0 = (DV / 64) * (int)me;   // of DV / 32 chunks of 32 columns
-      auto drain_o = [&](auto&& store_chunk) {
-        uint32_t oa[32], ob[32];
-        auto blank = [&](uint32_t(&o)[32]) {
-          if (!blind) return;
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0;
-        };
-        tmem_ld32(tmem + TM_O + c0 * 32 + lane_off, oa);
+      auto drain_o = [&](auto&& store_chunk) {   // of DV / 32 chunks of 32 columns, those of this group
 #pragma unroll 1
-        for (int c = c0; c < c0 + DV / 64; c += 2) {
-          tmem_wait_ld_regs(oa);
-          tmem_ld32(tmem + TM_O + (c + 1) * 32 + lane_off, ob);
-          blank(oa);
-          store_chunk(c, oa);
-          tmem_wait_ld_regs(ob);
-          if (c + 2 < c0 + DV / 64) tmem_ld32(tmem + TM_O + (c + 2) * 32 + lane_off, oa);
-          blank(ob);
-          store_chunk(c + 1, ob);
+        for (int c = (int)me; c < DV / 32; c += kGroups) {
+          uint32_t o[32];
+          tmem_ld32(tmem + TM_O + c * 32 + lane_off, o);
+          tmem_wait_ld_regs(o);
+          if (blind) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0;
+          }
+          store_chunk(c, o);
         }
       };
       const int i = (n % a.s_q) * kTokens + k_token;
@@ -757,6 +730,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (lane == 0) mbar_arrive(&o_free);
       ++seg;
     }
+    // Rows without a query score 0; a key that no token sees holds zeros.
+    if (__any_sync(0xffffffffu, !(half_max <= MLA_FP16_SCORE_LIMIT)) && lane == 0 && a.status)
+      atomicOr(a.status, MLA_DEVICE_SCORE_RANGE);
   }
 
   // ---------------------------------------------------------------- teardown

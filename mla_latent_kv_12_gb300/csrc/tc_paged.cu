@@ -28,7 +28,6 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math_constants.h>
-#include <stdlib.h>
 
 #include "mla_internal.h"
 #include "tc_common.cuh"
@@ -57,6 +56,10 @@ constexpr int kLoadWarp = 4 * kGroups, kScoreWarp = kLoadWarp + 1, kPvWarp = kLo
 constexpr int kRegsLaunch = 128;
 constexpr int kRegsSoftmax = 144, kRegsIssue = 72;
 static_assert(kGroups * kRegsSoftmax + kRegsIssue <= (kGroups + 1) * kRegsLaunch, "more registers than the launch has");
+// Up to this many query rows of a batch row go in lockstep, each with a cluster, so that they read a tile at the same
+// time (verify of 8 x 4 tokens of 65536: 396 us, one row at a time 447; 8 trees of 64 nodes behind 8000 to 15000 keys:
+// 1207 us, by two 1237, by eight 1244, alone 1247: eight leave four of 76 clusters idle).
+constexpr int kLockstep = 4;
 // Tiles pulled into L2 ahead of their load: farther for a lockstep group.
 constexpr int kPrefetchAheadGroup = 8, kPrefetchAheadRow = 3;
 
@@ -390,7 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t xin_peer = mapa(smem_u32(xin), peer) + (uint32_t)h * 16u;
     const uint32_t x_full_peer = mapa(smem_u32(&x_full[me]), peer), x_free_peer = mapa(smem_u32(&x_free[me]), peer);
     uint32_t tile = 0, seg = 0, poison_phase = 0, use = 0;   // use: tiles of this group so far
-    float half_max = 0.f;   // largest |half score| sent (checked against the fp16 exchange's range)
+    float half_max = 0.f;   // largest |half score| sent, scaled (checked against the fp16 exchange's range)
     // P.V(k) has completed once its commit arrives on empty_bar[k % STAGES].  Each group waits for one of every
     // kGroups < STAGES at least, and P.V(k + STAGES) cannot have started, so the phase parity identifies the completion.
     auto wait_pv = [&](uint32_t k) -> bool {
@@ -438,26 +441,136 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (member_segment(a, keys_p, u, member, n, t0, t1)) return n;
       return -1;
     };
-    int u, n, t0, t1;
-    bool whole;
-    if (me == 0) {
-      const int first_row = next_row();
-      if (first_row >= 0) load_query(first_row);
-    }
-    while (!aborted() && it.next(u, t0, t1, whole)) {
-      const bool any = member_segment(a, keys_p, u, member, n, t0, t1);
-      const int64_t slot = ((int64_t)u + group) * a.width + member;
-      if (!any) {
+    int u, n = 0, t0, t1;
+    bool whole, live = false;            // live: row n's segment is still in TMEM
+    int64_t slot = 0;
+    float m = -CUDART_INF_F, l = 0.f;    // this group's sum l is relative to 2^m
+    // (One place each for the query and for the epilogue: code that runs once per segment is fetched cold, and behind
+    // a streamed cache from DRAM.  With a second copy of the query load for the first segment, a boundary took 14,000
+    // cycles.)
+    for (;;) {
+      // ---- the coming segment's query, as soon as the last scores of the one before are read (by the group that will
+      // read its first scores)
+      if (tile % kGroups == me) {
+        const int nn = next_row();
+        if (nn >= 0) {
+          if (tile > 0 && !mbar_wait_warp(&s_free[(tile - 1) % kGroups], (tile - 1) / kGroups & 1u, kWaitLimit)) { fail(); break; }
+          tc_fence_after();
+          load_query(nn);
+        }
+      }
+      if (live) {
+        // ---- the groups' sums (their slots are free once every warp has left the segment before)
+        if (seg > 0 && !mbar_wait_warp(&o_free, (seg - 1) & 1u, kWaitLimit)) { fail(); break; }
+        sum_s[me][h] = l;
+        sum_ref_s[me][h] = m;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_done);
+        if (!mbar_wait_warp(&seg_done, seg & 1u, kWaitLimit)) { fail(); break; }
+        {
+          float top = m;   // the segment's last reference, which O is relative to, is the largest
+  #pragma unroll
+          for (uint32_t g = 0; g < kGroups; ++g) top = fmaxf(top, sum_ref_s[g][h]);
+          l = 0.f;
+  #pragma unroll
+          for (uint32_t g = 0; g < kGroups; ++g) {
+            const float lg = sum_s[g][h], mg = sum_ref_s[g][h];
+            l += mg == top || mg == -CUDART_INF_F ? lg : lg * ex2_approx(mg - top);   // (without a reference: 0, or NaN)
+          }
+          m = top;
+        }
+        // ---- epilogue: the segment's last P.V, then this group's half of the context
+        if (!wait_pv(tile - 1)) { fail(); break; }
+        tc_fence_after();
+        const bool blind = kPair && limit_of(n, k_token) == 0;
+        if (blind) l = 0.f;
+        auto drain_o = [&](auto&& store_chunk) {   // of DV / 32 chunks of 32 columns, those of this group
+  #pragma unroll 1
+          for (int c = (int)me; c < DV / 32; c += kGroups) {
+            uint32_t o[32];
+            tmem_ld32(tmem + TM_O + c * 32 + lane_off, o);
+            tmem_wait_ld_regs(o);
+            if (blind) {
+  #pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = 0;
+            }
+            store_chunk(c, o);
+          }
+        };
+        const int i = (n % a.s_q) * kTokens + k_token;
+        const int64_t token = (int64_t)(n / a.s_q) * a.tok_q + i;
+        const float inv = l != 0.f ? 1.f / l : 0.f;   // 0: no entry; NaN stays NaN
+        if (head >= a.heads || i >= a.tok_q) {
+          // a padding row: nothing to store
+        } else if (whole) {
+          const int64_t off = token * a.ctx_row_stride + (int64_t)head * a.ctx_head_stride + dim_base;
+          if (a.out_f32) {
+            drain_o([&](int c, const uint32_t(&o)[32]) {
+              float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.ctx) + off + c * 32);
+  #pragma unroll
+              for (int v = 0; v < 8; ++v)
+                dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
+                                     __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
+            });
+          } else {
+            drain_o([&](int c, const uint32_t(&o)[32]) {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.ctx) + off + c * 32);
+  #pragma unroll
+              for (int v = 0; v < 4; ++v)
+                dst[v] = make_uint4(pack_bf16x2(__uint_as_float(o[8 * v]) * inv, __uint_as_float(o[8 * v + 1]) * inv),
+                                    pack_bf16x2(__uint_as_float(o[8 * v + 2]) * inv, __uint_as_float(o[8 * v + 3]) * inv),
+                                    pack_bf16x2(__uint_as_float(o[8 * v + 4]) * inv, __uint_as_float(o[8 * v + 5]) * inv),
+                                    pack_bf16x2(__uint_as_float(o[8 * v + 6]) * inv, __uint_as_float(o[8 * v + 7]) * inv));
+            });
+          }
+          if (rank == 0 && me == 0 && a.lse)
+            a.lse[token * a.heads + head] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+        } else {
+          // Partial: this piece's context normalised by its own sum in fp16, (m, l) in f32 beside it, kept in L2.
+          const float m_piece = l == 0.f ? -CUDART_INF_F : m == -CUDART_INF_F ? 0.f : m;   // -inf marks an empty one
+          const uint64_t keep = l2_policy_evict_last();
+          uint4* dst = a.ws_o + (slot * (RANK / 8) + dim_base / 8) * HEADS + h;
+          float vmax = 0.f;
+          drain_o([&](int c, const uint32_t(&o)[32]) {
+  #pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t w[4];
+  #pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float x0 = __uint_as_float(o[8 * q + 2 * j]) * inv, x1 = __uint_as_float(o[8 * q + 2 * j + 1]) * inv;
+                vmax = fmaxf(vmax, fmaxf(fabsf(x0), fabsf(x1)));   // beyond 65504 the fp16 value is infinite
+                const __half2 hv = __floats2half2_rn(x0, x1);
+                w[j] = *reinterpret_cast<const uint32_t*>(&hv);
+              }
+              st_global_v4_policy(dst + (int64_t)(4 * c + q) * HEADS, make_uint4(w[0], w[1], w[2], w[3]), keep);
+            }
+          });
+          if (!(vmax <= 65504.f) && a.status) atomicOr(a.status, MLA_DEVICE_VALUE_RANGE);
+          if (rank == 0 && me == 0) {
+            st_global_f32_policy(a.ws_ml + (slot * 2) * HEADS + h, m_piece, keep);
+            st_global_f32_policy(a.ws_ml + (slot * 2 + 1) * HEADS + h, l, keep);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_free);
+        ++seg;
+      }
+      live = false;
+      while (it.next(u, t0, t1, whole)) {
+        slot = ((int64_t)u + group) * a.width + member;
+        live = member_segment(a, keys_p, u, member, n, t0, t1);
+        if (live) break;
         // Nothing of this row in the group's range: an empty partial (weight 0).
         if (!whole && rank == 0 && me == 0 && head < a.heads) {
           a.ws_ml[(slot * 2) * HEADS + h] = -CUDART_INF_F;
           a.ws_ml[(slot * 2 + 1) * HEADS + h] = 0.f;
         }
-        continue;
       }
+      if (!live || aborted()) break;
       const Sight sight = sight_of(n, k_token), other = kPair ? sight_of(n, k_token ^ 1) : sight;
       const int t_pf = t1 - kQueryPrefetchTiles > t0 ? t1 - kQueryPrefetchTiles : t0;
-      float m = -CUDART_INF_F, l = 0.f;   // this group's sum l is relative to 2^m
+      m = -CUDART_INF_F, l = 0.f;
       for (int t = t0; t < t1; ++t, ++tile) {
         if (tile % kGroups != me) continue;
         // A few tiles before this segment ends, the next segment's query row is pulled into L2.
@@ -485,17 +598,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(sa[k]), x[32 + k] = __uint_as_float(sb[k]);
         }
-        // Scores that fp16 cannot hold are rare: the tile's largest magnitude decides once whether they are clamped
-        // (NaN stays NaN).
-        float top = 0.f;
-#pragma unroll
-        for (int k = 0; k < 32; ++k) top = fmax3(top, fabsf(x[k]), fabsf(x[32 + k]));
-        half_max = fmaxf(half_max, top);
-        if (__any_sync(0xffffffffu, !(top * a.scale_log2 < 65504.f))) {
-          const float limit = 65504.f / a.scale_log2;   // (rounds back to 65504 in fp16)
-#pragma unroll
-          for (int k = 0; k < BN; ++k) x[k] = clamp_nan(x[k], limit);
-        }
         // ---- sent to the peer in fp16, once it has read the tile two back
         const uint32_t xb = (tile & 1u) * XH_BYTES;
         if (tile >= 2 && !mbar_wait_warp(&x_free[(tile - 2) % kGroups], (tile - 2) / kGroups & 1u, kWaitLimit)) { fail(); break; }
@@ -507,12 +609,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             const int k = 8 * c + 2 * q;
             const float2 sc = mul_f32x2(make_float2(x[k], x[k + 1]), make_float2(a.scale_log2, a.scale_log2));
             x[k] = sc.x, x[k + 1] = sc.y;
-            const __half2 hv = __floats2half2_rn(sc.x, sc.y);
+            // clamped to +-65504 (NaN stays NaN)
+            const __half2 hv = __hmin2_nan(__hmax2_nan(__floats2half2_rn(sc.x, sc.y), __float2half2_rn(-65504.f)), __float2half2_rn(65504.f));
             w[q] = *reinterpret_cast<const uint32_t*>(&hv);
           }
           st_async_v4(xin_peer + xb + (uint32_t)(c * 128 * 16), w[0], w[1], w[2], w[3], x_full_peer);
         }
         if (h == 0) mbar_arrive_expect_tx(&x_full[me], XH_BYTES);
+        // While the peer's half is on its way: the largest magnitude (scores that fp16 cannot hold are rare: it decides
+        // once whether ours are clamped too), and the reference that the group of the tile before has handed on.
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) top = fmax3(top, fabsf(x[k]), fabsf(x[32 + k]));
+        half_max = fmaxf(half_max, top);
+        if (__any_sync(0xffffffffu, !(top <= 65504.f))) {
+#pragma unroll
+          for (int k = 0; k < BN; ++k) x[k] = clamp_nan(x[k], 65504.f);
+        }
+        float m_ref = -CUDART_INF_F;
+        if (t > t0) {
+          if (!mbar_wait_warp(&ref_full[before][quarter], (tile - 1) / kGroups & 1u, kWaitLimit)) { fail(); break; }
+          m_ref = ref_s[before][h];
+        }
         uint64_t poison = 0;
         if (kPair && (!sight.whole(t) || !other.whole(t)) && (valid ^ seen_of(other, t)) != 0ull) {
           const uint32_t k = tile % kSlots;
@@ -564,13 +682,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         // arrive ordered by that dependency.
         __syncwarp();
         if (lane == 0) mbar_arrive_remote_relaxed_dep(x_free_peer, __float_as_uint(mx));
-        // ---- the reference: handed over by the group of the tile before; it moves only when the tile's
-        // maximum exceeds it by more than the threshold (or on the first visible entry)
-        float m_ref = -CUDART_INF_F;
-        if (t > t0) {
-          if (!mbar_wait_warp(&ref_full[before][quarter], (tile - 1) / kGroups & 1u, kWaitLimit)) { fail(); break; }
-          m_ref = ref_s[before][h];
-        }
+        // ---- the reference moves only when the tile's maximum exceeds it by more than the threshold (or on the first
+        // visible entry)
         const bool moved = mx != -CUDART_INF_F && (m_ref == -CUDART_INF_F || mx > m_ref + kRescaleThreshold);
         const float m_new = moved ? mx : m_ref;
         ref_s[me][h] = m_new;
@@ -624,114 +737,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (lane == 0) mbar_arrive(&p_full);
       }
       if (aborted()) break;
-      // ---- the next segment's query, as soon as the last scores of this one are read (by the group that will read
-      // its first scores)
-      if (tile % kGroups == me) {
-        const int nn = next_row();
-        if (nn >= 0) {
-          if (!mbar_wait_warp(&s_free[(tile - 1) % kGroups], (tile - 1) / kGroups & 1u, kWaitLimit)) { fail(); break; }
-          tc_fence_after();
-          load_query(nn);
-        }
-      }
-      // ---- the groups' sums (their slots are free once every warp has left the segment before)
-      if (seg > 0 && !mbar_wait_warp(&o_free, (seg - 1) & 1u, kWaitLimit)) { fail(); break; }
-      sum_s[me][h] = l;
-      sum_ref_s[me][h] = m;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&seg_done);
-      if (!mbar_wait_warp(&seg_done, seg & 1u, kWaitLimit)) { fail(); break; }
-      {
-        float top = m;   // the segment's last reference, which O is relative to, is the largest
-#pragma unroll
-        for (uint32_t g = 0; g < kGroups; ++g) top = fmaxf(top, sum_ref_s[g][h]);
-        l = 0.f;
-#pragma unroll
-        for (uint32_t g = 0; g < kGroups; ++g) {
-          const float lg = sum_s[g][h], mg = sum_ref_s[g][h];
-          l += mg == top || mg == -CUDART_INF_F ? lg : lg * ex2_approx(mg - top);   // (without a reference: 0, or NaN)
-        }
-        m = top;
-      }
-      // ---- epilogue: the segment's last P.V, then this group's half of the context
-      if (!wait_pv(tile - 1)) { fail(); break; }
-      tc_fence_after();
-      const bool blind = kPair && limit_of(n, k_token) == 0;
-      if (blind) l = 0.f;
-      auto drain_o = [&](auto&& store_chunk) {   // of DV / 32 chunks of 32 columns, those of this group
-#pragma unroll 1
-        for (int c = (int)me; c < DV / 32; c += kGroups) {
-          uint32_t o[32];
-          tmem_ld32(tmem + TM_O + c * 32 + lane_off, o);
-          tmem_wait_ld_regs(o);
-          if (blind) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = 0;
-          }
-          store_chunk(c, o);
-        }
-      };
-      const int i = (n % a.s_q) * kTokens + k_token;
-      const int64_t token = (int64_t)(n / a.s_q) * a.tok_q + i;
-      const float inv = l != 0.f ? 1.f / l : 0.f;   // 0: no entry; NaN stays NaN
-      if (head >= a.heads || i >= a.tok_q) {
-        // a padding row: nothing to store
-      } else if (whole) {
-        const int64_t off = token * a.ctx_row_stride + (int64_t)head * a.ctx_head_stride + dim_base;
-        if (a.out_f32) {
-          drain_o([&](int c, const uint32_t(&o)[32]) {
-            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.ctx) + off + c * 32);
-#pragma unroll
-            for (int v = 0; v < 8; ++v)
-              dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
-                                   __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
-          });
-        } else {
-          drain_o([&](int c, const uint32_t(&o)[32]) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.ctx) + off + c * 32);
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-              dst[v] = make_uint4(pack_bf16x2(__uint_as_float(o[8 * v]) * inv, __uint_as_float(o[8 * v + 1]) * inv),
-                                  pack_bf16x2(__uint_as_float(o[8 * v + 2]) * inv, __uint_as_float(o[8 * v + 3]) * inv),
-                                  pack_bf16x2(__uint_as_float(o[8 * v + 4]) * inv, __uint_as_float(o[8 * v + 5]) * inv),
-                                  pack_bf16x2(__uint_as_float(o[8 * v + 6]) * inv, __uint_as_float(o[8 * v + 7]) * inv));
-          });
-        }
-        if (rank == 0 && me == 0 && a.lse)
-          a.lse[token * a.heads + head] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
-      } else {
-        // Partial: this piece's context normalised by its own sum in fp16, (m, l) in f32 beside it, kept in L2.
-        const float m_piece = l == 0.f ? -CUDART_INF_F : m == -CUDART_INF_F ? 0.f : m;   // -inf marks an empty one
-        const uint64_t keep = l2_policy_evict_last();
-        uint4* dst = a.ws_o + (slot * (RANK / 8) + dim_base / 8) * HEADS + h;
-        float vmax = 0.f;
-        drain_o([&](int c, const uint32_t(&o)[32]) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float x0 = __uint_as_float(o[8 * q + 2 * j]) * inv, x1 = __uint_as_float(o[8 * q + 2 * j + 1]) * inv;
-              vmax = fmaxf(vmax, fmaxf(fabsf(x0), fabsf(x1)));   // beyond 65504 the fp16 value is infinite
-              const __half2 hv = __floats2half2_rn(x0, x1);
-              w[j] = *reinterpret_cast<const uint32_t*>(&hv);
-            }
-            st_global_v4_policy(dst + (int64_t)(4 * c + q) * HEADS, make_uint4(w[0], w[1], w[2], w[3]), keep);
-          }
-        });
-        if (!(vmax <= 65504.f) && a.status) atomicOr(a.status, MLA_DEVICE_VALUE_RANGE);
-        if (rank == 0 && me == 0) {
-          st_global_f32_policy(a.ws_ml + (slot * 2) * HEADS + h, m_piece, keep);
-          st_global_f32_policy(a.ws_ml + (slot * 2 + 1) * HEADS + h, l, keep);
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&o_free);
-      ++seg;
     }
     // Rows without a query score 0; a key that no token sees holds zeros.
-    if (__any_sync(0xffffffffu, !(half_max <= MLA_FP16_SCORE_LIMIT)) && lane == 0 && a.status)
+    if (__any_sync(0xffffffffu, !(half_max <= MLA_FP16_SCORE_LIMIT * a.scale_log2)) && lane == 0 && a.status)
       atomicOr(a.status, MLA_DEVICE_SCORE_RANGE);
   }
 
@@ -778,10 +786,10 @@ cudaError_t launch_tc_paged(const DecodeGeometry& g, int out_dtype, void* worksp
   a.tree = g.tree;
   a.tree_words = g.tree_words;
   a.num_clusters = device_sm_count() / 2;
-  a.width = a.s_q < 8 ? a.s_q : 8;
-  if (const char* w = getenv("MLA_W")) a.width = a.s_q < atoi(w) ? a.s_q : atoi(w);
+  a.width = a.s_q < kLockstep ? a.s_q : kLockstep;
   a.n_units = (a.n_q + a.width - 1) / a.width;
   a.min_tiles = kMinTilesPerGroup;
+  a.start_charge = kUnitStartCharge;
   a.plan_in_kernel = a.n_q <= kMaxRowsInKernelPlan ? 1 : 0;
   a.box_rows = BN;   // the largest box that divides a tile and a page
   while (g.page_size % a.box_rows != 0) a.box_rows >>= 1;

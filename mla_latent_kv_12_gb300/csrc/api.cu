@@ -1139,6 +1139,7 @@ int mla_decode_attend_paged(const void* q, int64_t q_row_stride, int64_t q_head_
                 ctx_row_stride % ovec == 0 && ctx_head_stride % ovec == 0,
             "decode_paged: strides must be multiples of 16 bytes");
   MLA_CHECK((int64_t)batch * s_q <= (1 << 20), "decode_paged: at most 2^20 query rows");
+  MLA_CHECK(q_row_stride > 0 || (int64_t)batch * s_q == 1, "decode_paged: q_row_stride must be positive");
   MLA_CHECK(num_pages == 1 || (latent_page_stride > 0 && rope_page_stride > 0),
             "decode_paged: page strides must be positive");
   if (selected_positions || page_size % 8 != 0) {

@@ -44,6 +44,10 @@ constexpr int STAGES = 5;
 constexpr int GROUP_BYTES = 4 * 1024;
 constexpr int LATENT_BYTES = 8 * GROUP_BYTES;
 constexpr int STAGE_BYTES = LATENT_BYTES + BN * 64;
+// The query of a segment comes through the ring ahead of its tiles, as two fills: latent chunks 0, 1 and 2, 3 of 64
+// dims, each [128 rows x 128 bytes] (128-byte swizzle), with the rope dims of rows 0..63 and 64..127 (64-byte swizzle).
+constexpr int QCHUNK_BYTES = 128 * 128;
+static_assert(2 * QCHUNK_BYTES == LATENT_BYTES, "two query chunks take a stage's place");
 constexpr int XH_BYTES = 128 * BN * 2;    // fp16 partial scores of one tile
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 2 * XH_BYTES;
 constexpr uint32_t TM_O = 0, TM_Q = 256, TM_S = 400, TM_P = 464;  // TMEM columns (Q: 128 + 16)
@@ -86,6 +90,7 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t w, bool& found) {
 template <int kPrefetchAhead, bool kPair>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tc_paged_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_constant__ CUtensorMap rope_map,
+                    const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap qrope_map,
                     const __grid_constant__ TcDecodeArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if ((smem_u32(smem_raw) & 1023u) != 0) {   // the same in every CTA: nothing waits on anything yet
@@ -121,6 +126,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&lat_map);
     tma_prefetch_desc(&rope_map);
+    tma_prefetch_desc(&q_map);
+    tma_prefetch_desc(&qrope_map);
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full_bar[s], 1);
       mbar_init(&empty_bar[s], 1);
@@ -199,6 +206,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       int stage = 0;
       uint32_t phase = 0;
       int fills = 0;   // the ring's first STAGES fills need no free slot
+      int tiles = 0;
+      auto wait_empty = [&]() { return fills < STAGES || mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit); };
+      auto next_stage = [&]() {
+        ++fills;
+        if (++stage == STAGES) stage = 0, phase ^= 1u;
+      };
       const int boxes = BN / a.box_rows;   // 1, 2, 4 or 8 of a tile, one per lane
       const int groups = a.box_rows >> 3;
       int u, n, t0, t1;
@@ -240,6 +253,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
           __syncwarp();
         };
+        // the query: MMA rows 0..63 and 64..127 are heads 0.. and 64.. of a token, or two tokens (heads or a token that
+        // are not there read as zeros: no such coordinate in the map)
+        if (loads) {
+          const int b = n / a.s_q, i = (n % a.s_q) * kTokens, token = b * a.tok_q + i;
+          const int head2 = kPair ? 0 : 64, token2 = !kPair ? token : i + 1 < a.tok_q ? token + 1 : a.n_tokens;
+          for (int half = 0; half < 2; ++half) {
+            if (!wait_empty()) { fail(); break; }
+            if (lane == 0) {
+              uint8_t* dst = stages + stage * STAGE_BYTES;
+              mbar_arrive_expect_tx(&full_bar[stage], STAGE_BYTES);
+              for (int c = 0; c < 2; ++c) {
+                tma_load_3d(dst + c * QCHUNK_BYTES, &q_map, &full_bar[stage], dim_base + 64 * (2 * half + c), 0, token);
+                tma_load_3d(dst + c * QCHUNK_BYTES + 64 * 128, &q_map, &full_bar[stage], dim_base + 64 * (2 * half + c), head2, token2);
+              }
+              tma_load_3d(dst + LATENT_BYTES, &qrope_map, &full_bar[stage], RANK + 32 * (int)rank, half ? head2 : 0, half ? token2 : token);
+            }
+            __syncwarp();
+            next_stage();
+          }
+          if (aborted()) break;
+        }
         // the segment's first tiles that the loop's look-ahead will not cover
         if (!loads)
           for (int t = t0 + STAGES; t < t0 + kPrefetchAhead && t < t1; ++t) prefetch_tile(t);
@@ -248,7 +282,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             int pg, rw;
             box_of(t, pg, rw);
             const uint32_t there = __ballot_sync(0xffffffffu, pg >= 0);
-            if (fills >= STAGES && !mbar_wait_warp(&empty_bar[stage], phase ^ 1u, kWaitLimit)) { fail(); break; }
+            if (!wait_empty()) { fail(); break; }
             if (lane == 0) mbar_arrive_expect_tx(&full_bar[stage], __popc(there) * a.box_rows * (STAGE_BYTES / BN));
             __syncwarp();
             if (pg >= 0) {
@@ -257,17 +291,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               tma_load_3d(dst + LATENT_BYTES + lane * a.box_rows * 64, &rope_map, &full_bar[stage], 32 * (int)rank, rw, pg);
             }
             __syncwarp();
-            if (lane == 0) loaded_s = fills + 1;
+            next_stage();
+            if (lane == 0) loaded_s = tiles + 1;
           } else {
             // with the loads of tile t, or at once if those are farther already (a counter, not the stage's barrier: a
             // late reader of a barrier's parity could miss a phase)
             const long long begin = clock64();
-            while (loaded_s <= fills && !abort_s && clock64() - begin < kWaitLimit) __nanosleep(100);
+            while (loaded_s <= tiles && !abort_s && clock64() - begin < kWaitLimit) __nanosleep(100);
             __syncwarp();
             if (t + kPrefetchAhead < t1) prefetch_tile(t + kPrefetchAhead);
+            if (t == (t1 - kQueryPrefetchTiles > t0 ? t1 - kQueryPrefetchTiles : t0) && lane == 0) {
+              // the next segment's query
+              WorkIter peek = it;
+              int un, nn, tn0, tn1;
+              bool wn;
+              while (peek.next(un, tn0, tn1, wn)) {
+                if (!member_segment(a, keys_p, un, member, nn, tn0, tn1)) continue;
+                const int i = (nn % a.s_q) * kTokens, token = (nn / a.s_q) * a.tok_q + i;
+                const int head2 = kPair ? 0 : 64, token2 = kPair ? token + 1 : token;
+                for (int c = 0; c < 4; ++c) {
+                  tma_prefetch_l2_3d(&q_map, dim_base + 64 * c, 0, token);
+                  if (kPair ? i + 1 < a.tok_q : a.heads > 64) tma_prefetch_l2_3d(&q_map, dim_base + 64 * c, head2, token2);
+                }
+                break;
+              }
+            }
+            __syncwarp();
           }
-          ++fills;
-          if (++stage == STAGES) stage = 0, phase ^= 1u;
+          ++tiles;
         }
       }
       // Drain: every issued fill must land before this CTA may exit.
@@ -284,6 +335,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
         const Sight s0 = sight_of(n, 0), s1 = kPair ? sight_of(n, 1) : s0;
         if (!mbar_wait_warp(&q_full, seg & 1u, kWaitLimit)) { fail(); break; }
+        for (int half = 0; half < 2; ++half) {   // the query is in TMEM: its two stages are free
+          if (lane == 0) mbar_arrive(&empty_bar[stage]);
+          if (++stage == STAGES) stage = 0, phase ^= 1u;
+        }
         for (int t = t0; t < t1; ++t) {
           const uint64_t seen0 = seen_of(s0, t), seen1 = kPair ? seen_of(s1, t) : seen0;
           if (!mbar_wait_warp(&full_bar[stage], phase, kWaitLimit)) { fail(); break; }
@@ -355,6 +410,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       bool whole;
       while (!aborted() && it.next(u, t0, t1, whole)) {
         if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
+        stage = (stage + 2) % STAGES;   // behind the query's
         for (int t = t0; t < t1; ++t) {
           const bool first = (t == t0);
           // O is overwritten by a segment's first P.V: the previous segment's epilogue must have read it.
@@ -394,43 +450,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t x_full_peer = mapa(smem_u32(&x_full[me]), peer), x_free_peer = mapa(smem_u32(&x_free[me]), peer);
     uint32_t tile = 0, seg = 0, poison_phase = 0, use = 0;   // use: tiles of this group so far
     float half_max = 0.f;   // largest |half score| sent, scaled (checked against the fp16 exchange's range)
-    // P.V(k) has completed once its commit arrives on empty_bar[k % STAGES].  Each group waits for one of every
-    // kGroups < STAGES at least, and P.V(k + STAGES) cannot have started, so the phase parity identifies the completion.
+    // P.V(k) of the current segment has completed once its commit arrives on the barrier of its stage: fill k + 2 (seg +
+    // 1), two per segment up to this one being queries.  The phase parity identifies the completion: the fill STAGES
+    // before has been freed when this is called (this group has waited for a P.V at most kGroups tiles back, and read
+    // scores behind this segment's query), and the fill STAGES behind cannot have been: it is a tile of this segment behind
+    // the P.V that the caller is yet to allow, or lies behind the epilogue of this segment, which a later segment's
+    // P.V's and the one after the next's query wait for.
     auto wait_pv = [&](uint32_t k) -> bool {
-      return mbar_wait_warp(&empty_bar[k % STAGES], (k / STAGES) & 1u, kWaitLimit);
+      const uint32_t f = k + 2 * (seg + 1);
+      return mbar_wait_warp(&empty_bar[f % STAGES], (f / STAGES) & 1u, kWaitLimit);
     };
-    // This MMA row's query of row n, or null (padding, or a token that the batch row does not have).
-    auto query_of = [&](int n) -> const __nv_bfloat16* {
-      const int b = n / a.s_q, i = (n % a.s_q) * kTokens + k_token;
-      if (i >= a.tok_q || head >= a.heads) return nullptr;
-      return a.q + ((int64_t)b * a.tok_q + i) * a.q_row_stride + (int64_t)head * a.q_head_stride + dim_base;
-    };
-    auto load_query = [&](int n) {
-      const __nv_bfloat16* qrow = query_of(n);
-      uint4 qv[36];   // all 36 loads in flight at once: 256 latent dims, then the 32 rope dims
-      const uint4* qlat = reinterpret_cast<const uint4*>(qrow);
-      const uint4* qrope = qlat + (RANK - dim_base + 32 * (int)rank) / 8;
+    // The coming segment's query from its two stages (fills f, f + 1) into TMEM.
+    auto take_query = [&](uint32_t f) -> bool {
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half, ++f) {
+        if (!mbar_wait_warp(&full_bar[f % STAGES], (f / STAGES) & 1u, kWaitLimit)) return false;
+        const uint8_t* st = stages + (f % STAGES) * STAGE_BYTES;
 #pragma unroll
-      for (int v = 0; v < 32; ++v) qv[v] = qrow ? __ldg(qlat + v) : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < 2; ++c) {
+          uint32_t r[32];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) qv[32 + v] = qrow ? __ldg(qrope + v) : make_uint4(0, 0, 0, 0);
+          for (int v = 0; v < 8; ++v) {
+            const uint4 w = *reinterpret_cast<const uint4*>(st + c * QCHUNK_BYTES + h * 128 + ((v ^ (h & 7)) << 4));
+            r[4 * v] = w.x, r[4 * v + 1] = w.y, r[4 * v + 2] = w.z, r[4 * v + 3] = w.w;
+          }
+          tmem_st32(tmem + TM_Q + (2 * half + c) * 32 + lane_off, r);
+        }
+        if (h >> 6 == half) {   // (whole warps)
+          uint32_t r[16];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t r[32];
-#pragma unroll
-        for (int v = 0; v < 8; ++v)
-          r[4 * v] = qv[8 * c + v].x, r[4 * v + 1] = qv[8 * c + v].y, r[4 * v + 2] = qv[8 * c + v].z, r[4 * v + 3] = qv[8 * c + v].w;
-        tmem_st32(tmem + TM_Q + c * 32 + lane_off, r);
+          for (int v = 0; v < 4; ++v) {
+            const uint4 w = *reinterpret_cast<const uint4*>(st + LATENT_BYTES + (h & 63) * 64 + ((v ^ ((h >> 1) & 3)) << 4));
+            r[4 * v] = w.x, r[4 * v + 1] = w.y, r[4 * v + 2] = w.z, r[4 * v + 3] = w.w;
+          }
+          tmem_st16(tmem + TM_Q + 128 + lane_off, r);
+        }
       }
-      uint32_t r[16];
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        r[4 * v] = qv[32 + v].x, r[4 * v + 1] = qv[32 + v].y, r[4 * v + 2] = qv[32 + v].z, r[4 * v + 3] = qv[32 + v].w;
-      tmem_st16(tmem + TM_Q + 128 + lane_off, r);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full);
+      return true;
     };
     // This member's next segment behind `it`, or -1.
     auto next_row = [&]() {
@@ -452,11 +512,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       // ---- the coming segment's query, as soon as the last scores of the one before are read (by the group that will
       // read its first scores)
       if (tile % kGroups == me) {
-        const int nn = next_row();
-        if (nn >= 0) {
+        if (next_row() >= 0) {
           if (tile > 0 && !mbar_wait_warp(&s_free[(tile - 1) % kGroups], (tile - 1) / kGroups & 1u, kWaitLimit)) { fail(); break; }
+          // (and every group has left the segment before this one: its waits on the stages' barriers are over)
+          if (seg > 0 && !mbar_wait_warp(&o_free, (seg - 1) & 1u, kWaitLimit)) { fail(); break; }
           tc_fence_after();
-          load_query(nn);
+          if (!take_query(tile + 2 * (live ? seg + 1 : 0))) { fail(); break; }
         }
       }
       if (live) {
@@ -569,19 +630,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
       if (!live || aborted()) break;
       const Sight sight = sight_of(n, k_token), other = kPair ? sight_of(n, k_token ^ 1) : sight;
-      const int t_pf = t1 - kQueryPrefetchTiles > t0 ? t1 - kQueryPrefetchTiles : t0;
       m = -CUDART_INF_F, l = 0.f;
       for (int t = t0; t < t1; ++t, ++tile) {
         if (tile % kGroups != me) continue;
-        // A few tiles before this segment ends, the next segment's query row is pulled into L2.
-        if (t >= t_pf && t < t_pf + (int)kGroups) {
-          const int nn = next_row();
-          if (const __nv_bfloat16* qnext = nn >= 0 ? query_of(nn) : nullptr) {
-#pragma unroll
-            for (int l4 = 0; l4 < 4; ++l4) prefetch_l2(qnext + 64 * l4);
-            prefetch_l2(qnext + RANK - dim_base + 32 * (int)rank);
-          }
-        }
         const uint64_t valid = seen_of(sight, t);
         // ---- this CTA's partial scores, in f32 and log2 units
         if (!mbar_wait_warp(&s_full[me], use & 1u, kWaitLimit)) { fail(); break; }
@@ -713,8 +764,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         ps2[4] = add_f32x2(add_f32x2(ps2[4], ps2[5]), add_f32x2(ps2[6], ps2[7]));
         ps2[0] = add_f32x2(ps2[0], ps2[4]);
         l += ps2[0].x + ps2[0].y;
-        // ---- P into TMEM once the previous P.V has consumed it (and O is stable)
-        if (tile > 0 && !wait_pv(tile - 1)) { fail(); break; }
+        // ---- P into TMEM once the previous P.V has consumed it (and O is stable; the last of a segment has been waited
+        // for in its epilogue)
+        if (t > t0 && !wait_pv(tile - 1)) { fail(); break; }
         tc_fence_after();
         // tcgen05.ld / st are warp-collective: the whole warp takes the
         // rescale pass when any of its rows needs it, the others with factor 1.
@@ -769,6 +821,7 @@ cudaError_t launch_tc_paged(const DecodeGeometry& g, int out_dtype, void* worksp
   a.tokens = g.heads == 64 && g.s_q > 1 ? 2 : 1;
   a.s_q = (g.s_q + a.tokens - 1) / a.tokens;
   a.n_q = g.batch * a.s_q;
+  a.n_tokens = g.batch * g.s_q;
   a.heads = g.heads;
   a.scale_log2 = g.scale_log2;
   a.ctx = g.ctx_out;
@@ -796,7 +849,7 @@ cudaError_t launch_tc_paged(const DecodeGeometry& g, int out_dtype, void* worksp
   if (a.box_rows < 8) return cudaErrorInvalidValue;
   lay_out_workspace(a, workspace);
 
-  CUtensorMap lat_map, rope_map;
+  CUtensorMap lat_map, rope_map, q_map, qrope_map;
   {
     const uint64_t row = (uint64_t)g.latent_row_stride * 2;
     const uint64_t page = g.num_pages > 1 ? (uint64_t)g.latent_page_stride * 2 : row * g.page_size;   // (one page: no stride)
@@ -812,6 +865,15 @@ cudaError_t launch_tc_paged(const DecodeGeometry& g, int out_dtype, void* worksp
     const uint64_t strides[2] = {row, page};
     const uint32_t box[3] = {32, (uint32_t)a.box_rows, 1};
     if (!encode_tmap_bf16(&rope_map, g.rope, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B)) return cudaErrorInvalidValue;
+  }
+  {
+    const uint64_t row = a.n_tokens > 1 ? (uint64_t)g.q_row_stride * 2 : (uint64_t)g.q_head_stride * 2 * g.heads;
+    const uint64_t dims[3] = {(uint64_t)(g.rank + g.rope_dim), (uint64_t)g.heads, (uint64_t)a.n_tokens};
+    const uint64_t strides[2] = {(uint64_t)g.q_head_stride * 2, row};
+    const uint32_t box[3] = {64, 64, 1}, rbox[3] = {32, 64, 1};
+    if (!encode_tmap_bf16(&q_map, g.q, 3, dims, strides, box) ||
+        !encode_tmap_bf16(&qrope_map, g.q, 3, dims, strides, rbox, CU_TENSOR_MAP_SWIZZLE_64B))
+      return cudaErrorInvalidValue;
   }
   const bool lockstep = a.width > 1;
   auto* const kernel = a.tokens == 2 ? (lockstep ? tc_paged_kernel<kPrefetchAheadGroup, true> : tc_paged_kernel<kPrefetchAheadRow, true>)
@@ -832,7 +894,7 @@ cudaError_t launch_tc_paged(const DecodeGeometry& g, int out_dtype, void* worksp
     if (ea != cudaSuccess) return ea;
   }
   cudaError_t e = a.plan_in_kernel ? cudaSuccess : launch_split_plan(a, stream);
-  if (e == cudaSuccess) e = launch_pdl(kernel, dim3(2 * a.num_clusters), dim3(THREADS), SMEM_BYTES, stream, lat_map, rope_map, a);
+  if (e == cudaSuccess) e = launch_pdl(kernel, dim3(2 * a.num_clusters), dim3(THREADS), SMEM_BYTES, stream, lat_map, rope_map, q_map, qrope_map, a);
   if (e == cudaSuccess) e = launch_split_combine(a, stream);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -44,8 +44,8 @@ struct TcDecodeArgs {
   const int32_t* kv_len;
   int32_t s_q, n_q;    // query rows: of a batch row, in all
   int32_t heads;       // 64 or 128; rows h >= heads of the MMA's M side are zero padding (or another token's)
-  // Tokens of a query row (2: two tokens of 64 heads share the MMA's 128 rows) and of a batch row.
-  int32_t tokens, tok_q;
+  // Tokens of a query row (2: two tokens of 64 heads share the MMA's 128 rows), of a batch row and in all.
+  int32_t tokens, tok_q, n_tokens;
   const int32_t* sel;
   const int32_t* sel_count;
   int32_t k_max;

@@ -345,21 +345,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if ((seen0 & seen1) != ~0ull) {
             const uint64_t any = seen0 | seen1, one = seen0 ^ seen1;
             uint8_t* st = stages + stage * STAGE_BYTES;
+            // Lane l takes rows l and 32 + l, their pieces of 16 bytes in an order without bank conflicts.
             uint64_t poison = 0;
 #pragma unroll 1
-            for (int i = lane; i < BN * 36; i += 32) {
-              const int r = i / 36, v = i - 36 * r;
-              uint4* at = reinterpret_cast<uint4*>(st + (v < 32 ? (r >> 3) * GROUP_BYTES + (v >> 3) * 1024 + (r & 7) * 128 + (v & 7) * 16
-                                                                : LATENT_BYTES + r * 64 + (v - 32) * 16));
-              if (!(any >> r & 1)) {
-                *at = make_uint4(0, 0, 0, 0);
-              } else if (kPair && (one >> r & 1)) {
-                uint4 w = *at;
-                bool found = false;
-                w = make_uint4(finite_pair(w.x, found), finite_pair(w.y, found), finite_pair(w.z, found), finite_pair(w.w, found));
-                if (found) *at = w, poison |= 1ull << r;
+            for (int r = lane; r < BN; r += 32) {
+              const bool clear = !(any >> r & 1), check = kPair && (one >> r & 1);
+              if (!clear && !check) continue;
+              uint8_t* lat = st + (r >> 3) * GROUP_BYTES + (r & 7) * 128;
+              uint8_t* rope = st + LATENT_BYTES + r * 64;
+              bool bad = false;
+#pragma unroll 4
+              for (int v = 0; v < 36; ++v) {
+                uint4* at = reinterpret_cast<uint4*>(v < 32 ? lat + (v >> 3) * 1024 + (((v ^ r) & 7) << 4)
+                                                            : rope + (((v ^ (r >> 1)) & 3) << 4));
+                if (clear) {
+                  *at = make_uint4(0, 0, 0, 0);
+                } else if (kPair) {
+                  uint4 w = *at;
+                  bool found = false;
+                  w = make_uint4(finite_pair(w.x, found), finite_pair(w.y, found), finite_pair(w.z, found), finite_pair(w.w, found));
+                  if (found) *at = w, bad = true;
+                }
               }
+              if (bad) poison |= 1ull << r;
             }
+            __syncwarp();
             fence_proxy_async_smem();
             __syncwarp();
             if (kPair && one != 0ull) {
@@ -693,17 +703,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (!mbar_wait_warp(&x_full[me], use & 1u, kWaitLimit)) { fail(); break; }
         ++use;
         const uint8_t* const xi = xin + xb + h * 16;
-        if (valid != ~0ull || poison != 0ull) {
-          // Keys that this token does not see: the peer's half becomes fp16 -inf, so that the score is -inf whatever
-          // our own (finite) half; a seen key that is not finite: NaN.  A rolled loop with computed addresses: it
-          // runs at a row's last tiles only.
+        if (kPair && poison != 0ull) {   // a key that is not finite, and that the other token does not see: NaN
           const uint32_t row = smem_u32(xi);
-          uint64_t inv = ~valid | poison;
 #pragma unroll 1
-          while (inv != 0ull) {
-            const int k = __ffsll((long long)inv) - 1;
-            inv &= inv - 1ull;
-            st_shared_u16(row + (uint32_t)((k >> 3) * 128 * 16 + (k & 7) * 2), (poison >> k & 1) ? 0x7E00u : 0xFC00u);
+          for (uint64_t left = poison; left != 0ull; left &= left - 1ull) {
+            const int k = __ffsll((long long)left) - 1;
+            st_shared_u16(row + (uint32_t)((k >> 3) * 128 * 16 + (k & 7) * 2), 0x7E00u);
           }
         }
 #pragma unroll
@@ -714,6 +719,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           for (int q = 0; q < 4; ++q) {
             x[8 * c + 2 * q] = add_f16lo(iw[q], x[8 * c + 2 * q]);
             x[8 * c + 2 * q + 1] = add_f16hi(iw[q], x[8 * c + 2 * q + 1]);
+          }
+        }
+        if (valid != ~0ull) {   // (a rolled loop over the keys that are not seen, in shared memory, took 130 cycles for each)
+          const uint32_t lo = (uint32_t)valid, hi = (uint32_t)(valid >> 32);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            x[k] = lo >> k & 1u ? x[k] : -CUDART_INF_F;
+            x[32 + k] = hi >> k & 1u ? x[32 + k] : -CUDART_INF_F;
           }
         }
         // ---- tile maximum (three-input max tree)

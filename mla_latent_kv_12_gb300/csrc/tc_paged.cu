@@ -58,8 +58,11 @@ constexpr int THREADS = 128 * (kGroups + 1);
 constexpr int kLoadWarp = 4 * kGroups, kScoreWarp = kLoadWarp + 1, kPvWarp = kLoadWarp + 2, kPrefetchWarp = kLoadWarp + 3;
 // Registers per thread of each warpgroup; their sum fits the launch's.
 constexpr int kRegsLaunch = 128;
-constexpr int kRegsSoftmax = 144, kRegsIssue = 72;
-static_assert(kGroups * kRegsSoftmax + kRegsIssue <= (kGroups + 1) * kRegsLaunch, "more registers than the launch has");
+__host__ __device__ constexpr int regs_softmax(bool pair) { return pair ? 136 : 152; }
+__host__ __device__ constexpr int regs_issue(bool pair) { return pair ? 104 : 56; }
+static_assert(kGroups * regs_softmax(false) + regs_issue(false) <= (kGroups + 1) * kRegsLaunch &&
+                  kGroups * regs_softmax(true) + regs_issue(true) <= (kGroups + 1) * kRegsLaunch,
+              "more registers than the launch has");
 // Up to this many query rows of a batch row go in lockstep, each with a cluster, so that they read a tile at the same
 // time (verify of 8 x 4 tokens of 65536: 396 us, one row at a time 447; 8 trees of 64 nodes behind 8000 to 15000 keys:
 // 1207 us, by two 1237, by eight 1244, alone 1247: eight leave four of 76 clusters idle).
@@ -175,31 +178,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     abort_s = 1;
     if (a.status) atomicOr(a.status, MLA_DEVICE_TIMEOUT);
   };
-  // What token k of query row n sees: keys [0, limit), in a tree from `first` on by its mask.
-  struct Sight {
-    int limit, first;
-    const uint64_t* mask;
-    __device__ bool whole(int t) const { return (t + 1) * BN <= min(limit, first); }
-  };
-  // A token that sees nothing beside one that does is scored like that one (and its result dropped).
+  // What token k of query row n sees: keys [0, limit), in a tree from `first` on by its mask.  A token that sees nothing
+  // beside one that does is scored like that one (and its result dropped).
   auto limit_of = [&](int n, int k) {
     return a.plan_in_kernel ? limit_s[kTokens * n + k] : token_limit(a, n / a.s_q, (n % a.s_q) * kTokens + k);
   };
-  auto sight_of = [&](int n, int k) {
-    Sight s;
-    s.limit = limit_of(n, k);
-    if (kPair && s.limit == 0) s.limit = limit_of(n, k ^= 1);
+  auto seen_of = [&](int n, int k, int t) -> uint64_t {   // of the keys of tile t
+    int limit = limit_of(n, k);
+    if (kPair && limit == 0) limit = limit_of(n, k ^= 1);
     const int b = n / a.s_q, i = (n % a.s_q) * kTokens + k;
-    s.mask = i < a.tok_q ? tree_of(a, b * a.tok_q + i) : nullptr;
+    const uint64_t* mask = i < a.tok_q ? tree_of(a, b * a.tok_q + i) : nullptr;
+    return paged_seen(t * BN, limit, !mask ? limit : a.plan_in_kernel ? row_first_s[n] : paged_first(a, b), mask, a.tree_words);
+  };
+  // One token per row: what it sees, kept in registers (looked up again in a row's last tiles, as with two tokens, the
+  // loop over the tiles came out 5 % slower; kept for two tokens, 10 %).
+  struct Sight {
+    int limit, first;
+    const uint64_t* mask;
+  };
+  auto sight_of = [&](int n) {
+    const int b = n / a.s_q;
+    Sight s;
+    s.limit = limit_of(n, 0);
+    s.mask = tree_of(a, b * a.tok_q + n % a.s_q);
     s.first = !s.mask ? s.limit : a.plan_in_kernel ? row_first_s[n] : paged_first(a, b);
     return s;
   };
-  auto seen_of = [&](const Sight& s, int t) {
-    return s.whole(t) ? ~0ull : paged_seen(t * BN, s.limit, s.first, s.mask, a.tree_words);
+  auto seen_of_one = [&](const Sight& s, int t) {
+    return (t + 1) * BN <= min(s.limit, s.first) ? ~0ull : paged_seen(t * BN, s.limit, s.first, s.mask, a.tree_words);
+  };
+  // Two tokens: the first tiles of row n, which both see in whole.
+  auto whole_of = [&](int n) {
+    const int keys0 = limit_of(n, 0), keys1 = limit_of(n, 1);
+    int keys = keys0 == 0 ? keys1 : keys1 == 0 ? keys0 : min(keys0, keys1);
+    if (a.tree) keys = min(keys, a.plan_in_kernel ? row_first_s[n] : paged_first(a, n / a.s_q));
+    return max(keys, 0) / BN;
   };
 
   if (warp >= kLoadWarp) {
-    reg_dealloc<kRegsIssue>();
+    reg_dealloc<regs_issue(kPair)>();
     if (warp == kLoadWarp || warp == kPrefetchWarp) {
       // ============================================================ loads, and L2 prefetch a few tiles ahead of them
       const bool loads = warp == kLoadWarp;
@@ -333,41 +350,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       bool whole;
       while (!aborted() && it.next(u, t0, t1, whole)) {
         if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
-        const Sight s0 = sight_of(n, 0), s1 = kPair ? sight_of(n, 1) : s0;
+        const Sight sight = kPair ? Sight{} : sight_of(n);
+        const int whole_tiles = kPair ? whole_of(n) : 0;
         if (!mbar_wait_warp(&q_full, seg & 1u, kWaitLimit)) { fail(); break; }
         for (int half = 0; half < 2; ++half) {   // the query is in TMEM: its two stages are free
           if (lane == 0) mbar_arrive(&empty_bar[stage]);
           if (++stage == STAGES) stage = 0, phase ^= 1u;
         }
         for (int t = t0; t < t1; ++t) {
-          const uint64_t seen0 = seen_of(s0, t), seen1 = kPair ? seen_of(s1, t) : seen0;
+          uint64_t seen0 = ~0ull, seen1 = ~0ull;
+          if constexpr (kPair) {
+            if (t >= whole_tiles) seen0 = seen_of(n, 0, t), seen1 = seen_of(n, 1, t);
+          } else {
+            seen0 = seen1 = seen_of_one(sight, t);
+          }
           if (!mbar_wait_warp(&full_bar[stage], phase, kWaitLimit)) { fail(); break; }
           if ((seen0 & seen1) != ~0ull) {
             const uint64_t any = seen0 | seen1, one = seen0 ^ seen1;
             uint8_t* st = stages + stage * STAGE_BYTES;
-            // Lane l takes rows l and 32 + l, their pieces of 16 bytes in an order without bank conflicts.
-            uint64_t poison = 0;
+            // Rows that nobody sees: lane l clears rows l and 32 + l, their pieces of 16 bytes in an order without bank
+            // conflicts.
 #pragma unroll 1
             for (int r = lane; r < BN; r += 32) {
-              const bool clear = !(any >> r & 1), check = kPair && (one >> r & 1);
-              if (!clear && !check) continue;
+              if (any >> r & 1) continue;
               uint8_t* lat = st + (r >> 3) * GROUP_BYTES + (r & 7) * 128;
               uint8_t* rope = st + LATENT_BYTES + r * 64;
-              bool bad = false;
 #pragma unroll 4
-              for (int v = 0; v < 36; ++v) {
-                uint4* at = reinterpret_cast<uint4*>(v < 32 ? lat + (v >> 3) * 1024 + (((v ^ r) & 7) << 4)
-                                                            : rope + (((v ^ (r >> 1)) & 3) << 4));
-                if (clear) {
-                  *at = make_uint4(0, 0, 0, 0);
-                } else if (kPair) {
-                  uint4 w = *at;
+              for (int v = 0; v < 32; ++v) *reinterpret_cast<uint4*>(lat + (v >> 3) * 1024 + (((v ^ r) & 7) << 4)) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+              for (int v = 0; v < 4; ++v) *reinterpret_cast<uint4*>(rope + (((v ^ (r >> 1)) & 3) << 4)) = make_uint4(0, 0, 0, 0);
+            }
+            // Rows that one token sees, two at a time: lane l looks at piece l of the latents, and l % 4 of the rope dims
+            // of the first (lanes 0..3) or second.
+            uint64_t poison = 0;
+            if constexpr (kPair) {
+#pragma unroll 1
+              for (uint64_t left = one; left != 0ull;) {
+                const int r0 = __ffsll((long long)left) - 1;
+                left &= left - 1ull;
+                const int r1 = left ? __ffsll((long long)left) - 1 : r0;
+                left &= left - (left != 0ull);
+                const uint32_t lat = smem_u32(st) + (lane >> 3) * 1024 + (lane & 7) * 16;
+                const uint32_t at0 = lat + (r0 >> 3) * GROUP_BYTES + (r0 & 7) * 128, at1 = lat + (r1 >> 3) * GROUP_BYTES + (r1 & 7) * 128;
+                const int rr = lane & 4 ? r1 : r0;
+                const uint32_t at2 = smem_u32(st) + LATENT_BYTES + rr * 64 + (lane & 3) * 16;
+                uint4 w0 = ld_shared_16(at0), w1 = ld_shared_16(at1), w2 = ld_shared_16(at2);
+                auto fix = [&](uint32_t at, uint4 w, int r) {
                   bool found = false;
                   w = make_uint4(finite_pair(w.x, found), finite_pair(w.y, found), finite_pair(w.z, found), finite_pair(w.w, found));
-                  if (found) *at = w, bad = true;
-                }
+                  if (!found) return;
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+                  poison |= 1ull << r;
+                };
+                fix(at0, w0, r0);
+                fix(at1, w1, r1);
+                fix(at2, w2, rr);
               }
-              if (bad) poison |= 1ull << r;
             }
             __syncwarp();
             fence_proxy_async_smem();
@@ -449,7 +487,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   } else {
     // ============================================================ exchange, softmax, epilogue
-    reg_alloc<kRegsSoftmax>();
+    reg_alloc<regs_softmax(kPair)>();
     const int quarter = warp & 3;
     const uint32_t me = warp >> 2;                        // this group takes the tiles me, me + kGroups, ...
     const int h = 32 * quarter + lane;                    // MMA row = TMEM lane
@@ -639,11 +677,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
       }
       if (!live || aborted()) break;
-      const Sight sight = sight_of(n, k_token), other = kPair ? sight_of(n, k_token ^ 1) : sight;
+      const Sight sight = kPair ? Sight{} : sight_of(n);
+      const int whole_tiles = kPair ? whole_of(n) : 0;
       m = -CUDART_INF_F, l = 0.f;
       for (int t = t0; t < t1; ++t, ++tile) {
         if (tile % kGroups != me) continue;
-        const uint64_t valid = seen_of(sight, t);
+        uint64_t valid = ~0ull;
+        bool one = false;   // kPair: a key that one of the two tokens sees
+        if constexpr (kPair) {
+          if (t >= whole_tiles) {
+            valid = seen_of(n, k_token, t);
+            one = valid != seen_of(n, k_token ^ 1, t);
+          }
+        } else {
+          valid = seen_of_one(sight, t);
+        }
         // ---- this CTA's partial scores, in f32 and log2 units
         if (!mbar_wait_warp(&s_full[me], use & 1u, kWaitLimit)) { fail(); break; }
         tc_fence_after();
@@ -693,7 +741,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           m_ref = ref_s[before][h];
         }
         uint64_t poison = 0;
-        if (kPair && (!sight.whole(t) || !other.whole(t)) && (valid ^ seen_of(other, t)) != 0ull) {
+        if (kPair && one) {
           const uint32_t k = tile % kSlots;
           if (!mbar_wait_warp(&poison_full[k], poison_phase >> k & 1u, kWaitLimit)) { fail(); break; }
           poison_phase ^= 1u << k;

@@ -1,4 +1,5 @@
-"""Builds libmla.so (the C-ABI library) in-tree with nvcc for sm_103a.
+"""Builds libmla.so (the C-ABI library) in-tree with nvcc for sm_103a, and _native.so (the Python binding of its paged
+cache) with the host compiler.
 
 Each ``csrc/*.cu`` translation unit is compiled in parallel, then linked into
 ``mla_latent_kv_12_gb300/libmla.so``.  Objects go to ``_build/`` next to it.
@@ -12,12 +13,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmla.so")
+NATIVE = os.path.join(PKG, "_native.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -45,6 +48,30 @@ def _compile(src: str, obj: str, log: str) -> tuple[str, int, str]:
     return src, r.returncode, r.stdout + r.stderr
 
 
+def _compile_native(obj: str, log: str) -> tuple[str, int, str]:
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I" + os.path.join(ROOT, "include"), "-isystem", inc, "-isystem", os.path.join(inc, "torch/csrc/api/include"),
+           "-isystem", sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    with open(log, "w") as f:
+        f.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+    return "binding.cpp", r.returncode, r.stdout + r.stderr
+
+
+def _link_native(obj: str) -> None:
+    import torch
+    tmp = NATIVE + ".tmp"
+    # torch's libraries are loaded before this one is imported; libmla.so lies beside it
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-lmla", "-Wl,-rpath,$ORIGIN",
+           "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
+    os.replace(tmp, NATIVE)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link; returns the library path.  Raises on a compile error."""
     os.makedirs(BUILD, exist_ok=True)
@@ -57,9 +84,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
         objs.append(o)
         if force or not os.path.exists(o) or os.path.getmtime(o) < max(os.path.getmtime(s), hdr):
             jobs.append((s, o, o + ".log"))
-    if jobs:
-        with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
+    native_obj = os.path.join(BUILD, "binding.o")
+    native_src = os.path.join(CSRC, "binding.cpp")
+    native_stale = force or not os.path.exists(native_obj) or os.path.getmtime(native_obj) < max(
+        os.path.getmtime(native_src), os.path.getmtime(os.path.join(ROOT, "include", "mla.h")))
+    if jobs or native_stale:
+        with cf.ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
+            native = ex.submit(_compile_native, native_obj, native_obj + ".log") if native_stale else None
             results = list(ex.map(lambda j: _compile(*j), jobs))
+            if native:
+                results.append(native.result())
         bad = [(s, out) for s, rc, out in results if rc != 0]
         if bad:
             raise RuntimeError("nvcc failed:\n" + "\n".join(f"{s}:\n{out}" for s, out in bad))
@@ -77,6 +111,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
         os.replace(tmp, LIB)
+    if native_stale or not os.path.exists(NATIVE):
+        _link_native(native_obj)
     return LIB
 
 

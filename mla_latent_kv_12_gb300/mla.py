@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libmla (the C ABI declared in ``include/mla.h``).
+"""Thin binding of libmla (the C ABI declared in ``include/mla.h``): ctypes, and for the paged cache the extension
+module ``_native`` (``csrc/binding.cpp``).
 
 Argument marshalling only: every step runs in the library's CUDA kernels.
 PyTorch supplies device memory and the current stream.  Importing this module
@@ -150,6 +151,7 @@ def _load() -> ctypes.CDLL:
 
 
 lib = _load()
+from . import _native  # noqa: E402  (the binding of the paged cache; it is linked with the library)
 
 
 def _check(status: int) -> None:
@@ -688,21 +690,10 @@ def cache_compact(arrays, kv_start, kept: torch.Tensor, counts: torch.Tensor, de
 
 
 # ---------------------------------------------------------------- paged cache
+#
+# The tensors are checked and their sizes and strides taken in ``_native``.
 
-def _pool_strides(pool: torch.Tensor):
-    """``(pages, page rows, features, row stride, page stride)`` of a pool ``[num_pages, page_size, F]``."""
-    page, row, last = pool.stride()
-    pages, rows, features = pool.shape
-    assert last == 1, "the last axis must be contiguous"
-    return pages, rows, features, row, page
-
-
-def _table_strides(table: torch.Tensor, batch: int):
-    """``(row stride, width)`` of a page table ``[>= batch, width]`` int32."""
-    row, last = table.stride()
-    rows, width = table.shape
-    assert table.dtype is torch.int32 and last == 1 and rows >= batch, "page_table: [>= batch, width] int32, rows contiguous"
-    return row, width
+_native.setup(MLAError, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
 
 
 def append_paged(latent_raw: torch.Tensor, rope_raw: torch.Tensor, norm_weight: torch.Tensor, eps: float, theta: float,
@@ -714,26 +705,8 @@ def append_paged(latent_raw: torch.Tensor, rope_raw: torch.Tensor, norm_weight: 
     ``latent`` ``[num_pages, page_size, rank]`` / ``rope`` ``[num_pages, page_size, rope]``; ``page_table``
     ``[B, width]`` int32.  ``counts`` ``[B]``: how many of the S tokens each row has (all); ``positions`` ``[B, S]``:
     where they are rotated (at their key index)."""
-    B, S, rank = latent_raw.shape
-    l_batch, l_token, l_last = latent_raw.stride()
-    r_batch, r_token, r_last = rope_raw.stride()
-    pages, page_size, width, p_row, p_page = _pool_strides(latent)
-    k_pages, k_size, rope_dim, k_row, k_page = _pool_strides(rope)
-    t_row, t_width = _table_strides(page_table, B)
-    dtype = latent_raw.dtype
-    assert l_last == 1 and r_last == 1 and norm_weight.is_contiguous() and width == rank == norm_weight.numel()
-    assert rope_raw.dtype is dtype and norm_weight.dtype is dtype and rope_raw.shape == (B, S, rope_dim)
-    assert k_pages == pages and k_size == page_size and rope.dtype is latent.dtype
-    _check_int32(B, kv_len, kv_len_out, counts)
-    _check_int32(B * S, positions)
-    _check_status(device_status)
-    handle = _launch_stream(stream, latent_raw, rope_raw, norm_weight, latent, rope, page_table, kv_len, kv_len_out,
-                            positions, counts, device_status)
-    _check(lib.mla_append_paged(
-        latent_raw.data_ptr(), l_batch, l_token, rope_raw.data_ptr(), r_batch, r_token, _dt(latent_raw),
-        norm_weight.data_ptr(), eps, theta, _ptr(positions), latent.data_ptr(), p_row, p_page, rope.data_ptr(), k_row,
-        k_page, _dt(latent), page_table.data_ptr(), t_row, t_width, page_size, pages, kv_len.data_ptr(), _ptr(counts),
-        _ptr(kv_len_out), B, S, rank, rope_dim, _ptr(device_status), handle))
+    _native.append_paged(latent_raw, rope_raw, norm_weight, eps, theta, latent, rope, page_table, kv_len, kv_len_out,
+                         positions, counts, device_status, stream)
 
 
 def tree_plan(parents: torch.Tensor, kv_len: Optional[torch.Tensor], positions: torch.Tensor, tree_mask: torch.Tensor,
@@ -742,16 +715,7 @@ def tree_plan(parents: torch.Tensor, kv_len: Optional[torch.Tensor], positions: 
     """Positions ``[B, n]`` int32 and ancestor masks ``[B * n, ceil(n / 64)]`` int64 (bits) of drafted trees, from
     ``parents`` ``[B, n]`` int32 (a node's parent before it, -1: a root); ``kv_len``: the rows' lengths before the
     trees are appended."""
-    B, n = parents.shape
-    row, last = parents.stride()
-    assert parents.dtype is torch.int32 and last == 1 and tree_mask.dtype is torch.int64
-    assert tree_mask.is_contiguous() and tree_mask.numel() >= B * n * (-(-n // 64))
-    _check_int32(B, kv_len, counts)
-    _check_int32(B * n, positions)
-    _check_status(device_status)
-    handle = _launch_stream(stream, parents, kv_len, positions, tree_mask, counts, device_status)
-    _check(lib.mla_tree_plan(parents.data_ptr(), row, _ptr(kv_len), _ptr(counts), B, n, positions.data_ptr(),
-                             tree_mask.data_ptr(), _ptr(device_status), handle))
+    _native.tree_plan(parents, kv_len, positions, tree_mask, counts, device_status, stream)
     return tree_mask
 
 
@@ -763,39 +727,13 @@ def decode_attend_paged(q: torch.Tensor, latent: torch.Tensor, rope: torch.Tenso
                         device_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """``decode_attend`` over pages: ``q`` ``[batch * s_q, H, rank+rope]``, pools and table as for ``append_paged``,
     ``kv_len`` with the new tokens; ``tree_mask`` as ``tree_plan`` writes it (none: the tokens follow one another)."""
-    n_q, heads, width = q.shape
-    q_row, q_head, q_last = q.stride()
-    x_row, x_head, x_last = ctx_out.stride()
-    pages, page_size, rank, p_row, p_page = _pool_strides(latent)
-    k_pages, k_size, rope_dim, k_row, k_page = _pool_strides(rope)
-    t_row, t_width = _table_strides(page_table, batch)
-    assert q_last == 1 and x_last == 1 and width == rank + rope_dim and n_q == batch * s_q
-    assert ctx_out.shape == (n_q, heads, rank) and rope.dtype is q.dtype and latent.dtype is q.dtype
-    assert k_pages == pages and k_size == page_size
-    _check_int32(batch, kv_len, counts)
-    _check_status(device_status)
-    if lse_out is not None:
-        assert lse_out.dtype is torch.float32 and lse_out.is_contiguous() and lse_out.numel() == n_q * heads
-    if tree_mask is not None:
-        assert tree_mask.dtype is torch.int64 and tree_mask.is_contiguous()
-        assert tree_mask.numel() >= n_q * (-(-s_q // 64))
-    k_max = 0
-    if sel is not None:
-        k_max = sel.shape[1]
-        assert sel.shape[0] == n_q and sel_count is not None and sel_count.numel() == n_q
-        _check_int32(n_q, sel, sel_count)
     if workspace is None:
-        nbytes = decode_workspace_size(batch, s_q, heads, rank, rope_dim, t_width * page_size, k_max, sel is not None,
-                                       q.dtype)
+        nbytes = decode_workspace_size(batch, s_q, q.shape[1], latent.shape[2], rope.shape[2],
+                                       page_table.shape[1] * latent.shape[1], 0 if sel is None else sel.shape[1],
+                                       sel is not None, q.dtype)
         workspace = _scratch(max(nbytes, 1), q.device, stream)
-    assert workspace.element_size() == 1 and workspace.is_contiguous()
-    handle = _launch_stream(stream, q, latent, rope, page_table, kv_len, ctx_out, lse_out, counts, tree_mask, sel,
-                            sel_count, workspace, device_status)
-    _check(lib.mla_decode_attend_paged(
-        q.data_ptr(), q_row, q_head, latent.data_ptr(), p_row, p_page, rope.data_ptr(), k_row, k_page, _dt(q),
-        page_table.data_ptr(), t_row, t_width, page_size, pages, kv_len.data_ptr(), _ptr(counts), _ptr(tree_mask), batch,
-        s_q, heads, rank, rope_dim, _ptr(sel), _ptr(sel_count), k_max, softmax_scale, ctx_out.data_ptr(), x_row, x_head,
-        _dt(ctx_out), _ptr(lse_out), workspace.data_ptr(), workspace.numel(), _ptr(device_status), handle))
+    _native.decode_attend_paged(q, latent, rope, page_table, kv_len, batch, s_q, softmax_scale, ctx_out, lse_out, counts,
+                                tree_mask, sel, sel_count, workspace, device_status, stream)
     return ctx_out
 
 
@@ -806,14 +744,18 @@ class PagedArrays:
     def __init__(self, arrays) -> None:
         self.tensors = list(arrays)
         first = self.tensors[0]
-        self.pages, self.page_size = first.shape[:2]
+        self.pages, self.page_size, _ = first.shape
+        self.device = first.get_device()
         states = []
         for a in self.tensors:
-            pages, rows, features, row, page = _pool_strides(a)
+            pages, rows, features = a.shape
+            page, row, last = a.stride()
             size = a.element_size()
+            assert last == 1, "the last axis must be contiguous"
             assert pages == self.pages and rows == self.page_size and a.device == first.device
             states.append((a.data_ptr(), row * size, page * size, features * size))
         self.states = (StateArray * len(states))(*states)
+        self.address = ctypes.addressof(self.states)
 
 
 def commit_paged(arrays, page_table: torch.Tensor, kv_len: torch.Tensor, path: torch.Tensor, counts: torch.Tensor,
@@ -824,13 +766,5 @@ def commit_paged(arrays, page_table: torch.Tensor, kv_len: torch.Tensor, path: t
     ``kv_len``: the lengths before the trees were appended."""
     if not isinstance(arrays, PagedArrays):
         arrays = PagedArrays(arrays)
-    batch, width = path.shape
-    row, last = path.stride()
-    t_row, t_width = _table_strides(page_table, batch)
-    assert path.dtype is torch.int32 and last == 1
-    _check_int32(batch, kv_len, counts, kv_len_out)
-    _check_status(device_status)
-    handle = _launch_stream(stream, arrays.tensors[0], page_table, kv_len, path, counts, kv_len_out, device_status)
-    _check(lib.mla_commit_paged(arrays.states, len(arrays.states), page_table.data_ptr(), t_row, t_width,
-                                arrays.page_size, arrays.pages, kv_len.data_ptr(), path.data_ptr(), row, width,
-                                counts.data_ptr(), _ptr(kv_len_out), batch, _ptr(device_status), handle))
+    _native.commit_paged(arrays.address, len(arrays.states), arrays.pages, arrays.page_size, arrays.device, page_table,
+                         kv_len, path, counts, kv_len_out, device_status, stream)

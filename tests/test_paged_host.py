@@ -192,13 +192,18 @@ def test_wrong_tensors_are_refused(mla, call, name, value):
 
 
 @pytest.mark.parametrize("call", list(CALLS))
-def test_full_tensors_pass_the_checks(mla, call, monkeypatch):
-    """The same calls with whole tensors get as far as the launch."""
-    def reached(*_):
-        raise KeyError("the launch")
-    monkeypatch.setattr(mla, "_launch_stream", reached)
-    with pytest.raises(KeyError, match="the launch"):
+def test_full_tensors_pass_the_checks(mla, call):
+    """The same calls with whole tensors get as far as the device: there is none, or these are not on it."""
+    with pytest.raises((RuntimeError, ValueError), match="NVIDIA|CUDA"):
         CALLS[call][0](mla, tensors())
+
+
+@pytest.mark.parametrize("call", list(CALLS))
+def test_what_is_no_tensor_is_refused(mla, call):
+    s = tensors()
+    s["len"] = [1, 2, 3]
+    with pytest.raises(TypeError):
+        CALLS[call][0](mla, s)
 
 
 def test_pools_of_a_handle(mla):

@@ -1064,7 +1064,11 @@ int mla_append_paged(const void* latent_raw, int64_t latent_raw_row_stride, int6
   p.rope_dim = rope_dim;
   p.status = device_status;
   if (rope_dim > 0) rope_inverse_frequencies(theta, rope_dim, p.inv_freq);
-  return cuda_status(launch_append_paged(p, dtype, cache_dtype, (cudaStream_t)stream), "append_paged launch");
+  const int64_t ivec = dtype == MLA_DTYPE_F32 ? 4 : 8, cvec = cache_dtype == MLA_DTYPE_F32 ? 4 : 8;   // elements of 16 bytes
+  const bool vec = rank % 8 == 0 && aligned16(latent_raw) && aligned16(norm_weight) && aligned16(latent) &&
+                   latent_raw_row_stride % ivec == 0 && latent_raw_token_stride % ivec == 0 &&
+                   latent_row_stride % cvec == 0 && latent_page_stride % cvec == 0;
+  return cuda_status(launch_append_paged(p, dtype, cache_dtype, vec, (cudaStream_t)stream), "append_paged launch");
 }
 
 int mla_tree_plan(const int32_t* parents, int64_t parents_row_stride, const int32_t* kv_len,

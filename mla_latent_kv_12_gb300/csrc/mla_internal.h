@@ -255,10 +255,11 @@ struct AppendPagedParams {
   int32_t* kv_len_out;
   int32_t batch, s_new, rank, rope_dim;
   int32_t* status;
-  int32_t lengths_here;       // set by the launcher: the kernel writes kv_len_out
+  int32_t lengths_here;       // set by the launcher: the kernel writes kv_len_out (2: which is kv_len)
   float inv_freq[kMaxRotaryDims / 2];
 };
-cudaError_t launch_append_paged(AppendPagedParams p, int in_dtype, int cache_dtype, cudaStream_t stream);
+// vec: rank a multiple of 8, latents and the norm weight in rows of whole 16 bytes.
+cudaError_t launch_append_paged(AppendPagedParams p, int in_dtype, int cache_dtype, bool vec, cudaStream_t stream);
 
 constexpr int kMaxTreeNodes = 1024;
 struct TreePlanParams {

@@ -29,50 +29,118 @@ __device__ __forceinline__ void flag(int32_t* status, int bit) {
 
 constexpr int kAppendWarps = 8;
 
-// One warp per new token.
-template <typename TI, typename TC>
+// Eight consecutive values, 16-byte aligned.
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[2 * j] = __uint_as_float(w[j] << 16), v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+    w[j] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// grid (ceil(s_new / warps), batch rows): one warp per new token, which holds
+// its values in registers between the sum of squares and the store.  Bound by
+// memory for prompt chunks (2 (rank + rope) elements per token), by the chain
+// of dependent loads (length, page, store) for single tokens: what does not
+// depend on them is loaded first.  kGroups: groups of eight values per lane
+// (rank a multiple of 8 up to 256 kGroups, aligned rows), or 0: one by one.
+template <typename TI, typename TC, int kGroups>
 __global__ void __launch_bounds__(kAppendWarps * 32) append_paged_kernel(const __grid_constant__ AppendPagedParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ float freq_s[kMaxRotaryDims / 2];
-  const int half = p.rope_dim >> 1;
-  if ((int)threadIdx.x < half) freq_s[threadIdx.x] = p.inv_freq[threadIdx.x];
-  __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t tokens = (int64_t)p.batch * p.s_new, capacity = (int64_t)p.table_width * p.page_size;
-  for (int64_t k = (int64_t)blockIdx.x * kAppendWarps + warp; k < tokens; k += (int64_t)gridDim.x * kAppendWarps) {
-    const int b = (int)(k / p.s_new), t = (int)(k % p.s_new);
+  const int half = p.rope_dim >> 1;
+  const int t = blockIdx.x * (blockDim.x >> 5) + warp;
+  const int64_t capacity = (int64_t)p.table_width * p.page_size;
+  const TI* w = static_cast<const TI*>(p.weight);
+  for (int b = blockIdx.y; b < p.batch; b += gridDim.y) {
     const int len = p.kv_len[b], count = paged_count(p.counts, b, p.s_new);
+    const TI* x = static_cast<const TI*>(p.latent_raw) + b * p.lr_row_stride + t * p.lr_tok_stride;
+    const TI* rr = static_cast<const TI*>(p.rope_raw) + b * p.rr_row_stride + t * p.rr_tok_stride;
+    float v[kGroups ? kGroups : 1][8], re0 = 0.f, im0 = 0.f;
+    auto load = [&] {
+      if constexpr (kGroups > 0) {
+#pragma unroll
+        for (int c = 0; c < kGroups; ++c)
+          if (256 * c + 8 * lane < p.rank) load8(x + 256 * c + 8 * lane, v[c]);
+      }
+      if (lane < half) re0 = to_f(rr[2 * lane]), im0 = to_f(rr[2 * lane + 1]);
+    };
+    const bool early = !p.counts && t < p.s_new;   // before the length is known: every token is there
+    if (early) load();
     const bool fits = len >= 0 && count >= 0 && (int64_t)len + count <= capacity;
-    if (lane == 0 && t == 0) {
-      if (!fits) flag(p.status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
-      if (p.lengths_here) p.kv_len_out[b] = fits ? len + count : len;
+    if (blockIdx.x == 0) {
+      if (p.lengths_here == 2) __syncthreads();   // (one CTA per row: its warps have read the length that is overwritten)
+      if (threadIdx.x == 0) {
+        if (!fits) flag(p.status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
+        if (p.lengths_here) p.kv_len_out[b] = fits ? len + count : len;
+      }
     }
     if (!fits || t >= count) continue;
     const int row = len + t, at = row / p.page_size;
     const int page = p.table[b * p.table_stride + at];
-    const int64_t pos = p.positions ? (int64_t)p.positions[k] : (int64_t)row;
-    if (page < 0 || page >= p.num_pages || pos < 0) {
+    const int64_t pos = p.positions ? (int64_t)p.positions[(int64_t)b * p.s_new + t] : (int64_t)row;
+    if (!early) load();
+    float inv;
+    {
+      float sq = 0.f;
+      if constexpr (kGroups > 0) {
+#pragma unroll
+        for (int c = 0; c < kGroups; ++c)
+          if (256 * c + 8 * lane < p.rank) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sq = fmaf(v[c][j], v[c][j], sq);
+          }
+      } else {
+        for (int i = lane; i < p.rank; i += 32) {
+          const float u = to_f(x[i]);
+          sq = fmaf(u, u, sq);
+        }
+      }
+      inv = rsqrtf(warp_sum(sq) / (float)p.rank + p.eps);
+    }
+    if (page < 0 || page >= p.num_pages || pos < 0) {   // (the same in the whole warp)
       if (lane == 0) flag(p.status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
       continue;
     }
     const int in_page = row - at * p.page_size;
-    const TI* x = static_cast<const TI*>(p.latent_raw) + b * p.lr_row_stride + t * p.lr_tok_stride;
-    const TI* w = static_cast<const TI*>(p.weight);
     TC* dl = static_cast<TC*>(p.latent) + page * p.l_page_stride + in_page * p.l_row_stride;
-    float sq = 0.f;
-    for (int i = lane; i < p.rank; i += 32) {
-      const float v = to_f(x[i]);
-      sq = fmaf(v, v, sq);
-    }
-    const float inv = rsqrtf(warp_sum(sq) / (float)p.rank + p.eps);
-    for (int i = lane; i < p.rank; i += 32) put(dl + i, to_f(x[i]) * inv * to_f(w[i]));
-    const TI* rr = static_cast<const TI*>(p.rope_raw) + b * p.rr_row_stride + t * p.rr_tok_stride;
     TC* dr = static_cast<TC*>(p.rope) + page * p.r_page_stride + in_page * p.r_row_stride;
+    if constexpr (kGroups > 0) {
+#pragma unroll
+      for (int c = 0; c < kGroups; ++c)
+        if (256 * c + 8 * lane < p.rank) {
+          float g[8];
+          load8(w + 256 * c + 8 * lane, g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) g[j] = v[c][j] * inv * g[j];
+          store8(dl + 256 * c + 8 * lane, g);
+        }
+    } else {
+      for (int i = lane; i < p.rank; i += 32) put(dl + i, to_f(x[i]) * inv * to_f(w[i]));
+    }
     for (int j = lane; j < half; j += 32) {
-      float re, im;
-      rope_rotate_pair(to_f(rr[2 * j]), to_f(rr[2 * j + 1]), pos, freq_s[j], re, im);
-      put(dr + j, re);
-      put(dr + half + j, im);
+      if (j != lane) re0 = to_f(rr[2 * j]), im0 = to_f(rr[2 * j + 1]);
+      const float angle = rope_angle(pos, p.inv_freq[j]);
+      float s, c;
+      if (angle <= kSmallAngle) sincos_small(angle, s, c); else sincosf(angle, &s, &c);
+      put(dr + j, re0 * c - im0 * s);
+      put(dr + half + j, im0 * c + re0 * s);
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -93,43 +161,58 @@ __global__ void __launch_bounds__(256) paged_lengths_kernel(const int32_t* kv_le
 
 // ------------------------------------------------------------------ trees
 
-// One CTA per tree, one thread per node.  A node's ancestors have smaller
-// numbers, so walking up from it fills its mask's words from the last to the
-// first.
+// One CTA per tree, one thread per node.  Each node holds the mask of itself
+// and the ancestors found so far, and the ancestor behind them; in a round it
+// takes over both from that ancestor, so paths double in length (walking up
+// node by node took 8.9 us for 64 trees of 256 nodes and depths around 45,
+// launches included).
 __global__ void __launch_bounds__(kMaxTreeNodes) tree_plan_kernel(const __grid_constant__ TreePlanParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ int32_t parent_s[kMaxTreeNodes];
-  const int b = blockIdx.x, j = threadIdx.x;
-  int count = paged_count(p.counts, b, p.n_nodes);
+  extern __shared__ uint64_t mask_s[];   // [n_nodes][words]
+  __shared__ int32_t up_s[kMaxTreeNodes];
+  const int b = blockIdx.x, j = threadIdx.x, n = p.n_nodes, words = (n + 63) >> 6;
+  int up = j < n ? p.parents[b * p.parents_stride + j] : -1;
+  int count = paged_count(p.counts, b, n);
   const int len = p.kv_len ? p.kv_len[b] : 0;
   if (count < 0 || len < 0) {
     if (j == 0) flag(p.status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
     count = 0;
   }
-  if (j < p.n_nodes) {
-    int up = -1;
-    if (j < count) {
-      up = p.parents[b * p.parents_stride + j];
-      if (up < -1 || up >= j) {   // not below an earlier node: a root
-        flag(p.status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
-        up = -1;
-      }
-    }
-    parent_s[j] = up;
+  if (j >= count) {
+    up = -1;
+  } else if (up < -1 || up >= j) {   // not below an earlier node: a root
+    flag(p.status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
+    up = -1;
   }
-  __syncthreads();
-  if (j < p.n_nodes) {
-    const int words = (p.n_nodes + 63) >> 6;
-    uint64_t* mask = p.mask + ((int64_t)b * p.n_nodes + j) * words;
-    int at = words - 1, depth = -1;
-    uint64_t word = 0;
-    for (int node = j < count ? j : -1; node >= 0; node = parent_s[node]) {
-      for (; at > node >> 6; --at) mask[at] = word, word = 0;
-      word |= 1ull << (node & 63);
-      ++depth;
+  uint64_t* mine = mask_s + j * words;
+  const int own = j >> 6;   // ancestors have smaller numbers: the words behind a node's own stay empty
+  if (j < n) {
+    for (int k = 0; k < words; ++k) mine[k] = k == own && j < count ? 1ull << (j & 63) : 0ull;
+    up_s[j] = up;
+  }
+  while (__syncthreads_or(up >= 0)) {
+    uint64_t w[kMaxTreeNodes / 64];
+    int next = -1;
+    if (up >= 0) {
+      next = up_s[up];
+#pragma unroll
+      for (int k = 0; k < kMaxTreeNodes / 64; ++k)
+        if (k <= own) w[k] = mask_s[up * words + k];
     }
-    for (; at >= 0; --at) mask[at] = word, word = 0;
-    p.positions[(int64_t)b * p.n_nodes + j] = len + (depth > 0 ? depth : 0);
+    __syncthreads();
+    if (up >= 0) {
+#pragma unroll
+      for (int k = 0; k < kMaxTreeNodes / 64; ++k)
+        if (k <= own) mine[k] |= w[k];
+      up_s[j] = up = next;
+    }
+  }
+  uint64_t* mask = p.mask + (int64_t)b * n * words;
+  for (int i = j; i < n * words; i += blockDim.x) mask[i] = mask_s[i];
+  if (j < n) {
+    int nodes = 0;
+    for (int k = 0; k <= own; ++k) nodes += __popcll(mine[k]);
+    p.positions[(int64_t)b * n + j] = len + (nodes > 0 ? nodes - 1 : 0);
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -217,29 +300,41 @@ cudaError_t launch_lengths(const int32_t* kv_len, const int32_t* counts, int32_t
 
 }  // namespace
 
-cudaError_t launch_append_paged(AppendPagedParams p, int in_dtype, int cache_dtype, cudaStream_t stream) {
-  const int64_t tokens = (int64_t)p.batch * p.s_new;
-  const int64_t ctas = (tokens + kAppendWarps - 1) / kAppendWarps, most = 8LL * device_sm_count();
-  const dim3 grid((unsigned)(ctas < most ? ctas : most)), block(kAppendWarps * 32);
-  // lengths that other CTAs still read are written by a launch of their own
-  const bool after = p.kv_len_out == p.kv_len;
-  p.lengths_here = p.kv_len_out && !after;
+cudaError_t launch_append_paged(AppendPagedParams p, int in_dtype, int cache_dtype, bool vec, cudaStream_t stream) {
+  const int warps = p.s_new < kAppendWarps ? p.s_new : kAppendWarps;
+  const dim3 grid((unsigned)((p.s_new + warps - 1) / warps), (unsigned)(p.batch < 65535 ? p.batch : 65535)), block(warps * 32);
+  // Lengths written in place: by the kernel where one CTA has a row's tokens, else by a launch of their own.
+  const bool in_place = p.kv_len_out == p.kv_len, after = in_place && grid.x > 1;
+  p.lengths_here = !p.kv_len_out || after ? 0 : in_place ? 2 : 1;
+  auto launch = [&](auto in, auto out) {
+    using TI = decltype(in);
+    using TC = decltype(out);
+    return !vec             ? launch_pdl(append_paged_kernel<TI, TC, 0>, grid, block, 0, stream, p)
+           : p.rank <= 512 ? launch_pdl(append_paged_kernel<TI, TC, 2>, grid, block, 0, stream, p)
+                           : launch_pdl(append_paged_kernel<TI, TC, kMaxAppendRank / 256>, grid, block, 0, stream, p);
+  };
   cudaError_t e;
   if (in_dtype == MLA_DTYPE_F32 && cache_dtype == MLA_DTYPE_F32)
-    e = launch_pdl(append_paged_kernel<float, float>, grid, block, 0, stream, p);
+    e = launch(0.f, 0.f);
   else if (in_dtype == MLA_DTYPE_F32)
-    e = launch_pdl(append_paged_kernel<float, __nv_bfloat16>, grid, block, 0, stream, p);
+    e = launch(0.f, __nv_bfloat16());
   else if (cache_dtype == MLA_DTYPE_F32)
-    e = launch_pdl(append_paged_kernel<__nv_bfloat16, float>, grid, block, 0, stream, p);
+    e = launch(__nv_bfloat16(), 0.f);
   else
-    e = launch_pdl(append_paged_kernel<__nv_bfloat16, __nv_bfloat16>, grid, block, 0, stream, p);
+    e = launch(__nv_bfloat16(), __nv_bfloat16());
   if (e == cudaSuccess && after)
     e = launch_lengths(p.kv_len, p.counts, p.s_new, (int64_t)p.table_width * p.page_size, p.batch, p.kv_len_out, stream);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_tree_plan(const TreePlanParams& p, cudaStream_t stream) {
-  const cudaError_t e = launch_pdl(tree_plan_kernel, dim3((unsigned)p.batch), dim3((unsigned)((p.n_nodes + 31) & ~31)), 0,
+  constexpr int most = kMaxTreeNodes * (kMaxTreeNodes / 64) * 8;
+  const size_t smem = (size_t)p.n_nodes * ((p.n_nodes + 63) / 64) * 8;
+  if (smem > 40 * 1024) {   // (48 KB a kernel has without asking, less its static part)
+    const cudaError_t ea = set_max_dynamic_smem(tree_plan_kernel, most);
+    if (ea != cudaSuccess) return ea;
+  }
+  const cudaError_t e = launch_pdl(tree_plan_kernel, dim3((unsigned)p.batch), dim3((unsigned)((p.n_nodes + 31) & ~31)), smem,
                                    stream, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -1745,6 +1745,7 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
   a.n_units = n_q / a.width;
   a.min_tiles = kMinTilesPerGroup;
   a.start_charge = kUnitStartCharge;
+  a.charge_min_span = kChargeMinSpan;
   const bool q8 = g.codes != nullptr;   // codes are copied row by row: only rope keys are mapped
   a.batch_in_map = ((g.latent_batch_stride != 0 && !q8) || g.rope_batch_stride != 0) ? 1 : 0;
   a.plan_in_kernel = n_q <= kMaxRowsInKernelPlan ? 1 : 0;

@@ -67,6 +67,10 @@ static_assert(kGroups * regs_softmax(false) + regs_issue(false) <= (kGroups + 1)
 // time (verify of 8 x 4 tokens of 65536: 396 us, one row at a time 447; 8 trees of 64 nodes behind 8000 to 15000 keys:
 // 1207 us, by two 1237, by eight 1244, alone 1247: eight leave four of 76 clusters idle).
 constexpr int kLockstep = 4;
+// A unit's start is charged as this many tiles where the ranges are at least so long (the query waits for the last
+// scores of the unit before, and its context is stored): one tree of 16 nodes behind 4050 keys 33.2 -> 29.8 us, of 64
+// nodes 76 -> 72, of 20 nodes in 4 rows of 20000 309 -> 297; between 3 and 14 the charge itself moves them by 2 %.
+constexpr int kStartCharge = 7, kChargeSpan = 8;
 // Tiles pulled into L2 ahead of their load: farther for a lockstep group.
 constexpr int kPrefetchAheadGroup = 8, kPrefetchAheadRow = 3;
 
@@ -903,7 +907,8 @@ cudaError_t launch_tc_paged(const DecodeGeometry& g, int out_dtype, void* worksp
   a.width = a.s_q < kLockstep ? a.s_q : kLockstep;
   a.n_units = (a.n_q + a.width - 1) / a.width;
   a.min_tiles = kMinTilesPerGroup;
-  a.start_charge = kUnitStartCharge;
+  a.start_charge = kStartCharge;
+  a.charge_min_span = kChargeSpan;
   a.plan_in_kernel = a.n_q <= kMaxRowsInKernelPlan ? 1 : 0;
   a.box_rows = BN;   // the largest box that divides a tile and a page
   while (g.page_size % a.box_rows != 0) a.box_rows >>= 1;

@@ -63,7 +63,7 @@ struct TcDecodeArgs {
   int32_t width;       // query rows per work unit = clusters per group
   int32_t n_units;     // n_q / width
   int32_t min_tiles;   // smallest tile range given to a group
-  int32_t start_charge;  // kUnitStartCharge, or the kernel's own
+  int32_t start_charge, charge_min_span;  // kUnitStartCharge and kChargeMinSpan, or the kernel's own
   int32_t batch_in_map;  // 1: use batch coordinate b in the tensor maps
   int32_t gather_tma;    // 1: selected rows come by TMA gather4 (else cp.async)
   int32_t lat_rows_per_batch, rope_rows_per_batch;  // batch stride in rows (gather maps)
@@ -136,7 +136,7 @@ __device__ __forceinline__ int group_span(const TcDecodeArgs& a, int total) {
 // The start charge of a plan whose units hold `raw` tiles in all.
 __device__ __forceinline__ int unit_start_charge(const TcDecodeArgs& a, int raw) {
   const int ngroups = a.num_clusters / a.width;
-  return (raw + ngroups - 1) / ngroups >= kChargeMinSpan ? a.start_charge : 0;
+  return (raw + ngroups - 1) / ngroups >= a.charge_min_span ? a.start_charge : 0;
 }
 
 struct WorkIter {

@@ -177,6 +177,7 @@ __device__ __forceinline__ void gather_paged_group(const TcDecodeArgs& a, const 
 
 // ------------------------------------------------------------------ planner
 
+template <bool kPaged>
 __global__ void __launch_bounds__(1024) tc_plan_kernel(const __grid_constant__ TcDecodeArgs a) {
   pdl_wait();
   __shared__ int warp_sums[32];
@@ -188,9 +189,9 @@ __global__ void __launch_bounds__(1024) tc_plan_kernel(const __grid_constant__ T
   int raw = 0;
   for (int u = threadIdx.x; u < a.n_units; u += 1024) {
     int tiles = 0;
-    for (int i = 0; i < a.width && u * a.width + i < a.n_q; ++i) {
+    for (int i = 0; i < a.width && (!kPaged || u * a.width + i < a.n_q); ++i) {
       const int n = u * a.width + i;
-      const int keys = row_keys(a, n, true);
+      const int keys = row_keys<kPaged>(a, n, true);
       a.keys[n] = keys;
       const int t = (keys + BN - 1) / BN;
       tiles = t > tiles ? t : tiles;
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(1024) tc_plan_kernel(const __grid_constant__ T
     int ext = 0;
     if (u < a.n_units) {
       int tiles = 0;
-      for (int i = 0; i < a.width && u * a.width + i < a.n_q; ++i) {
+      for (int i = 0; i < a.width && (!kPaged || u * a.width + i < a.n_q); ++i) {
         const int t = (a.keys[u * a.width + i] + BN - 1) / BN;
         tiles = t > tiles ? t : tiles;
       }
@@ -353,7 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int32_t* keys_p = a.keys;
   const int32_t* prefix_p = a.prefix;
   if (a.plan_in_kernel) {
-    plan_rows(a, plan_keys_s, plan_prefix_s, blockIdx.x == 0, row_start_s, row_limit_s);
+    plan_rows<kPaged>(a, plan_keys_s, plan_prefix_s, blockIdx.x == 0, row_start_s, row_limit_s);
     keys_p = plan_keys_s;
     prefix_p = plan_prefix_s;
     if (blockIdx.x == 0) {   // a copy in the workspace, where the planner launch puts it above 128 rows
@@ -383,7 +384,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int u, n, t0, t1;
     bool whole;
     while (!aborted() && it.next(u, t0, t1, whole)) {
-      if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
+      if (!member_segment<kPaged>(a, keys_p, u, member, n, t0, t1)) continue;
       const int keys = keys_p[n];
       const uint64_t* mask = kPaged ? tree_of(a, n) : nullptr;
       const int first = !kPaged || !mask ? keys : a.plan_in_kernel ? row_start_s[n] : paged_first(a, n / a.s_q);
@@ -462,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int u, n, t0, t1;
     bool whole;
     while (!aborted() && it.next(u, t0, t1, whole)) {
-      if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
+      if (!member_segment<kPaged>(a, keys_p, u, member, n, t0, t1)) continue;
       for (int t = t0; t < t1; ++t) {
         const bool first = (t == t0);
         // O is overwritten by a segment's first P.V: the previous segment's
@@ -502,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int u, n, t0, t1;
     bool whole;
     while (!aborted() && it.next(u, t0, t1, whole)) {
-      if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
+      if (!member_segment<kPaged>(a, keys_p, u, member, n, t0, t1)) continue;
       const int b = n / a.s_q, keys = keys_p[n];
       const int start = a.plan_in_kernel ? row_start_s[n] : (a.kv_start ? a.kv_start[b] : 0);
       const bool window = !gather || a.sel_count[n] == -1;
@@ -560,7 +561,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int u, n, t0, t1;
     bool whole;
     while (!aborted() && it.next(u, t0, t1, whole)) {
-      if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
+      if (!member_segment<kPaged>(a, keys_p, u, member, n, t0, t1)) continue;
       const int b = n / a.s_q;
       Q8Rows rows;
       rows.codes = a.codes + b * a.codes_batch_stride + dim_base + 16 * c;
@@ -570,7 +571,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       rows.rope = a.rope + b * a.rope_batch_stride + 32 * (int)rank + 8 * (c & 3);
       rows.rope_stride = a.rope_row_stride;
       rows.start = a.plan_in_kernel ? row_start_s[n] : (a.kv_start ? a.kv_start[b] : 0);
-      rows.limit = a.plan_in_kernel ? row_limit_s[n] : row_limit(a, n);
+      rows.limit = a.plan_in_kernel ? row_limit_s[n] : row_limit<kPaged>(a, n);
       rows.entries = keys_p[n];
       rows.list = (gather && a.sel_count[n] != -1) ? a.sel + (int64_t)n * a.k_max : nullptr;
       rows.status = rank == 0 && c < DecodeFetch::kIters ? a.status : nullptr;   // one lane per entry flags it
@@ -631,10 +632,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int u, n, t0, t1;
     bool whole;
     while (!aborted() && it.next(u, t0, t1, whole)) {
-      if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
+      if (!member_segment<kPaged>(a, keys_p, u, member, n, t0, t1)) continue;
       const int b = n / a.s_q;
       const int start = a.plan_in_kernel ? row_start_s[n] : (a.kv_start ? a.kv_start[b] : 0);
-      const int limit = a.plan_in_kernel ? row_limit_s[n] : row_limit(a, n);
+      const int limit = a.plan_in_kernel ? row_limit_s[n] : row_limit<kPaged>(a, n);
       const int keys = keys_p[n];
       const int zb = a.batch_in_map ? b : 0;
       const int32_t* list = (gather && (!kPaged || a.sel) && a.sel_count[n] != -1) ? a.sel + (int64_t)n * a.k_max : nullptr;
@@ -749,10 +750,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int u, n, t0, t1;
       bool whole;
       while (!aborted() && it.next(u, t0, t1, whole)) {
-        if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
+        if (!member_segment<kPaged>(a, keys_p, u, member, n, t0, t1)) continue;
         const int b = n / a.s_q;
         const int start = a.plan_in_kernel ? row_start_s[n] : (a.kv_start ? a.kv_start[b] : 0);
-        const int limit = a.plan_in_kernel ? row_limit_s[n] : row_limit(a, n);
+        const int limit = a.plan_in_kernel ? row_limit_s[n] : row_limit<kPaged>(a, n);
         const int keys = keys_p[n];
         const int32_t* list = (!kPaged || a.sel) && a.sel_count[n] != -1 ? a.sel + (int64_t)n * a.k_max : nullptr;
         for (int t = t0; t < t1 && !aborted(); ++t) {
@@ -790,7 +791,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int u, n, t0, t1;
     bool whole;
     while (!aborted() && it.next(u, t0, t1, whole)) {
-      if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
+      if (!member_segment<kPaged>(a, keys_p, u, member, n, t0, t1)) continue;
       {
         // This head's query (this CTA's latent dims [dim_base, dim_base+256)
         // into TMEM columns 0..127 of Q, its rope dims [32*rank, 32*rank+32)
@@ -848,7 +849,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           int un, nn, tn0, tn1;
           bool wn;
           while (peek.next(un, tn0, tn1, wn)) {
-            if (!member_segment(a, keys_p, un, member, nn, tn0, tn1)) continue;
+            if (!member_segment<kPaged>(a, keys_p, un, member, nn, tn0, tn1)) continue;
             if (h < a.heads) {
               const __nv_bfloat16* qnext = a.q + (int64_t)nn * a.q_row_stride + (int64_t)h * a.q_head_stride;
 #pragma unroll
@@ -972,7 +973,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int u, n, t0, t1;
     bool whole;
     while (!aborted() && it.next(u, t0, t1, whole)) {
-      const bool any = member_segment(a, keys_p, u, member, n, t0, t1);
+      const bool any = member_segment<kPaged>(a, keys_p, u, member, n, t0, t1);
       const int64_t slot = ((int64_t)u + group) * a.width + member;
       if (!any) {
         // Nothing of this row in the group's range: an empty partial (weight 0).
@@ -983,7 +984,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         continue;
       }
       const int keys = keys_p[n];
-      const int limit = a.plan_in_kernel ? row_limit_s[n] : row_limit(a, n);
+      const int limit = a.plan_in_kernel ? row_limit_s[n] : row_limit<kPaged>(a, n);
       const int32_t* list = (gather && (!kPaged || a.sel) && a.sel_count[n] != -1) ? a.sel + (int64_t)n * a.k_max : nullptr;
       const uint64_t* mask = kPaged ? tree_of(a, n) : nullptr;
       const int first = !kPaged || !mask ? keys : a.plan_in_kernel ? row_start_s[n] : paged_first(a, n / a.s_q);
@@ -1278,7 +1279,7 @@ __device__ __forceinline__ void unpack_partial(const uint4 r, float (&x)[8]) {
 constexpr int CDIMS = 8;
 constexpr int kCombineWideRows = 8;   // rows up to which the combine loads 16 pieces at once
 
-template <int kCombineBatch>
+template <int kCombineBatch, bool kPaged>
 __global__ void __launch_bounds__(128) tc_combine_kernel(const __grid_constant__ TcDecodeArgs a) {
   __shared__ int32_t keys_s[kMaxRowsInKernelPlan];
   __shared__ int32_t prefix_s[kMaxRowsInKernelPlan + 2];
@@ -1295,7 +1296,7 @@ __global__ void __launch_bounds__(128) tc_combine_kernel(const __grid_constant__
   int keys;
   const int32_t* prefix;
   if (a.plan_in_kernel) {
-    plan_rows(a, keys_s, prefix_s, false);   // 128 threads >= n_q
+    plan_rows<kPaged>(a, keys_s, prefix_s, false);   // 128 threads >= n_q
     keys = keys_s[n];
     prefix = prefix_s;
   } else {
@@ -1312,7 +1313,7 @@ __global__ void __launch_bounds__(128) tc_combine_kernel(const __grid_constant__
   // the token and head of MMA row h (two tokens of 64 heads, or padding from a.heads on)
   int64_t token = n;
   int head = h;
-  if (a.tokens == 2) {
+  if (kPaged && a.tokens == 2) {
     const int i = 2 * (n % a.s_q) + (h >> 6);
     if (i >= a.tok_q) return;
     token = (int64_t)(n / a.s_q) * a.tok_q + i;
@@ -1491,7 +1492,7 @@ __global__ void __launch_bounds__(PROJ_THREADS) tc_combine_project_kernel(const 
   // recomputed here, the same way the decode kernel computes it, before the
   // wait; the pieces' partial buffers are touched (L2 prefetch: address
   // translation and lines) so that the loads after the wait hit.
-  plan_rows(a, keys_s, prefix_s, false);
+  plan_rows<false>(a, keys_s, prefix_s, false);
   {
     const int per = group_span(a, prefix_s[a.n_units]);
     for (int n = threadIdx.x >> 5; n < a.n_q; n += PROJ_THREADS / 32) {
@@ -1694,13 +1695,15 @@ void tc::lay_out_workspace(TcDecodeArgs& a, void* workspace) {
 }
 
 cudaError_t tc::launch_split_plan(const TcDecodeArgs& a, cudaStream_t stream) {
-  return launch_pdl(tc_plan_kernel, dim3(1), dim3(1024), 0, stream, a);
+  return launch_pdl(a.table ? tc_plan_kernel<true> : tc_plan_kernel<false>, dim3(1), dim3(1024), 0, stream, a);
 }
 
 cudaError_t tc::launch_split_combine(const TcDecodeArgs& a, cudaStream_t stream) {
   // batch 16 (128 registers, 4 CTAs per SM) while the grid fits one wave
   // at that occupancy, else 4
-  auto* const combine = a.n_q <= kCombineWideRows ? tc_combine_kernel<16> : tc_combine_kernel<4>;
+  const bool wide = a.n_q <= kCombineWideRows;
+  auto* const combine = a.table ? (wide ? tc_combine_kernel<16, true> : tc_combine_kernel<4, true>)
+                                : (wide ? tc_combine_kernel<16, false> : tc_combine_kernel<4, false>);
   return launch_pdl(combine, dim3(a.n_q, RANK / CDIMS), dim3(HEADS), 0, stream, a);
 }
 

@@ -171,7 +171,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const int32_t* keys_p = a.keys;
   const int32_t* prefix_p = a.prefix;
   if (a.plan_in_kernel) {
-    plan_rows(a, plan_keys_s, plan_prefix_s, blockIdx.x == 0, row_first_s, limit_s);
+    plan_rows<true>(a, plan_keys_s, plan_prefix_s, blockIdx.x == 0, row_first_s, limit_s);
     keys_p = plan_keys_s;
     prefix_p = plan_prefix_s;
   }
@@ -238,7 +238,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       int u, n, t0, t1;
       bool whole;
       while (!aborted() && it.next(u, t0, t1, whole)) {
-        if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
+        if (!member_segment<true>(a, keys_p, u, member, n, t0, t1)) continue;
         const int keys = keys_p[n];
         const int32_t* table = a.table + (n / a.s_q) * a.table_stride;
         // Lane l holds the page (-1: no key in the box) and first row there of box 32 * block + l, and of the
@@ -327,7 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               int un, nn, tn0, tn1;
               bool wn;
               while (peek.next(un, tn0, tn1, wn)) {
-                if (!member_segment(a, keys_p, un, member, nn, tn0, tn1)) continue;
+                if (!member_segment<true>(a, keys_p, un, member, nn, tn0, tn1)) continue;
                 const int i = (nn % a.s_q) * kTokens, token = (nn / a.s_q) * a.tok_q + i;
                 const int head2 = kPair ? 0 : 64, token2 = kPair ? token + 1 : token;
                 for (int c = 0; c < 4; ++c) {
@@ -353,7 +353,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       int u, n, t0, t1;
       bool whole;
       while (!aborted() && it.next(u, t0, t1, whole)) {
-        if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
+        if (!member_segment<true>(a, keys_p, u, member, n, t0, t1)) continue;
         const Sight sight = kPair ? Sight{} : sight_of(n);
         const int whole_tiles = kPair ? whole_of(n) : 0;
         if (!mbar_wait_warp(&q_full, seg & 1u, kWaitLimit)) { fail(); break; }
@@ -461,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       int u, n, t0, t1;
       bool whole;
       while (!aborted() && it.next(u, t0, t1, whole)) {
-        if (!member_segment(a, keys_p, u, member, n, t0, t1)) continue;
+        if (!member_segment<true>(a, keys_p, u, member, n, t0, t1)) continue;
         stage = (stage + 2) % STAGES;   // behind the query's
         for (int t = t0; t < t1; ++t) {
           const bool first = (t == t0);
@@ -550,7 +550,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       int u, n, t0, t1;
       bool whole;
       while (peek.next(u, t0, t1, whole))
-        if (member_segment(a, keys_p, u, member, n, t0, t1)) return n;
+        if (member_segment<true>(a, keys_p, u, member, n, t0, t1)) return n;
       return -1;
     };
     int u, n = 0, t0, t1;
@@ -672,7 +672,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       live = false;
       while (it.next(u, t0, t1, whole)) {
         slot = ((int64_t)u + group) * a.width + member;
-        live = member_segment(a, keys_p, u, member, n, t0, t1);
+        live = member_segment<true>(a, keys_p, u, member, n, t0, t1);
         if (live) break;
         // Nothing of this row in the group's range: an empty partial (weight 0).
         if (!whole && rank == 0 && me == 0 && head < a.heads) {

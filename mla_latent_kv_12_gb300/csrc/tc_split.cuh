@@ -105,9 +105,11 @@ __device__ __forceinline__ int token_limit(const TcDecodeArgs& a, int b, int i) 
   return paged_limit(len, count, i, i < a.tok_q ? tree_of(a, b * a.tok_q + i) : nullptr, a.tree_words);
 }
 
+// (What only paged rows need stays out of the other instances of kernels that plan.)
+template <bool kPaged>
 __device__ __forceinline__ int row_limit(const TcDecodeArgs& a, int n) {
   const int b = n / a.s_q, i = n % a.s_q;
-  if (a.table) {
+  if constexpr (kPaged) {
     const int limit = token_limit(a, b, i * a.tokens);
     return a.tokens == 2 ? max(limit, token_limit(a, b, 2 * i + 1)) : limit;
   }
@@ -192,10 +194,11 @@ __device__ __forceinline__ int last_group_of(const int32_t* prefix, int u, int p
 // A member's share of a unit segment: its query row n and the segment's tiles
 // clipped to that row's own tiles (a verify token sees a shorter prefix than
 // the last token).  False if nothing is left.
+template <bool kPaged>
 __device__ __forceinline__ bool member_segment(const TcDecodeArgs& a, const int32_t* keys, int u, int member,
                                                int& n, int& t0, int& t1) {
   n = u * a.width + member;
-  if (n >= a.n_q) return false;   // the last unit may have fewer rows
+  if (kPaged && n >= a.n_q) return false;   // the last unit may have fewer rows
   const int tiles = (keys[n] + BN - 1) / BN;
   if (t1 > tiles) t1 = tiles;
   return t0 < t1;
@@ -205,9 +208,10 @@ __device__ __forceinline__ bool member_segment(const TcDecodeArgs& a, const int3
 // Per query row the number of visible entries; the planner (or the decode
 // prologue) turns them into tiles and the exclusive prefix of tiles over work
 // units.  Bad selection counts give 0 and are flagged where `flag` is set.
+template <bool kPaged>
 __device__ __forceinline__ int row_keys(const TcDecodeArgs& a, int n, bool flag) {
-  int keys = row_limit(a, n);
-  if (a.table) {
+  int keys = row_limit<kPaged>(a, n);
+  if constexpr (kPaged) {
     const int b = n / a.s_q, len = a.kv_len[b];
     if (flag && a.status && (len < 0 || len > a.t_max || paged_count(a.counts, b, a.tok_q) < 0))
       atomicOr(a.status, MLA_DEVICE_INDEX_OUT_OF_RANGE);
@@ -243,20 +247,21 @@ __device__ __forceinline__ int row_keys(const TcDecodeArgs& a, int n, bool flag)
 // scanned by warp 0 (four units per lane, in unit order).
 // With start_s / limit_s, also each row's first cache row (of a paged row: the
 // first of its new tokens' keys) and the window limit of each of its tokens.
+template <bool kPaged>
 __device__ __forceinline__ void plan_rows(const TcDecodeArgs& a, int32_t* keys_s, int32_t* prefix_s, bool flag,
                                           int32_t* start_s = nullptr, int32_t* limit_s = nullptr) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x < a.n_q) {
     const int n = threadIdx.x;
-    keys_s[n] = row_keys(a, n, flag);
+    keys_s[n] = row_keys<kPaged>(a, n, flag);
     if (start_s) {
       const int b = n / a.s_q;
-      start_s[n] = a.table ? paged_first(a, b) : a.kv_start ? a.kv_start[b] : 0;
-      if (a.tokens == 2) {
+      start_s[n] = kPaged ? paged_first(a, b) : a.kv_start ? a.kv_start[b] : 0;
+      if (kPaged && a.tokens == 2) {
         limit_s[2 * n] = token_limit(a, b, 2 * (n % a.s_q));
         limit_s[2 * n + 1] = token_limit(a, b, 2 * (n % a.s_q) + 1);
       } else {
-        limit_s[n] = row_limit(a, n);
+        limit_s[n] = row_limit<kPaged>(a, n);
       }
     }
   }
@@ -269,7 +274,7 @@ __device__ __forceinline__ void plan_rows(const TcDecodeArgs& a, int32_t* keys_s
       const int u = 32 * j + lane;
       int tiles = 0;
       if (u < a.n_units)
-        for (int i = 0; i < a.width && u * a.width + i < a.n_q; ++i)
+        for (int i = 0; i < a.width && (!kPaged || u * a.width + i < a.n_q); ++i)
           tiles = max(tiles, (keys_s[u * a.width + i] + BN - 1) / BN);
       tl[j] = tiles;
       raw += tiles;

@@ -707,13 +707,13 @@ int mla_cache_compact(const mla_state_array* arrays, int32_t n_arrays, const int
  * kv_len_out[b] (may be NULL, may be kv_len) receives kv_len[b] + count.
  *
  * mla_tree_plan: node j < count of row b hangs below node parents[b *
- * parents_row_stride + j] < j (a stride of 0: one tree for every row), or (-1) below the row's last cached key; another
- * value sets MLA_DEVICE_INDEX_OUT_OF_RANGE and counts as -1.  positions[b *
- * n_nodes + j] = kv_len[b] + the node's depth (kv_len NULL: 0), and
- * tree_mask[(b*n_nodes + j)*words + w], words = ceil(n_nodes / 64), has bit
- * i % 64 of word i / 64 set for the node itself and its ancestors i.  A node
- * j >= count gets position kv_len[b] and an empty mask.  n_nodes <=
- * MLA_MAX_TREE_NODES.
+ * parents_row_stride + j] < j (a stride of 0: one tree for every row), or (-1)
+ * below the row's last cached key; another value sets
+ * MLA_DEVICE_INDEX_OUT_OF_RANGE and counts as -1.  positions[b * n_nodes + j] =
+ * kv_len[b] + the node's depth (kv_len NULL: 0), and tree_mask[(b*n_nodes + j)
+ * * words + w], words = ceil(n_nodes / 64), has bit i % 64 of word i / 64 set
+ * for the node itself and its ancestors i.  A node j >= count gets position
+ * kv_len[b] and an empty mask.  n_nodes <= MLA_MAX_TREE_NODES.
  *
  * mla_decode_attend_paged: mla_decode_attend over pages.  The row's last count
  * keys are its new tokens.  Token i < count sees the keys t <= kv_len[b] -
@@ -724,8 +724,9 @@ int mla_cache_compact(const mla_state_array* arrays, int32_t n_arrays, const int
  * key; its selection is not read.  Selections are as in mla_decode_attend and
  * exclude tree_mask (list the ancestors instead).  The workspace is that of
  * mla_decode_workspace_size with t_max = table_width * page_size.
- * bf16 is served for the shapes of mla_decode_attend, with pool pointers
- * 16-byte aligned and strides multiples of 16 bytes.  Page sizes that are
+ * bf16 is served for the shapes of mla_decode_attend, with q, pools and ctx_out
+ * 16-byte aligned, strides multiples of 16 bytes, and a positive q_row_stride if
+ * there is more than one query row (at most 2^20).  Page sizes that are
  * multiples of 8 rows are read by TMA boxes; others, and selections, row by
  * row, which needs page strides that are whole numbers of rows and pools of
  * fewer than 2^31 rows (else MLA_ERR_UNSUPPORTED).  f32 for any shape, at most

@@ -894,7 +894,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               half_max = fmax3(half_max, fabsf(lo_raw), fabsf(hi_raw));
               // sent already scaled (log2 units): the softmax then only adds
               const float2 sc = mul_f32x2(make_float2(lo_raw, hi_raw), make_float2(a.scale_log2, a.scale_log2));
-              const __half2 hv = __floats2half2_rn(fminf(fmaxf(sc.x, -65504.f), 65504.f), fminf(fmaxf(sc.y, -65504.f), 65504.f));
+              // clamped to +-65504 (over pages NaN stays NaN; windows are of finite data, and drop such a key)
+              const __half2 hv = kPaged ? __hmin2_nan(__hmax2_nan(__floats2half2_rn(sc.x, sc.y), __float2half2_rn(-65504.f)), __float2half2_rn(65504.f))
+                                        : __floats2half2_rn(fminf(fmaxf(sc.x, -65504.f), 65504.f), fminf(fmaxf(sc.y, -65504.f), 65504.f));
               w[q] = *reinterpret_cast<const uint32_t*>(&hv);
             }
             *reinterpret_cast<uint4*>(xo + (c * 128 + h) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -1209,7 +1211,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // cache stream would otherwise push the early pieces out to DRAM.
         const float inv = l != 0.f ? 1.f / l : 0.f;
         // m of the piece: -inf marks an empty one, so a sum of NaN alone gets a finite one
-        const float m_piece = l == 0.f ? -CUDART_INF_F : (kQ8 && m_used == -CUDART_INF_F) ? 0.f : m_used - kRaise;
+        const float m_piece = l == 0.f ? -CUDART_INF_F : ((kQ8 || kPaged) && m_used == -CUDART_INF_F) ? 0.f : m_used - kRaise;
         const uint64_t keep = l2_policy_evict_last();
         uint4* dst = a.ws_o + (slot * (RANK / 8) + dim_base / 8) * HEADS + h;
         float vmax = 0.f;

@@ -711,6 +711,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(sa[k]), x[32 + k] = __uint_as_float(sb[k]);
         }
+        // Keys with something that is not finite in this CTA's dims, seen by one token and cleared for the other: NaN for
+        // the one, here and (it crosses with the scores) in the peer.
+        if (kPair && one) {
+          const uint32_t k = tile % kSlots;
+          if (!mbar_wait_warp(&poison_full[k], poison_phase >> k & 1u, kWaitLimit)) { fail(); break; }
+          poison_phase ^= 1u << k;
+          const uint64_t poison = poison_s[k] & valid;
+          if (poison != 0ull) {
+            const uint32_t lo = (uint32_t)poison, hi = (uint32_t)(poison >> 32);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              if (lo >> j & 1u) x[j] = CUDART_NAN_F;
+              if (hi >> j & 1u) x[32 + j] = CUDART_NAN_F;
+            }
+          }
+        }
         // ---- sent to the peer in fp16, once it has read the tile two back
         const uint32_t xb = (tile & 1u) * XH_BYTES;
         if (tile >= 2 && !mbar_wait_warp(&x_free[(tile - 2) % kGroups], (tile - 2) / kGroups & 1u, kWaitLimit)) { fail(); break; }
@@ -744,25 +760,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if (!mbar_wait_warp(&ref_full[before][quarter], (tile - 1) / kGroups & 1u, kWaitLimit)) { fail(); break; }
           m_ref = ref_s[before][h];
         }
-        uint64_t poison = 0;
-        if (kPair && one) {
-          const uint32_t k = tile % kSlots;
-          if (!mbar_wait_warp(&poison_full[k], poison_phase >> k & 1u, kWaitLimit)) { fail(); break; }
-          poison_phase ^= 1u << k;
-          poison = poison_s[k] & valid;
-        }
         // ---- the peer's half (its remote stores complete as transaction bytes on this barrier)
         if (!mbar_wait_warp(&x_full[me], use & 1u, kWaitLimit)) { fail(); break; }
         ++use;
         const uint8_t* const xi = xin + xb + h * 16;
-        if (kPair && poison != 0ull) {   // a key that is not finite, and that the other token does not see: NaN
-          const uint32_t row = smem_u32(xi);
-#pragma unroll 1
-          for (uint64_t left = poison; left != 0ull; left &= left - 1ull) {
-            const int k = __ffsll((long long)left) - 1;
-            st_shared_u16(row + (uint32_t)((k >> 3) * 128 * 16 + (k & 7) * 2), 0x7E00u);
-          }
-        }
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const uint4 i4 = *reinterpret_cast<const uint4*>(xi + c * 128 * 16);

@@ -315,6 +315,118 @@ def test_keys_that_are_not_seen_may_hold_anything(mla, size):
     assert torch.isnan(ctx[7]).any()
 
 
+@pytest.mark.parametrize("size", [64, 24, 5])
+def test_a_key_that_is_not_finite_is_seen_by_some(mla, size):
+    """One element of a key, in either half of the latents or of the rope dims: every token that sees the key gets NaN
+    in its whole result, every other one what it got before, also where two tokens of 64 heads share a tile."""
+    s_q = 9
+    lens = [s_q, 60 + s_q, 64 * 3 + s_q]
+    chain = [list(range(i + 1)) for i in range(s_q)]
+    star = [[0, i] if i else [0] for i in range(s_q)]
+    for heads in (64, 128):
+        for lists in (None, star):
+            c = Case(13, lens, s_q, heads, size, tree=lists is not None)
+            if lists is not None:
+                c.set_nodes(lists * c.B)
+            clean = c.run(mla)
+            assert clean[2] == 0
+            c.check(*clean[:2])
+            for node, dim, value in ((5, 3, "nan"), (4, 300, "nan"), (8, 515, "nan"), (3, 570, "nan"), (1, 511, "inf")):
+                pool, at = (c.latent, dim) if dim < 512 else (c.rope, dim - 512)
+                held = []
+                for b, n in enumerate(lens):
+                    t = n - s_q + node
+                    where = int(c.table[b, t // size]), t % size, at
+                    held.append((where, pool[where].clone()))
+                    pool[where] = float(value)
+                ctx, lse, _ = c.run(mla)
+                for where, was in held:
+                    pool[where] = was
+                hit = [node in (lists or chain)[i] for i in range(s_q)] * c.B
+                for n, seen in enumerate(hit):
+                    if not seen:
+                        assert torch.equal(ctx[n], clean[0][n]) and torch.equal(lse[n], clean[1][n]), (heads, node, n)
+                    elif value == "nan":
+                        assert torch.isnan(ctx[n]).all() and torch.isnan(lse[n]).all(), (heads, node, n)
+                    else:
+                        assert not torch.isfinite(ctx[n, :, at]).any(), (heads, node, n)
+
+
+@pytest.mark.parametrize("size", [64, 16, 5])
+def test_two_tokens_whose_masks_hide_what_is_not_finite(mla, size):
+    """64 heads: siblings that are NaN or infinite, masks that are no tree, an empty one beside a full one."""
+    s_q = 71
+    lens = [s_q, 30 + s_q, 64 + s_q]
+    c = Case(17, lens, s_q, 64, size, counts=[71, 70, 69])
+    rng = np.random.default_rng(4)
+    lists = []
+    for n in range(c.B * s_q):
+        i = n % s_q
+        keep = [j for j in range(s_q) if rng.random() < 0.3 and j not in (3, 40, 66)]
+        lists.append([] if i in (5, 20, 21) else [68] if i == 6 else [3, 40] if i == 7 else keep)
+    c.set_nodes(lists)
+    clean = c.run(mla)
+    assert clean[2] == 0
+    c.check(*clean[:2])
+    for b, n in enumerate(lens):
+        for node, value in ((3, float("nan")), (40, float("inf")), (66, -float("inf"))):
+            t = n - c.counts[b] + node
+            page = int(c.table[b, t // size])
+            c.latent[page, t % size] = value
+            c.rope[page, t % size] = value
+    ctx, lse, _ = c.run(mla)
+    others = torch.tensor([n for n in range(c.B * s_q) if n % s_q != 7], device=DEV)
+    assert torch.equal(ctx[others], clean[0][others]) and torch.equal(lse[others], clean[1][others])
+    assert torch.isnan(ctx[7::s_q]).all()
+
+
+@pytest.mark.parametrize("heads", [64, 128])
+@pytest.mark.parametrize("size,s_q,lens,counts,tree", [
+    (8, 3, [700, 3, 65], None, False),
+    (24, 5, [500, 100], [5, 4], True),
+    (40, 2, [1000, 41, 2], None, False),
+    (192, 7, [193, 1000], None, True),
+    (16, 300, [900, 310], [300, 257], True),
+    (64, 1024, [1500], None, True),
+])
+def test_f32_results_odd_pages_and_large_trees(mla, heads, size, s_q, lens, counts, tree):
+    c = Case(heads + size, lens, s_q, heads, size, counts=counts, tree=tree)
+    ctx, lse, st = c.run(mla, out_dtype=F32)
+    assert st == 0
+    c.check(ctx, lse, rows=sorted({i * (c.B * s_q - 1) // 24 for i in range(25)}))
+
+
+@pytest.mark.parametrize("heads", [64, 128])
+def test_many_short_rows(mla, heads):
+    """Segments of one tile, hundreds of them to a cluster's stream, with rows of nothing between."""
+    rng = np.random.default_rng(6)
+    lens = [int(n) for n in rng.integers(0, 130, 700)]
+    c = Case(81, lens, 2, heads, 16, counts=[min(n, int(k)) for n, k in zip(lens, rng.integers(0, 3, 700))])
+    ctx, lse, st = c.run(mla)
+    assert st == 0
+    c.check(ctx, lse, rows=range(0, 1400, 9))
+
+
+def test_calls_at_once_on_two_streams(mla):
+    """Two attentions and an append into other pages at once, each call with a workspace of its own from the stream that
+    it runs on."""
+    cases = [Case(91, [5000, 900], 3, 128, 16), Case(92, [3000, 64, 1], 8, 64, 64, tree=True)]
+    want = [c.run(mla) for c in cases]
+    lens = [i32(c.lens) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = []
+    for _ in range(20):
+        for c, n, side in zip(cases, lens, streams):
+            with torch.cuda.stream(side):
+                ctx = torch.empty(c.B * c.s_q, c.heads, 512, dtype=BF16, device=DEV)
+                mla.decode_attend_paged(c.q, c.latent, c.rope, c.table, n, c.B, c.s_q, SCALE, ctx, tree_mask=c.mask)
+                outs.append(ctx)
+    torch.cuda.synchronize()
+    for k, ctx in enumerate(outs):
+        assert torch.equal(ctx, want[k % 2][0])
+
+
 @pytest.mark.parametrize("size", [64, 16, 3])
 def test_attend_selected(mla, size):
     s_q, k_max = 2, 200

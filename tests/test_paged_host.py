@@ -84,6 +84,7 @@ ATTEND = [MB, 128 * 576, 576, MB, 512, 512 * 16, MB, 64, 64 * 16, 1, MB, 8, 8, 1
     ({17: MB, 19: 1025, 33: 1 << 60}, 1, "nodes"), ({17: MB + 4}, 1, "8-byte"),
     ({20: 16}, 2, "bf16 is served"), ({21: 256}, 2, "bf16 is served"), ({22: 32}, 2, "bf16 is served"),
     ({17: MB, 23: MB, 24: MB, 25: 4}, 2, "tree_mask"),
+    ({1: 0}, 1, "q_row_stride"), ({18: 1 << 20, 19: 2, 33: 1 << 60}, 1, "2^20"),
     # rows one by one: page strides of whole rows, fewer than 2^31 rows
     ({13: 15, 5: 512 * 16 + 8}, 2, "whole rows"), ({23: MB, 24: MB, 25: 4, 8: 64 * 16 + 8}, 2, "whole rows"),
     ({13: 1, 14: 2 ** 31 - 1, 5: 1024}, 2, "2^31"),

@@ -730,7 +730,9 @@ int mla_cache_compact(const mla_state_array* arrays, int32_t n_arrays, const int
  * multiples of 8 rows are read by TMA boxes; others, and selections, row by
  * row, which needs page strides that are whole numbers of rows and pools of
  * fewer than 2^31 rows (else MLA_ERR_UNSUPPORTED).  f32 for any shape, at most
- * 65535 query rows.
+ * 65535 query rows.  MLA_ERR_UNSUPPORTED also for tables of more than 2^30 keys
+ * a row, and in bf16 for batch * s_q * table_width * page_size of 2^37 and more
+ * (read by boxes with s_q >= 8: 2^39), or a little less.
  *
  * mla_commit_paged: after verification, moves the accepted path of each row's
  * tree to the end of its sequence: for j < counts[b], key kv_len[b] + j of every

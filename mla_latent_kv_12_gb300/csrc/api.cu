@@ -1129,9 +1129,13 @@ int mla_decode_attend_paged(const void* q, int64_t q_row_stride, int64_t q_head_
             "decode_paged: workspace of %zu bytes < %zu needed", workspace_bytes, need);
   MLA_CHECK((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0,
             "decode_paged: workspace must be 256-byte aligned");
+  // A kernel's key index runs up to a few thousand past a row's last key.  (Memory bounds the rows of a window, but a
+  // table may name a page more than once.)
+  const bool too_long = t_max > (1 << 30);
   if (dtype == MLA_DTYPE_F32) {
     if ((int64_t)batch * s_q > 65535)
       return fail(MLA_ERR_UNSUPPORTED, "decode_paged: f32 is served for at most 65535 query rows");
+    if (too_long) return fail(MLA_ERR_UNSUPPORTED, "decode_paged: table_width * page_size above 2^30");
     return cuda_status(launch_simt_decode(g, dtype, out_dtype, workspace, workspace_bytes, (cudaStream_t)stream),
                        "decode_paged launch");
   }
@@ -1146,15 +1150,22 @@ int mla_decode_attend_paged(const void* q, int64_t q_row_stride, int64_t q_head_
   MLA_CHECK(q_row_stride > 0 || (int64_t)batch * s_q == 1, "decode_paged: q_row_stride must be positive");
   MLA_CHECK(num_pages == 1 || (latent_page_stride > 0 && rope_page_stride > 0),
             "decode_paged: page strides must be positive");
-  if (selected_positions || page_size % 8 != 0) {
+  const bool boxes = !selected_positions && page_size % 8 == 0;
+  if (!boxes) {
     const int64_t lp = latent_page_stride / latent_row_stride, rp = rope_page_stride / rope_row_stride;
     if (latent_page_stride % latent_row_stride != 0 || rope_page_stride % rope_row_stride != 0 ||
         lp * (num_pages - 1) + page_size >= (1LL << 31) || rp * (num_pages - 1) + page_size >= (1LL << 31))
       return fail(MLA_ERR_UNSUPPORTED, "decode_paged: selections and page sizes that are no multiple of 8 need page "
                                        "strides of whole rows and fewer than 2^31 rows");
+  }
+  if (too_long) return fail(MLA_ERR_UNSUPPORTED, "decode_paged: table_width * page_size above 2^30");
+  const int64_t units = (int64_t)batch * s_q / (boxes && s_q >= 8 ? 4 : 1) + 1;   // of the split plan, or more
+  if (units * (t_max / 64 + 16) >= (1LL << 31))
+    return fail(MLA_ERR_UNSUPPORTED, "decode_paged: batch %d x s_q %d over tables of %lld keys: more tiles of 64 keys than "
+                                     "a plan holds", batch, s_q, (long long)t_max);
+  if (!boxes)
     return cuda_status(launch_tc_decode(g, out_dtype, workspace, workspace_bytes, (cudaStream_t)stream),
                        "decode_paged (rows) launch");
-  }
   return cuda_status(launch_tc_paged(g, out_dtype, workspace, workspace_bytes, (cudaStream_t)stream),
                      "decode_paged (tensor core) launch");
 }

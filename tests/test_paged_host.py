@@ -99,6 +99,23 @@ def test_attend_refusals(mla, changes, status, needle):
     assert needle in mla.lib.mla_last_error_detail().decode()
 
 
+@pytest.mark.parametrize("changes,needle", [
+    ({11: 1 << 24, 12: (1 << 24) + 1, 13: 64}, "page_table_stride"),
+    ({11: 1 << 25, 12: (1 << 24) + 1, 13: 64}, "2^30"),                             # keys of a row: by boxes, row by row, f32
+    ({11: 1 << 31, 12: (1 << 30) + 1, 13: 1}, "2^30"),
+    ({11: 1 << 25, 12: (1 << 24) + 1, 13: 64, 9: 0, 33: 1 << 60}, "2^30"),
+    ({11: 1 << 21, 12: 1 << 21, 13: 64, 18: 1024, 33: 1 << 60}, "plan"),            # 2^37 keys of all query rows
+    ({11: 1 << 21, 12: 1 << 21, 13: 64, 18: 512, 19: 8, 33: 1 << 60}, "plan"),      # four tokens share a unit
+    ({11: 1 << 21, 12: 1 << 21, 13: 63, 18: 256, 19: 8, 33: 1 << 60}, "plan"),
+])
+def test_attend_refuses_more_keys_than_its_indexes_hold(mla, changes, needle):
+    args = list(ATTEND)
+    for i, v in changes.items():
+        args[i] = v
+    assert mla.lib.mla_decode_attend_paged(*args) == (1 if needle == "page_table_stride" else 2)
+    assert needle in mla.lib.mla_last_error_detail().decode()
+
+
 # parents, stride, kv_len, counts, batch, nodes, positions, mask, status, stream
 PLAN = [MB, 16, MB, None, 4, 16, MB, MB, None, None]
 

@@ -357,7 +357,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     plan_rows<kPaged>(a, plan_keys_s, plan_prefix_s, blockIdx.x == 0, row_start_s, row_limit_s);
     keys_p = plan_keys_s;
     prefix_p = plan_prefix_s;
-    if (blockIdx.x == 0) {   // a copy in the workspace, where the planner launch puts it above 128 rows
+    if (kPaged) {
+      if (blockIdx.x == 0 && warp == 0) store_pieces(a, keys_p, prefix_p);
+    } else if (blockIdx.x == 0) {   // a copy in the workspace, where the planner launch puts it above 128 rows
       for (int i = threadIdx.x; i < a.n_q; i += blockDim.x) a.keys[i] = plan_keys_s[i];
       for (int i = threadIdx.x; i <= a.n_units + 1; i += blockDim.x) a.prefix[i] = plan_prefix_s[i];
     }
@@ -1294,24 +1296,31 @@ __global__ void __launch_bounds__(128) tc_combine_kernel(const __grid_constant__
   // decode CTA passes its own dependency wait before it lets this grid start,
   // so all of those launches have completed.  (The copy of an in-kernel plan
   // that the decode kernel stores is not read: it is visible only after the
-  // wait.)
+  // wait.)  A paged call that plans in its kernel leaves the pieces themselves.
   int keys;
   const int32_t* prefix;
-  if (a.plan_in_kernel) {
-    plan_rows<kPaged>(a, keys_s, prefix_s, false);   // 128 threads >= n_q
-    keys = keys_s[n];
-    prefix = prefix_s;
-  } else {
-    keys = a.keys[n];
-    prefix = a.prefix;
-  }
   int c0 = 0, c1 = 0;
-  if (keys != 0) {
-    const int per = group_span(a, prefix[a.n_units]);
-    c0 = first_group_of(prefix, u, per, prefix[a.n_units + 1]);
-    c1 = last_group_of(prefix, u, per);
+  if (kPaged && a.plan_in_kernel) {
+    pdl_wait();
+    const int pieces = a.keys[n];
+    keys = pieces >= 0;
+    c0 = pieces & 0xFFFF, c1 = pieces >> 16;
+  } else {
+    if (a.plan_in_kernel) {
+      plan_rows<kPaged>(a, keys_s, prefix_s, false);   // 128 threads >= n_q
+      keys = keys_s[n];
+      prefix = prefix_s;
+    } else {
+      keys = a.keys[n];
+      prefix = a.prefix;
+    }
+    if (keys != 0) {
+      const int per = group_span(a, prefix[a.n_units]);
+      c0 = first_group_of(prefix, u, per, prefix[a.n_units + 1]);
+      c1 = last_group_of(prefix, u, per);
+    }
+    pdl_wait();
   }
-  pdl_wait();
   // the token and head of MMA row h (two tokens of 64 heads, or padding from a.heads on)
   int64_t token = n;
   int head = h;

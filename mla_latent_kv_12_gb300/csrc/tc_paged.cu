@@ -12,12 +12,12 @@
 //    chunks of 1024 bytes, 128-byte swizzle, which both MMAs read through their
 //    descriptors' strides (scores: 4096 bytes between groups of 8 keys; P.V:
 //    1024 between chunks of 64 dims).
-//  * Two groups of four softmax warps take the tiles in turn.  A tile's scores
+//  * Three groups of four softmax warps take the tiles in turn.  A tile's scores
 //    are summed and their maximum taken before the reference that the tile
 //    before left is known; the reference is handed on before the exponentials,
-//    so these phases of two tiles overlap.  Each group keeps its own sum, and
-//    the two are joined at the end of a segment, whose context they store half
-//    each.
+//    so these phases of the tiles overlap.  Each group keeps its own sum, and
+//    they are joined at the end of a segment, whose context each stores a
+//    part of.
 //  * kPair: two tokens of 64 heads share the MMA's 128 rows.
 //  * Masks.  A tile that a token sees in part has its scores masked; rows that no
 //    token of the query row sees are cleared before the scores (a probability
@@ -485,6 +485,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (aborted()) break;
         ++seg;
       }
+      if (a.plan_in_kernel && blockIdx.x == 0) store_pieces(a, keys_p, prefix_p);   // (while the last P.V runs)
       if (lane == 0) mma_commit(&pv_drain);
       __syncwarp();
       mbar_wait_warp(&pv_drain, 0, kWaitLimit);
@@ -544,17 +545,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (lane == 0) mbar_arrive(&q_full);
       return true;
     };
-    // This member's next segment behind `it`, or -1.
+    // Whether this member has a segment behind `it`.
     auto next_row = [&]() {
       WorkIter peek = it;
       int u, n, t0, t1;
       bool whole;
       while (peek.next(u, t0, t1, whole))
-        if (member_segment<true>(a, keys_p, u, member, n, t0, t1)) return n;
-      return -1;
+        if (member_segment<true>(a, keys_p, u, member, n, t0, t1)) return true;
+      return false;
     };
     int u, n = 0, t0, t1;
     bool whole, live = false;            // live: row n's segment is still in TMEM
+    bool more = next_row();              // this member has a segment behind `it`
     int64_t slot = 0;
     float m = -CUDART_INF_F, l = 0.f;    // this group's sum l is relative to 2^m
     // (One place each for the query and for the epilogue: code that runs once per segment is fetched cold, and behind
@@ -563,14 +565,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     for (;;) {
       // ---- the coming segment's query, as soon as the last scores of the one before are read (by the group that will
       // read its first scores)
-      if (tile % kGroups == me) {
-        if (next_row() >= 0) {
-          if (tile > 0 && !mbar_wait_warp(&s_free[(tile - 1) % kGroups], (tile - 1) / kGroups & 1u, kWaitLimit)) { fail(); break; }
-          // (and every group has left the segment before this one: its waits on the stages' barriers are over)
-          if (seg > 0 && !mbar_wait_warp(&o_free, (seg - 1) & 1u, kWaitLimit)) { fail(); break; }
-          tc_fence_after();
-          if (!take_query(tile + 2 * (live ? seg + 1 : 0))) { fail(); break; }
-        }
+      if (more && tile % kGroups == me) {
+        if (tile > 0 && !mbar_wait_warp(&s_free[(tile - 1) % kGroups], (tile - 1) / kGroups & 1u, kWaitLimit)) { fail(); break; }
+        // (and every group has left the segment before this one: its waits on the stages' barriers are over)
+        if (seg > 0 && !mbar_wait_warp(&o_free, (seg - 1) & 1u, kWaitLimit)) { fail(); break; }
+        tc_fence_after();
+        if (!take_query(tile + 2 * (live ? seg + 1 : 0))) { fail(); break; }
       }
       if (live) {
         // ---- the groups' sums (their slots are free once every warp has left the segment before)
@@ -592,7 +592,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
           m = top;
         }
-        // ---- epilogue: the segment's last P.V, then this group's half of the context
+        // ---- epilogue: the segment's last P.V, then this group's part of the context
         if (!wait_pv(tile - 1)) { fail(); break; }
         tc_fence_after();
         const bool blind = kPair && limit_of(n, k_token) == 0;
@@ -681,6 +681,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
       }
       if (!live || aborted()) break;
+      more = next_row();
       const Sight sight = kPair ? Sight{} : sight_of(n);
       const int whole_tiles = kPair ? whole_of(n) : 0;
       m = -CUDART_INF_F, l = 0.f;

@@ -304,6 +304,19 @@ __device__ __forceinline__ void plan_rows(const TcDecodeArgs& a, int32_t* keys_s
   __syncthreads();
 }
 
+// The groups that hold a row's pieces, for the combine of a paged call that plans in its kernel (one warp of one CTA; in
+// `keys`, which only the planner launch uses otherwise): first | last << 16, or -1 for a row without keys.  With the
+// plan made again in the combine, as over windows, a tree of 16 nodes behind 4050 keys took 32.1 us
+// instead of 30.6, four of 20 nodes behind 20000 keys 313 instead of 300.
+__device__ __forceinline__ void store_pieces(const TcDecodeArgs& a, const int32_t* keys, const int32_t* prefix) {
+  const int per = group_span(a, prefix[a.n_units]);
+#pragma unroll 1
+  for (int n = threadIdx.x & 31; n < a.n_q; n += 32) {
+    const int u = n / a.width;
+    a.keys[n] = keys[n] > 0 ? first_group_of(prefix, u, per, prefix[a.n_units + 1]) | last_group_of(prefix, u, per) << 16 : -1;
+  }
+}
+
 // The planner launch (more than kMaxRowsInKernelPlan rows), and the merge of
 // the split rows behind a decode kernel.
 cudaError_t launch_split_plan(const TcDecodeArgs& a, cudaStream_t stream);

@@ -71,8 +71,10 @@ constexpr int kLockstep = 4;
 // scores of the unit before, and its context is stored): one tree of 16 nodes behind 4050 keys 33.2 -> 29.8 us, of 64
 // nodes 76 -> 72, of 20 nodes in 4 rows of 20000 309 -> 297; between 3 and 14 the charge itself moves them by 2 %.
 constexpr int kStartCharge = 7, kChargeSpan = 8;
-// Tiles pulled into L2 ahead of their load: farther for a lockstep group.
-constexpr int kPrefetchAheadGroup = 8, kPrefetchAheadRow = 3;
+// Tiles that a row alone pulls into L2 ahead of their load (32 ragged rows 125 us, without 128).  Rows in lockstep read
+// each tile four times as it is, and at the power limit every further request costs clock: verify of 8 x 4 tokens of
+// 65536 in a loop of a second 436 us, 8 ahead 457, 8 ahead by one of the four in turn 441.
+constexpr int kPrefetchAheadGroup = 0, kPrefetchAheadRow = 3;
 
 __device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, uint64_t* bar, int x, int y, int z, int w, int v) {
   asm volatile(
@@ -85,6 +87,25 @@ __device__ __forceinline__ void tma_prefetch_l2_5d(const void* tmap, int x, int 
   asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %3, %4, %5}];"
                ::"l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v)
                : "memory");
+}
+
+// Two values in fp16, those beyond its range +-65504 (NaN stays NaN).
+__device__ __forceinline__ uint32_t pack_f16x2_sat(float lo, float hi) {
+  uint32_t w;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
+}
+
+// (a0 * b0 + c0, a1 * b1 + c1) as one packed f32x2 operation.
+__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
+  uint64_t x, y, z, r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c.x), "f"(c.y));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(r));
+  return d;
 }
 
 // bf16 pairs with infinities and NaN replaced by 0; `found` is set if there was one.
@@ -295,9 +316,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
           if (aborted()) break;
         }
-        // the segment's first tiles that the loop's look-ahead will not cover
-        if (!loads)
-          for (int t = t0 + STAGES; t < t0 + kPrefetchAhead && t < t1; ++t) prefetch_tile(t);
         for (int t = t0; t < t1 && !aborted(); ++t) {
           if (loads) {
             int pg, rw;
@@ -320,7 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             const long long begin = clock64();
             while (loaded_s <= tiles && !abort_s && clock64() - begin < kWaitLimit) __nanosleep(100);
             __syncwarp();
-            if (t + kPrefetchAhead < t1) prefetch_tile(t + kPrefetchAhead);
+            if (kPrefetchAhead > 0 && t + kPrefetchAhead < t1) prefetch_tile(t + kPrefetchAhead);
             if (t == (t1 - kQueryPrefetchTiles > t0 ? t1 - kQueryPrefetchTiles : t0) && lane == 0) {
               // the next segment's query
               WorkIter peek = it;
@@ -502,7 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t xin_peer = mapa(smem_u32(xin), peer) + (uint32_t)h * 16u;
     const uint32_t x_full_peer = mapa(smem_u32(&x_full[me]), peer), x_free_peer = mapa(smem_u32(&x_free[me]), peer);
     uint32_t tile = 0, seg = 0, poison_phase = 0, use = 0;   // use: tiles of this group so far
-    float half_max = 0.f;   // largest |half score| sent, scaled (checked against the fp16 exchange's range)
+    float half_max = 0.f;   // largest |half score| sent (checked against the fp16 exchange's range)
     // P.V(k) of the current segment has completed once its commit arrives on the barrier of its stage: fill k + 2 (seg +
     // 1), two per segment up to this one being queries.  The phase parity identifies the completion: the fill STAGES
     // before has been freed when this is called (this group has waited for a P.V at most kGroups tiles back, and read
@@ -697,7 +715,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         } else {
           valid = seen_of_one(sight, t);
         }
-        // ---- this CTA's partial scores, in f32 and log2 units
+        // ---- this CTA's partial scores, in f32
         if (!mbar_wait_warp(&s_full[me], use & 1u, kWaitLimit)) { fail(); break; }
         tc_fence_after();
         float x[BN];
@@ -737,11 +755,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int k = 8 * c + 2 * q;
-            const float2 sc = mul_f32x2(make_float2(x[k], x[k + 1]), make_float2(a.scale_log2, a.scale_log2));
-            x[k] = sc.x, x[k + 1] = sc.y;
-            // clamped to +-65504 (NaN stays NaN)
-            const __half2 hv = __hmin2_nan(__hmax2_nan(__floats2half2_rn(sc.x, sc.y), __float2half2_rn(-65504.f)), __float2half2_rn(65504.f));
-            w[q] = *reinterpret_cast<const uint32_t*>(&hv);
+            w[q] = pack_f16x2_sat(x[k], x[k + 1]);
           }
           st_async_v4(xin_peer + xb + (uint32_t)(c * 128 * 16), w[0], w[1], w[2], w[3], x_full_peer);
         }
@@ -800,6 +814,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         // arrive ordered by that dependency.
         __syncwarp();
         if (lane == 0) mbar_arrive_remote_relaxed_dep(x_free_peer, __float_as_uint(mx));
+        mx *= a.scale_log2;   // (from here on in log2 units)
         // ---- the reference moves only when the tile's maximum exceeds it by more than the threshold (or on the first
         // visible entry)
         const bool moved = mx != -CUDART_INF_F && (m_ref == -CUDART_INF_F || mx > m_ref + kRescaleThreshold);
@@ -820,7 +835,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         for (int k = 0; k < 8; ++k) ps2[k] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < BN; k += 2) {
-          const float2 xs = add_f32x2(make_float2(x[k], x[k + 1]), make_float2(shift, shift));
+          const float2 xs = fma_f32x2(make_float2(x[k], x[k + 1]), make_float2(a.scale_log2, a.scale_log2), make_float2(shift, shift));
           const float p0 = ex2_approx(xs.x);
           const float p1 = ex2_approx(xs.y);
           ps2[(k >> 1) & 7] = add_f32x2(ps2[(k >> 1) & 7], make_float2(p0, p1));
@@ -858,7 +873,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (aborted()) break;
     }
     // Rows without a query score 0; a key that no token sees holds zeros.
-    if (__any_sync(0xffffffffu, !(half_max <= MLA_FP16_SCORE_LIMIT * a.scale_log2)) && lane == 0 && a.status)
+    if (__any_sync(0xffffffffu, !(half_max <= MLA_FP16_SCORE_LIMIT)) && lane == 0 && a.status)
       atomicOr(a.status, MLA_DEVICE_SCORE_RANGE);
   }
 

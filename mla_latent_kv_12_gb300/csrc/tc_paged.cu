@@ -25,6 +25,15 @@
 //    tokens, a key that only one of them sees may not be cleared: its elements
 //    that are not finite are replaced by 0 and the token that does see it gets
 //    NaN.
+//
+// Measured: 32 rows of 1024 to 32768 keys 127 us (5.0 TB/s; window decode 138),
+// 8 x 4 tokens of 65536 367 to 387 us (1.5 PFLOP/s), 8 trees of 64 nodes behind
+// 8000 to 15000 keys 1072 us (1.5 PFLOP/s), one row of 4096 15.7 us.  With many
+// tokens per key it is bound by the tensor cores (busy in 68 % of the cycles)
+// and, in a loop of a second, by the power limit: verify 430, the trees 1281.
+// Single tokens read at 75 % of the copy rate.  The instructions of the softmax
+// do not bind it: 96 fewer of some 900 that a scheduler issues per tile
+// changed nothing but the clock under that limit (1 %).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math_constants.h>
@@ -64,8 +73,9 @@ static_assert(kGroups * regs_softmax(false) + regs_issue(false) <= (kGroups + 1)
                   kGroups * regs_softmax(true) + regs_issue(true) <= (kGroups + 1) * kRegsLaunch,
               "more registers than the launch has");
 // Up to this many query rows of a batch row go in lockstep, each with a cluster, so that they read a tile at the same
-// time (verify of 8 x 4 tokens of 65536: 396 us, one row at a time 447; 8 trees of 64 nodes behind 8000 to 15000 keys:
-// 1207 us, by two 1237, by eight 1244, alone 1247: eight leave four of 76 clusters idle).
+// time.  By 1, 2, 4, 8 rows: verify of 8 x 4 tokens of 65536 438, 395, 377, 378 us; 8 trees of 64 nodes behind 8000 to
+// 15000 keys 1146, 1110, 1118, 1120; trees of 20 nodes in 4 rows of 20000 332, 307, 300, 309 (eight leave four of 76
+// clusters idle).
 constexpr int kLockstep = 4;
 // A unit's start is charged as this many tiles where the ranges are at least so long (the query waits for the last
 // scores of the unit before, and its context is stored): one tree of 16 nodes behind 4050 keys 33.2 -> 29.8 us, of 64

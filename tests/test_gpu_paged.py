@@ -427,6 +427,58 @@ def test_calls_at_once_on_two_streams(mla):
         assert torch.equal(ctx, want[k % 2][0])
 
 
+@pytest.mark.parametrize("heads", [64, 128])
+@pytest.mark.parametrize("gain", [1, 4, 64, 512])
+def test_scores_at_and_past_the_exchange_range(mla, heads, gain):
+    """Halves of a score up to the documented range meet the bf16 bounds; a larger one sets the flag and no other bit."""
+    c = Case(15, [900, 40, 333], 2, heads, 64)
+    c.q = (c.q.float() * gain).bfloat16()
+    ctx, lse, st = torch.zeros(6, heads, 512, dtype=BF16, device=DEV), torch.zeros(6, heads, device=DEV), status()
+    mla.decode_attend_paged(c.q, c.latent, c.rope, c.table, i32(c.lens), 3, 2, SCALE, ctx, lse, device_status=st)
+    most = 0.0
+    for n in range(6):
+        lat, rope = (P.keys64(p, c.table[n // 2], c.lens[n // 2] - 1 + n % 2) for p in (c.latent, c.rope))
+        q = P.as64(c.q[n])
+        for r in (0, 1):
+            half = q[:, 256 * r:256 * r + 256] @ lat[:, 256 * r:256 * r + 256].T
+            most = max(most, np.abs(half + q[:, 512 + 32 * r:544 + 32 * r] @ rope[:, 32 * r:32 * r + 32].T).max())
+    assert int(st) == (mla.DEVICE_SCORE_RANGE if most > mla.FP16_SCORE_LIMIT else 0)
+    if most <= mla.FP16_SCORE_LIMIT:
+        c.check(ctx, lse)
+    assert torch.isfinite(ctx).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("heads", [64, 128])
+@pytest.mark.parametrize("size", [64, 8])
+def test_halves_past_fp16_are_clamped(mla, heads, size):
+    """One feature of each half decides, with products that fp16 holds exactly or that pass 65504: keys whose clamped
+    halves tie for the largest sum share a row's weight, all others have none."""
+    c = Case(16, [700, 65], 2, heads, size)
+    rng = np.random.default_rng(4)
+    for pool_dim in (0, 256):
+        fill(c.latent[..., pool_dim:pool_dim + 1], c.table, c.lens,
+             torch.from_numpy(rng.integers(-8, 9, (2, 700, 1)).astype(np.float32)).to(DEV))
+    c.q.zero_()
+    c.q[..., 0], c.q[..., 256] = 2.0 ** 14, 2.0 ** 13
+    c.q[:, 1::2] *= -1
+    ctx, lse, st = torch.zeros(4, heads, 512, dtype=BF16, device=DEV), torch.zeros(4, heads, device=DEV), status()
+    mla.decode_attend_paged(c.q, c.latent, c.rope, c.table, i32(c.lens), 2, 2, SCALE, ctx, lse, device_status=st)
+    assert int(st) == mla.DEVICE_SCORE_RANGE
+    for n in range(4):
+        lat = P.keys64(c.latent, c.table[n // 2], c.lens[n // 2] - 1 + n % 2)
+        for h in (0, 1, heads - 1):
+            sign = 1 - 2 * (h % 2)
+            score = sum(np.clip(sign * g * lat[:, d], -65504, 65504) for g, d in ((2.0 ** 14, 0), (2.0 ** 13, 256)))
+            tied = lat[score == score.max()]
+            want = tied.mean(0)
+            # the result's rounding; against it the weights of ties are rounded alike, a piece's context to fp16
+            bound = np.abs(want) * 2.0 ** -8 + np.abs(tied).mean(0) * 2.0 ** -9
+            assert (np.abs(P.as64(ctx[n, h]) - want) <= bound).all()
+            # four roundings of a value near it
+            top = score.max() * SCALE + np.log(len(tied))
+            assert abs(float(lse[n, h]) - top) <= top * 2.0 ** -21
+
+
 @pytest.mark.parametrize("size", [64, 16, 3])
 def test_attend_selected(mla, size):
     s_q, k_max = 2, 200

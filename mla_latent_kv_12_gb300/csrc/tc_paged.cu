@@ -530,7 +530,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t xin_peer = mapa(smem_u32(xin), peer) + (uint32_t)h * 16u;
     const uint32_t x_full_peer = mapa(smem_u32(&x_full[me]), peer), x_free_peer = mapa(smem_u32(&x_free[me]), peer);
     uint32_t tile = 0, seg = 0, poison_phase = 0, use = 0;   // use: tiles of this group so far
-    float half_max = 0.f;   // largest |half score| sent (checked against the fp16 exchange's range)
+    float half_max = 0.f;   // the segment's largest |half score| (checked against the fp16 exchange's range)
     // P.V(k) of the current segment has completed once its commit arrives on the barrier of its stage: fill k + 2 (seg +
     // 1), two per segment up to this one being queries.  The phase parity identifies the completion: the fill STAGES
     // before has been freed when this is called (this group has waited for a P.V at most kGroups tiles back, and read
@@ -625,6 +625,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         tc_fence_after();
         const bool blind = kPair && limit_of(n, k_token) == 0;
         if (blind) l = 0.f;
+        // (Rows without a query score 0, a key that no token of the row sees holds zeros; the query of a token that sees
+        // nothing may hold anything.)
+        if (__any_sync(0xffffffffu, !blind && !(half_max <= MLA_FP16_SCORE_LIMIT)) && lane == 0 && a.status)
+          atomicOr(a.status, MLA_DEVICE_SCORE_RANGE);
+        half_max = 0.f;
         auto drain_o = [&](auto&& store_chunk) {   // of DV / 32 chunks of 32 columns, those of this group
   #pragma unroll 1
           for (int c = (int)me; c < DV / 32; c += kGroups) {
@@ -740,12 +745,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(sa[k]), x[32 + k] = __uint_as_float(sb[k]);
         }
-        // Keys with something that is not finite in this CTA's dims, seen by one token and cleared for the other: NaN for
-        // the one, here and (it crosses with the scores) in the peer.
+        // Keys that the other token alone sees: no scores of this one (they would count for the exchange's range).  Keys
+        // with something that is not finite in this CTA's dims, seen by one token and cleared for the other: NaN for the
+        // one, here and (it crosses with the scores) in the peer.
         if (kPair && one) {
           const uint32_t k = tile % kSlots;
           if (!mbar_wait_warp(&poison_full[k], poison_phase >> k & 1u, kWaitLimit)) { fail(); break; }
           poison_phase ^= 1u << k;
+          {
+            const uint32_t lo = (uint32_t)valid, hi = (uint32_t)(valid >> 32);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = lo >> j & 1u ? x[j] : 0.f, x[32 + j] = hi >> j & 1u ? x[32 + j] : 0.f;
+          }
           const uint64_t poison = poison_s[k] & valid;
           if (poison != 0ull) {
             const uint32_t lo = (uint32_t)poison, hi = (uint32_t)(poison >> 32);
@@ -882,9 +893,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
       if (aborted()) break;
     }
-    // Rows without a query score 0; a key that no token sees holds zeros.
-    if (__any_sync(0xffffffffu, !(half_max <= MLA_FP16_SCORE_LIMIT)) && lane == 0 && a.status)
-      atomicOr(a.status, MLA_DEVICE_SCORE_RANGE);
   }
 
   // ---------------------------------------------------------------- teardown

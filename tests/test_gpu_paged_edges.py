@@ -1,0 +1,102 @@
+"""The paged attention's flags and edges on the GPU: what no token sees raises no flag, selections beside freed pages and
+bad positions, pages of one row inside wider rows, workspaces of the size asked for, repeated calls."""
+import numpy as np
+import pytest
+import torch
+
+from tests import paged_reference as P
+from tests.test_gpu_paged import DEV, F32, SCALE, Case, fill, i32, normal, gen, status
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def mla():
+    from mla_latent_kv_12_gb300 import mla
+    return mla
+
+
+def attend(mla, c, **kw):
+    """Case.run with every bit of the status."""
+    n_q = c.B * c.s_q
+    ctx = torch.full((n_q, c.heads, c.rank), 7.0, dtype=c.dtype, device=DEV)
+    lse, st = torch.full((n_q, c.heads), 7.0, device=DEV), status()
+    mla.decode_attend_paged(c.q, c.latent, c.rope, c.table, i32(c.lens), c.B, c.s_q, SCALE, ctx, lse, counts=c.counts_d,
+                            tree_mask=c.mask, device_status=st, **kw)
+    return ctx, lse, int(st)
+
+
+# ---------------------------------------------------------------- the score range
+
+@pytest.mark.parametrize("heads", [64, 128])
+@pytest.mark.parametrize("size", [64, 16, 7])
+@pytest.mark.parametrize("tree", [False, True])
+def test_tokens_that_are_not_there_set_no_flag(mla, heads, size, tree):
+    """A padded batch: the query memory of tokens at and past a row's count holds anything."""
+    lens, counts = [700, 64, 300, 130, 1], [3, 1, 0, 5, 1]
+    c = Case(heads + size, lens, 5, heads, size, counts=counts, tree=tree)
+    clean = attend(mla, c)
+    assert clean[2] == 0
+    c.check(*clean[:2])
+    there = torch.tensor([i < counts[b] for b in range(5) for i in range(5)], device=DEV)
+    for value in (3000.0, 1e30, float("inf"), float("nan")):
+        c.q[~there] = value
+        ctx, lse, st = attend(mla, c)
+        assert st == 0, value
+        assert torch.equal(ctx, clean[0]) and torch.equal(lse, clean[1])
+
+
+@pytest.mark.parametrize("heads", [64, 128])
+@pytest.mark.parametrize("size", [64, 8, 7])
+def test_large_keys_that_a_token_does_not_see_set_no_flag(mla, heads, size):
+    """A sibling that only one token sees, whose query is 0: its large finite key is nobody's large score.  Seen by a
+    token with a query, it is."""
+    s_q, big = 6, 5
+    lens = [s_q, 61 + s_q, 500]
+    star = [[0, i] if i else [0] for i in range(s_q)]
+    chain = [list(range(i + 1)) for i in range(s_q)]
+    for lists in (star, chain):
+        c = Case(23, lens, s_q, heads, size, tree=True)
+        c.set_nodes(lists * 3)
+        c.q.view(3, s_q, heads, 576)[:, big] = 0
+        clean = attend(mla, c)
+        assert clean[2] == 0
+        c.check(*clean[:2])
+        for b, n in enumerate(lens):
+            t = n - s_q + big
+            c.latent[int(c.table[b, t // size]), t % size] = 3000.0
+        ctx, lse, st = attend(mla, c)
+        assert st == 0
+        others = torch.tensor([n for n in range(3 * s_q) if n % s_q != big], device=DEV)
+        assert torch.equal(ctx[others], clean[0][others]) and torch.equal(lse[others], clean[1][others])
+        # one head of that token in one row, on one feature of either half
+        for dim in (1, 300):
+            c.q[s_q + big, heads - 1, dim] = 1.0
+            assert attend(mla, c)[2] == mla.DEVICE_SCORE_RANGE
+            c.q[s_q + big, heads - 1, dim] = 0
+        assert attend(mla, c)[2] == 0
+
+
+@pytest.mark.parametrize("heads", [64, 128])
+def test_a_large_score_in_any_tile_sets_the_flag(mla, heads):
+    """One key of a row, one token and head: in a whole tile, in the last one, in a row behind padding."""
+    lens, counts, s_q = [400, 200, 131], [3, 0, 1], 3
+    for b, t, i in ((0, 3, 0), (0, 397, 0), (0, 399, 2), (2, 5, 0), (2, 130, 0)):
+        c = Case(29, lens, s_q, heads, 16, counts=counts)
+        c.q[..., 7] = 0
+        page = int(c.table[b, t // 16])
+        c.latent[page, t % 16, 7] = 1000.0
+        assert attend(mla, c)[2] == 0
+        c.q[b * s_q + i, 11, 7] = 1.0
+        assert attend(mla, c)[2] == mla.DEVICE_SCORE_RANGE, (b, t, i)
+
+
+def test_calls_repeat_bit_for_bit(mla):
+    for case in (Case(41, [4096], 1, 128, 64), Case(42, [9000, 300, 5000], 4, 128, 16), Case(43, [3000, 700], 90, 64, 64),
+                 Case(44, [4000], 16, 128, 64, tree=True), Case(45, [2000, 900], 64, 128, 32, tree=True),
+                 Case(46, [900, 80], 5, 64, 7)):
+        first = attend(mla, case)
+        for _ in range(5):
+            again = attend(mla, case)
+            assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1]) and again[2] == first[2]

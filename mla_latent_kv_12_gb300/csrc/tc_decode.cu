@@ -143,25 +143,29 @@ __device__ __forceinline__ void gather_key_group(const TcDecodeArgs& a, const CU
 }
 
 // The same over pages: the four rows are found through the row's page table.
-// Entries past the count, or that name a key out of range, load the row's first
-// key; a page outside the pool (flagged) is read as page 0.
+// Entries past the count, or that name a key out of range (flagged), load the
+// pool's first row and need no page; a page outside the pool (flagged) is read
+// as page 0.
 __device__ __forceinline__ void gather_paged_group(const TcDecodeArgs& a, const CUtensorMap* lat_rows_map,
                                                    const CUtensorMap* rope_rows_map, uint8_t* dst, uint64_t* bar, int g,
                                                    int t, int limit, int keys, const int32_t* table,
                                                    const int32_t* list, uint32_t rank, int dim_base) {
   int lr[4], rr[4], pos[4], page[4], row[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int e = t * BN + 4 * g + j;
-    pos[j] = e < keys ? (list ? __ldg(list + e) : e) : 0;
-  }
   bool bad = false;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    if (pos[j] < 0 || pos[j] >= limit) bad = true, pos[j] = 0;
-    const int at = pos[j] / a.page_size;
-    row[j] = pos[j] - at * a.page_size;
-    page[j] = __ldg(table + at);
+    const int e = t * BN + 4 * g + j;
+    pos[j] = e < keys ? (list ? __ldg(list + e) : e) : -1;
+    if (pos[j] < 0 || pos[j] >= limit) bad |= e < keys, pos[j] = -1;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    page[j] = row[j] = 0;
+    if (pos[j] >= 0) {
+      const int at = pos[j] / a.page_size;
+      row[j] = pos[j] - at * a.page_size;
+      page[j] = __ldg(table + at);
+    }
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {

@@ -100,3 +100,35 @@ def test_calls_repeat_bit_for_bit(mla):
         for _ in range(5):
             again = attend(mla, case)
             assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1]) and again[2] == first[2]
+
+
+# ---------------------------------------------------------------- selections
+
+def selection(c, rng, lows, counts, k_max):
+    """Positions of each row from ``lows`` on, a multiset in any order."""
+    sel = np.stack([rng.integers(low, n, k_max) for low, n in zip(lows, c.lens)]).astype(np.int32)
+    lists = [None if k == -1 else sel[b, :k].astype(np.int64) for b, k in enumerate(counts)]
+    return torch.from_numpy(sel).to(DEV), i32(counts), lists
+
+
+@pytest.mark.parametrize("heads,dtype", [(64, BF16), (128, BF16), (3, F32)])
+@pytest.mark.parametrize("size", [64, 16, 3])
+def test_selections_that_need_no_first_page(mla, heads, dtype, size):
+    """The pages of a row's first keys are freed; its selection names none of their keys, in numbers that fill a tile,
+    end inside one, or are one."""
+    shape = {} if dtype == BF16 else dict(rank=40, rope=8, dtype=F32)
+    counts = [200, 64, 1, 130, 65]
+    c = Case(50 + size, [1000, 500, 400, 900, 300], 1, heads, size, **shape)
+    sel, cnt, lists = selection(c, np.random.default_rng(1), [64] * 5, counts, 200)
+    for b in range(5):
+        c.table[b, :64 // size] = -1 if b % 2 else 10 ** 6
+    n = c.B * c.s_q
+    ctx, lse, st = attend(mla, c, sel=sel, sel_count=cnt)
+    assert st == 0
+    whole = c.table.clone()
+    c.table[:, :64 // size] = 0                       # (the reference reads the row's pages whole)
+    c.check(ctx, lse, rows=range(n), lists=lists)
+    # the page of a key that is named is still needed
+    c.table.copy_(whole)
+    sel[1, 5] = 0
+    assert attend(mla, c, sel=sel, sel_count=cnt)[2] == mla.DEVICE_INDEX_OUT_OF_RANGE

@@ -269,9 +269,9 @@ __global__ void __launch_bounds__(1024) tc_plan_kernel(const __grid_constant__ T
 // kPaged: the instance with the extra gather warps over pages, row by row
 // (tc_paged.cu reads whole pieces of pages): selections, and page sizes that
 // such pieces do not fit.  A token of a tree sees some keys of its last tiles
-// only; rows of a tile that its token does not see are cleared before the
-// scores: a probability of 0 must not meet what another token, or nobody, left
-// there.
+// only; rows of a tile that its token does not see, or that a selection names
+// by no position of a key, are cleared before the scores: a probability of 0
+// must not meet what another token, or nobody, left there.
 template <int kPrefetchAhead, int kThreads, bool kLateP, bool kQ8 = false, bool kPaged = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_decode_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_constant__ CUtensorMap rope_map,
@@ -394,10 +394,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int keys = keys_p[n];
       const uint64_t* mask = kPaged ? tree_of(a, n) : nullptr;
       const int first = !kPaged || !mask ? keys : a.plan_in_kernel ? row_start_s[n] : paged_first(a, n / a.s_q);
+      const int32_t* list = kPaged && a.sel && a.sel_count[n] != -1 ? a.sel + (int64_t)n * a.k_max : nullptr;
+      const int limit = !list ? 0 : a.plan_in_kernel ? row_limit_s[n] : row_limit<kPaged>(a, n);
+      int pos0 = -1, pos1 = -1;   // positions of the lane's two entries, read a tile ahead
+      auto look = [&](int t) {
+        const int e = t * BN + lane;
+        pos0 = e < keys ? __ldg(list + e) : -1;
+        pos1 = e + 32 < keys ? __ldg(list + e + 32) : -1;
+      };
+      if (kPaged && list) look(t0);
       if (!mbar_wait_warp(&q_full, seg & 1u, kWaitLimit)) { fail(); break; }
       for (int t = t0; t < t1; ++t) {
         uint64_t seen = ~0ull;
-        if (kPaged && (t + 1) * BN > min(keys, first)) seen = paged_seen(t * BN, keys, first, mask, a.tree_words);
+        if (kPaged && list) {   // positions out of range hold another key's row
+          seen = (uint64_t)__ballot_sync(0xffffffffu, pos0 >= 0 && pos0 < limit) |
+                 (uint64_t)__ballot_sync(0xffffffffu, pos1 >= 0 && pos1 < limit) << 32;
+          if (t + 1 < t1) look(t + 1);
+        } else if (kPaged && (t + 1) * BN > min(keys, first)) {
+          seen = paged_seen(t * BN, keys, first, mask, a.tree_words);
+        }
         if (!mbar_wait_warp(&full_bar[stage], phase, kWaitLimit)) { fail(); break; }
         if (kPaged && seen != ~0ull) {
           uint8_t* st = stages + stage * STAGE_BYTES;

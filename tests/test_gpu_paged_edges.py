@@ -132,3 +132,37 @@ def test_selections_that_need_no_first_page(mla, heads, dtype, size):
     c.table.copy_(whole)
     sel[1, 5] = 0
     assert attend(mla, c, sel=sel, sel_count=cnt)[2] == mla.DEVICE_INDEX_OUT_OF_RANGE
+
+
+@pytest.mark.parametrize("heads,dtype", [(64, BF16), (128, BF16), (3, F32)])
+@pytest.mark.parametrize("size", [64, 16, 3])
+def test_bad_positions_meet_no_key(mla, heads, dtype, size):
+    """Positions out of range in any place of a selection: flagged and left out, whatever the row's first key and the
+    pool's first row hold."""
+    shape = {} if dtype == BF16 else dict(rank=40, rope=8, dtype=F32)
+    counts = [200, 64, 2, 70]
+    c = Case(60 + size, [1000, 500, 400, 90], 1, heads, size, **shape)
+    sel, cnt, lists = selection(c, np.random.default_rng(2), [1] * 4, counts, 200)
+    for value in (float("nan"), float("inf"), 3e4):
+        for b in range(4):
+            c.latent[int(c.table[b, 0]), 0] = value
+            c.rope[int(c.table[b, 0]), 0] = value
+        pool_row = c.latent[0, 0].clone()
+        owner = [(b, int(k)) for b in range(4) for k in (c.table[b] == 0).nonzero().flatten()[:1]]
+        if not any(k * size in lists[b] for b, k in owner):
+            c.latent[0, 0] = value
+        assert attend(mla, c, sel=sel, sel_count=cnt)[2] == 0
+        held = sel.clone()
+        sel[0, [0, 63, 64, 199]] = i32([-1, 1000, 2 ** 31 - 1, -2 ** 31])
+        sel[1, 7], sel[2, 1], sel[3, 64:70] = 500, 400, -7
+        left = [np.delete(lists[0], [0, 63, 64, 199]), np.delete(lists[1], 7), lists[2][:1], lists[3][:64]]
+        ctx, lse, st = attend(mla, c, sel=sel, sel_count=cnt)
+        assert st == mla.DEVICE_INDEX_OUT_OF_RANGE
+        c.check(ctx, lse, lists=left)
+        sel.copy_(held)
+        c.latent[0, 0] = pool_row
+    # nothing but bad positions: no key at all
+    sel[2, :2] = -1
+    ctx, lse, st = attend(mla, c, sel=sel, sel_count=cnt)
+    assert st == mla.DEVICE_INDEX_OUT_OF_RANGE
+    assert (ctx[2] == 0).all() and torch.isneginf(lse[2]).all()

@@ -117,6 +117,17 @@ mla_stream_t stream_for(PyObject* stream, const int64_t* device_of_arrays, Ts...
   return static_cast<mla_stream_t>(p);
 }
 
+// The interpreter's lock is released during a call of the library: its launches wait while the stream's queue is full,
+// and what empties that queue may need another Python thread.
+template <typename F>
+int unlocked(F&& call) {
+  struct Lock {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Lock() { PyEval_RestoreThread(state); }
+  } lock;
+  return call();
+}
+
 PyObject* finish(int status) {
   if (status == MLA_OK) Py_RETURN_NONE;
   PyObject* e = PyObject_CallFunction(g_error, "is", status, mla_last_error_detail());
@@ -167,12 +178,14 @@ PyObject* append_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     need_int32(positions, batch * s);
     need_status(status);
     const mla_stream_t stream = stream_for(a[13], nullptr, &raw, &raw_rope, &gain, &latent, &rope, &table, &len, out, positions, counts, status);
-    return finish(mla_append_paged(
-        raw.data_ptr(), raw.stride(0), raw.stride(1), raw_rope.data_ptr(), raw_rope.stride(0), raw_rope.stride(1),
-        dtype_of(raw), gain.data_ptr(), eps, theta, data<int32_t>(positions), latent.data_ptr(), l.row, l.page,
-        rope.data_ptr(), r.row, r.page, dtype_of(latent), t.data, t.row, t.width, l.page_size, l.pages,
-        data<int32_t>(len), data<int32_t>(counts), data<int32_t>(out), size32(batch), size32(s), size32(rank), r.features,
-        data<int32_t>(status), stream));
+    return finish(unlocked([&] {
+      return mla_append_paged(
+          raw.data_ptr(), raw.stride(0), raw.stride(1), raw_rope.data_ptr(), raw_rope.stride(0), raw_rope.stride(1),
+          dtype_of(raw), gain.data_ptr(), eps, theta, data<int32_t>(positions), latent.data_ptr(), l.row, l.page,
+          rope.data_ptr(), r.row, r.page, dtype_of(latent), t.data, t.row, t.width, l.page_size, l.pages,
+          data<int32_t>(len), data<int32_t>(counts), data<int32_t>(out), size32(batch), size32(s), size32(rank), r.features,
+          data<int32_t>(status), stream);
+    }));
   });
 }
 
@@ -192,9 +205,11 @@ PyObject* tree_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     need_int32(&positions, batch * nodes);
     need_status(status);
     const mla_stream_t stream = stream_for(a[6], nullptr, &parents, len, &positions, &mask, counts, status);
-    return finish(mla_tree_plan(data<int32_t>(parents), parents.stride(0), data<int32_t>(len), data<int32_t>(counts),
-                                size32(batch), size32(nodes), data<int32_t>(positions), data<uint64_t>(mask),
-                                data<int32_t>(status), stream));
+    return finish(unlocked([&] {
+      return mla_tree_plan(data<int32_t>(parents), parents.stride(0), data<int32_t>(len), data<int32_t>(counts),
+                           size32(batch), size32(nodes), data<int32_t>(positions), data<uint64_t>(mask),
+                           data<int32_t>(status), stream);
+    }));
   });
 }
 
@@ -237,12 +252,14 @@ PyObject* decode_attend_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     NEED(ws.element_size() == 1 && ws.is_contiguous(), "workspace: contiguous bytes");
     const mla_stream_t stream =
         stream_for(a[16], nullptr, &q, &latent, &rope, &table, &len, &ctx, lse, counts, mask, sel, sel_count, &ws, status);
-    return finish(mla_decode_attend_paged(
-        q.data_ptr(), q.stride(0), q.stride(1), latent.data_ptr(), l.row, l.page, rope.data_ptr(), r.row, r.page,
-        dtype_of(q), t.data, t.row, t.width, l.page_size, l.pages, data<int32_t>(len), data<int32_t>(counts),
-        data<uint64_t>(mask), batch, s, size32(heads), l.features, r.features, data<int32_t>(sel),
-        sel ? data<int32_t>(sel_count) : nullptr, k_max, scale, ctx.data_ptr(), ctx.stride(0), ctx.stride(1), dtype_of(ctx),
-        data<float>(lse), ws.data_ptr(), (size_t)ws.numel(), data<int32_t>(status), stream));
+    return finish(unlocked([&] {
+      return mla_decode_attend_paged(
+          q.data_ptr(), q.stride(0), q.stride(1), latent.data_ptr(), l.row, l.page, rope.data_ptr(), r.row, r.page,
+          dtype_of(q), t.data, t.row, t.width, l.page_size, l.pages, data<int32_t>(len), data<int32_t>(counts),
+          data<uint64_t>(mask), batch, s, size32(heads), l.features, r.features, data<int32_t>(sel),
+          sel ? data<int32_t>(sel_count) : nullptr, k_max, scale, ctx.data_ptr(), ctx.stride(0), ctx.stride(1), dtype_of(ctx),
+          data<float>(lse), ws.data_ptr(), (size_t)ws.numel(), data<int32_t>(status), stream);
+    }));
   });
 }
 
@@ -262,9 +279,11 @@ PyObject* commit_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     need_int32(out, batch);
     need_status(status);
     const mla_stream_t stream = stream_for(a[11], &device, &table, &len, &path, &counts, out, status);
-    return finish(mla_commit_paged(arrays, n_arrays, t.data, t.row, t.width, page_size, pages, data<int32_t>(len),
-                                   data<int32_t>(path), path.stride(0), size32(path.size(1)), data<int32_t>(counts),
-                                   data<int32_t>(out), size32(batch), data<int32_t>(status), stream));
+    return finish(unlocked([&] {
+      return mla_commit_paged(arrays, n_arrays, t.data, t.row, t.width, page_size, pages, data<int32_t>(len),
+                              data<int32_t>(path), path.stride(0), size32(path.size(1)), data<int32_t>(counts),
+                              data<int32_t>(out), size32(batch), data<int32_t>(status), stream);
+    }));
   });
 }
 

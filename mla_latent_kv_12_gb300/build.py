@@ -4,7 +4,8 @@ cache) with the host compiler.
 Each ``csrc/*.cu`` translation unit is compiled in parallel, then linked into
 ``mla_latent_kv_12_gb300/libmla.so``.  Objects go to ``_build/`` next to it.
 A unit is recompiled when it, or any header under ``csrc/`` or ``include/``,
-is newer than its object.
+is newer than its object; the binding also when torch or Python are others
+than those it was built for.
 """
 from __future__ import annotations
 
@@ -48,6 +49,21 @@ def _compile(src: str, obj: str, log: str) -> tuple[str, int, str]:
     return src, r.returncode, r.stdout + r.stderr
 
 
+def _native_tag() -> str:
+    import torch
+    return "\n".join((torch.__version__, os.path.dirname(torch.__file__), str(sysconfig.get_config_var("SOABI"))))
+
+
+def _native_stale(obj: str, tag: str) -> bool:
+    if not all(map(os.path.exists, (obj, tag, NATIVE))):
+        return True
+    with open(tag) as f:
+        if f.read() != _native_tag():
+            return True
+    sources = os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "mla.h")
+    return os.path.getmtime(obj) < max(map(os.path.getmtime, sources))
+
+
 def _compile_native(obj: str, log: str) -> tuple[str, int, str]:
     import torch
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
@@ -85,9 +101,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if force or not os.path.exists(o) or os.path.getmtime(o) < max(os.path.getmtime(s), hdr):
             jobs.append((s, o, o + ".log"))
     native_obj = os.path.join(BUILD, "binding.o")
-    native_src = os.path.join(CSRC, "binding.cpp")
-    native_stale = force or not os.path.exists(native_obj) or os.path.getmtime(native_obj) < max(
-        os.path.getmtime(native_src), os.path.getmtime(os.path.join(ROOT, "include", "mla.h")))
+    native_tag = os.path.join(BUILD, "binding.tag")   # what a finished binding was built for
+    native_stale = force or _native_stale(native_obj, native_tag)
+    if native_stale and os.path.exists(native_tag):
+        os.remove(native_tag)
     if jobs or native_stale:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
             native = ex.submit(_compile_native, native_obj, native_obj + ".log") if native_stale else None
@@ -111,8 +128,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
         os.replace(tmp, LIB)
-    if native_stale or not os.path.exists(NATIVE):
+    if native_stale:
         _link_native(native_obj)
+        with open(native_tag, "w") as f:
+            f.write(_native_tag())
     return LIB
 
 

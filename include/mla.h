@@ -728,8 +728,9 @@ int mla_cache_compact(const mla_state_array* arrays, int32_t n_arrays, const int
  * 16-byte aligned, strides multiples of 16 bytes, and a positive q_row_stride if
  * there is more than one query row (at most 2^20).  Page sizes that are
  * multiples of 8 rows are read by TMA boxes; others, and selections, row by
- * row, which needs page strides that are whole numbers of rows and pools of
- * fewer than 2^31 rows (else MLA_ERR_UNSUPPORTED).  f32 for any shape, at most
+ * row, which needs page strides that are whole numbers of rows (of any width
+ * where a page is one row) and pools of fewer than 2^31 rows (else
+ * MLA_ERR_UNSUPPORTED).  f32 for any shape, at most
  * 65535 query rows.  MLA_ERR_UNSUPPORTED also for tables of more than 2^30 keys
  * a row, and in bf16 for batch * s_q * table_width * page_size of 2^37 and more
  * (read by boxes with s_q >= 8: 2^39), or a little less.

@@ -1152,6 +1152,11 @@ int mla_decode_attend_paged(const void* q, int64_t q_row_stride, int64_t q_head_
             "decode_paged: page strides must be positive");
   const bool boxes = !selected_positions && page_size % 8 == 0;
   if (!boxes) {
+    // (A page of one row: its row stride is no distance between rows.)
+    if (page_size == 1 && latent_page_stride % latent_row_stride != 0 && latent_page_stride >= rank)
+      g.latent_row_stride = latent_row_stride = latent_page_stride;
+    if (page_size == 1 && rope_page_stride % rope_row_stride != 0 && rope_page_stride >= rope_dim)
+      g.rope_row_stride = rope_row_stride = rope_page_stride;
     const int64_t lp = latent_page_stride / latent_row_stride, rp = rope_page_stride / rope_row_stride;
     if (latent_page_stride % latent_row_stride != 0 || rope_page_stride % rope_row_stride != 0 ||
         lp * (num_pages - 1) + page_size >= (1LL << 31) || rp * (num_pages - 1) + page_size >= (1LL << 31))

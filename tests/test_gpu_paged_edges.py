@@ -166,3 +166,44 @@ def test_bad_positions_meet_no_key(mla, heads, dtype, size):
     ctx, lse, st = attend(mla, c, sel=sel, sel_count=cnt)
     assert st == mla.DEVICE_INDEX_OUT_OF_RANGE
     assert (ctx[2] == 0).all() and torch.isneginf(lse[2]).all()
+
+
+# ---------------------------------------------------------------- pages of one row
+
+@pytest.mark.parametrize("heads", [64, 128])
+def test_pages_of_one_row_inside_wider_rows(mla, heads):
+    """A pool [pages, width] seen as pages of one row: the stride of the page axis alone says where a row lies."""
+    lens, s_q = [300, 64, 5], 3
+    for tree in (False, True):
+        c = Case(70, lens, s_q, heads, 1, tree=tree)
+        clean = attend(mla, c)
+        assert clean[2] == 0
+        c.check(*clean[:2])
+        wide = torch.full((c.latent.shape[0], 712), float("nan"), dtype=BF16, device=DEV)
+        wide[:, 32:544], wide[:, 600:664] = c.latent[:, 0], c.rope[:, 0]
+        held = c.latent, c.rope
+        c.latent, c.rope = wide[:, 32:544].unsqueeze(1), wide[:, 600:664].unsqueeze(1)
+        assert c.latent.stride() == (712, 512, 1) and c.rope.stride() == (712, 64, 1)
+        ctx, lse, st = attend(mla, c)
+        assert st == 0 and torch.equal(ctx, clean[0]) and torch.equal(lse, clean[1])
+    sel = torch.arange(3 * s_q * 70, device=DEV, dtype=torch.int32).view(3 * s_q, 70).remainder(5).clamp(max=2)
+    cnt = i32([70, 65, 1] * 3)
+    got = attend(mla, c_without_tree(c), sel=sel, sel_count=cnt)
+    c.latent, c.rope = held
+    want = attend(mla, c, sel=sel, sel_count=cnt)
+    assert got[2] == want[2] == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # append and commit over the same views
+    g = gen(3)
+    raw, raw_rope = normal(g, 3, 2, 512).bfloat16(), normal(g, 3, 2, 64).bfloat16()
+    gain = torch.ones(512, device=DEV).bfloat16()
+    for latent, rope in (held, (wide[:, 32:544].unsqueeze(1), wide[:, 600:664].unsqueeze(1))):
+        mla.append_paged(raw, raw_rope, gain, 1e-6, 1e4, latent, rope, c.table, i32([n - 2 for n in lens]))
+        mla.commit_paged([latent, rope], c.table, i32([n - 3 for n in lens]), i32([[1]] * 3), i32([1, 0, 1]))
+    assert torch.equal(torch.nan_to_num(wide[:, 32:544]), torch.nan_to_num(held[0][:, 0]))
+    assert torch.equal(torch.nan_to_num(wide[:, 600:664]), torch.nan_to_num(held[1][:, 0]))
+    assert torch.isnan(wide[:, :32]).all() and torch.isnan(wide[:, 544:600]).all() and torch.isnan(wide[:, 664:]).all()
+
+
+def c_without_tree(c):
+    c.nodes = c.mask = None
+    return c

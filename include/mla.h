@@ -722,8 +722,11 @@ int mla_cache_compact(const mla_state_array* arrays, int32_t n_arrays, const int
  * whose bit is set (any bits, a tree or not).  Keys that a token does not see
  * have no part in its result, whatever they hold.  A token i >= count sees no
  * key; its selection is not read.  Selections are as in mla_decode_attend and
- * exclude tree_mask (list the ancestors instead).  The workspace is that of
- * mla_decode_workspace_size with t_max = table_width * page_size.
+ * exclude tree_mask (list the ancestors instead).  The workspace holds
+ * mla_decode_paged_workspace_size(...) bytes (256-byte aligned) with t_max =
+ * table_width * page_size; in bf16 that is 8 bytes a query row and, whatever
+ * their number, at most 129 KB for each of the GPU's SMs (20 MB).
+ * mla_decode_workspace_size, which grows by 129 KB a query row, is never less.
  * bf16 is served for the shapes of mla_decode_attend, with q, pools and ctx_out
  * 16-byte aligned, strides multiples of 16 bytes, and a positive q_row_stride if
  * there is more than one query row (at most 2^20).  Page sizes that are
@@ -762,6 +765,8 @@ int mla_append_paged(const void* latent_raw, int64_t latent_raw_row_stride, int6
 int mla_tree_plan(const int32_t* parents, int64_t parents_row_stride, const int32_t* kv_len,
                   const int32_t* token_counts, int32_t batch, int32_t n_nodes, int32_t* positions, uint64_t* tree_mask,
                   int32_t* device_status, mla_stream_t stream);
+size_t mla_decode_paged_workspace_size(int32_t batch, int32_t s_q, int32_t heads, int32_t rank, int32_t rope_dim,
+                                       int64_t t_max, int32_t k_max, int selected, int dtype);
 int mla_decode_attend_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* latent,
                             int64_t latent_row_stride, int64_t latent_page_stride, const void* rope,
                             int64_t rope_row_stride, int64_t rope_page_stride, int dtype, const int32_t* page_table,

@@ -233,16 +233,15 @@ static int decode_geometry(DecodeGeometry& g, const void* q, int64_t q_row_strid
   return MLA_OK;
 }
 
-size_t mla_decode_workspace_size(int32_t batch, int32_t s_q, int32_t heads, int32_t rank,
-                                 int32_t rope_dim, int64_t t_max, int32_t k_max, int selected,
-                                 int dtype) {
+static size_t workspace_size(int32_t batch, int32_t s_q, int32_t heads, int32_t rank, int32_t rope_dim, int64_t t_max,
+                             int32_t k_max, int selected, int dtype, bool paged) {
   if (batch <= 0 || s_q <= 0 || heads <= 0 || rank <= 0 || rope_dim < 0 || t_max <= 0 ||
       !valid_dtype(dtype) || (selected && k_max <= 0))
     return 0;
   const int64_t n_q = (int64_t)batch * s_q;   // 64-bit: no overflow before the limits below
   if (dtype == MLA_DTYPE_BF16) {
     if (!tc_decode_shape(heads, rank, rope_dim, dtype) || n_q > (1 << 20)) return 0;
-    return (tc_decode_workspace((int32_t)n_q) + 255) & ~(size_t)255;
+    return ((paged ? tc_paged_workspace((int32_t)n_q) : tc_decode_workspace((int32_t)n_q)) + 255) & ~(size_t)255;
   }
   if (n_q > (1 << 24)) return 0;
   DecodeGeometry g;
@@ -257,6 +256,17 @@ size_t mla_decode_workspace_size(int32_t batch, int32_t s_q, int32_t heads, int3
   g.sel = selected ? reinterpret_cast<const int32_t*>(16) : nullptr;
   const size_t need = simt_decode_workspace(g, nullptr);
   return (need + 255) & ~(size_t)255;
+}
+
+size_t mla_decode_workspace_size(int32_t batch, int32_t s_q, int32_t heads, int32_t rank,
+                                 int32_t rope_dim, int64_t t_max, int32_t k_max, int selected,
+                                 int dtype) {
+  return workspace_size(batch, s_q, heads, rank, rope_dim, t_max, k_max, selected, dtype, false);
+}
+
+size_t mla_decode_paged_workspace_size(int32_t batch, int32_t s_q, int32_t heads, int32_t rank, int32_t rope_dim,
+                                       int64_t t_max, int32_t k_max, int selected, int dtype) {
+  return workspace_size(batch, s_q, heads, rank, rope_dim, t_max, k_max, selected, dtype, true);
 }
 
 int mla_decode_attend(const void* q, int64_t q_row_stride, int64_t q_head_stride,
@@ -1123,8 +1133,8 @@ int mla_decode_attend_paged(const void* q, int64_t q_row_stride, int64_t q_head_
   if (dtype == MLA_DTYPE_BF16 && !tc_decode_shape(heads, rank, rope_dim, dtype))
     return fail(MLA_ERR_UNSUPPORTED, "decode_paged: bf16 is served for heads 64 or 128, rank 512, rope_dim 64 "
                                      "(got heads %d, rank %d, rope_dim %d)", heads, rank, rope_dim);
-  const size_t need = mla_decode_workspace_size(batch, s_q, heads, rank, rope_dim, t_max, k_max,
-                                                selected_positions != nullptr, dtype);
+  const size_t need = mla_decode_paged_workspace_size(batch, s_q, heads, rank, rope_dim, t_max, k_max,
+                                                      selected_positions != nullptr, dtype);
   MLA_CHECK(workspace_bytes >= need && (need == 0 || workspace),
             "decode_paged: workspace of %zu bytes < %zu needed", workspace_bytes, need);
   MLA_CHECK((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0,

@@ -79,6 +79,7 @@ struct DecodeTail {
   int32_t heads, nope, v_dim, rank;
 };
 size_t tc_decode_workspace(int32_t n_q);
+size_t tc_paged_workspace(int32_t n_q);   // of the same kernels over pages
 cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* workspace,
                              size_t workspace_bytes, cudaStream_t stream, const DecodeTail* tail = nullptr);
 

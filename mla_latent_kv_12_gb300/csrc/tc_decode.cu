@@ -997,7 +997,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool whole;
     while (!aborted() && it.next(u, t0, t1, whole)) {
       const bool any = member_segment<kPaged>(a, keys_p, u, member, n, t0, t1);
-      const int64_t slot = ((int64_t)u + group) * a.width + member;
+      const int64_t slot = slot_of<kPaged>(a, u, group, member, t0 == 0);
       if (!any) {
         // Nothing of this row in the group's range: an empty partial (weight 0).
         if (!whole && rank == 0 && h < a.heads) {
@@ -1361,7 +1361,6 @@ __global__ void __launch_bounds__(128) tc_combine_kernel(const __grid_constant__
     if (c0 == c1) {
       write = false;                       // finished in place by its group
     } else {
-      auto slot_of = [&](int g) -> int64_t { return ((int64_t)u + g) * a.width + member; };
       for (int cb = c0; cb <= c1; cb += kCombineBatch) {
         float mq[kCombineBatch], lq[kCombineBatch];
         uint4 raw[kCombineBatch];
@@ -1371,7 +1370,7 @@ __global__ void __launch_bounds__(128) tc_combine_kernel(const __grid_constant__
           lq[q] = 0.f;
           raw[q] = make_uint4(0, 0, 0, 0);
           if (cb + q <= c1) {
-            const int64_t sl = slot_of(cb + q);
+            const int64_t sl = slot_of<kPaged>(a, u, cb + q, member, cb + q == c0);
             mq[q] = a.ws_ml[(sl * 2) * HEADS + h];
             lq[q] = a.ws_ml[(sl * 2 + 1) * HEADS + h];
             raw[q] = ld_partial(a.ws_o + (sl * (RANK / 8) + d0 / 8) * HEADS + h);
@@ -1705,20 +1704,23 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 int tc_decode_clusters() { return device_sm_count() / 2; }
 
 // The partials are laid out for the MMA's 128 rows whatever the head count.
-size_t tc_decode_workspace(int32_t n_q) {
-  const size_t slots = (size_t)n_q + tc_decode_clusters();
+static size_t split_workspace(int32_t n_q, size_t slots) {
   return align256((size_t)(n_q + 2) * 4) + align256((size_t)n_q * 4) +
          align256(slots * HEADS * RANK * 2) + align256(slots * HEADS * 2 * 4);
 }
+static size_t decode_slots(int32_t n_q) { return (size_t)n_q + tc_decode_clusters(); }
+size_t tc_decode_workspace(int32_t n_q) { return split_workspace(n_q, decode_slots(n_q)); }
+size_t tc_paged_workspace(int32_t n_q) { return split_workspace(n_q, (size_t)piece_slots(n_q, tc_decode_clusters())); }
 
 void tc::lay_out_workspace(TcDecodeArgs& a, void* workspace) {
+  a.few_units = few_units(a.n_units, a.num_clusters / a.width);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   size_t off = 0;
   a.prefix = reinterpret_cast<int32_t*>(ws + off);
   off += align256((size_t)(a.n_q + 2) * 4);
   a.keys = reinterpret_cast<int32_t*>(ws + off);
   off += align256((size_t)a.n_q * 4);
-  const size_t slots = (size_t)a.n_q + tc_decode_clusters();
+  const size_t slots = a.table ? (size_t)piece_slots(a.n_q, tc_decode_clusters()) : decode_slots(a.n_q);
   a.ws_o = reinterpret_cast<uint4*>(ws + off);
   off += align256(slots * HEADS * RANK * 2);
   a.ws_ml = reinterpret_cast<float*>(ws + off);
@@ -1741,7 +1743,7 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
                              cudaStream_t stream, const DecodeTail* tail) {
   const int n_q = g.batch * g.s_q;
   const int nclusters = tc_decode_clusters();
-  if (workspace_bytes < tc_decode_workspace(n_q)) return cudaErrorInvalidValue;
+  if (workspace_bytes < (g.table ? tc_paged_workspace(n_q) : tc_decode_workspace(n_q))) return cudaErrorInvalidValue;
   if (g.heads != 64 && g.heads != HEADS) return cudaErrorInvalidValue;
   TcDecodeArgs a = {};
   a.q = static_cast<const __nv_bfloat16*>(g.q);
@@ -1768,7 +1770,6 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
   a.out_f32 = out_dtype == MLA_DTYPE_F32;
   a.lse = g.lse_out;
   a.status = g.device_status;
-  lay_out_workspace(a, workspace);
   a.num_clusters = nclusters;
   // A dense multi-token verify serves each batch row's tokens with a group of
   // clusters in lockstep; everything else is one query row per unit.
@@ -1801,6 +1802,7 @@ cudaError_t launch_tc_decode(const DecodeGeometry& g, int out_dtype, void* works
   a.counts = g.counts;
   a.tree = g.tree;
   a.tree_words = g.tree_words;
+  lay_out_workspace(a, workspace);
 
   // Tensor maps over [B_buf, t_max, dims] (the batch axis has extent 1 for a
   // packed-flat cache whose batch stride is 0).

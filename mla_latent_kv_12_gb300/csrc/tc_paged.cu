@@ -704,7 +704,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
       live = false;
       while (it.next(u, t0, t1, whole)) {
-        slot = ((int64_t)u + group) * a.width + member;
+        slot = slot_of<true>(a, u, group, member, t0 == 0);
         live = member_segment<true>(a, keys_p, u, member, n, t0, t1);
         if (live) break;
         // Nothing of this row in the group's range: an empty partial (weight 0).
@@ -910,7 +910,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
 cudaError_t launch_tc_paged(const DecodeGeometry& g, int out_dtype, void* workspace, size_t workspace_bytes,
                             cudaStream_t stream) {
-  if (workspace_bytes < tc_decode_workspace(g.batch * g.s_q)) return cudaErrorInvalidValue;
+  if (workspace_bytes < tc_paged_workspace(g.batch * g.s_q)) return cudaErrorInvalidValue;
   if (g.heads != 64 && g.heads != HEADS) return cudaErrorInvalidValue;
   TcDecodeArgs a = {};
   a.q = static_cast<const __nv_bfloat16*>(g.q);

@@ -5,6 +5,7 @@
 
 #include "mla_internal.h"
 #include "paged.cuh"
+#include "pieces.cuh"
 #include "tc_common.cuh"
 
 namespace mla {
@@ -57,7 +58,7 @@ struct TcDecodeArgs {
   int32_t* status;
   int32_t* prefix;     // [n_units + 2] the split plan: prefix over work units, then the start charge
   int32_t* keys;       // [n_q] visible entries per query row (planner)
-  uint4* ws_o;         // [slots][RANK/8][H] partial context, 8 fp16 dims per entry (O / l of the piece)
+  uint4* ws_o;         // [slots][RANK/8][H] partial context, 8 fp16 dims per entry (O / l of the piece); slots: see slot_of
   float* ws_ml;        // [slots][2][H] partial (m, l), log2 domain
   int32_t num_clusters;
   int32_t width;       // query rows per work unit = clusters per group
@@ -87,6 +88,7 @@ struct TcDecodeArgs {
   const int32_t* counts;
   const uint64_t* tree;
   int32_t tree_words;
+  bool few_units;      // no more work units than groups of clusters (set with the workspace)
 };
 
 // ------------------------------------------------------------------ helpers
@@ -189,6 +191,14 @@ __device__ __forceinline__ int first_group_of(const int32_t* prefix, int u, int 
 }
 __device__ __forceinline__ int last_group_of(const int32_t* prefix, int u, int per) {
   return (prefix[u + 1] - 1) / per;
+}
+
+// Where in the workspace the piece of unit u's row `member` lies that group g
+// leaves (`begins`: g holds the unit's first tile).
+template <bool kPaged>
+__device__ __forceinline__ int64_t slot_of(const TcDecodeArgs& a, int u, int g, int member, bool begins) {
+  const int place = kPaged ? piece_place(a.few_units, u, g, begins) : u + g;
+  return (int64_t)place * a.width + member;
 }
 
 // A member's share of a unit segment: its query row n and the segment's tiles
@@ -321,7 +331,7 @@ __device__ __forceinline__ void store_pieces(const TcDecodeArgs& a, const int32_
 // the split rows behind a decode kernel.
 cudaError_t launch_split_plan(const TcDecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_split_combine(const TcDecodeArgs& a, cudaStream_t stream);
-// Points prefix, keys, ws_o and ws_ml into a workspace of tc_decode_workspace(n_q) bytes.
+// Points prefix, keys, ws_o and ws_ml (once n_units, num_clusters and width are set) into a workspace of tc_decode_workspace(n_q) or tc_paged_workspace(n_q) bytes.
 void lay_out_workspace(TcDecodeArgs& a, void* workspace);
 
 }  // namespace tc

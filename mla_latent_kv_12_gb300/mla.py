@@ -38,7 +38,7 @@ EXPORTS = (
     "mla_cache_shift_rows", "mla_rollback_lengths", "mla_reconstruct_kv", "mla_prefill_attend",
     "mla_append_compressed_q8", "mla_quantize_cache", "mla_dequantize_cache", "mla_decode_attend_q8",
     "mla_key_weights", "mla_key_weights_q8", "mla_evict_plan", "mla_cache_compact",
-    "mla_append_paged", "mla_tree_plan", "mla_decode_attend_paged", "mla_commit_paged",
+    "mla_append_paged", "mla_tree_plan", "mla_decode_paged_workspace_size", "mla_decode_attend_paged", "mla_commit_paged",
 )
 
 
@@ -80,6 +80,8 @@ def _load() -> ctypes.CDLL:
                                       ctypes.c_int, vp, vp, sz, vp, vp]
     lib.mla_decode_workspace_size.restype = sz
     lib.mla_decode_workspace_size.argtypes = [i32, i32, i32, i32, i32, i64, i32, ctypes.c_int, ctypes.c_int]
+    lib.mla_decode_paged_workspace_size.restype = sz
+    lib.mla_decode_paged_workspace_size.argtypes = lib.mla_decode_workspace_size.argtypes
     lib.mla_decode_kernel_kind.restype = ctypes.c_int
     lib.mla_decode_kernel_kind.argtypes = [i32, i32, i32, ctypes.c_int, ctypes.c_int]
     lib.mla_project_v.restype = ctypes.c_int
@@ -719,6 +721,13 @@ def tree_plan(parents: torch.Tensor, kv_len: Optional[torch.Tensor], positions: 
     return tree_mask
 
 
+def decode_paged_workspace_size(batch, s_q, heads, rank, rope_dim, t_max, k_max=0, selected=False,
+                                dtype=torch.bfloat16) -> int:
+    """Bytes of ``decode_attend_paged``'s workspace; ``t_max``: keys of a row's whole table."""
+    return lib.mla_decode_paged_workspace_size(batch, s_q, heads, rank, rope_dim, t_max, k_max, 1 if selected else 0,
+                                               _DT[dtype])
+
+
 def decode_attend_paged(q: torch.Tensor, latent: torch.Tensor, rope: torch.Tensor, page_table: torch.Tensor,
                         kv_len: torch.Tensor, batch: int, s_q: int, softmax_scale: float, ctx_out: torch.Tensor,
                         lse_out: Optional[torch.Tensor] = None, counts: Optional[torch.Tensor] = None,
@@ -728,9 +737,9 @@ def decode_attend_paged(q: torch.Tensor, latent: torch.Tensor, rope: torch.Tenso
     """``decode_attend`` over pages: ``q`` ``[batch * s_q, H, rank+rope]``, pools and table as for ``append_paged``,
     ``kv_len`` with the new tokens; ``tree_mask`` as ``tree_plan`` writes it (none: the tokens follow one another)."""
     if workspace is None:
-        nbytes = decode_workspace_size(batch, s_q, q.shape[1], latent.shape[2], rope.shape[2],
-                                       page_table.shape[1] * latent.shape[1], 0 if sel is None else sel.shape[1],
-                                       sel is not None, q.dtype)
+        nbytes = decode_paged_workspace_size(batch, s_q, q.shape[1], latent.shape[2], rope.shape[2],
+                                             page_table.shape[1] * latent.shape[1], 0 if sel is None else sel.shape[1],
+                                             sel is not None, q.dtype)
         workspace = _scratch(max(nbytes, 1), q.device, stream)
     _native.decode_attend_paged(q, latent, rope, page_table, kv_len, batch, s_q, softmax_scale, ctx_out, lse_out, counts,
                                 tree_mask, sel, sel_count, workspace, device_status, stream)

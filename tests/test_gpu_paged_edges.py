@@ -207,3 +207,37 @@ def test_pages_of_one_row_inside_wider_rows(mla, heads):
 def c_without_tree(c):
     c.nodes = c.mask = None
     return c
+
+
+# ---------------------------------------------------------------- workspaces
+
+@pytest.mark.parametrize("lens,s_q,heads,size,tree", [
+    ([4096], 1, 128, 64, False),                           # one row in many pieces
+    ([9000, 300, 5000], 4, 128, 16, False),
+    ([2500, 1900, 77], 300, 64, 64, False),                # pairs, many more units than groups of clusters
+    ([2500, 700], 150, 128, 32, False),
+    ([3000, 900], 90, 64, 16, True),
+    ([int(n) for n in np.random.default_rng(6).integers(0, 700, 500)], 1, 128, 16, False),
+    ([2500, 300], 40, 128, 7, False),                      # row by row: a unit a token
+    ([1500] * 80, 1, 64, 5, False),
+    ([20000] * 19, 4, 128, 64, False),                     # as many units as groups, one more, two
+    ([20000] * 19 + [9000], 4, 128, 64, False),
+    ([4000] * 77, 1, 128, 64, False),
+])
+def test_the_workspace_asked_for_is_enough(mla, lens, s_q, heads, size, tree):
+    """Of that size to the byte, between bytes that must stay, filled with NaN before the call; a larger one gives the
+    same bits."""
+    c = Case(80, lens, s_q, heads, size, counts=[min(n, s_q) for n in lens], tree=tree)
+    need = mla.decode_paged_workspace_size(c.B, s_q, heads, 512, 64, c.table.shape[1] * size)
+    guard = 1 << 16
+    room = torch.full((need + 2 * guard,), 0xFF, dtype=torch.uint8, device=DEV)
+    ctx, lse, st = attend(mla, c, workspace=room[guard:guard + need])
+    assert st == 0
+    assert (room[:guard] == 0xFF).all() and (room[guard + need:] == 0xFF).all()
+    c.check(ctx, lse, rows=sorted({k * (c.B * s_q - 1) // 12 for k in range(13)}))
+    large = torch.full((mla.decode_workspace_size(c.B, s_q, heads, 512, 64, c.table.shape[1] * size) + 4096,), 0xFF,
+                       dtype=torch.uint8, device=DEV)
+    again = attend(mla, c, workspace=large)
+    assert torch.equal(again[0], ctx) and torch.equal(again[1], lse)
+    with pytest.raises(mla.MLAError):
+        attend(mla, c, workspace=room[guard:guard + need - 256])

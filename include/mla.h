@@ -748,7 +748,8 @@ int mla_cache_compact(const mla_state_array* arrays, int32_t n_arrays, const int
  * right.  A node that is not above its predecessor, below j or behind the table
  * sets MLA_DEVICE_INDEX_OUT_OF_RANGE and is not moved; the row's length grows
  * all the same.  `arrays` is a HOST array of n_arrays <= MLA_MAX_COMMIT_ARRAYS
- * pools (all layers at once); batch_stride_bytes is the stride between pages.
+ * pools (all layers at once) that do not overlap, none listed twice;
+ * batch_stride_bytes is the stride between pages.
  * Rows of one call must not share the pages that they write.
  * At most 65535 batch rows in mla_tree_plan and mla_commit_paged.
  */

@@ -5,6 +5,8 @@
 #include <string.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "e4m3.cuh"
 #include "mla_internal.h"
 
@@ -1213,6 +1215,11 @@ int mla_commit_paged(const mla_state_array* arrays, int32_t n_arrays, const int3
       unit >>= 1;
     p.a[i] = CommitArray{static_cast<uint8_t*>(a.data), a.token_stride_bytes, a.batch_stride_bytes, a.row_bytes, unit};
   }
+  auto below = [](const CommitArray& x, const CommitArray& y) { return x.data < y.data; };
+  if (!std::is_sorted(p.a, p.a + n_arrays, below)) std::sort(p.a, p.a + n_arrays, below);   // (any order serves)
+  MLA_CHECK(std::adjacent_find(p.a, p.a + n_arrays, [](const CommitArray& x, const CommitArray& y) { return x.data == y.data; }) ==
+                p.a + n_arrays,
+            "commit_paged: an array is listed twice");
   p.n_arrays = n_arrays;
   p.table = page_table;
   p.table_stride = page_table_stride;

@@ -57,3 +57,15 @@ def test_other_threads_run_during_a_call(tmp_path):
     r = subprocess.run([sys.executable, "-c", textwrap.dedent(SCRIPT), str(lib)], cwd=ROOT, capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
+def test_an_array_listed_twice_is_refused():
+    """Its rows would be moved by two workers at once.  (The pointers are no device memory: nothing may launch.)"""
+    from mla_latent_kv_12_gb300 import mla
+    mb = 1 << 20
+    for order in ([0, 1, 2, 1], [3, 2, 1, 3], [5, 5], list(range(250)) + [17]):
+        states = (mla.StateArray * len(order))()
+        for s, k in zip(states, order):
+            s.data, s.token_stride_bytes, s.batch_stride_bytes, s.row_bytes = mb * (k + 1), 1024, 16384, 1024
+        assert mla.lib.mla_commit_paged(states, len(order), mb, 8, 8, 16, 100, mb, mb, 16, 16, mb, None, 4, None, None) == 1
+        assert "twice" in mla.lib.mla_last_error_detail().decode()

@@ -241,3 +241,75 @@ def test_the_workspace_asked_for_is_enough(mla, lens, s_q, heads, size, tree):
     assert torch.equal(again[0], ctx) and torch.equal(again[1], lse)
     with pytest.raises(mla.MLAError):
         attend(mla, c, workspace=room[guard:guard + need - 256])
+
+
+# ---------------------------------------------------------------- threads and graphs
+
+def test_calls_from_two_threads(mla):
+    """Each thread on its own stream; a call leaves the interpreter to the other thread while it launches."""
+    import threading
+
+    cases = [Case(91, [3000, 900], 3, 128, 16), Case(92, [2000, 64, 1], 8, 64, 64, tree=True)]
+    want = [attend(mla, c) for c in cases]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(c, ref):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(50):
+                    got = attend(mla, c)
+                    if not (torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1]) and got[2] == ref[2]):
+                        raise AssertionError("another result")
+                    with pytest.raises(AssertionError):
+                        mla.tree_plan(c.table.long(), None, c.table, c.table)
+        except BaseException as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(cases, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+
+
+@pytest.mark.parametrize("heads,size,s_q,tree", [(128, 64, 1, False), (64, 16, 5, False), (128, 7, 3, False), (64, 32, 40, True)])
+def test_a_graph_follows_its_inputs(mla, heads, size, s_q, tree):
+    """Lengths, counts, pages, masks and queries change between replays: each gives what a call then gives."""
+    lens = [900, 300, 64]
+    c = Case(95, lens, s_q, heads, size, counts=[s_q] * 3, tree=tree)
+    n_q = 3 * s_q
+    length, st = i32(lens), status()
+    ctx, lse = torch.zeros(n_q, heads, 512, dtype=BF16, device=DEV), torch.zeros(n_q, heads, device=DEV)
+    ws = torch.empty(mla.decode_paged_workspace_size(3, s_q, heads, 512, 64, c.table.shape[1] * size), dtype=torch.uint8,
+                     device=DEV)
+
+    def call():
+        mla.decode_attend_paged(c.q, c.latent, c.rope, c.table, length, 3, s_q, SCALE, ctx, lse, counts=c.counts_d,
+                                tree_mask=c.mask, workspace=ws, device_status=st)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    zeros = [0] * 3
+    for cut, counts in ((zeros, [s_q, s_q, 1]), ([899, 300, 1], [1, 0, s_q]), ([5, 64, 7], [0, 0, 0]), (zeros, [s_q] * 3)):
+        c.table.copy_(c.table.roll(1, 0))                # a row's pages go along with its length
+        lens = lens[-1:] + lens[:-1]
+        length.copy_(i32([max(0, n - k) for n, k in zip(lens, cut)]))
+        c.counts_d.copy_(i32(counts))
+        c.q.copy_(c.q.roll(1, 0))
+        if tree:
+            c.mask.copy_(c.mask.roll(1, 0) | 1)
+        graph.replay()
+        got = ctx.clone(), lse.clone()
+        ctx.fill_(7), lse.fill_(7)
+        call()
+        assert torch.equal(ctx, got[0]) and torch.equal(lse, got[1])
+        there = torch.tensor([i < counts[b] and int(length[b]) > 0 for b in range(3) for i in range(s_q)], device=DEV)
+        assert (got[0][~there] == 0).all() and torch.isneginf(got[1][~there]).all()
+        assert torch.isfinite(got[0]).all()
+    assert int(st) == 0

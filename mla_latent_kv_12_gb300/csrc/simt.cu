@@ -113,6 +113,10 @@ constexpr int kMaxRankPerLane = kMaxRank / 32;
 // kQ8: the latent comes from e4m3 codes and their block's exponent.
 // kPaged: the rows are found through the page table, and a tree's token passes
 // over the keys that it does not see.
+// Bound by the chain of one key after another in each warp, and every head of
+// every token reads the cache again.  Over pages: 4 heads of rank 32 over 1500
+// keys 39 us; 8 heads of rank 128, 4 rows of 2048 keys 51, trees of 32 nodes
+// over the same 1289; 16 heads of rank 512, 4 rows of 2048 keys 180.
 template <typename T, typename TO, bool kQ8 = false, bool kPaged = false>
 __global__ void __launch_bounds__(kDecodeWarps * 32)
     simt_decode_kernel(const __grid_constant__ DecodeGeometry g, float* __restrict__ ws, int splits) {

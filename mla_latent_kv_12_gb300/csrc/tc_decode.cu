@@ -272,6 +272,12 @@ __global__ void __launch_bounds__(1024) tc_plan_kernel(const __grid_constant__ T
 // only; rows of a tile that its token does not see, or that a selection names
 // by no position of a key, are cleared before the scores: a probability of 0
 // must not meet what another token, or nobody, left there.
+// Bound by the issue of 80 gather copies a tile; tokens share neither tiles nor,
+// with 64 heads, MMA rows.  Over pages of 1, 7 or 12 rows (in parentheses 16
+// rows, by boxes): one row of 4096 keys 20.6 us (16.4), 32 rows of 1024 to 32768
+// 250 (127), 8 x 4 tokens of 16384 236 (111), 8 trees of 64 nodes behind 8000
+// keys 1793 (792), 2 chunks of 512 tokens and 64 heads 3032 (703).  2048
+// selected of 32768 keys: one row 21.1 us, 8 rows 23.2, 8 x 4 tokens 49.8.
 template <int kPrefetchAhead, int kThreads, bool kLateP, bool kQ8 = false, bool kPaged = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_decode_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_constant__ CUtensorMap rope_map,

@@ -26,14 +26,16 @@
 //    that are not finite are replaced by 0 and the token that does see it gets
 //    NaN.
 //
-// Measured: 32 rows of 1024 to 32768 keys 127 us (5.0 TB/s; window decode 138),
-// 8 x 4 tokens of 65536 367 to 387 us (1.5 PFLOP/s), 8 trees of 64 nodes behind
-// 8000 to 15000 keys 1072 us (1.5 PFLOP/s), one row of 4096 15.7 us.  With many
-// tokens per key it is bound by the tensor cores (busy in 68 % of the cycles)
-// and, in a loop of a second, by the power limit: verify 430, the trees 1281.
-// Single tokens read at 75 % of the copy rate.  The instructions of the softmax
-// do not bind it: 96 fewer of some 900 that a scheduler issues per tile
-// changed nothing but the clock under that limit (1 %).
+// Measured, in bursts: 32 rows of 1024 to 32768 keys 120 to 127 us (5.0 TB/s;
+// window decode 138), 8 x 4 tokens of 65536 367 us (1.6 PFLOP/s; 387 to 403 over
+// pages of 16 rows), 8 trees of 64 nodes behind 8000 to 15000 keys 1073 to 1110
+// (1.5 PFLOP/s), one row of 4096 15.7.  With many tokens per key it is bound by
+// the tensor cores (busy in 68 % of the cycles) and, in a loop of a second, by
+// the power limit: verify over pages of 16 rows 430, the trees 1281.  Single
+// tokens read at 75 % of the copy rate, in a loop at 70; neither memory nor the
+// tensor cores bind them.  The instructions of the softmax do not bind it: 96
+// fewer of some 900 that a scheduler issues per tile changed nothing but the
+// clock under that limit (1 %).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math_constants.h>
@@ -75,7 +77,9 @@ static_assert(kGroups * regs_softmax(false) + regs_issue(false) <= (kGroups + 1)
 // Up to this many query rows of a batch row go in lockstep, each with a cluster, so that they read a tile at the same
 // time.  By 1, 2, 4, 8 rows: verify of 8 x 4 tokens of 65536 438, 395, 377, 378 us; 8 trees of 64 nodes behind 8000 to
 // 15000 keys 1146, 1110, 1118, 1120; trees of 20 nodes in 4 rows of 20000 332, 307, 300, 309 (eight leave four of 76
-// clusters idle).
+// clusters idle).  Units are cut from the flat list of query rows, and a cluster whose row has no keys waits for the
+// others: 32 rows of 1024 to 32768 keys take 396 us with four tokens each, 381 with one of four (120 in a call of one
+// token), and with 5, 6 and 8 tokens, of which the first two straddle batch rows, 583, 661 and 805.
 constexpr int kLockstep = 4;
 // A unit's start is charged as this many tiles where the ranges are at least so long (the query waits for the last
 // scores of the unit before, and its context is stored): one tree of 16 nodes behind 4050 keys 33.2 -> 29.8 us, of 64

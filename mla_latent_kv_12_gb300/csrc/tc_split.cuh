@@ -15,7 +15,7 @@ constexpr int BN = 64;                    // keys per tile
 constexpr int HEADS = 128, RANK = 512, DV = 256;  // DV: latent dims per CTA
 constexpr long long kWaitLimit = 1LL << 32;  // clock cycles (~2 s)
 constexpr float kRescaleThreshold = 8.0f;    // log2 units
-// A group's tile range is at least this long: each split writes a 256 KB f32
+// A group's tile range is at least this long: each split writes a 128 KB fp16
 // partial, worth it only against a few 72 KB tiles of cache read.
 constexpr int kMinTilesPerGroup = 4;
 // Each work unit with tiles is charged this many tiles' worth of time for
@@ -62,7 +62,7 @@ struct TcDecodeArgs {
   float* ws_ml;        // [slots][2][H] partial (m, l), log2 domain
   int32_t num_clusters;
   int32_t width;       // query rows per work unit = clusters per group
-  int32_t n_units;     // n_q / width
+  int32_t n_units;     // n_q / width (over pages rounded up)
   int32_t min_tiles;   // smallest tile range given to a group
   int32_t start_charge, charge_min_span;  // kUnitStartCharge and kChargeMinSpan, or the kernel's own
   int32_t batch_in_map;  // 1: use batch coordinate b in the tensor maps

@@ -748,7 +748,7 @@ def decode_attend_paged(q: torch.Tensor, latent: torch.Tensor, rope: torch.Tenso
 
 class PagedArrays:
     """Pools ``[num_pages, page_size, F]`` that ``commit_paged`` moves together (every layer's latent and rope keys,
-    say), checked once and kept."""
+    say), checked once and kept: their memory must stay where it is (no ``resize_`` or ``set_``)."""
 
     def __init__(self, arrays) -> None:
         self.tensors = list(arrays)
@@ -771,7 +771,8 @@ def commit_paged(arrays, page_table: torch.Tensor, kv_len: torch.Tensor, path: t
                  kv_len_out: Optional[torch.Tensor] = None, device_status: Optional[torch.Tensor] = None,
                  stream=None) -> None:
     """Moves the accepted path of each row's tree to the end of its sequence in every pool of ``arrays`` (a
-    ``PagedArrays``, or the pools): ``path`` ``[B, width]`` int32 node numbers, ascending, ``counts`` ``[B]`` of them;
+    ``PagedArrays``, or the pools, which are then looked through at every call: for 48 pools 55 us of host time instead
+    of 3): ``path`` ``[B, width]`` int32 node numbers, ascending, ``counts`` ``[B]`` of them;
     ``kv_len``: the lengths before the trees were appended."""
     if not isinstance(arrays, PagedArrays):
         arrays = PagedArrays(arrays)
